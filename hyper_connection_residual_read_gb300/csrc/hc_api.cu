@@ -22,6 +22,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 Ctx g_ctx[kMaxDevices];
 
+}  // namespace
+
 Ctx* current_ctx(int* err) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -35,6 +37,8 @@ Ctx* current_ctx(int* err) {
     *err = HC_OK;
     return &g_ctx[dev];
 }
+
+namespace {
 
 void free_ctx(Ctx& c) {
     if (c.device >= 0) cudaSetDevice(c.device);
@@ -55,6 +59,8 @@ struct Range {
 
 bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
+}  // namespace
+
 // A pointer the kernels may dereference: not null, 16-byte aligned, and device
 // (or managed) memory of the context's device. Host pointers are refused here
 // so that no kernel ever receives one.
@@ -70,6 +76,8 @@ int check_ptr(const void* p, int device) {
     if (at.type == cudaMemoryTypeDevice && at.device != device) return HC_ERR_ARG;
     return HC_OK;
 }
+
+namespace {
 
 int validate(const Ctx& c, const ReadArgs& a) {
     if (a.T < 0 || a.T > c.max_tokens) return HC_ERR_ARG;
@@ -245,7 +253,7 @@ extern "C" const char* hc_read_strerror(int code) {
         case HC_ERR_TIMEOUT: return "a bounded device-side wait gave up";
         case HC_ERR_CHECK: return "self check found a mismatch";
         case HC_ERR_NOMEM: return "scratch allocation failed";
-        case HC_ERR_BOUNDS: return "the bounds-checked build skipped an out-of-range access";
+        case HC_ERR_BOUNDS: return "an out-of-range access was skipped (a bad index in device memory, or the bounds-checked build)";
         default: return "unknown status";
     }
 }

@@ -93,6 +93,11 @@ struct Ctx {
     mutable WupMapCache wu_maps;     // decode: W_up tensor maps by address
 };
 
+// The current device's context, or nullptr with *err set; and whether p is 16-byte
+// aligned memory of `device` that kernels may dereference (hc_api.cu).
+Ctx* current_ctx(int* err);
+int check_ptr(const void* p, int device);
+
 // 128-token tiles of the partials.
 inline int partial_tiles(int max_tokens) { return (max_tokens + 127) / 128; }
 
