@@ -50,6 +50,8 @@ void free_ctx(Ctx& c) {
     cudaFree(c.ssq);
     cudaFree(c.lo3);
     cudaFree(c.gated);
+    cudaFree(c.attn_pieces);
+    cudaFree(c.attn_arrivals);
     c = Ctx();
 }
 
@@ -296,12 +298,16 @@ extern "C" int hc_read_init(int device, int max_tokens, float eps) {
     ok &= cudaMalloc(&c.partials, sizeof(float) * ts * kStreams * 4 * kRank) == cudaSuccess;
     ok &= cudaMalloc(&c.ssq, sizeof(float) * ts * kStreams * 4) == cudaSuccess;
     ok &= cudaMalloc(&c.lo3, sizeof(uint16_t) * 3 * (size_t)max_tokens * kRank) == cudaSuccess;
+    const size_t arrivals = sizeof(unsigned) * kAttnCtasPerSm * c.sm_count;
+    ok &= cudaMalloc(&c.attn_pieces, sizeof(float) * attention_scratch_floats(c.sm_count)) == cudaSuccess;
+    ok &= cudaMalloc(&c.attn_arrivals, arrivals) == cudaSuccess;
     if (!ok) {
         cudaGetLastError();
         free_ctx(c);
         return HC_ERR_NOMEM;
     }
-    if (cudaMemset(c.s.status, 0, sizeof(int)) != cudaSuccess ||
+    if (cudaMemset(c.attn_arrivals, 0, arrivals) != cudaSuccess ||
+        cudaMemset(c.s.status, 0, sizeof(int)) != cudaSuccess ||
         cudaMemset(c.s.sync, 0, kSyncWords * sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(c.s.sched, 0, 2 * kSchedPairs * sizeof(int)) != cudaSuccess ||
         decode_setup(device) != cudaSuccess ||
@@ -411,7 +417,8 @@ extern "C" int hc_read_status(void* stream) {
         // a kernel that gave up may have left its scheduler pair or the one-kernel
         // decode read's exchange counters mid-count (the stream is idle here)
         if (cudaMemset(c->s.sched, 0, 2 * kSchedPairs * sizeof(int)) != cudaSuccess ||
-            cudaMemset(c->s.sync, 0, kSyncWords * sizeof(unsigned)) != cudaSuccess)
+            cudaMemset(c->s.sync, 0, kSyncWords * sizeof(unsigned)) != cudaSuccess ||
+            cudaMemset(c->attn_arrivals, 0, sizeof(unsigned) * kAttnCtasPerSm * c->sm_count) != cudaSuccess)
             return HC_ERR_CUDA;
         return HC_ERR_TIMEOUT;
     }

@@ -1,15 +1,667 @@
-// Attention over the cache held in 4 bits.
+// Attention over the cache held in 4 bits, for windows of few rows: the new tokens times
+// the query heads of one kv head, at most 32.
+//
+// With few rows the cache's bytes bound the operator: head_dim / 2 + 4 bytes a token for
+// the key and as much for the value, read once. Everything else has to keep out of their
+// way:
+//
+// * Codes go from their words straight into matrix fragments. The keys are the left
+//   operand (16 tokens x 16 dimensions) and the queries the right one, so that 8 rows fill
+//   an mma.m16n8k16 and each further 8 rows reuse the decoded keys; the values,
+//   transposed, are the left operand of the second product. (tcgen05 would take its
+//   operands from shared or tensor memory: a second trip for every decoded value, four
+//   times its bytes in the cache, and 128 rows where 8 are wanted.)
+// * S_j = s_j (q . (c_j - 8)) + (m_j + 8 s_j) sum(q): the codes enter as whole numbers,
+//   exactly, and step and minimum are applied to the product in fp32, once a token and
+//   row instead of once a value. Likewise o = sum w_j (c_j - 8) + sum p_j (m_j + 8 s_j)
+//   with w_j = p_j s_j. w_j is rounded to fp16 (11 bits: the one rounding of the
+//   product), after division by a power of two near the largest step seen; p_j itself
+//   is summed in fp32.
+// * The order of dimensions within a product is free as long as both operands agree, and
+//   so is that of the tokens: both follow from which words a lane loads (16 bytes of a
+//   key row, 8 of a value row), so that no value moves between lanes. Only the weights
+//   do: an 8 x 8 transpose (movmatrix) turns the first product's result into the second
+//   one's operand.
+// * The running maximum is raised only when a logit passes it by 2^8 (weights stay
+//   within fp16, sums in fp32): one vote a step instead of a reduction over lanes.
+//
+// Work is cut evenly, whatever the lengths: the units (256 tokens of one request and kv
+// head) are numbered through, and each CTA takes an equal run of them. A CTA's eight
+// warps take 32 tokens of each unit each and merge at the end of a (request, head). One
+// that is split between CTAs is joined by the last of them to finish, in the order of
+// the CTAs, from fp32 sums in scratch of a fixed size (a CTA can have at most two such
+// pieces).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <math_constants.h>
 #include <stdint.h>
 
-#include "hc_common.cuh"
-#include "hc_window_internal.h"
+#include "hc_attention.cuh"
 
 namespace hc {
 namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = (kWarps + 1) * 32;      // and one warp that issues the copies
+constexpr int kStep = 32;                        // tokens of a warp's step
+constexpr int kUnit = kWarps * kStep;            // tokens of a unit
+constexpr int kStages = 2;                       // steps of a warp's ring
+constexpr float kRaise = 8.f;                    // log2 by which a logit may pass the maximum
+constexpr float kStepRoom = 16.f;                // factor by which a step may pass the reference
+
+// A step's ring slot: key codes, value codes, key scales, value scales of 32 tokens.
+template <int kD>
+struct Slot {
+    static constexpr int kCodes = kStep * kD / 2;
+    static constexpr int kScales = kStep * 4;
+    static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+};
+
+template <int kD, int kNT>
+struct Smem {
+    static constexpr int kRing = kWarps * kStages * Slot<kD>::kBytes;
+    static constexpr int kMerge = kRing;                               // [kWarps][8][kD] floats
+    static constexpr int kQueries = kMerge + kWarps * 8 * kD * 4;      // fragments, a copy a warp
+    static constexpr int kQueryBytes = kNT > 1 ? kWarps * kNT * 8 * kD * 2 : 0;
+    static constexpr int kStats = kQueries + kQueryBytes;              // max, sum [kWarps][8 kNT]
+    static constexpr int kBars = kStats + 2 * kWarps * 8 * kNT * 4;
+    static constexpr int kBytes = kBars + 2 * kWarps * kStages * 8;
+};
+
+// Fixed scratch: per CTA two pieces of up to 32 rows, and a counter of arrivals.
+constexpr int kPieceRows = 32;
+constexpr int kPieceFloats = kPieceRows * (128 + 2);
+
+// The walk of a CTA through its run of units, piece by piece.
+struct Walk {
+    int b, h, u0, u1, units;
+    int64_t left, base;          // units left, and the number of unit (b, h, 0)
+    Window w;
+};
+
+__device__ __forceinline__ int window_units(const Window& w) {
+    return w.n > 0 ? max((w.kv + kUnit - 1) / kUnit, 1) : 0;
+}
+
+__device__ __forceinline__ void walk_piece(Walk& k) {
+    k.u1 = static_cast<int>(min(static_cast<int64_t>(k.units), k.u0 + k.left));
+    k.left -= k.u1 - k.u0;
+}
+
+// To the next piece; false at the end of the run.
+__device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
+    if (k.left == 0) return false;
+    k.base += k.units;
+    k.u0 = 0;
+    if (++k.h == a.c.kv_heads) {
+        k.h = 0;
+        do {
+            ++k.b;
+            if (k.b >= a.requests) return false;
+            k.w = load_window(a, k.b, nullptr);
+            k.units = window_units(k.w);
+        } while (k.units == 0);
+    }
+    walk_piece(k);
+    return true;
+}
+
+struct Run {
+    int b;
+    int64_t offset, begin, end, total, ctas;
+};
+
+// The CTA's run of units: every CTA sums the units of all requests, and the thread whose
+// share of the requests holds the run's first unit says where it lies.
+__device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* status) {
+    const int tid = threadIdx.x;
+    const int per = (a.requests + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += static_cast<int64_t>(window_units(load_window(a, b, blockIdx.x == 0 ? status : nullptr))) * a.c.kv_heads;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t t = __shfl_up_sync(~0u, upto, d);
+        if ((tid & 31) >= d) upto += t;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = upto;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == (tid >> 5)) upto += total;
+        total += sums[w];
+    }
+    // CTAs beyond the number of units have none, so that no run before them is empty
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), i = blockIdx.x;
+    const int64_t begin = i < ctas ? total * i / ctas : total, end = i < ctas ? total * (i + 1) / ctas : total;
+    if (tid == 0) {
+        run->begin = begin;
+        run->end = end;
+        run->total = total;
+        run->ctas = ctas;
+    }
+    if (begin < end && begin < upto && begin >= upto - mine) {
+        int64_t at = upto - mine;
+        for (int b = b0; b < b1; ++b) {
+            const int64_t n = static_cast<int64_t>(window_units(load_window(a, b, nullptr))) * a.c.kv_heads;
+            if (begin < at + n) {
+                run->b = b;
+                run->offset = begin - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ Walk walk_start(const AttentionArgs& a, const Run& run) {
+    Walk k;
+    k.b = run.b;
+    k.w = load_window(a, k.b, nullptr);
+    k.units = window_units(k.w);
+    k.h = static_cast<int>(run.offset / k.units);
+    k.u0 = static_cast<int>(run.offset - static_cast<int64_t>(k.h) * k.units);
+    k.left = run.end - run.begin;
+    k.base = run.begin - k.u0;
+    walk_piece(k);
+    return k;
+}
+
+// D += A (16 x 16, row-major fragments) B (16 x 8), fp16 with fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t permute(uint32_t x, uint32_t y, uint32_t how) {
+    return __byte_perm(x, y, how);
+}
+
+// The token of a 16-token tile that row m of the first product stands for. Any order
+// would do; this one keeps the lanes that load together on different banks.
+__device__ __forceinline__ int tile_token(int m) { return m ^ ((m >> 1) & 1); }
+
+// Where float pair `c` (of kD / 2) of row `row` lies in the merge buffer's row: moved
+// within its neighbourhood so that the lanes of a warp, which hold pairs kD / 16 apart,
+// store to different banks.
+template <int kD>
+__device__ __forceinline__ int merge_move(int row, int c) {
+    return ((c / (kD / 16)) & 7) ^ ((row >> 1) & 1);
+}
+
+template <int kD, int kDtype, int kNT>
+__global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
+    window_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
+    constexpr int kW = kD / 32;              // words of a key row that a lane loads
+    constexpr int kVW = kD / 64;             // words of a value row that a lane loads
+    constexpr int kRows = 8 * kNT;
+    using S = Smem<kD, kNT>;
+    using L = Slot<kD>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Run run;
+    __shared__ int64_t sums[kThreads / 32];
+    __shared__ unsigned last_one;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
+    uint64_t* empty = full + kWarps * kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+    const int group = a.q_heads / a.c.kv_heads;
+
+    if (threadIdx.x < kWarps * kStages) {
+        tc::mbar_init(&full[threadIdx.x], 1);
+        tc::mbar_init(&empty[threadIdx.x], 1);
+        tc::fence_barrier_init();
+    }
+    find_run(a, &run, sums, status);         // synchronises
+    if (run.begin >= run.end) return;
+    Walk k = walk_start(a, run);
+    volatile int never = 0;                  // no abort flag: each wait is bounded by itself
+
+    if (warp == kWarps) {
+        // ---- copies: lane 4 w + part brings one part of warp w's step
+        const int w = lane >> 2, part = lane & 3;
+        const int sh = 31 - __clz(a.c.block_size);
+        const uint32_t row_bytes = part < 2 ? kD / 2 : 4;
+        const unsigned char* src = part < 2 ? a.c.codes : reinterpret_cast<const unsigned char*>(a.c.scales);
+        const int at = part < 2 ? part * L::kCodes : 2 * L::kCodes + (part - 2) * L::kScales;
+        const int pieces = a.c.block_size < kStep ? kStep / 16 : 1;      // pages of a step
+        const int tokens = kStep / pieces;
+        int stage = 0, turn = 0;
+        bool dead = false;
+        do {
+            for (int u = k.u0; u < k.u1; ++u) {
+                const int t0 = u * kUnit + w * kStep;
+                const bool have = t0 < k.w.kv && !dead;
+                int block[2] = {};
+                const int count = have ? min(pieces, (k.w.kv - t0 + tokens - 1) / tokens) : 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (i < count) block[i] = load_block(a, k.b, (t0 + i * tokens) >> sh, status);
+                uint64_t* bar = &full[w * kStages + stage];
+                if (have && turn > 0) {
+                    if (!tc::mbar_wait(&empty[w * kStages + stage], (turn - 1) & 1, &never, status)) dead = true;
+                }
+                const bool go = have && !dead;
+                if (go && part == 0)
+                    tc::mbar_arrive_expect_tx(bar, count * tokens * (kD + 8));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (go && i < count) {
+                        const int64_t row = ((static_cast<int64_t>(block[i]) * 2 + (part & 1)) * a.c.kv_heads + k.h) *
+                                                a.c.block_size + ((t0 + i * tokens) & (a.c.block_size - 1));
+                        bulk_load(smem + (w * kStages + stage) * L::kBytes + at + i * tokens * row_bytes,
+                                  src + row * row_bytes, tokens * row_bytes, bar);
+                    }
+                // a warp's ring turns with its own steps
+                if (have && ++stage == kStages) stage = 0, ++turn;
+            }
+        } while (walk_next(a, k));
+        return;
+    }
+
+    // ---- products
+    int stage = 0, turn = 0;
+    bool dead = false;
+    const unsigned char* ring = smem + warp * kStages * L::kBytes;
+    uint32_t* my_q = reinterpret_cast<uint32_t*>(smem + S::kQueries) + warp * (kNT * 8 * kD / 2);
+    float* s_max = reinterpret_cast<float*>(smem + S::kStats);
+    float* s_sum = s_max + kWarps * kRows;
+    do {
+        // queries: row g of each 8, the dimensions that go with this lane's key words
+        const int rows = k.w.rows * group;
+        uint32_t q[kNT == 1 ? 4 * kW : 1];
+        float qsum[kNT][2];
+        float factor;
+        {
+            uint4 raw[kNT][kW];
+            float top = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                const int r = nt * 8 + g;
+                const int64_t from = static_cast<int64_t>(k.w.begin + r / group) * a.q_token +
+                                     static_cast<int64_t>(k.h * group + r % group) * a.q_head + tq * (8 * kW);
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    raw[nt][i] = make_uint4(0, 0, 0, 0);
+                    if (r < rows) raw[nt][i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from + 8 * i);
+                    const uint32_t x[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = widen2<kDtype>(x[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            const int e = query_exponent(top);
+            const float down = power_of_two(-e);
+            factor = a.scale * kLog2e * power_of_two(e);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    const uint32_t x[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+                    float f[8];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 y = widen2<kDtype>(x[p]);
+                        f[2 * p] = y.x * down, f[2 * p + 1] = y.y * down;
+                    }
+                    uint32_t o[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        o[p] = pack_half2(f[p], f[p + 4]);
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&o[p]));
+                        sum += y.x + y.y;
+                    }
+                    if (kNT == 1) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) q[(4 * i + p) % (kNT == 1 ? 4 * kW : 1)] = o[p];
+                    } else {
+                        *reinterpret_cast<uint4*>(my_q + ((nt * kW + i) * 32 + lane) * 4) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                sum += __shfl_xor_sync(~0u, sum, 1);
+                sum += __shfl_xor_sync(~0u, sum, 2);
+                qsum[nt][0] = __shfl_sync(~0u, sum, 8 * tq);
+                qsum[nt][1] = __shfl_sync(~0u, sum, 8 * tq + 4);
+            }
+            __syncwarp();
+        }
+
+        float o[kVW * 4][kNT][4] = {};
+        float top[kNT][2], sum[kNT][2], flat[kNT][2];      // maximum, sum of p, sum of p (m + 8 s)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[nt][e] = -CUDART_INF_F, sum[nt][e] = 0.f, flat[nt][e] = 0.f;
+        float vdown = 0.f;                                  // 2^-E of the value steps; 0: none seen
+        const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1);   // every row sees what lies before
+
+        for (int u = k.u0; u < k.u1; ++u) {
+            const int t0 = u * kUnit + warp * kStep;
+            if (t0 >= k.w.kv || dead) continue;
+            if (!tc::mbar_wait(&full[warp * kStages + stage], turn & 1, &never, status)) {
+                dead = true;
+                continue;
+            }
+            const unsigned char* slot = ring + stage * L::kBytes;
+            const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + 2 * L::kCodes);
+            // first product
+            float s[2][kNT][4] = {};
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+                uint32_t bq[kNT][4];
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                    if (kNT == 1) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) bq[nt][p] = q[(4 * i + p) % (kNT == 1 ? 4 * kW : 1)];
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4*>(my_q + ((nt * kW + i) * 32 + lane) * 4);
+                        bq[nt][0] = x.x, bq[nt][1] = x.y, bq[nt][2] = x.z, bq[nt][3] = x.w;
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t lo[4], hi[4];
+                    decode_word(*reinterpret_cast<const uint32_t*>(slot + (mt * 16 + tile_token(g)) * (kD / 2) + tq * (kD / 8) + 4 * i), lo);
+                    decode_word(*reinterpret_cast<const uint32_t*>(slot + (mt * 16 + 8 + tile_token(g)) * (kD / 2) + tq * (kD / 8) + 4 * i), hi);
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt) {
+                        mma(s[mt][nt], lo[0], hi[0], lo[1], hi[1], bq[nt][0], bq[nt][1]);
+                        mma(s[mt][nt], lo[2], hi[2], lo[3], hi[3], bq[nt][2], bq[nt][3]);
+                    }
+                }
+            }
+            // logits in powers of two
+            const bool all = t0 + kStep <= clear;
+            float vs[4], vm[4];
+            float vtop = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {                    // tokens g, g + 8 of both tiles
+                const int j = (x >> 1) * 16 + (x & 1) * 8 + tile_token(g);
+                uint32_t ks = sc[j], vv = sc[kStep + j];
+                if (t0 + j >= k.w.kv) ks = vv = 0;
+                const float ss = bf16_lo(ks), mm = bf16_hi(ks);
+                const float sf = ss * factor, off = fmaf(8.f, ss, mm) * factor;
+                vs[x] = bf16_lo(vv);
+                vm[x] = fmaf(8.f, vs[x], bf16_hi(vv));
+                vtop = fmaxf(vtop, vs[x]);
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float& z = s[x >> 1][nt][(x & 1) * 2 + e];
+                        z = fmaf(sf, z, off * qsum[nt][e]);
+                    }
+            }
+            if (!all) {
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = nt * 8 + 2 * tq + e, i = r / group;
+                        uint64_t bits = 0;
+                        if (a.mask && r < rows) bits = a.mask[k.w.begin + i];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int j = t0 + (x >> 1) * 16 + (x & 1) * 8 + tile_token(g), back = j - k.w.first;
+                            const bool sees = j < k.w.kv && (a.mask ? back < 0 || (back < 64 && ((bits >> back) & 1)) : back <= i);
+                            if (!sees) s[x >> 1][nt][(x & 1) * 2 + e] = -CUDART_INF_F;
+                        }
+                    }
+            }
+            // raise the maximum, or the reference of the value steps, where they are passed
+            bool raise = vtop * vdown > kStepRoom || (vdown == 0.f && vtop > 0.f);
+            float peak[kNT][2];
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    peak[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+                    raise |= peak[nt][e] > top[nt][e] + kRaise;
+                }
+            if (__any_sync(~0u, raise)) {
+                uint32_t vbits = __reduce_max_sync(~0u, __float_as_uint(vtop));
+                const float was = vdown;
+                vbits &= 0x7F800000u;
+                float now = vbits ? __uint_as_float(0x7F000000u - vbits) : 0.f;
+                if (was != 0.f && (now == 0.f || now > was)) now = was;
+                vdown = now;
+                const float vfix = was == 0.f ? 1.f : now / was;
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float p = peak[nt][e];
+                        p = fmaxf(p, __shfl_xor_sync(~0u, p, 4));
+                        p = fmaxf(p, __shfl_xor_sync(~0u, p, 8));
+                        p = fmaxf(p, __shfl_xor_sync(~0u, p, 16));
+                        const float to = fmaxf(p, top[nt][e]);
+                        const float fix = top[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(top[nt][e] - to);
+                        top[nt][e] = to;
+                        sum[nt][e] *= fix;
+                        flat[nt][e] *= fix;
+#pragma unroll
+                        for (int m = 0; m < kVW * 4; ++m) {
+                            o[m][nt][e] *= fix * vfix;
+                            o[m][nt][2 + e] *= fix * vfix;
+                        }
+                    }
+            }
+            // weights
+            uint32_t pw[2][kNT][2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) vs[x] *= vdown;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                const float top0 = top[nt][0] == -CUDART_INF_F ? 0.f : top[nt][0];
+                const float top1 = top[nt][1] == -CUDART_INF_F ? 0.f : top[nt][1];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float z0 = s[x >> 1][nt][(x & 1) * 2], z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
+                    const float p0 = exp2_fast(z0 - top0), p1 = exp2_fast(z1 - top1);
+                    float w0 = p0 * vs[x], w1 = p1 * vs[x];
+                    float f0 = p0 * vm[x], f1 = p1 * vm[x];
+                    if (!all) {                              // a hidden value may be NaN
+                        if (z0 == -CUDART_INF_F) w0 = f0 = 0.f;
+                        if (z1 == -CUDART_INF_F) w1 = f1 = 0.f;
+                    }
+                    sum[nt][0] += p0, sum[nt][1] += p1;
+                    flat[nt][0] += f0, flat[nt][1] += f1;
+                    pw[x >> 1][nt][x & 1] = transpose8x8(pack_half2(w0, w1));
+                }
+            }
+            // second product
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                const unsigned char* v = slot + L::kCodes + mt * 16 * (kD / 2) + g * (kD / 16);
+                const int ta = (2 * tq) ^ (tq & 1), tb = (2 * tq + 1) ^ (tq & 1);
+                uint32_t wa[kVW], wb[kVW], wc[kVW], wd[kVW];
+                if (kVW == 2) {
+                    const uint2 xa = *reinterpret_cast<const uint2*>(v + ta * (kD / 2)), xb = *reinterpret_cast<const uint2*>(v + tb * (kD / 2));
+                    const uint2 xc = *reinterpret_cast<const uint2*>(v + (ta + 8) * (kD / 2)), xd = *reinterpret_cast<const uint2*>(v + (tb + 8) * (kD / 2));
+                    wa[0] = xa.x, wb[0] = xb.x, wc[0] = xc.x, wd[0] = xd.x;
+                    wa[kVW - 1] = xa.y, wb[kVW - 1] = xb.y, wc[kVW - 1] = xc.y, wd[kVW - 1] = xd.y;
+                } else {
+                    wa[0] = *reinterpret_cast<const uint32_t*>(v + ta * (kD / 2)), wb[0] = *reinterpret_cast<const uint32_t*>(v + tb * (kD / 2));
+                    wc[0] = *reinterpret_cast<const uint32_t*>(v + (ta + 8) * (kD / 2)), wd[0] = *reinterpret_cast<const uint32_t*>(v + (tb + 8) * (kD / 2));
+                }
+#pragma unroll
+                for (int i = 0; i < kVW; ++i)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t ab[4], cd[4];
+                        decode_word(permute(wa[i], wb[i], half ? 0x7632 : 0x5410), ab);
+                        decode_word(permute(wc[i], wd[i], half ? 0x7632 : 0x5410), cd);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt)
+                                mma(o[i * 4 + half * 2 + y][nt], ab[2 * y], ab[2 * y + 1], cd[2 * y], cd[2 * y + 1],
+                                    pw[mt][nt][0], pw[mt][nt][1]);
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&empty[warp * kStages + stage]);
+            if (++stage == kStages) stage = 0, ++turn;
+        }
+
+        // ---- merge the warps, 8 rows at a time
+        float* merge = reinterpret_cast<float*>(smem + S::kMerge);
+        const float vup = vdown == 0.f ? 0.f : 1.f / vdown;
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");   // the last piece's statistics are read
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    sum[nt][e] += __shfl_xor_sync(~0u, sum[nt][e], d);
+                    flat[nt][e] += __shfl_xor_sync(~0u, flat[nt][e], d);
+                }
+                if (g == 0) {
+                    s_max[warp * kRows + nt * 8 + 2 * tq + e] = top[nt][e];
+                    s_sum[warp * kRows + nt * 8 + 2 * tq + e] = sum[nt][e];
+                }
+            }
+        const bool whole = k.u0 == 0 && k.u1 == k.units;
+        float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (k.u0 == 0 ? 1 : 0)) * kPieceFloats;
+        constexpr int kLanesRow = kD / 4;                    // threads of a row: 4 dimensions each
+        const int my_row = threadIdx.x / kLanesRow, my_d = (threadIdx.x % kLanesRow) * 4;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * tq + e;
+                float peak = -CUDART_INF_F;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) peak = fmaxf(peak, s_max[w * kRows + nt * 8 + r]);
+                const float fix = top[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(top[nt][e] - peak);
+#pragma unroll
+                for (int m = 0; m < kVW * 4; ++m) {
+                    const int c = g * (kD / 16) + m;
+                    float2 x;
+                    x.x = fix == 0.f ? 0.f : fmaf(o[m][nt][e], vup, flat[nt][e]) * fix;
+                    x.y = fix == 0.f ? 0.f : fmaf(o[m][nt][2 + e], vup, flat[nt][e]) * fix;
+                    *reinterpret_cast<float2*>(merge + (warp * 8 + r) * kD + 2 * (c ^ merge_move<kD>(r, c))) = x;
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+            const int r = nt * 8 + my_row;
+            if (my_row < 8 && r < rows) {
+                float peak = -CUDART_INF_F, total = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) peak = fmaxf(peak, s_max[w * kRows + r]);
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int c = my_d / 2, z = merge_move<kD>(my_row, c);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float m = s_max[w * kRows + r];
+                    if (m != -CUDART_INF_F) total += s_sum[w * kRows + r] * exp2_fast(m - peak);
+                    float4 y = *reinterpret_cast<const float4*>(merge + (w * 8 + my_row) * kD + 2 * ((c ^ z) & ~1));
+                    if (z & 1) y = make_float4(y.z, y.w, y.x, y.y);
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
+                if (whole) {
+                    const float inv = total == 0.f ? 0.f : 1.f / total;
+                    const int64_t at = static_cast<int64_t>(k.w.begin + r / group) * a.q_heads + k.h * group + r % group;
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * kD + my_d) =
+                        make_uint2(narrow2<kDtype>(x.x * inv, x.y * inv), narrow2<kDtype>(x.z * inv, x.w * inv));
+                    if (a.lse && my_d == 0) a.lse[at] = total == 0.f ? -CUDART_INF_F : (peak + log2f(total)) * kLn2;
+                } else {
+                    __stcg(reinterpret_cast<float4*>(piece + r * kD + my_d), x);
+                    if (my_d == 0) {
+                        __stcg(piece + kPieceRows * kD + r, peak);
+                        __stcg(piece + kPieceRows * kD + kPieceRows + r, total);
+                    }
+                }
+            }
+        }
+        if (!whole) {
+            // the CTAs that share this (request, head): from the one with its first unit on
+            const int64_t total = run.total, n = run.ctas;
+            const int c0 = static_cast<int>(((k.base + 1) * n - 1) / total);
+            const int c1 = static_cast<int>(((k.base + k.units) * n - 1) / total);
+            __threadfence();
+            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+            if (threadIdx.x == 0) {
+                const unsigned before = atomicAdd(&arrivals[c0], 1u);
+                last_one = before == static_cast<unsigned>(c1 - c0);
+                if (last_one) arrivals[c0] = 0;              // for the next launch
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+            if (last_one) {
+                __threadfence();
+                for (int r = my_row; r < rows; r += kWarps * 32 / kLanesRow) {
+                    float peak = -CUDART_INF_F, sum_all = 0.f;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* from = scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats;
+                        const float m = __ldcg(from + kPieceRows * kD + r), t = __ldcg(from + kPieceRows * kD + kPieceRows + r);
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + r * kD + my_d));
+                        if (m == -CUDART_INF_F) continue;
+                        const float to = fmaxf(peak, m);
+                        const float fx = peak == -CUDART_INF_F ? 0.f : exp2_fast(peak - to), fy = exp2_fast(m - to);
+                        peak = to;
+                        sum_all = sum_all * fx + t * fy;
+                        x.x = x.x * fx + y.x * fy, x.y = x.y * fx + y.y * fy;
+                        x.z = x.z * fx + y.z * fy, x.w = x.w * fx + y.w * fy;
+                    }
+                    const float inv = sum_all == 0.f ? 0.f : 1.f / sum_all;
+                    const int64_t at = static_cast<int64_t>(k.w.begin + r / group) * a.q_heads + k.h * group + r % group;
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * kD + my_d) =
+                        make_uint2(narrow2<kDtype>(x.x * inv, x.y * inv), narrow2<kDtype>(x.z * inv, x.w * inv));
+                    if (a.lse && my_d == 0) a.lse[at] = sum_all == 0.f ? -CUDART_INF_F : (peak + log2f(sum_all)) * kLn2;
+                }
+            }
+        }
+    } while (walk_next(a, k));
+}
+
+template <int kD, int kDtype, int kNT>
+cudaError_t launch_window(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+    using S = Smem<kD, kNT>;
+    auto* kernel = window_kernel<kD, kDtype, kNT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    if (e != cudaSuccess) return e;
+    // as many CTAs as are resident at once, and no more than there can be units
+    const int64_t most = static_cast<int64_t>(a.requests) * a.c.kv_heads *
+                         ((static_cast<int64_t>(a.width) * a.c.block_size + kUnit - 1) / kUnit);
+    const int64_t resident = static_cast<int64_t>(ctx.sm_count) * (kNT == 1 ? 2 : 1);
+    const int grid = static_cast<int>(most < resident ? most : resident);
+    kernel<<<grid, kThreads, S::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals, ctx.s.status);
+    return cudaGetLastError();
+}
+
+template <int kD, int kDtype>
+cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+    const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads);
+    if (rows <= 8) return launch_window<kD, kDtype, 1>(ctx, a, st);
+    if (rows <= 16) return launch_window<kD, kDtype, 2>(ctx, a, st);
+    return launch_window<kD, kDtype, 4>(ctx, a, st);
+}
+
+// ---------------------------------------------------------------------------
+// any number of rows, one warp a row (placeholder of the chunk kernel)
+// ---------------------------------------------------------------------------
 
 template <int kDtype>
 __device__ __forceinline__ float widen(const void* p, int64_t i) {
@@ -93,7 +745,14 @@ void launch_dim(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t 
 
 }  // namespace
 
+size_t attention_scratch_floats(int sm_count) { return static_cast<size_t>(sm_count) * 2 * 2 * kPieceFloats; }
+
 cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+    if (static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= 32) {
+        if (a.c.head_dim == 64)
+            return dtype == HC_DTYPE_BF16 ? launch_rows<64, HC_DTYPE_BF16>(ctx, a, st) : launch_rows<64, HC_DTYPE_FP16>(ctx, a, st);
+        return dtype == HC_DTYPE_BF16 ? launch_rows<128, HC_DTYPE_BF16>(ctx, a, st) : launch_rows<128, HC_DTYPE_FP16>(ctx, a, st);
+    }
     if (a.c.head_dim == 64) launch_dim<64>(ctx, a, dtype, st);
     else launch_dim<128>(ctx, a, dtype, st);
     return cudaGetLastError();

@@ -91,12 +91,21 @@ struct Ctx {
     // tokens whose lo the last tile-path call left in lo3 (0: none)
     int lo_tokens = 0;
     mutable WupMapCache wu_maps;     // decode: W_up tensor maps by address
+    // attention over the 4-bit cache: fp32 sums of the pieces of requests that several
+    // CTAs share, and per CTA the number of them that have written theirs (0 between
+    // launches)
+    float* attn_pieces = nullptr;
+    unsigned* attn_arrivals = nullptr;
 };
 
 // The current device's context, or nullptr with *err set; and whether p is 16-byte
 // aligned memory of `device` that kernels may dereference (hc_api.cu).
 Ctx* current_ctx(int* err);
 int check_ptr(const void* p, int device);
+
+// Floats of Ctx::attn_pieces (hc_attention.cu); CTAs that may share requests.
+size_t attention_scratch_floats(int sm_count);
+constexpr int kAttnCtasPerSm = 2;
 
 // 128-token tiles of the partials.
 inline int partial_tiles(int max_tokens) { return (max_tokens + 127) / 128; }
