@@ -11,12 +11,14 @@
 //   transposed, are the left operand of the second product. (tcgen05 would take its
 //   operands from shared or tensor memory: a second trip for every decoded value, four
 //   times its bytes in the cache, and 128 rows where 8 are wanted.)
-// * S_j = s_j (q . (c_j - 8)) + (m_j + 8 s_j) sum(q): the codes enter as whole numbers,
-//   exactly, and step and minimum are applied to the product in fp32, once a token and
-//   row instead of once a value. Likewise o = sum w_j (c_j - 8) + sum p_j (m_j + 8 s_j)
-//   with w_j = p_j s_j. w_j is rounded to fp16 (11 bits: the one rounding of the
-//   product), after division by a power of two near the largest step seen; p_j itself
-//   is summed in fp32.
+// * S_j = s_j (q . c_j) + m_j sum(q): the codes enter as whole numbers, exactly (as fp16
+//   subnormals, one logical operation for two), and step and minimum are applied to the
+//   product in fp32, once a token and row instead of once a value. Likewise o = sum w_j
+//   (c_j - 8) + sum p_j (m_j + 8 s_j) with w_j = p_j s_j. w_j is rounded to fp16 (11 bits:
+//   the one rounding of the product), after division by a power of two near the largest
+//   step seen; p_j itself is summed in fp32. 8 sum w_j comes from the same rounded
+//   weights, by one more product with a constant, so that their errors meet c_j - 8 and
+//   not c_j, which is three times as large.
 // * The order of dimensions within a product is free as long as both operands agree, and
 //   so is that of the tokens: both follow from which words a lane loads (16 bytes of a
 //   key row, 8 of a value row), so that no value moves between lanes. Only the weights
@@ -26,7 +28,8 @@
 //   within fp16, sums in fp32): one vote a step instead of a reduction over lanes.
 //
 // Work is cut evenly, whatever the lengths: the units (256 tokens of one request and kv
-// head) are numbered through, and each CTA takes an equal run of them. A CTA's eight
+// head) are numbered through, and each CTA takes an equal run of them (with two more
+// counted for each request and head, for its start and merge). A CTA's eight
 // warps take 32 tokens of each unit each and merge at the end of a (request, head). One
 // that is split between CTAs is joined by the last of them to finish, in the order of
 // the CTAs, from fp32 sums in scratch of a fixed size (a CTA can have at most two such
@@ -36,20 +39,24 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hc_attention.cuh"
 
 namespace hc {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = (kWarps + 1) * 32;      // and one warp that issues the copies
+constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                        // tokens of a warp's step
 constexpr int kUnit = kWarps * kStep;            // tokens of a unit
-constexpr int kStages = 2;                       // steps of a warp's ring
 constexpr float kRaise = 8.f;                    // log2 by which a logit may pass the maximum
 constexpr float kStepRoom = 16.f;                // factor by which a step may pass the reference
 
-// A step's ring slot: key codes, value codes, key scales, value scales of 32 tokens.
+constexpr int kStages = 3;                       // steps of a warp's ring
+constexpr int kPieceCost = 2;                    // what a piece costs beside its units, in units
+
+// A step's slot in a warp's ring: key codes, value codes, key scales, value scales.
 template <int kD>
 struct Slot {
     static constexpr int kCodes = kStep * kD / 2;
@@ -59,40 +66,46 @@ struct Slot {
 
 template <int kD, int kNT>
 struct Smem {
-    static constexpr int kRing = kWarps * kStages * Slot<kD>::kBytes;
-    static constexpr int kMerge = kRing;                               // [kWarps][8][kD] floats
-    static constexpr int kQueries = kMerge + kWarps * 8 * kD * 4;      // fragments, a copy a warp
-    static constexpr int kQueryBytes = kNT > 1 ? kWarps * kNT * 8 * kD * 2 : 0;
+    static constexpr int kMerge = kWarps * kStages * Slot<kD>::kBytes;  // 2 [kWarps][32] float4
+    static constexpr int kQueries = kMerge + 2 * kWarps * 32 * 16;
+    static constexpr int kQueryBytes = kNT > 1 ? kWarps * kNT * 8 * kD * 2 : 0;   // fragments, a copy a warp
     static constexpr int kStats = kQueries + kQueryBytes;              // max, sum [kWarps][8 kNT]
-    static constexpr int kBars = kStats + 2 * kWarps * 8 * kNT * 4;
-    static constexpr int kBytes = kBars + 2 * kWarps * kStages * 8;
+    static constexpr int kBytes = kStats + 2 * kWarps * 8 * kNT * 4;
 };
 
 // Fixed scratch: per CTA two pieces of up to 32 rows, and a counter of arrivals.
 constexpr int kPieceRows = 32;
 constexpr int kPieceFloats = kPieceRows * (128 + 2);
 
-// The walk of a CTA through its run of units, piece by piece.
+// The walk of a CTA through its run. Runs are cut in slots: a (request, head) has its
+// units, and before them kPieceCost slots that stand for the work of starting and merging.
 struct Walk {
-    int b, h, u0, u1, units;
-    int64_t left, base;          // units left, and the number of unit (b, h, 0)
+    int b, h, u0, u1, units;     // the units [u0, u1) of (b, h), of `units`
+    int64_t left, base;          // slots left, and the number of (b, h)'s first slot
     Window w;
 };
 
 __device__ __forceinline__ int window_units(const Window& w) {
     return w.n > 0 ? max((w.kv + kUnit - 1) / kUnit, 1) : 0;
 }
+__device__ __forceinline__ int64_t window_slots(const AttentionArgs& a, const Window& w) {
+    const int units = window_units(w);
+    return units ? static_cast<int64_t>(units + kPieceCost) * a.c.kv_heads : 0;
+}
 
-__device__ __forceinline__ void walk_piece(Walk& k) {
-    k.u1 = static_cast<int>(min(static_cast<int64_t>(k.units), k.u0 + k.left));
-    k.left -= k.u1 - k.u0;
+// Takes the slots of (b, h) from `from` on; false if none of them is a unit.
+__device__ __forceinline__ bool walk_piece(Walk& k, int from) {
+    const int64_t to = min(static_cast<int64_t>(k.units + kPieceCost), from + k.left);
+    k.left -= to - from;
+    k.u0 = max(from - kPieceCost, 0);
+    k.u1 = static_cast<int>(to) - kPieceCost;
+    return k.u1 > k.u0;
 }
 
 // To the next piece; false at the end of the run.
 __device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
     if (k.left == 0) return false;
-    k.base += k.units;
-    k.u0 = 0;
+    k.base += k.units + kPieceCost;
     if (++k.h == a.c.kv_heads) {
         k.h = 0;
         do {
@@ -102,8 +115,7 @@ __device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
             k.units = window_units(k.w);
         } while (k.units == 0);
     }
-    walk_piece(k);
-    return true;
+    return walk_piece(k, 0);     // a run that ends within the leading slots has no unit there
 }
 
 struct Run {
@@ -111,15 +123,15 @@ struct Run {
     int64_t offset, begin, end, total, ctas;
 };
 
-// The CTA's run of units: every CTA sums the units of all requests, and the thread whose
-// share of the requests holds the run's first unit says where it lies.
+// The CTA's run: every CTA sums the slots of all requests, and the thread whose share of
+// the requests holds the run's first slot says where it lies.
 __device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* status) {
     const int tid = threadIdx.x;
     const int per = (a.requests + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += static_cast<int64_t>(window_units(load_window(a, b, blockIdx.x == 0 ? status : nullptr))) * a.c.kv_heads;
+        mine += window_slots(a, load_window(a, b, blockIdx.x == 0 ? status : nullptr));
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -133,7 +145,7 @@ __device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* s
         if (w == (tid >> 5)) upto += total;
         total += sums[w];
     }
-    // CTAs beyond the number of units have none, so that no run before them is empty
+    // CTAs beyond the number of slots have none, so that no run before them is empty
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), i = blockIdx.x;
     const int64_t begin = i < ctas ? total * i / ctas : total, end = i < ctas ? total * (i + 1) / ctas : total;
     if (tid == 0) {
@@ -145,7 +157,7 @@ __device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* s
     if (begin < end && begin < upto && begin >= upto - mine) {
         int64_t at = upto - mine;
         for (int b = b0; b < b1; ++b) {
-            const int64_t n = static_cast<int64_t>(window_units(load_window(a, b, nullptr))) * a.c.kv_heads;
+            const int64_t n = window_slots(a, load_window(a, b, nullptr));
             if (begin < at + n) {
                 run->b = b;
                 run->offset = begin - at;
@@ -157,17 +169,18 @@ __device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* s
     __syncthreads();
 }
 
-__device__ __forceinline__ Walk walk_start(const AttentionArgs& a, const Run& run) {
-    Walk k;
+// The first piece of the run; false if it has none.
+__device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, Walk& k) {
+    if (run.begin >= run.end) return false;
     k.b = run.b;
     k.w = load_window(a, k.b, nullptr);
     k.units = window_units(k.w);
-    k.h = static_cast<int>(run.offset / k.units);
-    k.u0 = static_cast<int>(run.offset - static_cast<int64_t>(k.h) * k.units);
+    const int slots = k.units + kPieceCost;
+    k.h = static_cast<int>(run.offset / slots);
+    const int from = static_cast<int>(run.offset - static_cast<int64_t>(k.h) * slots);
     k.left = run.end - run.begin;
-    k.base = run.begin - k.u0;
-    walk_piece(k);
-    return k;
+    k.base = run.begin - from;
+    return walk_piece(k, from) || walk_next(a, k);
 }
 
 // D += A (16 x 16, row-major fragments) B (16 x 8), fp16 with fp32 sums.
@@ -194,14 +207,6 @@ __device__ __forceinline__ uint32_t permute(uint32_t x, uint32_t y, uint32_t how
 // would do; this one keeps the lanes that load together on different banks.
 __device__ __forceinline__ int tile_token(int m) { return m ^ ((m >> 1) & 1); }
 
-// Where float pair `c` (of kD / 2) of row `row` lies in the merge buffer's row: moved
-// within its neighbourhood so that the lanes of a warp, which hold pairs kD / 16 apart,
-// store to different banks.
-template <int kD>
-__device__ __forceinline__ int merge_move(int row, int c) {
-    return ((c / (kD / 16)) & 7) ^ ((row >> 1) & 1);
-}
-
 template <int kD, int kDtype, int kNT>
 __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     window_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
@@ -214,72 +219,64 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     __shared__ Run run;
     __shared__ int64_t sums[kThreads / 32];
     __shared__ unsigned last_one;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
-    uint64_t* empty = full + kWarps * kStages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int group = a.q_heads / a.c.kv_heads;
 
-    if (threadIdx.x < kWarps * kStages) {
-        tc::mbar_init(&full[threadIdx.x], 1);
-        tc::mbar_init(&empty[threadIdx.x], 1);
-        tc::fence_barrier_init();
-    }
     find_run(a, &run, sums, status);         // synchronises
-    if (run.begin >= run.end) return;
-    Walk k = walk_start(a, run);
-    volatile int never = 0;                  // no abort flag: each wait is bounded by itself
+    Walk k;
+    if (!walk_start(a, run, k)) return;
 
-    if (warp == kWarps) {
-        // ---- copies: lane 4 w + part brings one part of warp w's step
-        const int w = lane >> 2, part = lane & 3;
-        const int sh = 31 - __clz(a.c.block_size);
-        const uint32_t row_bytes = part < 2 ? kD / 2 : 4;
-        const unsigned char* src = part < 2 ? a.c.codes : reinterpret_cast<const unsigned char*>(a.c.scales);
-        const int at = part < 2 ? part * L::kCodes : 2 * L::kCodes + (part - 2) * L::kScales;
-        const int pieces = a.c.block_size < kStep ? kStep / 16 : 1;      // pages of a step
-        const int tokens = kStep / pieces;
-        int stage = 0, turn = 0;
-        bool dead = false;
-        do {
-            for (int u = k.u0; u < k.u1; ++u) {
-                const int t0 = u * kUnit + w * kStep;
-                const bool have = t0 < k.w.kv && !dead;
-                int block[2] = {};
-                const int count = have ? min(pieces, (k.w.kv - t0 + tokens - 1) / tokens) : 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (i < count) block[i] = load_block(a, k.b, (t0 + i * tokens) >> sh, status);
-                uint64_t* bar = &full[w * kStages + stage];
-                if (have && turn > 0) {
-                    if (!tc::mbar_wait(&empty[w * kStages + stage], (turn - 1) & 1, &never, status)) dead = true;
-                }
-                const bool go = have && !dead;
-                if (go && part == 0)
-                    tc::mbar_arrive_expect_tx(bar, count * tokens * (kD + 8));
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (go && i < count) {
-                        const int64_t row = ((static_cast<int64_t>(block[i]) * 2 + (part & 1)) * a.c.kv_heads + k.h) *
-                                                a.c.block_size + ((t0 + i * tokens) & (a.c.block_size - 1));
-                        bulk_load(smem + (w * kStages + stage) * L::kBytes + at + i * tokens * row_bytes,
-                                  src + row * row_bytes, tokens * row_bytes, bar);
-                    }
-                // a warp's ring turns with its own steps
-                if (have && ++stage == kStages) stage = 0, ++turn;
-            }
-        } while (walk_next(a, k));
-        return;
-    }
-
-    // ---- products
-    int stage = 0, turn = 0;
-    bool dead = false;
-    const unsigned char* ring = smem + warp * kStages * L::kBytes;
     uint32_t* my_q = reinterpret_cast<uint32_t*>(smem + S::kQueries) + warp * (kNT * 8 * kD / 2);
     float* s_max = reinterpret_cast<float*>(smem + S::kStats);
     float* s_sum = s_max + kWarps * kRows;
-    do {
+    const int sh = 31 - __clz(a.c.block_size);
+    const int64_t to_values = static_cast<int64_t>(a.c.kv_heads) * a.c.block_size;   // groups from keys to values
+    const unsigned char* ring = smem + warp * (kStages * L::kBytes);
+    const uint32_t ring_at = tc::smem_u32(ring) + lane * 16;
+            // the blocks that hold the two halves of this warp's step of unit u
+            int ids[2];
+            auto look_up = [&](const Walk& k, int u) {
+                const int t0 = u * kUnit + warp * kStep;
+    #pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    ids[i] = u < k.u1 && t0 + 16 * i < k.w.kv ? load_block(a, k.b, (t0 + 16 * i) >> sh, status) : 0;
+            };
+            // brings them to a slot of the ring, 16 bytes a lane (a group of copies, if an empty one)
+            auto fetch = [&](const Walk& k, int u, int slot) {
+                const int t0 = u * kUnit + warp * kStep;
+                if (u < k.u1 && t0 < k.w.kv) {
+                    const uint32_t to = ring_at + slot * L::kBytes;
+                    const bool two = t0 + 16 < k.w.kv;
+                    const int64_t at0 = (static_cast<int64_t>(ids[0]) * 2 * a.c.kv_heads + k.h) * a.c.block_size + (t0 & (a.c.block_size - 1));
+                    const int64_t at1 = (static_cast<int64_t>(ids[1]) * 2 * a.c.kv_heads + k.h) * a.c.block_size + ((t0 + 16) & (a.c.block_size - 1));
+                    constexpr int kChunks = kD / 32;             // 512-byte pieces of the step's keys
+    #pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int half = i * 2 / kChunks;
+                        if (half && !two) continue;
+                        const unsigned char* from = a.c.codes + (half ? at1 : at0) * (kD / 2) + (i - half * (kChunks / 2)) * 512 + lane * 16;
+                        copy16(to + i * 512, from);
+                        copy16(to + L::kCodes + i * 512, from + to_values * (kD / 2));
+                    }
+                    // scales: 16 bytes hold 4 tokens; lanes 0-7 keys, 8-15 values
+                    if (lane < 16 && ((lane & 4) == 0 || two))
+                        copy16(to + 2 * L::kCodes, a.c.scales + (((lane & 4) ? at1 : at0) + (lane >= 8 ? to_values : 0)) * 2 + (lane & 3) * 8);
+                }
+                copy_commit();
+            };
+    // a piece's first steps, on their way before the piece before it is merged
+    auto begin = [&](const Walk& k) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            look_up(k, k.u0 + i);
+            fetch(k, k.u0 + i, i);
+        }
+        look_up(k, k.u0 + kStages - 1);
+    };
+    begin(k);
+    bool more = true;
+    while (more) {
+        int slot = 0;
         // queries: row g of each 8, the dimensions that go with this lane's key words
         const int rows = k.w.rows * group;
         uint32_t q[kNT == 1 ? 4 * kW : 1];
@@ -320,14 +317,14 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         const float2 y = widen2<kDtype>(x[p]);
-                        f[2 * p] = y.x * down, f[2 * p + 1] = y.y * down;
+                        f[2 * p] = y.x * down, f[2 * p + 1] = y.y * (down * kOdd);
                     }
                     uint32_t o[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         o[p] = pack_half2(f[p], f[p + 4]);
                         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&o[p]));
-                        sum += y.x + y.y;
+                        sum += (p & 1) ? (y.x + y.y) * (1.f / kOdd) : y.x + y.y;
                     }
                     if (kNT == 1) {
 #pragma unroll
@@ -344,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             __syncwarp();
         }
 
-        float o[kVW * 4][kNT][4] = {};
+        float o[kVW * 4][kNT][4] = {}, eight[kNT][4] = {};   // and 8 times the sum of the weights
         float top[kNT][2], sum[kNT][2], flat[kNT][2];      // maximum, sum of p, sum of p (m + 8 s)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
@@ -353,17 +350,26 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         float vdown = 0.f;                                  // 2^-E of the value steps; 0: none seen
         const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1);   // every row sees what lies before
 
-        for (int u = k.u0; u < k.u1; ++u) {
+        // One step. kTail: some of its tokens are hidden from some rows, or lie behind the end.
+        auto step = [&](auto tail, int u) {
+            constexpr bool kTail = decltype(tail)::value;
             const int t0 = u * kUnit + warp * kStep;
-            if (t0 >= k.w.kv || dead) continue;
-            if (!tc::mbar_wait(&full[warp * kStages + stage], turn & 1, &never, status)) {
-                dead = true;
-                continue;
-            }
-            const unsigned char* slot = ring + stage * L::kBytes;
-            const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + 2 * L::kCodes);
+            const unsigned char* in = ring + slot * L::kBytes;
+            const uint32_t* scales = reinterpret_cast<const uint32_t*>(in + 2 * L::kCodes);
             // first product
             float s[2][kNT][4] = {};
+            uint32_t kw[4][kW];                              // tokens g, g + 8 of both tiles
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const unsigned char* from = in + (x * 8 + tile_token(g)) * (kD / 2) + tq * (kD / 8);
+                if (kW == 4) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(from);
+                    kw[x][0] = y.x, kw[x][1] = y.y, kw[x][kW - 2] = y.z, kw[x][kW - 1] = y.w;
+                } else {
+                    const uint2 y = *reinterpret_cast<const uint2*>(from);
+                    kw[x][0] = y.x, kw[x][1] = y.y;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
                 uint32_t bq[kNT][4];
@@ -380,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     uint32_t lo[4], hi[4];
-                    decode_word(*reinterpret_cast<const uint32_t*>(slot + (mt * 16 + tile_token(g)) * (kD / 2) + tq * (kD / 8) + 4 * i), lo);
-                    decode_word(*reinterpret_cast<const uint32_t*>(slot + (mt * 16 + 8 + tile_token(g)) * (kD / 2) + tq * (kD / 8) + 4 * i), hi);
+                    decode_word(kw[2 * mt][i], lo);
+                    decode_word(kw[2 * mt + 1][i], hi);
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt) {
                         mma(s[mt][nt], lo[0], hi[0], lo[1], hi[1], bq[nt][0], bq[nt][1]);
@@ -390,16 +396,14 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 }
             }
             // logits in powers of two
-            const bool all = t0 + kStep <= clear;
             float vs[4], vm[4];
             float vtop = 0.f;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {                    // tokens g, g + 8 of both tiles
-                const int j = (x >> 1) * 16 + (x & 1) * 8 + tile_token(g);
-                uint32_t ks = sc[j], vv = sc[kStep + j];
-                if (t0 + j >= k.w.kv) ks = vv = 0;
-                const float ss = bf16_lo(ks), mm = bf16_hi(ks);
-                const float sf = ss * factor, off = fmaf(8.f, ss, mm) * factor;
+                const int j = x * 8 + tile_token(g);
+                uint32_t kk = scales[j], vv = scales[kStep + j];
+                if (kTail && t0 + j >= k.w.kv) kk = vv = 0;
+                const float sf = bf16_lo(kk) * (factor * kCodeUp), off = bf16_hi(kk) * factor;
                 vs[x] = bf16_lo(vv);
                 vm[x] = fmaf(8.f, vs[x], bf16_hi(vv));
                 vtop = fmaxf(vtop, vs[x]);
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                         z = fmaf(sf, z, off * qsum[nt][e]);
                     }
             }
-            if (!all) {
+            if (kTail) {
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                         if (a.mask && r < rows) bits = a.mask[k.w.begin + i];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int j = t0 + (x >> 1) * 16 + (x & 1) * 8 + tile_token(g), back = j - k.w.first;
+                            const int j = t0 + x * 8 + tile_token(g), back = j - k.w.first;
                             const bool sees = j < k.w.kv && (a.mask ? back < 0 || (back < 64 && ((bits >> back) & 1)) : back <= i);
                             if (!sees) s[x >> 1][nt][(x & 1) * 2 + e] = -CUDART_INF_F;
                         }
@@ -458,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                         top[nt][e] = to;
                         sum[nt][e] *= fix;
                         flat[nt][e] *= fix;
+                        eight[nt][e] *= fix * vfix;
 #pragma unroll
                         for (int m = 0; m < kVW * 4; ++m) {
                             o[m][nt][e] *= fix * vfix;
@@ -471,45 +476,46 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             for (int x = 0; x < 4; ++x) vs[x] *= vdown;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
-                const float top0 = top[nt][0] == -CUDART_INF_F ? 0.f : top[nt][0];
-                const float top1 = top[nt][1] == -CUDART_INF_F ? 0.f : top[nt][1];
+                const float top0 = kTail && top[nt][0] == -CUDART_INF_F ? 0.f : top[nt][0];
+                const float top1 = kTail && top[nt][1] == -CUDART_INF_F ? 0.f : top[nt][1];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float z0 = s[x >> 1][nt][(x & 1) * 2], z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
                     const float p0 = exp2_fast(z0 - top0), p1 = exp2_fast(z1 - top1);
-                    float w0 = p0 * vs[x], w1 = p1 * vs[x];
-                    float f0 = p0 * vm[x], f1 = p1 * vm[x];
-                    if (!all) {                              // a hidden value may be NaN
-                        if (z0 == -CUDART_INF_F) w0 = f0 = 0.f;
-                        if (z1 == -CUDART_INF_F) w1 = f1 = 0.f;
+                    float w0 = p0 * vs[x], w1 = p1 * vs[x], m0 = vm[x], m1 = vm[x];
+                    if (kTail) {                             // a hidden value may be NaN
+                        if (z0 == -CUDART_INF_F) w0 = m0 = 0.f;
+                        if (z1 == -CUDART_INF_F) w1 = m1 = 0.f;
                     }
                     sum[nt][0] += p0, sum[nt][1] += p1;
-                    flat[nt][0] += f0, flat[nt][1] += f1;
+                    flat[nt][0] = fmaf(p0, m0, flat[nt][0]), flat[nt][1] = fmaf(p1, m1, flat[nt][1]);
                     pw[x >> 1][nt][x & 1] = transpose8x8(pack_half2(w0, w1));
                 }
             }
             // second product
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-                const unsigned char* v = slot + L::kCodes + mt * 16 * (kD / 2) + g * (kD / 16);
-                const int ta = (2 * tq) ^ (tq & 1), tb = (2 * tq + 1) ^ (tq & 1);
-                uint32_t wa[kVW], wb[kVW], wc[kVW], wd[kVW];
-                if (kVW == 2) {
-                    const uint2 xa = *reinterpret_cast<const uint2*>(v + ta * (kD / 2)), xb = *reinterpret_cast<const uint2*>(v + tb * (kD / 2));
-                    const uint2 xc = *reinterpret_cast<const uint2*>(v + (ta + 8) * (kD / 2)), xd = *reinterpret_cast<const uint2*>(v + (tb + 8) * (kD / 2));
-                    wa[0] = xa.x, wb[0] = xb.x, wc[0] = xc.x, wd[0] = xd.x;
-                    wa[kVW - 1] = xa.y, wb[kVW - 1] = xb.y, wc[kVW - 1] = xc.y, wd[kVW - 1] = xd.y;
-                } else {
-                    wa[0] = *reinterpret_cast<const uint32_t*>(v + ta * (kD / 2)), wb[0] = *reinterpret_cast<const uint32_t*>(v + tb * (kD / 2));
-                    wc[0] = *reinterpret_cast<const uint32_t*>(v + (ta + 8) * (kD / 2)), wd[0] = *reinterpret_cast<const uint32_t*>(v + (tb + 8) * (kD / 2));
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+                    mma(eight[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pw[mt][nt][0], pw[mt][nt][1]);
+                uint32_t vw[4][kVW];                         // tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const unsigned char* from = in + L::kCodes + (mt * 16 + tile_token(2 * tq + (x & 1)) + (x >> 1) * 8) * (kD / 2) + g * (kD / 16);
+                    if (kVW == 2) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(from);
+                        vw[x][0] = y.x, vw[x][kVW - 1] = y.y;
+                    } else {
+                        vw[x][0] = *reinterpret_cast<const uint32_t*>(from);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < kVW; ++i)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t ab[4], cd[4];
-                        decode_word(permute(wa[i], wb[i], half ? 0x7632 : 0x5410), ab);
-                        decode_word(permute(wc[i], wd[i], half ? 0x7632 : 0x5410), cd);
+                        decode_word(permute(vw[0][i], vw[1][i], half ? 0x7632 : 0x5410), ab);
+                        decode_word(permute(vw[2][i], vw[3][i], half ? 0x7632 : 0x5410), cd);
 #pragma unroll
                         for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -518,15 +524,30 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                                     pw[mt][nt][0], pw[mt][nt][1]);
                     }
             }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&empty[warp * kStages + stage]);
-            if (++stage == kStages) stage = 0, ++turn;
+        };
+        for (int u = k.u0; u < k.u1; ++u) {
+            const int t = u * kUnit + warp * kStep;
+            if (t >= k.w.kv) break;
+            copy_wait<kStages - 2>();
+            __syncwarp();                                    // every lane's copies, and its reads of the slot before
+            fetch(k, u + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+            look_up(k, u + kStages);
+            if (t + kStep <= clear) step(std::false_type(), u);
+            else step(std::true_type(), u);
+            if (++slot == kStages) slot = 0;
         }
+        copy_wait<0>();
+        __syncwarp();
+        const Walk done = k;
+        more = walk_next(a, k);
+        if (more) begin(k);
 
-        // ---- merge the warps, 8 rows at a time
-        float* merge = reinterpret_cast<float*>(smem + S::kMerge);
-        const float vup = vdown == 0.f ? 0.f : 1.f / vdown;
+        // ---- merge the warps: their fragments lie alike, so that unit m of 4 values a lane
+        // is exchanged through [warp][lane] and summed by warp m % 8
+        float4* merge = reinterpret_cast<float4*>(smem + S::kMerge);
+        const float vup = vdown == 0.f ? 0.f : kCodeUp / vdown;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");   // the last piece's statistics are read
+        // rows 2 tq and 2 tq + 1 of each 8
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -541,56 +562,72 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     s_sum[warp * kRows + nt * 8 + 2 * tq + e] = sum[nt][e];
                 }
             }
-        const bool whole = k.u0 == 0 && k.u1 == k.units;
-        float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (k.u0 == 0 ? 1 : 0)) * kPieceFloats;
-        constexpr int kLanesRow = kD / 4;                    // threads of a row: 4 dimensions each
-        const int my_row = threadIdx.x / kLanesRow, my_d = (threadIdx.x % kLanesRow) * 4;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        const bool whole = done.u0 == 0 && done.u1 == done.units;
+        float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (done.u0 == 0 ? 1 : 0)) * kPieceFloats;
+        constexpr int kParts = kVW * 4;                      // units of one nt
+        auto write_rows = [&](int nt, int m, const float4& x, const float (&peak)[2], const float (&total)[2]) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 2 * tq + e;
-                float peak = -CUDART_INF_F;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) peak = fmaxf(peak, s_max[w * kRows + nt * 8 + r]);
-                const float fix = top[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(top[nt][e] - peak);
-#pragma unroll
-                for (int m = 0; m < kVW * 4; ++m) {
-                    const int c = g * (kD / 16) + m;
-                    float2 x;
-                    x.x = fix == 0.f ? 0.f : fmaf(o[m][nt][e], vup, flat[nt][e]) * fix;
-                    x.y = fix == 0.f ? 0.f : fmaf(o[m][nt][2 + e], vup, flat[nt][e]) * fix;
-                    *reinterpret_cast<float2*>(merge + (warp * 8 + r) * kD + 2 * (c ^ merge_move<kD>(r, c))) = x;
-                }
+                const int r = nt * 8 + 2 * tq + e;
+                if (r >= rows) continue;
+                const float inv = total[e] == 0.f ? 0.f : 1.f / total[e];
+                const int64_t at = static_cast<int64_t>(done.w.begin + r / group) * a.q_heads + done.h * group + r % group;
+                const int d = g * (kD / 8) + 2 * m;
+                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * kD + d) =
+                    e ? narrow2<kDtype>(x.y * inv, x.w * inv) : narrow2<kDtype>(x.x * inv, x.z * inv);
+                if (a.lse && d == 0) a.lse[at] = total[e] == 0.f ? -CUDART_INF_F : (peak[e] + log2f(total[e])) * kLn2;
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-            const int r = nt * 8 + my_row;
-            if (my_row < 8 && r < rows) {
-                float peak = -CUDART_INF_F, total = 0.f;
+        };
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) peak = fmaxf(peak, s_max[w * kRows + r]);
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int c = my_d / 2, z = merge_move<kD>(my_row, c);
+        for (int nt = 0; nt < kNT; ++nt) {
+            float peak[2], total[2], fix[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nt * 8 + 2 * tq + e;
+                peak[e] = -CUDART_INF_F, total[e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) peak[e] = fmaxf(peak[e], s_max[w * kRows + r]);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float m = s_max[w * kRows + r];
-                    if (m != -CUDART_INF_F) total += s_sum[w * kRows + r] * exp2_fast(m - peak);
-                    float4 y = *reinterpret_cast<const float4*>(merge + (w * 8 + my_row) * kD + 2 * ((c ^ z) & ~1));
-                    if (z & 1) y = make_float4(y.z, y.w, y.x, y.y);
-                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                    if (m != -CUDART_INF_F) total[e] += s_sum[w * kRows + r] * exp2_fast(m - peak[e]);
                 }
-                if (whole) {
-                    const float inv = total == 0.f ? 0.f : 1.f / total;
-                    const int64_t at = static_cast<int64_t>(k.w.begin + r / group) * a.q_heads + k.h * group + r % group;
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * kD + my_d) =
-                        make_uint2(narrow2<kDtype>(x.x * inv, x.y * inv), narrow2<kDtype>(x.z * inv, x.w * inv));
-                    if (a.lse && my_d == 0) a.lse[at] = total == 0.f ? -CUDART_INF_F : (peak + log2f(total)) * kLn2;
-                } else {
-                    __stcg(reinterpret_cast<float4*>(piece + r * kD + my_d), x);
-                    if (my_d == 0) {
-                        __stcg(piece + kPieceRows * kD + r, peak);
-                        __stcg(piece + kPieceRows * kD + kPieceRows + r, total);
+                fix[e] = top[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(top[nt][e] - peak[e]);
+            }
+#pragma unroll
+            for (int m = 0; m < kParts; ++m) {
+                const int turn_m = nt * kParts + m;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (fix[0] != 0.f) {
+                    x.x = fmaf(o[m][nt][0] - eight[nt][0], vup, flat[nt][0]) * fix[0];
+                    x.z = fmaf(fmaf(o[m][nt][2], kOdd, -eight[nt][0]), vup, flat[nt][0]) * fix[0];
+                }
+                if (fix[1] != 0.f) {
+                    x.y = fmaf(o[m][nt][1] - eight[nt][1], vup, flat[nt][1]) * fix[1];
+                    x.w = fmaf(fmaf(o[m][nt][3], kOdd, -eight[nt][1]), vup, flat[nt][1]) * fix[1];
+                }
+                float4* buffer = merge + (turn_m & 1) * kWarps * 32;
+                buffer[warp * 32 + lane] = x;
+                asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+                if (warp == turn_m % kWarps) {
+                    x = buffer[lane];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        const float4 y = buffer[w * 32 + lane];
+                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                    }
+                    if (whole) {
+                        write_rows(nt, m, x, peak, total);
+                    } else {
+                        __stcg(reinterpret_cast<float4*>(piece) + turn_m * 32 + lane, x);
+                        if (m == 0 && g == 0) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                __stcg(piece + kPieceRows * kD + nt * 8 + 2 * tq + e, peak[e]);
+                                __stcg(piece + kPieceRows * kD + kPieceRows + nt * 8 + 2 * tq + e, total[e]);
+                            }
+                        }
                     }
                 }
             }
@@ -598,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         if (!whole) {
             // the CTAs that share this (request, head): from the one with its first unit on
             const int64_t total = run.total, n = run.ctas;
-            const int c0 = static_cast<int>(((k.base + 1) * n - 1) / total);
-            const int c1 = static_cast<int>(((k.base + k.units) * n - 1) / total);
+            const int c0 = static_cast<int>(((done.base + kPieceCost + 1) * n - 1) / total);
+            const int c1 = static_cast<int>(((done.base + kPieceCost + done.units) * n - 1) / total);
             __threadfence();
             asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
             if (threadIdx.x == 0) {
@@ -610,30 +647,33 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
             if (last_one) {
                 __threadfence();
-                for (int r = my_row; r < rows; r += kWarps * 32 / kLanesRow) {
-                    float peak = -CUDART_INF_F, sum_all = 0.f;
+                for (int u = warp; u < kNT * kParts; u += kWarps) {
+                    const int nt = u / kParts, m = u % kParts;
+                    float peak[2] = {-CUDART_INF_F, -CUDART_INF_F}, sums_all[2] = {};
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                     for (int c = c0; c <= c1; ++c) {
                         const float* from = scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats;
-                        const float m = __ldcg(from + kPieceRows * kD + r), t = __ldcg(from + kPieceRows * kD + kPieceRows + r);
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + r * kD + my_d));
-                        if (m == -CUDART_INF_F) continue;
-                        const float to = fmaxf(peak, m);
-                        const float fx = peak == -CUDART_INF_F ? 0.f : exp2_fast(peak - to), fy = exp2_fast(m - to);
-                        peak = to;
-                        sum_all = sum_all * fx + t * fy;
-                        x.x = x.x * fx + y.x * fy, x.y = x.y * fx + y.y * fy;
-                        x.z = x.z * fx + y.z * fy, x.w = x.w * fx + y.w * fy;
+                        const float2 top2 = __ldcg(reinterpret_cast<const float2*>(from + kPieceRows * kD + nt * 8 + 2 * tq));
+                        const float2 sum2 = __ldcg(reinterpret_cast<const float2*>(from + kPieceRows * kD + kPieceRows + nt * 8 + 2 * tq));
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(from) + u * 32 + lane);
+                        float fx[2], fy[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float mine = e ? top2.y : top2.x, to = fmaxf(peak[e], mine);
+                            fx[e] = peak[e] == -CUDART_INF_F ? 0.f : exp2_fast(peak[e] - to);
+                            fy[e] = mine == -CUDART_INF_F ? 0.f : exp2_fast(mine - to);
+                            peak[e] = to;
+                            sums_all[e] = sums_all[e] * fx[e] + (e ? sum2.y : sum2.x) * fy[e];
+                        }
+                        x.x = x.x * fx[0] + y.x * fy[0], x.z = x.z * fx[0] + y.z * fy[0];
+                        x.y = x.y * fx[1] + y.y * fy[1], x.w = x.w * fx[1] + y.w * fy[1];
                     }
-                    const float inv = sum_all == 0.f ? 0.f : 1.f / sum_all;
-                    const int64_t at = static_cast<int64_t>(k.w.begin + r / group) * a.q_heads + k.h * group + r % group;
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * kD + my_d) =
-                        make_uint2(narrow2<kDtype>(x.x * inv, x.y * inv), narrow2<kDtype>(x.z * inv, x.w * inv));
-                    if (a.lse && my_d == 0) a.lse[at] = sum_all == 0.f ? -CUDART_INF_F : (peak + log2f(sum_all)) * kLn2;
+                    write_rows(nt, m, x, peak, sums_all);
                 }
             }
         }
-    } while (walk_next(a, k));
+    }
 }
 
 template <int kD, int kDtype, int kNT>

@@ -56,26 +56,21 @@ __device__ __forceinline__ int load_block(const AttentionArgs& a, int b, int pag
     return block;
 }
 
-// 8 codes of a word as 4 pairs of fp16 numbers code - 8, exactly: pair i holds the codes
-// at i and i + 4. A code in the low bits of an fp16 pattern 0x6400 is 1024 + code; four
-// bits higher it is 1024 + 16 code.
+// 8 codes of a word as 4 pairs of fp16 numbers: pair i holds the codes at i and i + 4. A
+// 4-bit number in the low bits of an fp16 pattern is the subnormal code * 2^-24, which a
+// tensor core multiplies exactly as any other value; four bits higher it is 16 times
+// that. So pairs 0 and 2 are code * 2^-24 and pairs 1 and 3 code * 2^-20: one logical
+// operation each, and the powers of two are divided out of the other operand (kOdd) or of
+// the result.
+constexpr float kCodeUp = 16777216.f;        // 2^24
+constexpr float kOdd = 0.0625f;
+
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
-    constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u, kMagic = 0x64006400u;
-    const __half2 minus = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f),
-                  minus_hi = __float2half2_rn(-72.f);
     const uint32_t w8 = w >> 8;
-    uint32_t t[4];
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t[0]) : "r"(w), "r"(kLo), "r"(kMagic));
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t[1]) : "r"(w), "r"(kHi), "r"(kMagic));
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t[2]) : "r"(w8), "r"(kLo), "r"(kMagic));
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t[3]) : "r"(w8), "r"(kHi), "r"(kMagic));
-    __half2 r[4];
-    r[0] = __hadd2(*reinterpret_cast<__half2*>(&t[0]), minus);
-    r[1] = __hfma2(*reinterpret_cast<__half2*>(&t[1]), sixteenth, minus_hi);
-    r[2] = __hadd2(*reinterpret_cast<__half2*>(&t[2]), minus);
-    r[3] = __hfma2(*reinterpret_cast<__half2*>(&t[3]), sixteenth, minus_hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<uint32_t*>(&r[i]);
+    h[0] = w & 0x000F000Fu;
+    h[1] = w & 0x00F000F0u;
+    h[2] = w8 & 0x000F000Fu;
+    h[3] = w8 & 0x00F000F0u;
 }
 
 template <int kDtype>
@@ -109,13 +104,14 @@ __device__ __forceinline__ int query_exponent(float top) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// One contiguous global -> shared copy counted on `bar` (16-byte aligned, whole 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            tc::smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-        : "memory");
+// 16 bytes global -> shared, past L1, in groups that the thread waits for in order.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 cudaError_t launch_attention_window(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
