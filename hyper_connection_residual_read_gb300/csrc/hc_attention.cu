@@ -232,38 +232,41 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     const int sh = 31 - __clz(a.c.block_size);
     const int64_t to_values = static_cast<int64_t>(a.c.kv_heads) * a.c.block_size;   // groups from keys to values
     const unsigned char* ring = smem + warp * (kStages * L::kBytes);
-    const uint32_t ring_at = tc::smem_u32(ring) + lane * 16;
-            // the blocks that hold the two halves of this warp's step of unit u
-            int ids[2];
-            auto look_up = [&](const Walk& k, int u) {
-                const int t0 = u * kUnit + warp * kStep;
-    #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    ids[i] = u < k.u1 && t0 + 16 * i < k.w.kv ? load_block(a, k.b, (t0 + 16 * i) >> sh, status) : 0;
-            };
-            // brings them to a slot of the ring, 16 bytes a lane (a group of copies, if an empty one)
-            auto fetch = [&](const Walk& k, int u, int slot) {
-                const int t0 = u * kUnit + warp * kStep;
-                if (u < k.u1 && t0 < k.w.kv) {
-                    const uint32_t to = ring_at + slot * L::kBytes;
-                    const bool two = t0 + 16 < k.w.kv;
-                    const int64_t at0 = (static_cast<int64_t>(ids[0]) * 2 * a.c.kv_heads + k.h) * a.c.block_size + (t0 & (a.c.block_size - 1));
-                    const int64_t at1 = (static_cast<int64_t>(ids[1]) * 2 * a.c.kv_heads + k.h) * a.c.block_size + ((t0 + 16) & (a.c.block_size - 1));
-                    constexpr int kChunks = kD / 32;             // 512-byte pieces of the step's keys
-    #pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        const int half = i * 2 / kChunks;
-                        if (half && !two) continue;
-                        const unsigned char* from = a.c.codes + (half ? at1 : at0) * (kD / 2) + (i - half * (kChunks / 2)) * 512 + lane * 16;
-                        copy16(to + i * 512, from);
-                        copy16(to + L::kCodes + i * 512, from + to_values * (kD / 2));
-                    }
-                    // scales: 16 bytes hold 4 tokens; lanes 0-7 keys, 8-15 values
-                    if (lane < 16 && ((lane & 4) == 0 || two))
-                        copy16(to + 2 * L::kCodes, a.c.scales + (((lane & 4) ? at1 : at0) + (lane >= 8 ? to_values : 0)) * 2 + (lane & 3) * 8);
-                }
-                copy_commit();
-            };
+            // Copies: lanes 0-15 bring the first 16 tokens of the warp's step, lanes 16-31 the others, 16
+    // bytes a lane and copy; four lanes of each half the keys' scales and four the values'.
+    const int half = lane >> 4, l16 = lane & 15;
+    const uint32_t block_bytes = static_cast<uint32_t>(2 * to_values * (kD / 2));
+    const uint32_t put = tc::smem_u32(ring) + half * (L::kCodes / 2) + l16 * 16;
+    const uint32_t put_scales = tc::smem_u32(ring) + 2 * L::kCodes + (l16 >> 2) * L::kScales + half * (L::kScales / 2) + (l16 & 3) * 16;
+    const unsigned char* my_codes = a.c.codes + l16 * 16;
+    const unsigned char* my_scales = reinterpret_cast<const unsigned char*>(a.c.scales) + (l16 >> 2) * to_values * 4 + (l16 & 3) * 16;
+    int id = 0;                              // the block of this lane's half of the step to be copied next
+    auto look_up = [&](const Walk& k, int u) {
+        const int t = u * kUnit + warp * kStep + half * 16;
+        if (u < k.u1 && t < k.w.kv) id = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
+    };
+    // brings the step of unit u to a slot of the ring (a group of copies, if an empty one)
+    auto fetch = [&](const Walk& k, int u, int slot) {
+        const int t = u * kUnit + warp * kStep + half * 16;
+        if (u < k.u1 && t < k.w.kv) {
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.c.blocks)) {
+                atomicOr(status, kStatusBounds);
+                id = 0;                      // wrong values, from the cache's own memory
+            }
+            const uint32_t within = (k.h * a.c.block_size + (t & (a.c.block_size - 1))) * (kD / 2);
+            const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes + within;
+            const unsigned char* keys = my_codes + at;
+            const unsigned char* values = keys + to_values * (kD / 2);
+            const uint32_t to = put + slot * L::kBytes;
+#pragma unroll
+            for (int i = 0; i < kD / 32; ++i) {
+                copy16(to + i * 256, keys + i * 256);
+                copy16(to + L::kCodes + i * 256, values + i * 256);
+            }
+            if (l16 < 8) copy16(put_scales + slot * L::kBytes, my_scales + at / (kD / 8));
+        }
+        copy_commit();
+    };
     // a piece's first steps, on their way before the piece before it is merged
     auto begin = [&](const Walk& k) {
 #pragma unroll
@@ -342,11 +345,12 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         }
 
         float o[kVW * 4][kNT][4] = {}, eight[kNT][4] = {};   // and 8 times the sum of the weights
-        float top[kNT][2], sum[kNT][2], flat[kNT][2];      // maximum, sum of p, sum of p (m + 8 s)
+        float base[kNT][2], sum[kNT][2], flat[kNT][2];     // maximum, sum of p, sum of p (m + 8 s)
+        uint32_t fresh = (1u << (2 * kNT)) - 1;            // rows of this lane without a maximum (base is 0)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) top[nt][e] = -CUDART_INF_F, sum[nt][e] = 0.f, flat[nt][e] = 0.f;
+            for (int e = 0; e < 2; ++e) base[nt][e] = 0.f, sum[nt][e] = 0.f, flat[nt][e] = 0.f;
         float vdown = 0.f;                                  // 2^-E of the value steps; 0: none seen
         const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1);   // every row sees what lies before
 
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     }
                 }
             }
-            // logits in powers of two
+            // logits in powers of two, less the maximum so far
             float vs[4], vm[4];
             float vtop = 0.f;
 #pragma unroll
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float& z = s[x >> 1][nt][(x & 1) * 2 + e];
-                        z = fmaf(sf, z, off * qsum[nt][e]);
+                        z = fmaf(sf, z, fmaf(off, qsum[nt][e], -base[nt][e]));
                     }
             }
             if (kTail) {
@@ -432,14 +436,14 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     }
             }
             // raise the maximum, or the reference of the value steps, where they are passed
-            bool raise = vtop * vdown > kStepRoom || (vdown == 0.f && vtop > 0.f);
+            bool raise = vtop * vdown > kStepRoom || (vdown == 0.f && vtop > 0.f) || fresh != 0;
             float peak[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     peak[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
-                    raise |= peak[nt][e] > top[nt][e] + kRaise;
+                    raise |= peak[nt][e] > kRaise;
                 }
             if (__any_sync(~0u, raise)) {
                 uint32_t vbits = __reduce_max_sync(~0u, __float_as_uint(vtop));
@@ -457,9 +461,15 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                         p = fmaxf(p, __shfl_xor_sync(~0u, p, 4));
                         p = fmaxf(p, __shfl_xor_sync(~0u, p, 8));
                         p = fmaxf(p, __shfl_xor_sync(~0u, p, 16));
-                        const float to = fmaxf(p, top[nt][e]);
-                        const float fix = top[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(top[nt][e] - to);
-                        top[nt][e] = to;
+                        // by how much the maximum rises (of a fresh row: to the first logit seen)
+                        const uint32_t bit = 1u << (2 * nt + e);
+                        const bool first = (fresh & bit) != 0;
+                        const float up = first ? (p == -CUDART_INF_F ? 0.f : p) : fmaxf(p, 0.f);
+                        if (first && p != -CUDART_INF_F) fresh &= ~bit;
+                        const float fix = first ? 1.f : exp2_fast(-up);
+                        base[nt][e] += up;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[x >> 1][nt][(x & 1) * 2 + e] -= up;
                         sum[nt][e] *= fix;
                         flat[nt][e] *= fix;
                         eight[nt][e] *= fix * vfix;
@@ -476,12 +486,10 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             for (int x = 0; x < 4; ++x) vs[x] *= vdown;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
-                const float top0 = kTail && top[nt][0] == -CUDART_INF_F ? 0.f : top[nt][0];
-                const float top1 = kTail && top[nt][1] == -CUDART_INF_F ? 0.f : top[nt][1];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float z0 = s[x >> 1][nt][(x & 1) * 2], z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
-                    const float p0 = exp2_fast(z0 - top0), p1 = exp2_fast(z1 - top1);
+                    const float p0 = exp2_fast(z0), p1 = exp2_fast(z1);
                     float w0 = p0 * vs[x], w1 = p1 * vs[x], m0 = vm[x], m1 = vm[x];
                     if (kTail) {                             // a hidden value may be NaN
                         if (z0 == -CUDART_INF_F) w0 = m0 = 0.f;
@@ -548,10 +556,12 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         const float vup = vdown == 0.f ? 0.f : kCodeUp / vdown;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");   // the last piece's statistics are read
         // rows 2 tq and 2 tq + 1 of each 8
+        float top[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                top[nt][e] = (fresh >> (2 * nt + e)) & 1 ? -CUDART_INF_F : base[nt][e];
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     sum[nt][e] += __shfl_xor_sync(~0u, sum[nt][e], d);
