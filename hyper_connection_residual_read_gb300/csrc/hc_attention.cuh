@@ -114,6 +114,8 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-cudaError_t launch_attention_window(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+// More than 32 rows (hc_attention_chunk.cu).
+cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+size_t attention_chunk_scratch_floats(int sm_count);
 
 }  // namespace hc

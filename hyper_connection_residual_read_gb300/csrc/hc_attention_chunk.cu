@@ -1,0 +1,791 @@
+// Attention over the cache held in 4 bits, for chunks: more than 32 rows (new tokens times
+// the query heads of a kv head), on tcgen05.
+//
+// Both products run on the tensor cores in fp16 with fp32 sums, 128 rows x 128 keys at a
+// time: S = Q K'^T from shared memory, O += P V' with P in tensor memory. Four kinds of
+// warps share a CTA: two warpgroups of softmax (a thread a row), one that decodes keys and
+// values, one warp that issues the products.
+//
+// * The decoded values are exact. A step has 8 significant bits (bf16) and |code - 8| <= 8
+//   at most 3, so s (code - 8) has 11 at most, which is what fp16 holds: K' = 2^-E s_j
+//   (c_j - 8), with E from the largest step of the tile, is exact for steps down to 2^-9 of
+//   that one and within 2^-20 of the largest value below. One logical and one fp16
+//   operation decode two codes: a code's bits alone are the subnormal code * 2^-24, and fma
+//   with S = 2^24 2^-E s gives S code 2^-24 - S 8 2^-24.
+// * What is left of a key, m_j + 8 s_j, is the same for all its dimensions: it meets
+//   sum(q) in the softmax, one fma a logit in fp32. Likewise sum p_j (m_j + 8 s_j) is
+//   summed in fp32 beside O. So the one rounding of the product is that of p to fp16.
+// * Rows are the new tokens times the query heads of one kv head, so that a key is
+//   decoded once for all the heads that read it.
+// * Two row tiles (256 rows) share each decoded key tile; their products alternate, so
+//   that one softmax runs while the other's products do. Windows of up to 128 rows use
+//   both warpgroups on the same rows, each on every other key tile.
+// * Work is cut as in the window kernel: runs of equal cost over the CTAs, in key tiles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hc_attention.cuh"
+
+namespace hc {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;                 // keys of a tile, rows of a row tile
+constexpr int kStages = 2;                 // key tiles and value tiles in shared memory
+constexpr int kCols = 4;                   // column data of tiles (see the ring below)
+constexpr int kPieceCost = 2;              // what a piece costs beside its tiles, in tiles
+constexpr float kRaise = 8.f;              // log2 by which a logit may pass the maximum
+constexpr int kPieceFloats = 256 * 128 + 512;
+
+// What softmax needs of a tile's keys beside S and P. Four of them: a tile's data is
+// rewritten for the tile four later, whose keys are decoded only after the products of the
+// tile two later, which follow the softmax of this one.
+struct Column {
+    float k[kTile], v[kTile];              // m + 8 s of keys and values
+    int ek, ev;                            // exponents divided out of K' and V'
+    int pad[2];
+};
+
+template <int kD>
+struct Smem {
+    static constexpr int kOne = kTile * kD * 2;                        // a decoded tile, a row tile
+    static constexpr int kQ = 0;
+    static constexpr int kK = 2 * kOne;
+    static constexpr int kV = kK + kStages * kOne;
+    static constexpr int kColumn = kV + kStages * kOne;
+    static constexpr int kSteps = kColumn + kCols * static_cast<int>(sizeof(Column));   // fp16 S of keys, values
+    static constexpr int kBytes = kSteps + 2 * kTile * 2 + 1024;       // and room to align
+};
+
+struct Bars {
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], col_full[kCols];
+};
+
+// The walk through a CTA's run: as in the window kernel, with row tiles.
+struct Walk {
+    int b, h, row0;              // request, kv head, first row of the row tile
+    int rows;                    // rows of the tile that exist
+    int t0, t1, tiles;           // key tiles [t0, t1) of `tiles`
+    int64_t left, base;
+    Window w;
+};
+
+// Row tiles of a window, and the key tiles that row tile i sees.
+__device__ __forceinline__ int row_tiles(const Window& w, int group, int step) {
+    return (w.rows * group + step - 1) / step;
+}
+__device__ __forceinline__ int key_tiles(const AttentionArgs& a, const Window& w, int group, int step, int i) {
+    const int last = min(((i + 1) * step - 1) / group, w.rows - 1);
+    const int seen = a.mask ? w.kv : min(w.kv, w.first + last + 1);
+    return max((seen + kTile - 1) / kTile, 1);
+}
+__device__ __forceinline__ int64_t head_slots(const AttentionArgs& a, const Window& w, int group, int step) {
+    int64_t n = 0;
+    for (int i = row_tiles(w, group, step) - 1; i >= 0; --i) n += key_tiles(a, w, group, step, i) + kPieceCost;
+    return n;
+}
+
+__device__ __forceinline__ bool walk_piece(Walk& k, int from) {
+    const int64_t to = min(static_cast<int64_t>(k.tiles + kPieceCost), from + k.left);
+    k.left -= to - from;
+    k.t0 = max(from - kPieceCost, 0);
+    k.t1 = static_cast<int>(to) - kPieceCost;
+    return k.t1 > k.t0;
+}
+
+__device__ __forceinline__ void walk_row_tile(const AttentionArgs& a, Walk& k, int group, int step, int i) {
+    k.row0 = i * step;
+    k.rows = min(k.w.rows * group - k.row0, step);
+    k.tiles = key_tiles(a, k.w, group, step, i);
+}
+
+__device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k, int group, int step) {
+    if (k.left == 0) return false;
+    k.base += k.tiles + kPieceCost;
+    int i = k.row0 / step + 1;
+    if (i == row_tiles(k.w, group, step)) {
+        i = 0;
+        if (++k.h == a.c.kv_heads) {
+            k.h = 0;
+            do {
+                ++k.b;
+                if (k.b >= a.requests) return false;
+                k.w = load_window(a, k.b, nullptr);
+            } while (row_tiles(k.w, group, step) == 0);
+        }
+    }
+    walk_row_tile(a, k, group, step, i);
+    return walk_piece(k, 0);
+}
+
+struct Run {
+    int b;
+    int64_t offset, head, begin, end, total, ctas;
+};
+
+__device__ void find_run(const AttentionArgs& a, int group, int step, Run* run, int64_t* sums, int* status) {
+    const int tid = threadIdx.x;
+    const int per = (a.requests + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += head_slots(a, load_window(a, b, blockIdx.x == 0 ? status : nullptr), group, step) * a.c.kv_heads;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t t = __shfl_up_sync(~0u, upto, d);
+        if ((tid & 31) >= d) upto += t;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = upto;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == (tid >> 5)) upto += total;
+        total += sums[w];
+    }
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), i = blockIdx.x;
+    const int64_t begin = i < ctas ? total * i / ctas : total, end = i < ctas ? total * (i + 1) / ctas : total;
+    if (tid == 0) {
+        run->begin = begin;
+        run->end = end;
+        run->total = total;
+        run->ctas = ctas;
+    }
+    if (begin < end && begin < upto && begin >= upto - mine) {
+        int64_t at = upto - mine;
+        for (int b = b0; b < b1; ++b) {
+            const int64_t head = head_slots(a, load_window(a, b, nullptr), group, step), n = head * a.c.kv_heads;
+            if (begin < at + n) {
+                run->b = b;
+                run->offset = begin - at;
+                run->head = head;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, int group, int step, Walk& k) {
+    if (run.begin >= run.end) return false;
+    k.b = run.b;
+    k.w = load_window(a, k.b, nullptr);
+    k.h = static_cast<int>(run.offset / run.head);
+    int64_t from = run.offset - k.h * run.head;
+    int i = 0;
+    while (true) {
+        walk_row_tile(a, k, group, step, i);
+        if (from < k.tiles + kPieceCost) break;
+        from -= k.tiles + kPieceCost;
+        ++i;
+    }
+    k.left = run.end - run.begin;
+    k.base = run.begin - from;
+    return walk_piece(k, static_cast<int>(from)) || walk_next(a, k, group, step);
+}
+
+// ---- tensor memory
+
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+
+// A decoded word scaled: pairs 0 and 2 hold c 2^-24, pairs 1 and 3 c 2^-20; s = (S, S'), the
+// steps of the two codes of a pair, and s16 = s / 16, low = -8 2^-24 s.
+__device__ __forceinline__ void scale_word(uint32_t (&h)[4], __half2 s, __half2 s16, __half2 low) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&h[i]), (i & 1) ? s16 : s, low);
+        h[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+}
+
+template <int kD, int kDtype>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const AttentionArgs a, int same, float* scratch, unsigned* arrivals, int* status) {
+    using S = Smem<kD>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Bars bars;
+    __shared__ Run run;
+    __shared__ int64_t sums[kThreads / 32];
+    __shared__ uint32_t tmem_slot;
+    __shared__ unsigned last_one[2];
+    __shared__ uint32_t step_max[2][2][4];
+    __shared__ volatile int abort_flag;
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Column* columns = reinterpret_cast<Column*>(smem + S::kColumn);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = a.q_heads / a.c.kv_heads;
+    const int step = same ? kTile : 2 * kTile;         // rows of a piece
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bars.q_full[i], 128);
+            tc::mbar_init(&bars.s_full[i], 1);
+            tc::mbar_init(&bars.p_full[i], 128);
+            tc::mbar_init(&bars.o_done[i], 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&bars.k_full[i], 128);
+            tc::mbar_init(&bars.k_empty[i], 1);
+            tc::mbar_init(&bars.v_full[i], 128);
+            tc::mbar_init(&bars.v_empty[i], 1);
+        }
+        for (int i = 0; i < kCols; ++i) tc::mbar_init(&bars.col_full[i], 128);
+        tc::fence_barrier_init();
+    }
+    if (warp == 12) tc::tmem_alloc(&tmem_slot, 512);
+    tc::tc_fence_before();
+    find_run(a, group, step, &run, sums, status);      // synchronises
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Walk k;
+    const bool any = walk_start(a, run, group, step, k);
+
+    // Every wait is bounded (tc::mbar_wait); one that gives up raises the abort flag, after
+    // which the others return at once: the roles then run to their ends on whatever is there.
+    auto wait = [&](uint64_t& bar, uint32_t phase) { tc::mbar_wait(&bar, phase & 1, &abort_flag, status); };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        const int wg = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_mem = tmem + lanes + wg * kTile, o_mem = tmem + lanes + 2 * kTile + wg * kTile;
+        unsigned char* q_tile = smem + S::kQ + wg * S::kOne;
+        uint32_t s_phase = 0, o_phase = 0;
+        uint32_t column = 0;                           // tiles that the producers have been through
+        if (any) do {
+            const int r = k.row0 + (same ? 0 : wg * kTile) + row;     // row of the window
+            const bool active = same || wg == 0 || k.rows > kTile;    // this warpgroup has rows
+            const bool here = r < k.row0 + k.rows && r < k.w.rows * group;
+            const int i = r / group, hq = k.h * group + r % group;
+            float factor = 0.f, qsum = 0.f;
+            if (active) {
+                // ---- this row of Q: scaled to fp16, in the order of the decoded keys
+                const int64_t from = static_cast<int64_t>(k.w.begin + i) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
+                const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from);
+                float top = 0.f;
+#pragma unroll 8
+                for (int c = 0; c < kD / 8; ++c) {
+                    const uint4 raw = here ? in[c] : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = widen2<kDtype>(x[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                const int e = query_exponent(top);
+                const float down = power_of_two(-e);
+                factor = a.scale * kLog2e * power_of_two(e);
+#pragma unroll 4
+                for (int c = 0; c < kD / 8; ++c) {
+                    const uint4 raw = here ? in[c] : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+                    float f[8];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 y = widen2<kDtype>(x[p]);
+                        f[2 * p] = y.x * down, f[2 * p + 1] = y.y * down;
+                    }
+                    uint32_t o[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        o[p] = pack_half2(f[p], f[p + 4]);
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&o[p]));
+                        qsum += y.x + y.y;
+                    }
+                    *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kTile * 128) + tc::sw128_offset(row, (c & 7) * 8)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(&bars.q_full[wg]);
+            }
+
+            float base = 0.f, sum = 0.f, flat = 0.f;
+            bool fresh = true;
+            int ev = 0, done_tiles = 0;
+            const float g = factor * qsum;
+            const uint64_t bits = a.mask && here ? a.mask[k.w.begin + i] : 0;
+            for (int j = k.t0; j < k.t1; ++j, ++column) {
+                if (!active || (same && ((j - k.t0) & 1) != wg)) continue;
+                const Column& col = columns[column % kCols];
+                wait(bars.col_full[column % kCols], column / kCols);
+                wait(bars.s_full[wg], s_phase++);
+                tc::tc_fence_after();
+                const float f = ldexpf(factor, col.ek);
+                // hidden keys: behind the end, or behind this row's token, or out of its mask
+                const int t = j * kTile;
+                const bool tail = t + kTile > min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);
+                const int limit = (a.mask ? k.w.kv : min(k.w.kv, k.w.first + i + 1)) - t;
+                // Weights against the maximum so far, 32 keys at a time, held as P until all are
+                // known: a logit that passes the maximum by 2^8 (and a row's first one) raises it,
+                // and the tile is done again.
+                uint32_t pw[2][32];
+                float peak, sum_now, flat_now;
+                auto weigh = [&]() {
+                    peak = -CUDART_INF_F, sum_now = sum, flat_now = flat;
+#pragma unroll
+                    for (int part = 0; part < 4; ++part) {
+                        uint32_t raw[32];
+                        tmem_load32(s_mem + part * 32, raw);
+                        tmem_wait_load();
+                        float x[32];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 off = *reinterpret_cast<const float4*>(&col.k[part * 32 + c]);
+                            x[c] = fmaf(__uint_as_float(raw[c]), f, fmaf(off.x, g, -base));
+                            x[c + 1] = fmaf(__uint_as_float(raw[c + 1]), f, fmaf(off.y, g, -base));
+                            x[c + 2] = fmaf(__uint_as_float(raw[c + 2]), f, fmaf(off.z, g, -base));
+                            x[c + 3] = fmaf(__uint_as_float(raw[c + 3]), f, fmaf(off.w, g, -base));
+                        }
+                        if (tail) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                bool sees = part * 32 + c < limit;
+                                if (a.mask) {
+                                    const int back = t + part * 32 + c - k.w.first;
+                                    sees &= back < 0 || (back < 64 && ((bits >> back) & 1));
+                                }
+                                if (!sees) x[c] = -CUDART_INF_F;
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) peak = fmaxf(peak, x[c]);
+                        // and the weights' products with what is common to a value's dimensions
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 off = *reinterpret_cast<const float4*>(&col.v[part * 32 + c]);
+                            const float o4[4] = {off.x, off.y, off.z, off.w};
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                const bool hidden = tail && x[c + n] == -CUDART_INF_F;
+                                x[c + n] = exp2_fast(x[c + n]);
+                                sum_now += x[c + n];
+                                flat_now = fmaf(x[c + n], hidden ? 0.f : o4[n], flat_now);
+                            }
+                        }
+                        // P: column c * 8 + n of each 64 is token n * 8 + c, the order of the decoded
+                        // values: word 4 c + n holds tokens 16 n + c and 16 n + 8 + c
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                pw[part >> 1][4 * c + 2 * (part & 1) + n] = pack_half2(x[16 * n + c], x[16 * n + 8 + c]);
+                    }
+                };
+                float fix = 1.f;
+                weigh();
+                const bool rise = (fresh && peak != -CUDART_INF_F) || peak > kRaise;
+                if (__any_sync(~0u, rise)) {
+                    if (rise) {
+                        const float up = fresh ? peak : fmaxf(peak, 0.f);
+                        fix = fresh ? 1.f : exp2_fast(-up);
+                        fresh = false;
+                        base += up;
+                        sum *= fix;
+                        flat *= fix;
+                    }
+                    weigh();
+                }
+                sum = sum_now, flat = flat_now;
+                if (done_tiles == 0) {
+                    ev = col.ev;
+                } else {
+                    const bool other = col.ev != ev;
+                    if (__any_sync(~0u, fix != 1.f || other)) {
+                        // O of the tiles before is complete, and this warp's lanes of it are rescaled
+                        wait(bars.o_done[wg], o_phase + done_tiles - 1);
+                        tc::tc_fence_after();
+                        const float by = other ? ldexpf(fix, ev - col.ev) : fix;
+                        ev = col.ev;
+#pragma unroll 1
+                        for (int c = 0; c < kD / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_load32(o_mem + c * 32, v);
+                            tmem_wait_load();
+#pragma unroll
+                            for (int n = 0; n < 32; ++n) v[n] = __float_as_uint(__uint_as_float(v[n]) * by);
+                            tmem_store32(o_mem + c * 32, v);
+                        }
+                    }
+                }
+                tmem_store32(s_mem, pw[0]);
+                tmem_store32(s_mem + 32, pw[1]);
+                tmem_wait_store();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&bars.p_full[wg]);
+                ++done_tiles;
+            }
+            // ---- the end of the piece
+            if (done_tiles > 0) {
+                wait(bars.o_done[wg], o_phase + done_tiles - 1);
+                tc::tc_fence_after();
+            }
+            o_phase += done_tiles;
+            if (fresh) base = -CUDART_INF_F;
+            const bool whole = k.t0 == 0 && k.t1 == k.tiles;
+            float other_base = -CUDART_INF_F, other_sum = 0.f;
+            float* exchange = reinterpret_cast<float*>(smem + S::kQ);          // [kD][128], both row tiles' room
+            __shared__ float2 stats[kTile];
+            if (same) {
+                // the two warpgroups' sums over the same rows
+                asm volatile("bar.sync 1, 256;" ::: "memory");         // no product reads Q any more
+                if (wg == 1) {
+                    stats[row] = make_float2(base, sum);
+#pragma unroll
+                    for (int c = 0; c < kD / 32; ++c) {
+                        uint32_t v[32];
+                        if (done_tiles > 0) tmem_load32(o_mem + c * 32, v);
+                        tmem_wait_load();
+                        const float up = done_tiles > 0 ? ldexpf(1.f, ev) : 0.f;
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            exchange[(c * 32 + n) * kTile + row] = done_tiles > 0 ? fmaf(__uint_as_float(v[n]), up, flat) : 0.f;
+                    }
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (wg == 0) other_base = stats[row].x, other_sum = stats[row].y;
+            }
+            const bool writes = active && !(same && wg == 1);
+            float peak = base, total = sum, mine = base == -CUDART_INF_F ? 0.f : 1.f, other = 0.f;
+            if (same && wg == 0) {
+                peak = fmaxf(base, other_base);
+                mine = base == -CUDART_INF_F ? 0.f : exp2_fast(base - peak);
+                other = other_base == -CUDART_INF_F ? 0.f : exp2_fast(other_base - peak);
+                total = sum * mine + other_sum * other;
+            }
+            const int64_t at = static_cast<int64_t>(k.w.begin + i) * a.q_heads + hq;
+            float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (k.t0 == 0 ? 1 : 0)) * kPieceFloats;
+            const int prow = (same ? 0 : wg * kTile) + row;
+            auto write = [&](int c, const float (&v)[32], float inv) {
+                uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * kD + c * 32);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    to[n] = make_uint4(narrow2<kDtype>(v[8 * n] * inv, v[8 * n + 1] * inv), narrow2<kDtype>(v[8 * n + 2] * inv, v[8 * n + 3] * inv),
+                                       narrow2<kDtype>(v[8 * n + 4] * inv, v[8 * n + 5] * inv), narrow2<kDtype>(v[8 * n + 6] * inv, v[8 * n + 7] * inv));
+            };
+            if (writes) {
+                const float up = done_tiles > 0 ? ldexpf(1.f, ev) : 0.f, inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                for (int c = 0; c < kD / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_load32(o_mem + c * 32, v);
+                    tmem_wait_load();
+                    float o[32];
+#pragma unroll
+                    for (int n = 0; n < 32; ++n) {
+                        o[n] = mine == 0.f ? 0.f : fmaf(__uint_as_float(v[n]), up, flat) * mine;
+                        if (same && other != 0.f) o[n] = fmaf(exchange[(c * 32 + n) * kTile + row], other, o[n]);
+                    }
+                    if (whole) {
+                        if (here) write(c, o, inv);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+                            __stcg(reinterpret_cast<float4*>(piece) + (c * 8 + n) * 256 + prow,
+                                   make_float4(o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]));
+                    }
+                }
+                if (whole) {
+                    if (here && a.lse) a.lse[at] = total == 0.f ? -CUDART_INF_F : (peak + log2f(total)) * kLn2;
+                } else {
+                    __stcg(reinterpret_cast<float2*>(piece + 256 * kD) + prow, make_float2(peak, total));
+                }
+            }
+            tc::tc_fence_before();
+            if (same) asm volatile("bar.sync 1, 256;" ::: "memory");   // the exchange is read
+            if (!whole && writes) {
+                // each row tile is joined by the last CTA that has part of it
+                const int64_t n = run.ctas;
+                const int c0 = static_cast<int>(((k.base + kPieceCost + 1) * n - 1) / run.total);
+                const int c1 = static_cast<int>(((k.base + kPieceCost + k.tiles) * n - 1) / run.total);
+                __threadfence();
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                if (row == 0) {
+                    const unsigned before = atomicAdd(&arrivals[2 * c0 + wg], 1u);
+                    last_one[wg] = before == static_cast<unsigned>(c1 - c0);
+                    if (last_one[wg]) arrivals[2 * c0 + wg] = 0;
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                if (last_one[wg]) {
+                    __threadfence();
+                    auto from = [&](int c) { return scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats; };
+                    float top = -CUDART_INF_F, all = 0.f;
+                    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow).x);
+                    for (int c = c0; c <= c1; ++c) {
+                        const float2 st = __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow);
+                        if (st.x != -CUDART_INF_F) all += st.y * exp2_fast(st.x - top);
+                    }
+                    const float inv = all == 0.f ? 0.f : 1.f / all;
+#pragma unroll 1
+                    for (int d = 0; d < kD / 32; ++d) {
+                        float o[32] = {};
+                        for (int c = c0; c <= c1; ++c) {
+                            const float2 st = __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow);
+                            const float by = st.x == -CUDART_INF_F ? 0.f : exp2_fast(st.x - top);
+                            if (by == 0.f) continue;
+#pragma unroll
+                            for (int m = 0; m < 8; ++m) {
+                                const float4 y = __ldcg(reinterpret_cast<const float4*>(from(c)) + (d * 8 + m) * 256 + prow);
+                                o[4 * m] = fmaf(y.x, by, o[4 * m]), o[4 * m + 1] = fmaf(y.y, by, o[4 * m + 1]);
+                                o[4 * m + 2] = fmaf(y.z, by, o[4 * m + 2]), o[4 * m + 3] = fmaf(y.w, by, o[4 * m + 3]);
+                            }
+                        }
+                        if (here) write(d, o, inv);
+                    }
+                    if (here && a.lse) a.lse[at] = all == 0.f ? -CUDART_INF_F : (top + log2f(all)) * kLn2;
+                }
+            }
+        } while (walk_next(a, k, group, step));
+    } else if (warp < 12) {
+        // ------------------------------------------------------------------ keys and values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        constexpr int kW = 4;                                   // words of a thread's keys
+        constexpr int kUnits = kD / 32;                         // 16-byte pieces of keys a thread decodes
+        constexpr int kVW = kD / 64;                            // words of a thread's values of one token
+        const int p = threadIdx.x - 256, w = warp - 8;
+        const int sh = 31 - __clz(a.c.block_size);
+        const int64_t to_values = static_cast<int64_t>(a.c.kv_heads) * a.c.block_size;
+        const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.c.scales);
+        __half* steps = reinterpret_cast<__half*>(smem + S::kSteps);
+        // keys: piece u of this thread is 16 bytes, `seg`, of token key_token(u)
+        constexpr int kSegs = kD / 32;
+        const int seg = (lane >> 3) % kSegs;
+        auto key_token = [&](int u) { return (u * (128 / kUnits) + w * (32 / kUnits) + (lane >> 3) / kSegs * 8 + (lane & 7)); };
+        // values: tokens n * 8 + vc of the 64-token half vh, kVW words from dimension vd on
+        const int vc = lane & 7, vh = w >> 1, vd = ((w & 1) * 4 + (lane >> 3)) * (8 * kVW);
+        uint32_t column = 0;
+        if (any) do {
+            int ev = 0;
+            bool have_ev = false;
+            uint32_t kraw[kUnits][kW], vraw[8][kVW], ks = 0, vs = 0;
+            auto group_at = [&](int t) {                        // group of token t's key, which exists
+                const int64_t id = load_block(a, k.b, t >> sh, status);
+                return (id * 2 * a.c.kv_heads + k.h) * a.c.block_size + (t & (a.c.block_size - 1));
+            };
+            auto load_scales = [&](int j) {
+                const int t = j * kTile + p;
+                ks = vs = 0;
+                if (t < k.w.kv) {
+                    const int64_t at = group_at(t);
+                    ks = scales[at];
+                    vs = scales[at + to_values];
+                }
+            };
+            auto load_keys = [&](int j) {
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const int t = j * kTile + key_token(u);
+                    uint4 y = make_uint4(0, 0, 0, 0);
+                    if (t < k.w.kv) y = ldg_stream_v4(a.c.codes + group_at(t) * (kD / 2) + seg * 16);
+                    kraw[u][0] = y.x, kraw[u][1] = y.y, kraw[u][2] = y.z, kraw[u][3] = y.w;
+                }
+            };
+            auto load_values = [&](int j) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const int t = j * kTile + vh * 64 + n * 8 + vc;
+                    uint2 y = make_uint2(0, 0);
+                    if (t < k.w.kv) {
+                        const unsigned char* from = a.c.codes + (group_at(t) + to_values) * (kD / 2) + vd / 2;
+                        if (kVW == 2) y = *reinterpret_cast<const uint2*>(from);
+                        else y.x = *reinterpret_cast<const uint32_t*>(from);
+                    }
+                    vraw[n][0] = y.x;
+                    if (kVW == 2) vraw[n][kVW - 1] = y.y;
+                }
+            };
+            load_scales(k.t0);
+            load_keys(k.t0);
+            load_values(k.t0);
+            for (int j = k.t0; j < k.t1; ++j, ++column) {
+                const int stage = column % kStages, turn = column / kStages;
+                // ---- steps and minima: a group held as NaN keeps the NaN in its common part alone
+                float s_k = bf16_lo(ks), s_v = bf16_lo(vs);
+                const float o_k = fmaf(8.f, s_k, bf16_hi(ks)), o_v = fmaf(8.f, s_v, bf16_hi(vs));
+                if (!(s_k <= 3.0e38f)) s_k = 0.f;
+                if (!(s_v <= 3.0e38f)) s_v = 0.f;
+                const uint32_t mk = __reduce_max_sync(~0u, __float_as_uint(s_k)), mv = __reduce_max_sync(~0u, __float_as_uint(s_v));
+                if (lane == 0) step_max[column & 1][0][w] = mk, step_max[column & 1][1][w] = mv;
+                asm volatile("bar.sync 4, 128;" ::: "memory");
+                const uint32_t* m0 = step_max[column & 1][0];
+                const uint32_t* m1 = step_max[column & 1][1];
+                const uint32_t top_k = max(max(m0[0], m0[1]), max(m0[2], m0[3])), top_v = max(max(m1[0], m1[1]), max(m1[2], m1[3]));
+                // K': the largest step in [2^-9, 2^-8); V': the first tile's in [2^-12, 2^-11), and
+                // later ones below 2^-8, else the exponent follows
+                const int ek = top_k ? static_cast<int>(top_k >> 23) - 127 + 9 : 0;
+                if (top_v && (!have_ev || static_cast<int>(top_v >> 23) - 127 + 9 > ev)) {
+                    ev = static_cast<int>(top_v >> 23) - 127 + 12;
+                    have_ev = true;
+                }
+                Column& col = columns[column % kCols];
+                // the softmax of the tile four before has been through with this one: see Column
+                if (turn > 0) wait(bars.k_empty[stage], turn - 1);
+                col.k[p] = o_k;
+                col.v[p] = o_v;
+                if (p == 0) col.ek = ek, col.ev = ev;
+                tc::mbar_arrive(&bars.col_full[column % kCols]);
+                steps[p] = __float2half_rn(ldexpf(s_k, 24 - ek));
+                steps[kTile + p] = __float2half_rn(ldexpf(s_v, 24 - ev));
+                asm volatile("bar.sync 4, 128;" ::: "memory");
+                const bool more = j + 1 < k.t1;
+                if (more) load_scales(j + 1);
+                // ---- keys
+                const __half2 sixteenth = __float2half2_rn(0.0625f), eighth = __float2half2_rn(-4.76837158203125e-7f);   // -8 2^-24
+                unsigned char* to = smem + S::kK + stage * S::kOne;
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const int t = key_token(u);
+                    const __half2 s = __half2half2(steps[t]), s16 = __hmul2(s, sixteenth), low = __hmul2(s, eighth);
+#pragma unroll
+                    for (int n = 0; n < kW; ++n) {
+                        uint32_t h[4];
+                        decode_word(kraw[u][n], h);
+                        scale_word(h, s, s16, low);
+                        const int c = seg * 4 + n;               // 8 dimensions
+                        *reinterpret_cast<uint4*>(to + (c >> 3) * (kTile * 128) + tc::sw128_offset(t, (c & 7) * 8)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(&bars.k_full[stage]);
+                if (more) load_keys(j + 1);
+                // ---- values, transposed
+                if (turn > 0) wait(bars.v_empty[stage], turn - 1);
+                to = smem + S::kV + stage * S::kOne + vh * (kD * 128);
+                __half2 s[4], s16[4], low[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    s[n] = __halves2half2(steps[kTile + vh * 64 + 16 * n + vc], steps[kTile + vh * 64 + 16 * n + 8 + vc]);
+                    s16[n] = __hmul2(s[n], sixteenth), low[n] = __hmul2(s[n], eighth);
+                }
+#pragma unroll
+                for (int x = 0; x < kVW; ++x)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t h[4][4];                        // [token pair][dimension]
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            decode_word(__byte_perm(vraw[2 * n][x], vraw[2 * n + 1][x], half ? 0x7632 : 0x5410), h[n]);
+                            scale_word(h[n], s[n], s16[n], low[n]);
+                        }
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            *reinterpret_cast<uint4*>(to + tc::sw128_offset(vd + x * 8 + half * 4 + d, vc * 8)) =
+                                make_uint4(h[0][d], h[1][d], h[2][d], h[3][d]);
+                    }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(&bars.v_full[stage]);
+                if (more) load_values(j + 1);
+            }
+        } while (walk_next(a, k, group, step));
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 12 && lane == 0 && any) {
+            // -------------------------------------------------------------- products
+            constexpr uint32_t kS = tc::idesc_f16_f32(kTile, kTile), kO = tc::idesc_f16_f32(kTile, kD);
+            uint32_t q_phase[2] = {}, p_phase[2] = {};
+            uint32_t column = 0;                                // of the piece's first tile
+            do {
+                const int tiles = k.t1 - k.t0;
+                const bool both = same || k.rows > kTile;
+                // Group g's tiles: all (row tiles apart), or every other one (the same rows).
+                const int stride = same ? 2 : 1;
+                auto first_product = [&](int g, int j) {        // S of group g and tile j
+                    const uint32_t c = column + j, stage = c % kStages;
+                    wait(bars.k_full[stage], c / kStages);
+                    tc::tc_fence_after();
+                    const uint32_t qa = tc::smem_u32(smem + S::kQ + g * S::kOne), kb = tc::smem_u32(smem + S::kK + stage * S::kOne);
+#pragma unroll
+                    for (int x = 0; x < kD / 16; ++x) {
+                        const uint32_t off = (x >> 2) * (kTile * 128) + (x & 3) * 32;
+                        tc::mma_f16(tmem + g * kTile, tc::desc_sw128(qa + off), tc::desc_sw128(kb + off), kS, x > 0);
+                    }
+                    tc::mma_commit(&bars.s_full[g]);
+                    if (same || g == 1 || !both) tc::mma_commit(&bars.k_empty[stage]);   // the tile's last use
+                };
+                for (int g = 0; g < (both ? 2 : 1); ++g) {
+                    const int j = same ? g : 0;
+                    if (j >= tiles && same) continue;
+                    wait(bars.q_full[g], q_phase[g]++);
+                    tc::tc_fence_after();
+                    first_product(g, j);
+                }
+                if (same && tiles < 2) wait(bars.q_full[1], q_phase[1]++);
+                for (int j = 0; j < tiles; ++j) {
+                    for (int x = 0; x < (same ? 1 : both ? 2 : 1); ++x) {
+                        const int g = same ? (j & 1) : x;
+                        const uint32_t c = column + j, stage = c % kStages;
+                        wait(bars.p_full[g], p_phase[g]++);
+                        wait(bars.v_full[stage], c / kStages);
+                        tc::tc_fence_after();
+                        const uint32_t vb = tc::smem_u32(smem + S::kV + stage * S::kOne);
+#pragma unroll
+                        for (int n = 0; n < kTile / 16; ++n)
+                            mma_ts(tmem + 2 * kTile + g * kTile, tmem + g * kTile + n * 8,
+                                   tc::desc_sw128(vb + (n >> 2) * (kD * 128) + (n & 3) * 32), kO, n > 0 || j >= stride);
+                        tc::mma_commit(&bars.o_done[g]);
+                        if (same || x == 1 || !both) tc::mma_commit(&bars.v_empty[stage]);
+                        if (j + stride < tiles) first_product(g, j + stride);
+                    }
+                }
+                column += tiles;
+            } while (walk_next(a, k, group, step));
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 12) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int kD, int kDtype>
+cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+    auto* kernel = chunk_kernel<kD, kDtype>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
+    if (e != cudaSuccess) return e;
+    const int same = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= kTile;
+    kernel<<<ctx.sm_count, kThreads, Smem<kD>::kBytes, st>>>(a, same, ctx.attn_pieces, ctx.attn_arrivals, ctx.s.status);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attention_chunk_scratch_floats(int sm_count) { return static_cast<size_t>(sm_count) * 2 * kPieceFloats; }
+
+cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+    if (a.c.head_dim == 64)
+        return dtype == HC_DTYPE_BF16 ? launch_chunk<64, HC_DTYPE_BF16>(ctx, a, st) : launch_chunk<64, HC_DTYPE_FP16>(ctx, a, st);
+    return dtype == HC_DTYPE_BF16 ? launch_chunk<128, HC_DTYPE_BF16>(ctx, a, st) : launch_chunk<128, HC_DTYPE_FP16>(ctx, a, st);
+}
+
+}  // namespace hc
