@@ -26,6 +26,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hc_attention.cuh"
 
 namespace hc {
@@ -36,7 +38,8 @@ constexpr int kTile = 128;                 // keys of a tile, rows of a row tile
 constexpr int kStages = 2;                 // key tiles and value tiles in shared memory
 constexpr int kCols = 4;                   // column data of tiles (see the ring below)
 constexpr int kPieceCost = 2;              // what a piece costs beside its tiles, in tiles
-constexpr float kRaise = 8.f;              // log2 by which a logit may pass the maximum
+constexpr float kRaise = 8.f;              // log2 by which a logit may pass the maximum before it is raised
+constexpr float kMost = 15.f;              // and the most that a weight may have as fp16
 constexpr int kPieceFloats = 256 * 128 + 512;
 
 // What softmax needs of a tile's keys beside S and P. Four of them: a tile's data is
@@ -203,6 +206,16 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Four floats of shared memory as two pairs; volatile, so that a loop's loads stay in it.
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
+    asm volatile("ld.volatile.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(tc::smem_u32(p)));
+}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -330,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             float base = 0.f, sum = 0.f, flat = 0.f;
             bool fresh = true;
+            float later = 1.f;                         // what O is to be multiplied by before its next product
             int ev = 0, done_tiles = 0;
             const float g = factor * qsum;
             const uint64_t bits = a.mask && here ? a.mask[k.w.begin + i] : 0;
@@ -344,77 +358,90 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = j * kTile;
                 const bool tail = t + kTile > min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);
                 const int limit = (a.mask ? k.w.kv : min(k.w.kv, k.w.first + i + 1)) - t;
-                // Weights against the maximum so far, 32 keys at a time, held as P until all are
-                // known: a logit that passes the maximum by 2^8 (and a row's first one) raises it,
-                // and the tile is done again.
+                auto sees = [&](int c) {
+                    if (c >= limit) return false;
+                    const int back = t + c - k.w.first;
+                    return !a.mask || back < 0 || (back < 64 && ((bits >> back) & 1));
+                };
+                float fix = 1.f;
+                // a row's first maximum: of the logits of this tile that it sees
+                if (__any_sync(~0u, fresh)) {
+                    float peak = -CUDART_INF_F;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kTile; c0 += 16) {
+                        uint32_t raw[16];
+                        tmem_load16(s_mem + c0, raw);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float x = fmaf(__uint_as_float(raw[c]), f, col.k[c0 + c] * g);
+                            if (!tail || sees(c0 + c)) peak = fmaxf(peak, x);
+                        }
+                    }
+                    if (fresh && peak != -CUDART_INF_F) base = peak, fresh = false;
+                }
+                // Weights against the maximum so far, 32 keys at a time, two to an instruction, held
+                // as P until the tile is done; and their products with what is common to a value's
+                // dimensions.
                 uint32_t pw[2][32];
                 float peak, sum_now, flat_now;
-                auto weigh = [&]() {
-                    peak = -CUDART_INF_F, sum_now = sum, flat_now = flat;
+                auto weigh = [&](auto with_tail) {
+                    constexpr bool kTail = decltype(with_tail)::value;
+                    const uint64_t f2 = pair(f, f), g2 = pair(g, g), b2 = pair(-base, -base);
+                    uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
+                    peak = -CUDART_INF_F;
 #pragma unroll
                     for (int part = 0; part < 4; ++part) {
                         uint32_t raw[32];
                         tmem_load32(s_mem + part * 32, raw);
                         tmem_wait_load();
-                        float x[32];
+                        float e[32];
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 off = *reinterpret_cast<const float4*>(&col.k[part * 32 + c]);
-                            x[c] = fmaf(__uint_as_float(raw[c]), f, fmaf(off.x, g, -base));
-                            x[c + 1] = fmaf(__uint_as_float(raw[c + 1]), f, fmaf(off.y, g, -base));
-                            x[c + 2] = fmaf(__uint_as_float(raw[c + 2]), f, fmaf(off.z, g, -base));
-                            x[c + 3] = fmaf(__uint_as_float(raw[c + 3]), f, fmaf(off.w, g, -base));
-                        }
-                        if (tail) {
+                            uint64_t ko[2], vo[2];
+                            load_pairs(&col.k[part * 32 + c], ko);
+                            load_pairs(&col.v[part * 32 + c], vo);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                bool sees = part * 32 + c < limit;
-                                if (a.mask) {
-                                    const int back = t + part * 32 + c - k.w.first;
-                                    sees &= back < 0 || (back < 64 && ((bits >> back) & 1));
+                            for (int n = 0; n < 2; ++n) {
+                                const uint64_t z = fma2(pair(__uint_as_float(raw[c + 2 * n]), __uint_as_float(raw[c + 2 * n + 1])), f2,
+                                                        fma2(ko[n], g2, b2));
+                                float2 x = unpair(z);
+                                if (kTail) {
+                                    float2 v = unpair(vo[n]);        // a hidden value may be NaN
+                                    if (!sees(part * 32 + c + 2 * n)) x.x = -CUDART_INF_F, v.x = 0.f;
+                                    if (!sees(part * 32 + c + 2 * n + 1)) x.y = -CUDART_INF_F, v.y = 0.f;
+                                    vo[n] = pair(v.x, v.y);
                                 }
-                                if (!sees) x[c] = -CUDART_INF_F;
+                                peak = max3(peak, x.x, x.y);
+                                e[c + 2 * n] = exp2_fast(x.x), e[c + 2 * n + 1] = exp2_fast(x.y);
+                                const uint64_t w = pair(e[c + 2 * n], e[c + 2 * n + 1]);
+                                sum2 = add2(sum2, w);
+                                flat2 = fma2(w, vo[n], flat2);
                             }
                         }
+                        // P: column c * 8 + n of each 32 is token n * 4 + c, the order of the decoded values
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) peak = fmaxf(peak, x[c]);
-                        // and the weights' products with what is common to a value's dimensions
+                        for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 off = *reinterpret_cast<const float4*>(&col.v[part * 32 + c]);
-                            const float o4[4] = {off.x, off.y, off.z, off.w};
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                const bool hidden = tail && x[c + n] == -CUDART_INF_F;
-                                x[c + n] = exp2_fast(x[c + n]);
-                                sum_now += x[c + n];
-                                flat_now = fmaf(x[c + n], hidden ? 0.f : o4[n], flat_now);
-                            }
-                        }
-                        // P: column c * 8 + n of each 64 is token n * 8 + c, the order of the decoded
-                        // values: word 4 c + n holds tokens 16 n + c and 16 n + 8 + c
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                pw[part >> 1][4 * c + 2 * (part & 1) + n] = pack_half2(x[16 * n + c], x[16 * n + 8 + c]);
+                            for (int n = 0; n < 4; ++n)
+                                pw[part >> 1][(part & 1) * 16 + 4 * c + n] = pack_half2(e[8 * n + c], e[8 * n + 4 + c]);
                     }
+                    const float2 s2 = unpair(sum2), l2 = unpair(flat2);
+                    sum_now = s2.x + s2.y, flat_now = l2.x + l2.y;
                 };
-                float fix = 1.f;
-                weigh();
-                const bool rise = (fresh && peak != -CUDART_INF_F) || peak > kRaise;
-                if (__any_sync(~0u, rise)) {
-                    if (rise) {
-                        const float up = fresh ? peak : fmaxf(peak, 0.f);
-                        fix = fresh ? 1.f : exp2_fast(-up);
-                        fresh = false;
-                        base += up;
-                        sum *= fix;
-                        flat *= fix;
+                // done again only where a weight is beyond fp16 (the second time none is)
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (tail) weigh(std::true_type());
+                    else weigh(std::false_type());
+                    if (pass || !__any_sync(~0u, peak > kMost)) break;
+                    if (peak > kMost) {
+                        const float by = exp2_fast(-peak);
+                        fix *= by, sum *= by, flat *= by, base += peak;
                     }
-                    weigh();
                 }
                 sum = sum_now, flat = flat_now;
+                fix *= later, later = 1.f;
                 if (done_tiles == 0) {
                     ev = col.ev;
                 } else {
@@ -442,6 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tc_fence_before();
                 tc::mbar_arrive(&bars.p_full[wg]);
                 ++done_tiles;
+                // a maximum that was passed is raised for the tiles to come
+                if (peak > kRaise) {
+                    later = exp2_fast(-peak);
+                    sum *= later, flat *= later, base += peak;
+                }
             }
             // ---- the end of the piece
             if (done_tiles > 0) {
@@ -464,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t v[32];
                         if (done_tiles > 0) tmem_load32(o_mem + c * 32, v);
                         tmem_wait_load();
-                        const float up = done_tiles > 0 ? ldexpf(1.f, ev) : 0.f;
+                        const float up = done_tiles > 0 ? ldexpf(later, ev) : 0.f;
 #pragma unroll
                         for (int n = 0; n < 32; ++n)
                             exchange[(c * 32 + n) * kTile + row] = done_tiles > 0 ? fmaf(__uint_as_float(v[n]), up, flat) : 0.f;
@@ -475,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool writes = active && !(same && wg == 1);
             float peak = base, total = sum, mine = base == -CUDART_INF_F ? 0.f : 1.f, other = 0.f;
+            const float up = done_tiles > 0 ? ldexpf(later, ev) : 0.f;
             if (same && wg == 0) {
                 peak = fmaxf(base, other_base);
                 mine = base == -CUDART_INF_F ? 0.f : exp2_fast(base - peak);
@@ -492,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        narrow2<kDtype>(v[8 * n + 4] * inv, v[8 * n + 5] * inv), narrow2<kDtype>(v[8 * n + 6] * inv, v[8 * n + 7] * inv));
             };
             if (writes) {
-                const float up = done_tiles > 0 ? ldexpf(1.f, ev) : 0.f, inv = total == 0.f ? 0.f : 1.f / total;
+                const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
                 for (int c = 0; c < kD / 32; ++c) {
                     uint32_t v[32];
@@ -579,42 +612,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kSegs = kD / 32;
         const int seg = (lane >> 3) % kSegs;
         auto key_token = [&](int u) { return (u * (128 / kUnits) + w * (32 / kUnits) + (lane >> 3) / kSegs * 8 + (lane & 7)); };
-        // values: tokens n * 8 + vc of the 64-token half vh, kVW words from dimension vd on
-        const int vc = lane & 7, vh = w >> 1, vd = ((w & 1) * 4 + (lane >> 3)) * (8 * kVW);
+        // values: tokens n * 4 + vt (n = 0..7) of the 64-token half vh, kVW words from dimension vd on
+        const int vc = lane & 7, vt = (vc >> 2) * 32 + (vc & 3), vh = w >> 1, vd = ((w & 1) * 4 + (lane >> 3)) * (8 * kVW);
         uint32_t column = 0;
         if (any) do {
             int ev = 0;
             bool have_ev = false;
             uint32_t kraw[kUnits][kW], vraw[8][kVW], ks = 0, vs = 0;
-            auto group_at = [&](int t) {                        // group of token t's key, which exists
-                const int64_t id = load_block(a, k.b, t >> sh, status);
-                return (id * 2 * a.c.kv_heads + k.h) * a.c.block_size + (t & (a.c.block_size - 1));
+            // Lanes 0-7 hold the blocks of a tile's eight 16-token parts, looked up a tile ahead.
+            int ids = 0;
+            const uint32_t block_bytes = static_cast<uint32_t>(2 * to_values * (kD / 2));
+            const unsigned char* codes = a.c.codes + static_cast<int64_t>(k.h) * a.c.block_size * (kD / 2);
+            const int in_block = a.c.block_size - 1;
+            auto look_up = [&](int j) {
+                const int t = j * kTile + lane * 16;
+                if (lane < 8 && j < k.t1 && t < k.w.kv) ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
+            };
+            auto check = [&]() {
+                if (static_cast<unsigned>(ids) >= static_cast<unsigned>(a.c.blocks)) {
+                    atomicOr(status, kStatusBounds);
+                    ids = 0;                                    // wrong values, from the cache's own memory
+                }
+            };
+            // bytes from `codes` to the codes of token `x` of tile j
+            auto place = [&](int j, int x) -> uint64_t {
+                const uint32_t id = __shfl_sync(~0u, ids, x >> 4);
+                return static_cast<uint64_t>(id) * block_bytes + static_cast<uint32_t>(((j * kTile + x) & in_block) * (kD / 2));
             };
             auto load_scales = [&](int j) {
-                const int t = j * kTile + p;
+                const uint64_t at = place(j, p);
                 ks = vs = 0;
-                if (t < k.w.kv) {
-                    const int64_t at = group_at(t);
-                    ks = scales[at];
-                    vs = scales[at + to_values];
+                if (j * kTile + p < k.w.kv) {
+                    const uint32_t* from = scales + static_cast<int64_t>(k.h) * a.c.block_size + at / (kD / 2);
+                    ks = from[0];
+                    vs = from[to_values];
                 }
             };
             auto load_keys = [&](int j) {
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) {
-                    const int t = j * kTile + key_token(u);
+                    const uint64_t at = place(j, key_token(u));
                     uint4 y = make_uint4(0, 0, 0, 0);
-                    if (t < k.w.kv) y = ldg_stream_v4(a.c.codes + group_at(t) * (kD / 2) + seg * 16);
+                    if (j * kTile + key_token(u) < k.w.kv) y = ldg_stream_v4(codes + at + seg * 16);
                     kraw[u][0] = y.x, kraw[u][1] = y.y, kraw[u][2] = y.z, kraw[u][3] = y.w;
                 }
             };
             auto load_values = [&](int j) {
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    const int t = j * kTile + vh * 64 + n * 8 + vc;
+                    const int x = vh * 64 + n * 4 + vt;
+                    const uint64_t at = place(j, x);
                     uint2 y = make_uint2(0, 0);
-                    if (t < k.w.kv) {
-                        const unsigned char* from = a.c.codes + (group_at(t) + to_values) * (kD / 2) + vd / 2;
+                    if (j * kTile + x < k.w.kv) {
+                        const unsigned char* from = codes + at + to_values * (kD / 2) + vd / 2;
                         if (kVW == 2) y = *reinterpret_cast<const uint2*>(from);
                         else y.x = *reinterpret_cast<const uint32_t*>(from);
                     }
@@ -622,9 +672,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kVW == 2) vraw[n][kVW - 1] = y.y;
                 }
             };
+            look_up(k.t0);
+            check();
             load_scales(k.t0);
             load_keys(k.t0);
             load_values(k.t0);
+            look_up(k.t0 + 1);
             for (int j = k.t0; j < k.t1; ++j, ++column) {
                 const int stage = column % kStages, turn = column / kStages;
                 // ---- steps and minima: a group held as NaN keeps the NaN in its common part alone
@@ -656,7 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 steps[kTile + p] = __float2half_rn(ldexpf(s_v, 24 - ev));
                 asm volatile("bar.sync 4, 128;" ::: "memory");
                 const bool more = j + 1 < k.t1;
-                if (more) load_scales(j + 1);
+                if (more) {
+                    check();
+                    load_scales(j + 1);
+                }
                 // ---- keys
                 const __half2 sixteenth = __float2half2_rn(0.0625f), eighth = __float2half2_rn(-4.76837158203125e-7f);   // -8 2^-24
                 unsigned char* to = smem + S::kK + stage * S::kOne;
@@ -683,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __half2 s[4], s16[4], low[4];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    s[n] = __halves2half2(steps[kTile + vh * 64 + 16 * n + vc], steps[kTile + vh * 64 + 16 * n + 8 + vc]);
+                    s[n] = __halves2half2(steps[kTile + vh * 64 + 8 * n + vt], steps[kTile + vh * 64 + 8 * n + 4 + vt]);
                     s16[n] = __hmul2(s[n], sixteenth), low[n] = __hmul2(s[n], eighth);
                 }
 #pragma unroll
@@ -704,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(&bars.v_full[stage]);
                 if (more) load_values(j + 1);
+                look_up(j + 2);
             }
         } while (walk_next(a, k, group, step));
     } else {
