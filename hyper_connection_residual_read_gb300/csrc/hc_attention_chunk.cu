@@ -2,9 +2,9 @@
 // the query heads of a kv head), on tcgen05.
 //
 // Both products run on the tensor cores in fp16 with fp32 sums, 128 rows x 128 keys at a
-// time: S = Q K'^T from shared memory, O += P V' with P in tensor memory. Four kinds of
-// warps share a CTA: two warpgroups of softmax (a thread a row), one that decodes keys and
-// values, one warp that issues the products.
+// time: S = Q K'^T from shared memory, O += P V' with P in tensor memory. A CTA has two
+// warpgroups of softmax (a thread a row), each of which also issues its row tile's products,
+// one warpgroup that decodes keys and one that decodes values.
 //
 // * The decoded values are exact. A step has 8 significant bits (bf16) and |code - 8| <= 8
 //   at most 3, so s (code - 8) has 11 at most, which is what fp16 holds: K' = 2^-E s_j
@@ -47,8 +47,9 @@ constexpr int kPieceFloats = 256 * 128 + 512;
 // tile two later, which follow the softmax of this one.
 struct Column {
     float k[kTile], v[kTile];              // m + 8 s of keys and values
-    int ek, ev;                            // exponents divided out of K' and V'
-    int pad[2];
+    float up[2];                           // 2^E of K', in two factors
+    int ev;                                // E of V'
+    int pad;
 };
 
 template <int kD>
@@ -63,7 +64,7 @@ struct Smem {
 };
 
 struct Bars {
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], o_done[2];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], col_full[kCols];
 };
 
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int64_t sums[kThreads / 32];
     __shared__ uint32_t tmem_slot;
     __shared__ unsigned last_one[2];
-    __shared__ uint32_t step_max[2][2][4];
+    __shared__ uint32_t step_max[2][2][4];     // [keys or values][tile parity][warp]
     __shared__ volatile int abort_flag;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Column* columns = reinterpret_cast<Column*>(smem + S::kColumn);
@@ -258,21 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bars.q_full[i], 128);
             tc::mbar_init(&bars.s_full[i], 1);
-            tc::mbar_init(&bars.p_full[i], 128);
             tc::mbar_init(&bars.o_done[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&bars.k_full[i], 128);
-            tc::mbar_init(&bars.k_empty[i], 1);
+            tc::mbar_init(&bars.k_empty[i], 2);     // one for each row tile
             tc::mbar_init(&bars.v_full[i], 128);
-            tc::mbar_init(&bars.v_empty[i], 1);
+            tc::mbar_init(&bars.v_empty[i], 2);
         }
-        for (int i = 0; i < kCols; ++i) tc::mbar_init(&bars.col_full[i], 128);
+        for (int i = 0; i < kCols; ++i) tc::mbar_init(&bars.col_full[i], 256);
         tc::fence_barrier_init();
     }
-    if (warp == 12) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
     tc::tc_fence_before();
     find_run(a, group, step, &run, sums, status);      // synchronises
     tc::tc_fence_after();
@@ -292,7 +291,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_mem = tmem + lanes + wg * kTile, o_mem = tmem + lanes + 2 * kTile + wg * kTile;
         unsigned char* q_tile = smem + S::kQ + wg * S::kOne;
         uint32_t s_phase = 0, o_phase = 0;
-        uint32_t column = 0;                           // tiles that the producers have been through
+        uint32_t column = 0;                           // tiles before this one, over all pieces
+        constexpr uint32_t kS = tc::idesc_f16_f32(kTile, kTile), kO = tc::idesc_f16_f32(kTile, kD);
+        const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(q_tile));
+        const uint64_t k_desc = tc::desc_sw128(tc::smem_u32(smem + S::kK)), v_desc = tc::desc_sw128(tc::smem_u32(smem + S::kV));
+        constexpr uint32_t kStageStep = S::kOne / 16, kAtom = kTile * 128 / 16, kAtomV = kD * 128 / 16;   // in the descriptors' 16 bytes
+        // The products of this row tile, issued by one thread. S of the tile that is number c of all:
+        auto issue_s = [&](uint32_t c, bool alone) {
+            const uint32_t stage = c % kStages;
+            wait(bars.k_full[stage], c / kStages);
+            tc::tc_fence_after();
+            const uint64_t kb = k_desc + stage * kStageStep;
+#pragma unroll
+            for (int x = 0; x < kD / 16; ++x) {
+                const uint32_t off = (x >> 2) * kAtom + (x & 3) * 2;
+                tc::mma_f16(tmem + wg * kTile, q_desc + off, kb + off, kS, x > 0);
+            }
+            tc::mma_commit(&bars.s_full[wg]);
+            tc::mma_commit(&bars.k_empty[stage]);
+            if (alone) tc::mma_commit(&bars.k_empty[stage]);
+        };
+        // and P V', which follows S's reader and comes before S's next writer in issue order
+        auto issue_o = [&](uint32_t c, bool alone, bool more) {
+            const uint32_t stage = c % kStages;
+            wait(bars.v_full[stage], c / kStages);
+            tc::tc_fence_after();
+            const uint64_t vb = v_desc + stage * kStageStep;
+#pragma unroll
+            for (int n = 0; n < kTile / 16; ++n)
+                mma_ts(tmem + 2 * kTile + wg * kTile, tmem + wg * kTile + n * 8, vb + (n >> 2) * kAtomV + (n & 3) * 2, kO, n > 0 || more);
+            tc::mma_commit(&bars.o_done[wg]);
+            tc::mma_commit(&bars.v_empty[stage]);
+            if (alone) tc::mma_commit(&bars.v_empty[stage]);
+        };
         if (any) do {
             const int r = k.row0 + (same ? 0 : wg * kTile) + row;     // row of the window
             const bool active = same || wg == 0 || k.rows > kTile;    // this warpgroup has rows
@@ -338,7 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&bars.q_full[wg]);
+            }
+            // this row tile's key tiles: all, or every other one, which then no other row tile uses
+            const int stride = same ? 2 : 1, j0 = k.t0 + (same ? wg : 0);
+            const bool alone = same || k.rows <= kTile;
+            if (active) {
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                if (row == 0 && j0 < k.t1) issue_s(column + (j0 - k.t0), alone);
             }
 
             float base = 0.f, sum = 0.f, flat = 0.f;
@@ -352,8 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Column& col = columns[column % kCols];
                 wait(bars.col_full[column % kCols], column / kCols);
                 wait(bars.s_full[wg], s_phase++);
+                __syncwarp();
                 tc::tc_fence_after();
-                const float f = ldexpf(factor, col.ek);
+                const float f = factor * col.up[0] * col.up[1];
                 // hidden keys: behind the end, or behind this row's token, or out of its mask
                 const int t = j * kTile;
                 const bool tail = t + kTile > min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);
@@ -390,11 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t f2 = pair(f, f), g2 = pair(g, g), b2 = pair(-base, -base);
                     uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
                     peak = -CUDART_INF_F;
+                    uint32_t ahead[2][32];
+                    tmem_load32(s_mem, ahead[0]);
 #pragma unroll
                     for (int part = 0; part < 4; ++part) {
-                        uint32_t raw[32];
-                        tmem_load32(s_mem + part * 32, raw);
                         tmem_wait_load();
+                        uint32_t(&raw)[32] = ahead[part & 1];
+                        if (part < 3) tmem_load32(s_mem + (part + 1) * 32, ahead[(part + 1) & 1]);
                         float e[32];
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
@@ -449,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (__any_sync(~0u, fix != 1.f || other)) {
                         // O of the tiles before is complete, and this warp's lanes of it are rescaled
                         wait(bars.o_done[wg], o_phase + done_tiles - 1);
+                        __syncwarp();
                         tc::tc_fence_after();
                         const float by = other ? ldexpf(fix, ev - col.ev) : fix;
                         ev = col.ev;
@@ -467,7 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_store32(s_mem + 32, pw[1]);
                 tmem_wait_store();
                 tc::tc_fence_before();
-                tc::mbar_arrive(&bars.p_full[wg]);
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                if (row == 0) {
+                    issue_o(column, alone, done_tiles > 0);
+                    if (j + stride < k.t1) issue_s(column + stride, alone);
+                }
                 ++done_tiles;
                 // a maximum that was passed is raised for the tiles to come
                 if (peak > kRaise) {
@@ -478,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the end of the piece
             if (done_tiles > 0) {
                 wait(bars.o_done[wg], o_phase + done_tiles - 1);
+                __syncwarp();
                 tc::tc_fence_after();
             }
             o_phase += done_tiles;
@@ -553,7 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc::tc_fence_before();
-            if (same) asm volatile("bar.sync 1, 256;" ::: "memory");   // the exchange is read
+            // Both together to the next piece: the exchange is read; and a warpgroup without rows
+            // must not run ahead, since a wait tells only whether a phase of its parity is over.
+            if (alone) asm volatile("bar.sync 1, 256;" ::: "memory");
             if (!whole && writes) {
                 // each row tile is joined by the last CTA that has part of it
                 const int64_t n = run.ctas;
@@ -597,33 +645,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } while (walk_next(a, k, group, step));
-    } else if (warp < 12) {
-        // ------------------------------------------------------------------ keys and values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        constexpr int kW = 4;                                   // words of a thread's keys
-        constexpr int kUnits = kD / 32;                         // 16-byte pieces of keys a thread decodes
-        constexpr int kVW = kD / 64;                            // words of a thread's values of one token
-        const int p = threadIdx.x - 256, w = warp - 8;
-        const int sh = 31 - __clz(a.c.block_size);
+    } else {
+        // ------------------------------------------------------------------ keys, values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        const bool is_v = warp >= 12;
+        const int p = threadIdx.x & 127, w = warp & 3;
+        const int sh = 31 - __clz(a.c.block_size), in_block = a.c.block_size - 1;
         const int64_t to_values = static_cast<int64_t>(a.c.kv_heads) * a.c.block_size;
-        const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.c.scales);
-        __half* steps = reinterpret_cast<__half*>(smem + S::kSteps);
-        // keys: piece u of this thread is 16 bytes, `seg`, of token key_token(u)
-        constexpr int kSegs = kD / 32;
+        const uint32_t block_bytes = static_cast<uint32_t>(2 * to_values * (kD / 2));
+        __half* steps = reinterpret_cast<__half*>(smem + S::kSteps) + (is_v ? kTile : 0);
+        const __half2 sixteenth = __float2half2_rn(0.0625f), eighth = __float2half2_rn(-4.76837158203125e-7f);   // -8 2^-24
+        // Keys: piece u of a thread is 16 bytes, `seg`, of token key_token(u). Values: tokens n * 4
+        // + vt (n = 0..7) of the 64-token half vh, kVW words from dimension vd on.
+        constexpr int kUnits = kD / 32, kSegs = kD / 32, kVW = kD / 64;
         const int seg = (lane >> 3) % kSegs;
-        auto key_token = [&](int u) { return (u * (128 / kUnits) + w * (32 / kUnits) + (lane >> 3) / kSegs * 8 + (lane & 7)); };
-        // values: tokens n * 4 + vt (n = 0..7) of the 64-token half vh, kVW words from dimension vd on
+        auto key_token = [&](int u) { return u * (128 / kUnits) + w * (32 / kUnits) + (lane >> 3) / kSegs * 8 + (lane & 7); };
         const int vc = lane & 7, vt = (vc >> 2) * 32 + (vc & 3), vh = w >> 1, vd = ((w & 1) * 4 + (lane >> 3)) * (8 * kVW);
         uint32_t column = 0;
         if (any) do {
-            int ev = 0;
-            bool have_ev = false;
-            uint32_t kraw[kUnits][kW], vraw[8][kVW], ks = 0, vs = 0;
             // Lanes 0-7 hold the blocks of a tile's eight 16-token parts, looked up a tile ahead.
             int ids = 0;
-            const uint32_t block_bytes = static_cast<uint32_t>(2 * to_values * (kD / 2));
-            const unsigned char* codes = a.c.codes + static_cast<int64_t>(k.h) * a.c.block_size * (kD / 2);
-            const int in_block = a.c.block_size - 1;
+            const int64_t first = (static_cast<int64_t>(k.h) + (is_v ? a.c.kv_heads : 0)) * a.c.block_size;   // group in a block
+            const unsigned char* codes = a.c.codes + first * (kD / 2) + (is_v ? vd / 2 : seg * 16);
+            const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.c.scales) + first;
             auto look_up = [&](int j) {
                 const int t = j * kTile + lane * 16;
                 if (lane < 8 && j < k.t1 && t < k.w.kv) ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
@@ -634,192 +678,133 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ids = 0;                                    // wrong values, from the cache's own memory
                 }
             };
-            // bytes from `codes` to the codes of token `x` of tile j
+            // bytes from `codes` to those of token `x` of tile j
             auto place = [&](int j, int x) -> uint64_t {
                 const uint32_t id = __shfl_sync(~0u, ids, x >> 4);
                 return static_cast<uint64_t>(id) * block_bytes + static_cast<uint32_t>(((j * kTile + x) & in_block) * (kD / 2));
             };
+            uint32_t raw[16], scale = 0;                        // keys [kUnits][4], or values [8][kVW]
             auto load_scales = [&](int j) {
                 const uint64_t at = place(j, p);
-                ks = vs = 0;
-                if (j * kTile + p < k.w.kv) {
-                    const uint32_t* from = scales + static_cast<int64_t>(k.h) * a.c.block_size + at / (kD / 2);
-                    ks = from[0];
-                    vs = from[to_values];
-                }
+                scale = 0;
+                if (j * kTile + p < k.w.kv) scale = scales[at / (kD / 2)];
             };
-            auto load_keys = [&](int j) {
+            auto load_codes = [&](int j) {
+                if (!is_v) {
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const uint64_t at = place(j, key_token(u));
-                    uint4 y = make_uint4(0, 0, 0, 0);
-                    if (j * kTile + key_token(u) < k.w.kv) y = ldg_stream_v4(codes + at + seg * 16);
-                    kraw[u][0] = y.x, kraw[u][1] = y.y, kraw[u][2] = y.z, kraw[u][3] = y.w;
-                }
-            };
-            auto load_values = [&](int j) {
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const int x = vh * 64 + n * 4 + vt;
-                    const uint64_t at = place(j, x);
-                    uint2 y = make_uint2(0, 0);
-                    if (j * kTile + x < k.w.kv) {
-                        const unsigned char* from = codes + at + to_values * (kD / 2) + vd / 2;
-                        if (kVW == 2) y = *reinterpret_cast<const uint2*>(from);
-                        else y.x = *reinterpret_cast<const uint32_t*>(from);
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint64_t at = place(j, key_token(u));
+                        uint4 y = make_uint4(0, 0, 0, 0);
+                        if (j * kTile + key_token(u) < k.w.kv) y = *reinterpret_cast<const uint4*>(codes + at);
+                        raw[4 * u] = y.x, raw[4 * u + 1] = y.y, raw[4 * u + 2] = y.z, raw[4 * u + 3] = y.w;
                     }
-                    vraw[n][0] = y.x;
-                    if (kVW == 2) vraw[n][kVW - 1] = y.y;
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const int x = vh * 64 + n * 4 + vt;
+                        const uint64_t at = place(j, x);
+                        uint2 y = make_uint2(0, 0);
+                        if (j * kTile + x < k.w.kv) {
+                            if (kVW == 2) y = *reinterpret_cast<const uint2*>(codes + at);
+                            else y.x = *reinterpret_cast<const uint32_t*>(codes + at);
+                        }
+                        raw[n * kVW] = y.x;
+                        if (kVW == 2) raw[n * kVW + kVW - 1] = y.y;
+                    }
                 }
             };
             look_up(k.t0);
             check();
             load_scales(k.t0);
-            load_keys(k.t0);
-            load_values(k.t0);
+            load_codes(k.t0);
             look_up(k.t0 + 1);
+            int ev = 0;
+            bool have_ev = false;
             for (int j = k.t0; j < k.t1; ++j, ++column) {
                 const int stage = column % kStages, turn = column / kStages;
-                // ---- steps and minima: a group held as NaN keeps the NaN in its common part alone
-                float s_k = bf16_lo(ks), s_v = bf16_lo(vs);
-                const float o_k = fmaf(8.f, s_k, bf16_hi(ks)), o_v = fmaf(8.f, s_v, bf16_hi(vs));
-                if (!(s_k <= 3.0e38f)) s_k = 0.f;
-                if (!(s_v <= 3.0e38f)) s_v = 0.f;
-                const uint32_t mk = __reduce_max_sync(~0u, __float_as_uint(s_k)), mv = __reduce_max_sync(~0u, __float_as_uint(s_v));
-                if (lane == 0) step_max[column & 1][0][w] = mk, step_max[column & 1][1][w] = mv;
-                asm volatile("bar.sync 4, 128;" ::: "memory");
-                const uint32_t* m0 = step_max[column & 1][0];
-                const uint32_t* m1 = step_max[column & 1][1];
-                const uint32_t top_k = max(max(m0[0], m0[1]), max(m0[2], m0[3])), top_v = max(max(m1[0], m1[1]), max(m1[2], m1[3]));
-                // K': the largest step in [2^-9, 2^-8); V': the first tile's in [2^-12, 2^-11), and
-                // later ones below 2^-8, else the exponent follows
-                const int ek = top_k ? static_cast<int>(top_k >> 23) - 127 + 9 : 0;
-                if (top_v && (!have_ev || static_cast<int>(top_v >> 23) - 127 + 9 > ev)) {
-                    ev = static_cast<int>(top_v >> 23) - 127 + 12;
-                    have_ev = true;
-                }
+                // steps and minima: a group held as NaN keeps the NaN in its common part alone
+                float s_own = bf16_lo(scale);
+                const float common = fmaf(8.f, s_own, bf16_hi(scale));
+                if (!(s_own <= 3.0e38f)) s_own = 0.f;
+                const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(s_own));
+                uint32_t* tops = step_max[is_v][column & 1];
+                if (lane == 0) tops[w] = most;
+                asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
+                const uint32_t top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+                // K': the largest step in [2^-9, 2^-8). V': that of the piece's first tile in [2^-12,
+                // 2^-11), and later ones below 2^-8, else the exponent follows.
+                const int e9 = top ? static_cast<int>(top >> 23) - 127 + 9 : 0;
+                if (is_v && top && (!have_ev || e9 > ev)) ev = e9 + 3, have_ev = true;
+                const int e = is_v ? ev : e9;
+                // the softmax of the tile four before has been through with its column: see Column
+                if (turn > 0) wait(is_v ? bars.v_empty[stage] : bars.k_empty[stage], turn - 1);
                 Column& col = columns[column % kCols];
-                // the softmax of the tile four before has been through with this one: see Column
-                if (turn > 0) wait(bars.k_empty[stage], turn - 1);
-                col.k[p] = o_k;
-                col.v[p] = o_v;
-                if (p == 0) col.ek = ek, col.ev = ev;
+                (is_v ? col.v : col.k)[p] = common;
+                if (p == 0) {
+                    if (is_v) col.ev = ev;
+                    else col.up[0] = power_of_two(e9 / 2), col.up[1] = power_of_two(e9 - e9 / 2);
+                }
                 tc::mbar_arrive(&bars.col_full[column % kCols]);
-                steps[p] = __float2half_rn(ldexpf(s_k, 24 - ek));
-                steps[kTile + p] = __float2half_rn(ldexpf(s_v, 24 - ev));
-                asm volatile("bar.sync 4, 128;" ::: "memory");
+                // 2^24 2^-E s, for E of any step
+                steps[p] = __float2half_rn(s_own * power_of_two((24 - e) / 2) * power_of_two(24 - e - (24 - e) / 2));
+                asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
                 const bool more = j + 1 < k.t1;
                 if (more) {
                     check();
                     load_scales(j + 1);
                 }
-                // ---- keys
-                const __half2 sixteenth = __float2half2_rn(0.0625f), eighth = __float2half2_rn(-4.76837158203125e-7f);   // -8 2^-24
-                unsigned char* to = smem + S::kK + stage * S::kOne;
+                if (!is_v) {
+                    unsigned char* to = smem + S::kK + stage * S::kOne;
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const int t = key_token(u);
-                    const __half2 s = __half2half2(steps[t]), s16 = __hmul2(s, sixteenth), low = __hmul2(s, eighth);
-#pragma unroll
-                    for (int n = 0; n < kW; ++n) {
-                        uint32_t h[4];
-                        decode_word(kraw[u][n], h);
-                        scale_word(h, s, s16, low);
-                        const int c = seg * 4 + n;               // 8 dimensions
-                        *reinterpret_cast<uint4*>(to + (c >> 3) * (kTile * 128) + tc::sw128_offset(t, (c & 7) * 8)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                }
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&bars.k_full[stage]);
-                if (more) load_keys(j + 1);
-                // ---- values, transposed
-                if (turn > 0) wait(bars.v_empty[stage], turn - 1);
-                to = smem + S::kV + stage * S::kOne + vh * (kD * 128);
-                __half2 s[4], s16[4], low[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    s[n] = __halves2half2(steps[kTile + vh * 64 + 8 * n + vt], steps[kTile + vh * 64 + 8 * n + 4 + vt]);
-                    s16[n] = __hmul2(s[n], sixteenth), low[n] = __hmul2(s[n], eighth);
-                }
-#pragma unroll
-                for (int x = 0; x < kVW; ++x)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t h[4][4];                        // [token pair][dimension]
+                    for (int u = 0; u < kUnits; ++u) {
+                        const int t = key_token(u);
+                        const __half2 s = __half2half2(steps[t]), s16 = __hmul2(s, sixteenth), low = __hmul2(s, eighth);
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            decode_word(__byte_perm(vraw[2 * n][x], vraw[2 * n + 1][x], half ? 0x7632 : 0x5410), h[n]);
-                            scale_word(h[n], s[n], s16[n], low[n]);
+                            uint32_t h[4];
+                            decode_word(raw[4 * u + n], h);
+                            scale_word(h, s, s16, low);
+                            const int c = seg * 4 + n;           // 8 dimensions
+                            *reinterpret_cast<uint4*>(to + (c >> 3) * (kTile * 128) + tc::sw128_offset(t, (c & 7) * 8)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
                         }
-#pragma unroll
-                        for (int d = 0; d < 4; ++d)
-                            *reinterpret_cast<uint4*>(to + tc::sw128_offset(vd + x * 8 + half * 4 + d, vc * 8)) =
-                                make_uint4(h[0][d], h[1][d], h[2][d], h[3][d]);
                     }
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&bars.v_full[stage]);
-                if (more) load_values(j + 1);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&bars.k_full[stage]);
+                } else {
+                    // transposed: a row of V' is a dimension
+                    unsigned char* to = smem + S::kV + stage * S::kOne + vh * (kD * 128);
+                    __half2 s[4], s16[4], low[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        s[n] = __halves2half2(steps[vh * 64 + 8 * n + vt], steps[vh * 64 + 8 * n + 4 + vt]);
+                        s16[n] = __hmul2(s[n], sixteenth), low[n] = __hmul2(s[n], eighth);
+                    }
+#pragma unroll
+                    for (int x = 0; x < kVW; ++x)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t h[4][4];                    // [token pair][dimension]
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                decode_word(__byte_perm(raw[2 * n * kVW + x], raw[(2 * n + 1) * kVW + x], half ? 0x7632 : 0x5410), h[n]);
+                                scale_word(h[n], s[n], s16[n], low[n]);
+                            }
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)
+                                *reinterpret_cast<uint4*>(to + tc::sw128_offset(vd + x * 8 + half * 4 + d, vc * 8)) =
+                                    make_uint4(h[0][d], h[1][d], h[2][d], h[3][d]);
+                        }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&bars.v_full[stage]);
+                }
+                if (more) load_codes(j + 1);
                 look_up(j + 2);
             }
         } while (walk_next(a, k, group, step));
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 12 && lane == 0 && any) {
-            // -------------------------------------------------------------- products
-            constexpr uint32_t kS = tc::idesc_f16_f32(kTile, kTile), kO = tc::idesc_f16_f32(kTile, kD);
-            uint32_t q_phase[2] = {}, p_phase[2] = {};
-            uint32_t column = 0;                                // of the piece's first tile
-            do {
-                const int tiles = k.t1 - k.t0;
-                const bool both = same || k.rows > kTile;
-                // Group g's tiles: all (row tiles apart), or every other one (the same rows).
-                const int stride = same ? 2 : 1;
-                auto first_product = [&](int g, int j) {        // S of group g and tile j
-                    const uint32_t c = column + j, stage = c % kStages;
-                    wait(bars.k_full[stage], c / kStages);
-                    tc::tc_fence_after();
-                    const uint32_t qa = tc::smem_u32(smem + S::kQ + g * S::kOne), kb = tc::smem_u32(smem + S::kK + stage * S::kOne);
-#pragma unroll
-                    for (int x = 0; x < kD / 16; ++x) {
-                        const uint32_t off = (x >> 2) * (kTile * 128) + (x & 3) * 32;
-                        tc::mma_f16(tmem + g * kTile, tc::desc_sw128(qa + off), tc::desc_sw128(kb + off), kS, x > 0);
-                    }
-                    tc::mma_commit(&bars.s_full[g]);
-                    if (same || g == 1 || !both) tc::mma_commit(&bars.k_empty[stage]);   // the tile's last use
-                };
-                for (int g = 0; g < (both ? 2 : 1); ++g) {
-                    const int j = same ? g : 0;
-                    if (j >= tiles && same) continue;
-                    wait(bars.q_full[g], q_phase[g]++);
-                    tc::tc_fence_after();
-                    first_product(g, j);
-                }
-                if (same && tiles < 2) wait(bars.q_full[1], q_phase[1]++);
-                for (int j = 0; j < tiles; ++j) {
-                    for (int x = 0; x < (same ? 1 : both ? 2 : 1); ++x) {
-                        const int g = same ? (j & 1) : x;
-                        const uint32_t c = column + j, stage = c % kStages;
-                        wait(bars.p_full[g], p_phase[g]++);
-                        wait(bars.v_full[stage], c / kStages);
-                        tc::tc_fence_after();
-                        const uint32_t vb = tc::smem_u32(smem + S::kV + stage * S::kOne);
-#pragma unroll
-                        for (int n = 0; n < kTile / 16; ++n)
-                            mma_ts(tmem + 2 * kTile + g * kTile, tmem + g * kTile + n * 8,
-                                   tc::desc_sw128(vb + (n >> 2) * (kD * 128) + (n & 3) * 32), kO, n > 0 || j >= stride);
-                        tc::mma_commit(&bars.o_done[g]);
-                        if (same || x == 1 || !both) tc::mma_commit(&bars.v_empty[stage]);
-                        if (j + stride < tiles) first_product(g, j + stride);
-                    }
-                }
-                column += tiles;
-            } while (walk_next(a, k, group, step));
-        }
-        __syncwarp();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 0) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
