@@ -26,8 +26,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "hc_attention.cuh"
 
 namespace hc {
@@ -207,15 +205,14 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
 }
-// Four floats of shared memory as two pairs; volatile, so that a loop's loads stay in it.
+// Four floats of shared memory as two pairs.
 __device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
-    asm volatile("ld.volatile.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(tc::smem_u32(p)));
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(tc::smem_u32(p)));
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -396,39 +393,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = j * kTile;
                 const bool tail = t + kTile > min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);
                 const int limit = (a.mask ? k.w.kv : min(k.w.kv, k.w.first + i + 1)) - t;
-                auto sees = [&](int c) {
-                    if (c >= limit) return false;
-                    const int back = t + c - k.w.first;
-                    return !a.mask || back < 0 || (back < 64 && ((bits >> back) & 1));
-                };
-                float fix = 1.f;
-                // a row's first maximum: of the logits of this tile that it sees
-                if (__any_sync(~0u, fresh)) {
-                    float peak = -CUDART_INF_F;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kTile; c0 += 16) {
-                        uint32_t raw[16];
-                        tmem_load16(s_mem + c0, raw);
-                        tmem_wait_load();
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float x = fmaf(__uint_as_float(raw[c]), f, col.k[c0 + c] * g);
-                            if (!tail || sees(c0 + c)) peak = fmaxf(peak, x);
-                        }
-                    }
-                    if (fresh && peak != -CUDART_INF_F) base = peak, fresh = false;
-                }
-                // Weights against the maximum so far, 32 keys at a time, two to an instruction, held
-                // as P until the tile is done; and their products with what is common to a value's
-                // dimensions.
-                uint32_t pw[2][32];
-                float peak, sum_now, flat_now;
-                auto weigh = [&](auto with_tail) {
-                    constexpr bool kTail = decltype(with_tail)::value;
-                    const uint64_t f2 = pair(f, f), g2 = pair(g, g), b2 = pair(-base, -base);
-                    uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
-                    peak = -CUDART_INF_F;
-                    uint32_t ahead[2][32];
+                float fix = 1.f, peak = -CUDART_INF_F;
+                const uint64_t f2 = pair(f, f), g2 = pair(g, g);
+                uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
+                bool quick = !tail && !__any_sync(~0u, fresh);
+                if (quick) {
+                    // Weights against the maximum so far, 32 keys at a time, two to an instruction,
+                    // held as P until all are known to be within fp16; and their products with what is
+                    // common to a value's dimensions.
+                    const uint64_t b2 = pair(-base, -base);
+                    uint32_t ahead[2][32], pw[2][32];
                     tmem_load32(s_mem, ahead[0]);
 #pragma unroll
                     for (int part = 0; part < 4; ++part) {
@@ -443,15 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load_pairs(&col.v[part * 32 + c], vo);
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
-                                const uint64_t z = fma2(pair(__uint_as_float(raw[c + 2 * n]), __uint_as_float(raw[c + 2 * n + 1])), f2,
-                                                        fma2(ko[n], g2, b2));
-                                float2 x = unpair(z);
-                                if (kTail) {
-                                    float2 v = unpair(vo[n]);        // a hidden value may be NaN
-                                    if (!sees(part * 32 + c + 2 * n)) x.x = -CUDART_INF_F, v.x = 0.f;
-                                    if (!sees(part * 32 + c + 2 * n + 1)) x.y = -CUDART_INF_F, v.y = 0.f;
-                                    vo[n] = pair(v.x, v.y);
-                                }
+                                const float2 x = unpair(fma2(pair(__uint_as_float(raw[c + 2 * n]), __uint_as_float(raw[c + 2 * n + 1])), f2,
+                                                             fma2(ko[n], g2, b2)));
                                 peak = max3(peak, x.x, x.y);
                                 e[c + 2 * n] = exp2_fast(x.x), e[c + 2 * n + 1] = exp2_fast(x.y);
                                 const uint64_t w = pair(e[c + 2 * n], e[c + 2 * n + 1]);
@@ -466,21 +433,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int n = 0; n < 4; ++n)
                                 pw[part >> 1][(part & 1) * 16 + 4 * c + n] = pack_half2(e[8 * n + c], e[8 * n + 4 + c]);
                     }
-                    const float2 s2 = unpair(sum2), l2 = unpair(flat2);
-                    sum_now = s2.x + s2.y, flat_now = l2.x + l2.y;
-                };
-                // done again only where a weight is beyond fp16 (the second time none is)
-#pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    if (tail) weigh(std::true_type());
-                    else weigh(std::false_type());
-                    if (pass || !__any_sync(~0u, peak > kMost)) break;
-                    if (peak > kMost) {
-                        const float by = exp2_fast(-peak);
-                        fix *= by, sum *= by, flat *= by, base += peak;
+                    quick = !__any_sync(~0u, peak > kMost);
+                    if (quick) {
+                        tmem_store32(s_mem, pw[0]);
+                        tmem_store32(s_mem + 32, pw[1]);
                     }
                 }
-                sum = sum_now, flat = flat_now;
+                if (!quick) {
+                    // In two passes, the maximum first: tiles with hidden keys, a row's first tile, and
+                    // tiles whose logits pass the maximum by so much that the weights overflow. Rolled:
+                    // what every tile runs has to stay in the instruction cache.
+                    uint32_t seen[4];                            // one bit a key
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int left = limit - 32 * n;
+                        seen[n] = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                    }
+                    if (a.mask) {
+                        // bit 0 of `bits` is the key at `at`; keys before it are seen
+                        const int at = k.w.first - t;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const int from = 32 * n - at;        // bit of this word's first key
+                            uint32_t m;
+                            if (from <= -32) m = ~0u;
+                            else if (from < 0) m = (static_cast<uint32_t>(bits) << -from) | ((1u << -from) - 1u);
+                            else m = from < 64 ? static_cast<uint32_t>(bits >> from) : 0u;
+                            seen[n] &= m;
+                        }
+                    }
+                    peak = -CUDART_INF_F;
+#pragma unroll 1
+                    for (int n = 0; n < 4; ++n) {
+                        uint32_t raw[32];
+                        tmem_load32(s_mem + n * 32, raw);
+                        tmem_wait_load();
+                        const uint32_t visible = n == 0 ? seen[0] : n == 1 ? seen[1] : n == 2 ? seen[2] : seen[3];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = fmaf(__uint_as_float(raw[c]), f, fmaf(col.k[n * 32 + c], g, -base));
+                            if ((visible >> c) & 1) peak = fmaxf(peak, x);
+                        }
+                    }
+                    if (fresh ? peak != -CUDART_INF_F : peak > kRaise) {
+                        fix = fresh ? 1.f : exp2_fast(-peak);
+                        base += peak, sum *= fix, flat *= fix;
+                        fresh = false;
+                    }
+                    peak = 0.f;
+                    const uint64_t b2 = pair(-base, -base);
+                    sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
+#pragma unroll 1
+                    for (int n = 0; n < 4; ++n) {
+                        uint32_t raw[32];
+                        tmem_load32(s_mem + n * 32, raw);
+                        tmem_wait_load();
+                        const uint32_t visible = n == 0 ? seen[0] : n == 1 ? seen[1] : n == 2 ? seen[2] : seen[3];
+                        float e[32];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            uint64_t ko[2], vo[2];
+                            load_pairs(&col.k[n * 32 + c], ko);
+                            load_pairs(&col.v[n * 32 + c], vo);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                const int c2 = c + 2 * m;
+                                const float2 x = unpair(fma2(pair(__uint_as_float(raw[c2]), __uint_as_float(raw[c2 + 1])), f2, fma2(ko[m], g2, b2)));
+                                float2 v = unpair(vo[m]);        // a hidden value may be NaN
+                                if ((visible >> c2) & 1) e[c2] = exp2_fast(x.x);
+                                else e[c2] = 0.f, v.x = 0.f;
+                                if ((visible >> (c2 + 1)) & 1) e[c2 + 1] = exp2_fast(x.y);
+                                else e[c2 + 1] = 0.f, v.y = 0.f;
+                                const uint64_t w = pair(e[c2], e[c2 + 1]);
+                                sum2 = add2(sum2, w);
+                                flat2 = fma2(w, pair(v.x, v.y), flat2);
+                            }
+                        }
+                        uint32_t p[16];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) p[4 * c + m] = pack_half2(e[8 * m + c], e[8 * m + 4 + c]);
+                        tmem_store16(s_mem + n * 16, p);         // over keys that have been read
+                    }
+                }
+                {
+                    const float2 s2 = unpair(sum2), l2 = unpair(flat2);
+                    sum = s2.x + s2.y, flat = l2.x + l2.y;
+                }
                 fix *= later, later = 1.f;
                 if (done_tiles == 0) {
                     ev = col.ev;
@@ -504,8 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                tmem_store32(s_mem, pw[0]);
-                tmem_store32(s_mem + 32, pw[1]);
                 tmem_wait_store();
                 tc::tc_fence_before();
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
@@ -537,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("bar.sync 1, 256;" ::: "memory");         // no product reads Q any more
                 if (wg == 1) {
                     stats[row] = make_float2(base, sum);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kD / 32; ++c) {
                         uint32_t v[32];
                         if (done_tiles > 0) tmem_load32(o_mem + c * 32, v);
@@ -572,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (writes) {
                 const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kD / 32; ++c) {
                     uint32_t v[32];
                     tmem_load32(o_mem + c * 32, v);
