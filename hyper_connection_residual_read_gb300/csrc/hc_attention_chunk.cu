@@ -217,6 +217,13 @@ __device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -247,9 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ unsigned last_one[2];
     __shared__ uint32_t step_max[2][2][4];     // [keys or values][tile parity][warp]
     __shared__ volatile int abort_flag;
+    // Each warpgroup's walk, kept here and not in registers: a spilled register of the loops
+    // below is a trip to L2, since shared memory leaves L1 no room.
+    __shared__ Walk walks[4];
+    __shared__ int walking[4];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Column* columns = reinterpret_cast<Column*>(smem + S::kColumn);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform
     const int group = a.q_heads / a.c.kv_heads;
     const int step = same ? kTile : 2 * kTile;         // rows of a piece
 
@@ -273,8 +284,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     find_run(a, group, step, &run, sums, status);      // synchronises
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    Walk k;
-    const bool any = walk_start(a, run, group, step, k);
+    Walk& k = walks[warp >> 2];
+    int& on = walking[warp >> 2];
+    const bool leads = (threadIdx.x & 127) == 0;
+    if (leads) on = walk_start(a, run, group, step, k);
+    __syncthreads();
+    // to the next piece, by all threads of a warpgroup (named barrier `bar`) that are done with this one
+    auto advance = [&](int bar) {
+        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+        if (leads) on = walk_next(a, k, group, step);
+        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+    };
 
     // Every wait is bounded (tc::mbar_wait); one that gives up raises the abort flag, after
     // which the others return at once: the roles then run to their ends on whatever is there.
@@ -293,20 +313,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(q_tile));
         const uint64_t k_desc = tc::desc_sw128(tc::smem_u32(smem + S::kK)), v_desc = tc::desc_sw128(tc::smem_u32(smem + S::kV));
         constexpr uint32_t kStageStep = S::kOne / 16, kAtom = kTile * 128 / 16, kAtomV = kD * 128 / 16;   // in the descriptors' 16 bytes
-        // The products of this row tile, issued by one thread. S of the tile that is number c of all:
+        // The products of this row tile, issued by one thread of its first warp (the warp stays
+        // together, so that descriptors are uniform). S of the tile that is number c of all:
         auto issue_s = [&](uint32_t c, bool alone) {
             const uint32_t stage = c % kStages;
             wait(bars.k_full[stage], c / kStages);
             tc::tc_fence_after();
             const uint64_t kb = k_desc + stage * kStageStep;
+            if (elected()) {
 #pragma unroll
-            for (int x = 0; x < kD / 16; ++x) {
-                const uint32_t off = (x >> 2) * kAtom + (x & 3) * 2;
-                tc::mma_f16(tmem + wg * kTile, q_desc + off, kb + off, kS, x > 0);
+                for (int x = 0; x < kD / 16; ++x) {
+                    const uint32_t off = (x >> 2) * kAtom + (x & 3) * 2;
+                    tc::mma_f16(tmem + wg * kTile, q_desc + off, kb + off, kS, x > 0);
+                }
+                tc::mma_commit(&bars.s_full[wg]);
+                tc::mma_commit(&bars.k_empty[stage]);
+                if (alone) tc::mma_commit(&bars.k_empty[stage]);
             }
-            tc::mma_commit(&bars.s_full[wg]);
-            tc::mma_commit(&bars.k_empty[stage]);
-            if (alone) tc::mma_commit(&bars.k_empty[stage]);
+            __syncwarp();
         };
         // and P V', which follows S's reader and comes before S's next writer in issue order
         auto issue_o = [&](uint32_t c, bool alone, bool more) {
@@ -314,14 +338,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(bars.v_full[stage], c / kStages);
             tc::tc_fence_after();
             const uint64_t vb = v_desc + stage * kStageStep;
+            if (elected()) {
 #pragma unroll
-            for (int n = 0; n < kTile / 16; ++n)
-                mma_ts(tmem + 2 * kTile + wg * kTile, tmem + wg * kTile + n * 8, vb + (n >> 2) * kAtomV + (n & 3) * 2, kO, n > 0 || more);
-            tc::mma_commit(&bars.o_done[wg]);
-            tc::mma_commit(&bars.v_empty[stage]);
-            if (alone) tc::mma_commit(&bars.v_empty[stage]);
+                for (int n = 0; n < kTile / 16; ++n)
+                    mma_ts(tmem + 2 * kTile + wg * kTile, tmem + wg * kTile + n * 8, vb + (n >> 2) * kAtomV + (n & 3) * 2, kO, n > 0 || more);
+                tc::mma_commit(&bars.o_done[wg]);
+                tc::mma_commit(&bars.v_empty[stage]);
+                if (alone) tc::mma_commit(&bars.v_empty[stage]);
+            }
+            __syncwarp();
         };
-        if (any) do {
+        while (on) {
             const int r = k.row0 + (same ? 0 : wg * kTile) + row;     // row of the window
             const bool active = same || wg == 0 || k.rows > kTile;    // this warpgroup has rows
             const bool here = r < k.row0 + k.rows && r < k.w.rows * group;
@@ -372,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool alone = same || k.rows <= kTile;
             if (active) {
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
-                if (row == 0 && j0 < k.t1) issue_s(column + (j0 - k.t0), alone);
+                if ((warp & 3) == 0 && j0 < k.t1) issue_s(column + (j0 - k.t0), alone);
             }
 
             float base = 0.f, sum = 0.f, flat = 0.f;
@@ -381,8 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ev = 0, done_tiles = 0;
             const float g = factor * qsum;
             const uint64_t bits = a.mask && here ? a.mask[k.w.begin + i] : 0;
-            for (int j = k.t0; j < k.t1; ++j, ++column) {
-                if (!active || (same && ((j - k.t0) & 1) != wg)) continue;
+            const int t1 = k.t1, kv = k.w.kv, first = k.w.first;
+            const int clear = min(kv, a.mask ? first : first + 1 + k.row0 / group);      // every row sees what lies before
+            for (int j = k.t0; j < t1; ++j, ++column) {
+                if (!active || (same && ((j - j0) & 1))) continue;
                 const Column& col = columns[column % kCols];
                 wait(bars.col_full[column % kCols], column / kCols);
                 wait(bars.s_full[wg], s_phase++);
@@ -391,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float f = factor * col.up[0] * col.up[1];
                 // hidden keys: behind the end, or behind this row's token, or out of its mask
                 const int t = j * kTile;
-                const bool tail = t + kTile > min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);
-                const int limit = (a.mask ? k.w.kv : min(k.w.kv, k.w.first + i + 1)) - t;
+                const bool tail = t + kTile > clear;
+                const int limit = (a.mask ? kv : min(kv, first + i + 1)) - t;
                 float fix = 1.f, peak = -CUDART_INF_F;
                 const uint64_t f2 = pair(f, f), g2 = pair(g, g);
                 uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
@@ -402,19 +431,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // held as P until all are known to be within fp16; and their products with what is
                     // common to a value's dimensions.
                     const uint64_t b2 = pair(-base, -base);
-                    uint32_t ahead[2][32], pw[2][32];
-                    tmem_load32(s_mem, ahead[0]);
+                    uint32_t pw[2][32];
+                    uint64_t ko[2], vo[2];
+                    load_pairs(&col.k[0], ko);
+                    load_pairs(&col.v[0], vo);
 #pragma unroll
                     for (int part = 0; part < 4; ++part) {
+                        uint32_t raw[32];
+                        tmem_load32(s_mem + part * 32, raw);
                         tmem_wait_load();
-                        uint32_t(&raw)[32] = ahead[part & 1];
-                        if (part < 3) tmem_load32(s_mem + (part + 1) * 32, ahead[(part + 1) & 1]);
                         float e[32];
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            uint64_t ko[2], vo[2];
-                            load_pairs(&col.k[part * 32 + c], ko);
-                            load_pairs(&col.v[part * 32 + c], vo);
+                            uint64_t kn[2] = {}, vn[2] = {};         // the next four keys'
+                            if (part * 32 + c + 4 < kTile) {
+                                load_pairs(&col.k[part * 32 + c + 4], kn);
+                                load_pairs(&col.v[part * 32 + c + 4], vn);
+                            }
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
                                 const float2 x = unpair(fma2(pair(__uint_as_float(raw[c + 2 * n]), __uint_as_float(raw[c + 2 * n + 1])), f2,
@@ -425,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 sum2 = add2(sum2, w);
                                 flat2 = fma2(w, vo[n], flat2);
                             }
+                            ko[0] = kn[0], ko[1] = kn[1], vo[0] = vn[0], vo[1] = vn[1];
                         }
                         // P: column c * 8 + n of each 32 is token n * 4 + c, the order of the decoded values
 #pragma unroll
@@ -451,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (a.mask) {
                         // bit 0 of `bits` is the key at `at`; keys before it are seen
-                        const int at = k.w.first - t;
+                        const int at = first - t;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
                             const int from = 32 * n - at;        // bit of this word's first key
@@ -547,9 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_store();
                 tc::tc_fence_before();
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
-                if (row == 0) {
+                if ((warp & 3) == 0) {
                     issue_o(column, alone, done_tiles > 0);
-                    if (j + stride < k.t1) issue_s(column + stride, alone);
+                    if (j + stride < t1) issue_s(column + stride, alone);
                 }
                 ++done_tiles;
                 // a maximum that was passed is raised for the tiles to come
@@ -682,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (here && a.lse) a.lse[at] = all == 0.f ? -CUDART_INF_F : (top + log2f(all)) * kLn2;
                 }
             }
-        } while (walk_next(a, k, group, step));
+            advance(2 + wg);
+        }
     } else {
         // ------------------------------------------------------------------ keys, values
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -700,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto key_token = [&](int u) { return u * (128 / kUnits) + w * (32 / kUnits) + (lane >> 3) / kSegs * 8 + (lane & 7); };
         const int vc = lane & 7, vt = (vc >> 2) * 32 + (vc & 3), vh = w >> 1, vd = ((w & 1) * 4 + (lane >> 3)) * (8 * kVW);
         uint32_t column = 0;
-        if (any) do {
+        while (on) {
             // Lanes 0-7 hold the blocks of a tile's eight 16-token parts, looked up a tile ahead.
             int ids = 0;
             const int64_t first = (static_cast<int64_t>(k.h) + (is_v ? a.c.kv_heads : 0)) * a.c.block_size;   // group in a block
@@ -839,7 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (more) load_codes(j + 1);
                 look_up(j + 2);
             }
-        } while (walk_next(a, k, group, step));
+            advance(4 + is_v);
+        }
     }
     __syncthreads();
     if (warp == 0) {
