@@ -214,6 +214,12 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
 __device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(tc::smem_u32(p)));
 }
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ------------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int wg = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_mem = tmem + lanes + wg * kTile, o_mem = tmem + lanes + 2 * kTile + wg * kTile;
@@ -349,13 +355,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         };
         while (on) {
-            const int r = k.row0 + (same ? 0 : wg * kTile) + row;     // row of the window
             const bool active = same || wg == 0 || k.rows > kTile;    // this warpgroup has rows
-            const bool here = r < k.row0 + k.rows && r < k.w.rows * group;
-            const int i = r / group, hq = k.h * group + r % group;
+            // This thread's row, worked out anew for each use: what it would cost to keep is
+            // registers of the loop over the tiles.
+            struct Row {
+                bool here;
+                int i, hq;                             // token of the window, query head
+            };
+            auto my_row = [&]() {
+                int x = row;
+                asm volatile("" : "+r"(x));            // not the values of an earlier use
+                const int r = k.row0 + (same ? 0 : wg * kTile) + x;
+                return Row{r < k.row0 + k.rows, r / group, k.h * group + r % group};
+            };
             float factor = 0.f, qsum = 0.f;
             if (active) {
                 // ---- this row of Q: scaled to fp16, in the order of the decoded keys
+                const Row m = my_row();
+                const bool here = m.here;
+                const int i = m.i, hq = m.hq;
                 const int64_t from = static_cast<int64_t>(k.w.begin + i) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
                 const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from);
                 float top = 0.f;
@@ -407,9 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float later = 1.f;                         // what O is to be multiplied by before its next product
             int ev = 0, done_tiles = 0;
             const float g = factor * qsum;
-            const uint64_t bits = a.mask && here ? a.mask[k.w.begin + i] : 0;
-            const int t1 = k.t1, kv = k.w.kv, first = k.w.first;
-            const int clear = min(kv, a.mask ? first : first + 1 + k.row0 / group);      // every row sees what lies before
+            const int t1 = k.t1;
+            const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);   // every row sees what lies before
             for (int j = k.t0; j < t1; ++j, ++column) {
                 if (!active || (same && ((j - j0) & 1))) continue;
                 const Column& col = columns[column % kCols];
@@ -421,7 +438,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // hidden keys: behind the end, or behind this row's token, or out of its mask
                 const int t = j * kTile;
                 const bool tail = t + kTile > clear;
-                const int limit = (a.mask ? kv : min(kv, first + i + 1)) - t;
                 float fix = 1.f, peak = -CUDART_INF_F;
                 const uint64_t f2 = pair(f, f), g2 = pair(g, g);
                 uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
@@ -431,52 +447,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // held as P until all are known to be within fp16; and their products with what is
                     // common to a value's dimensions.
                     const uint64_t b2 = pair(-base, -base);
-                    uint32_t pw[2][32];
+                    uint32_t pw[4][16], ahead[2][16];
                     uint64_t ko[2], vo[2];
                     load_pairs(&col.k[0], ko);
                     load_pairs(&col.v[0], vo);
+                    tmem_load16(s_mem, ahead[0]);
 #pragma unroll
-                    for (int part = 0; part < 4; ++part) {
-                        uint32_t raw[32];
-                        tmem_load32(s_mem + part * 32, raw);
+                    for (int part = 0; part < 8; ++part) {
                         tmem_wait_load();
-                        float e[32];
+                        uint32_t(&raw)[16] = ahead[part & 1];
+                        if (part < 7) tmem_load16(s_mem + (part + 1) * 16, ahead[(part + 1) & 1]);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            uint64_t kn[2] = {}, vn[2] = {};         // the next four keys'
-                            if (part * 32 + c + 4 < kTile) {
-                                load_pairs(&col.k[part * 32 + c + 4], kn);
-                                load_pairs(&col.v[part * 32 + c + 4], vn);
-                            }
+                        for (int c = 0; c < 16; c += 8) {
+                            float e[8];
 #pragma unroll
-                            for (int n = 0; n < 2; ++n) {
-                                const float2 x = unpair(fma2(pair(__uint_as_float(raw[c + 2 * n]), __uint_as_float(raw[c + 2 * n + 1])), f2,
-                                                             fma2(ko[n], g2, b2)));
-                                peak = max3(peak, x.x, x.y);
-                                e[c + 2 * n] = exp2_fast(x.x), e[c + 2 * n + 1] = exp2_fast(x.y);
-                                const uint64_t w = pair(e[c + 2 * n], e[c + 2 * n + 1]);
-                                sum2 = add2(sum2, w);
-                                flat2 = fma2(w, vo[n], flat2);
+                            for (int c4 = 0; c4 < 8; c4 += 4) {
+                                uint64_t kn[2] = {}, vn[2] = {};     // the next four keys'
+                                if (part * 16 + c + c4 + 4 < kTile) {
+                                    load_pairs(&col.k[part * 16 + c + c4 + 4], kn);
+                                    load_pairs(&col.v[part * 16 + c + c4 + 4], vn);
+                                }
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    const int at = c4 + 2 * n;
+                                    const float2 x = unpair(fma2(pair(__uint_as_float(raw[c + at]), __uint_as_float(raw[c + at + 1])), f2,
+                                                                 fma2(ko[n], g2, b2)));
+                                    peak = max3(peak, x.x, x.y);
+                                    e[at] = exp2_fast(x.x), e[at + 1] = exp2_fast(x.y);
+                                    const uint64_t w = pair(e[at], e[at + 1]);
+                                    sum2 = add2(sum2, w);
+                                    flat2 = fma2(w, vo[n], flat2);
+                                }
+                                ko[0] = kn[0], ko[1] = kn[1], vo[0] = vn[0], vo[1] = vn[1];
                             }
-                            ko[0] = kn[0], ko[1] = kn[1], vo[0] = vn[0], vo[1] = vn[1];
+                            // P: column x * 8 + n of each 32 is token n * 4 + x, the order of the decoded values
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                pw[part >> 1][4 * x + 2 * (part & 1) + c / 8] = pack_half2(e[x], e[4 + x]);
                         }
-                        // P: column c * 8 + n of each 32 is token n * 4 + c, the order of the decoded values
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int n = 0; n < 4; ++n)
-                                pw[part >> 1][(part & 1) * 16 + 4 * c + n] = pack_half2(e[8 * n + c], e[8 * n + 4 + c]);
                     }
                     quick = !__any_sync(~0u, peak > kMost);
                     if (quick) {
-                        tmem_store32(s_mem, pw[0]);
-                        tmem_store32(s_mem + 32, pw[1]);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) tmem_store16(s_mem + n * 16, pw[n]);
                     }
                 }
                 if (!quick) {
                     // In two passes, the maximum first: tiles with hidden keys, a row's first tile, and
                     // tiles whose logits pass the maximum by so much that the weights overflow. Rolled:
                     // what every tile runs has to stay in the instruction cache.
+                    const Row m = my_row();
+                    const int limit = (a.mask ? k.w.kv : min(k.w.kv, k.w.first + m.i + 1)) - t;
                     uint32_t seen[4];                            // one bit a key
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
@@ -485,15 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (a.mask) {
                         // bit 0 of `bits` is the key at `at`; keys before it are seen
-                        const int at = first - t;
+                        const uint64_t bits = m.here ? a.mask[k.w.begin + m.i] : 0;
+                        const int at = k.w.first - t;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
                             const int from = 32 * n - at;        // bit of this word's first key
-                            uint32_t m;
-                            if (from <= -32) m = ~0u;
-                            else if (from < 0) m = (static_cast<uint32_t>(bits) << -from) | ((1u << -from) - 1u);
-                            else m = from < 64 ? static_cast<uint32_t>(bits >> from) : 0u;
-                            seen[n] &= m;
+                            uint32_t word;
+                            if (from <= -32) word = ~0u;
+                            else if (from < 0) word = (static_cast<uint32_t>(bits) << -from) | ((1u << -from) - 1u);
+                            else word = from < 64 ? static_cast<uint32_t>(bits >> from) : 0u;
+                            seen[n] &= word;
                         }
                     }
                     peak = -CUDART_INF_F;
@@ -632,7 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 other = other_base == -CUDART_INF_F ? 0.f : exp2_fast(other_base - peak);
                 total = sum * mine + other_sum * other;
             }
-            const int64_t at = static_cast<int64_t>(k.w.begin + i) * a.q_heads + hq;
+            const Row mine_row = my_row();
+            const bool here = mine_row.here;
+            const int64_t at = static_cast<int64_t>(k.w.begin + mine_row.i) * a.q_heads + mine_row.hq;
             float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (k.t0 == 0 ? 1 : 0)) * kPieceFloats;
             const int prow = (same ? 0 : wg * kTile) + row;
             auto write = [&](int c, const float (&v)[32], float inv) {
@@ -720,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------------ keys, values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         const bool is_v = warp >= 12;
         const int p = threadIdx.x & 127, w = warp & 3;
         const int sh = 31 - __clz(a.c.block_size), in_block = a.c.block_size - 1;
