@@ -8,8 +8,8 @@
 //
 // * The decoded values are exact. A step has 8 significant bits (bf16) and |code - 8| <= 8
 //   at most 3, so s (code - 8) has 11 at most, which is what fp16 holds: K' = 2^-E s_j
-//   (c_j - 8), with E from the largest step of the tile, is exact for steps down to 2^-9 of
-//   that one and within 2^-20 of the largest value below. One logical and one fp16
+//   (c_j - 8), with E from the largest step of the tile (of V', of the tiles so far), is exact
+//   for steps down to 2^-9 of that one and within 2^-20 of the largest value below. One logical and one fp16
 //   operation decode two codes: a code's bits alone are the subnormal code * 2^-24, and fma
 //   with S = 2^24 2^-E s gives S code 2^-24 - S 8 2^-24.
 // * What is left of a key, m_j + 8 s_j, is the same for all its dimensions: it meets
@@ -57,8 +57,8 @@ struct Smem {
     static constexpr int kK = 2 * kOne;
     static constexpr int kV = kK + kStages * kOne;
     static constexpr int kColumn = kV + kStages * kOne;
-    static constexpr int kSteps = kColumn + kCols * static_cast<int>(sizeof(Column));   // fp16 S of keys, values
-    static constexpr int kBytes = kSteps + 2 * kTile * 2 + 1024;       // and room to align
+    static constexpr int kSteps = kColumn + kCols * static_cast<int>(sizeof(Column));   // fp16 S [values?][tile parity]
+    static constexpr int kBytes = kSteps + 4 * kTile * 2 + 1024;       // and room to align
 };
 
 struct Bars {
@@ -750,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sh = 31 - __clz(a.c.block_size), in_block = a.c.block_size - 1;
         const int64_t to_values = static_cast<int64_t>(a.c.kv_heads) * a.c.block_size;
         const uint32_t block_bytes = static_cast<uint32_t>(2 * to_values * (kD / 2));
-        __half* steps = reinterpret_cast<__half*>(smem + S::kSteps) + (is_v ? kTile : 0);
         const __half2 sixteenth = __float2half2_rn(0.0625f), eighth = __float2half2_rn(-4.76837158203125e-7f);   // -8 2^-24
         // Keys: piece u of a thread is 16 bytes, `seg`, of token key_token(u). Values: tokens n * 4
         // + vt (n = 0..7) of the 64-token half vh, kVW words from dimension vd on.
@@ -769,28 +768,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = j * kTile + lane * 16;
                 if (lane < 8 && j < k.t1 && t < k.w.kv) ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
             };
-            auto check = [&]() {
+            uint64_t parts = 0, parts_next = 0;                 // bytes from `codes` to those of lane's part
+            auto check = [&](int j) -> uint64_t {
                 if (static_cast<unsigned>(ids) >= static_cast<unsigned>(a.c.blocks)) {
                     atomicOr(status, kStatusBounds);
                     ids = 0;                                    // wrong values, from the cache's own memory
                 }
+                return static_cast<uint64_t>(static_cast<uint32_t>(ids)) * block_bytes +
+                       static_cast<uint32_t>(((j * kTile + lane * 16) & in_block) * (kD / 2));
             };
-            // bytes from `codes` to those of token `x` of tile j
-            auto place = [&](int j, int x) -> uint64_t {
-                const uint32_t id = __shfl_sync(~0u, ids, x >> 4);
-                return static_cast<uint64_t>(id) * block_bytes + static_cast<uint32_t>(((j * kTile + x) & in_block) * (kD / 2));
+            // bytes from `codes` to those of token `x` of that tile
+            auto place = [&](uint64_t parts, int x) -> uint64_t {
+                return __shfl_sync(~0u, parts, x >> 4) + static_cast<uint32_t>((x & 15) * (kD / 2));
             };
-            uint32_t raw[16], scale = 0;                        // keys [kUnits][4], or values [8][kVW]
-            auto load_scales = [&](int j) {
-                const uint64_t at = place(j, p);
-                scale = 0;
-                if (j * kTile + p < k.w.kv) scale = scales[at / (kD / 2)];
+            uint32_t raw[16];                                   // keys [kUnits][4], or values [8][kVW]
+            uint32_t scale = 0, scale_next = 0;                 // of token p of this tile and the next
+            auto load_scale = [&](int j, uint64_t parts) -> uint32_t {
+                const uint64_t at = place(parts, p);
+                return j < k.t1 && j * kTile + p < k.w.kv ? scales[at / (kD / 2)] : 0;
             };
             auto load_codes = [&](int j) {
                 if (!is_v) {
 #pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
-                        const uint64_t at = place(j, key_token(u));
+                        const uint64_t at = place(parts, key_token(u));
                         uint4 y = make_uint4(0, 0, 0, 0);
                         if (j * kTile + key_token(u) < k.w.kv) y = *reinterpret_cast<const uint4*>(codes + at);
                         raw[4 * u] = y.x, raw[4 * u + 1] = y.y, raw[4 * u + 2] = y.z, raw[4 * u + 3] = y.w;
@@ -799,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
                         const int x = vh * 64 + n * 4 + vt;
-                        const uint64_t at = place(j, x);
+                        const uint64_t at = place(parts, x);
                         uint2 y = make_uint2(0, 0);
                         if (j * kTile + x < k.w.kv) {
                             if (kVW == 2) y = *reinterpret_cast<const uint2*>(codes + at);
@@ -810,45 +811,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
+            // the largest step of a tile, exchanged between the warps a tile ahead
+            auto tell = [&](uint32_t scale, uint32_t parity) {
+                const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(fmaxf(bf16_lo(scale), 0.f)));   // of a NaN, 0
+                if (lane == 0) step_max[is_v][parity][w] = m;
+            };
             look_up(k.t0);
-            check();
-            load_scales(k.t0);
+            parts = check(k.t0);
+            scale = load_scale(k.t0, parts);
             load_codes(k.t0);
             look_up(k.t0 + 1);
-            int ev = 0;
-            bool have_ev = false;
+            parts = check(k.t0 + 1);
+            scale_next = load_scale(k.t0 + 1, parts);
+            look_up(k.t0 + 2);
+            tell(scale, column & 1);
+            asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
+            int e = 0;
+            bool have_e = false;
             for (int j = k.t0; j < k.t1; ++j, ++column) {
                 const int stage = column % kStages, turn = column / kStages;
-                // steps and minima: a group held as NaN keeps the NaN in its common part alone
-                float s_own = bf16_lo(scale);
-                const float common = fmaf(8.f, s_own, bf16_hi(scale));
-                if (!(s_own <= 3.0e38f)) s_own = 0.f;
-                const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(s_own));
-                uint32_t* tops = step_max[is_v][column & 1];
-                if (lane == 0) tops[w] = most;
-                asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
+                // E: the largest step of K' in [2^-9, 2^-8); of V', that of the piece so far
+                const uint32_t* tops = step_max[is_v][column & 1];
                 const uint32_t top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-                // K': the largest step in [2^-9, 2^-8). V': that of the piece's first tile in [2^-12,
-                // 2^-11), and later ones below 2^-8, else the exponent follows.
-                const int e9 = top ? static_cast<int>(top >> 23) - 127 + 9 : 0;
-                if (is_v && top && (!have_ev || e9 > ev)) ev = e9 + 3, have_ev = true;
-                const int e = is_v ? ev : e9;
+                const int e9 = static_cast<int>(top >> 23) - 127 + 9;
+                if (top && (!is_v || !have_e || e9 > e)) e = e9, have_e = true;
                 // the softmax of the tile four before has been through with its column: see Column
                 if (turn > 0) wait(is_v ? bars.v_empty[stage] : bars.k_empty[stage], turn - 1);
                 Column& col = columns[column % kCols];
-                (is_v ? col.v : col.k)[p] = common;
+                // two of them: other threads may still be decoding the tile before
+                __half* steps = reinterpret_cast<__half*>(smem + S::kSteps) + (is_v * 2 + (column & 1)) * kTile;
+                // 2^24 2^-E s, for E of any step
+                const float up0 = power_of_two((24 - e) / 2), up1 = power_of_two(24 - e - (24 - e) / 2);
+                // a group held as NaN keeps the NaN in its common part alone
+                const float own = bf16_lo(scale);
+                (is_v ? col.v : col.k)[p] = fmaf(8.f, own, bf16_hi(scale));
+                steps[p] = __float2half_rn(own <= 3.0e38f ? own * up0 * up1 : 0.f);
                 if (p == 0) {
-                    if (is_v) col.ev = ev;
-                    else col.up[0] = power_of_two(e9 / 2), col.up[1] = power_of_two(e9 - e9 / 2);
+                    if (is_v) col.ev = e;
+                    else col.up[0] = power_of_two(e / 2), col.up[1] = power_of_two(e - e / 2);
                 }
                 tc::mbar_arrive(&bars.col_full[column % kCols]);
-                // 2^24 2^-E s, for E of any step
-                steps[p] = __float2half_rn(s_own * power_of_two((24 - e) / 2) * power_of_two(24 - e - (24 - e) / 2));
+                tell(scale_next, (column + 1) & 1);
                 asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
                 const bool more = j + 1 < k.t1;
                 if (more) {
-                    check();
-                    load_scales(j + 1);
+                    parts_next = check(j + 2);
+                    scale = scale_next;
+                    scale_next = load_scale(j + 2, parts_next);
                 }
                 if (!is_v) {
                     unsigned char* to = smem + S::kK + stage * S::kOne;
@@ -896,7 +905,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::mbar_arrive(&bars.v_full[stage]);
                 }
                 if (more) load_codes(j + 1);
-                look_up(j + 2);
+                parts = parts_next;
+                look_up(j + 3);
             }
             advance(4 + is_v);
         }
