@@ -52,6 +52,8 @@ void free_ctx(Ctx& c) {
     cudaFree(c.gated);
     cudaFree(c.attn_pieces);
     cudaFree(c.attn_arrivals);
+    cudaFree(c.score_parts);
+    cudaFree(c.score_arrivals);
     c = Ctx();
 }
 
@@ -301,12 +303,16 @@ extern "C" int hc_read_init(int device, int max_tokens, float eps) {
     const size_t arrivals = sizeof(unsigned) * kAttnCtasPerSm * c.sm_count;
     ok &= cudaMalloc(&c.attn_pieces, sizeof(float) * attention_scratch_floats(c.sm_count)) == cudaSuccess;
     ok &= cudaMalloc(&c.attn_arrivals, arrivals) == cudaSuccess;
+    const size_t rows = sizeof(unsigned) * kScoreRowsPerSm * c.sm_count;
+    ok &= cudaMalloc(&c.score_parts, score_scratch_bytes(c.sm_count)) == cudaSuccess;
+    ok &= cudaMalloc(&c.score_arrivals, rows) == cudaSuccess;
     if (!ok) {
         cudaGetLastError();
         free_ctx(c);
         return HC_ERR_NOMEM;
     }
     if (cudaMemset(c.attn_arrivals, 0, arrivals) != cudaSuccess ||
+        cudaMemset(c.score_arrivals, 0, rows) != cudaSuccess ||
         cudaMemset(c.s.status, 0, sizeof(int)) != cudaSuccess ||
         cudaMemset(c.s.sync, 0, kSyncWords * sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(c.s.sched, 0, 2 * kSchedPairs * sizeof(int)) != cudaSuccess ||

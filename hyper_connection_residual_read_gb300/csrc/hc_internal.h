@@ -96,6 +96,10 @@ struct Ctx {
     // launches)
     float* attn_pieces = nullptr;
     unsigned* attn_arrivals = nullptr;
+    // log probabilities: results of the segments of split rows, and per row the number of
+    // them that are there (0 between launches)
+    unsigned char* score_parts = nullptr;
+    unsigned* score_arrivals = nullptr;
 };
 
 // The current device's context, or nullptr with *err set; and whether p is 16-byte
@@ -106,6 +110,9 @@ int check_ptr(const void* p, int device);
 // Floats of Ctx::attn_pieces (hc_attention.cu); CTAs that may share requests.
 size_t attention_scratch_floats(int sm_count);
 constexpr int kAttnCtasPerSm = 2;
+// Bytes of Ctx::score_parts (hc_score.cu); rows that may be split.
+size_t score_scratch_bytes(int sm_count);
+constexpr int kScoreRowsPerSm = 2;
 
 // 128-token tiles of the partials.
 inline int partial_tiles(int max_tokens) { return (max_tokens + 127) / 128; }

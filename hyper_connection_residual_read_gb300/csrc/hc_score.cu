@@ -1,40 +1,77 @@
 // Log probabilities of given tokens, with the entropy, the rank and the most likely
-// alternatives.
+// alternatives: one pass over the logits, whose bytes bound it.
+//
+// A CTA takes a row, or a segment of one where there are few rows. Each thread runs over its
+// vectors of 16 bytes with sums about a reference of its own, sum e^(x - r) and sum (x - r)
+// e^(x - r), and keeps its largest logit and where that was. fp32 has the room to leave
+// the reference behind: it moves only when a logit passes it by 40 binary orders. Sums
+// of different references join as s e^(r - R) and e^(r - R) (b + s (r - R)).
+//
+// The alternatives cost the pass nothing: with the threads' largest logits known, the k-th
+// largest of those is a bound that at least k logits reach, and only the k threads that
+// reach it have to look at their logits again (a warp reads such a thread's vectors
+// in one gather). Logits and their indexes are compared as one number, so that equal
+// logits count in the order of their indexes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
 
-#include "hc_common.cuh"
-#include "hc_window_internal.h"
+#include "hc_attention.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;                    // vectors of a thread on their way
+constexpr int kList = 2048;                  // candidates that fit; more take the slow way
+constexpr float kPass = 27.7f;               // 40 ln 2: by how much a logit may pass the reference
+constexpr int kMaxSplits = 64;
+
+// ---- logits
 
 template <int kDtype>
-__device__ __forceinline__ float logit(const void* p, int64_t i) {
-    if (kDtype == HC_DTYPE_FP32) return static_cast<const float*>(p)[i];
-    if (kDtype == HC_DTYPE_BF16) return bf16_lo(static_cast<const uint16_t*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
-}
+struct Logits;
+template <>
+struct Logits<HC_DTYPE_FP32> {
+    static constexpr int kN = 4;             // of a vector
+    static __device__ __forceinline__ float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    static __device__ __forceinline__ float at(const uint4& v, int i) {
+        return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+    }
+};
+template <>
+struct Logits<HC_DTYPE_BF16> {
+    static constexpr int kN = 8;
+    static constexpr float kLow = -1e30f;    // below it, differences may be infinite
+    static __device__ __forceinline__ float one(const void* p, int64_t i) { return bf16_lo(static_cast<const uint16_t*>(p)[i]); }
+    static __device__ __forceinline__ float at(const uint4& v, int i) {
+        const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+        return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+    }
+    using Two = __nv_bfloat162;
+    static __device__ __forceinline__ Two two(float x) { return __float2bfloat162_rn(x); }
+    static __device__ __forceinline__ float2 widen(Two x) { return make_float2(__low2float(x), __high2float(x)); }
+};
+template <>
+struct Logits<HC_DTYPE_FP16> {
+    static constexpr int kN = 8;
+    static constexpr float kLow = -65504.f;
+    static __device__ __forceinline__ float one(const void* p, int64_t i) { return __half2float(static_cast<const __half*>(p)[i]); }
+    static __device__ __forceinline__ float at(const uint4& v, int i) {
+        const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+        const __half2 h = *reinterpret_cast<const __half2*>(&w);
+        return (i & 1) ? __high2float(h) : __low2float(h);
+    }
+    using Two = __half2;
+    static __device__ __forceinline__ Two two(float x) { return __float2half2_rn(x); }
+    static __device__ __forceinline__ float2 widen(Two x) { return __half22float2(x); }
+};
 
-template <typename T, typename F>
-__device__ T block_reduce(T v, T* s, F f) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = f(v, __shfl_xor_sync(~0u, v, d));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = s[0];
-    for (int w = 1; w < kThreads / 32; ++w) v = f(v, s[w]);
-    return v;
-}
-
-// Value, then index, in one whole number that grows with the value and falls with the
-// index (0 is below every entry).
+// Value, then index, in one whole number that grows with the value and falls with the index
+// (0 is below every entry; -0 and 0 are one value).
 __device__ __forceinline__ uint64_t order_key(float x, int i) {
     uint32_t u = __float_as_uint(x + 0.0f);
     u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -44,64 +81,364 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     const uint32_t u = static_cast<uint32_t>(k >> 32);
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
 }
+__device__ __forceinline__ int key_index(uint64_t k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
+
+// ---- sums about a reference
+
+struct Sums {
+    float ref, s, b;
+    __host__ __device__ Sums() : ref(-__builtin_huge_valf()), s(0.f), b(0.f) {}
+    // to a reference that is at least as large; 0 e^(-inf) is 0
+    __device__ __forceinline__ void move(float to) {
+        if (ref == to || s == 0.f) {
+            ref = to;
+            return;
+        }
+        const float d = ref - to, f = exp2_fast(d * kLog2e);
+        b = f == 0.f ? 0.f : f * fmaf(s, d, b);
+        s = f * s;
+        ref = to;
+    }
+    __device__ __forceinline__ void add(float x) {               // any logit
+        const float d = x - ref;
+        const float e = exp2_fast(d * kLog2e);
+        s += e;
+        if (e != 0.f) b = fmaf(e, d, b);
+    }
+    __device__ __forceinline__ bool passed(float x) const { return x > ref + kPass; }   // always, at first
+};
+
+// ---- the largest 32 of a list of keys
+
+__device__ __forceinline__ uint64_t max64(uint64_t x, uint64_t y) { return x > y ? x : y; }
+__device__ __forceinline__ uint64_t min64(uint64_t x, uint64_t y) { return x < y ? x : y; }
+
+// A warp's 32 keys (one a lane), a bitonic sequence, in falling order; and any 32 keys.
+__device__ __forceinline__ uint64_t bitonic_merge(uint64_t k, int lane) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const uint64_t o = __shfl_xor_sync(~0u, k, d);
+        k = (lane & d) ? min64(k, o) : max64(k, o);
+    }
+    return k;
+}
+__device__ __forceinline__ uint64_t bitonic_sort(uint64_t k, int lane) {
+#pragma unroll
+    for (int n = 2; n < 32; n <<= 1)
+#pragma unroll
+        for (int d = n >> 1; d > 0; d >>= 1) {
+            const uint64_t o = __shfl_xor_sync(~0u, k, d);
+            k = (((lane & d) != 0) != ((lane & n) != 0)) ? min64(k, o) : max64(k, o);
+        }
+    return bitonic_merge(k, lane);
+}
+
+// The largest 32 of list[0..n) in falling order, in every warp, a key a lane (0: none). Every
+// thread calls it; `list` and `buffer` [kWarps * 32] are shared memory.
+__device__ uint64_t top32(const uint64_t* list, int n, uint64_t* buffer) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t best = 0;
+    for (int c = warp * 32; c < n; c += kThreads) {
+        const uint64_t k = bitonic_sort(c + lane < n ? list[c + lane] : 0, lane);
+        // the larger of each and its mirror image are the largest 32 of both, in bitonic order
+        best = c == warp * 32 ? k : bitonic_merge(max64(best, __shfl_sync(~0u, k, 31 - lane)), lane);
+    }
+    buffer[threadIdx.x] = best;
+    __syncthreads();
+    const int lists = min(kWarps, (n + 31) / 32);
+#pragma unroll 1
+    for (int stride = 1; stride < lists; stride <<= 1) {
+        if ((warp & (2 * stride - 1)) == 0 && warp + stride < lists) {
+            best = bitonic_merge(max64(best, buffer[(warp + stride) * 32 + 31 - lane]), lane);
+            buffer[threadIdx.x] = best;
+        }
+        __syncthreads();
+    }
+    best = buffer[lane];
+    __syncthreads();
+    return best;
+}
+
+template <typename F>
+__device__ __forceinline__ float reduce_float(float v, float* s, F f) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = f(v, __shfl_xor_sync(~0u, v, d));
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = s[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v = f(v, s[w]);
+    __syncthreads();
+    return v;
+}
+
+// A segment's result in scratch.
+struct Part {
+    float ref, s, b;
+    int above;
+    uint64_t keys[32];
+};
 
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs a) {
-    __shared__ float sf[kThreads / 32];
-    __shared__ int si[kThreads / 32];
-    __shared__ uint64_t sk[kThreads / 32];
-    const int64_t base = blockIdx.x * a.row;
-    const int id = a.ids[blockIdx.x];
+__global__ void __launch_bounds__(kThreads, 5)
+    score_kernel(const LogprobArgs a, int splits, unsigned char* scratch, unsigned* arrivals) {
+    using L = Logits<kDtype>;
+    constexpr int kN = L::kN;
+    __shared__ uint64_t list[kList];
+    __shared__ uint64_t buffer[kThreads];
+    __shared__ float sf[kWarps];
+    __shared__ int count, last_one, si[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / splits, split = blockIdx.x % splits;
+    constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2;
+    const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.row * kItem;
+    // the row: single logits up to 16-byte alignment, vectors, single logits
+    const int head = min(a.vocab, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / kItem);
+    const int vectors = (a.vocab - head) / kN, tail = a.vocab - head - vectors * kN;
+    const uint4* vec = reinterpret_cast<const uint4*>(x + head * kItem);
+    const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * split / splits);
+    const int v1 = static_cast<int>(static_cast<int64_t>(vectors) * (split + 1) / splits);
+    const int id = a.ids[row];
     const bool known = id >= 0 && id < a.vocab;
-    const float mine = known ? logit<kDtype>(a.logits, base + id) : -CUDART_INF_F;
-    float top = -CUDART_INF_F;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) top = fmaxf(top, logit<kDtype>(a.logits, base + i));
-    top = block_reduce(top, sf, [](float x, float y) { return fmaxf(x, y); });
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
-    float sum = 0.f, below = 0.f;
+    const float mine = known ? L::one(x, id) : CUDART_INF_F;
+
+    // ---- the pass
+    Sums sums;
+    float best = -CUDART_INF_F;
+    int best_v = -1;                             // the vector with this thread's largest logit
     int above = 0;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-        const float x = logit<kDtype>(a.logits, base + i), e = expf(x - ref);
-        sum += e;
-        if (e != 0.f) below += e * (x - ref);
-        above += x > mine;
-    }
-    sum = block_reduce(sum, sf, [](float x, float y) { return x + y; });
-    below = block_reduce(below, sf, [](float x, float y) { return x + y; });
-    above = block_reduce(above, si, [](int x, int y) { return x + y; });
-    const float lse = ref + logf(sum);
-    const bool empty = top == -CUDART_INF_F && sum == 0.f;
-    auto lp = [&](float x) { return x == -CUDART_INF_F && !(lse != lse) ? x : x - lse; };
-    if (threadIdx.x == 0) {
-        a.lse[blockIdx.x] = empty ? -CUDART_INF_F : lse;
-        a.logprob[blockIdx.x] = lp(mine);
-        a.entropy[blockIdx.x] = empty ? 0.f : logf(sum) - below / sum;
-        a.rank[blockIdx.x] = known ? above : a.vocab;
-    }
-    uint64_t last = ~0ull;
-    for (int k = 0; k < a.top; ++k) {
-        uint64_t best = 0;
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-            const uint64_t key = order_key(logit<kDtype>(a.logits, base + i), i);
-            if (key < last && key > best) best = key;
+    auto vector = [&](const uint4& v, int at) {
+        if constexpr (kDtype == HC_DTYPE_FP32) {
+            const float y[4] = {L::at(v, 0), L::at(v, 1), L::at(v, 2), L::at(v, 3)};
+            const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            if (best_v < 0 || top > best) best = top, best_v = at;
+            if (sums.passed(top)) sums.move(top);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (sums.ref != -CUDART_INF_F || y[i] != y[i]) sums.add(y[i]);
+                above += y[i] > mine;
+            }
+        } else {
+            using Two = typename L::Two;
+            const Two w[4] = {*reinterpret_cast<const Two*>(&v.x), *reinterpret_cast<const Two*>(&v.y),
+                              *reinterpret_cast<const Two*>(&v.z), *reinterpret_cast<const Two*>(&v.w)};
+            const float2 hi = L::widen(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+            const float2 lo = L::widen(__hmin2(__hmin2(w[0], w[1]), __hmin2(w[2], w[3])));
+            const float top = fmaxf(hi.x, hi.y);
+            if (best_v < 0 || top > best) best = top, best_v = at;
+            if (sums.passed(top)) sums.move(top);
+            const Two m = L::two(mine);
+            const float2 more = L::widen(__hadd2(__hadd2(__hgt2(w[0], m), __hgt2(w[1], m)), __hadd2(__hgt2(w[2], m), __hgt2(w[3], m))));
+            above += static_cast<int>(more.x + more.y);
+            if (fminf(lo.x, lo.y) < L::kLow || sums.ref == -CUDART_INF_F) {
+                // infinities, or so far down that their differences may be
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = L::at(v, i);
+                    if (sums.ref != -CUDART_INF_F || y != y) sums.add(y);
+                }
+            } else {
+                const uint64_t r2 = pair(-sums.ref, -sums.ref), l2 = pair(kLog2e, kLog2e);
+                uint64_t s2 = pair(sums.s, 0.f), b2 = pair(sums.b, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = L::widen(w[i]);
+                    const uint64_t d = add2(pair(y.x, y.y), r2);
+                    const float2 z = unpair(mul2(d, l2));
+                    const uint64_t e = pair(exp2_fast(z.x), exp2_fast(z.y));
+                    s2 = add2(s2, e);
+                    b2 = fma2(e, d, b2);
+                }
+                const float2 s = unpair(s2), b = unpair(b2);
+                sums.s = s.x + s.y, sums.b = b.x + b.y;
+            }
         }
-        best = block_reduce(best, sk, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
-        if (threadIdx.x == 0) {
-            a.top_ids[static_cast<int64_t>(blockIdx.x) * a.top + k] =
-                static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-            a.top_logprobs[static_cast<int64_t>(blockIdx.x) * a.top + k] = lp(key_value(best));
-        }
-        last = best;
+    };
+    int at = v0 + tid;
+    for (; at + (kAhead - 1) * kThreads < v1; at += kAhead * kThreads) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) v[i] = ldg_stream_v4(vec + at + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) vector(v[i], at + i * kThreads);
     }
+    for (; at < v1; at += kThreads) vector(ldg_stream_v4(vec + at), at);
+    // the single logits, one a thread, by the first segment's CTA
+    const int singles = split == 0 ? head + tail : 0;
+    const int single = tid < head ? tid : a.vocab - tail + (tid - head);
+    float y1 = -CUDART_INF_F;
+    if (tid < singles) {
+        y1 = L::one(x, single);
+        if (sums.passed(y1)) sums.move(y1);
+        if (sums.ref != -CUDART_INF_F || y1 != y1) sums.add(y1);
+        above += y1 > mine;
+    }
+
+    // ---- the CTA's sums
+    auto larger = [](float p, float q) { return fmaxf(p, q); };
+    auto plus = [](float p, float q) { return p + q; };
+    {
+        const float ref = reduce_float(sums.ref, sf, larger);
+        sums.move(ref);
+        sums.s = reduce_float(sums.s, sf, plus);
+        sums.b = reduce_float(sums.b, sf, plus);
+        above = __reduce_add_sync(~0u, above);
+        if (lane == 0) si[warp] = above;
+        __syncthreads();
+        above = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) above += si[w];
+    }
+
+    // ---- its largest logits
+    uint64_t top = 0;                            // lane i: the i-th
+    if (a.top > 0) {
+        uint64_t key = 0;
+        if (best_v >= 0) {
+            const uint4 v = vec[best_v];
+            const int first = head + best_v * kN;
+            key = order_key(L::at(v, 0), first);                 // of NaN alone
+#pragma unroll
+            for (int i = kN - 1; i >= 0; --i)
+                if (L::at(v, i) == best) key = order_key(best, first + i);
+        }
+        list[tid] = key;
+        if (tid < singles) list[kThreads + tid] = order_key(y1, single);
+        __syncthreads();
+        top = top32(list, kThreads + singles, buffer);
+        if (a.top > 1) {
+            // every logit that reaches the bound, of the threads and single logits that do
+            const uint64_t bound = __shfl_sync(~0u, top, a.top - 1);
+            if (tid == 0) count = 0;
+            __syncthreads();
+            const bool again = key != 0 && key >= bound;
+            const uint64_t mine_too = tid < singles ? order_key(y1, single) : 0;
+            if (mine_too != 0 && mine_too >= bound) {
+                const int to = atomicAdd(&count, 1);
+                if (to < kList) list[to] = mine_too;
+            }
+            for (uint32_t todo = __ballot_sync(~0u, again); todo != 0; todo &= todo - 1) {
+                const int who = warp * 32 + __ffs(todo) - 1;
+                for (int i = v0 + who + lane * kThreads; i < v1; i += 32 * kThreads) {
+                    const uint4 v = vec[i];
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) {
+                        const uint64_t k = order_key(L::at(v, n), head + i * kN + n);
+                        if (k >= bound) {
+                            const int to = atomicAdd(&count, 1);
+                            if (to < kList) list[to] = k;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            if (count <= kList) {
+                top = top32(list, count, buffer);
+            } else {
+                // so many only where a few threads have most of the largest logits: one by one
+                uint64_t last = ~0ull;
+                for (int n = 0; n < a.top; ++n) {
+                    uint64_t next = mine_too < last ? mine_too : 0;
+                    for (int i = v0 + tid; i < v1; i += kThreads) {
+                        const uint4 v = vec[i];
+                        for (int m = 0; m < kN; ++m) {
+                            const uint64_t k = order_key(L::at(v, m), head + i * kN + m);
+                            if (k < last) next = max64(next, k);
+                        }
+                    }
+                    buffer[tid] = next;
+                    __syncthreads();
+                    for (int d = kThreads / 2; d > 0; d >>= 1) {
+                        if (tid < d) buffer[tid] = max64(buffer[tid], buffer[tid + d]);
+                        __syncthreads();
+                    }
+                    last = buffer[0];
+                    __syncthreads();
+                    if (lane == n) top = last;
+                }
+            }
+        }
+    }
+
+    // ---- segments joined by the last of them
+    if (splits > 1) {
+        Part* parts = reinterpret_cast<Part*>(scratch) + static_cast<int64_t>(row) * splits;
+        if (warp == 0) {
+            if (lane == 0) {
+                __stcg(&parts[split].ref, sums.ref);
+                __stcg(&parts[split].s, sums.s);
+                __stcg(&parts[split].b, sums.b);
+                __stcg(&parts[split].above, above);
+            }
+            __stcg(reinterpret_cast<unsigned long long*>(&parts[split].keys[lane]), static_cast<unsigned long long>(top));
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) {
+                last_one = atomicAdd(&arrivals[row], 1u) == static_cast<unsigned>(splits - 1);
+                if (last_one) arrivals[row] = 0;                 // for the next launch
+            }
+        }
+        __syncthreads();
+        if (!last_one) return;
+        __threadfence();
+        // in the order of the segments
+        float ref = -CUDART_INF_F;
+        for (int p = 0; p < splits; ++p) ref = fmaxf(ref, __ldcg(&parts[p].ref));
+        Sums all;
+        all.ref = ref;
+        above = 0;
+        for (int p = 0; p < splits; ++p) {
+            Sums one;
+            one.ref = __ldcg(&parts[p].ref), one.s = __ldcg(&parts[p].s), one.b = __ldcg(&parts[p].b);
+            one.move(ref);
+            all.s += one.s, all.b += one.b;
+            above += __ldcg(&parts[p].above);
+        }
+        sums = all;
+        if (a.top > 0) {
+            for (int i = tid; i < splits * 32; i += kThreads)
+                list[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&parts[i >> 5].keys[i & 31]));
+            __syncthreads();
+            top = top32(list, splits * 32, buffer);
+        }
+    }
+
+    // ---- results
+    const bool empty = sums.ref == -CUDART_INF_F && sums.s == 0.f;         // -inf alone
+    const float lse = empty ? -CUDART_INF_F : sums.ref + logf(sums.s);
+    auto logprob = [&](float y) { return y == -CUDART_INF_F && lse == lse && lse != CUDART_INF_F ? y : lse == CUDART_INF_F ? CUDART_NAN_F : y - lse; };
+    if (tid == 0) {
+        a.lse[row] = lse;
+        a.logprob[row] = known ? logprob(mine) : lse == lse ? -CUDART_INF_F : lse;
+        a.entropy[row] = empty ? 0.f : logf(sums.s) - sums.b / sums.s;
+        a.rank[row] = known ? above : a.vocab;
+    }
+    if (warp == 0 && lane < a.top) {
+        a.top_ids[static_cast<int64_t>(row) * a.top + lane] = key_index(top);
+        a.top_logprobs[static_cast<int64_t>(row) * a.top + lane] = logprob(key_value(top));
+    }
+}
+
+// Rows up to which they are split, and the segments of one: twice as many CTAs as SMs, of 4096
+// logits at least.
+int row_splits(int sm_count, int rows, int vocab) {
+    const int want = (2 * sm_count + rows - 1) / rows, most = vocab / 4096;
+    int n = want < most ? want : most;
+    if (n > kMaxSplits) n = kMaxSplits;
+    return rows >= 2 * sm_count || n < 1 ? 1 : n;
 }
 
 }  // namespace
 
-cudaError_t launch_logprobs(const Ctx&, const LogprobArgs& a, int dtype, cudaStream_t st) {
+size_t score_scratch_bytes(int sm_count) { return static_cast<size_t>(4) * sm_count * sizeof(Part); }
+
+cudaError_t launch_logprobs(const Ctx& ctx, const LogprobArgs& a, int dtype, cudaStream_t st) {
+    const int splits = row_splits(ctx.sm_count, a.tokens, a.vocab);
+    const unsigned grid = static_cast<unsigned>(a.tokens) * splits;
     switch (dtype) {
-        case HC_DTYPE_BF16: logprob_kernel<HC_DTYPE_BF16><<<a.tokens, kThreads, 0, st>>>(a); break;
-        case HC_DTYPE_FP16: logprob_kernel<HC_DTYPE_FP16><<<a.tokens, kThreads, 0, st>>>(a); break;
-        default: logprob_kernel<HC_DTYPE_FP32><<<a.tokens, kThreads, 0, st>>>(a);
+        case HC_DTYPE_BF16: score_kernel<HC_DTYPE_BF16><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals); break;
+        case HC_DTYPE_FP16: score_kernel<HC_DTYPE_FP16><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals); break;
+        default: score_kernel<HC_DTYPE_FP32><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals);
     }
     return cudaGetLastError();
 }
