@@ -66,27 +66,34 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB)
     return out
 
 
-def build_pycall(verbose: bool = False) -> str | None:
-    """The CPython module behind the binding's hc_read / hc_read_path calls
-    (csrc/hc_pycall.c, marshalling only). Without a C compiler or Python headers it
-    is skipped and the binding calls the library through ctypes alone."""
+# CPython modules behind the binding's calls (marshalling only) and their sources.
+PYCALLS = {"_hcpycall": "hc_pycall.c", "_hcpywindow": "hc_pywindow.c"}
+
+
+def build_pycall(verbose: bool = False) -> list[str]:
+    """The CPython modules behind the binding's calls (csrc/hc_pycall.c, csrc/hc_pywindow.c,
+    marshalling only). Without a C compiler or Python headers they are skipped and the
+    binding calls the library through ctypes alone."""
     import sysconfig
-    out = os.path.join(PKG, "_hcpycall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
     inc = sysconfig.get_paths()["include"]
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None or not os.path.exists(os.path.join(inc, "Python.h")):
         if verbose:
-            print("skipped the Python call module (no C compiler or Python headers)")
-        return None
-    tmp = out + ".tmp"
-    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", inc, os.path.join(CSRC, "hc_pycall.c"), "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"building the Python call module failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, out)
-    if verbose:
-        print(f"built {out}")
-    return out
+            print("skipped the Python call modules (no C compiler or Python headers)")
+        return []
+    built = []
+    for name, src in PYCALLS.items():
+        out = os.path.join(PKG, name + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+        tmp = out + ".tmp"
+        cmd = [cc, "-O2", "-shared", "-fPIC", "-I", inc, os.path.join(CSRC, src), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"building the Python call module {name} failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, out)
+        built.append(out)
+        if verbose:
+            print(f"built {out}")
+    return built
 
 
 def build_bounds_checked(verbose: bool = False) -> str:
