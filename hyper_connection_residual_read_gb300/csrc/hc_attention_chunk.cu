@@ -12,9 +12,12 @@
 //   for steps down to 2^-9 of that one and within 2^-20 of the largest value below. One logical and one fp16
 //   operation decode two codes: a code's bits alone are the subnormal code * 2^-24, and fma
 //   with S = 2^24 2^-E s gives S code 2^-24 - S 8 2^-24.
-// * What is left of a key, m_j + 8 s_j, is the same for all its dimensions: it meets
-//   sum(q) in the softmax, one fma a logit in fp32. Likewise sum p_j (m_j + 8 s_j) is
-//   summed in fp32 beside O. So the one rounding of the product is that of p to fp16.
+// * What is left of a key, m_j + 8 s_j, is the same for all its dimensions and meets
+//   sum(q): a further step of the first product, with both in two fp16 terms (22 bits),
+//   adds it to S. (As an fma a logit in the softmax, with the keys' terms read from shared
+//   memory, it took 2.08 ms where this takes KKK, the 8K chunk behind 8K tokens.) Likewise
+//   sum p_j (m_j + 8 s_j) is summed in fp32 beside O. So the one rounding of the product
+//   is that of p to fp16.
 // * Rows are the new tokens times the query heads of one kv head, so that a key is
 //   decoded once for all the heads that read it.
 // * Two row tiles (256 rows) share each decoded key tile; their products alternate, so
@@ -44,7 +47,7 @@ constexpr int kPieceFloats = 256 * 128 + 512;
 // rewritten for the tile four later, whose keys are decoded only after the products of the
 // tile two later, which follow the softmax of this one.
 struct Column {
-    float k[kTile], v[kTile];              // m + 8 s of keys and values
+    float v[kTile];                        // m + 8 s of the values
     float up[2];                           // 2^E of K', in two factors
     int ev;                                // E of V'
     int pad;
@@ -58,7 +61,11 @@ struct Smem {
     static constexpr int kV = kK + kStages * kOne;
     static constexpr int kColumn = kV + kStages * kOne;
     static constexpr int kSteps = kColumn + kCols * static_cast<int>(sizeof(Column));   // fp16 S [values?][tile parity]
-    static constexpr int kBytes = kSteps + 4 * kTile * 2 + 1024;       // and room to align
+    // the further step of the first product: [rows][16], of a row tile and of a key tile
+    static constexpr int kMore = kTile * 32;
+    static constexpr int kQMore = (kSteps + 4 * kTile * 2 + 255) / 256 * 256;
+    static constexpr int kKMore = kQMore + 2 * kMore;
+    static constexpr int kBytes = kKMore + kStages * kMore + 1024;     // and room to align
 };
 
 struct Bars {
@@ -210,9 +217,10 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
-// Four floats of shared memory as two pairs.
-__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
+// Eight floats of shared memory as pairs.
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[4]) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(tc::smem_u32(p)));
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2]), "=l"(v[3]) : "r"(tc::smem_u32(p) + 16));
 }
 __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -222,6 +230,26 @@ __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of a K-major tile of 16 16-bit elements a row stored with the 32-byte swizzle (8-row
+// atoms of 256 bytes), and the byte offset of 16-byte chunk c of row r in it.
+__device__ __forceinline__ uint64_t desc_sw32(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(256 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(6) << 61;
+    return d;
+}
+__device__ __forceinline__ uint32_t sw32_offset(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
+
+// x in two fp16 terms.
+__device__ __forceinline__ void split2(float x, __half& hi, __half& lo) {
+    hi = __float2half_rn(x);
+    lo = __float2half_rn(x - __half2float(hi));
+}
+constexpr float kMoreUp = 256.f;             // 2^8: the keys' terms up, the queries' down
 
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elected() {
@@ -317,6 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t column = 0;                           // tiles before this one, over all pieces
         constexpr uint32_t kS = tc::idesc_f16_f32(kTile, kTile), kO = tc::idesc_f16_f32(kTile, kD);
         const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(q_tile));
+        unsigned char* q_more = smem + S::kQMore + wg * S::kMore;
+        const uint64_t qm_desc = desc_sw32(tc::smem_u32(q_more)), km_desc = desc_sw32(tc::smem_u32(smem + S::kKMore));
         const uint64_t k_desc = tc::desc_sw128(tc::smem_u32(smem + S::kK)), v_desc = tc::desc_sw128(tc::smem_u32(smem + S::kV));
         constexpr uint32_t kStageStep = S::kOne / 16, kAtom = kTile * 128 / 16, kAtomV = kD * 128 / 16;   // in the descriptors' 16 bytes
         // The products of this row tile, issued by one thread of its first warp (the warp stays
@@ -332,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t off = (x >> 2) * kAtom + (x & 3) * 2;
                     tc::mma_f16(tmem + wg * kTile, q_desc + off, kb + off, kS, x > 0);
                 }
+                tc::mma_f16(tmem + wg * kTile, qm_desc, km_desc + stage * (S::kMore / 16), kS, true);
                 tc::mma_commit(&bars.s_full[wg]);
                 tc::mma_commit(&bars.k_empty[stage]);
                 if (alone) tc::mma_commit(&bars.k_empty[stage]);
@@ -410,6 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kTile * 128) + tc::sw128_offset(row, (c & 7) * 8)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
                 }
+                // sum(q), met by the keys' m + 8 s
+                __half hi, lo;
+                split2(qsum * (1.f / kMoreUp), hi, lo);
+                const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
+                *reinterpret_cast<uint4*>(q_more + sw32_offset(row, 0)) =
+                    make_uint4(*reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&l2), 0, 0);
+                *reinterpret_cast<uint4*>(q_more + sw32_offset(row, 1)) = make_uint4(0, 0, 0, 0);
                 tc::fence_proxy_async_smem();
             }
             // this row tile's key tiles: all, or every other one, which then no other row tile uses
@@ -424,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool fresh = true;
             float later = 1.f;                         // what O is to be multiplied by before its next product
             int ev = 0, done_tiles = 0;
-            const float g = factor * qsum;
             const int t1 = k.t1;
             const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);   // every row sees what lies before
             for (int j = k.t0; j < t1; ++j, ++column) {
@@ -439,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = j * kTile;
                 const bool tail = t + kTile > clear;
                 float fix = 1.f, peak = -CUDART_INF_F;
-                const uint64_t f2 = pair(f, f), g2 = pair(g, g);
+                const uint64_t f2 = pair(f, f);
                 uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
                 bool quick = !tail && !__any_sync(~0u, fresh);
                 if (quick) {
@@ -448,8 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // common to a value's dimensions.
                     const uint64_t b2 = pair(-base, -base);
                     uint32_t pw[4][16], ahead[2][16];
-                    uint64_t ko[2], vo[2];
-                    load_pairs(&col.k[0], ko);
+                    uint64_t vo[4];                              // of 8 keys
                     load_pairs(&col.v[0], vo);
                     tmem_load16(s_mem, ahead[0]);
 #pragma unroll
@@ -459,27 +495,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (part < 7) tmem_load16(s_mem + (part + 1) * 16, ahead[(part + 1) & 1]);
 #pragma unroll
                         for (int c = 0; c < 16; c += 8) {
+                            uint64_t vn[4] = {};                 // the next eight keys'
+                            if (part * 16 + c + 8 < kTile) load_pairs(&col.v[part * 16 + c + 8], vn);
                             float e[8];
 #pragma unroll
-                            for (int c4 = 0; c4 < 8; c4 += 4) {
-                                uint64_t kn[2] = {}, vn[2] = {};     // the next four keys'
-                                if (part * 16 + c + c4 + 4 < kTile) {
-                                    load_pairs(&col.k[part * 16 + c + c4 + 4], kn);
-                                    load_pairs(&col.v[part * 16 + c + c4 + 4], vn);
-                                }
-#pragma unroll
-                                for (int n = 0; n < 2; ++n) {
-                                    const int at = c4 + 2 * n;
-                                    const float2 x = unpair(fma2(pair(__uint_as_float(raw[c + at]), __uint_as_float(raw[c + at + 1])), f2,
-                                                                 fma2(ko[n], g2, b2)));
-                                    peak = max3(peak, x.x, x.y);
-                                    e[at] = exp2_fast(x.x), e[at + 1] = exp2_fast(x.y);
-                                    const uint64_t w = pair(e[at], e[at + 1]);
-                                    sum2 = add2(sum2, w);
-                                    flat2 = fma2(w, vo[n], flat2);
-                                }
-                                ko[0] = kn[0], ko[1] = kn[1], vo[0] = vn[0], vo[1] = vn[1];
+                            for (int n = 0; n < 4; ++n) {
+                                const float2 x = unpair(fma2(pair(__uint_as_float(raw[c + 2 * n]), __uint_as_float(raw[c + 2 * n + 1])), f2, b2));
+                                peak = max3(peak, x.x, x.y);
+                                e[2 * n] = exp2_fast(x.x), e[2 * n + 1] = exp2_fast(x.y);
+                                const uint64_t w = pair(e[2 * n], e[2 * n + 1]);
+                                sum2 = add2(sum2, w);
+                                flat2 = fma2(w, vo[n], flat2);
                             }
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) vo[n] = vn[n];
                             // P: column x * 8 + n of each 32 is token n * 4 + x, the order of the decoded values
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
@@ -527,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t visible = n == 0 ? seen[0] : n == 1 ? seen[1] : n == 2 ? seen[2] : seen[3];
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const float x = fmaf(__uint_as_float(raw[c]), f, fmaf(col.k[n * 32 + c], g, -base));
+                            const float x = fmaf(__uint_as_float(raw[c]), f, -base);
                             if ((visible >> c) & 1) peak = fmaxf(peak, x);
                         }
                     }
@@ -547,14 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t visible = n == 0 ? seen[0] : n == 1 ? seen[1] : n == 2 ? seen[2] : seen[3];
                         float e[32];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            uint64_t ko[2], vo[2];
-                            load_pairs(&col.k[n * 32 + c], ko);
+                        for (int c = 0; c < 32; c += 8) {
+                            uint64_t vo[4];
                             load_pairs(&col.v[n * 32 + c], vo);
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {
+                            for (int m = 0; m < 4; ++m) {
                                 const int c2 = c + 2 * m;
-                                const float2 x = unpair(fma2(pair(__uint_as_float(raw[c2]), __uint_as_float(raw[c2 + 1])), f2, fma2(ko[m], g2, b2)));
+                                const float2 x = unpair(fma2(pair(__uint_as_float(raw[c2]), __uint_as_float(raw[c2 + 1])), f2, b2));
                                 float2 v = unpair(vo[m]);        // a hidden value may be NaN
                                 if ((visible >> c2) & 1) e[c2] = exp2_fast(x.x);
                                 else e[c2] = 0.f, v.x = 0.f;
@@ -768,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = j * kTile + lane * 16;
                 if (lane < 8 && j < k.t1 && t < k.w.kv) ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
             };
-            uint64_t parts = 0, parts_next = 0;                 // bytes from `codes` to those of lane's part
+            uint64_t parts, parts_next = 0;                     // bytes from `codes` to those of lane's part
             auto check = [&](int j) -> uint64_t {
                 if (static_cast<unsigned>(ids) >= static_cast<unsigned>(a.c.blocks)) {
                     atomicOr(status, kStatusBounds);
@@ -785,7 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t scale = 0, scale_next = 0;                 // of token p of this tile and the next
             auto load_scale = [&](int j, uint64_t parts) -> uint32_t {
                 const uint64_t at = place(parts, p);
-                return j < k.t1 && j * kTile + p < k.w.kv ? scales[at / (kD / 2)] : 0;
+                if (j >= k.t1 || j * kTile + p >= k.w.kv) return 0;
+                prefetch_l2(a.c.codes + first * (kD / 2) + at);  // its codes are loaded a tile later
+                return scales[at / (kD / 2)];
             };
             auto load_codes = [&](int j) {
                 if (!is_v) {
@@ -813,7 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // the largest step of a tile, exchanged between the warps a tile ahead
             auto tell = [&](uint32_t scale, uint32_t parity) {
-                const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(fmaxf(bf16_lo(scale), 0.f)));   // of a NaN, 0
+                // of a NaN, 0; of a key whose common part would leave fp16, as much as that asks for
+                const float own = bf16_lo(scale), rest = fabsf(fmaf(8.f, own, bf16_hi(scale)));
+                const float most = fmaxf(fmaxf(own, 0.f), is_v ? 0.f : rest * (1.f / 32768.f));
+                const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(most));
                 if (lane == 0) step_max[is_v][parity][w] = m;
             };
             look_up(k.t0);
@@ -844,7 +877,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float up0 = power_of_two((24 - e) / 2), up1 = power_of_two(24 - e - (24 - e) / 2);
                 // a group held as NaN keeps the NaN in its common part alone
                 const float own = bf16_lo(scale);
-                (is_v ? col.v : col.k)[p] = fmaf(8.f, own, bf16_hi(scale));
+                const float rest = fmaf(8.f, own, bf16_hi(scale));
+                if (is_v) {
+                    col.v[p] = rest;
+                } else {
+                    __half hi, lo;
+                    split2(rest * (up0 * (1.f / 65536.f)) * up1, hi, lo);          // 2^8 2^-E
+                    const __half2 h2 = __halves2half2(hi, lo);
+                    const uint32_t h = *reinterpret_cast<const uint32_t*>(&h2);
+                    unsigned char* more = smem + S::kKMore + stage * S::kMore;
+                    *reinterpret_cast<uint4*>(more + sw32_offset(p, 0)) = make_uint4(h, h, 0, 0);
+                    *reinterpret_cast<uint4*>(more + sw32_offset(p, 1)) = make_uint4(0, 0, 0, 0);
+                }
                 steps[p] = __float2half_rn(own <= 3.0e38f ? own * up0 * up1 : 0.f);
                 if (p == 0) {
                     if (is_v) col.ev = e;
