@@ -7,11 +7,13 @@
 // the reference behind: it moves only when a logit passes it by 40 binary orders. Sums
 // of different references join as s e^(r - R) and e^(r - R) (b + s (r - R)).
 //
-// The alternatives cost the pass nothing: with the threads' largest logits known, the k-th
-// largest of those is a bound that at least k logits reach, and only the k threads that
-// reach it have to look at their logits again (a warp reads such a thread's vectors
-// in one gather). Logits and their indexes are compared as one number, so that equal
-// logits count in the order of their indexes.
+// The alternatives cost the pass next to nothing: with the threads' largest logits known,
+// the k-th largest of those is a bound that at least k logits reach, and only the k threads
+// that reach it have to look again: at the one vector with their largest, or, where their
+// second largest vector reaches the bound too, at all of theirs (a warp reads them in one
+// gather; without the second, all k threads did, and half the row's bytes more came from
+// DRAM). Logits and their indexes are compared as one number, so that equal logits count
+// in the order of their indexes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,6 +30,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;                    // vectors of a thread on their way
 constexpr int kList = 2048;                  // candidates that fit; more take the slow way
 constexpr float kPass = 27.7f;               // 40 ln 2: by how much a logit may pass the reference
+constexpr float kFar = 1024.f;               // references up to which fp32 holds x log2(e) - r log2(e) well
 constexpr int kMaxSplits = 64;
 
 // ---- logits
@@ -37,6 +40,8 @@ struct Logits;
 template <>
 struct Logits<HC_DTYPE_FP32> {
     static constexpr int kN = 4;             // of a vector
+    using Two = float2;
+    static __device__ __forceinline__ Two two(float x) { return make_float2(x, x); }
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     static __device__ __forceinline__ float at(const uint4& v, int i) {
         return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
@@ -45,20 +50,20 @@ struct Logits<HC_DTYPE_FP32> {
 template <>
 struct Logits<HC_DTYPE_BF16> {
     static constexpr int kN = 8;
-    static constexpr float kLow = -1e30f;    // below it, differences may be infinite
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return bf16_lo(static_cast<const uint16_t*>(p)[i]); }
     static __device__ __forceinline__ float at(const uint4& v, int i) {
         const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
         return (i & 1) ? bf16_hi(w) : bf16_lo(w);
     }
     using Two = __nv_bfloat162;
+    // the larger of both, NaN where x is
+    static __device__ __forceinline__ Two not_below(Two x, Two low) { return __hmax2_nan(x, low); }
     static __device__ __forceinline__ Two two(float x) { return __float2bfloat162_rn(x); }
     static __device__ __forceinline__ float2 widen(Two x) { return make_float2(__low2float(x), __high2float(x)); }
 };
 template <>
 struct Logits<HC_DTYPE_FP16> {
     static constexpr int kN = 8;
-    static constexpr float kLow = -65504.f;
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return __half2float(static_cast<const __half*>(p)[i]); }
     static __device__ __forceinline__ float at(const uint4& v, int i) {
         const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
@@ -66,6 +71,7 @@ struct Logits<HC_DTYPE_FP16> {
         return (i & 1) ? __high2float(h) : __low2float(h);
     }
     using Two = __half2;
+    static __device__ __forceinline__ Two not_below(Two x, Two low) { return __hmax2_nan(x, low); }
     static __device__ __forceinline__ Two two(float x) { return __float2half2_rn(x); }
     static __device__ __forceinline__ float2 widen(Two x) { return __half22float2(x); }
 };
@@ -134,12 +140,15 @@ __device__ __forceinline__ uint64_t bitonic_sort(uint64_t k, int lane) {
 }
 
 // The largest 32 of list[0..n) in falling order, in every warp, a key a lane (0: none). Every
-// thread calls it; `list` and `buffer` [kWarps * 32] are shared memory.
+// thread calls it; `list` and `buffer` [kWarps * 32] are shared memory. kFalling: each 32 of
+// the list are in falling order already.
+template <bool kFalling>
 __device__ uint64_t top32(const uint64_t* list, int n, uint64_t* buffer) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t best = 0;
     for (int c = warp * 32; c < n; c += kThreads) {
-        const uint64_t k = bitonic_sort(c + lane < n ? list[c + lane] : 0, lane);
+        uint64_t k = c + lane < n ? list[c + lane] : 0;
+        if (!kFalling) k = bitonic_sort(k, lane);
         // the larger of each and its mirror image are the largest 32 of both, in bitonic order
         best = c == warp * 32 ? k : bitonic_merge(max64(best, __shfl_sync(~0u, k, 31 - lane)), lane);
     }
@@ -159,21 +168,22 @@ __device__ uint64_t top32(const uint64_t* list, int n, uint64_t* buffer) {
     return best;
 }
 
-template <typename F>
-__device__ __forceinline__ float reduce_float(float v, float* s, F f) {
+// The sums of a warp's lanes, in every lane.
+__device__ __forceinline__ Sums warp_sums(Sums x) {
+    float ref = x.ref;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = f(v, __shfl_xor_sync(~0u, v, d));
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = s[0];
+    for (int d = 16; d > 0; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(~0u, ref, d));
+    x.move(ref);
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) v = f(v, s[w]);
-    __syncthreads();
-    return v;
+    for (int d = 16; d > 0; d >>= 1) {
+        x.s += __shfl_xor_sync(~0u, x.s, d);
+        x.b += __shfl_xor_sync(~0u, x.b, d);
+    }
+    return x;
 }
 
 // A segment's result in scratch.
-struct Part {
+struct alignas(16) Part {
     float ref, s, b;
     int above;
     uint64_t keys[32];
@@ -186,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, 5)
     constexpr int kN = L::kN;
     __shared__ uint64_t list[kList];
     __shared__ uint64_t buffer[kThreads];
-    __shared__ float sf[kWarps];
-    __shared__ int count, last_one, si[kWarps];
+    __shared__ float4 warps[kWarps];
+    __shared__ int count, last_one;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / splits, split = blockIdx.x % splits;
     constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2;
@@ -204,14 +214,27 @@ __global__ void __launch_bounds__(kThreads, 5)
 
     // ---- the pass
     Sums sums;
-    float best = -CUDART_INF_F;
+    float best = -CUDART_INF_F, second = -CUDART_INF_F;
     int best_v = -1;                             // the vector with this thread's largest logit
     int above = 0;
-    auto vector = [&](const uint4& v, int at) {
+    auto rank_in = [&](float top, int at) {
+        second = fmaxf(second, fminf(best, top));
+        if (top > best || best_v < 0) best = top, best_v = at;
+    };
+    // 16-bit logits: two at a time, about the reference in powers of two
+    float limit = CUDART_NAN_F;                  // what a logit may be without a look at the reference (NaN: none)
+    uint64_t s2 = 0, z2 = 0, r2 = 0;             // sums of e = 2^z and z e, and the reference
+    [[maybe_unused]] float floor_at = 0.f;       // logits below it count as it: e = 0, and z is finite
+    auto fold = [&]() {
+        const float2 s = unpair(s2), z = unpair(z2);
+        sums.s += s.x + s.y, sums.b = fmaf(z.x + z.y, kLn2, sums.b);
+        s2 = z2 = 0;
+    };
+    auto vector = [&](const uint4& v, int at, auto& count) {
         if constexpr (kDtype == HC_DTYPE_FP32) {
             const float y[4] = {L::at(v, 0), L::at(v, 1), L::at(v, 2), L::at(v, 3)};
             const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-            if (best_v < 0 || top > best) best = top, best_v = at;
+            rank_in(top, at);
             if (sums.passed(top)) sums.move(top);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -223,35 +246,42 @@ __global__ void __launch_bounds__(kThreads, 5)
             const Two w[4] = {*reinterpret_cast<const Two*>(&v.x), *reinterpret_cast<const Two*>(&v.y),
                               *reinterpret_cast<const Two*>(&v.z), *reinterpret_cast<const Two*>(&v.w)};
             const float2 hi = L::widen(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
-            const float2 lo = L::widen(__hmin2(__hmin2(w[0], w[1]), __hmin2(w[2], w[3])));
             const float top = fmaxf(hi.x, hi.y);
-            if (best_v < 0 || top > best) best = top, best_v = at;
-            if (sums.passed(top)) sums.move(top);
+            rank_in(top, at);
             const Two m = L::two(mine);
-            const float2 more = L::widen(__hadd2(__hadd2(__hgt2(w[0], m), __hgt2(w[1], m)), __hadd2(__hgt2(w[2], m), __hgt2(w[3], m))));
-            above += static_cast<int>(more.x + more.y);
-            if (fminf(lo.x, lo.y) < L::kLow || sums.ref == -CUDART_INF_F) {
-                // infinities, or so far down that their differences may be
-#pragma unroll
+            count = __hadd2(count, __hadd2(__hadd2(__hgt2(w[0], m), __hgt2(w[1], m)), __hadd2(__hgt2(w[2], m), __hgt2(w[3], m))));
+            if (!(top <= limit)) {
+                // the first logits, some that pass the reference, NaN, or a reference far from 0
+                fold();
+                if (sums.passed(top)) sums.move(top);
+#pragma unroll 1
                 for (int i = 0; i < 8; ++i) {
                     const float y = L::at(v, i);
                     if (sums.ref != -CUDART_INF_F || y != y) sums.add(y);
                 }
+                limit = fabsf(sums.ref) <= kFar ? sums.ref + kPass : CUDART_NAN_F;
+                floor_at = sums.ref - 200.f;
+                r2 = pair(-sums.ref * kLog2e, -sums.ref * kLog2e);
             } else {
-                const uint64_t r2 = pair(-sums.ref, -sums.ref), l2 = pair(kLog2e, kLog2e);
-                uint64_t s2 = pair(sums.s, 0.f), b2 = pair(sums.b, 0.f);
+                const uint64_t l2 = pair(kLog2e, kLog2e);
+                const Two low = L::two(floor_at);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 y = L::widen(w[i]);
-                    const uint64_t d = add2(pair(y.x, y.y), r2);
-                    const float2 z = unpair(mul2(d, l2));
-                    const uint64_t e = pair(exp2_fast(z.x), exp2_fast(z.y));
+                    const float2 y = L::widen(L::not_below(w[i], low));
+                    const uint64_t z = fma2(pair(y.x, y.y), l2, r2);
+                    const float2 zz = unpair(z);
+                    const uint64_t e = pair(exp2_fast(zz.x), exp2_fast(zz.y));
                     s2 = add2(s2, e);
-                    b2 = fma2(e, d, b2);
+                    z2 = fma2(e, z, z2);
                 }
-                const float2 s = unpair(s2), b = unpair(b2);
-                sums.s = s.x + s.y, sums.b = b.x + b.y;
             }
+        }
+    };
+    using Count = typename L::Two;
+    auto count_up = [&](Count& count) {
+        if constexpr (kDtype != HC_DTYPE_FP32) {
+            const float2 n = L::widen(count);
+            above += static_cast<int>(n.x + n.y);
         }
     };
     int at = v0 + tid;
@@ -259,10 +289,17 @@ __global__ void __launch_bounds__(kThreads, 5)
         uint4 v[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) v[i] = ldg_stream_v4(vec + at + i * kThreads);
+        Count count = L::two(0.f);               // at most 4 kAhead: exact
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) vector(v[i], at + i * kThreads);
+        for (int i = 0; i < kAhead; ++i) vector(v[i], at + i * kThreads, count);
+        count_up(count);
     }
-    for (; at < v1; at += kThreads) vector(ldg_stream_v4(vec + at), at);
+    for (; at < v1; at += kThreads) {
+        Count count = L::two(0.f);
+        vector(ldg_stream_v4(vec + at), at, count);
+        count_up(count);
+    }
+    fold();
     // the single logits, one a thread, by the first segment's CTA
     const int singles = split == 0 ? head + tail : 0;
     const int single = tid < head ? tid : a.vocab - tail + (tid - head);
@@ -274,66 +311,69 @@ __global__ void __launch_bounds__(kThreads, 5)
         above += y1 > mine;
     }
 
-    // ---- the CTA's sums
-    auto larger = [](float p, float q) { return fmaxf(p, q); };
-    auto plus = [](float p, float q) { return p + q; };
+    // ---- the CTA's sums: of each warp, then in every thread of the warps in order
+    sums = warp_sums(sums);
+    above = __reduce_add_sync(~0u, above);
+    if (lane == 0) warps[warp] = make_float4(sums.ref, sums.s, sums.b, __int_as_float(above));
+    // of this thread's largest logit, with the index of its vector's first: vectors of different
+    // threads compare by that as their logits do by their own
+    uint64_t key = 0;
+    if (a.top > 0) {
+        if (best_v >= 0) key = order_key(best, head + best_v * kN);
+        list[tid] = key;
+        if (tid < singles) list[kThreads + tid] = order_key(y1, single);
+        if (tid == 0) count = 0;
+    }
+    __syncthreads();
     {
-        const float ref = reduce_float(sums.ref, sf, larger);
-        sums.move(ref);
-        sums.s = reduce_float(sums.s, sf, plus);
-        sums.b = reduce_float(sums.b, sf, plus);
-        above = __reduce_add_sync(~0u, above);
-        if (lane == 0) si[warp] = above;
-        __syncthreads();
+        Sums all;
         above = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) above += si[w];
+        for (int w = 0; w < kWarps; ++w) all.ref = fmaxf(all.ref, warps[w].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            Sums one;
+            one.ref = warps[w].x, one.s = warps[w].y, one.b = warps[w].z;
+            one.move(all.ref);
+            all.s += one.s, all.b += one.b;
+            above += __float_as_int(warps[w].w);
+        }
+        sums = all;
     }
 
     // ---- its largest logits
     uint64_t top = 0;                            // lane i: the i-th
     if (a.top > 0) {
-        uint64_t key = 0;
-        if (best_v >= 0) {
-            const uint4 v = vec[best_v];
-            const int first = head + best_v * kN;
-            key = order_key(L::at(v, 0), first);                 // of NaN alone
-#pragma unroll
-            for (int i = kN - 1; i >= 0; --i)
-                if (L::at(v, i) == best) key = order_key(best, first + i);
-        }
-        list[tid] = key;
-        if (tid < singles) list[kThreads + tid] = order_key(y1, single);
-        __syncthreads();
-        top = top32(list, kThreads + singles, buffer);
-        if (a.top > 1) {
+        top = top32<false>(list, kThreads + singles, buffer);
+        {
             // every logit that reaches the bound, of the threads and single logits that do
             const uint64_t bound = __shfl_sync(~0u, top, a.top - 1);
-            if (tid == 0) count = 0;
-            __syncthreads();
             const bool again = key != 0 && key >= bound;
             const uint64_t mine_too = tid < singles ? order_key(y1, single) : 0;
+            auto look = [&](int i) {
+                const uint4 v = vec[i];
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    const float y = L::at(v, n);
+                    if (order_key(y, head + i * kN) >= bound) {
+                        const int to = atomicAdd(&count, 1);
+                        if (to < kList) list[to] = order_key(y, head + i * kN + n);
+                    }
+                }
+            };
+            const bool all = again && !(second < key_value(bound));
             if (mine_too != 0 && mine_too >= bound) {
                 const int to = atomicAdd(&count, 1);
                 if (to < kList) list[to] = mine_too;
             }
-            for (uint32_t todo = __ballot_sync(~0u, again); todo != 0; todo &= todo - 1) {
+            if (again && !all) look(best_v);
+            for (uint32_t todo = __ballot_sync(~0u, all); todo != 0; todo &= todo - 1) {
                 const int who = warp * 32 + __ffs(todo) - 1;
-                for (int i = v0 + who + lane * kThreads; i < v1; i += 32 * kThreads) {
-                    const uint4 v = vec[i];
-#pragma unroll
-                    for (int n = 0; n < kN; ++n) {
-                        const uint64_t k = order_key(L::at(v, n), head + i * kN + n);
-                        if (k >= bound) {
-                            const int to = atomicAdd(&count, 1);
-                            if (to < kList) list[to] = k;
-                        }
-                    }
-                }
+                for (int i = v0 + who + lane * kThreads; i < v1; i += 32 * kThreads) look(i);
             }
             __syncthreads();
             if (count <= kList) {
-                top = top32(list, count, buffer);
+                top = top32<false>(list, count, buffer);
             } else {
                 // so many only where a few threads have most of the largest logits: one by one
                 uint64_t last = ~0ull;
@@ -364,13 +404,9 @@ __global__ void __launch_bounds__(kThreads, 5)
     if (splits > 1) {
         Part* parts = reinterpret_cast<Part*>(scratch) + static_cast<int64_t>(row) * splits;
         if (warp == 0) {
-            if (lane == 0) {
-                __stcg(&parts[split].ref, sums.ref);
-                __stcg(&parts[split].s, sums.s);
-                __stcg(&parts[split].b, sums.b);
-                __stcg(&parts[split].above, above);
-            }
-            __stcg(reinterpret_cast<unsigned long long*>(&parts[split].keys[lane]), static_cast<unsigned long long>(top));
+            if (lane == 0) __stcg(reinterpret_cast<float4*>(&parts[split]), make_float4(sums.ref, sums.s, sums.b, __int_as_float(above)));
+            if (lane < a.top)
+                __stcg(reinterpret_cast<unsigned long long*>(&parts[split].keys[lane]), static_cast<unsigned long long>(top));
             __threadfence();
             __syncwarp();
             if (lane == 0) {
@@ -381,25 +417,26 @@ __global__ void __launch_bounds__(kThreads, 5)
         __syncthreads();
         if (!last_one) return;
         __threadfence();
-        // in the order of the segments
-        float ref = -CUDART_INF_F;
-        for (int p = 0; p < splits; ++p) ref = fmaxf(ref, __ldcg(&parts[p].ref));
-        Sums all;
-        all.ref = ref;
+        // the segments' sums, two a lane at most, in a fixed order
+        Sums mine_of[2];
         above = 0;
-        for (int p = 0; p < splits; ++p) {
-            Sums one;
-            one.ref = __ldcg(&parts[p].ref), one.s = __ldcg(&parts[p].s), one.b = __ldcg(&parts[p].b);
-            one.move(ref);
-            all.s += one.s, all.b += one.b;
-            above += __ldcg(&parts[p].above);
+#pragma unroll
+        for (int n = 0; n < kMaxSplits / 32; ++n) {
+            if (lane + 32 * n >= splits) continue;
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(&parts[lane + 32 * n]));
+            mine_of[n].ref = x.x, mine_of[n].s = x.y, mine_of[n].b = x.z;
+            above += __float_as_int(x.w);
         }
-        sums = all;
+        const float ref = fmaxf(mine_of[0].ref, mine_of[1].ref);
+        mine_of[0].move(ref), mine_of[1].move(ref);
+        mine_of[0].s += mine_of[1].s, mine_of[0].b += mine_of[1].b;
+        sums = warp_sums(mine_of[0]);
+        above = __reduce_add_sync(~0u, above);
         if (a.top > 0) {
             for (int i = tid; i < splits * 32; i += kThreads)
-                list[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&parts[i >> 5].keys[i & 31]));
+                list[i] = (i & 31) < a.top ? __ldcg(reinterpret_cast<const unsigned long long*>(&parts[i >> 5].keys[i & 31])) : 0;
             __syncthreads();
-            top = top32(list, splits * 32, buffer);
+            top = top32<true>(list, splits * 32, buffer);
         }
     }
 
@@ -419,10 +456,11 @@ __global__ void __launch_bounds__(kThreads, 5)
     }
 }
 
-// Rows up to which they are split, and the segments of one: twice as many CTAs as SMs, of 4096
-// logits at least.
-int row_splits(int sm_count, int rows, int vocab) {
-    const int want = (2 * sm_count + rows - 1) / rows, most = vocab / 4096;
+// The segments of a row, where there are too few rows to fill the GPU: twice as many CTAs as
+// SMs, but no segment below the vectors that a CTA's threads have on their way at once (8 x
+// 131072 bf16: 16 segments a row take KKK us, 38 took 15.3).
+int row_splits(int sm_count, int rows, int vocab, int vector) {
+    const int want = (2 * sm_count + rows - 1) / rows, most = vocab / (kThreads * kAhead * vector);
     int n = want < most ? want : most;
     if (n > kMaxSplits) n = kMaxSplits;
     return rows >= 2 * sm_count || n < 1 ? 1 : n;
@@ -433,7 +471,7 @@ int row_splits(int sm_count, int rows, int vocab) {
 size_t score_scratch_bytes(int sm_count) { return static_cast<size_t>(4) * sm_count * sizeof(Part); }
 
 cudaError_t launch_logprobs(const Ctx& ctx, const LogprobArgs& a, int dtype, cudaStream_t st) {
-    const int splits = row_splits(ctx.sm_count, a.tokens, a.vocab);
+    const int splits = row_splits(ctx.sm_count, a.tokens, a.vocab, dtype == HC_DTYPE_FP32 ? 4 : 8);
     const unsigned grid = static_cast<unsigned>(a.tokens) * splits;
     switch (dtype) {
         case HC_DTYPE_BF16: score_kernel<HC_DTYPE_BF16><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals); break;
