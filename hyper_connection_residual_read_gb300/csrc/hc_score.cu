@@ -30,7 +30,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;                    // vectors of a thread on their way
 constexpr int kList = 2048;                  // candidates that fit; more take the slow way
 constexpr float kPass = 27.7f;               // 40 ln 2: by how much a logit may pass the reference
-constexpr float kFar = 1024.f;               // references up to which fp32 holds x log2(e) - r log2(e) well
 constexpr int kMaxSplits = 64;
 
 // ---- logits
@@ -40,6 +39,7 @@ struct Logits;
 template <>
 struct Logits<HC_DTYPE_FP32> {
     static constexpr int kN = 4;             // of a vector
+    static constexpr float kFar = 1e6f;      // references up to which r - 200 is well below r
     using Two = float2;
     static __device__ __forceinline__ Two two(float x) { return make_float2(x, x); }
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
@@ -50,6 +50,7 @@ struct Logits<HC_DTYPE_FP32> {
 template <>
 struct Logits<HC_DTYPE_BF16> {
     static constexpr int kN = 8;
+    static constexpr float kFar = 1024.f;    // references up to which fp32 holds x log2(e) - r log2(e) well
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return bf16_lo(static_cast<const uint16_t*>(p)[i]); }
     static __device__ __forceinline__ float at(const uint4& v, int i) {
         const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
@@ -64,6 +65,7 @@ struct Logits<HC_DTYPE_BF16> {
 template <>
 struct Logits<HC_DTYPE_FP16> {
     static constexpr int kN = 8;
+    static constexpr float kFar = 1024.f;    // references up to which fp32 holds x log2(e) - r log2(e) well
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return __half2float(static_cast<const __half*>(p)[i]); }
     static __device__ __forceinline__ float at(const uint4& v, int i) {
         const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
@@ -88,6 +90,12 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
 }
 __device__ __forceinline__ int key_index(uint64_t k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
+
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
 
 // ---- sums about a reference
 
@@ -221,13 +229,14 @@ __global__ void __launch_bounds__(kThreads, 5)
         second = fmaxf(second, fminf(best, top));
         if (top > best || best_v < 0) best = top, best_v = at;
     };
-    // 16-bit logits: two at a time, about the reference in powers of two
+    // Two at a time, about the reference: 16-bit logits in powers of two (one fma), fp32 ones by
+    // their difference (which keeps their last bits)
     float limit = CUDART_NAN_F;                  // what a logit may be without a look at the reference (NaN: none)
-    uint64_t s2 = 0, z2 = 0, r2 = 0;             // sums of e = 2^z and z e, and the reference
-    [[maybe_unused]] float floor_at = 0.f;       // logits below it count as it: e = 0, and z is finite
+    uint64_t s2 = 0, z2 = 0, r2 = 0;             // sums of e and z e (d e), and the reference
+    float floor_at = 0.f;       // logits below it count as it: e = 0, and z is finite
     auto fold = [&]() {
         const float2 s = unpair(s2), z = unpair(z2);
-        sums.s += s.x + s.y, sums.b = fmaf(z.x + z.y, kLn2, sums.b);
+        sums.s += s.x + s.y, sums.b = fmaf(z.x + z.y, kDtype == HC_DTYPE_FP32 ? 1.f : kLn2, sums.b);
         s2 = z2 = 0;
     };
     auto vector = [&](const uint4& v, int at, auto& count) {
@@ -235,11 +244,27 @@ __global__ void __launch_bounds__(kThreads, 5)
             const float y[4] = {L::at(v, 0), L::at(v, 1), L::at(v, 2), L::at(v, 3)};
             const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
             rank_in(top, at);
-            if (sums.passed(top)) sums.move(top);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (sums.ref != -CUDART_INF_F || y[i] != y[i]) sums.add(y[i]);
-                above += y[i] > mine;
+            for (int i = 0; i < 4; ++i) above += y[i] > mine;
+            if (!(top <= limit)) {
+                fold();
+                if (sums.passed(top)) sums.move(top);
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i)
+                    if (sums.ref != -CUDART_INF_F || L::at(v, i) != L::at(v, i)) sums.add(L::at(v, i));
+                limit = fabsf(sums.ref) <= L::kFar ? sums.ref + kPass : CUDART_NAN_F;
+                floor_at = sums.ref - 200.f;
+                r2 = pair(-sums.ref, -sums.ref);
+            } else {
+                const uint64_t l2 = pair(kLog2e, kLog2e);
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const uint64_t d = add2(pair(max_nan(y[i], floor_at), max_nan(y[i + 1], floor_at)), r2);
+                    const float2 z = unpair(mul2(d, l2));
+                    const uint64_t e = pair(exp2_fast(z.x), exp2_fast(z.y));
+                    s2 = add2(s2, e);
+                    z2 = fma2(e, d, z2);
+                }
             }
         } else {
             using Two = typename L::Two;
@@ -259,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 5)
                     const float y = L::at(v, i);
                     if (sums.ref != -CUDART_INF_F || y != y) sums.add(y);
                 }
-                limit = fabsf(sums.ref) <= kFar ? sums.ref + kPass : CUDART_NAN_F;
+                limit = fabsf(sums.ref) <= L::kFar ? sums.ref + kPass : CUDART_NAN_F;
                 floor_at = sums.ref - 200.f;
                 r2 = pair(-sums.ref * kLog2e, -sums.ref * kLog2e);
             } else {
