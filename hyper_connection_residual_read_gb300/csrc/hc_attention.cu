@@ -28,8 +28,8 @@
 //   within fp16, sums in fp32): one vote a step instead of a reduction over lanes.
 //
 // Work is cut evenly, whatever the lengths: the units (256 tokens of one request and kv
-// head) are numbered through, and each CTA takes an equal run of them (with two more
-// counted for each request and head, for its start and merge). A CTA's eight
+// head) are numbered through, and each CTA takes an equal run of them (with four
+// more counted for each request and head, for its start and merge). A CTA's eight
 // warps take 32 tokens of each unit each and merge at the end of a (request, head). One
 // that is split between CTAs is joined by the last of them to finish, in the order of
 // the CTAs, from fp32 sums in scratch of a fixed size (a CTA can have at most two such
@@ -54,7 +54,8 @@ constexpr float kRaise = 8.f;                    // log2 by which a logit may pa
 constexpr float kStepRoom = 16.f;                // factor by which a step may pass the reference
 
 constexpr int kStages = 3;                       // steps of a warp's ring
-constexpr int kPieceCost = 2;                    // what a piece costs beside its units, in units
+constexpr int kPieceCost = 4;                    // what a piece costs beside its units, in units (64 ragged requests:
+                                                 // 131 us with 2, 118 with 4, 120 with 7)
 
 // A step's slot in a warp's ring: key codes, value codes, key scales, value scales.
 template <int kD>
@@ -122,12 +123,44 @@ __device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
 struct Run {
     int b;
     int64_t offset, begin, end, total, ctas;
+    Window w;                    // of request b
 };
 
+__device__ __forceinline__ void cut_run(Run& run, int64_t total) {
+    // CTAs beyond the number of slots have none, so that no run before them is empty
+    run.total = total;
+    run.ctas = min(static_cast<int64_t>(gridDim.x), total);
+    const int64_t i = blockIdx.x;
+    run.begin = i < run.ctas ? total * i / run.ctas : total;
+    run.end = i < run.ctas ? total * (i + 1) / run.ctas : total;
+}
+
 // The CTA's run: every CTA sums the slots of all requests, and the thread whose share of
-// the requests holds the run's first slot says where it lies.
-__device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* status) {
-    const int tid = threadIdx.x;
+// the requests holds the run's first slot says where it lies. Up to 32 requests each warp
+// does so for itself, a request a lane, without a barrier.
+__device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int* status) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (a.requests <= 32) {
+        Window w = {};
+        if (lane < a.requests) w = load_window(a, lane, blockIdx.x == 0 ? status : nullptr);
+        const int64_t mine = lane < a.requests ? window_slots(a, w) : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t t = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += t;
+        }
+        Run run;
+        cut_run(run, __shfl_sync(~0u, upto, 31));
+        run.b = min(__popc(__ballot_sync(~0u, upto <= run.begin)), 31);
+        run.offset = run.begin - __shfl_sync(~0u, upto - mine, run.b);
+        run.w.begin = __shfl_sync(~0u, w.begin, run.b);
+        run.w.n = __shfl_sync(~0u, w.n, run.b);
+        run.w.rows = __shfl_sync(~0u, w.rows, run.b);
+        run.w.kv = __shfl_sync(~0u, w.kv, run.b);
+        run.w.first = __shfl_sync(~0u, w.first, run.b);
+        return run;
+    }
     const int per = (a.requests + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
     int64_t mine = 0;
@@ -137,44 +170,41 @@ __device__ void find_run(const AttentionArgs& a, Run* run, int64_t* sums, int* s
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t t = __shfl_up_sync(~0u, upto, d);
-        if ((tid & 31) >= d) upto += t;
+        if (lane >= d) upto += t;
     }
-    if ((tid & 31) == 31) sums[tid >> 5] = upto;
+    if (lane == 31) sums[tid >> 5] = upto;
     __syncthreads();
     int64_t total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w == (tid >> 5)) upto += total;
         total += sums[w];
     }
-    // CTAs beyond the number of slots have none, so that no run before them is empty
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), i = blockIdx.x;
-    const int64_t begin = i < ctas ? total * i / ctas : total, end = i < ctas ? total * (i + 1) / ctas : total;
-    if (tid == 0) {
-        run->begin = begin;
-        run->end = end;
-        run->total = total;
-        run->ctas = ctas;
-    }
-    if (begin < end && begin < upto && begin >= upto - mine) {
+    Run run;
+    cut_run(run, total);
+    if (run.begin < run.end && run.begin < upto && run.begin >= upto - mine) {
         int64_t at = upto - mine;
         for (int b = b0; b < b1; ++b) {
-            const int64_t n = window_slots(a, load_window(a, b, nullptr));
-            if (begin < at + n) {
-                run->b = b;
-                run->offset = begin - at;
+            const Window w = load_window(a, b, nullptr);
+            const int64_t n = window_slots(a, w);
+            if (run.begin < at + n) {
+                run.b = b;
+                run.offset = run.begin - at;
+                run.w = w;
+                *shared = run;
                 break;
             }
             at += n;
         }
     }
     __syncthreads();
+    return run.begin < run.end ? *shared : run;
 }
 
 // The first piece of the run; false if it has none.
 __device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, Walk& k) {
     if (run.begin >= run.end) return false;
     k.b = run.b;
-    k.w = load_window(a, k.b, nullptr);
+    k.w = run.w;
     k.units = window_units(k.w);
     const int slots = k.units + kPieceCost;
     k.h = static_cast<int>(run.offset / slots);
@@ -217,13 +247,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     using S = Smem<kD, kNT>;
     using L = Slot<kD>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Run run;
+    __shared__ Run shared_run;
     __shared__ int64_t sums[kThreads / 32];
     __shared__ unsigned last_one;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int group = a.q_heads / a.c.kv_heads;
 
-    find_run(a, &run, sums, status);         // synchronises
+    const Run run = find_run(a, &shared_run, sums, status);
     Walk k;
     if (!walk_start(a, run, k)) return;
 
@@ -662,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     const int nt = u / kParts, m = u % kParts;
                     float peak[2] = {-CUDART_INF_F, -CUDART_INF_F}, sums_all[2] = {};
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = c0; c <= c1; ++c) {
                         const float* from = scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats;
                         const float2 top2 = __ldcg(reinterpret_cast<const float2*>(from + kPieceRows * kD + nt * 8 + 2 * tq));

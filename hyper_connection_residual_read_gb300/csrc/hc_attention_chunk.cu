@@ -38,7 +38,8 @@ constexpr int kThreads = 512;
 constexpr int kTile = 128;                 // keys of a tile, rows of a row tile
 constexpr int kStages = 2;                 // key tiles and value tiles in shared memory
 constexpr int kCols = 4;                   // column data of tiles (see the ring below)
-constexpr int kPieceCost = 2;              // what a piece costs beside its tiles, in tiles
+constexpr int kPieceCost = 5;              // what a piece costs beside its tiles, in tiles (ragged chunks:
+                                           // 108 us with 1, 102 with 2, 97 with 5)
 constexpr float kRaise = 8.f;              // log2 by which a logit may pass the maximum before it is raised
 constexpr float kMost = 15.f;              // and the most that a weight may have as fp16
 constexpr int kPieceFloats = 256 * 128 + 512;
@@ -276,10 +277,15 @@ __device__ __forceinline__ void scale_word(uint32_t (&h)[4], __half2 s, __half2 
     }
 }
 
-template <int kD, int kDtype>
+// kSame: both warpgroups have the same rows.
+template <int kD, int kDtype, bool kSame>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const AttentionArgs a, int same, float* scratch, unsigned* arrivals, int* status) {
+    chunk_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
     using S = Smem<kD>;
+    constexpr bool same = kSame;
+    // registers of a softmax thread and of a decoding one, 512 in all for two of each
+    constexpr int kMany = kSame ? 152 : 168, kFew = 256 - kMany;
+    static_assert(2 * (kMany + kFew) * 128 <= 65536);
     extern __shared__ unsigned char smem_raw[];
     __shared__ Bars bars;
     __shared__ Run run;
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ------------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMany));
         const int wg = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_mem = tmem + lanes + wg * kTile, o_mem = tmem + lanes + 2 * kTile + wg * kTile;
@@ -772,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------------ keys, values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFew));
         const bool is_v = warp >= 12;
         const int p = threadIdx.x & 127, w = warp & 3;
         const int sh = 31 - __clz(a.c.block_size), in_block = a.c.block_size - 1;
@@ -817,28 +823,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 prefetch_l2(a.c.codes + first * (kD / 2) + at);  // its codes are loaded a tile later
                 return scales[at / (kD / 2)];
             };
-            auto load_codes = [&](int j) {
-                if (!is_v) {
+            // (a piece of keys, loaded again as soon as it is decoded; or the values' tokens)
+            auto load_keys = [&](int j, int u) {
+                const uint64_t at = place(parts, key_token(u));
+                uint4 y = make_uint4(0, 0, 0, 0);
+                if (j * kTile + key_token(u) < k.w.kv) y = *reinterpret_cast<const uint4*>(codes + at);
+                raw[4 * u] = y.x, raw[4 * u + 1] = y.y, raw[4 * u + 2] = y.z, raw[4 * u + 3] = y.w;
+            };
+            auto load_values = [&](int j) {
 #pragma unroll
-                    for (int u = 0; u < kUnits; ++u) {
-                        const uint64_t at = place(parts, key_token(u));
-                        uint4 y = make_uint4(0, 0, 0, 0);
-                        if (j * kTile + key_token(u) < k.w.kv) y = *reinterpret_cast<const uint4*>(codes + at);
-                        raw[4 * u] = y.x, raw[4 * u + 1] = y.y, raw[4 * u + 2] = y.z, raw[4 * u + 3] = y.w;
+                for (int n = 0; n < 8; ++n) {
+                    const int x = vh * 64 + n * 4 + vt;
+                    const uint64_t at = place(parts, x);
+                    uint2 y = make_uint2(0, 0);
+                    if (j * kTile + x < k.w.kv) {
+                        if (kVW == 2) y = *reinterpret_cast<const uint2*>(codes + at);
+                        else y.x = *reinterpret_cast<const uint32_t*>(codes + at);
                     }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        const int x = vh * 64 + n * 4 + vt;
-                        const uint64_t at = place(parts, x);
-                        uint2 y = make_uint2(0, 0);
-                        if (j * kTile + x < k.w.kv) {
-                            if (kVW == 2) y = *reinterpret_cast<const uint2*>(codes + at);
-                            else y.x = *reinterpret_cast<const uint32_t*>(codes + at);
-                        }
-                        raw[n * kVW] = y.x;
-                        if (kVW == 2) raw[n * kVW + kVW - 1] = y.y;
-                    }
+                    raw[n * kVW] = y.x;
+                    if (kVW == 2) raw[n * kVW + kVW - 1] = y.y;
                 }
             };
             // the largest step of a tile, exchanged between the warps a tile ahead
@@ -852,7 +855,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             look_up(k.t0);
             parts = check(k.t0);
             scale = load_scale(k.t0, parts);
-            load_codes(k.t0);
+            if (is_v) {
+                load_values(k.t0);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) load_keys(k.t0, u);
+            }
             look_up(k.t0 + 1);
             parts = check(k.t0 + 1);
             scale_next = load_scale(k.t0 + 1, parts);
@@ -918,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4*>(to + (c >> 3) * (kTile * 128) + tc::sw128_offset(t, (c & 7) * 8)) =
                                 make_uint4(h[0], h[1], h[2], h[3]);
                         }
+                        if (more) load_keys(j + 1, u);
                     }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bars.k_full[stage]);
@@ -934,10 +943,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < kVW; ++x)
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            uint32_t h[4][4];                    // [token pair][dimension]
+                            uint32_t h[4][4], two[4];            // [token pair][dimension]
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                two[n] = __byte_perm(raw[2 * n * kVW + x], raw[(2 * n + 1) * kVW + x], half ? 0x7632 : 0x5410);
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
-                                decode_word(__byte_perm(raw[2 * n * kVW + x], raw[(2 * n + 1) * kVW + x], half ? 0x7632 : 0x5410), h[n]);
+                                decode_word(two[n], h[n]);
                                 scale_word(h[n], s[n], s16[n], low[n]);
                             }
 #pragma unroll
@@ -947,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bars.v_full[stage]);
+                    if (more) load_values(j + 1);
                 }
-                if (more) load_codes(j + 1);
                 parts = parts_next;
                 look_up(j + 3);
             }
@@ -962,14 +974,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int kD, int kDtype>
+template <int kD, int kDtype, bool kSame>
 cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
-    auto* kernel = chunk_kernel<kD, kDtype>;
+    auto* kernel = chunk_kernel<kD, kDtype, kSame>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
     if (e != cudaSuccess) return e;
-    const int same = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= kTile;
-    kernel<<<ctx.sm_count, kThreads, Smem<kD>::kBytes, st>>>(a, same, ctx.attn_pieces, ctx.attn_arrivals, ctx.s.status);
+    kernel<<<ctx.sm_count, kThreads, Smem<kD>::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals, ctx.s.status);
     return cudaGetLastError();
+}
+
+template <int kD, int kDtype>
+cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+    return static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= kTile ? launch_chunk<kD, kDtype, true>(ctx, a, st)
+                                                                                  : launch_chunk<kD, kDtype, false>(ctx, a, st);
 }
 
 }  // namespace
@@ -978,8 +995,8 @@ size_t attention_chunk_scratch_floats(int sm_count) { return static_cast<size_t>
 
 cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
     if (a.c.head_dim == 64)
-        return dtype == HC_DTYPE_BF16 ? launch_chunk<64, HC_DTYPE_BF16>(ctx, a, st) : launch_chunk<64, HC_DTYPE_FP16>(ctx, a, st);
-    return dtype == HC_DTYPE_BF16 ? launch_chunk<128, HC_DTYPE_BF16>(ctx, a, st) : launch_chunk<128, HC_DTYPE_FP16>(ctx, a, st);
+        return dtype == HC_DTYPE_BF16 ? launch_rows<64, HC_DTYPE_BF16>(ctx, a, st) : launch_rows<64, HC_DTYPE_FP16>(ctx, a, st);
+    return dtype == HC_DTYPE_BF16 ? launch_rows<128, HC_DTYPE_BF16>(ctx, a, st) : launch_rows<128, HC_DTYPE_FP16>(ctx, a, st);
 }
 
 }  // namespace hc
