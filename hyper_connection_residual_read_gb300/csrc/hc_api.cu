@@ -320,6 +320,8 @@ extern "C" int hc_read_init(int device, int max_tokens, float eps) {
         decode_fused_setup(&c.fused_decode) != cudaSuccess ||
         cudaMemset(c.lo3, 0, sizeof(uint16_t) * 3 * (size_t)max_tokens * kRank) != cudaSuccess ||
         prefill_setup(c) != cudaSuccess ||
+        window_setup() != cudaSuccess ||
+        attention_setup() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         free_ctx(c);
         return HC_ERR_CUDA;

@@ -1,5 +1,5 @@
 // Attention over the cache held in 4 bits, for windows of few rows: the new tokens times
-// the query heads of one kv head, at most 32.
+// the query heads of one kv head, at most 16.
 //
 // With few rows the cache's bytes bound the operator: head_dim / 2 + 4 bytes a token for
 // the key and as much for the value, read once. Everything else has to keep out of their
@@ -41,7 +41,7 @@
 
 #include <type_traits>
 
-#include "hc_attention.cuh"
+#include "hc_window.cuh"
 
 namespace hc {
 namespace {
@@ -74,8 +74,11 @@ struct Smem {
     static constexpr int kBytes = kStats + 2 * kWarps * 8 * kNT * 4;
 };
 
-// Fixed scratch: per CTA two pieces of up to 32 rows, and a counter of arrivals.
-constexpr int kMaxRows = 32;                     // of this kernel; more go to the chunk kernel
+// Fixed scratch: per CTA two pieces, and a counter of arrivals.
+// Rows of this kernel; more go to the chunk kernel. (Requests x tokens, 4 kv heads of 128: 64 x
+// 2K with 16 rows take 53 us here and 24 rows 77 us there, where 24 to 32 rows took 110 to 120
+// us here; one x 16K 21 us here with 16 rows, 39 us there with 24.)
+constexpr int kMaxRows = 16;
 constexpr int kPieceRows = kMaxRows;
 constexpr int kPieceFloats = kPieceRows * (128 + 2);
 
@@ -719,16 +722,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 
 template <int kD, int kDtype, int kNT>
 cudaError_t launch_window(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
-    using S = Smem<kD, kNT>;
-    auto* kernel = window_kernel<kD, kDtype, kNT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-    if (e != cudaSuccess) return e;
     // as many CTAs as are resident at once, and no more than there can be units
     const int64_t most = static_cast<int64_t>(a.requests) * a.c.kv_heads *
                          ((static_cast<int64_t>(a.width) * a.c.block_size + kUnit - 1) / kUnit);
     const int64_t resident = static_cast<int64_t>(ctx.sm_count) * (kNT == 1 ? kAttnCtasPerSm : 1);
     const int grid = static_cast<int>(most < resident ? most : resident);
-    kernel<<<grid, kThreads, S::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals, ctx.s.status);
+    window_kernel<kD, kDtype, kNT><<<grid, kThreads, Smem<kD, kNT>::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals,
+                                                                                  ctx.s.status);
     return cudaGetLastError();
 }
 
@@ -736,8 +736,17 @@ template <int kD, int kDtype>
 cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads);
     if (rows <= 8) return launch_window<kD, kDtype, 1>(ctx, a, st);
-    if (rows <= 16) return launch_window<kD, kDtype, 2>(ctx, a, st);
-    return launch_window<kD, kDtype, 4>(ctx, a, st);
+    return launch_window<kD, kDtype, 2>(ctx, a, st);
+}
+
+template <int kD, int kDtype, int kNT>
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(window_kernel<kD, kDtype, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD, kNT>::kBytes);
+}
+template <int kD, int kDtype>
+cudaError_t allow_rows() {
+    const cudaError_t e = allow_smem<kD, kDtype, 1>();
+    return e != cudaSuccess ? e : allow_smem<kD, kDtype, 2>();
 }
 
 }  // namespace
@@ -746,6 +755,14 @@ size_t attention_scratch_floats(int sm_count) {
     const size_t window = static_cast<size_t>(sm_count) * kAttnCtasPerSm * 2 * kPieceFloats;
     const size_t chunk = attention_chunk_scratch_floats(sm_count);
     return window > chunk ? window : chunk;
+}
+
+cudaError_t attention_setup() {
+    cudaError_t e = allow_rows<64, HC_DTYPE_BF16>();
+    if (e == cudaSuccess) e = allow_rows<64, HC_DTYPE_FP16>();
+    if (e == cudaSuccess) e = allow_rows<128, HC_DTYPE_BF16>();
+    if (e == cudaSuccess) e = allow_rows<128, HC_DTYPE_FP16>();
+    return e == cudaSuccess ? attention_chunk_setup() : e;
 }
 
 cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {

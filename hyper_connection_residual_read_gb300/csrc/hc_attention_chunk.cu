@@ -1,4 +1,4 @@
-// Attention over the cache held in 4 bits, for chunks: more than 32 rows (new tokens times
+// Attention over the cache held in 4 bits, for chunks: more than 16 rows (new tokens times
 // the query heads of a kv head), on tcgen05.
 //
 // Both products run on the tensor cores in fp16 with fp32 sums, 128 rows x 128 keys at a
@@ -15,7 +15,7 @@
 // * What is left of a key, m_j + 8 s_j, is the same for all its dimensions and meets
 //   sum(q): a further step of the first product, with both in two fp16 terms (22 bits),
 //   adds it to S. (As an fma a logit in the softmax, with the keys' terms read from shared
-//   memory, it took 2.08 ms where this takes KKK, the 8K chunk behind 8K tokens.) Likewise
+//   memory, it took 2.08 ms where this took 1.83, the 8K chunk behind 8K tokens.) Likewise
 //   sum p_j (m_j + 8 s_j) is summed in fp32 beside O. So the one rounding of the product
 //   is that of p to fp16.
 // * Rows are the new tokens times the query heads of one kv head, so that a key is
@@ -29,7 +29,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "hc_attention.cuh"
+#include <type_traits>
+
+#include "hc_window.cuh"
 
 namespace hc {
 namespace {
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = k.t0 == 0 && k.t1 == k.tiles;
             float other_base = -CUDART_INF_F, other_sum = 0.f;
             float* exchange = reinterpret_cast<float*>(smem + S::kQ);          // [kD][128], both row tiles' room
-            __shared__ float2 stats[kTile];
+            __shared__ float2 stats[kTile], joined[2][kTile];
             if (same) {
                 // the two warpgroups' sums over the same rows
                 asm volatile("bar.sync 1, 256;" ::: "memory");         // no product reads Q any more
@@ -713,18 +715,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o[n] = mine == 0.f ? 0.f : fmaf(__uint_as_float(v[n]), up, flat) * mine;
                         if (same && other != 0.f) o[n] = fmaf(exchange[(c * 32 + n) * kTile + row], other, o[n]);
                     }
-                    if (whole) {
-                        if (here) write(c, o, inv);
-                    } else {
+                    if (here && whole) {
+                        write(c, o, inv);
+                    } else if (here) {
 #pragma unroll
                         for (int n = 0; n < 8; ++n)
                             __stcg(reinterpret_cast<float4*>(piece) + (c * 8 + n) * 256 + prow,
                                    make_float4(o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]));
                     }
+                    __syncwarp();
                 }
                 if (whole) {
                     if (here && a.lse) a.lse[at] = total == 0.f ? -CUDART_INF_F : (peak + log2f(total)) * kLn2;
-                } else {
+                } else if (here) {
                     __stcg(reinterpret_cast<float2*>(piece + 256 * kD) + prow, make_float2(peak, total));
                 }
             }
@@ -748,30 +751,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last_one[wg]) {
                     __threadfence();
                     auto from = [&](int c) { return scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats; };
-                    float top = -CUDART_INF_F, all = 0.f;
-                    for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow).x);
-                    for (int c = c0; c <= c1; ++c) {
-                        const float2 st = __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow);
-                        if (st.x != -CUDART_INF_F) all += st.y * exp2_fast(st.x - top);
-                    }
-                    const float inv = all == 0.f ? 0.f : 1.f / all;
-#pragma unroll 1
-                    for (int d = 0; d < kD / 32; ++d) {
-                        float o[32] = {};
+                    if (here) {
+                        float top = -CUDART_INF_F, all = 0.f;
+#pragma unroll 8
+                        for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow).x);
+#pragma unroll 8
                         for (int c = c0; c <= c1; ++c) {
                             const float2 st = __ldcg(reinterpret_cast<const float2*>(from(c) + 256 * kD) + prow);
-                            const float by = st.x == -CUDART_INF_F ? 0.f : exp2_fast(st.x - top);
-                            if (by == 0.f) continue;
-#pragma unroll
-                            for (int m = 0; m < 8; ++m) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4*>(from(c)) + (d * 8 + m) * 256 + prow);
-                                o[4 * m] = fmaf(y.x, by, o[4 * m]), o[4 * m + 1] = fmaf(y.y, by, o[4 * m + 1]);
-                                o[4 * m + 2] = fmaf(y.z, by, o[4 * m + 2]), o[4 * m + 3] = fmaf(y.w, by, o[4 * m + 3]);
-                            }
+                            if (st.x != -CUDART_INF_F) all += st.y * exp2_fast(st.x - top);
                         }
-                        if (here) write(d, o, inv);
+                        joined[wg][row] = make_float2(top, all == 0.f ? 0.f : 1.f / all);
+                        if (a.lse) a.lse[at] = all == 0.f ? -CUDART_INF_F : (top + log2f(all)) * kLn2;
                     }
-                    if (here && a.lse) a.lse[at] = all == 0.f ? -CUDART_INF_F : (top + log2f(all)) * kLn2;
+                    asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                    // Four dimensions of each half or quarter of a row a thread, of kAhead parts at
+                    // a time: their latency is what a join waits for. (A row a thread and part after
+                    // part, 30 rows of one request of 16384 tokens took 94 us where this takes 45;
+                    // quarters, which suit few parts, make the kernel of shared rows spill: 16
+                    // verify windows 115 us with halves, 143 with quarters.)
+                    constexpr int kOf = kSame ? 2 : 4, kAhead = kSame ? 6 : 4, kSpan = kD / 4 / kOf;
+                    const int rows = same ? k.rows : min(k.rows - wg * kTile, kTile), at_row = prow - row;
+                    for (int n = row; n < rows * kSpan; n += 128) {
+                        const int r = n % rows, q = n / rows;
+                        const float2 join = joined[wg][r];
+                        float4 o[kOf] = {};
+                        auto join_parts = [&](int c, auto count) {
+                            constexpr int kCount = decltype(count)::value;
+                            float2 st[kCount];
+                            float4 y[kCount][kOf];
+#pragma unroll
+                            for (int m = 0; m < kCount; ++m) {
+                                const float* part = from(c + m);
+                                st[m] = __ldcg(reinterpret_cast<const float2*>(part + 256 * kD) + at_row + r);
+#pragma unroll
+                                for (int x = 0; x < kOf; ++x)
+                                    y[m][x] = __ldcg(reinterpret_cast<const float4*>(part) + (x * kSpan + q) * 256 + at_row + r);
+                            }
+#pragma unroll
+                            for (int m = 0; m < kCount; ++m) {
+                                if (st[m].x == -CUDART_INF_F) continue;
+                                const float by = exp2_fast(st[m].x - join.x);
+#pragma unroll
+                                for (int x = 0; x < kOf; ++x) {
+                                    o[x].x = fmaf(y[m][x].x, by, o[x].x), o[x].y = fmaf(y[m][x].y, by, o[x].y);
+                                    o[x].z = fmaf(y[m][x].z, by, o[x].z), o[x].w = fmaf(y[m][x].w, by, o[x].w);
+                                }
+                            }
+                        };
+                        int c = c0;
+                        for (; c + kAhead <= c1 + 1; c += kAhead) join_parts(c, std::integral_constant<int, kAhead>{});
+                        for (; c + 2 <= c1 + 1; c += 2) join_parts(c, std::integral_constant<int, 2>{});
+                        if (c <= c1) join_parts(c, std::integral_constant<int, 1>{});
+                        const int of = k.row0 + (same ? 0 : wg * kTile) + r;
+                        const int64_t to = (static_cast<int64_t>(k.w.begin + of / group) * a.q_heads + k.h * group + of % group) * kD;
+#pragma unroll
+                        for (int x = 0; x < kOf; ++x)
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + (x * kSpan + q) * 4) =
+                                make_uint2(narrow2<kDtype>(o[x].x * join.y, o[x].y * join.y), narrow2<kDtype>(o[x].z * join.y, o[x].w * join.y));
+                    }
                 }
             }
             advance(2 + wg);
@@ -976,10 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kD, int kDtype, bool kSame>
 cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
-    auto* kernel = chunk_kernel<kD, kDtype, kSame>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<ctx.sm_count, kThreads, Smem<kD>::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals, ctx.s.status);
+    chunk_kernel<kD, kDtype, kSame><<<ctx.sm_count, kThreads, Smem<kD>::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals,
+                                                                                      ctx.s.status);
     return cudaGetLastError();
 }
 
@@ -989,7 +1024,21 @@ cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st)
                                                                                   : launch_chunk<kD, kDtype, false>(ctx, a, st);
 }
 
+template <int kD, int kDtype>
+cudaError_t allow_smem() {
+    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<kD, kDtype, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(chunk_kernel<kD, kDtype, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
+}
+
 }  // namespace
+
+cudaError_t attention_chunk_setup() {
+    cudaError_t e = allow_smem<64, HC_DTYPE_BF16>();
+    if (e == cudaSuccess) e = allow_smem<64, HC_DTYPE_FP16>();
+    if (e == cudaSuccess) e = allow_smem<128, HC_DTYPE_BF16>();
+    if (e == cudaSuccess) e = allow_smem<128, HC_DTYPE_FP16>();
+    return e;
+}
 
 size_t attention_chunk_scratch_floats(int sm_count) { return static_cast<size_t>(sm_count) * 2 * kPieceFloats; }
 

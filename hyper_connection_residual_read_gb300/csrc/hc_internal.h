@@ -107,6 +107,10 @@ struct Ctx {
 Ctx* current_ctx(int* err);
 int check_ptr(const void* p, int device);
 
+// Kernel attributes of the window operators, once a context (hc_window.cu, hc_attention.cu).
+cudaError_t window_setup();
+cudaError_t attention_setup();
+
 // Floats of Ctx::attn_pieces (hc_attention.cu); CTAs that may share requests.
 size_t attention_scratch_floats(int sm_count);
 constexpr int kAttnCtasPerSm = 2;

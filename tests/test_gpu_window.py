@@ -325,6 +325,25 @@ def test_attention_of_many_short_requests():
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("heads", [(8, 8, 64), (8, 4, 128)], ids=str)
+def test_attention_of_many_chunks(heads):
+    """Chunks of all sizes in one call: blocks of the launch that go through pieces of one
+    and of two row tiles, whole and shared, in every order."""
+    g = np.random.default_rng(7)
+    lens = []
+    for _ in range(60):
+        new = int(g.integers(0, 300))
+        lens.append((new + int(g.integers(0, 700)), new))
+    c = Case(7, lens, *heads, 16, "fp16")
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("new", [5, 7, 9, 17, 32])
+def test_attention_of_one_window_split_over_the_launch(new):
+    c = Case(8, [(16001, new)], 8, 2, 128, 32, "bf16", mask=tree)
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("new", [1, 70])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("kind", ["large q", "small q", "offset", "spread", "zero scale", "negative scale"])
