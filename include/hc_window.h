@@ -43,8 +43,11 @@
  * elements. Outputs must not overlap inputs or each other unless said.
  *
  * What the device reads from arrays (lengths, block ids, slots, offsets) is checked by
- * the kernels: an entry that points outside its array is skipped and hc_read_status
- * reports HC_ERR_BOUNDS.
+ * the kernels, in every build, and hc_read_status reports HC_ERR_BOUNDS for an entry that
+ * points outside its array. A slot that does is skipped (hc_kv4_load: read as zeros);
+ * hc_kv4_attention reads block 0 in place of a block that does not exist, so that the
+ * request's output is wrong but no memory outside the cache is touched, and cuts lengths
+ * that do not fit to what does.
  */
 #ifndef HC_WINDOW_H
 #define HC_WINDOW_H
