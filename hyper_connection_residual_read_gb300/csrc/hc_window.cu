@@ -383,16 +383,20 @@ __global__ void __launch_bounds__(kCacheThreads) load_kernel(const CacheArgs a, 
     const int64_t at = (t * a.c.kv_heads + head) * kD + sub * 8;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
+        // A code stays where it is in its half word: 16^i c as the low bits of 2^23 + 16^i c, met by
+        // s / 16^i (exact: s has 8 bits and is 2^-126 at least, or 0), so that the sum is rounded
+        // once and the same.
         const float s = bf16_lo(sm[kv]), m = bf16_hi(sm[kv]);
+        const uint64_t s01 = pair(s, s * 0x1p-4f), s23 = pair(s * 0x1p-8f, s * 0x1p-12f);
+        const uint64_t m2 = pair(m, m), less = pair(-8388608.f, -8388608.f);
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            // 2^23 + code, less 2^23
-            const uint32_t w = code[kv] >> (4 * i);
-            const uint64_t c = add2(pair(__uint_as_float((w & 15u) | 0x4B000000u),
-                                         __uint_as_float(((w >> 4) & 15u) | 0x4B000000u)),
-                                    pair(-8388608.f, -8388608.f));
-            const float2 y = unpair(fma2(pair(s, s), c, pair(m, m)));
+            const uint32_t w = code[kv] >> (i / 4 * 16);
+            const int at = i % 4 * 4;
+            const uint64_t c = add2(pair(__uint_as_float((w & (15u << at)) | 0x4B000000u),
+                                         __uint_as_float((w & (240u << at)) | 0x4B000000u)), less);
+            const float2 y = unpair(fma2(i % 4 ? s23 : s01, c, m2));
             x[i] = y.x, x[i + 1] = y.y;
         }
         Raw8<kDtype> raw;
