@@ -830,19 +830,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vc = lane & 7, vt = (vc >> 2) * 32 + (vc & 3), vh = w >> 1, vd = ((w & 1) * 4 + (lane >> 3)) * (8 * kVW);
         uint32_t column = 0;
         while (on) {
-            // Lanes 0-7 hold the blocks of a tile's eight 16-token parts, looked up a tile ahead.
+            // Lanes 0-7 hold the blocks of a tile's eight 16-token parts, looked up a tile ahead. Loads
+            // have no conditions: tokens behind the end are read from the last block or one known
+            // before, and count for nothing once their scale is taken as 0. (A condition makes the
+            // loaded register one of two, joined, and so waited for, long before its use.)
             int ids = 0;
             const int64_t first = (static_cast<int64_t>(k.h) + (is_v ? a.c.kv_heads : 0)) * a.c.block_size;   // group in a block
             const unsigned char* codes = a.c.codes + first * (kD / 2) + (is_v ? vd / 2 : seg * 16);
             const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.c.scales) + first;
             auto look_up = [&](int j) {
-                const int t = j * kTile + lane * 16;
-                if (lane < 8 && j < k.t1 && t < k.w.kv) ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
+                const int t = max(min(j * kTile + lane * 16, k.w.kv - 1), 0);
+                ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
             };
             uint64_t parts, parts_next = 0;                     // bytes from `codes` to those of lane's part
             auto check = [&](int j) -> uint64_t {
                 if (static_cast<unsigned>(ids) >= static_cast<unsigned>(a.c.blocks)) {
-                    atomicOr(status, kStatusBounds);
+                    if (k.w.kv > 0) atomicOr(status, kStatusBounds);
                     ids = 0;                                    // wrong values, from the cache's own memory
                 }
                 return static_cast<uint64_t>(static_cast<uint32_t>(ids)) * block_bytes +
@@ -854,31 +857,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             uint32_t raw[16];                                   // keys [kUnits][4], or values [8][kVW]
             uint32_t scale = 0, scale_next = 0;                 // of token p of this tile and the next
-            auto load_scale = [&](int j, uint64_t parts) -> uint32_t {
+            auto load_scale = [&](uint64_t parts) -> uint32_t {
                 const uint64_t at = place(parts, p);
-                if (j >= k.t1 || j * kTile + p >= k.w.kv) return 0;
                 prefetch_l2(a.c.codes + first * (kD / 2) + at);  // its codes are loaded a tile later
                 return scales[at / (kD / 2)];
             };
             // (a piece of keys, loaded again as soon as it is decoded; or the values' tokens)
-            auto load_keys = [&](int j, int u) {
+            auto load_keys = [&](int u) {
                 const uint64_t at = place(parts, key_token(u));
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (j * kTile + key_token(u) < k.w.kv) y = *reinterpret_cast<const uint4*>(codes + at);
+                const uint4 y = *reinterpret_cast<const uint4*>(codes + at);
                 raw[4 * u] = y.x, raw[4 * u + 1] = y.y, raw[4 * u + 2] = y.z, raw[4 * u + 3] = y.w;
             };
-            auto load_values = [&](int j) {
+            auto load_values = [&]() {
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                     const int x = vh * 64 + n * 4 + vt;
                     const uint64_t at = place(parts, x);
-                    uint2 y = make_uint2(0, 0);
-                    if (j * kTile + x < k.w.kv) {
-                        if (kVW == 2) y = *reinterpret_cast<const uint2*>(codes + at);
-                        else y.x = *reinterpret_cast<const uint32_t*>(codes + at);
+                    if (kVW == 2) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(codes + at);
+                        raw[n * kVW] = y.x, raw[n * kVW + kVW - 1] = y.y;
+                    } else {
+                        raw[n] = *reinterpret_cast<const uint32_t*>(codes + at);
                     }
-                    raw[n * kVW] = y.x;
-                    if (kVW == 2) raw[n * kVW + kVW - 1] = y.y;
                 }
             };
             // the largest step of a tile, exchanged between the warps a tile ahead
@@ -891,17 +891,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             look_up(k.t0);
             parts = check(k.t0);
-            scale = load_scale(k.t0, parts);
+            scale = load_scale(parts);
+            auto seen = [&](int j, uint32_t scale) { return j * kTile + p < k.w.kv ? scale : 0u; };
             if (is_v) {
-                load_values(k.t0);
+                load_values();
             } else {
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) load_keys(k.t0, u);
+                for (int u = 0; u < kUnits; ++u) load_keys(u);
             }
             look_up(k.t0 + 1);
             parts = check(k.t0 + 1);
-            scale_next = load_scale(k.t0 + 1, parts);
+            scale_next = load_scale(parts);
             look_up(k.t0 + 2);
+            scale = seen(k.t0, scale);
             tell(scale, column & 1);
             asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
             int e = 0;
@@ -940,13 +942,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else col.up[0] = power_of_two(e / 2), col.up[1] = power_of_two(e - e / 2);
                 }
                 tc::mbar_arrive(&bars.col_full[column % kCols]);
-                tell(scale_next, (column + 1) & 1);
+                scale = seen(j + 1, scale_next);
+                tell(scale, (column + 1) & 1);
                 asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
                 const bool more = j + 1 < k.t1;
                 if (more) {
                     parts_next = check(j + 2);
-                    scale = scale_next;
-                    scale_next = load_scale(j + 2, parts_next);
+                    scale_next = load_scale(parts_next);
                 }
                 if (!is_v) {
                     unsigned char* to = smem + S::kK + stage * S::kOne;
@@ -963,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4*>(to + (c >> 3) * (kTile * 128) + tc::sw128_offset(t, (c & 7) * 8)) =
                                 make_uint4(h[0], h[1], h[2], h[3]);
                         }
-                        if (more) load_keys(j + 1, u);
+                        if (more) load_keys(u);
                     }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bars.k_full[stage]);
@@ -996,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bars.v_full[stage]);
-                    if (more) load_values(j + 1);
+                    if (more) load_values();
                 }
                 parts = parts_next;
                 look_up(j + 3);
