@@ -34,6 +34,10 @@
 // that is split between CTAs is joined by the last of them to finish, in the order of
 // the CTAs, from fp32 sums in scratch of a fixed size (a CTA can have at most two such
 // pieces).
+//
+// Measured: 64 requests of one token over up to 16K tokens, 32/8 heads of 128, 119 us, 4.9
+// TB/s of cache (72% of the copy rate): issue bounds it, the ALU pipe at 57%, 534
+// instructions a warp for 32 tokens of 4 rows. One request over 4K tokens 11.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -14,6 +14,10 @@
 // gather; without the second, all k threads did, and half the row's bytes more came from
 // DRAM). Logits and their indexes are compared as one number, so that equal logits count
 // in the order of their indexes.
+//
+// Measured: 4096 x 131072 bf16 with the top 20, 203 us, 5.3 TB/s (78% of the copy rate): issue
+// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 10.4 us, 96 x 50257 fp32 12.8
+// us: half of that is the join of the segments and the choice of the top ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
