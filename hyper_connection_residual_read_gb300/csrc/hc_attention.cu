@@ -35,9 +35,9 @@
 // the CTAs, from fp32 sums in scratch of a fixed size (a CTA can have at most two such
 // pieces).
 //
-// Measured: 64 requests of one token over up to 16K tokens, 32/8 heads of 128, 119 us, 4.9
+// Measured: 64 requests of one token over up to 16K tokens, 32/8 heads of 128, 120 us, 4.9
 // TB/s of cache (72% of the copy rate): issue bounds it, the ALU pipe at 57%, 534
-// instructions a warp for 32 tokens of 4 rows. One request over 4K tokens 11.4 us.
+// instructions a warp for 32 tokens of 4 rows. One request over 4K tokens 10.3 us, over 200 6.7.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -91,30 +91,31 @@ constexpr int kPieceFloats = kPieceRows * (128 + 2);
 struct Walk {
     int b, h, u0, u1, units;     // the units [u0, u1) of (b, h), of `units`
     int64_t left, base;          // slots left, and the number of (b, h)'s first slot
+    int cost;                    // slots before its units
     Window w;
 };
 
 __device__ __forceinline__ int window_units(const Window& w) {
     return w.n > 0 ? max((w.kv + kUnit - 1) / kUnit, 1) : 0;
 }
-__device__ __forceinline__ int64_t window_slots(const AttentionArgs& a, const Window& w) {
+__device__ __forceinline__ int64_t window_slots(const AttentionArgs& a, const Window& w, int cost) {
     const int units = window_units(w);
-    return units ? static_cast<int64_t>(units + kPieceCost) * a.c.kv_heads : 0;
+    return units ? static_cast<int64_t>(units + cost) * a.c.kv_heads : 0;
 }
 
 // Takes the slots of (b, h) from `from` on; false if none of them is a unit.
 __device__ __forceinline__ bool walk_piece(Walk& k, int from) {
-    const int64_t to = min(static_cast<int64_t>(k.units + kPieceCost), from + k.left);
+    const int64_t to = min(static_cast<int64_t>(k.units + k.cost), from + k.left);
     k.left -= to - from;
-    k.u0 = max(from - kPieceCost, 0);
-    k.u1 = static_cast<int>(to) - kPieceCost;
+    k.u0 = max(from - k.cost, 0);
+    k.u1 = static_cast<int>(to) - k.cost;
     return k.u1 > k.u0;
 }
 
 // To the next piece; false at the end of the run.
 __device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
     if (k.left == 0) return false;
-    k.base += k.units + kPieceCost;
+    k.base += k.units + k.cost;
     if (++k.h == a.c.kv_heads) {
         k.h = 0;
         do {
@@ -130,6 +131,7 @@ __device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
 struct Run {
     int b;
     int64_t offset, begin, end, total, ctas;
+    int cost;
     Window w;                    // of request b
 };
 
@@ -150,7 +152,11 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
     if (a.requests <= 32) {
         Window w = {};
         if (lane < a.requests) w = load_window(a, lane, blockIdx.x == 0 ? status : nullptr);
-        const int64_t mine = lane < a.requests ? window_slots(a, w) : 0;
+        // no more units than CTAs: one each (a piece's cost would leave CTAs without one, and others
+        // with two: one request of 8K tokens 16.3 us against 14.6)
+        const int units = __reduce_add_sync(~0u, lane < a.requests ? window_units(w) : 0);
+        const int cost = static_cast<int64_t>(units) * a.c.kv_heads <= gridDim.x ? 0 : kPieceCost;
+        const int64_t mine = lane < a.requests ? window_slots(a, w, cost) : 0;
         int64_t upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -158,6 +164,7 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
             if (lane >= d) upto += t;
         }
         Run run;
+        run.cost = cost;
         cut_run(run, __shfl_sync(~0u, upto, 31));
         run.b = min(__popc(__ballot_sync(~0u, upto <= run.begin)), 31);
         run.offset = run.begin - __shfl_sync(~0u, upto - mine, run.b);
@@ -172,7 +179,7 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
     const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += window_slots(a, load_window(a, b, blockIdx.x == 0 ? status : nullptr));
+        mine += window_slots(a, load_window(a, b, blockIdx.x == 0 ? status : nullptr), kPieceCost);
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -187,12 +194,13 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
         total += sums[w];
     }
     Run run;
+    run.cost = kPieceCost;
     cut_run(run, total);
     if (run.begin < run.end && run.begin < upto && run.begin >= upto - mine) {
         int64_t at = upto - mine;
         for (int b = b0; b < b1; ++b) {
             const Window w = load_window(a, b, nullptr);
-            const int64_t n = window_slots(a, w);
+            const int64_t n = window_slots(a, w, kPieceCost);
             if (run.begin < at + n) {
                 run.b = b;
                 run.offset = run.begin - at;
@@ -213,7 +221,8 @@ __device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& ru
     k.b = run.b;
     k.w = run.w;
     k.units = window_units(k.w);
-    const int slots = k.units + kPieceCost;
+    k.cost = run.cost;
+    const int slots = k.units + k.cost;
     k.h = static_cast<int>(run.offset / slots);
     const int from = static_cast<int>(run.offset - static_cast<int64_t>(k.h) * slots);
     k.left = run.end - run.begin;
@@ -589,8 +598,11 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         if (more) begin(k);
 
         // ---- merge the warps: their fragments lie alike, so that unit m of 4 values a lane
-        // is exchanged through [warp][lane] and summed by warp m % 8
-        float4* merge = reinterpret_cast<float4*>(smem + S::kMerge);
+        // is exchanged through [warp][lane] and summed by warp m % 8: one after the other through
+        // two buffers, or, after the last piece, all at once through the ring (2 us
+        // less: a request of 200 tokens 8.9 -> 6.9 us)
+        static_assert(S::kMerge >= kNT * kVW * 4 * kWarps * 32 * 16, "the ring holds every unit");
+        float4* merge = reinterpret_cast<float4*>(smem + (more ? S::kMerge : 0));
         const float vup = vdown == 0.f ? 0.f : kCodeUp / vdown;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");   // the last piece's statistics are read
         // rows 2 tq and 2 tq + 1 of each 8
@@ -627,6 +639,26 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 if (a.lse && d == 0) a.lse[at] = total[e] == 0.f ? -CUDART_INF_F : (peak[e] + log2f(total[e])) * kLn2;
             }
         };
+        auto finish = [&](int nt, int m, const float4* buffer, const float (&peak)[2], const float (&total)[2]) {
+            float4 x = buffer[lane];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 y = buffer[w * 32 + lane];
+                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
+            if (whole) {
+                write_rows(nt, m, x, peak, total);
+            } else {
+                __stcg(reinterpret_cast<float4*>(piece) + (nt * kParts + m) * 32 + lane, x);
+                if (m == 0 && g == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        __stcg(piece + kPieceRows * kD + nt * 8 + 2 * tq + e, peak[e]);
+                        __stcg(piece + kPieceRows * kD + kPieceRows + nt * 8 + 2 * tq + e, total[e]);
+                    }
+                }
+            }
+        };
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             float peak[2], total[2], fix[2];
@@ -655,46 +687,33 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     x.y = fmaf(o[m][nt][1] - eight[nt][1], vup, flat[nt][1]) * fix[1];
                     x.w = fmaf(fmaf(o[m][nt][3], kOdd, -eight[nt][1]), vup, flat[nt][1]) * fix[1];
                 }
-                float4* buffer = merge + (turn_m & 1) * kWarps * 32;
+                float4* buffer = merge + (more ? turn_m & 1 : turn_m) * kWarps * 32;
                 buffer[warp * 32 + lane] = x;
-                asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-                if (warp == turn_m % kWarps) {
-                    x = buffer[lane];
-#pragma unroll
-                    for (int w = 1; w < kWarps; ++w) {
-                        const float4 y = buffer[w * 32 + lane];
-                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                    }
-                    if (whole) {
-                        write_rows(nt, m, x, peak, total);
-                    } else {
-                        __stcg(reinterpret_cast<float4*>(piece) + turn_m * 32 + lane, x);
-                        if (m == 0 && g == 0) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                __stcg(piece + kPieceRows * kD + nt * 8 + 2 * tq + e, peak[e]);
-                                __stcg(piece + kPieceRows * kD + kPieceRows + nt * 8 + 2 * tq + e, total[e]);
-                            }
-                        }
-                    }
+                if (more) {
+                    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+                    if (warp == turn_m % kWarps) finish(nt, m, buffer, peak, total);
                 }
+            }
+            if (!more) {
+                asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+#pragma unroll 1
+                for (int m = 0; m < kParts; ++m)
+                    if (warp == (nt * kParts + m) % kWarps) finish(nt, m, merge + (nt * kParts + m) * kWarps * 32, peak, total);
             }
         }
         if (!whole) {
             // the CTAs that share this (request, head): from the one with its first unit on
             const int64_t total = run.total, n = run.ctas;
-            const int c0 = static_cast<int>(((done.base + kPieceCost + 1) * n - 1) / total);
-            const int c1 = static_cast<int>(((done.base + kPieceCost + done.units) * n - 1) / total);
-            __threadfence();
+            const int c0 = static_cast<int>(((done.base + done.cost + 1) * n - 1) / total);
+            const int c1 = static_cast<int>(((done.base + done.cost + done.units) * n - 1) / total);
             asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
             if (threadIdx.x == 0) {
-                const unsigned before = atomicAdd(&arrivals[c0], 1u);
+                const unsigned before = arrive(&arrivals[c0]);
                 last_one = before == static_cast<unsigned>(c1 - c0);
                 if (last_one) arrivals[c0] = 0;              // for the next launch
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
             if (last_one) {
-                __threadfence();
                 for (int u = warp; u < kNT * kParts; u += kWarps) {
                     const int nt = u / kParts, m = u % kParts;
                     float peak[2] = {-CUDART_INF_F, -CUDART_INF_F}, sums_all[2] = {};

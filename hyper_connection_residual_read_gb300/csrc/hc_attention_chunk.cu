@@ -746,16 +746,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t n = run.ctas;
                 const int c0 = static_cast<int>(((k.base + kPieceCost + 1) * n - 1) / run.total);
                 const int c1 = static_cast<int>(((k.base + kPieceCost + k.tiles) * n - 1) / run.total);
-                __threadfence();
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
                 if (row == 0) {
-                    const unsigned before = atomicAdd(&arrivals[2 * c0 + wg], 1u);
+                    const unsigned before = arrive(&arrivals[2 * c0 + wg]);
                     last_one[wg] = before == static_cast<unsigned>(c1 - c0);
                     if (last_one[wg]) arrivals[2 * c0 + wg] = 0;
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
                 if (last_one[wg]) {
-                    __threadfence();
                     auto from = [&](int c) { return scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats; };
                     if (here) {
                         float top = -CUDART_INF_F, all = 0.f;

@@ -16,7 +16,7 @@
 // in the order of their indexes.
 //
 // Measured: 4096 x 131072 bf16 with the top 20, 203 us, 5.3 TB/s (78% of the copy rate): issue
-// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 10.4 us, 96 x 50257 fp32 12.8
+// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 10.2 us, 96 x 50257 fp32 12.8
 // us: half of that is the join of the segments and the choice of the top ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -430,16 +430,14 @@ __global__ void __launch_bounds__(kThreads, 5)
             if (lane == 0) __stcg(reinterpret_cast<float4*>(&parts[split]), make_float4(sums.ref, sums.s, sums.b, __int_as_float(above)));
             if (lane < a.top)
                 __stcg(reinterpret_cast<unsigned long long*>(&parts[split].keys[lane]), static_cast<unsigned long long>(top));
-            __threadfence();
             __syncwarp();
             if (lane == 0) {
-                last_one = atomicAdd(&arrivals[row], 1u) == static_cast<unsigned>(splits - 1);
+                last_one = arrive(&arrivals[row]) == static_cast<unsigned>(splits - 1);
                 if (last_one) arrivals[row] = 0;                 // for the next launch
             }
         }
         __syncthreads();
         if (!last_one) return;
-        __threadfence();
         // the segments' sums, two a lane at most, in a fixed order
         Sums mine_of[2];
         above = 0;

@@ -120,6 +120,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
+// Counts a block of the launch that has written its part; the count before it. One thread calls
+// it, behind a barrier that the writers have passed: release and acquire cover what the barrier
+// ordered, on both sides (a fence by every writer, and one by every reader, cost 0.3 us more).
+__device__ __forceinline__ unsigned arrive(unsigned* counter) {
+    unsigned before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
+}
 // The larger, NaN if either is.
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;

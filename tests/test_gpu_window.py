@@ -338,6 +338,12 @@ def test_attention_of_many_chunks(heads):
     c.check(*c.run())
 
 
+def test_attention_of_chunks_that_see_no_cache():
+    """Requests whose tokens are not in the cache at all: their table rows hold nothing."""
+    c = Case(9, [(0, 40), (30, 30), (0, 200), (17, 90)], 8, 2, 128, 16, "bf16")
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("new", [5, 7, 9, 17, 32])
 def test_attention_of_one_window_split_over_the_launch(new):
     c = Case(8, [(16001, new)], 8, 2, 128, 32, "bf16", mask=tree)
