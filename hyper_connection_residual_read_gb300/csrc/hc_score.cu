@@ -15,8 +15,8 @@
 // DRAM). Logits and their indexes are compared as one number, so that equal logits count
 // in the order of their indexes.
 //
-// Measured: 4096 x 131072 bf16 with the top 20, 203 us, 5.3 TB/s (78% of the copy rate): issue
-// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 10.2 us, 96 x 50257 fp32 12.8
+// Measured: 4096 x 131072 bf16 with the top 20, 200 us, 5.4 TB/s (79% of the copy rate): issue
+// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 9.7 us, 96 x 50257 fp32 12.2
 // us: half of that is the join of the segments and the choice of the top ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -214,6 +214,10 @@ __global__ void __launch_bounds__(kThreads, 5)
     const uint4* vec = reinterpret_cast<const uint4*>(x + head * kItem);
     const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * split / splits);
     const int v1 = static_cast<int>(static_cast<int64_t>(vectors) * (split + 1) / splits);
+    // the first logits on their way while the token's is found
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (v0 + tid + i * kThreads < v1 && (lane & 7) == 0) prefetch_l2(vec + v0 + tid + i * kThreads);
     const int id = a.ids[row];
     const bool known = id >= 0 && id < a.vocab;
     const float mine = known ? L::one(x, id) : CUDART_INF_F;
@@ -438,6 +442,9 @@ __global__ void __launch_bounds__(kThreads, 5)
         }
         __syncthreads();
         if (!last_one) return;
+        // the segments' largest, on their way while their sums are joined
+        for (int i = tid; a.top > 0 && i < splits * 32; i += kThreads)
+            list[i] = (i & 31) < a.top ? __ldcg(reinterpret_cast<const unsigned long long*>(&parts[i >> 5].keys[i & 31])) : 0;
         // the segments' sums, two a lane at most, in a fixed order
         Sums mine_of[2];
         above = 0;
@@ -454,8 +461,6 @@ __global__ void __launch_bounds__(kThreads, 5)
         sums = warp_sums(mine_of[0]);
         above = __reduce_add_sync(~0u, above);
         if (a.top > 0) {
-            for (int i = tid; i < splits * 32; i += kThreads)
-                list[i] = (i & 31) < a.top ? __ldcg(reinterpret_cast<const unsigned long long*>(&parts[i >> 5].keys[i & 31])) : 0;
             __syncthreads();
             top = top32<true>(list, splits * 32, buffer);
         }
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 5)
 
 // The segments of a row, where there are too few rows to fill the GPU: twice as many CTAs as
 // SMs, but no segment below the vectors that a CTA's threads have on their way at once (8 x
-// 131072 bf16: 16 segments a row take 10.3 us, 38 took 15.3).
+// 131072 bf16: 16 segments a row took 10.3 us, 38 took 15.3).
 int row_splits(int sm_count, int rows, int vocab, int vector) {
     const int want = (2 * sm_count + rows - 1) / rows, most = vocab / (kThreads * kAhead * vector);
     int n = want < most ? want : most;
