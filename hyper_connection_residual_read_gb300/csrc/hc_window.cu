@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
 // codes as one word. A CTA takes the tokens of one tile for one head, key and value of a
 // token in the same lanes, both loads on their way before either is rounded. Every value is
 // read and written once, 16 bytes a lane, so that memory bounds long calls: 8191 tokens of 8
-// heads of 128 in bf16, written and read back, take 21.7 us for 85 MB, 3.9 TB/s. (Four
+// heads of 128 in fp16, written and read back, take 21.7 us for 85 MB, 3.9 TB/s. (Four
 // tokens a thread at once took 23.6 us, and min, max and codes one value at a time 25.3.) 32
 // tokens take 3.9 us for both launches.
 
