@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int group = a.q_heads / a.c.kv_heads;
 
+    begin_early();
     const Run run = find_run(a, &shared_run, sums, status);
     Walk k;
     if (!walk_start(a, run, k)) return;
@@ -750,9 +751,8 @@ cudaError_t launch_window(const Ctx& ctx, const AttentionArgs& a, cudaStream_t s
                          ((static_cast<int64_t>(a.width) * a.c.block_size + kUnit - 1) / kUnit);
     const int64_t resident = static_cast<int64_t>(ctx.sm_count) * (kNT == 1 ? kAttnCtasPerSm : 1);
     const int grid = static_cast<int>(most < resident ? most : resident);
-    window_kernel<kD, kDtype, kNT><<<grid, kThreads, Smem<kD, kNT>::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals,
-                                                                                  ctx.s.status);
-    return cudaGetLastError();
+    return launch_early(window_kernel<kD, kDtype, kNT>, dim3(grid), kThreads, Smem<kD, kNT>::kBytes, st, a, ctx.attn_pieces,
+                        ctx.attn_arrivals, ctx.s.status);
 }
 
 template <int kD, int kDtype>

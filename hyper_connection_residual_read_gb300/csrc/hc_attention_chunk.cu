@@ -289,6 +289,7 @@ __device__ __forceinline__ void scale_word(uint32_t (&h)[4], __half2 s, __half2 
 template <int kD, int kDtype, bool kSame>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
+    pdl_wait();                                // also before tensor memory is taken, which the kernel before may hold
     using S = Smem<kD>;
     constexpr bool same = kSame;
     // registers of a softmax thread and of a decoding one, 512 in all for two of each
@@ -1024,9 +1025,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kD, int kDtype, bool kSame>
 cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
-    chunk_kernel<kD, kDtype, kSame><<<ctx.sm_count, kThreads, Smem<kD>::kBytes, st>>>(a, ctx.attn_pieces, ctx.attn_arrivals,
-                                                                                      ctx.s.status);
-    return cudaGetLastError();
+    return launch_early(chunk_kernel<kD, kDtype, kSame>, dim3(ctx.sm_count), kThreads, Smem<kD>::kBytes, st, a, ctx.attn_pieces,
+                        ctx.attn_arrivals, ctx.s.status);
 }
 
 template <int kD, int kDtype>

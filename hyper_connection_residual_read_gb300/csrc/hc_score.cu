@@ -16,7 +16,7 @@
 // in the order of their indexes.
 //
 // Measured: 4096 x 131072 bf16 with the top 20, 200 us, 5.4 TB/s (79% of the copy rate): issue
-// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 9.7 us, 96 x 50257 fp32 12.2
+// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 9.3 us, 96 x 50257 fp32 12.1
 // us: half of that is the join of the segments and the choice of the top ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -218,6 +218,9 @@ __global__ void __launch_bounds__(kThreads, 5)
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         if (v0 + tid + i * kThreads < v1 && (lane & 7) == 0) prefetch_l2(vec + v0 + tid + i * kThreads);
+    // (without asking for the next kernel: its CTAs would lie unevenly over what the SMs have left,
+    // 96 rows 14.2 us against 12.1)
+    pdl_wait();
     const int id = a.ids[row];
     const bool known = id >= 0 && id < a.vocab;
     const float mine = known ? L::one(x, id) : CUDART_INF_F;
@@ -500,11 +503,10 @@ cudaError_t launch_logprobs(const Ctx& ctx, const LogprobArgs& a, int dtype, cud
     const int splits = row_splits(ctx.sm_count, a.tokens, a.vocab, dtype == HC_DTYPE_FP32 ? 4 : 8);
     const unsigned grid = static_cast<unsigned>(a.tokens) * splits;
     switch (dtype) {
-        case HC_DTYPE_BF16: score_kernel<HC_DTYPE_BF16><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals); break;
-        case HC_DTYPE_FP16: score_kernel<HC_DTYPE_FP16><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals); break;
-        default: score_kernel<HC_DTYPE_FP32><<<grid, kThreads, 0, st>>>(a, splits, ctx.score_parts, ctx.score_arrivals);
+        case HC_DTYPE_BF16: return launch_early(score_kernel<HC_DTYPE_BF16>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals);
+        case HC_DTYPE_FP16: return launch_early(score_kernel<HC_DTYPE_FP16>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals);
+        default: return launch_early(score_kernel<HC_DTYPE_FP32>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace hc

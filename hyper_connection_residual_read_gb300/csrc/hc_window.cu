@@ -42,6 +42,7 @@ __device__ __forceinline__ int count_le(const int* a, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, int* status) {
+    begin_early();
     extern __shared__ int smem[];
     const int n = a.requests, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int* s_cached = smem;                   // [n]
@@ -165,9 +166,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
 // codes as one word. A CTA takes the tokens of one tile for one head, key and value of a
 // token in the same lanes, both loads on their way before either is rounded. Every value is
 // read and written once, 16 bytes a lane, so that memory bounds long calls: 8191 tokens of 8
-// heads of 128 in fp16, written and read back, take 21.7 us for 85 MB, 3.9 TB/s. (Four
+// heads of 128 in fp16, written and read back, take 21.3 us for 85 MB, 4.0 TB/s. (Four
 // tokens a thread at once took 23.6 us, and min, max and codes one value at a time 25.3.) 32
-// tokens take 3.9 us for both launches.
+// tokens take 3.5 us for both launches.
 
 constexpr int kCacheThreads = 256;
 
@@ -341,6 +342,7 @@ __device__ __forceinline__ int64_t group_index(const hc_kv4_cache& c, int sh, in
 
 template <int kD, int kDtype>
 __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs a, int* status) {
+    begin_early();
     constexpr int kLanes = kD / 8, kTile = kCacheThreads / kLanes;
     const int sub = threadIdx.x % kLanes, head = blockIdx.y;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x / kLanes;
@@ -367,6 +369,7 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs a
 
 template <int kD, int kDtype>
 __global__ void __launch_bounds__(kCacheThreads) load_kernel(const CacheArgs a, int* status) {
+    begin_early();
     constexpr int kLanes = kD / 8, kTile = kCacheThreads / kLanes;
     const int sub = threadIdx.x % kLanes, head = blockIdx.y;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x / kLanes;
@@ -410,9 +413,8 @@ template <int kD, int kDtype>
 cudaError_t cache_call(const Ctx& ctx, const CacheArgs& a, bool append, cudaStream_t st) {
     constexpr int kTile = kCacheThreads / (kD / 8);
     const dim3 grid((a.tokens + kTile - 1) / kTile, a.c.kv_heads);
-    if (append) append_kernel<kD, kDtype><<<grid, kCacheThreads, 0, st>>>(a, ctx.s.status);
-    else load_kernel<kD, kDtype><<<grid, kCacheThreads, 0, st>>>(a, ctx.s.status);
-    return cudaGetLastError();
+    return append ? launch_early(append_kernel<kD, kDtype>, grid, kCacheThreads, 0, st, a, ctx.s.status)
+                  : launch_early(load_kernel<kD, kDtype>, grid, kCacheThreads, 0, st, a, ctx.s.status);
 }
 
 template <int kDtype>
@@ -438,8 +440,7 @@ cudaError_t window_setup() {
 cudaError_t launch_plan(const Ctx& ctx, const PlanArgs& a, cudaStream_t st) {
     const size_t smem = static_cast<size_t>(a.requests) * 13;
     const int grid = a.capacity > kPlanTokens ? (a.capacity + kPlanTokens - 1) / kPlanTokens : 1;
-    plan_kernel<<<grid, kPlanThreads, smem, st>>>(a, ctx.s.status);
-    return cudaGetLastError();
+    return launch_early(plan_kernel, dim3(grid), kPlanThreads, smem, st, a, ctx.s.status);
 }
 
 cudaError_t launch_kv4_append(const Ctx& ctx, const CacheArgs& a, int dtype, cudaStream_t st) {

@@ -120,6 +120,29 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
+// Launch with programmatic stream serialisation: the kernel's CTAs may be set up while the previous
+// kernel of the stream ends. Every thread begins with pdl_wait, before anything is read or
+// written, and most kernels then let the next one be set up. (Called one after the other on a
+// stream: 8191 tokens written and read back 26.6 -> 21.3 us, 8 rows scored 12.3 -> 9.0.)
+template <typename... KArgs, typename... Args>
+cudaError_t launch_early(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+__device__ __forceinline__ void begin_early() {
+    pdl_wait();
+    pdl_launch_dependents();
+}
+
 // Counts a block of the launch that has written its part; the count before it. One thread calls
 // it, behind a barrier that the writers have passed: release and acquire cover what the barrier
 // ordered, on both sides (a fence by every writer, and one by every reader, cost 0.3 us more).
