@@ -81,3 +81,55 @@ def test_a_request_without_blocks_waits():
     gained = d.accept(p, r["top_ids"], prompt=True)
     assert len(gained[0]) == 1 and gained[1] == [] and d.cached.tolist() == [90, 0]
     assert hc.hc_read_status() == hc.HC_OK
+
+
+def test_operators_called_one_after_the_other_wait_for_each_other():
+    """Each kernel is set up while the one before it runs: the results are those of calls
+    with a synchronisation between them, bit for bit."""
+    heads, dim, block, requests = 4, 128, 16, 6
+    ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    hc.hc_read_init(0, 512, 1e-6)
+
+    def run(pause):
+        wait = torch.cuda.synchronize if pause else (lambda: None)
+        gen = torch.Generator().manual_seed(5)
+        codes = torch.zeros((256, 2, heads, block, dim // 2), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros((256, 2, heads, block, 2), dtype=torch.bfloat16, device="cuda")
+        cached, table = ints(requests), ints(requests, 64)
+        free, count, left = torch.arange(256, dtype=torch.int32, device="cuda"), ints(1) + 256, ints(1)
+        cu, kv = ints(requests + 1), ints(requests)
+        results = []
+        for new in (40, 1, 8, 1, 33, 3, 1, 8):
+            total = new * requests
+            x = torch.randn((total, 4 * heads + 2 * heads, dim), generator=gen).bfloat16().cuda()
+            q, k, v = x.split([4 * heads, heads, heads], 1)
+            lens = ints(requests) + new
+            slots, at, pos = torch.empty(total, dtype=torch.int64, device="cuda"), ints(total), ints(total)
+            o, ko, vo = torch.empty_like(q.contiguous()), torch.empty_like(k.contiguous()), torch.empty_like(v.contiguous())
+            n = total * 4 * heads
+            f32 = [torch.empty(n, device="cuda") for _ in range(3)]
+            rank, ids, top = ints(n), ints(n, 3), torch.empty((n, 3), device="cuda")
+            token = (torch.arange(n, device="cuda") % dim).int()
+            wait()
+            hc.hc_window_plan(cached, lens, free, count, block, table, slots, at, pos, cu, kv, left)
+            wait()
+            hc.hc_kv4_append(k, v, slots, codes, scales)
+            wait()
+            hc.hc_kv4_attention(q, codes, scales, table, cu, kv, new, o)
+            wait()
+            hc.hc_kv4_load(slots, codes, scales, ko, vo)
+            wait()
+            hc.hc_token_logprobs(o.view(n, dim), token, *f32, rank, ids, top)
+            wait()
+            cached, kv, count, left = kv, cached, left, count
+            results += [o, ko, vo, slots, *f32, rank, ids, top]
+        torch.cuda.synchronize()
+        return results
+
+    first = run(False)
+    for _ in range(3):
+        for a, b in zip(run(True), first):
+            assert torch.equal(a, b)
+        for a, b in zip(run(False), first):
+            assert torch.equal(a, b)
+    assert hc.hc_read_status() == hc.HC_OK
