@@ -30,6 +30,11 @@ __device__ __forceinline__ int add_sat(int a, int b) {
     return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7FFFFFFFu));
 }
 
+// Blocks of 2^sh tokens that hold n >= 0 tokens (unsigned: n may be 2^31 - 1).
+__device__ __forceinline__ int blocks_of(int n, int sh) {
+    return static_cast<int>((static_cast<unsigned>(n) + (1u << sh) - 1u) >> sh);
+}
+
 // Number of entries of the ascending a[0..n) that are <= x.
 __device__ __forceinline__ int count_le(const int* a, int n, int x) {
     int lo = 0, hi = n;
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
     for (int i = blockIdx.x * kPlanThreads + tid; i < taken; i += gridDim.x * kPlanThreads) {
         const int b = count_le(s_want, n, i);
         const int j = i - (b ? s_want[b - 1] : 0);
-        const int have = (s_cached[b] + a.block_size - 1) >> sh;
+        const int have = blocks_of(s_cached[b], sh);
         const size_t at = static_cast<size_t>(b) * a.width + have + j;
         if (HC_IN_RANGE(at, 1, static_cast<size_t>(n) * a.width, status) &&
             HC_IN_RANGE(count - 1 - i, 1, a.free_capacity, status))
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
             request = b;
             pos = add_sat(c, t - (b ? s_cu[b - 1] : 0));
             if (s_granted[b]) {
-                const int at = pos >> sh, have = (c + a.block_size - 1) >> sh;
+                const int at = pos >> sh, have = blocks_of(c, sh);
                 const int rank = (b ? s_want[b - 1] : 0) + at - have;
                 int block = 0;
                 if (at >= have) {
