@@ -33,8 +33,12 @@ bool any_meet(const Span* s, int outs, int n) {
     return false;
 }
 
+// A grid's second axis is at most 65535, and a block's bytes fit 32 bits with as many heads.
+constexpr int kMaxHeads = 65535;
+
 int check_cache(const hc_kv4_cache* c, int device) {
-    if (c == nullptr || c->blocks < 1 || c->kv_heads < 1 || !known_block(c->block_size)) return HC_ERR_ARG;
+    if (c == nullptr || c->blocks < 1 || c->kv_heads < 1 || c->kv_heads > kMaxHeads || !known_block(c->block_size))
+        return HC_ERR_ARG;
     if (c->head_dim != 64 && c->head_dim != 128) return HC_ERR_ARG;
     if (int e = check_ptr(c->codes, device)) return e;
     return check_ptr(c->scales, device);

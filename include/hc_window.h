@@ -70,7 +70,8 @@ enum hc_dtype {
 #define HC_KV4_MAX_MASKED 64
 #define HC_LOGPROBS_MAX_TOP 32
 
-/* One layer's cache. block_size: 16, 32, 64, 128 or 256; head_dim: 64 or 128. */
+/* One layer's cache. block_size: 16, 32, 64, 128 or 256; head_dim: 64 or 128; kv_heads: at
+ * most 65535. */
 typedef struct hc_kv4_cache {
     uint8_t* codes;
     uint16_t* scales;

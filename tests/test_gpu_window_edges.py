@@ -45,3 +45,28 @@ def test_plan_of_lengths_next_to_the_largest(cached, new):
     for name, x, y in zip(("table", "slots", "request_of", "positions", "cu", "kv", "left"), got, want):
         assert np.array_equal(x, y), name
     assert got[5].tolist() == [cached + new]
+
+
+# ---------------------------------------------------------------------------
+# arguments
+# ---------------------------------------------------------------------------
+
+def test_more_kv_heads_than_a_launch_has_room_for_are_refused():
+    heads = 65536
+    codes = torch.zeros((1, 2, heads, 16, 32), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((1, 2, heads, 16, 2), dtype=torch.bfloat16, device="cuda")
+    k, slots = torch.ones((1, heads, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    for call in (lambda: hc.hc_kv4_append(k, k, slots, codes, scales),
+                 lambda: hc.hc_kv4_load(slots, codes, scales, torch.empty_like(k), torch.empty_like(k)),
+                 lambda: hc.hc_kv4_attention(k, codes, scales, i32([[0]]), i32([0, 1]), i32([1]), 1, torch.empty_like(k))):
+        with pytest.raises(hc.HcReadError) as e:
+            call()
+        assert e.value.code == hc.HC_ERR_ARG
+    fewer = heads - 1
+    codes, scales, k = codes[:, :, :fewer].contiguous(), scales[:, :, :fewer].contiguous(), k[:, :fewer].contiguous()
+    hc.hc_kv4_append(k, k, slots, codes, scales)
+    o, p = torch.empty_like(k), torch.empty_like(k)
+    hc.hc_kv4_load(slots, codes, scales, o, p)
+    assert torch.equal(o, k) and torch.equal(p, k)
+    hc.hc_kv4_attention(k, codes, scales, i32([[0]]), i32([0, 1]), i32([1]), 1, o)
+    assert torch.equal(o, k)
