@@ -96,7 +96,7 @@ struct Walk {
 };
 
 __device__ __forceinline__ int window_units(const Window& w) {
-    return w.n > 0 ? max((w.kv + kUnit - 1) / kUnit, 1) : 0;
+    return w.n > 0 ? max((w.kv - 1) / kUnit + 1, 1) : 0;     // (kv may be 2^31 - 1)
 }
 __device__ __forceinline__ int64_t window_slots(const AttentionArgs& a, const Window& w, int cost) {
     const int units = window_units(w);
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             __syncwarp();                                    // every lane's copies, and its reads of the slot before
             fetch(k, u + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
             look_up(k, u + kStages);
-            if (t + kStep <= clear) step(std::false_type(), u);
+            if (t <= clear - kStep) step(std::false_type(), u);
             else step(std::true_type(), u);
             if (++slot == kStages) slot = 0;
         }

@@ -98,7 +98,7 @@ __device__ __forceinline__ int row_tiles(const Window& w, int group, int step) {
 __device__ __forceinline__ int key_tiles(const AttentionArgs& a, const Window& w, int group, int step, int i) {
     const int last = min(((i + 1) * step - 1) / group, w.rows - 1);
     const int seen = a.mask ? w.kv : min(w.kv, w.first + last + 1);
-    return max((seen + kTile - 1) / kTile, 1);
+    return max((seen - 1) / kTile + 1, 1);     // (seen may be 2^31 - 1)
 }
 __device__ __forceinline__ int64_t head_slots(const AttentionArgs& a, const Window& w, int group, int step) {
     int64_t n = 0;
@@ -489,10 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float f = factor * col.up[0] * col.up[1];
                 // hidden keys: behind the end, or behind this row's token, or out of its mask
                 const int t = j * kTile;
-                const bool tail = t + kTile > clear;
+                const bool tail = t > clear - kTile;
                 float fix = 1.f, peak = -CUDART_INF_F;
                 const uint64_t f2 = pair(f, f);
-                uint64_t sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
+                // of this tile alone: sums of millions of keys would not notice one key's weight
+                uint64_t sum2 = 0, flat2 = 0;
                 bool quick = !tail && !__any_sync(~0u, fresh);
                 if (quick) {
                     // Weights against the maximum so far, 32 keys at a time, two to an instruction,
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     peak = 0.f;
                     const uint64_t b2 = pair(-base, -base);
-                    sum2 = pair(sum, 0.f), flat2 = pair(flat, 0.f);
+                    sum2 = flat2 = 0;
 #pragma unroll 1
                     for (int n = 0; n < 4; ++n) {
                         uint32_t raw[32];
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 {
                     const float2 s2 = unpair(sum2), l2 = unpair(flat2);
-                    sum = s2.x + s2.y, flat = l2.x + l2.y;
+                    sum += s2.x + s2.y, flat += l2.x + l2.y;
                 }
                 fix *= later, later = 1.f;
                 if (done_tiles == 0) {
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned char* codes = a.c.codes + first * (kD / 2) + (is_v ? vd / 2 : seg * 16);
             const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.c.scales) + first;
             auto look_up = [&](int j) {
-                const int t = max(min(j * kTile + lane * 16, k.w.kv - 1), 0);
+                const unsigned t = min(static_cast<unsigned>(j) * kTile + lane * 16, static_cast<unsigned>(max(k.w.kv - 1, 0)));
                 ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
             };
             uint64_t parts, parts_next = 0;                     // bytes from `codes` to those of lane's part
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ids = 0;                                    // wrong values, from the cache's own memory
                 }
                 return static_cast<uint64_t>(static_cast<uint32_t>(ids)) * block_bytes +
-                       static_cast<uint32_t>(((j * kTile + lane * 16) & in_block) * (kD / 2));
+                       ((static_cast<unsigned>(j) * kTile + lane * 16) & in_block) * (kD / 2);
             };
             // bytes from `codes` to those of token `x` of that tile
             auto place = [&](uint64_t parts, int x) -> uint64_t {
@@ -896,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             look_up(k.t0);
             parts = check(k.t0);
             scale = load_scale(parts);
-            auto seen = [&](int j, uint32_t scale) { return j * kTile + p < k.w.kv ? scale : 0u; };
+            auto seen = [&](int j, uint32_t scale) { return static_cast<unsigned>(j) * kTile + p < static_cast<unsigned>(k.w.kv) ? scale : 0u; };
             if (is_v) {
                 load_values();
             } else {

@@ -47,6 +47,43 @@ def test_plan_of_lengths_next_to_the_largest(cached, new):
     assert got[5].tolist() == [cached + new]
 
 
+@pytest.mark.parametrize("q_heads,new", [(8, 1), (4, 3), (1, 40)])
+def test_attention_over_lengths_next_to_the_largest(q_heads, new):
+    """2^31 - 1 tokens: all pages but the last are one block, and the last one's keys have
+    logits that make up for their number; the slot behind the end is NaN. A lane sums up to
+    2^17 terms or tiles in fp32, 2^-8 relative at worst: so much of lse, and of values 4
+    apart twice that, and half an ulp of bf16 below 8."""
+    d, block, width, kv = 64, 256, 1 << 23, 2 ** 31 - 1
+    g = np.random.default_rng(3)
+    codes = g.integers(0, 256, (2, 2, 1, block, d // 2)).astype(np.uint8)
+    step = np.full((2, 2, 1, block), 0.125)
+    low = np.full(step.shape, -0.9375)
+    low[1, 0] += 2.0                                    # sum(q) is near 64: exp(16) times as much weight a key
+    low[1, 1] += 4.0
+    q = torch.from_numpy(1 + 0.15 * g.standard_normal((new, q_heads, d))).bfloat16()
+    scales = torch.from_numpy(np.stack([step, low], -1)).bfloat16().cuda()
+    scales[1, :, :, 255] = float("nan")
+    table = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    out = torch.zeros_like(q).cuda()
+    lse = torch.zeros((new, q_heads), device="cuda")
+    hc.hc_kv4_attention(q.cuda(), torch.from_numpy(codes).cuda(), scales, table, i32([0, new]), i32([kv]), new, out, lse=lse)
+    assert hc.hc_read_status() == hc.HC_OK
+    value = low[..., None] + step[..., None] * W.unpack(codes)              # [block][kv][1][token][d]
+    x = np.einsum("nhd,btd->nhbt", q.double().numpy(), value[:, 0, 0]) / 8
+    times = np.ones((new, 2, block))
+    times[:, 0] = width - 1
+    for i in range(new):
+        times[i, 1, 255 - new + i + 1:] = 0
+    p = np.exp(x) * times[:, None]
+    part = p[:, :, 1].sum(-1) / p.sum((-1, -2))
+    assert 0.05 < part.min() and part.max() < 0.95, "the last page matters, and not alone"
+    want_lse = np.log(p.sum((-1, -2)))
+    want = np.einsum("nhbt,btd->nhd", p, value[:, 1, 0]) / p.sum((-1, -2))[..., None]
+    assert np.abs(lse.double().cpu().numpy() - want_lse).max() <= 2.0 ** -8
+    assert np.abs(out.double().cpu().numpy() - want).max() <= 2 * 4 * 2.0 ** -8 + 2.0 ** -6
+
+
 # ---------------------------------------------------------------------------
 # arguments
 # ---------------------------------------------------------------------------
