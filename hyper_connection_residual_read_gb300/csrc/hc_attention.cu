@@ -612,12 +612,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                top[nt][e] = (fresh >> (2 * nt + e)) & 1 ? -CUDART_INF_F : base[nt][e];
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     sum[nt][e] += __shfl_xor_sync(~0u, sum[nt][e], d);
                     flat[nt][e] += __shfl_xor_sync(~0u, flat[nt][e], d);
                 }
+                // a row that has seen nothing but NaN has no maximum, but its sum has to be told
+                top[nt][e] = ((fresh >> (2 * nt + e)) & 1) && sum[nt][e] == sum[nt][e] ? -CUDART_INF_F : base[nt][e];
                 if (g == 0) {
                     s_max[warp * kRows + nt * 8 + 2 * tq + e] = top[nt][e];
                     s_sum[warp * kRows + nt * 8 + 2 * tq + e] = sum[nt][e];

@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tc_fence_after();
             }
             o_phase += done_tiles;
-            if (fresh) base = -CUDART_INF_F;
+            if (fresh && sum == sum) base = -CUDART_INF_F;     // (a sum of NaN alone has to be told, about 0)
             const bool whole = k.t0 == 0 && k.t1 == k.tiles;
             float other_base = -CUDART_INF_F, other_sum = 0.f;
             float* exchange = reinterpret_cast<float*>(smem + S::kQ);          // [kD][128], both row tiles' room

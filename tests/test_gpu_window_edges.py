@@ -85,6 +85,139 @@ def test_attention_over_lengths_next_to_the_largest(q_heads, new):
 
 
 # ---------------------------------------------------------------------------
+# attention: values
+# ---------------------------------------------------------------------------
+
+class Cache:
+    """Requests of (cached + new, new) tokens in a shuffled pool, from given steps and minima."""
+
+    def __init__(self, seed, lens, kv_heads, dim, block=16, spread=0.3):
+        g = np.random.default_rng(seed)
+        self.lens, self.block, self.dim = lens, block, dim
+        have = [-(-kv // block) for kv, _ in lens]
+        order, at = g.permutation(sum(have) + 1), 0
+        self.table = np.full((len(lens), max(1, max(have))), -1)
+        for b, n in enumerate(have):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        shape = (sum(have) + 1, 2, kv_heads, block)
+        self.codes = g.integers(0, 256, (*shape, dim // 2)).astype(np.uint8)
+        step = 0.25 * np.exp(spread * g.standard_normal(shape))
+        self.scales = np.stack([step, -7.5 * step + 0.2 * g.standard_normal(shape)], -1)
+        self.cu = np.concatenate([[0], np.cumsum([n for _, n in lens])])
+        self.kv = np.array([kv for kv, _ in lens])
+
+    def set(self, request, position, kind, head, step, low):
+        """The group of a token: kind 0 its key, 1 its value."""
+        at = self.table[request, position // self.block], kind, head, position % self.block
+        self.scales[at] = step, low
+
+    def run(self, q, mask=None, scale=None):
+        """out and lse in float64."""
+        out = torch.full(q.shape, 55.0, dtype=q.dtype, device="cuda")
+        lse = torch.full(q.shape[:2], 55.0, device="cuda")
+        bits = None if mask is None else torch.from_numpy(np.array(mask, dtype=np.uint64).view(np.int64)).cuda()
+        hc.hc_kv4_attention(q.cuda(), torch.from_numpy(self.codes).cuda(), torch.from_numpy(self.scales).bfloat16().cuda(),
+                            i32(self.table), i32(self.cu), i32(self.kv), max(n for _, n in self.lens), out, lse=lse, mask=bits,
+                            scale=scale)
+        assert hc.hc_read_status() == hc.HC_OK
+        return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+    def queries(self, heads, dtype=torch.bfloat16, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        return torch.randn(int(self.cu[-1]), heads, self.dim, generator=g).to(dtype)
+
+
+def expect(c, q, mask=None, scale=None):
+    """In 64 bits, request by request: out, lse, and what each may be off by. out: half an
+    ulp of its type; 2^-10 of sum p (|s (c - 8)| + |m + 8 s|), as each weight is rounded to
+    11 bits and carries its exponent's error; and for weights below 16 bits' range, of
+    every key, 2^-22 of the largest p s. lse: 2^-19 of 1 + the largest sum of a logit's
+    terms. All of it of the keys that the row sees, and of no others."""
+    scale = c.dim ** -0.5 if scale is None else scale
+    bits = torch.from_numpy(c.scales).bfloat16().double().numpy()
+    half = 2.0 ** (-8 if q.dtype == torch.bfloat16 else -11)
+    heads, x = q.shape[1], q.double().numpy()
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    lse, lse_tol = np.full(q.shape[:2], -np.inf), np.zeros(q.shape[:2])
+    for b, (kv, new) in enumerate(c.lens):
+        if not kv:
+            continue
+        at = np.arange(kv)
+        page, off = c.table[b][at // c.block], at % c.block
+        code = W.unpack(c.codes[page, :, :, off]).astype(np.float64)                 # [kv][2][h][d]
+        s, m = (bits[page, :, :, off][..., i:i + 1] for i in (0, 1))
+        value, terms = m + s * code, np.abs(s * (code - 8)) + np.abs(m + 8 * s)
+        rows = slice(c.cu[b], c.cu[b + 1])
+        if mask is None:
+            sees = at[None] <= (kv - new + np.arange(new))[:, None]
+        else:
+            back = at - (kv - new)
+            sees = (back < 0)[None] | (((np.array(mask[rows], dtype=object)[:, None] >> np.maximum(back, 0)[None]) & 1) == 1)
+        for h in range(heads):
+            g = h // (heads // value.shape[2])
+            z = np.where(sees, scale * (x[rows, h] @ value[:, 0, g].T), -np.inf)
+            size = np.where(sees, abs(scale) * (np.abs(x[rows, h]) @ terms[:, 0, g].T), 0.0)
+            top = z.max(-1, keepdims=True)
+            p = np.where(sees, np.exp(z - np.where(np.isfinite(top), top, 0)), 0.0)
+            total = p.sum(-1, keepdims=True)
+            with np.errstate(divide="ignore", invalid="ignore"):
+                lse[rows, h] = (top + np.log(total))[:, 0]
+                p = p / np.where(total > 0, total, 1)
+            out[rows, h] = np.where(p > 0, p, 0) @ value[:, 1, g]
+            tol[rows, h] = half * np.abs(out[rows, h]) + 2.0 ** -10 * (p @ terms[:, 1, g]) + \
+                2.0 ** -22 * kv * (p * s[:, 1, g, 0]).max(-1, keepdims=True) + 1e-30
+            lse_tol[rows, h] = 2.0 ** -19 * (1 + size.max(-1))
+            if kv > 1:
+                second = np.partition(z, -2, axis=-1)[:, -2]
+                with np.errstate(invalid="ignore"):
+                    gap = np.where(np.isfinite(second), top[:, 0] - second, np.inf)
+                    other = np.minimum(1.0, kv * np.exp(np.minimum(2 * lse_tol[rows, h] - gap, 0)))
+                tol[rows, h] += np.where(lse_tol[rows, h] > 2.0 ** -9, other * 2 * np.abs(value[:, 1, g]).max(), 0)[:, None]
+    return out, lse, tol, lse_tol
+
+
+def agrees(c, q, mask=None, scale=None, rows=None):
+    """The rows (all of them) of a call with what `expect` says."""
+    out, lse = c.run(q, mask, scale)
+    want, want_lse, tol, lse_tol = expect(c, q, mask, scale)
+    rows = np.ones(lse.shape, dtype=bool) if rows is None else rows
+    # what q's type cannot hold is an infinity of the same sign
+    beyond = (np.abs(want) + tol >= torch.finfo(q.dtype).max) & (out == np.sign(want) * np.inf)
+    with np.errstate(invalid="ignore"):
+        off, lse_off = np.where(beyond, 0, np.abs(out - want))[rows], np.abs(lse - want_lse)[rows & np.isfinite(want_lse)]
+    assert np.array_equal(np.isneginf(lse[rows]), np.isneginf(want_lse[rows]))
+    assert (off <= tol[rows]).all(), ("out", (off / tol[rows]).max())
+    assert (lse_off <= lse_tol[rows & np.isfinite(want_lse)]).all(), ("lse", (lse_off / lse_tol[rows & np.isfinite(want_lse)]).max())
+
+
+# query heads on one kv head, new tokens: each form of the two kernels (8 and 16 rows; 128
+# rows, and more)
+FORMS = [(4, 1), (3, 2), (5, 3), (4, 4), (10, 4), (2, 150)]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,new", FORMS)
+@pytest.mark.parametrize("kv", [1, 33, 700, 20000])
+def test_attention_that_sees_nothing_but_nan_is_nan(q_heads, new, dim, kv):
+    """Keys held as NaN alone; and queries that are NaN, beside rows that are not."""
+    new = min(new, kv)
+    c = Cache(1, [(kv, new), (50, new)], 1, dim)
+    c.set(0, np.arange(kv), 0, 0, np.nan, np.nan)
+    out, lse = c.run(c.queries(q_heads))
+    assert np.isnan(out[:new]).all() and np.isnan(lse[:new]).all()
+    assert not np.isnan(out[new:]).any() and not np.isnan(lse[new:]).any()
+    c = Cache(2, [(kv, new), (50, new)], 1, dim)
+    q = c.queries(q_heads)
+    q[0, 0, 3] = q[-1, q_heads - 1, 0] = float("nan")
+    out, lse = c.run(q)
+    bad = np.zeros(lse.shape, dtype=bool)
+    bad[0, 0] = bad[-1, q_heads - 1] = True
+    assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
+    agrees(c, q, rows=~bad)
+
+
+# ---------------------------------------------------------------------------
 # arguments
 # ---------------------------------------------------------------------------
 
