@@ -16,9 +16,10 @@
 //   product in fp32, once a token and row instead of once a value. Likewise o = sum w_j
 //   (c_j - 8) + sum p_j (m_j + 8 s_j) with w_j = p_j s_j. w_j is rounded to fp16 (11 bits:
 //   the one rounding of the product), after division by a power of two near the largest
-//   step seen; p_j itself is summed in fp32. 8 sum w_j comes from the same rounded
-//   weights, by one more product with a constant, so that their errors meet c_j - 8 and
-//   not c_j, which is three times as large.
+//   w_j that its row has seen (so that neither a step of a key that the row does not see nor
+//   one of next to no weight costs the others their bits); p_j itself is summed in fp32. 8 sum
+//   w_j comes from the same rounded weights, by one more product with a constant, so that
+//   their errors meet c_j - 8 and not c_j, which is three times as large.
 // * The order of dimensions within a product is free as long as both operands agree, and
 //   so is that of the tokens: both follow from which words a lane loads (16 bytes of a
 //   key row, 8 of a value row), so that no value moves between lanes. Only the weights
@@ -55,7 +56,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                        // tokens of a warp's step
 constexpr int kUnit = kWarps * kStep;            // tokens of a unit
 constexpr float kRaise = 8.f;                    // log2 by which a logit may pass the maximum
-constexpr float kStepRoom = 16.f;                // factor by which a step may pass the reference
+constexpr float kRoom = 32768.f;                 // by how much a weight times its step may pass their reference: fp16's range
 
 constexpr int kStages = 3;                       // steps of a warp's ring
 constexpr int kPieceCost = 4;                    // what a piece costs beside its units, in units (64 ragged requests:
@@ -271,39 +272,52 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 
     begin_early();
     const Run run = find_run(a, &shared_run, sums, status);
-    Walk k;
-    if (!walk_start(a, run, k)) return;
+    // The walk, a copy a warp, kept here and not in registers, which the loop over the steps has
+    // none to spare of.
+    __shared__ Walk walks[kWarps];
+    Walk& k = walks[warp];
+    auto keep = [&](const Walk& next) {
+        __syncwarp();
+        if (lane == 0) k = next;
+        __syncwarp();
+    };
+    {
+        Walk first;
+        if (!walk_start(a, run, first)) return;
+        keep(first);
+    }
 
     uint32_t* my_q = reinterpret_cast<uint32_t*>(smem + S::kQueries) + warp * (kNT * 8 * kD / 2);
     float* s_max = reinterpret_cast<float*>(smem + S::kStats);
     float* s_sum = s_max + kWarps * kRows;
     const int sh = 31 - __clz(a.c.block_size);
-    const int64_t to_values = static_cast<int64_t>(a.c.kv_heads) * a.c.block_size;   // groups from keys to values
+    const uint32_t to_values = static_cast<uint32_t>(a.c.kv_heads) * a.c.block_size;   // groups from keys to values
     const unsigned char* ring = smem + warp * (kStages * L::kBytes);
-            // Copies: lanes 0-15 bring the first 16 tokens of the warp's step, lanes 16-31 the others, 16
+    // Copies: lanes 0-15 bring the first 16 tokens of the warp's step, lanes 16-31 the others, 16
     // bytes a lane and copy; four lanes of each half the keys' scales and four the values'.
     const int half = lane >> 4, l16 = lane & 15;
-    const uint32_t block_bytes = static_cast<uint32_t>(2 * to_values * (kD / 2));
+    const uint32_t block_bytes = 2 * to_values * (kD / 2);
     const uint32_t put = tc::smem_u32(ring) + half * (L::kCodes / 2) + l16 * 16;
     const uint32_t put_scales = tc::smem_u32(ring) + 2 * L::kCodes + (l16 >> 2) * L::kScales + half * (L::kScales / 2) + (l16 & 3) * 16;
-    const unsigned char* my_codes = a.c.codes + l16 * 16;
-    const unsigned char* my_scales = reinterpret_cast<const unsigned char*>(a.c.scales) + (l16 >> 2) * to_values * 4 + (l16 & 3) * 16;
     int id = 0;                              // the block of this lane's half of the step to be copied next
-    auto look_up = [&](const Walk& k, int u) {
-        const int t = u * kUnit + warp * kStep + half * 16;
-        if (u < k.u1 && t < k.w.kv) id = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
+    int u1, kv;                              // of the piece whose steps are copied
+    const int32_t* pages;
+    const unsigned char* head_codes;
+    const unsigned char* head_scales;
+    auto look_up = [&](int u) {
+        const unsigned t = static_cast<unsigned>(u) * kUnit + warp * kStep + half * 16;
+        if (u < u1 && t < static_cast<unsigned>(kv)) id = pages[t >> sh];
     };
     // brings the step of unit u to a slot of the ring (a group of copies, if an empty one)
-    auto fetch = [&](const Walk& k, int u, int slot) {
-        const int t = u * kUnit + warp * kStep + half * 16;
-        if (u < k.u1 && t < k.w.kv) {
+    auto fetch = [&](int u, int slot) {
+        const unsigned t = static_cast<unsigned>(u) * kUnit + warp * kStep + half * 16;
+        if (u < u1 && t < static_cast<unsigned>(kv)) {
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.c.blocks)) {
                 atomicOr(status, kStatusBounds);
                 id = 0;                      // wrong values, from the cache's own memory
             }
-            const uint32_t within = (k.h * a.c.block_size + (t & (a.c.block_size - 1))) * (kD / 2);
-            const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes + within;
-            const unsigned char* keys = my_codes + at;
+            const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes + (t & (a.c.block_size - 1)) * (kD / 2);
+            const unsigned char* keys = head_codes + at;
             const unsigned char* values = keys + to_values * (kD / 2);
             const uint32_t to = put + slot * L::kBytes;
 #pragma unroll
@@ -311,20 +325,25 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 copy16(to + i * 256, keys + i * 256);
                 copy16(to + L::kCodes + i * 256, values + i * 256);
             }
-            if (l16 < 8) copy16(put_scales + slot * L::kBytes, my_scales + at / (kD / 8));
+            if (l16 < 8) copy16(put_scales + slot * L::kBytes, head_scales + at / (kD / 8));
         }
         copy_commit();
     };
     // a piece's first steps, on their way before the piece before it is merged
-    auto begin = [&](const Walk& k) {
+    auto begin = [&]() {
+        u1 = k.u1, kv = k.w.kv;
+        pages = a.table + static_cast<int64_t>(k.b) * a.width;
+        head_codes = a.c.codes + l16 * 16 + static_cast<int64_t>(k.h) * a.c.block_size * (kD / 2);
+        head_scales = reinterpret_cast<const unsigned char*>(a.c.scales) + static_cast<int64_t>((l16 >> 2) * to_values + k.h * a.c.block_size) * 4 + (l16 & 3) * 16;
+        const int u0 = k.u0;
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            look_up(k, k.u0 + i);
-            fetch(k, k.u0 + i, i);
+            look_up(u0 + i);
+            fetch(u0 + i, i);
         }
-        look_up(k, k.u0 + kStages - 1);
+        look_up(u0 + kStages - 1);
     };
-    begin(k);
+    begin();
     bool more = true;
     while (more) {
         int slot = 0;
@@ -394,12 +413,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 
         float o[kVW * 4][kNT][4] = {}, eight[kNT][4] = {};   // and 8 times the sum of the weights
         float base[kNT][2], sum[kNT][2], flat[kNT][2];     // maximum, sum of p, sum of p (m + 8 s)
+        float down[kNT][2];                                 // 2^-E of a row's largest weight times step; E is -126 at first
         uint32_t fresh = (1u << (2 * kNT)) - 1;            // rows of this lane without a maximum (base is 0)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) base[nt][e] = 0.f, sum[nt][e] = 0.f, flat[nt][e] = 0.f;
-        float vdown = 0.f;                                  // 2^-E of the value steps; 0: none seen
+            for (int e = 0; e < 2; ++e)
+                base[nt][e] = 0.f, sum[nt][e] = 0.f, flat[nt][e] = 0.f, down[nt][e] = power_of_two(126);
         const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1);   // every row sees what lies before
 
         // One step. kTail: some of its tokens are hidden from some rows, or lie behind the end.
@@ -449,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             }
             // logits in powers of two, less the maximum so far
             float vs[4], vm[4];
-            float vtop = 0.f;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {                    // tokens g, g + 8 of both tiles
                 const int j = x * 8 + tile_token(g);
@@ -458,14 +477,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 const float sf = bf16_lo(kk) * (factor * kCodeUp), off = bf16_hi(kk) * factor;
                 vs[x] = bf16_lo(vv);
                 vm[x] = fmaf(8.f, vs[x], bf16_hi(vv));
-                vtop = fmaxf(vtop, vs[x]);
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& z = s[x >> 1][nt][(x & 1) * 2 + e];
-                        z = fmaf(sf, z, fmaf(off, qsum[nt][e], -base[nt][e]));
-                    }
+                for (int nt = 0; nt < kNT; ++nt) {
+                    float& z0 = s[x >> 1][nt][(x & 1) * 2];
+                    float& z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
+                    const float2 z = unpair(fma2(pair(sf, sf), pair(z0, z1), fma2(pair(off, off), pair(qsum[nt][0], qsum[nt][1]), pair(-base[nt][0], -base[nt][1]))));
+                    z0 = z.x, z1 = z.y;
+                }
             }
             if (kTail) {
 #pragma unroll
@@ -483,71 +501,100 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                         }
                     }
             }
-            // raise the maximum, or the reference of the value steps, where they are passed
-            bool raise = vtop * vdown > kStepRoom || (vdown == 0.f && vtop > 0.f) || fresh != 0;
+            // weights p, and p times step in fp16
+            float p[4][kNT][2];
+            uint32_t w[4][kNT];
+            auto weigh = [&]() {
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float z0 = s[x >> 1][nt][(x & 1) * 2], z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
+                        const float p0 = p[x][nt][0] = exp2_fast(z0), p1 = p[x][nt][1] = exp2_fast(z1);
+                        // (in this order: a step may be as far above the reference as its weight is small)
+                        float2 y = unpair(mul2(mul2(pair(p0, p1), pair(vs[x], vs[x])), pair(down[nt][0], down[nt][1])));
+                        if (kTail) {                         // a hidden value may be NaN
+                            if (z0 == -CUDART_INF_F) y.x = 0.f;
+                            if (z1 == -CUDART_INF_F) y.y = 0.f;
+                        }
+                        w[x][nt] = pack_half2(y.x, y.y);
+                    }
+            };
+            weigh();
+            // raise the maximum, or the reference of weights times steps, where they are passed
+            bool raise = fresh != 0;
             float peak[kNT][2];
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt) {
+                const __half2* y = reinterpret_cast<const __half2*>(w[0]) + nt;
+                const __half2 most = __hmax2(__hmax2(y[0], y[kNT]), __hmax2(y[2 * kNT], y[3 * kNT]));
+                raise |= !__hble2(most, __float2half2_rn(kRoom));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     peak[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
                     raise |= peak[nt][e] > kRaise;
                 }
+            }
             if (__any_sync(~0u, raise)) {
-                uint32_t vbits = __reduce_max_sync(~0u, __float_as_uint(vtop));
-                const float was = vdown;
-                vbits &= 0x7F800000u;
-                float now = vbits ? __uint_as_float(0x7F000000u - vbits) : 0.f;
-                if (was != 0.f && (now == 0.f || now > was)) now = was;
-                vdown = now;
-                const float vfix = was == 0.f ? 1.f : now / was;
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float p = peak[nt][e];
-                        p = fmaxf(p, __shfl_xor_sync(~0u, p, 4));
-                        p = fmaxf(p, __shfl_xor_sync(~0u, p, 8));
-                        p = fmaxf(p, __shfl_xor_sync(~0u, p, 16));
+                        float top = peak[nt][e];
+                        top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
                         // by how much the maximum rises (of a fresh row: to the first logit seen)
                         const uint32_t bit = 1u << (2 * nt + e);
                         const bool first = (fresh & bit) != 0;
-                        const float up = first ? (p == -CUDART_INF_F ? 0.f : p) : fmaxf(p, 0.f);
-                        if (first && p != -CUDART_INF_F) fresh &= ~bit;
+                        const float up = first ? (top == -CUDART_INF_F ? 0.f : top) : fmaxf(top, 0.f);
+                        if (first && top != -CUDART_INF_F) fresh &= ~bit;
                         const float fix = first ? 1.f : exp2_fast(-up);
                         base[nt][e] += up;
 #pragma unroll
                         for (int x = 0; x < 4; ++x) s[x >> 1][nt][(x & 1) * 2 + e] -= up;
                         sum[nt][e] *= fix;
                         flat[nt][e] *= fix;
-                        eight[nt][e] *= fix * vfix;
+                        // the largest weight times step: of this step's (hidden ones are 0 or NaN), and
+                        // of those before, which the maximum has made smaller
+                        float most = 0.f;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) most = fmaxf(most, exp2_fast(s[x >> 1][nt][(x & 1) * 2 + e]) * vs[x]);
+                        most = fmaxf(most, __shfl_xor_sync(~0u, most, 4));
+                        most = fmaxf(most, __shfl_xor_sync(~0u, most, 8));
+                        most = fmaxf(most, __shfl_xor_sync(~0u, most, 16));
+                        const int was = 127 - static_cast<int>(__float_as_uint(down[nt][e]) >> 23);
+                        most = fmaxf(most, fix * power_of_two(was));
+                        const int now = max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -126);
+                        down[nt][e] = power_of_two(-now);
+                        // (in two factors: each alone is within fp32 where their product is)
+                        const int half = (was - now) / 2;
+                        const float by = fix * power_of_two(half) * power_of_two(was - now - half);
+                        eight[nt][e] *= by;
 #pragma unroll
                         for (int m = 0; m < kVW * 4; ++m) {
-                            o[m][nt][e] *= fix * vfix;
-                            o[m][nt][2 + e] *= fix * vfix;
+                            o[m][nt][e] *= by;
+                            o[m][nt][2 + e] *= by;
                         }
                     }
+                weigh();
             }
-            // weights
             uint32_t pw[2][kNT][2];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) vs[x] *= vdown;
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float z0 = s[x >> 1][nt][(x & 1) * 2], z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
-                    const float p0 = exp2_fast(z0), p1 = exp2_fast(z1);
-                    float w0 = p0 * vs[x], w1 = p1 * vs[x], m0 = vm[x], m1 = vm[x];
-                    if (kTail) {                             // a hidden value may be NaN
-                        if (z0 == -CUDART_INF_F) w0 = m0 = 0.f;
-                        if (z1 == -CUDART_INF_F) w1 = m1 = 0.f;
+                    float m0 = vm[x], m1 = vm[x];
+                    if (kTail) {
+                        if (s[x >> 1][nt][(x & 1) * 2] == -CUDART_INF_F) m0 = 0.f;
+                        if (s[x >> 1][nt][(x & 1) * 2 + 1] == -CUDART_INF_F) m1 = 0.f;
                     }
-                    sum[nt][0] += p0, sum[nt][1] += p1;
-                    flat[nt][0] = fmaf(p0, m0, flat[nt][0]), flat[nt][1] = fmaf(p1, m1, flat[nt][1]);
-                    pw[x >> 1][nt][x & 1] = transpose8x8(pack_half2(w0, w1));
+                    const uint64_t p2 = pair(p[x][nt][0], p[x][nt][1]);
+                    const float2 s2 = unpair(add2(pair(sum[nt][0], sum[nt][1]), p2));
+                    const float2 f2 = unpair(fma2(p2, pair(m0, m1), pair(flat[nt][0], flat[nt][1])));
+                    sum[nt][0] = s2.x, sum[nt][1] = s2.y, flat[nt][0] = f2.x, flat[nt][1] = f2.y;
+                    pw[x >> 1][nt][x & 1] = transpose8x8(w[x][nt]);
                 }
-            }
             // second product
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
@@ -581,13 +628,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     }
             }
         };
-        for (int u = k.u0; u < k.u1; ++u) {
+        for (int u = k.u0; u < u1; ++u) {
             const int t = u * kUnit + warp * kStep;
-            if (t >= k.w.kv) break;
+            if (t >= kv) break;
             copy_wait<kStages - 2>();
             __syncwarp();                                    // every lane's copies, and its reads of the slot before
-            fetch(k, u + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-            look_up(k, u + kStages);
+            fetch(u + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+            look_up(u + kStages);
             if (t <= clear - kStep) step(std::false_type(), u);
             else step(std::true_type(), u);
             if (++slot == kStages) slot = 0;
@@ -595,8 +642,14 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         copy_wait<0>();
         __syncwarp();
         const Walk done = k;
-        more = walk_next(a, k);
-        if (more) begin(k);
+        {
+            Walk next = done;
+            more = walk_next(a, next);
+            if (more) {
+                keep(next);
+                begin();
+            }
+        }
 
         // ---- merge the warps: their fragments lie alike, so that unit m of 4 values a lane
         // is exchanged through [warp][lane] and summed by warp m % 8: one after the other through
@@ -604,7 +657,6 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         // less: a request of 200 tokens 8.9 -> 6.9 us)
         static_assert(S::kMerge >= kNT * kVW * 4 * kWarps * 32 * 16, "the ring holds every unit");
         float4* merge = reinterpret_cast<float4*>(smem + (more ? S::kMerge : 0));
-        const float vup = vdown == 0.f ? 0.f : kCodeUp / vdown;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");   // the last piece's statistics are read
         // rows 2 tq and 2 tq + 1 of each 8
         float top[kNT][2];
@@ -663,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         };
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-            float peak[2], total[2], fix[2];
+            float peak[2], total[2], fix[2], vup[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = nt * 8 + 2 * tq + e;
@@ -676,18 +728,19 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     if (m != -CUDART_INF_F) total[e] += s_sum[w * kRows + r] * exp2_fast(m - peak[e]);
                 }
                 fix[e] = top[nt][e] == -CUDART_INF_F ? 0.f : exp2_fast(top[nt][e] - peak[e]);
+                vup[e] = 1.f / down[nt][e];
             }
 #pragma unroll
             for (int m = 0; m < kParts; ++m) {
                 const int turn_m = nt * kParts + m;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (fix[0] != 0.f) {
-                    x.x = fmaf(o[m][nt][0] - eight[nt][0], vup, flat[nt][0]) * fix[0];
-                    x.z = fmaf(fmaf(o[m][nt][2], kOdd, -eight[nt][0]), vup, flat[nt][0]) * fix[0];
+                    x.x = fmaf((o[m][nt][0] - eight[nt][0]) * kCodeUp, vup[0], flat[nt][0]) * fix[0];
+                    x.z = fmaf(fmaf(o[m][nt][2], kOdd, -eight[nt][0]) * kCodeUp, vup[0], flat[nt][0]) * fix[0];
                 }
                 if (fix[1] != 0.f) {
-                    x.y = fmaf(o[m][nt][1] - eight[nt][1], vup, flat[nt][1]) * fix[1];
-                    x.w = fmaf(fmaf(o[m][nt][3], kOdd, -eight[nt][1]), vup, flat[nt][1]) * fix[1];
+                    x.y = fmaf((o[m][nt][1] - eight[nt][1]) * kCodeUp, vup[1], flat[nt][1]) * fix[1];
+                    x.w = fmaf(fmaf(o[m][nt][3], kOdd, -eight[nt][1]) * kCodeUp, vup[1], flat[nt][1]) * fix[1];
                 }
                 float4* buffer = merge + (more ? turn_m & 1 : turn_m) * kWarps * 32;
                 buffer[warp * 32 + lane] = x;

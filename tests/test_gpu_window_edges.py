@@ -217,6 +217,28 @@ def test_attention_that_sees_nothing_but_nan_is_nan(q_heads, new, dim, kv):
     agrees(c, q, rows=~bad)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,new", [f for f in FORMS if f[0] * f[1] <= 16])
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 100, 3e38])
+def test_values_of_keys_that_weigh_nothing_cost_no_bits(q_heads, new, dim, dtype, size):
+    """Values far larger than the others, of the window's last token, which only its own row
+    sees (their first dimension aside they are 0: not to be seen is not to matter), and of
+    keys whose weight is next to nothing."""
+    c = Cache(3, [(300, new), (2000, new), (37, new)], 1, dim)
+    q = c.queries(q_heads, dtype) * 0.5 + 1
+    for b, (kv, _) in enumerate(c.lens):
+        if new > 1:
+            c.set(b, kv - 1, 1, 0, size / 20, -size / 3)
+        for position in (0, 18, kv // 2):
+            c.set(b, position, 0, 0, 0.01, -20.0)       # a logit below -150 where sum(q) is near dim
+            c.set(b, position, 1, 0, min(size, 2.0 ** 60), 0.0)
+    rows = np.ones((int(c.cu[-1]), q_heads), dtype=bool)
+    if new > 1:
+        rows[c.cu[1:] - 1] = False                      # the rows that see the large one
+    agrees(c, q, rows=rows)
+
+
 # ---------------------------------------------------------------------------
 # arguments
 # ---------------------------------------------------------------------------
