@@ -350,39 +350,35 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         // queries: row g of each 8, the dimensions that go with this lane's key words
         const int rows = k.w.rows * group;
         uint32_t q[kNT == 1 ? 4 * kW : 1];
-        float qsum[kNT][2];
-        float factor;
+        float qsum[kNT][2], factor[kNT][2];      // of rows 2 tq and 2 tq + 1: sum(q) 2^-24, and what makes logits of S 2^-24
         {
-            uint4 raw[kNT][kW];
-            float top = 0.f;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
+                uint4 raw[kW];
+                float top = 0.f;
                 const int r = nt * 8 + g;
                 const int64_t from = static_cast<int64_t>(k.w.begin + r / group) * a.q_token +
                                      static_cast<int64_t>(k.h * group + r % group) * a.q_head + tq * (8 * kW);
 #pragma unroll
                 for (int i = 0; i < kW; ++i) {
-                    raw[nt][i] = make_uint4(0, 0, 0, 0);
-                    if (r < rows) raw[nt][i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from + 8 * i);
-                    const uint32_t x[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+                    raw[i] = make_uint4(0, 0, 0, 0);
+                    if (r < rows) raw[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from + 8 * i);
+                    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 f = widen2<kDtype>(x[e]);
                         top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
                 }
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            const int e = query_exponent(top);
-            const float down = power_of_two(-e);
-            factor = a.scale * kLog2e * power_of_two(e);
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
+                // the row's largest: its scale is its own, so that no row has fewer bits for another's size
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                const int e = query_exponent(top);
+                const float down = power_of_two(-e), up = a.scale * kLog2e * power_of_two(e) * kCodeUp;
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < kW; ++i) {
-                    const uint32_t x[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+                    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                     float f[8];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
@@ -405,8 +401,11 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 }
                 sum += __shfl_xor_sync(~0u, sum, 1);
                 sum += __shfl_xor_sync(~0u, sum, 2);
+                sum *= 1.f / kCodeUp;
                 qsum[nt][0] = __shfl_sync(~0u, sum, 8 * tq);
                 qsum[nt][1] = __shfl_sync(~0u, sum, 8 * tq + 4);
+                factor[nt][0] = __shfl_sync(~0u, up, 8 * tq);
+                factor[nt][1] = __shfl_sync(~0u, up, 8 * tq + 4);
             }
             __syncwarp();
         }
@@ -474,14 +473,15 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 const int j = x * 8 + tile_token(g);
                 uint32_t kk = scales[j], vv = scales[kStep + j];
                 if (kTail && t0 + j >= k.w.kv) kk = vv = 0;
-                const float sf = bf16_lo(kk) * (factor * kCodeUp), off = bf16_hi(kk) * factor;
+                const float sj = bf16_lo(kk), mj = bf16_hi(kk);
                 vs[x] = bf16_lo(vv);
                 vm[x] = fmaf(8.f, vs[x], bf16_hi(vv));
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) {
                     float& z0 = s[x >> 1][nt][(x & 1) * 2];
                     float& z1 = s[x >> 1][nt][(x & 1) * 2 + 1];
-                    const float2 z = unpair(fma2(pair(sf, sf), pair(z0, z1), fma2(pair(off, off), pair(qsum[nt][0], qsum[nt][1]), pair(-base[nt][0], -base[nt][1]))));
+                    const uint64_t t = fma2(pair(sj, sj), pair(z0, z1), mul2(pair(mj, mj), pair(qsum[nt][0], qsum[nt][1])));
+                    const float2 z = unpair(fma2(t, pair(factor[nt][0], factor[nt][1]), pair(-base[nt][0], -base[nt][1])));
                     z0 = z.x, z1 = z.y;
                 }
             }

@@ -163,7 +163,7 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
-// The queries of a tile are multiplied by 2^-e, which brings the largest of them, of
+// The queries of a row are multiplied by 2^-e, which brings the largest of them, of
 // size `top`, into [2^13, 2^14): exact but for values 2^-27 below it, so that bf16
 // queries of any size keep their 8 bits as fp16. The exponents are bounded so that both
 // powers are normal; an infinity or NaN leaves e = 0.

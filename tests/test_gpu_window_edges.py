@@ -239,6 +239,22 @@ def test_values_of_keys_that_weigh_nothing_cost_no_bits(q_heads, new, dim, dtype
     agrees(c, q, rows=rows)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,new", FORMS)
+def test_queries_of_different_sizes_in_one_call(q_heads, new, dim):
+    """Rows 2^24 apart, and rows beyond fp16's range beside one with an infinity: each row
+    has the bits of its own size."""
+    c = Cache(4, [(300, new), (2000, new), (37, min(new, 37))], 1, dim)
+    q = c.queries(q_heads)
+    i = torch.arange(q.shape[0])[:, None] + torch.arange(q_heads)[None]
+    agrees(c, q * torch.exp2(-24.0 * (i % 3 == 0) + 24.0 * (i % 3 == 1))[..., None].bfloat16())
+    big = q * 2.0 ** 20
+    big[0, 0, 5] = float("inf")
+    rows = np.ones(q.shape[:2], dtype=bool)
+    rows[0, 0] = False
+    agrees(c, big, scale=2.0 ** -23, rows=rows)
+
+
 # ---------------------------------------------------------------------------
 # arguments
 # ---------------------------------------------------------------------------
