@@ -8,13 +8,20 @@
 //
 // * The decoded values are exact. A step has 8 significant bits (bf16) and |code - 8| <= 8
 //   at most 3, so s (code - 8) has 11 at most, which is what fp16 holds: K' = 2^-E s_j
-//   (c_j - 8), with E from the largest step of the tile (of V', of the tiles so far), is exact
-//   for steps down to 2^-9 of that one and within 2^-20 of the largest value below. One logical and one fp16
-//   operation decode two codes: a code's bits alone are the subnormal code * 2^-24, and fma
-//   with S = 2^24 2^-E s gives S code 2^-24 - S 8 2^-24.
+//   (c_j - 8), with E from the largest step of a tile, is exact for steps down to 2^-8 of
+//   that one, whose last bit is then fp16's least (a group whose m + 8 s is beyond 2^15 s counts
+//   as that over 2^15, beside which its rounding is nothing). So is V', whose E stays from tile
+//   to tile while all steps lie within that range of it. One logical and one fp16 operation
+//   decode two codes: a code's bits alone are the subnormal code * 2^-24, and fma with S = 2^24
+//   2^-E s gives S code 2^-24 - S 8 2^-24.
+// * A tile with steps further apart than 2^8 (it is "wide") has an E for each key, exact again.
+//   The softmax then multiplies a logit by 2^E of its key, and a weight by 2^E of its value over a
+//   power of two of the row's own, near the largest of these products: neither the size of
+//   a key that the row does not see nor that of one of no weight costs the others their bits.
 // * What is left of a key, m_j + 8 s_j, is the same for all its dimensions and meets
 //   sum(q): a further step of the first product, with both in two fp16 terms (22 bits),
-//   adds it to S. (As an fma a logit in the softmax, with the keys' terms read from shared
+//   adds it to S; the keys' second terms are held 2^11 up, so that they are not below fp16's
+//   range for keys far smaller than the tile's largest. (As an fma a logit in the softmax, with the keys' terms read from shared
 //   memory, it took 2.08 ms where this took 1.83, the 8K chunk behind 8K tokens.) Likewise
 //   sum p_j (m_j + 8 s_j) is summed in fp32 beside O. So the one rounding of the product
 //   is that of p to fp16.
@@ -55,12 +62,16 @@ constexpr int kPieceFloats = 256 * 128 + 512;
 // What softmax needs of a tile's keys beside S and P. Four of them: a tile's data is
 // rewritten for the tile four later, whose keys are decoded only after the products of the
 // tile two later, which follow the softmax of this one.
-struct Column {
+struct alignas(16) Column {
     float v[kTile];                        // m + 8 s of the values
     float up[2];                           // 2^E of K', in two factors
     int ev;                                // E of V'
-    int pad;
+    int wide[2];                           // whether keys, values have an E of their own each
+    int16_t e[2][kTile];                   // E of each key and value
 };
+static_assert(sizeof(Column) % 16 == 0, "Column::v is read 16 bytes at a time");
+constexpr int kSpan = 8;                   // log2 of how far apart the steps of a tile with one E may lie
+constexpr int kLower = 64;                 // and by how much E of V' may fall below the largest so far: O stays within fp32
 
 template <int kD>
 struct Smem {
@@ -254,11 +265,12 @@ __device__ __forceinline__ uint64_t desc_sw32(uint32_t saddr) {
 __device__ __forceinline__ uint32_t sw32_offset(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
 
 // x in two fp16 terms.
-__device__ __forceinline__ void split2(float x, __half& hi, __half& lo) {
+__device__ __forceinline__ void split2(float x, float low_up, __half& hi, __half& lo) {
     hi = __float2half_rn(x);
-    lo = __float2half_rn(x - __half2float(hi));
+    lo = __float2half_rn((x - __half2float(hi)) * low_up);
 }
 constexpr float kMoreUp = 256.f;             // 2^8: the keys' terms up, the queries' down
+constexpr float kLowUp = 2048.f;             // 2^11: the keys' second term up once more, and the queries' terms for it down
 
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elected() {
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int64_t sums[kThreads / 32];
     __shared__ uint32_t tmem_slot;
     __shared__ unsigned last_one[2];
-    __shared__ uint32_t step_max[2][2][4];     // [keys or values][tile parity][warp]
+    __shared__ uint2 step_ends[2][2][4];       // largest and smallest, [keys or values][tile parity][warp]
     __shared__ volatile int abort_flag;
     // Each warpgroup's walk, kept here and not in registers: a spilled register of the loops
     // below is a trip to L2, since shared memory leaves L1 no room.
@@ -458,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // sum(q), met by the keys' m + 8 s
                 __half hi, lo;
-                split2(qsum * (1.f / kMoreUp), hi, lo);
-                const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
+                split2(qsum * (1.f / kMoreUp), 1.f, hi, lo);
+                const __half2 both = __halves2half2(hi, lo), less = __hmul2(both, __float2half2_rn(1.f / kLowUp));
                 *reinterpret_cast<uint4*>(q_more + sw32_offset(row, 0)) =
-                    make_uint4(*reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&l2), 0, 0);
+                    make_uint4(*reinterpret_cast<const uint32_t*>(&both), *reinterpret_cast<const uint32_t*>(&less), 0, 0);
                 *reinterpret_cast<uint4*>(q_more + sw32_offset(row, 1)) = make_uint4(0, 0, 0, 0);
                 tc::fence_proxy_async_smem();
             }
@@ -486,7 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(bars.s_full[wg], s_phase++);
                 __syncwarp();
                 tc::tc_fence_after();
-                const float f = factor * col.up[0] * col.up[1];
+                // (all ask the same of shared memory: the vote tells the compiler that they branch together)
+                const bool wide = __any_sync(~0u, (col.wide[0] | col.wide[1]) != 0);
+                const float f = wide ? 1.f : factor * col.up[0] * col.up[1];
+                int to = col.ev;                             // 2^to: the unit of O with this tile
                 // hidden keys: behind the end, or behind this row's token, or out of its mask
                 const int t = j * kTile;
                 const bool tail = t > clear - kTile;
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t f2 = pair(f, f);
                 // of this tile alone: sums of millions of keys would not notice one key's weight
                 uint64_t sum2 = 0, flat2 = 0;
-                bool quick = !tail && !__any_sync(~0u, fresh);
+                bool quick = !tail && !wide && !__any_sync(~0u, fresh);
                 if (quick) {
                     // Weights against the maximum so far, 32 keys at a time, two to an instruction,
                     // held as P until all are known to be within fp16; and their products with what is
@@ -538,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!quick) {
-                    // In two passes, the maximum first: tiles with hidden keys, a row's first tile, and
-                    // tiles whose logits pass the maximum by so much that the weights overflow. Rolled:
-                    // what every tile runs has to stay in the instruction cache.
+                    // In two passes, the maximum first: tiles with hidden keys, a row's first tile, wide
+                    // tiles, and those whose logits pass the maximum by so much that the weights overflow.
+                    // Rolled: what every tile runs has to stay in the instruction cache.
                     const Row m = my_row();
                     const int limit = (a.mask ? k.w.kv : min(k.w.kv, k.w.first + m.i + 1)) - t;
                     uint32_t seen[4];                            // one bit a key
@@ -563,6 +578,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                             seen[n] &= word;
                         }
                     }
+                    float most = -CUDART_INF_F;                  // of a wide tile, the largest logit + E of its value
+                    if (wide) {
+                        // S becomes the logits: each key has an exponent of its own
+#pragma unroll 1
+                        for (int n = 0; n < 8; ++n) {
+                            uint32_t raw[16];
+                            tmem_load16(s_mem + n * 16, raw);
+                            tmem_wait_load();
+                            const uint32_t visible = (n < 4 ? n < 2 ? seen[0] : seen[1] : n < 6 ? seen[2] : seen[3]) >> (n & 1) * 16;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const int e = col.e[0][n * 16 + c];
+                                const float x = __uint_as_float(raw[c]) * (factor * power_of_two(e >> 1)) * power_of_two(e - (e >> 1));
+                                raw[c] = __float_as_uint(x);
+                                if ((visible >> c) & 1) most = fmaxf(most, x + static_cast<float>(col.e[1][n * 16 + c]));
+                            }
+                            tmem_store16(s_mem + n * 16, raw);
+                        }
+                        tmem_wait_store();
+                    }
                     peak = -CUDART_INF_F;
 #pragma unroll 1
                     for (int n = 0; n < 4; ++n) {
@@ -582,6 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fresh = false;
                     }
                     peak = 0.f;
+                    if (wide) {
+                        // the largest weight times 2^E of its value, or what is in O already, is the unit
+                        // (a row that sees nothing here keeps its own; the bounds are those of any E)
+                        const float kept = fix * later;
+                        to = static_cast<int>(ceilf(fminf(fmaxf(most - base, -250.f), 250.f)));
+                        if (done_tiles > 0 && kept > 0.f) to = max(to, ev + static_cast<int>(__float_as_uint(kept) >> 23) - 127);
+                    }
                     const uint64_t b2 = pair(-base, -base);
                     sum2 = flat2 = 0;
 #pragma unroll 1
@@ -609,6 +651,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 flat2 = fma2(w, pair(v.x, v.y), flat2);
                             }
                         }
+                        if (wide) {
+                            // (a weight that 2^126 would not bring up is 0)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const int up = col.e[1][n * 32 + c] - to;
+                                e[c] *= power_of_two(min(max(up, -126), 126));
+                            }
+                        }
                         uint32_t p[16];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
@@ -623,16 +673,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fix *= later, later = 1.f;
                 if (done_tiles == 0) {
-                    ev = col.ev;
+                    ev = to;
                 } else {
-                    const bool other = col.ev != ev;
+                    const bool other = to != ev;
                     if (__any_sync(~0u, fix != 1.f || other)) {
                         // O of the tiles before is complete, and this warp's lanes of it are rescaled
                         wait(bars.o_done[wg], o_phase + done_tiles - 1);
                         __syncwarp();
                         tc::tc_fence_after();
-                        const float by = other ? ldexpf(fix, ev - col.ev) : fix;
-                        ev = col.ev;
+                        const float by = other ? ldexpf(fix, ev - to) : fix;
+                        ev = to;
 #pragma unroll 1
                         for (int c = 0; c < kD / 32; ++c) {
                             uint32_t v[32];
@@ -886,13 +936,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            // the largest step of a tile, exchanged between the warps a tile ahead
-            auto tell = [&](uint32_t scale, uint32_t parity) {
-                // of a NaN, 0; of a key whose common part would leave fp16, as much as that asks for
+            // what a group asks of E: its step; of a NaN, 0; of a key whose common part would leave
+            // fp16, as much as that does
+            auto need = [&](uint32_t scale) {
                 const float own = bf16_lo(scale), rest = fabsf(fmaf(8.f, own, bf16_hi(scale)));
-                const float most = fmaxf(fmaxf(own, 0.f), is_v ? 0.f : rest * (1.f / 32768.f));
-                const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(most));
-                if (lane == 0) step_max[is_v][parity][w] = m;
+                return __float_as_uint(fmaxf(fmaxf(own, 0.f), is_v ? 0.f : rest * (1.f / 32768.f)));
+            };
+            auto exponent = [&](uint32_t need) { return static_cast<int>(need >> 23) - 127 + 9; };   // a step in [2^-9, 2^-8)
+            // the largest and the smallest of a tile, exchanged between the warps a tile ahead
+            uint32_t mine = 0;                                  // of token p of the tile told last
+            auto tell = [&](uint32_t scale, uint32_t parity) {
+                mine = need(scale);
+                const uint32_t most = __reduce_max_sync(~0u, mine), least = __reduce_min_sync(~0u, mine - 1u);   // not of 0
+                if (lane == 0) step_ends[is_v][parity][w] = make_uint2(most, least);
             };
             look_up(k.t0);
             parts = check(k.t0);
@@ -911,22 +967,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             scale = seen(k.t0, scale);
             tell(scale, column & 1);
             asm volatile("bar.sync %0, 128;" ::"r"(4 + is_v) : "memory");
-            int e = 0;
-            bool have_e = false;
+            int e = 0, e_most = -1000;
             for (int j = k.t0; j < k.t1; ++j, ++column) {
                 const int stage = column % kStages, turn = column / kStages;
-                // E: the largest step of K' in [2^-9, 2^-8); of V', that of the piece so far
-                const uint32_t* tops = step_max[is_v][column & 1];
-                const uint32_t top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-                const int e9 = static_cast<int>(top >> 23) - 127 + 9;
-                if (top && (!is_v || !have_e || e9 > e)) e = e9, have_e = true;
+                // E: the largest step of K' in [2^-9, 2^-8); of V', kept while the steps are in its range
+                const uint2* ends = step_ends[is_v][column & 1];
+                const uint32_t top = max(max(ends[0].x, ends[1].x), max(ends[2].x, ends[3].x));
+                const uint32_t low = min(min(ends[0].y, ends[1].y), min(ends[2].y, ends[3].y)) + 1u;
+                const int e_top = exponent(top), e_low = exponent(low);
+                bool wide = false;
+                if (top) {
+                    if (!is_v) {
+                        e = e_top;
+                    } else if (e_top > e || e_low < e - kSpan || e_most < -999) {
+                        e_most = max(e_most, e_top);
+                        e = max(e_top, e_most - kLower);
+                    }
+                    wide = e_low < e - kSpan;
+                }
+                int e_mine = e;
+                if (wide && mine) e_mine = exponent(mine);
                 // the softmax of the tile four before has been through with its column: see Column
                 if (turn > 0) wait(is_v ? bars.v_empty[stage] : bars.k_empty[stage], turn - 1);
                 Column& col = columns[column % kCols];
                 // two of them: other threads may still be decoding the tile before
                 __half* steps = reinterpret_cast<__half*>(smem + S::kSteps) + (is_v * 2 + (column & 1)) * kTile;
                 // 2^24 2^-E s, for E of any step
-                const float up0 = power_of_two((24 - e) / 2), up1 = power_of_two(24 - e - (24 - e) / 2);
+                const float up0 = power_of_two((24 - e_mine) / 2), up1 = power_of_two(24 - e_mine - (24 - e_mine) / 2);
                 // a group held as NaN keeps the NaN in its common part alone
                 const float own = bf16_lo(scale);
                 const float rest = fmaf(8.f, own, bf16_hi(scale));
@@ -934,15 +1001,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     col.v[p] = rest;
                 } else {
                     __half hi, lo;
-                    split2(rest * (up0 * (1.f / 65536.f)) * up1, hi, lo);          // 2^8 2^-E
-                    const __half2 h2 = __halves2half2(hi, lo);
-                    const uint32_t h = *reinterpret_cast<const uint32_t*>(&h2);
+                    split2(rest * (up0 * (1.f / 65536.f)) * up1, kLowUp, hi, lo);  // 2^8 2^-E
+                    const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
                     unsigned char* more = smem + S::kKMore + stage * S::kMore;
-                    *reinterpret_cast<uint4*>(more + sw32_offset(p, 0)) = make_uint4(h, h, 0, 0);
+                    *reinterpret_cast<uint4*>(more + sw32_offset(p, 0)) =
+                        make_uint4(*reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&l2), 0, 0);
                     *reinterpret_cast<uint4*>(more + sw32_offset(p, 1)) = make_uint4(0, 0, 0, 0);
                 }
                 steps[p] = __float2half_rn(own <= 3.0e38f ? own * up0 * up1 : 0.f);
+                col.e[is_v][p] = static_cast<int16_t>(e_mine);
                 if (p == 0) {
+                    col.wide[is_v] = wide;
                     if (is_v) col.ev = e;
                     else col.up[0] = power_of_two(e / 2), col.up[1] = power_of_two(e - e / 2);
                 }

@@ -183,8 +183,8 @@ def agrees(c, q, mask=None, scale=None, rows=None):
     want, want_lse, tol, lse_tol = expect(c, q, mask, scale)
     rows = np.ones(lse.shape, dtype=bool) if rows is None else rows
     # what q's type cannot hold is an infinity of the same sign
-    beyond = (np.abs(want) + tol >= torch.finfo(q.dtype).max) & (out == np.sign(want) * np.inf)
     with np.errstate(invalid="ignore"):
+        beyond = (np.abs(want) + tol >= torch.finfo(q.dtype).max) & (out == np.sign(want) * np.inf)
         off, lse_off = np.where(beyond, 0, np.abs(out - want))[rows], np.abs(lse - want_lse)[rows & np.isfinite(want_lse)]
     assert np.array_equal(np.isneginf(lse[rows]), np.isneginf(want_lse[rows]))
     assert (off <= tol[rows]).all(), ("out", (off / tol[rows]).max())
@@ -219,7 +219,7 @@ def test_attention_that_sees_nothing_but_nan_is_nan(q_heads, new, dim, kv):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("q_heads,new", [f for f in FORMS if f[0] * f[1] <= 16])
+@pytest.mark.parametrize("q_heads,new", FORMS)
 @pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 100, 3e38])
 def test_values_of_keys_that_weigh_nothing_cost_no_bits(q_heads, new, dim, dtype, size):
     """Values far larger than the others, of the window's last token, which only its own row
@@ -253,6 +253,67 @@ def test_queries_of_different_sizes_in_one_call(q_heads, new, dim):
     rows = np.ones(q.shape[:2], dtype=bool)
     rows[0, 0] = False
     agrees(c, big, scale=2.0 ** -23, rows=rows)
+
+
+@pytest.mark.parametrize("q_heads,new", FORMS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("up", [7, 8, 9, 12, 30, 100, 125])
+def test_keys_and_values_below_one_that_is_not_seen(q_heads, new, dim, up):
+    """The window's last token, which its own row alone sees, has a key and a value 2^up above
+    the others, whose steps have odd significands (all 8 bits are needed): it costs the
+    other rows nothing. With a mask too, where a token in the middle of the window is hidden."""
+    c = Cache(5, [(300, new), (2000, new), (140, min(new, 140))], 2, dim, spread=0)
+    g = np.random.default_rng(up)
+    c.scales[..., 0] = (129 + 2 * g.integers(0, 63, c.scales.shape[:-1])) / 1024.0
+    c.scales[..., 1] = -7.5 * c.scales[..., 0] + 0.2 * g.standard_normal(c.scales.shape[:-1])
+    q = c.queries(2 * q_heads, torch.float16)
+    if new == 1:
+        return agrees(c, q)
+    size = 2.0 ** min(up, 124)
+    hidden = [kv - 1 for kv, _ in c.lens]
+    for b, at in enumerate(hidden):
+        for kind in (0, 1):
+            for head in (0, 1):
+                c.set(b, at, kind, head, size / 8, -size)
+    rows = np.ones((int(c.cu[-1]), 2 * q_heads), dtype=bool)
+    rows[c.cu[1:] - 1] = False
+    agrees(c, q, rows=rows)
+    if new <= 64:
+        mask = [((1 << (i + 1)) - 1) & ~1 for _, n in c.lens for i in range(n)]      # nobody sees the window's first
+        for b, at in enumerate(hidden):
+            first = c.lens[b][0] - c.lens[b][1]
+            old = c.table[b, at // 16], at % 16
+            put = c.table[b, first // 16], first % 16
+            c.scales[put[0], :, :, put[1]], c.scales[old[0], :, :, old[1]] = \
+                c.scales[old[0], :, :, old[1]].copy(), c.scales[put[0], :, :, put[1]].copy()
+        agrees(c, q, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_heads,new", FORMS)
+@pytest.mark.parametrize("spread", [1.0, 2.5, 8.0])
+def test_steps_over_many_orders(q_heads, new, spread, dtype):
+    """Steps of keys and values spread over up to 2^70, all of them seen by some row."""
+    c = Cache(6, [(400, new), (1100, new), (90, min(new, 90))], 2, 64, spread=spread)
+    q = c.queries(2 * q_heads, dtype)
+    agrees(c, q * (0.25 ** 4 if spread == 8.0 else 1.0), scale=2.0 ** -12 if spread == 8.0 else None)
+
+
+@pytest.mark.parametrize("q_heads,new", FORMS)
+def test_values_that_fall_and_rise_by_tiles(q_heads, new):
+    """Values whose size changes from one stretch of 128 tokens to the next, by more than a
+    tile's range, up and down; constants and zeros among them."""
+    c = Cache(7, [(1500, new), (1030, new)], 1, 128)
+    for b, (kv, _) in enumerate(c.lens):
+        for tile in range(-(-kv // 128)):
+            at = np.arange(tile * 128, min(kv, tile * 128 + 128))
+            size = 2.0 ** [0, 12, -14, -13, 40, 39, -70, 3, 0, 0, 30, -30][tile]
+            index = c.table[b, at // 16], 1, slice(None), at % 16
+            c.scales[index] = c.scales[index] * size
+        c.set(b, np.arange(256, 300), 1, 0, 0.0, 0.0)
+        c.set(b, np.arange(900, 1000), 1, 0, 0.0, 1.5)
+        c.set(b, np.arange(600, 640), 0, 0, 0.0, 0.25)
+    agrees(c, c.queries(q_heads) * 2)
 
 
 # ---------------------------------------------------------------------------
