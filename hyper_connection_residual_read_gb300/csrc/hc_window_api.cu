@@ -50,10 +50,11 @@ uint64_t cache_tokens(const hc_kv4_cache& c) {
 
 unsigned item(int dtype) { return dtype == HC_DTYPE_FP32 ? 4 : 2; }
 
-// Strides of rows read 16 bytes at a time: whole 16-byte pieces, and not negative.
-bool good_strides(int64_t token, int64_t head, int dtype) {
+// Strides of rows read 16 bytes at a time: whole 16-byte pieces, and not negative. That of an
+// axis of one is never used.
+bool good_strides(int tokens, int heads, int64_t token, int64_t head, int dtype) {
     const int64_t n = 16 / item(dtype);
-    return token >= 0 && head >= 0 && token % n == 0 && head % n == 0;
+    return (tokens == 1 || (token >= 0 && token % n == 0)) && (heads == 1 || (head >= 0 && head % n == 0));
 }
 
 // Bytes from the first to behind the last element of a strided [tokens][heads][dim].
@@ -110,8 +111,8 @@ extern "C" int hc_kv4_append(const hc_kv4_cache* cache, int tokens, int dtype, c
     if (int e = check_cache(cache, c->device)) return e;
     if (tokens < 0 || dtype < HC_DTYPE_BF16 || dtype > HC_DTYPE_FP32) return HC_ERR_ARG;
     if (tokens == 0) return HC_OK;
-    if (!good_strides(k_token_stride, k_head_stride, dtype) ||
-        !good_strides(v_token_stride, v_head_stride, dtype))
+    if (!good_strides(tokens, cache->kv_heads, k_token_stride, k_head_stride, dtype) ||
+        !good_strides(tokens, cache->kv_heads, v_token_stride, v_head_stride, dtype))
         return HC_ERR_ARG;
     if (int e = check_ptr(k, c->device)) return e;
     if (int e = check_ptr(v, c->device)) return e;
@@ -165,7 +166,7 @@ extern "C" int hc_kv4_attention(const hc_kv4_cache* cache, int requests, int tok
     if (q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > HC_KV4_MAX_GROUP) return HC_ERR_ARG;
     if (mask != nullptr && max_new > HC_KV4_MAX_MASKED) return HC_ERR_ARG;
     if (requests == 0 || tokens == 0 || max_new == 0) return HC_OK;
-    if (!good_strides(q_token_stride, q_head_stride, dtype)) return HC_ERR_ARG;
+    if (!good_strides(tokens, q_heads, q_token_stride, q_head_stride, dtype)) return HC_ERR_ARG;
     if (int e = check_ptr(q, c->device)) return e;
     if (int e = check_ptr(out, c->device)) return e;
     const void* ints[] = {cu_lens, kv_lens, block_table};

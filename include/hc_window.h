@@ -115,7 +115,8 @@ int hc_window_plan(int requests, int table_width, int block_size, int capacity, 
 /* Rounds the keys and values of `tokens` tokens to 4 bits and writes them to their
  * slots (slots[tokens]; negative: the token is skipped; a slot given twice in one call
  * holds either token). k and v hold head_dim values of `dtype` at token * token_stride +
- * head * head_stride elements; strides are multiples of 16 bytes. */
+ * head * head_stride elements; strides are multiples of 16 bytes, but for that of an axis
+ * of one, which is not used. */
 int hc_kv4_append(const hc_kv4_cache* cache, int tokens, int dtype,
                   const void* k, int64_t k_token_stride, int64_t k_head_stride,
                   const void* v, int64_t v_token_stride, int64_t v_head_stride,
@@ -138,7 +139,7 @@ int hc_kv4_load(const hc_kv4_cache* cache, int tokens, const int64_t* slots, int
  * nothing gets zeros and lse = -inf. Query head h reads kv head h / (q_heads / kv_heads).
  *
  *   q     head_dim values of `dtype` (bf16 or fp16) at token * q_token_stride + head *
- *         q_head_stride elements; strides are multiples of 16 bytes
+ *         q_head_stride elements; strides as in hc_kv4_append
  *   out   [tokens][q_heads][head_dim] of `dtype`
  *   lse   [tokens][q_heads] fp32, or NULL
  *   max_new   an upper bound of the requests' new tokens, which chooses the kernel: a

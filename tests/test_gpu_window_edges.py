@@ -339,3 +339,31 @@ def test_more_kv_heads_than_a_launch_has_room_for_are_refused():
     assert torch.equal(o, k) and torch.equal(p, k)
     hc.hc_kv4_attention(k, codes, scales, i32([[0]]), i32([0, 1]), i32([1]), 1, o)
     assert torch.equal(o, k)
+
+
+def test_the_stride_of_an_axis_of_one_does_not_matter():
+    """One token, or one head, of rows of an odd length: what torch gives as that axis's
+    stride is never used; another axis's still has to be whole 16 bytes."""
+    wide = torch.randn(4 * 67, device="cuda").bfloat16()
+    codes = torch.zeros((1, 2, 4, 16, 32), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((1, 2, 4, 16, 2), dtype=torch.bfloat16, device="cuda")
+    one, odd = wide.as_strided((1, 4, 64), (67, 64, 1)), wide.as_strided((4, 1, 64), (64, 3, 1))
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+    back = torch.zeros((2, 1, 4, 64), device="cuda")
+    hc.hc_kv4_append(one, one, slots, codes, scales)
+    hc.hc_kv4_load(slots, codes, scales, back[0], back[1])
+    want, s, m = (torch.from_numpy(np.asarray(x, dtype=np.float32)) for x in W.round_group(one[0].double().cpu().numpy()))
+    assert torch.equal(back[0, 0].cpu(), m[:, None] + s[:, None] * want) and torch.equal(back[0], back[1])
+    out = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for q, o in ((one, out[0]), (one.contiguous().clone(), out[1])):
+        hc.hc_kv4_attention(q, codes, scales, i32([[0]]), i32([0, 1]), i32([1]), 1, o)
+    assert torch.equal(out[0], out[1]) and out.any()
+    single = codes[:, :, :1].contiguous(), scales[:, :, :1].contiguous()
+    hc.hc_kv4_append(odd, odd, torch.arange(4).cuda(), *single)
+    other = codes[:, :, :1].contiguous(), scales[:, :, :1].contiguous()
+    hc.hc_kv4_append(odd.contiguous().clone(), odd.contiguous().clone(), torch.arange(4).cuda(), *other)
+    assert torch.equal(single[0], other[0]) and torch.equal(single[1].view(torch.int16), other[1].view(torch.int16))
+    bad = torch.randn(4 * 67, device="cuda").bfloat16().as_strided((4, 1, 64), (67, 64, 1))
+    with pytest.raises(hc.HcReadError) as e:
+        hc.hc_kv4_append(bad, bad, torch.arange(4).cuda(), *single)
+    assert e.value.code == hc.HC_ERR_ARG
