@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
                 } else if (HC_IN_RANGE(at, 1, a.width, status)) {
                     block = a.table[static_cast<size_t>(b) * a.width + at];
                 }
-                slot = static_cast<int64_t>(block) * a.block_size + (pos & (a.block_size - 1));
+                if (block < 0) atomicOr(status, kStatusBounds);           // no block: no slot
+                else slot = static_cast<int64_t>(block) * a.block_size + (pos & (a.block_size - 1));
             }
         }
         a.slots[t] = slot;

@@ -98,7 +98,8 @@ typedef struct hc_kv4_cache {
  *   cu_lens[requests + 1]     first new token of each request, and their total
  *   kv_lens[requests]         cached + new where granted, else cached
  *   slots[capacity]           slot of each new token, -1 where its request was not
- *                             granted and past the total
+ *                             granted, where its block's id is negative (reported) and
+ *                             past the total
  *   request_of, positions     [capacity] the token's request and its position in it,
  *                             -1 past the total
  *   free_left[1]              free_count less the blocks taken; must not be free_count

@@ -367,3 +367,22 @@ def test_the_stride_of_an_axis_of_one_does_not_matter():
     with pytest.raises(hc.HcReadError) as e:
         hc.hc_kv4_append(bad, bad, torch.arange(4).cuda(), *single)
     assert e.value.code == hc.HC_ERR_ARG
+
+
+# ---------------------------------------------------------------------------
+# entries that are not valid
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", ["held", "free"])
+def test_plan_reports_blocks_that_are_none(bad):
+    """A negative id of a block that the request holds, or of one on the free list: its tokens
+    have no slot, which the write would skip without a word; the others' are right."""
+    held, free = [-1 if bad == "held" else 4, 9], [3, 2, -7 if bad == "free" else 1]
+    table = i32([[held[0], 55], [held[1], 55]])
+    out = [torch.full((24,), -9, dtype=torch.int64, device="cuda"), i32([-9] * 24), i32([-9] * 24), i32([0] * 3), i32([0] * 2), i32([0])]
+    hc.hc_window_plan(i32([10, 12]), i32([12, 10]), i32(free), i32([3]), 16, table, *out)
+    assert hc.hc_read_status() == hc.HC_ERR_BOUNDS and hc.hc_read_status() == hc.HC_OK
+    blocks = [[held[0], free[2]], [held[1], free[1]]]
+    want = [blocks[b][p // 16] * 16 + p % 16 if blocks[b][p // 16] >= 0 else -1
+            for b, (c, n) in enumerate(((10, 12), (12, 10))) for p in range(c, c + n)]
+    assert out[0].tolist() == want + [-1] * 2 and out[4].tolist() == [22, 22] and int(out[5]) == 1
