@@ -114,8 +114,9 @@ int hc_window_plan(int requests, int table_width, int block_size, int capacity, 
                    int32_t* free_left, void* stream);
 
 /* Rounds the keys and values of `tokens` tokens to 4 bits and writes them to their
- * slots (slots[tokens]; negative: the token is skipped; a slot given twice in one call
- * holds either token). k and v hold head_dim values of `dtype` at token * token_stride +
+ * slots (slots[tokens]; negative: the token is skipped). Give a slot once in a call: of
+ * several tokens given the same one, any may end in each 32-bit word of its codes and scales,
+ * so that what it holds need not be one of them. k and v hold head_dim values of `dtype` at token * token_stride +
  * head * head_stride elements; strides are multiples of 16 bytes, but for that of an axis
  * of one, which is not used. */
 int hc_kv4_append(const hc_kv4_cache* cache, int tokens, int dtype,

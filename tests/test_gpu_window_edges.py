@@ -386,3 +386,33 @@ def test_plan_reports_blocks_that_are_none(bad):
     want = [blocks[b][p // 16] * 16 + p % 16 if blocks[b][p // 16] >= 0 else -1
             for b, (c, n) in enumerate(((10, 12), (12, 10))) for p in range(c, c + n)]
     assert out[0].tolist() == want + [-1] * 2 and out[4].tolist() == [22, 22] and int(out[5]) == 1
+
+
+def test_a_slot_given_twice_holds_words_of_either_token_and_spoils_no_other():
+    """Duplicates within a warp, between warps and between blocks of the launch: each 32-bit
+    word is that of one of the tokens, and all other slots are as if there were none."""
+    g = torch.Generator().manual_seed(2)
+    tokens, heads, dim, block = 3000, 2, 128, 16
+    k, v = (torch.randn(tokens, heads, dim, generator=g).bfloat16().cuda() for _ in range(2))
+    slots = torch.randperm(4000, generator=g)[:tokens]
+    pairs = [(0, 1), (5, 40), (7, 2900), (100, 1500)]
+    for a, b in pairs:
+        slots[b] = slots[a]
+
+    def written(keep):
+        codes = torch.zeros((250, 2, heads, block, dim // 2), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros((250, 2, heads, block, 2), dtype=torch.bfloat16, device="cuda")
+        hc.hc_kv4_append(k, v, torch.where(keep, slots, -1).cuda(), codes, scales)
+        return torch.cat([codes.view(torch.int32), scales.view(torch.int32)], -1).transpose(2, 3).reshape(250, 2, block, -1)
+
+    first, second = torch.ones(tokens, dtype=torch.bool), torch.ones(tokens, dtype=torch.bool)
+    for a, b in pairs:
+        first[b] = second[a] = False
+    one, two = written(first), written(second)
+    for _ in range(5):
+        both = written(torch.ones(tokens, dtype=torch.bool))
+        assert ((both == one) | (both == two)).all()
+        same = torch.ones(250, block, dtype=torch.bool)
+        for a, _ in pairs:
+            same[slots[a] // block, slots[a] % block] = False
+        assert torch.equal(both.transpose(1, 2)[same.cuda()], one.transpose(1, 2)[same.cuda()])
