@@ -63,37 +63,41 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB)
         print(f"built {out} from {len(srcs)} sources")
     if out == LIB:
         build_pycall(verbose)
+        build_pywindow(verbose)
     return out
 
 
-# CPython modules behind the binding's calls (marshalling only) and their sources.
-PYCALLS = {"_hcpycall": "hc_pycall.c", "_hcpywindow": "hc_pywindow.c"}
-
-
-def build_pycall(verbose: bool = False) -> list[str]:
-    """The CPython modules behind the binding's calls (csrc/hc_pycall.c, csrc/hc_pywindow.c,
-    marshalling only). Without a C compiler or Python headers they are skipped and the
-    binding calls the library through ctypes alone."""
+def _build_call_module(name: str, src: str, verbose: bool) -> str | None:
+    """A CPython module behind the binding's calls (marshalling only). Without a C compiler
+    or Python headers it is skipped and the binding calls the library through ctypes alone."""
     import sysconfig
+    out = os.path.join(PKG, name + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
     inc = sysconfig.get_paths()["include"]
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None or not os.path.exists(os.path.join(inc, "Python.h")):
         if verbose:
-            print("skipped the Python call modules (no C compiler or Python headers)")
-        return []
-    built = []
-    for name, src in PYCALLS.items():
-        out = os.path.join(PKG, name + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
-        tmp = out + ".tmp"
-        cmd = [cc, "-O2", "-shared", "-fPIC", "-I", inc, os.path.join(CSRC, src), "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"building the Python call module {name} failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, out)
-        built.append(out)
-        if verbose:
-            print(f"built {out}")
-    return built
+            print(f"skipped the Python call module {name} (no C compiler or Python headers)")
+        return None
+    tmp = out + ".tmp"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", inc, os.path.join(CSRC, src), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the Python call module {name} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    if verbose:
+        print(f"built {out}")
+    return out
+
+
+def build_pycall(verbose: bool = False) -> str | None:
+    """The module behind the binding's hc_read / hc_read_path calls (csrc/hc_pycall.c): its
+    path, or None where it was skipped."""
+    return _build_call_module("_hcpycall", "hc_pycall.c", verbose)
+
+
+def build_pywindow(verbose: bool = False) -> str | None:
+    """The same for the window operators' calls (csrc/hc_pywindow.c)."""
+    return _build_call_module("_hcpywindow", "hc_pywindow.c", verbose)
 
 
 def build_bounds_checked(verbose: bool = False) -> str:
