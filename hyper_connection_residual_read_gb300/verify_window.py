@@ -96,11 +96,12 @@ class Decoder:
         return {**r, "logits": logits, "follow": follow, "slots": slots, "request_of": request_of,
                 "positions": positions, "last_keys_values": (k, v)}
 
-    def accept(self, windows, top_ids, prompt: bool = False) -> list:
+    def accept(self, windows, top_ids, prompt=False) -> list:
         """The tokens that each window gained: its drafted ones as far as each is the most
-        likely, and one more. The cache keeps what was verified (a prompt as a whole), and
-        blocks past it are free again. A request whose blocks were not granted gains
-        nothing."""
+        likely, and one more. The cache keeps what was verified (a prompt as a whole: ``prompt``
+        says of all windows, or of each, that they are), and blocks past it are free again. A
+        request whose blocks were not granted gains nothing."""
+        prompt = [prompt] * len(windows) if isinstance(prompt, bool) else prompt
         best, size = top_ids[:, 0].tolist(), self.block_size
         had, cached, left = self.kv.tolist(), self.cached.tolist(), int(self.free_left)
         gained, at = [], 0
@@ -108,7 +109,7 @@ class Decoder:
             n = 0
             if had[b] == cached[b]:
                 gained.append([])
-            elif prompt:
+            elif prompt[b]:
                 gained.append([best[at + len(w) - 1]])
                 cached[b] = had[b]
             else:
@@ -123,6 +124,13 @@ class Decoder:
         self.cached.copy_(torch.tensor(cached, dtype=torch.int32))
         self.free_count.fill_(left)
         return gained
+
+    def release(self, request: int) -> None:
+        """Drops what the cache holds of a request; its blocks are free again."""
+        held, left = -(-int(self.cached[request]) // self.block_size), int(self.free_count)
+        self.free[left:left + held] = self.table[request, :held]
+        self.free_count.fill_(left + held)
+        self.cached[request] = 0
 
     def read_back(self, layer: int, slots):
         """Keys and values that the cache holds in ``slots``."""
@@ -142,25 +150,33 @@ def draft(text: list, count: int) -> list:
 
 def generate(decoder: Decoder, prompts: list, tokens: int, propose=draft) -> tuple:
     """Continues ``prompts`` by at least ``tokens`` tokens each; returns the texts, the
-    steps after the prompt and the log probabilities of the accepted drafts."""
-    texts, steps, accepted = [list(p) for p in prompts], 0, []
-    r = decoder.step(prompts)
-    for text, more in zip(texts, decoder.accept(prompts, r["top_ids"], prompt=True)):
-        text += more
+    steps after the prompt and the log probabilities of the accepted drafts. A request
+    that finds no blocks for its prompt waits and sends it again; one that is done gives its
+    blocks back."""
+    texts, steps, accepted = [list(p) for p in prompts], -1, []
     goal = [len(p) + tokens for p in prompts]
+    waits, held = [True] * len(prompts), [False] * len(prompts)      # for its prompt to be cached; is cached
     while any(len(t) < n for t, n in zip(texts, goal)):
-        windows = [[t[-1], *propose(t, decoder.drafts)] if len(t) < n else [] for t, n in zip(texts, goal)]
+        windows = [[] if len(t) >= n else list(t) if w else [t[-1], *propose(t, decoder.drafts)]
+                   for t, n, w in zip(texts, goal, waits)]
         r = decoder.step(windows)
-        gained = decoder.accept(windows, r["top_ids"])
-        if not any(gained):
-            raise RuntimeError("no blocks left for any request")
+        gained = decoder.accept(windows, r["top_ids"], prompt=waits)
         logprob, at = r["logprob"].tolist(), 0
-        for text, window, more in zip(texts, windows, gained):
+        for b, (text, window, more) in enumerate(zip(texts, windows, gained)):
             text += more
-            accepted += logprob[at:at + len(more) - 1] if more else []
+            if more and not waits[b]:
+                accepted += logprob[at:at + len(more) - 1]
+            if more:
+                waits[b], held[b] = False, True
             at += len(window)
+        freed = [b for b, t in enumerate(texts) if held[b] and len(t) >= goal[b]]
+        for b in freed:
+            decoder.release(b)
+            held[b] = False
+        if not any(gained) and not freed:
+            raise RuntimeError("no blocks left for any request")
         steps += 1
-    return texts, steps, accepted
+    return texts, max(steps, 0), accepted
 
 
 def main() -> None:
