@@ -21,7 +21,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// The window of one request, with what does not fit its arrays cut off and reported.
+// The window of one request, with what does not fit its arrays cut off and reported. (That kv
+// fits the request's row of the table is what the kernels' lookups there rely on.)
 struct Window {
     int begin;     // its first token in q
     int n;         // its new tokens
@@ -42,18 +43,6 @@ __device__ __forceinline__ Window load_window(const AttentionArgs& a, int b, int
     w.first = w.kv - w.n;
     if ((bad || w.n > a.max_new || kv > room) && status) atomicOr(status, kStatusBounds);
     return w;
-}
-
-// The block that holds page `page` of request b; block 0, reported, for an entry that
-// is none (its values are wrong then, but they are read from the cache's own memory).
-__device__ __forceinline__ int load_block(const AttentionArgs& a, int b, int page, int* status) {
-    int block = -1;
-    if (page < a.width) block = a.table[static_cast<int64_t>(b) * a.width + page];
-    if (block < 0 || block >= a.c.blocks) {
-        atomicOr(status, kStatusBounds);
-        block = 0;
-    }
-    return block;
 }
 
 // 8 codes of a word as 4 pairs of fp16 numbers: pair i holds the codes at i and i + 4. A
