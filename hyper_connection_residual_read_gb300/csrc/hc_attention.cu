@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     const unsigned char* head_scales;
     auto look_up = [&](int u) {
         const unsigned t = static_cast<unsigned>(u) * kUnit + warp * kStep + half * 16;
-        if (u < u1 && t < static_cast<unsigned>(kv)) id = pages[t >> sh];
+        if (u < u1 && t < static_cast<unsigned>(kv) && HC_IN_RANGE(pages + (t >> sh) - a.table, 1, table_extent(a), status))
+            id = pages[t >> sh];
     };
     // brings the step of unit u to a slot of the ring (a group of copies, if an empty one)
     auto fetch = [&](int u, int slot) {
@@ -322,10 +323,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             const uint32_t to = put + slot * L::kBytes;
 #pragma unroll
             for (int i = 0; i < kD / 32; ++i) {
-                copy16(to + i * 256, keys + i * 256);
-                copy16(to + L::kCodes + i * 256, values + i * 256);
+                if (HC_IN_RANGE(keys + i * 256 - a.c.codes, 16, group_count(a.c) * (kD / 2), status)) copy16(to + i * 256, keys + i * 256);
+                if (HC_IN_RANGE(values + i * 256 - a.c.codes, 16, group_count(a.c) * (kD / 2), status))
+                    copy16(to + L::kCodes + i * 256, values + i * 256);
             }
-            if (l16 < 8) copy16(put_scales + slot * L::kBytes, head_scales + at / (kD / 8));
+            const unsigned char* from = head_scales + at / (kD / 8);
+            if (l16 < 8 && HC_IN_RANGE(from - reinterpret_cast<const unsigned char*>(a.c.scales), 16, group_count(a.c) * 4, status))
+                copy16(put_scales + slot * L::kBytes, from);
         }
         copy_commit();
     };
@@ -362,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < kW; ++i) {
                     raw[i] = make_uint4(0, 0, 0, 0);
-                    if (r < rows) raw[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from + 8 * i);
+                    if (r < rows && HC_IN_RANGE(from + 8 * i, 8, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), status))
+                        raw[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from + 8 * i);
                     const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                     for (int e = 0; e < 2; ++e) {
                         const int r = nt * 8 + 2 * tq + e, i = r / group;
                         uint64_t bits = 0;
-                        if (a.mask && r < rows) bits = a.mask[k.w.begin + i];
+                        if (a.mask && r < rows && HC_IN_RANGE(k.w.begin + i, 1, a.tokens, status)) bits = a.mask[k.w.begin + i];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const int j = t0 + x * 8 + tile_token(g), back = j - k.w.first;
@@ -688,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 const float inv = total[e] == 0.f ? 0.f : 1.f / total[e];
                 const int64_t at = static_cast<int64_t>(done.w.begin + r / group) * a.q_heads + done.h * group + r % group;
                 const int d = g * (kD / 8) + 2 * m;
+                if (!HC_IN_RANGE(at * kD + d, 2, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) continue;
                 *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * kD + d) =
                     e ? narrow2<kDtype>(x.y * inv, x.w * inv) : narrow2<kDtype>(x.x * inv, x.z * inv);
                 if (a.lse && d == 0) a.lse[at] = total[e] == 0.f ? -CUDART_INF_F : (peak[e] + log2f(total[e])) * kLn2;
@@ -761,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
             const int64_t total = run.total, n = run.ctas;
             const int c0 = static_cast<int>(((done.base + done.cost + 1) * n - 1) / total);
             const int c1 = static_cast<int>(((done.base + done.cost + done.units) * n - 1) / total);
+            if (!HC_IN_RANGE(c0, c1 - c0 + 1, gridDim.x, status)) break;      // scratch and counters go by CTA
             asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
             if (threadIdx.x == 0) {
                 const unsigned before = arrive(&arrivals[c0]);

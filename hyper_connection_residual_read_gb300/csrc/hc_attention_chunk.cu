@@ -430,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (active) {
                 // ---- this row of Q: scaled to fp16, in the order of the decoded keys
                 const Row m = my_row();
-                const bool here = m.here;
                 const int i = m.i, hq = m.hq;
                 const int64_t from = static_cast<int64_t>(k.w.begin + i) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
+                const bool here = m.here && HC_IN_RANGE(from, kD, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), status);
                 const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from);
                 float top = 0.f;
 #pragma unroll 8
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (a.mask) {
                         // bit 0 of `bits` is the key at `at`; keys before it are seen
-                        const uint64_t bits = m.here ? a.mask[k.w.begin + m.i] : 0;
+                        const uint64_t bits = m.here && HC_IN_RANGE(k.w.begin + m.i, 1, a.tokens, status) ? a.mask[k.w.begin + m.i] : 0;
                         const int at = k.w.first - t;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
@@ -749,8 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 total = sum * mine + other_sum * other;
             }
             const Row mine_row = my_row();
-            const bool here = mine_row.here;
             const int64_t at = static_cast<int64_t>(k.w.begin + mine_row.i) * a.q_heads + mine_row.hq;
+            const bool here = mine_row.here && HC_IN_RANGE(at, 1, static_cast<size_t>(a.tokens) * a.q_heads, status);
             float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (k.t0 == 0 ? 1 : 0)) * kPieceFloats;
             const int prow = (same ? 0 : wg * kTile) + row;
             auto write = [&](int c, const float (&v)[32], float inv) {
@@ -798,10 +798,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t n = run.ctas;
                 const int c0 = static_cast<int>(((k.base + kPieceCost + 1) * n - 1) / run.total);
                 const int c1 = static_cast<int>(((k.base + kPieceCost + k.tiles) * n - 1) / run.total);
+                const bool known = HC_IN_RANGE(c0, c1 - c0 + 1, gridDim.x, status);     // scratch and counters go by CTA
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
                 if (row == 0) {
-                    const unsigned before = arrive(&arrivals[2 * c0 + wg]);
-                    last_one[wg] = before == static_cast<unsigned>(c1 - c0);
+                    const unsigned before = known ? arrive(&arrivals[2 * c0 + wg]) : 0u;
+                    last_one[wg] = known && before == static_cast<unsigned>(c1 - c0);
                     if (last_one[wg]) arrivals[2 * c0 + wg] = 0;
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
@@ -860,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c <= c1) join_parts(c, std::integral_constant<int, 1>{});
                         const int of = k.row0 + (same ? 0 : wg * kTile) + r;
                         const int64_t to = (static_cast<int64_t>(k.w.begin + of / group) * a.q_heads + k.h * group + of % group) * kD;
+                        if (!HC_IN_RANGE(to, kD, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) continue;
 #pragma unroll
                         for (int x = 0; x < kOf; ++x)
                             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + (x * kSpan + q) * 4) =
@@ -896,7 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.c.scales) + first;
             auto look_up = [&](int j) {
                 const unsigned t = min(static_cast<unsigned>(j) * kTile + lane * 16, static_cast<unsigned>(max(k.w.kv - 1, 0)));
-                ids = a.table[static_cast<int64_t>(k.b) * a.width + (t >> sh)];
+                const int64_t at = static_cast<int64_t>(k.b) * a.width + (t >> sh);
+                if (HC_IN_RANGE(at, 1, table_extent(a), status)) ids = a.table[at];
             };
             uint64_t parts, parts_next = 0;                     // bytes from `codes` to those of lane's part
             auto check = [&](int j) -> uint64_t {
@@ -915,11 +918,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t scale = 0, scale_next = 0;                 // of token p of this tile and the next
             auto load_scale = [&](uint64_t parts) -> uint32_t {
                 const uint64_t at = place(parts, p);
+                if (!HC_IN_RANGE(first + at / (kD / 2), 1, group_count(a.c), status)) return 0;
                 prefetch_l2(a.c.codes + first * (kD / 2) + at);  // its codes are loaded a tile later
                 return scales[at / (kD / 2)];
             };
             // (a piece of keys, loaded again as soon as it is decoded; or the values' tokens)
             auto load_keys = [&](int u, uint64_t at) {
+                if (!HC_IN_RANGE(codes + at - a.c.codes, 16, group_count(a.c) * (kD / 2), status)) return;
                 const uint4 y = *reinterpret_cast<const uint4*>(codes + at);
                 raw[4 * u] = y.x, raw[4 * u + 1] = y.y, raw[4 * u + 2] = y.z, raw[4 * u + 3] = y.w;
             };
@@ -928,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int n = 0; n < 8; ++n) {
                     const int x = vh * 64 + n * 4 + vt;
                     const uint64_t at = place(parts, x);
+                    if (!HC_IN_RANGE(codes + at - a.c.codes, 4 * kVW, group_count(a.c) * (kD / 2), status)) continue;
                     if (kVW == 2) {
                         const uint2 y = *reinterpret_cast<const uint2*>(codes + at);
                         raw[n * kVW] = y.x, raw[n * kVW + kVW - 1] = y.y;
@@ -1105,10 +1111,21 @@ cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st)
                                                                                   : launch_chunk<kD, kDtype, false>(ctx, a, st);
 }
 
+// A kernel's shared memory; and that it was compiled with the registers which its warps share out
+// among themselves (a warp would wait for ever for what the launch does not have).
+template <int kD, int kDtype, bool kSame>
+cudaError_t allow_one() {
+    cudaFuncAttributes has;
+    const cudaError_t e = cudaFuncGetAttributes(&has, chunk_kernel<kD, kDtype, kSame>);
+    if (e != cudaSuccess) return e;
+    if ((has.numRegs + 7) / 8 * 8 * kThreads < 65536) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(chunk_kernel<kD, kDtype, kSame>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
+}
+
 template <int kD, int kDtype>
 cudaError_t allow_smem() {
-    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<kD, kDtype, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(chunk_kernel<kD, kDtype, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kD>::kBytes);
+    const cudaError_t e = allow_one<kD, kDtype, true>();
+    return e != cudaSuccess ? e : allow_one<kD, kDtype, false>();
 }
 
 }  // namespace

@@ -197,7 +197,7 @@ struct alignas(16) Part {
 
 template <int kDtype>
 __global__ void __launch_bounds__(kThreads, 5)
-    score_kernel(const LogprobArgs a, int splits, unsigned char* scratch, unsigned* arrivals) {
+    score_kernel(const LogprobArgs a, int splits, unsigned char* scratch, unsigned* arrivals, int* status) {
     using L = Logits<kDtype>;
     constexpr int kN = L::kN;
     __shared__ uint64_t list[kList];
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 5)
     // (without asking for the next kernel: its CTAs would lie unevenly over what the SMs have left,
     // 96 rows 14.2 us against 12.1)
     pdl_wait();
+    if (!HC_IN_RANGE(row, 1, a.tokens, status)) return;
     const int id = a.ids[row];
     const bool known = id >= 0 && id < a.vocab;
     const float mine = known ? L::one(x, id) : CUDART_INF_F;
@@ -307,6 +308,12 @@ __global__ void __launch_bounds__(kThreads, 5)
             }
         }
     };
+    // (a vector outside of the row counts as one of -inf)
+    constexpr uint32_t kNothing = kDtype == HC_DTYPE_FP32 ? 0xFF800000u : kDtype == HC_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+    auto bring = [&](int i) {
+        return HC_IN_RANGE(head + static_cast<int64_t>(i) * kN, kN, a.vocab, status) ? ldg_stream_v4(vec + i)
+                                                                                      : make_uint4(kNothing, kNothing, kNothing, kNothing);
+    };
     using Count = typename L::Two;
     auto count_up = [&](Count& count) {
         if constexpr (kDtype != HC_DTYPE_FP32) {
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 5)
     for (; at + (kAhead - 1) * kThreads < v1; at += kAhead * kThreads) {
         uint4 v[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) v[i] = ldg_stream_v4(vec + at + i * kThreads);
+        for (int i = 0; i < kAhead; ++i) v[i] = bring(at + i * kThreads);
         Count count = L::two(0.f);               // at most 4 kAhead: exact
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) vector(v[i], at + i * kThreads, count);
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 5)
     }
     for (; at < v1; at += kThreads) {
         Count count = L::two(0.f);
-        vector(ldg_stream_v4(vec + at), at, count);
+        vector(bring(at), at, count);
         count_up(count);
     }
     fold();
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 5)
     const int singles = split == 0 ? head + tail : 0;
     const int single = tid < head ? tid : a.vocab - tail + (tid - head);
     float y1 = -CUDART_INF_F;
-    if (tid < singles) {
+    if (tid < singles && HC_IN_RANGE(single, 1, a.vocab, status)) {
         y1 = L::one(x, single);
         if (sums.passed(y1)) sums.move(y1);
         if (sums.ref != -CUDART_INF_F || y1 != y1) sums.add(y1);
@@ -381,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 5)
             const bool again = key != 0 && key >= bound;
             const uint64_t mine_too = tid < singles ? order_key(y1, single) : 0;
             auto look = [&](int i) {
+                if (!HC_IN_RANGE(head + static_cast<int64_t>(i) * kN, kN, a.vocab, status)) return;
                 const uint4 v = vec[i];
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
@@ -410,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 5)
                 for (int n = 0; n < a.top; ++n) {
                     uint64_t next = mine_too < last ? mine_too : 0;
                     for (int i = v0 + tid; i < v1; i += kThreads) {
+                        if (!HC_IN_RANGE(head + static_cast<int64_t>(i) * kN, kN, a.vocab, status)) continue;
                         const uint4 v = vec[i];
                         for (int m = 0; m < kN; ++m) {
                             const uint64_t k = order_key(L::at(v, m), head + i * kN + m);
@@ -503,9 +512,9 @@ cudaError_t launch_logprobs(const Ctx& ctx, const LogprobArgs& a, int dtype, cud
     const int splits = row_splits(ctx.sm_count, a.tokens, a.vocab, dtype == HC_DTYPE_FP32 ? 4 : 8);
     const unsigned grid = static_cast<unsigned>(a.tokens) * splits;
     switch (dtype) {
-        case HC_DTYPE_BF16: return launch_early(score_kernel<HC_DTYPE_BF16>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals);
-        case HC_DTYPE_FP16: return launch_early(score_kernel<HC_DTYPE_FP16>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals);
-        default: return launch_early(score_kernel<HC_DTYPE_FP32>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals);
+        case HC_DTYPE_BF16: return launch_early(score_kernel<HC_DTYPE_BF16>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals, ctx.s.status);
+        case HC_DTYPE_FP16: return launch_early(score_kernel<HC_DTYPE_FP16>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals, ctx.s.status);
+        default: return launch_early(score_kernel<HC_DTYPE_FP32>, dim3(grid), kThreads, 0, st, a, splits, ctx.score_parts, ctx.score_arrivals, ctx.s.status);
     }
 }
 

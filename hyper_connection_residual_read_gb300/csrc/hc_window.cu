@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
                 else slot = static_cast<int64_t>(block) * a.block_size + (pos & (a.block_size - 1));
             }
         }
+        if (!HC_IN_RANGE(t, 1, a.capacity, status)) continue;
         a.slots[t] = slot;
         a.request_of[t] = request;
         a.positions[t] = pos;
@@ -358,8 +359,9 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs a
     int64_t slot = -1;
     if (t < a.tokens) {
         slot = a.slots[t];
-        raw[0].load(a.k, t * a.k_token + head * a.k_head + sub * 8);
-        raw[1].load(a.v, t * a.v_token + head * a.v_head + sub * 8);
+        const int64_t k = t * a.k_token + head * a.k_head + sub * 8, v = t * a.v_token + head * a.v_head + sub * 8;
+        if (HC_IN_RANGE(k, 8, row_extent(a.tokens, a.c.kv_heads, kD, a.k_token, a.k_head), status)) raw[0].load(a.k, k);
+        if (HC_IN_RANGE(v, 8, row_extent(a.tokens, a.c.kv_heads, kD, a.v_token, a.v_head), status)) raw[1].load(a.v, v);
     }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs a
         const uint32_t code = round_group<kLanes>(raw[kv], sm);
         if (slot < 0) continue;
         const int64_t g = group_index(a.c, sh, slot, kv, head, status);
-        if (g < 0) continue;
+        if (g < 0 || !HC_IN_RANGE(g, 1, group_count(a.c), status)) continue;
         reinterpret_cast<uint32_t*>(a.c.codes)[g * kLanes + sub] = code;
         if (sub == 0) reinterpret_cast<uint32_t*>(a.c.scales)[g] = sm;
     }
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kCacheThreads) load_kernel(const CacheArgs a, 
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         const int64_t g = slot < 0 ? -1 : group_index(a.c, sh, slot, kv, head, status);
-        if (g < 0) continue;
+        if (g < 0 || !HC_IN_RANGE(g, 1, group_count(a.c), status)) continue;
         code[kv] = reinterpret_cast<const uint32_t*>(a.c.codes)[g * kLanes + sub];
         sm[kv] = reinterpret_cast<const uint32_t*>(a.c.scales)[g];
     }
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kCacheThreads) load_kernel(const CacheArgs a, 
         }
         Raw8<kDtype> raw;
         raw.set(x);
-        raw.store(kv ? a.v_out : a.k_out, at);
+        if (HC_IN_RANGE(at, 8, static_cast<size_t>(a.tokens) * a.c.kv_heads * kD, status)) raw.store(kv ? a.v_out : a.k_out, at);
     }
 }
 

@@ -21,6 +21,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// What the bounds-checked build checks against: the groups of a cache (a key or a value of one
+// head), the elements of strided [tokens][heads][dim] rows, the entries of the table.
+__device__ __forceinline__ size_t group_count(const hc_kv4_cache& c) {
+    return static_cast<size_t>(2) * c.blocks * c.kv_heads * c.block_size;
+}
+__device__ __forceinline__ size_t row_extent(int tokens, int heads, int dim, int64_t token, int64_t head) {
+    return static_cast<size_t>(tokens - 1) * token + static_cast<size_t>(heads - 1) * head + dim;
+}
+__device__ __forceinline__ size_t table_extent(const AttentionArgs& a) { return static_cast<size_t>(a.requests) * a.width; }
+
 // The window of one request, with what does not fit its arrays cut off and reported. (That kv
 // fits the request's row of the table is what the kernels' lookups there rely on.)
 struct Window {
@@ -32,7 +42,8 @@ struct Window {
 };
 
 __device__ __forceinline__ Window load_window(const AttentionArgs& a, int b, int* status) {
-    Window w;
+    Window w = {};
+    if (!HC_IN_RANGE(b, 1, a.requests, status)) return w;
     const int lo = a.cu[b], hi = a.cu[b + 1], kv = a.kv[b];
     const int64_t room = static_cast<int64_t>(a.width) * a.c.block_size;
     const bool bad = lo < 0 || hi < lo || hi > a.tokens;

@@ -262,11 +262,11 @@ int hc_read_noalloc(int tokens,
 int hc_read_version(void);
 
 /* 1 if this library was compiled with -DHC_BOUNDS_CHECK, else 0. In that build every
- * hand-indexed global access of every kernel of the read is first checked against its buffer's
+ * hand-indexed global access of every kernel is first checked against its buffer's
  * extent as the kernel's arguments give it; an access out of range is skipped, and
  * hc_read_status reports HC_ERR_BOUNDS. There is no trap, so the context stays
- * usable. The normal build has no checks. (The window operators' kernels check what
- * they read from index arrays in both builds.) It stands in for a memory checker, and
+ * usable. The normal build has no such checks. (What the window operators' kernels read
+ * from index arrays they check in both builds.) It stands in for a memory checker, and
  * the pages have no counterpart of it. */
 int hc_read_bounds_checked(void);
 
