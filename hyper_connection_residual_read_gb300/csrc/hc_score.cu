@@ -480,12 +480,17 @@ __global__ void __launch_bounds__(kThreads, 5)
 
     // ---- results
     const bool empty = sums.ref == -CUDART_INF_F && sums.s == 0.f;         // -inf alone
-    const float lse = empty ? -CUDART_INF_F : sums.ref + logf(sums.s);
-    auto logprob = [&](float y) { return y == -CUDART_INF_F && lse == lse && lse != CUDART_INF_F ? y : lse == CUDART_INF_F ? CUDART_NAN_F : y - lse; };
+    const float ln_s = logf(sums.s), lse = empty ? -CUDART_INF_F : sums.ref + ln_s;
+    // y - lse, by the difference from the reference: beside a large one fp32 does not hold the logarithm
+    // (a row of the type's lowest value alone is as likely everywhere, -ln vocab)
+    auto logprob = [&](float y) {
+        if (y == -CUDART_INF_F && lse == lse && lse != CUDART_INF_F) return y;
+        return lse == CUDART_INF_F ? CUDART_NAN_F : (y - sums.ref) - ln_s;
+    };
     if (tid == 0) {
         a.lse[row] = lse;
         a.logprob[row] = known ? logprob(mine) : lse == lse ? -CUDART_INF_F : lse;
-        a.entropy[row] = empty ? 0.f : logf(sums.s) - sums.b / sums.s;
+        a.entropy[row] = empty ? 0.f : ln_s - sums.b / sums.s;
         a.rank[row] = known ? above : a.vocab;
     }
     if (warp == 0 && lane < a.top) {

@@ -126,7 +126,8 @@ def logprobs(x, ids, top):
         ref = np.where(np.isfinite(peak), peak, 0.0)
         total = np.exp(x - ref[:, None]).sum(-1)
         lse = np.where(total > 0, ref + np.log(total), -np.inf)
-        lp = np.where(np.isneginf(x), -np.inf, x - np.where(np.isneginf(lse), 0, lse)[:, None])
+        # x - lse without a sum of both: at 1e30, 64 bits do not hold the logarithm beside it
+        lp = np.where(np.isneginf(x), -np.inf, x - ref[:, None] - np.where(total > 0, np.log(total), 0)[:, None])
         p = np.exp(lp)
         entropy = -np.where(p > 0, p * lp, 0.0).sum(-1) + 0.0
     known = (ids >= 0) & (ids < vocab)
