@@ -17,7 +17,9 @@
 // * A tile with steps further apart than 2^8 (it is "wide") has an E for each key, exact again.
 //   The softmax then multiplies a logit by 2^E of its key, and a weight by 2^E of its value over a
 //   power of two of the row's own, near the largest of these products: neither the size of
-//   a key that the row does not see nor that of one of no weight costs the others their bits.
+//   a key that the row does not see nor that of one of no weight costs the others their bits, and
+//   weights that fp16 does not hold count where their values are as large. (So a tile is taken
+//   whose values are all far larger than those before.)
 // * What is left of a key, m_j + 8 s_j, is the same for all its dimensions and meets
 //   sum(q): a further step of the first product, with both in two fp16 terms (22 bits),
 //   adds it to S; the keys' second terms are held 2^11 up, so that they are not below fp16's
@@ -71,6 +73,7 @@ struct alignas(16) Column {
 };
 static_assert(sizeof(Column) % 16 == 0, "Column::v is read 16 bytes at a time");
 constexpr int kSpan = 8;                   // log2 of how far apart the steps of a tile with one E may lie
+constexpr int kRise = 10;                  // by how much E of V' may pass a row's unit: a weight far below 1 may matter then
 constexpr int kLower = 64;                 // and by how much E of V' may fall below the largest so far: O stays within fp32
 
 template <int kD>
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float base = 0.f, sum = 0.f, flat = 0.f;
             bool fresh = true;
             float later = 1.f;                         // what O is to be multiplied by before its next product
-            int ev = 0, done_tiles = 0;
+            int ev = 1000, done_tiles = 0;             // (above any E, until the first tile)
             const int t1 = k.t1;
             const int clear = min(k.w.kv, a.mask ? k.w.first : k.w.first + 1 + k.row0 / group);   // every row sees what lies before
             for (int j = k.t0; j < t1; ++j, ++column) {
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tc::tc_fence_after();
                 // (all ask the same of shared memory: the vote tells the compiler that they branch together)
-                const bool wide = __any_sync(~0u, (col.wide[0] | col.wide[1]) != 0);
+                const bool wide = __any_sync(~0u, (col.wide[0] | col.wide[1] | max(col.ev - ev - kRise, 0)) != 0);
                 const float f = wide ? 1.f : factor * col.up[0] * col.up[1];
                 int to = col.ev;                             // 2^to: the unit of O with this tile
                 // hidden keys: behind the end, or behind this row's token, or out of its mask
@@ -826,9 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // part, 30 rows of one request of 16384 tokens took 94 us where this takes 45;
                     // quarters, which suit few parts, make the kernel of shared rows spill: 16
                     // verify windows 115 us with halves, 143 with quarters.)
-                    constexpr int kOf = kSame ? 2 : 4, kAhead = kSame ? 6 : 4, kSpan = kD / 4 / kOf;
+                    constexpr int kOf = kSame ? 2 : 4, kAhead = kSame ? 6 : 4, kPart = kD / 4 / kOf;
                     const int rows = same ? k.rows : min(k.rows - wg * kTile, kTile), at_row = prow - row;
-                    for (int n = row; n < rows * kSpan; n += 128) {
+                    for (int n = row; n < rows * kPart; n += 128) {
                         const int r = n % rows, q = n / rows;
                         const float2 join = joined[wg][r];
                         float4 o[kOf] = {};
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 st[m] = __ldcg(reinterpret_cast<const float2*>(part + 256 * kD) + at_row + r);
 #pragma unroll
                                 for (int x = 0; x < kOf; ++x)
-                                    y[m][x] = __ldcg(reinterpret_cast<const float4*>(part) + (x * kSpan + q) * 256 + at_row + r);
+                                    y[m][x] = __ldcg(reinterpret_cast<const float4*>(part) + (x * kPart + q) * 256 + at_row + r);
                             }
 #pragma unroll
                             for (int m = 0; m < kCount; ++m) {
@@ -864,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!HC_IN_RANGE(to, kD, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) continue;
 #pragma unroll
                         for (int x = 0; x < kOf; ++x)
-                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + (x * kSpan + q) * 4) =
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + (x * kPart + q) * 4) =
                                 make_uint2(narrow2<kDtype>(o[x].x * join.y, o[x].y * join.y), narrow2<kDtype>(o[x].z * join.y, o[x].w * join.y));
                     }
                 }

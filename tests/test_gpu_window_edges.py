@@ -316,6 +316,54 @@ def test_values_that_fall_and_rise_by_tiles(q_heads, new):
     agrees(c, c.queries(q_heads) * 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,new", FORMS)
+@pytest.mark.parametrize("up", [6, 13, 20, 45])
+def test_values_as_large_as_their_weights_are_small(q_heads, new, dim, dtype, up):
+    """Stretches of tokens whose values are 2^up above the others' and whose weights are about
+    2^-up of theirs, so that both matter; after ordinary ones, before them, and among them (in so many requests that a block of
+    the launch has several tiles of one)."""
+    c = Cache(8, [(900, new)] * 24, 4, dim)
+    q = (1 + 0.05 * c.queries(4 * q_heads)).to(dtype)
+    c.scales[:, 1] /= 16                                # within fp16's range
+    down = up * np.log(2) / dim ** 0.5                   # of a key's minimum, which sum(q) = dim multiplies
+    for b, at in enumerate((np.arange(384, 640), np.arange(0, 200), np.arange(3, 700, 7))):
+        page = c.table[b, at // 16], at % 16
+        c.scales[page[0], 0, 0, page[1], 1] -= down
+        c.scales[page[0], 1, 0, page[1]] *= 2.0 ** up
+    agrees(c, q)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,new", FORMS)
+def test_sizes_that_change_within_the_tiles_of_one_block(q_heads, new, dim, dtype):
+    """Many requests, so that a block of the launch goes through several tiles of one: values
+    and keys whose sizes change from tile to tile, wide tiles among ordinary ones, and a
+    large key and value that only the window's last row sees."""
+    g = np.random.default_rng(9)
+    c = Cache(9, [(1300, new)] * 16, 4, dim)
+    sizes = [0, 0, 3, -9, 11, -12, 2, 14, -30, 0, 1]
+    for b in range(16):
+        order = g.permutation(sizes)
+        for tile in range(11):
+            at = np.arange(tile * 128, min(1300, tile * 128 + 128))
+            page = c.table[b, at // 16], at % 16
+            c.scales[page[0], 1, :, page[1]] *= 2.0 ** order[tile]
+            if tile % 4 == b % 4:                           # keys too, of some tokens of some tiles
+                some = at[g.random(len(at)) < 0.2]
+                c.scales[c.table[b, some // 16], 0, :, some % 16] *= 2.0 ** -11
+                c.scales[c.table[b, some // 16], 1, :, some % 16] *= 2.0 ** g.integers(-14, 3)
+        if new > 1 and b % 2:
+            for head in range(4):
+                c.set(b, 1299, 0, head, 2.0 ** 40, 0.0)
+                c.set(b, 1299, 1, head, 2.0 ** 70, 0.0)
+    rows = np.ones((int(c.cu[-1]), 4 * q_heads), dtype=bool)
+    rows[c.cu[1:] - 1] = new == 1
+    agrees(c, c.queries(4 * q_heads, dtype), rows=rows)
+
+
 # ---------------------------------------------------------------------------
 # arguments
 # ---------------------------------------------------------------------------
