@@ -42,7 +42,7 @@
  * enqueued on `stream` has completed. Outputs must not overlap each other or any
  * input. R and P are only read (R is not updated with P). The library owns its
  * scratch (slice partials, counters, lo, a device status word), allocated by
- * hc_read_init for up to max_tokens tokens.
+ * hc_read_init for up to max_tokens tokens, with 41 MB for the operators of hc_window.h.
  *
  * Ordering: the weights (w_norm, W_down, W_up) are layer parameters. The library
  * may start reading them before the kernel that precedes the call on `stream`

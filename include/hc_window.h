@@ -37,7 +37,8 @@
  * memory of the context's device (hc_read_init, any max_tokens), asynchronous on
  * `stream`, argument errors refused on the host before anything is enqueued. hc_kv4_*
  * and hc_token_logprobs share the context's scratch, whose size does not depend on any
- * argument: calls on one context must be issued on one stream at a time. `codes`,
+ * argument (41 MB, allocated by hc_read_init): calls on one context must be issued on one
+ * stream at a time. `codes`,
  * `scales`, q, k, v, their outputs, and the logits of hc_token_logprobs where noted, are
  * 16-byte aligned; arrays of 4- and 8-byte integers and floats are aligned to their
  * elements. Outputs must not overlap inputs or each other unless said.
@@ -147,7 +148,22 @@ int hc_kv4_load(const hc_kv4_cache* cache, int tokens, const int64_t* slots, int
  *   max_new   an upper bound of the requests' new tokens, which chooses the kernel: a
  *             request with more reports HC_ERR_BOUNDS and the rest of it is not written
  *
- * Output is bitwise deterministic for given lengths. */
+ * A request that hc_window_plan did not grant has tokens in q and none in the cache: its rows
+ * are computed as if its last cached tokens were they, and mean nothing.
+ *
+ * What is rounded: sums, maxima and softmax statistics are fp32, and keys and values enter
+ * as the cache holds them, exactly. q is held as fp16 over a power of two of each row's own
+ * (exact but for elements 2^-27 below the row's largest). Each weight p_j, or p_j times the
+ * value's step, is rounded once to fp16, 11 bits, relative to a power of two of each row's
+ * own (so that no row loses bits to what it does not see or hardly weighs); and for more
+ * than 16 rows (new tokens x query heads of a kv head) the part m + 8 s that a key's
+ * dimensions have in common, and the sum of q that it meets, are two fp16 terms each, 22
+ * bits. So out is within 2^-10 sum_j p_j (|s_j (c_j - 8)| + |m_j + 8 s_j|) of the formula
+ * before it is rounded to `dtype`, while the logits' terms stay below 2^8, and lse within
+ * 2^-19 of 1 + the largest sum of a logit's terms. A row that sees a key or value held as
+ * NaN, or whose query is NaN, is NaN.
+ *
+ * Output is bitwise deterministic for given inputs. */
 int hc_kv4_attention(const hc_kv4_cache* cache, int requests, int tokens, int q_heads,
                      int max_new, int table_width, float scale, int dtype,
                      const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -166,6 +182,10 @@ int hc_kv4_attention(const hc_kv4_cache* cache, int requests, int tokens, int q_
  * lse = logprob = -inf, top_logprobs = -inf and entropy 0. A token id outside the
  * vocabulary has logprob = -inf and rank = vocab. A row with a NaN or +inf has NaN as
  * logprob, entropy and top_logprobs (lse NaN or +inf), and unspecified rank and ids.
+ * All in fp32, with the hardware's powers of two (2^-22): lse within 2^-17 + 2^-22 of the
+ * row's largest |x|, log probabilities, which are taken from differences of logits, within
+ * 2^-17 + 2^-23 of the difference to the largest one for ordinary rows, the entropy within
+ * 2^-17 + 2^-20 (28 + ln vocab).
  * 0 <= top <= min(vocab, HC_LOGPROBS_MAX_TOP); 1 <= vocab. */
 int hc_token_logprobs(int tokens, int vocab, int top, int dtype, const void* logits,
                       int64_t row_stride, const int32_t* token_ids, float* logprob,
