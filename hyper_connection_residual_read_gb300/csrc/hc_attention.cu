@@ -36,9 +36,12 @@
 // the CTAs, from fp32 sums in scratch of a fixed size (a CTA can have at most two such
 // pieces).
 //
-// Measured: 64 requests of one token over up to 16K tokens, 32/8 heads of 128, 120 us, 4.9
-// TB/s of cache (72% of the copy rate): issue bounds it, the ALU pipe at 57%, 534
-// instructions a warp for 32 tokens of 4 rows. One request over 4K tokens 10.3 us, over 200 6.7.
+// Measured: 64 requests of one token over up to 16K tokens, 32/8 heads of 128, 116 us, 5.1
+// TB/s of cache (75% of the copy rate): issue bounds it, the ALU pipe at 58%, 509
+// instructions a warp for 32 tokens of 4 rows; 12 bytes a thread are spilled. One request over 4K
+// tokens 9.6 us, over 200 6.0. 64 windows of 16 rows over 2K tokens, 4 heads of 128, 48 us, 1.5 TB/s:
+// the 236 registers of 16 rows leave 8 warps an SM (12.5% of what it holds), which wait for
+// instructions, barriers and one another's results; no pipe is a quarter busy but ALU (24%).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -60,7 +63,7 @@ constexpr float kRoom = 32768.f;                 // by how much a weight times i
 
 constexpr int kStages = 3;                       // steps of a warp's ring
 constexpr int kPieceCost = 4;                    // what a piece costs beside its units, in units (64 ragged requests:
-                                                 // 131 us with 2, 118 with 4, 120 with 7)
+                                                 // 129 us with 2, 116 with 4, 115 with 7)
 
 // A step's slot in a warp's ring: key codes, value codes, key scales, value scales.
 template <int kD>
@@ -81,8 +84,8 @@ struct Smem {
 
 // Fixed scratch: per CTA two pieces, and a counter of arrivals.
 // Rows of this kernel; more go to the chunk kernel. (Requests x tokens, 4 kv heads of 128: 64 x
-// 2K with 16 rows take 53 us here and 24 rows 77 us there, where 24 to 32 rows took 110 to 120
-// us here; one x 16K 21 us here with 16 rows, 39 us there with 24.)
+// 2K with 16 rows take 48 us here and 24 rows 79 us there, where 24 to 32 rows took 110 to 120
+// us in a form of this kernel; one x 16K 20 us here with 16 rows, 44 us there with 30.)
 constexpr int kMaxRows = 16;
 constexpr int kPieceRows = kMaxRows;
 constexpr int kPieceFloats = kPieceRows * (128 + 2);
@@ -154,7 +157,7 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
         Window w = {};
         if (lane < a.requests) w = load_window(a, lane, blockIdx.x == 0 ? status : nullptr);
         // no more units than CTAs: one each (a piece's cost would leave CTAs without one, and others
-        // with two: one request of 8K tokens 16.3 us against 14.6)
+        // with two: one request of 8K tokens 14.7 us against 13.6)
         const int units = __reduce_add_sync(~0u, lane < a.requests ? window_units(w) : 0);
         const int cost = static_cast<int64_t>(units) * a.c.kv_heads <= gridDim.x ? 0 : kPieceCost;
         const int64_t mine = lane < a.requests ? window_slots(a, w, cost) : 0;

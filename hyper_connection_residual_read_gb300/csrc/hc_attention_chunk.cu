@@ -23,10 +23,10 @@
 // * What is left of a key, m_j + 8 s_j, is the same for all its dimensions and meets
 //   sum(q): a further step of the first product, with both in two fp16 terms (22 bits),
 //   adds it to S; the keys' second terms are held 2^11 up, so that they are not below fp16's
-//   range for keys far smaller than the tile's largest. (As an fma a logit in the softmax, with the keys' terms read from shared
-//   memory, it took 2.08 ms where this took 1.83, the 8K chunk behind 8K tokens.) Likewise
-//   sum p_j (m_j + 8 s_j) is summed in fp32 beside O. So the one rounding of the product
-//   is that of p to fp16.
+//   range for keys far smaller than the tile's largest. (As an fma a logit in the softmax, with
+//   the keys' terms read from shared memory, it took 2.08 ms where this took 1.83, the 8K chunk
+//   behind 8K tokens.) Likewise sum p_j (m_j + 8 s_j) is summed in fp32 beside O. So the one
+//   rounding of the product is that of p to fp16.
 // * Rows are the new tokens times the query heads of one kv head, so that a key is
 //   decoded once for all the heads that read it.
 // * Two row tiles (256 rows) share each decoded key tile; their products alternate, so
@@ -34,11 +34,12 @@
 //   both warpgroups on the same rows, each on every other key tile.
 // * Work is cut as in the window kernel: runs of equal cost over the CTAs, in key tiles.
 //
-// Measured: 8192 tokens behind 8192, 32/8 heads of 128, 1.66 ms, 993 TFLOP/s of the causal
+// Measured: 8192 tokens behind 8192, 32/8 heads of 128, 1.65 ms, 999 TFLOP/s of the causal
 // products (52% of the library's rate): softmax, key and value warps each need 4500 to 5000
 // cycles for a step of 256 rows x 128 keys, the products 2300. 16 windows of 8 tokens over up
 // to 32K tokens, 20/4 heads of 128, 110 us, 1.2 TB/s of cache: the key warps are busy all of
-// the time (4000 cycles a tile), the others wait for them.
+// the time (some 4000 cycles a tile), the others wait for them. 6 ragged chunks of up to 1001
+// tokens, 16 heads of 64, 96 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -56,7 +57,7 @@ constexpr int kTile = 128;                 // keys of a tile, rows of a row tile
 constexpr int kStages = 2;                 // key tiles and value tiles in shared memory
 constexpr int kCols = 4;                   // column data of tiles (see Column)
 constexpr int kPieceCost = 5;              // what a piece costs beside its tiles, in tiles (ragged chunks:
-                                           // 108 us with 1, 102 with 2, 97 with 5)
+                                           // 104 us with 1, 99 with 2, 96 with 5)
 constexpr float kRaise = 8.f;              // log2 by which a logit may pass the maximum before it is raised
 constexpr float kMost = 15.f;              // and the most that a weight may have as fp16
 constexpr int kPieceFloats = 256 * 128 + 512;

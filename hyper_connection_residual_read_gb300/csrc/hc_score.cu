@@ -15,8 +15,8 @@
 // DRAM). Logits and their indexes are compared as one number, so that equal logits count
 // in the order of their indexes.
 //
-// Measured: 4096 x 131072 bf16 with the top 20, 200 us, 5.4 TB/s (79% of the copy rate): issue
-// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 9.3 us, 96 x 50257 fp32 12.1
+// Measured: 4096 x 131072 bf16 with the top 20, 201 us, 5.3 TB/s (79% of the copy rate): issue
+// bounds it, ALU 56%, FMA 43%, exponentials 29% busy. 8 x 131072 9.1 us, 96 x 50257 fp32 12.4
 // us: half of that is the join of the segments and the choice of the top ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

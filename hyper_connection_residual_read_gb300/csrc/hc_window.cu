@@ -20,8 +20,8 @@ namespace {
 // requests for itself (two prefix sums over at most 8192 requests in shared memory) and
 // then writes its own share of the tokens and of the new blocks, finding the request of
 // each by bisection of the prefix sums. New blocks are looked up on the free list by
-// rank, not in the table, which other CTAs are writing. 32 requests of 8 tokens take 4.1 us,
-// 1024 of 128 tokens 7.7 us.
+// rank, not in the table, which other CTAs are writing. 32 requests of 8 tokens take 3.6 us,
+// 1024 of 128 tokens 7.4 us.
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanTokens = 2048;      // tokens of one CTA: four a thread
@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
 // codes as one word. A CTA takes the tokens of one tile for one head, key and value of a
 // token in the same lanes, both loads on their way before either is rounded. Every value is
 // read and written once, 16 bytes a lane, so that memory bounds long calls: 8191 tokens of 8
-// heads of 128 in fp16, written and read back, take 21.3 us for 85 MB, 4.0 TB/s. (Four
+// heads of 128 in fp16, written and read back, take 20.9 us for 85 MB, 4.1 TB/s. (Four
 // tokens a thread at once took 23.6 us, and min, max and codes one value at a time 25.3.) 32
-// tokens take 3.5 us for both launches.
+// tokens take 3.1 us for both launches.
 
 constexpr int kCacheThreads = 256;
 
