@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kCacheThreads) load_kernel(const CacheArgs a, 
 template <int kD, int kDtype>
 cudaError_t cache_call(const Ctx& ctx, const CacheArgs& a, bool append, cudaStream_t st) {
     constexpr int kTile = kCacheThreads / (kD / 8);
-    const dim3 grid((a.tokens + kTile - 1) / kTile, a.c.kv_heads);
+    const dim3 grid((a.tokens - 1) / kTile + 1, a.c.kv_heads);
     return append ? launch_early(append_kernel<kD, kDtype>, grid, kCacheThreads, 0, st, a, ctx.s.status)
                   : launch_early(load_kernel<kD, kDtype>, grid, kCacheThreads, 0, st, a, ctx.s.status);
 }
@@ -447,7 +447,7 @@ cudaError_t window_setup() {
 
 cudaError_t launch_plan(const Ctx& ctx, const PlanArgs& a, cudaStream_t st) {
     const size_t smem = static_cast<size_t>(a.requests) * 13;
-    const int grid = a.capacity > kPlanTokens ? (a.capacity + kPlanTokens - 1) / kPlanTokens : 1;
+    const int grid = a.capacity > kPlanTokens ? (a.capacity - 1) / kPlanTokens + 1 : 1;
     return launch_early(plan_kernel, dim3(grid), kPlanThreads, smem, st, a, ctx.s.status);
 }
 

@@ -47,6 +47,31 @@ def test_plan_of_lengths_next_to_the_largest(cached, new):
     assert got[5].tolist() == [cached + new]
 
 
+def test_calls_of_the_most_tokens():
+    """2^31 - 1 tokens: a plan whose arrays have room for as many, and a write of one key and
+    value (strides of 0) to as many slots, of which two are."""
+    n = 2 ** 31 - 1
+    slots = torch.full((n,), -9, dtype=torch.int64, device="cuda")
+    of, at = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    cu, kv, left, table = i32([0] * 3), i32([0] * 2), i32([0]), i32([[0, 0], [0, 0]])
+    hc.hc_window_plan(i32([0, 5]), i32([20, 3]), i32([7, 8, 9]), i32([3]), 16, table, slots, of, at, cu, kv, left)
+    assert cu.tolist() == [0, 20, 23] and kv.tolist() == [20, 8] and int(left) == 1
+    assert slots[:24].tolist() == [9 * 16 + i for i in range(16)] + [8 * 16 + i for i in range(4)] + [5, 6, 7, -1]
+    for x in (slots, of, at):
+        assert bool((x[23:24] == -1).all()) and bool((x[-5000:] == -1).all()) and int((x[:: 2 ** 20] == -9).sum()) == 0
+    del of, at
+    slots[:23] = -1
+    slots[1], slots[-1] = 3, 17
+    codes = torch.zeros((2, 2, 1, 16, 32), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((2, 2, 1, 16, 2), dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(64, device="cuda").bfloat16().expand(n, 1, 64)
+    hc.hc_kv4_append(one, one, slots, codes, scales)
+    want = torch.zeros_like(scales)
+    want[0, :, 0, 3, 1] = want[1, :, 0, 1, 1] = 1.0
+    assert torch.equal(scales, want) and not codes.any()
+    assert hc.hc_read_status() == hc.HC_OK
+
+
 @pytest.mark.parametrize("q_heads,new", [(8, 1), (4, 3), (1, 40)])
 def test_attention_over_lengths_next_to_the_largest(q_heads, new):
     """2^31 - 1 tokens: all pages but the last are one block, and the last one's keys have
