@@ -154,14 +154,16 @@ int hc_kv4_load(const hc_kv4_cache* cache, int tokens, const int64_t* slots, int
  * What is rounded: sums, maxima and softmax statistics are fp32, and keys and values enter
  * as the cache holds them, exactly. q is held as fp16 over a power of two of each row's own
  * (exact but for elements 2^-27 below the row's largest). Each weight p_j, or p_j times the
- * value's step, is rounded once to fp16, 11 bits, relative to a power of two of each row's
- * own (so that no row loses bits to what it does not see or hardly weighs); and for more
- * than 16 rows (new tokens x query heads of a kv head) the part m + 8 s that a key's
- * dimensions have in common, and the sum of q that it meets, are two fp16 terms each, 22
- * bits. So out is within 2^-10 sum_j p_j (|s_j (c_j - 8)| + |m_j + 8 s_j|) of the formula
- * before it is rounded to `dtype`, while the logits' terms stay below 2^8, and lse within
- * 2^-19 of 1 + the largest sum of a logit's terms. A row that sees a key or value held as
- * NaN, or whose query is NaN, is NaN.
+ * value's step, is rounded once to fp16 over a power of two of each row's own (so that no
+ * row loses bits to what it does not see or hardly weighs): to 11 bits down to 2^-14 of the
+ * largest that the row has seen, to 2^-25 of that below. For more than 16 rows (new tokens x
+ * query heads of a kv head) the part m + 8 s that a key's dimensions have in common, and the
+ * sum of q that it meets, are two fp16 terms each, 22 bits. So, while the sums of a logit's
+ * terms stay below 2^8, out is within 2^-10 sum_j p_j (|s_j (c_j - 8)| + |m_j + 8 s_j|) +
+ * 2^-22 n max_j p_j max_j s_j of the formula before it is rounded to `dtype`, n the keys that
+ * weigh less than 2^-14 of the largest (2^17 equal keys of 2^-18 each are rounded the same
+ * way and may be off by 2^-7 of what they add up to), and lse within 2^-19 of 1 + the largest
+ * such sum. A row that sees a key or value held as NaN, or whose query is NaN, is NaN.
  *
  * Output is bitwise deterministic for given inputs. */
 int hc_kv4_attention(const hc_kv4_cache* cache, int requests, int tokens, int q_heads,
