@@ -2,8 +2,8 @@
 C-ABI CUDA library and its Python binding.
 
 ``synth`` (seeded inputs) imports without the library. The read itself (``hc_read`` and
-friends) and the window operators (``hc_window_plan``, ``hc_kv4_*``,
-``hc_token_logprobs``) load ``libhcread.so`` on first use and raise if it is missing:
+friends) and the operators of a window (``hc_window_plan``, ``hc_kv4_*``,
+``hc_token_logprobs``, ``hc_sample_tokens``) load ``libhcread.so`` on first use and raise if it is missing:
 there is no fallback implementation.
 """
 from . import synth  # noqa: F401
@@ -23,6 +23,9 @@ _WINDOW = ("hc_window_plan", "hc_kv4_append", "hc_kv4_load", "hc_kv4_attention",
            "HC_PLAN_MAX_REQUESTS", "HC_KV4_MAX_BLOCK", "HC_KV4_MAX_GROUP", "HC_KV4_MAX_MASKED",
            "HC_LOGPROBS_MAX_TOP", "WINDOW_EXPORTS")
 
+_SERVE = ("hc_kv4_append_rotary", "hc_kv4_attention_shared", "hc_sample_tokens", "hc_rotary",
+          "HC_ROTARY_MAX_AXES", "HC_SAMPLE_MAX_VOCAB", "SERVE_EXPORTS")
+
 
 def __getattr__(name):
     if name in _BINDING:
@@ -31,4 +34,7 @@ def __getattr__(name):
     if name in _WINDOW:
         from . import _window
         return getattr(_window, name)
+    if name in _SERVE:
+        from . import _serve
+        return getattr(_serve, name)
     raise AttributeError(name)

@@ -64,6 +64,7 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str = LIB)
     if out == LIB:
         build_pycall(verbose)
         build_pywindow(verbose)
+        build_pyserve(verbose)
     return out
 
 
@@ -98,6 +99,11 @@ def build_pycall(verbose: bool = False) -> str | None:
 def build_pywindow(verbose: bool = False) -> str | None:
     """The same for the window operators' calls (csrc/hc_pywindow.c)."""
     return _build_call_module("_hcpywindow", "hc_pywindow.c", verbose)
+
+
+def build_pyserve(verbose: bool = False) -> str | None:
+    """The same for the operators of include/hc_serve.h (csrc/hc_pyserve.c)."""
+    return _build_call_module("_hcpyserve", "hc_pyserve.c", verbose)
 
 
 def build_bounds_checked(verbose: bool = False) -> str:

@@ -38,20 +38,32 @@ struct Window {
     int n;         // its new tokens
     int rows;      // those of them that are computed (at most max_new)
     int kv;        // its tokens in the cache
-    int first;     // position of its first new token (negative where kv < n)
+    int first;     // position of its first new token (negative where kv < n): all before it is seen
 };
 
+// What an attention kernel computes: requests against their caches; groups of requests against
+// the prefixes that they share, into the workspace; or the first joined with the second.
+enum Side { kOwn, kPrefix, kJoined };
+
+template <Side kSide>
 __device__ __forceinline__ Window load_window(const AttentionArgs& a, int b, int* status) {
     Window w = {};
     if (!HC_IN_RANGE(b, 1, a.requests, status)) return w;
-    const int lo = a.cu[b], hi = a.cu[b + 1], kv = a.kv[b];
+    int at = b, to = b + 1;
+    bool none = false;
+    if (kSide == kPrefix) {
+        at = a.groups[b], to = a.groups[b + 1];
+        none = at < 0 || to < at || to > a.members;
+        if (none) at = to = 0;
+    }
+    const int lo = a.cu[at], hi = a.cu[to], kv = a.kv[b];
     const int64_t room = static_cast<int64_t>(a.width) * a.c.block_size;
-    const bool bad = lo < 0 || hi < lo || hi > a.tokens;
+    const bool bad = none || lo < 0 || hi < lo || hi > a.tokens;
     w.begin = bad ? 0 : lo;
     w.n = bad ? 0 : hi - lo;
     w.rows = min(w.n, a.max_new);
     w.kv = kv < 0 ? 0 : static_cast<int>(kv > room ? room : kv);
-    w.first = w.kv - w.n;
+    w.first = kSide == kPrefix ? w.kv : w.kv - w.n;    // every row sees all of a prefix
     if ((bad || w.n > a.max_new || kv > room) && status) atomicOr(status, kStatusBounds);
     return w;
 }
@@ -173,6 +185,25 @@ __device__ __forceinline__ int query_exponent(float top) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// A prefix's part of a row in the workspace: where its (maximum, sum) lie, behind all rows' values.
+__device__ __forceinline__ float2* partial_stats(const AttentionArgs& a, int dim) {
+    return reinterpret_cast<float2*>(a.partial + static_cast<int64_t>(a.tokens) * a.q_heads * dim);
+}
+// A row's own part, sums x about 2^peak with the weights' sum `total`, joined with the prefix's,
+// means y: out = by_own x + by_prefix y, and ln of the joined sum. A part that has seen nothing has
+// a maximum of -inf, and counts for nothing; one with a NaN makes the row NaN.
+struct Join {
+    float by_own, by_prefix, lse;
+};
+__device__ __forceinline__ Join join_parts_of_row(float peak, float total, float2 prefix) {
+    const float top = fmaxf(peak, prefix.x);
+    const float own = peak == -CUDART_INF_F ? 0.f : exp2_fast(peak - top);
+    const float other = prefix.x == -CUDART_INF_F ? 0.f : prefix.y * exp2_fast(prefix.x - top);
+    const float sum = total * own + other;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    return Join{own * inv, other * inv, sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2};
+}
+
 // 16 bytes global -> shared, past L1, in groups that the thread waits for in order.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -183,9 +214,15 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// More than 16 rows (hc_attention_chunk.cu).
+// Launches by part (hc_attention.cuh; hc_attention_chunk.cuh: more than 16 rows).
+template <Side kSide>
+cudaError_t launch_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+template <Side kSide>
+cudaError_t attention_window_setup();
+template <Side kSide>
 cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
-size_t attention_chunk_scratch_floats(int sm_count);
+template <Side kSide>
 cudaError_t attention_chunk_setup();
+size_t attention_chunk_scratch_floats(int sm_count);
 
 }  // namespace hc

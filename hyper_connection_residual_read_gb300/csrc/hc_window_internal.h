@@ -51,8 +51,15 @@ struct AttentionArgs {
     const uint64_t* mask;
     void* out;
     float* lse;
+    // behind a shared prefix (hc_serve.h): the prefixes' part, whose `requests` are the groups, goes
+    // to `partial`, from where the own part takes it
+    const int32_t* groups;                      // first request of each group
+    int members;                                // requests of all groups
+    float* partial;                             // [tokens][q_heads][head_dim], then (maximum, sum) of each row
 };
 cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_kv4_attention_prefix(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_kv4_attention_joined(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
 
 struct LogprobArgs {
     int tokens, vocab, top;
