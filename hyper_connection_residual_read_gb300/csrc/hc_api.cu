@@ -322,6 +322,7 @@ extern "C" int hc_read_init(int device, int max_tokens, float eps) {
         prefill_setup(c) != cudaSuccess ||
         window_setup() != cudaSuccess ||
         attention_setup() != cudaSuccess ||
+        sample_setup() != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         free_ctx(c);
         return HC_ERR_CUDA;

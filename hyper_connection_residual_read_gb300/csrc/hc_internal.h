@@ -107,9 +107,11 @@ struct Ctx {
 Ctx* current_ctx(int* err);
 int check_ptr(const void* p, int device);
 
-// Kernel attributes of the window operators, once a context (hc_window.cu, hc_attention.cu).
+// Kernel attributes of the operators beside the read, once a context (hc_window.cu, hc_attention.cu,
+// hc_sample.cu).
 cudaError_t window_setup();
 cudaError_t attention_setup();
+cudaError_t sample_setup();
 
 // Floats of Ctx::attn_pieces (hc_attention.cu); CTAs that may share requests.
 size_t attention_scratch_floats(int sm_count);

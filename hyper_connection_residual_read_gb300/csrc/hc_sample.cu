@@ -4,9 +4,25 @@
 // same in any order: which token a uniform number falls on, and where a filter cuts, are decided
 // by comparing whole numbers.
 //
-// exp((x - M) / T) = 2^z, z = (x - M) log2(e) / T in two floats. z is cut into a multiple m / 32
-// and a rest |g| <= 1/64, 2^z = 2^(m / 32) (1 + p(g)): the first from a table of 45 bits, p by its
-// series to the fourth power (2^-33), in fp32 where it is below 2^-6: within 2^-29 in all.
+// exp((x - M) / T) = 2^z. 128 z = x c - M c, c = 128 log2(e) / T, is cut into a whole number m and a
+// rest g by one fma that rounds x c to a whole number and a second that leaves what that lacks: 2^z =
+// 2^(m / 128) (1 + p(g)), the first from a table of 59 bits, p by its series to the fourth power
+// (2^-38), held to 2^-30. c and M c are two floats each. In all 2^-28 of a weight.
+//
+// A row belongs to a cluster of CTAs, which hold it in their shared memory: it is read once. What
+// the filters leave is found in steps that look at less and less of it:
+//
+// * the largest logit; for a top-p without a top-k also the sum of all weights
+// * an estimate, from an eighth of the logits, of a bound above which what stays must lie, and a list
+//   of the logits above it (where it turns out too high, of all that have weight)
+// * counts or weights of the listed logits by value, in 512 bins; those of the bin in which the border
+//   lies again, in bins 512 times as narrow, until one value is left. Of equal logits the first ones in
+//   the order of their ids stay, so that a border is a value and how many of it stay.
+// * the sum of what stays by CTA, warp and lane, in the order of the ids, down to the token.
+//
+// Each step ends in a barrier of the cluster, after which every CTA reads what the others found and
+// comes to the same end. Lists and rows are gone through in the order of the ids, by each warp its part.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,193 +32,650 @@
 #include "hc_serve_internal.h"
 #include "hc_window.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace hc {
 namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBins = kThreads;              // a thread a bin when they are summed
+constexpr int kBinBits = 9;
 constexpr int kUnitBits = 45;
 constexpr uint64_t kOne = 1ull << kUnitBits;
-constexpr int kIdBits = 18;                  // of an index: HC_SAMPLE_MAX_VOCAB
-static_assert(HC_SAMPLE_MAX_VOCAB == 1 << kIdBits);
+constexpr int kMaxCtas = 8;                  // of a cluster
+constexpr int kSteps = 128;                  // of the table, an octave
+constexpr float kRound = 12582912.f;         // 1.5 2^23
+constexpr float kDeep = -46.5f;              // log2 of weights that are 0
+constexpr float kTop = 3.402823466e38f;
+static_assert(HC_SAMPLE_MAX_VOCAB <= kMaxCtas * 32768);
 
-// 2^(j / 32) 2^45
-__constant__ uint64_t kPowers[32] = {
-    0x200000000000ull, 0x20B361A62B0Bull, 0x216AB0D9F312ull, 0x222603A024B7ull,
-    0x22E57078FAA3ull, 0x23A90E62D173ull, 0x2470F4DCEAC4ull, 0x253D3BEA3FBEull,
-    0x260DFC14636Eull, 0x26E34E6E7554ull, 0x27BD4C982468ull, 0x289C10C0C312ull,
-    0x297FB5AA6C54ull, 0x2A6856AD3A9Full, 0x2B560FBA90A8ull, 0x2C48FD6074ABull,
-    0x2D413CCCFE78ull, 0x2E3EEBD1D8BFull, 0x2F4228E7D603ull, 0x304B1332999Cull,
-    0x3159CA845542ull, 0x326E6F619B8Cull, 0x3389230547E1ull, 0x34AA07647C4Bull,
-    0x35D13F32B5A7ull, 0x36FEEDE5F6BDull, 0x383337BB0AA5ull, 0x396E41B9DF21ull,
-    0x3AB031B9F749ull, 0x3BF92E66F737ull, 0x3D495F454922ull, 0x3EA0ECB6DC8Bull,
+// 2^(j / 128) 2^59
+__constant__ uint64_t kPowers[kSteps] = {
+    0x800000000000000ull, 0x80B1ED4FD999AB7ull, 0x8164D1F3BC03077ull, 0x8218AF4373FC25Full, 0x82CD8698AC2BA1Dull,
+    0x8383594EEFB6EE3ull, 0x843A28C3ACDE404ull, 0x84F1F656379C1A3ull, 0x85AAC367CC487B1ull, 0x8664915B923FBA0ull,
+    0x871F61969E8D101ull, 0x87DB357FF698D79ull, 0x88980E8092DA852ull, 0x8955EE03618E5FEull, 0x8A14D575496EFDAull,
+    0x8AD4C6452C72892ull, 0x8B95C1E3EA8BD6Eull, 0x8C57C9C4646F4DEull, 0x8D1ADF5B7E5BA9Eull, 0x8DDF042022E69CDull,
+    0x8EA4398B45CD53Cull, 0x8F6A8117E6C8E5Cull, 0x9031DC431466B1Eull, 0x90FA4C8BEEE4B13ull, 0x91C3D373AB11C33ull,
+    0x928E727D9531F9Bull, 0x935A2B2F13E6E93ull, 0x9426FF0FAB1C04Bull, 0x94F4EFA8FEF7096ull, 0x95C3FE86D6CC7FFull,
+    0x96942D3720185A0ull, 0x97657D49F17AB09ull, 0x9837F0518DB8A97ull, 0x990B87E266C189Bull, 0x99E0459320B7FA6ull,
+    0x9AB62AFC94FF865ull, 0x9B8D39B9D54E554ull, 0x9C6573682EC32C3ull, 0x9D3ED9A72CFFB75ull, 0x9E196E189D47242ull,
+    0x9EF5326091A111Bull, 0x9FD228256400DD0ull, 0xA0B0510FB9714FCull, 0xA18FAECA8544B6Eull, 0xA27043030C49682ull,
+    0xA3520F68E802BB9ull, 0xA43515AE09E680Aull, 0xA5195786BE9EF34ull, 0xA5FED6A9B15138Full, 0xA6E594CFEEE86B2ull,
+    0xA7CD93B4E965357ull, 0xA8B6D5167B320E1ull, 0xA9A15AB4EA7C0F0ull, 0xAA8D2652EC90763ull, 0xAB7A39B5A93ED33ull,
+    0xAC6896A4BE3FE93ull, 0xAD583EEA42A14ACull, 0xAE493452CA35B81ull, 0xAF3B78AD690A437ull, 0xB02F0DCBB6E0458ull,
+    0xB123F581D2AC259ull, 0xB21A31A66618FE4ull, 0xB311C412A911249ull, 0xB40AAEA2654B984ull, 0xB504F333F9DE648ull,
+    0xB60093A85ED5F77ull, 0xB6FD91E328D1779ull, 0xB7FBEFCA8CA41E8ull, 0xB8FBAF4762FB9EFull, 0xB9FCD2452C0B9DFull,
+    0xBAFF5AB2133E460ull, 0xBC034A7EF2E9FB1ull, 0xBD08A39F580C36Cull, 0xBE0F6809860993Eull, 0xBF1799B67A73108ull,
+    0xC0213AA1F0D08DBull, 0xC12C4CCA6670945ull, 0xC238D2311E3D667ull, 0xC346CCDA2497640ull, 0xC4563ECC5334CB3ull,
+    0xC5672A115506DAEull, 0xC67990B5AA245F8ull, 0xC78D74C8ABB9B16ull, 0xC8A2D85C8FFE2C4ull, 0xC9B9BD866E2F27Aull,
+    0xCAD2265E4290775ull, 0xCBEC14FEF2727C6ull, 0xCD078B86503DCDDull, 0xCE248C151F8480Eull, 0xCF4318CF191918Cull,
+    0xD06333DAEF2B259ull, 0xD184DF6251699ACull, 0xD2A81D91F12AE46ull, 0xD3CCF099859AC38ull, 0xD4F35AABCFEDFA2ull,
+    0xD61B5DFE9F9BCE0ull, 0xD744FCCAD69D6AFull, 0xD870394C6DB32C8ull, 0xD99D15C278AFD7Bull, 0xDACB946F2AC9CC7ull,
+    0xDBFBB797DAF2375ull, 0xDD2D818508324C2ull, 0xDE60F4825E0E912ull, 0xDF9612DEB8F0442ull, 0xE0CCDEEC2A94E11ull,
+    0xE2055AFFFE83D37ull, 0xE33F8972BE8A5A5ull, 0xE47B6CA0373DA89ull, 0xE5B906E77C8348Bull, 0xE6F85AAAEE1FCE2ull,
+    0xE8396A503C4BDC7ull, 0xE97C38406C4F8C5ull, 0xEAC0C6E7DD24393ull, 0xEC0718B64C1CBDEull, 0xED4F301ED9942B8ull,
+    0xEE990F980DA3026ull, 0xEFE4B99BDCDAF5Dull, 0xF13230A7AD09451ull, 0xF281773C59FFB14ull, 0xF3D28FDE3A641A6ull,
+    0xF5257D152486CC3ull, 0xF67A416C733F847ull, 0xF7D0DF730AD13BCull, 0xF92959BB5DD4BA7ull, 0xFA83B2DB722A034ull,
+    0xFBDFED6CE5F09C5ull, 0xFD3E0C0CF486C17ull, 0xFE9E115C7B8F885ull,
 };
 
+// Logits in shared memory.
 template <int kDtype>
-__device__ __forceinline__ float logit(const void* p, int64_t i) {
-    if (kDtype == HC_DTYPE_FP32) return static_cast<const float*>(p)[i];
-    const uint16_t u = static_cast<const uint16_t*>(p)[i];
+__device__ __forceinline__ float logit(const unsigned char* p, int i) {
+    if (kDtype == HC_DTYPE_FP32) return reinterpret_cast<const float*>(p)[i];
+    const uint16_t u = reinterpret_cast<const uint16_t*>(p)[i];
     return kDtype == HC_DTYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
 }
 
-// log2(e) / T in two floats.
+// A number that grows with x, without the bits that a 16-bit type's fp32 patterns do not use.
+template <int kDtype>
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return kDtype == HC_DTYPE_BF16 ? k >> 16 : kDtype == HC_DTYPE_FP16 ? k >> 13 : k;
+}
+
+// A row's temperature and largest logit, as the weights need them.
 struct Heat {
-    float hi, lo;
+    float c, c_low, a, rest;                 // c in two floats; 1.5 2^23 - rint(M c); what makes g(M) 0
+    float top, deep;                         // M; the logit below which weights are 0
+    float z, z_low;                          // c / 128 (for the slow way)
+    bool far;                                // M c is beyond what a rounds well
 };
-__device__ __forceinline__ Heat heat_of(float t) {
-    const double c = 1.4426950408889634 / static_cast<double>(t);
+__device__ __forceinline__ Heat heat_of(float t, float top) {
     Heat h;
-    h.hi = static_cast<float>(c);
-    h.lo = static_cast<float>(c - static_cast<double>(h.hi));
+    const double one = 1.4426950408889634 / static_cast<double>(t);
+    const double c = one * kSteps;
+    h.c = static_cast<float>(c), h.c_low = static_cast<float>(c - static_cast<double>(h.c));
+    // M's own weight is 2^45: its m is 0, and so is its g to 2^-25, whose p is held as 0
+    const double at = static_cast<double>(h.c) * static_cast<double>(top), whole = rint(at);
+    h.z = static_cast<float>(one), h.z_low = static_cast<float>(one - static_cast<double>(h.z));
+    h.a = kRound - static_cast<float>(whole);
+    h.rest = static_cast<float>(whole - at - static_cast<double>(h.c_low) * static_cast<double>(top));
+    h.top = top;
+    h.deep = fmaxf(static_cast<float>(static_cast<double>(top) + static_cast<double>(kDeep) / one), -kTop);    // never -inf
+    h.far = !(fabs(at) < 4000000.0 - 47.0 * kSteps);
     return h;
 }
 
-// The weight of logit x beside the largest, top, in multiples of 2^-45; x <= top, top finite.
-__device__ __forceinline__ uint64_t weight(float x, float top, Heat c, const uint64_t* powers) {
-    const float d = __fsub_rn(x, top);
-    const float z = __fmul_rn(d, c.hi);
-    if (!(z > -47.f)) return 0;
+// 2^(m / 128 + g / 128) in multiples of 2^-45, |g| <= 1.2, -47 128 <= m <= 1.
+__device__ __forceinline__ uint64_t power(int m, float g, const uint64_t* powers) {
+    const float p = g * fmaf(g, fmaf(g, fmaf(g, 3.5830323054e-11f, 2.6466421444e-08f), 1.4662262388e-05f), 5.4152123481e-03f);
+    const int part = __float_as_int(fmaf(p, 536870912.f, kRound)) - __float_as_int(kRound);      // 2^29 p
+    const uint64_t t = powers[m & (kSteps - 1)];
+    const int64_t more = static_cast<int64_t>(static_cast<int>(t >> 29)) * part;                 // 2^30 2^29
+    return (t + static_cast<uint64_t>(more)) >> (59 - kUnitBits - (m >> 7));
+}
+// Where M c is so large that the first way loses bits: from the difference to M, in two floats.
+__device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const uint64_t* powers) {
+    const float d = __fsub_rn(x, top), z = __fmul_rn(d, c);
+    if (!(z > kDeep)) return 0;
     const float b = __fsub_rn(d, x);
     const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));     // x - top = d + dl
-    const float zl = fmaf(dl, c.hi, fmaf(d, c.lo, fmaf(d, c.hi, -z)));
-    const int m = __float2int_rn(z * 32.f);
-    const float g = fmaf(static_cast<float>(m), -1.f / 32.f, z) + zl;
-    const float p = g * fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), kLn2);
-    const uint64_t t = powers[m & 31];
-    const int64_t more = static_cast<int64_t>(static_cast<int>(t >> 15)) * __float2int_rn(p * 68719476736.f);   // 2^30 2^36
-    const uint64_t w = t + static_cast<uint64_t>(more >> 21);
-    const int down = -(m >> 5);
-    return down == 0 ? w : (w + (1ull << (down - 1))) >> down;
+    const float zl = fmaf(dl, c, fmaf(d, c_low, fmaf(d, c, -z)));
+    const int m = __float2int_rn(z * kSteps);
+    return power(m, fmaf(z, kSteps, -static_cast<float>(m)) + zl * kSteps, powers);
+}
+__device__ __forceinline__ uint64_t weight(float x, const Heat& h, const uint64_t* powers) {
+    if (h.far) return weight_far(x, h.top, h.z, h.z_low, powers);
+    if (!(x >= h.deep)) return 0;
+    const float v = fmaf(x, h.c, h.a);
+    const float g = fmaf(x, h.c, h.a - v) + fmaf(x, h.c_low, h.rest);
+    return power(__float_as_int(v) - __float_as_int(kRound), g, powers);
 }
 
-// A logit and its index in one whole number: larger logits first, of equal ones lower ids.
-__device__ __forceinline__ uint64_t rank_of(float x, int id) {
-    uint32_t u = __float_as_uint(x + 0.0f);
-    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return (static_cast<uint64_t>(u) << kIdBits) | static_cast<uint32_t>(HC_SAMPLE_MAX_VOCAB - 1 - id);
-}
-
-__device__ __forceinline__ uint64_t block_sum(uint64_t x, uint64_t* buffer) {
+template <typename T>
+__device__ __forceinline__ T warp_sum(T x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0;
-    for (int w = 0; w < kWarps; ++w) x += buffer[w];
     return x;
 }
-__device__ __forceinline__ uint64_t block_max(uint64_t x, uint64_t* buffer) {
+// Sums of the lanes up to and with this one.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x, int lane) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const uint64_t o = __shfl_xor_sync(~0u, x, d);
-        x = x > o ? x : o;
+    for (int d = 1; d < 32; d <<= 1) {
+        const T y = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += y;
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0;
-    for (int w = 0; w < kWarps; ++w) x = buffer[w] > x ? buffer[w] : x;
     return x;
 }
 
-// A CTA a row. Every border is found by bisection: the largest rank down to which the logits are
-// as many, or as heavy, as the filter lets stay; the first id up to which they are as heavy as the
-// uniform number asks.
+struct Shared {
+    uint64_t powers[kSteps];
+    uint64_t mass[2][kBins];                 // of a step's bins, two steps' in turn
+    unsigned count[2][kBins];
+    // what a CTA tells the others
+    float top;
+    int bad, first;
+    uint64_t total;
+    uint64_t listed_mass;
+    unsigned listed;
+    uint64_t kept;                           // beside the equal ones at the border
+    unsigned ties;
+    // within the CTA
+    uint64_t warp_mass[kWarps];
+    unsigned warp_count[kWarps];
+    uint64_t before_mass, in_mass;           // of the bin with the border
+    unsigned before, in;
+    int bin;
+    int warp_listed[kWarps];
+};
+
+// Of equal logits at the border `key` the first `ties` stay, of smaller ones none.
+struct Cut {
+    uint32_t key;
+    unsigned ties;
+    uint64_t above;                          // weight of those above
+};
+
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, int* status) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int segment_bytes, int* status) {
+    constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
+    __shared__ Shared s;
+    extern __shared__ __align__(16) unsigned char smem[];
+    unsigned char* segment = smem;
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + segment_bytes);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / ctas, rank = blockIdx.x % ctas;
     begin_early();
-    __shared__ uint64_t buffer[kWarps], powers[32];
-    const int row = blockIdx.x, tid = threadIdx.x;
+    // (the whole cluster has one row, so that all of it leaves together)
     if (!HC_IN_RANGE(row, 1, a.tokens, status)) return;
-    constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2;
-    const void* x = static_cast<const unsigned char*>(a.logits) + row * a.row * kItem;
-    if (tid < 32) powers[tid] = kPowers[tid];
+
+    // ---- the CTA's part of the row: whole vectors of 16 bytes, with -inf for what lies around the row
+    const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.row * kItem;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15) / kItem;
+    const int vectors = (shift + a.vocab + kN - 1) / kN;
+    const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), v1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
+    const int id0 = v0 * kN - shift;             // the id of local index 0
+    float most = -CUDART_INF_F;
+    {
+        const uint4* from = reinterpret_cast<const uint4*>(x - shift * kItem) + v0;
+        uint4* to = reinterpret_cast<uint4*>(segment);
+        constexpr uint32_t kNothing = kDtype == HC_DTYPE_FP32 ? 0xFF800000u : kDtype == HC_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+        auto bring = [&](int i) {
+            const int id = id0 + i * kN;
+            if (id >= 0 && id + kN <= a.vocab) return ldg_stream_v4(from + i);
+            uint32_t w[4] = {kNothing, kNothing, kNothing, kNothing};
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                if (id + e < 0 || id + e >= a.vocab) continue;           // in every build
+                if (kItem == 4) {
+                    w[e % 4] = reinterpret_cast<const uint32_t*>(x)[id + e];
+                } else {
+                    const uint32_t y = reinterpret_cast<const uint16_t*>(x)[id + e];
+                    w[(e / 2) % 4] = (e & 1) ? (w[(e / 2) % 4] & 0xFFFFu) | (y << 16) : (w[(e / 2) % 4] & 0xFFFF0000u) | y;
+                }
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        auto put = [&](int i, const uint4& v) {
+            to[i] = v;
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (kDtype == HC_DTYPE_FP32) {
+                    most = max_nan(most, __uint_as_float(w[e]));
+                } else {
+                    const float2 y = widen2<kDtype>(w[e]);
+                    most = max_nan(most, max_nan(y.x, y.y));
+                }
+            }
+        };
+        const int n = v1 - v0;
+        int i = tid;
+        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
+            uint4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = bring(i + e * kThreads);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put(i + e * kThreads, v[e]);
+        }
+        for (; i < n; i += kThreads) put(i, bring(i));
+    }
     const float u = a.uniform[row], t = a.temperature ? a.temperature[row] : 1.f;
     const float p = a.top_p ? a.top_p[row] : 1.f, least = a.min_p ? a.min_p[row] : 0.f;
     const int k = a.top_k ? a.top_k[row] : 0;
+    bool bad = !(u == u && p == p && least == least) || !(fabsf(t) <= kTop);
+    for (int i = tid; i < kSteps; i += kThreads) s.powers[i] = kPowers[i];
+    for (int i = tid; i < kBins; i += kThreads) s.count[0][i] = s.count[1][i] = 0, s.mass[0][i] = s.mass[1][i] = 0;
 
-    uint64_t best = 0;
-    bool bad = !(u == u && p == p && least == least) || !(fabsf(t) <= 3.402823466e38f);
-    for (int i = tid; i < a.vocab; i += kThreads) {
-        const float y = logit<kDtype>(x, i);
-        bad |= !(y <= 3.402823466e38f);
-        const uint64_t r = rank_of(y, i);
-        best = r > best ? r : best;
+    // ---- the largest logit
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) most = max_nan(most, __shfl_xor_sync(~0u, most, d));
+    if (lane == 0) s.warp_count[warp] = __float_as_uint(most);
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kWarps; ++w) most = max_nan(most, __uint_as_float(s.warp_count[w]));
+        s.top = most;
     }
-    best = block_max(best, buffer);
-    bad = __syncthreads_or(bad);
-    const int first = HC_SAMPLE_MAX_VOCAB - 1 - static_cast<int>(best & (HC_SAMPLE_MAX_VOCAB - 1));
-    const float top = logit<kDtype>(x, first);
-    if (bad || top == -CUDART_INF_F || t < 5.421010862427522e-20f) {
-        const bool none = bad || top == -CUDART_INF_F;
+    cluster.sync();
+    float top = -CUDART_INF_F;
+    for (int r = 0; r < ctas; ++r) top = max_nan(top, cluster.map_shared_rank(&s, r)->top);
+    bad = bad || !(fabsf(top) <= kTop);
+    // each warp's part of the segment
+    const int all = (v1 - v0) * kN, per = ((v1 - v0 + kWarps - 1) / kWarps) * kN;
+    const int begin = min(warp * per, all), end = min(begin + per, all);
+    if (bad || t < 5.421010862427522e-20f) {
+        // nothing, or the first of the largest
+        int first = 0x7FFFFFFF;
+        if (!bad)
+            for (int i = begin + lane; i < end; i += 32)
+                if (logit<kDtype>(segment, i) == top) first = min(first, id0 + i);
+        first = __reduce_min_sync(~0u, first);
+        if (lane == 0) s.warp_listed[warp] = first;
+        __syncthreads();
         if (tid == 0) {
-            a.ids[row] = none ? -1 : first;
-            a.logprob[row] = none ? CUDART_NAN_F : 0.f;
+            for (int w = 1; w < kWarps; ++w) first = min(first, s.warp_listed[w]);
+            s.first = first;
         }
+        cluster.sync();
+        if (rank == 0 && tid == 0) {
+            for (int r = 1; r < ctas; ++r) first = min(first, cluster.map_shared_rank(&s, r)->first);
+            a.ids[row] = bad ? -1 : first;
+            a.logprob[row] = bad ? CUDART_NAN_F : 0.f;
+        }
+        cluster.sync();
         return;
     }
-    const Heat heat = heat_of(t);
-    // count or mass of the logits of rank `cut` and above, up to id `last`, that weigh `low` at least
-    auto count = [&](uint64_t cut) {
-        uint64_t n = 0;
-        for (int i = tid; i < a.vocab; i += kThreads) n += rank_of(logit<kDtype>(x, i), i) >= cut;
-        return block_sum(n, buffer);
-    };
-    auto mass = [&](uint64_t cut, uint64_t low, int last) {
-        uint64_t n = 0;
-        for (int i = tid; i <= last; i += kThreads) {
-            const float y = logit<kDtype>(x, i);
-            const uint64_t w = weight(y, top, heat, powers);
-            if (rank_of(y, i) >= cut && w >= low) n += w;
+    const Heat heat = heat_of(t, top);
+    const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1.f;
+    // sums of a value over the CTA, told to the others
+    auto tell = [&](uint64_t mass, unsigned count, uint64_t* to_mass, unsigned* to_count) {
+        mass = warp_sum(mass);
+        count = __reduce_add_sync(~0u, count);
+        if (lane == 0) s.warp_mass[warp] = mass, s.warp_count[warp] = count;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 1; w < kWarps; ++w) mass += s.warp_mass[w], count += s.warp_count[w];
+            *to_mass = mass;
+            if (to_count) *to_count = count;
         }
-        return block_sum(n, buffer);
     };
-    uint64_t cut = 0;
-    if (k > 0 && k < a.vocab) {
-        for (int bit = 31 + kIdBits; bit >= 0; --bit)
-            if (count(cut | 1ull << bit) >= static_cast<uint64_t>(k)) cut |= 1ull << bit;
-    }
-    if (p < 1.f) {
-        const double part = ceil(static_cast<double>(fmaxf(p, 0.f)) * static_cast<double>(mass(cut, 0, a.vocab - 1)));
-        const uint64_t want = part < 1.0 ? 1 : static_cast<uint64_t>(part);
-        uint64_t to = 0;
-        for (int bit = 31 + kIdBits; bit >= 0; --bit) {
-            const uint64_t next = to | 1ull << bit;
-            if (next <= cut || mass(next, 0, a.vocab - 1) >= want) to = next;
+
+    // ---- what stays is listed
+    bool listed = false;
+    int n = end - begin;                         // logits that this warp goes through
+    uint16_t* mine = list + begin;
+    auto entry = [&](int i) { return listed ? static_cast<int>(mine[i]) : begin + i; };
+    Cut cut = {0, 0, 0};
+    int turn = 0;                                // bins of the step
+    // Sums a step's bins over the cluster and finds the one in which the border lies: with the sums
+    // before it and in it.
+    auto find_bin = [&](bool count, uint64_t want) {
+        cluster.sync();
+        uint64_t mass = 0;
+        unsigned number = 0;
+        for (int r = 0; r < ctas; ++r) {
+            const Shared* o = cluster.map_shared_rank(&s, r);
+            mass += o->mass[turn][tid], number += o->count[turn][tid];
         }
-        cut = to > cut ? to : cut;
+        // the other bins, read by all in the step before, are free for the next
+        turn ^= 1;
+        s.count[turn][tid] = 0, s.mass[turn][tid] = 0;
+        uint64_t upto = warp_scan(mass, lane);
+        unsigned numbers = warp_scan(number, lane);
+        if (lane == 31) s.warp_mass[warp] = upto, s.warp_count[warp] = numbers;
+        if (tid == 0) s.bin = -1;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += s.warp_mass[w], numbers += s.warp_count[w];
+        const bool here = count ? numbers >= want && numbers - number < want : upto >= want && upto - mass < want;
+        if (here) s.bin = tid, s.before_mass = upto - mass, s.in_mass = mass, s.before = numbers - number, s.in = number;
+        __syncthreads();
+    };
+    if (by_count || by_mass) {
+        // an eighth of the logits, by how far they lie below the largest: the bins are octaves / 10
+        const float width = -kDeep / kBins * 0.6931472f * t;            // of a bin, in logits
+        const float per_logit = 1.f / width;
+        auto depth = [&](float y) { return (top - y) * per_logit; };
+        for (int i = tid; i < all / 8; i += kThreads) {
+            const float z = depth(logit<kDtype>(segment, i * 8 + (i & 7)));
+            if (z < static_cast<float>(kBins)) atomicAdd(&s.count[turn][min(static_cast<int>(z), kBins - 1)], 1u);
+        }
+        uint64_t total = 0;
+        if (!by_count)
+            for (int i = begin + lane; i < end; i += 32) total += weight(logit<kDtype>(segment, i), heat, s.powers);
+        tell(total, 0, &s.total, nullptr);
+        // turned into weights of whole bins once they are summed: see below
+        cluster.sync();
+        total = 0;
+        for (int r = 0; r < ctas; ++r) total += cluster.map_shared_rank(&s, r)->total;
+        unsigned number = 0;
+        for (int r = 0; r < ctas; ++r) number += cluster.map_shared_rank(&s, r)->count[turn][tid];
+        turn ^= 1;
+        const float share = 8.f * static_cast<float>(number) * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins));
+        uint64_t upto = warp_scan(by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f), lane);
+        if (lane == 31) s.warp_mass[warp] = upto;
+        if (tid == 0) s.bin = kBins - 1;
+        __syncthreads();
+        uint64_t sum = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) upto += sum;
+            sum += s.warp_mass[w];
+        }
+        uint64_t want = static_cast<uint64_t>(k) + k / 4 + 64;
+        uint64_t goal = 0;                       // of a top-p alone
+        if (!by_count) {
+            const double part = ceil(static_cast<double>(fmaxf(p, 0.f)) * static_cast<double>(total));
+            goal = part < 1.0 ? 1 : static_cast<uint64_t>(part);
+            // what may lie below the bound, a little less than the rest, from the estimate's end
+            const uint64_t rest = (total - goal) >> (kUnitBits - 30);
+            const uint64_t below = rest - rest / 8;
+            want = sum > below ? sum - below : 0;
+        }
+        if (upto >= want) atomicMin(&s.bin, tid);
+        __syncthreads();
+        float bound = top - static_cast<float>(s.bin + 1) * width;
+        for (int attempt = 0;; ++attempt) {
+            bound = attempt < 2 ? fmaxf(bound, heat.deep) : heat.deep;
+            int m = 0;
+            uint64_t mass = 0;
+            for (int i = begin; i < end; i += 32) {
+                const float y = i + lane < end ? logit<kDtype>(segment, i + lane) : -CUDART_INF_F;
+                const bool in = y >= bound;
+                const unsigned votes = __ballot_sync(~0u, in);
+                if (in) {
+                    mine[m + __popc(votes & ((1u << lane) - 1u))] = static_cast<uint16_t>(i + lane);
+                    if (!by_count) mass += weight(y, heat, s.powers);
+                }
+                m += __popc(votes);
+            }
+            listed = true;
+            n = m;
+            tell(mass, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
+            cluster.sync();
+            uint64_t have = 0;
+            for (int r = 0; r < ctas; ++r) {
+                const Shared* o = cluster.map_shared_rank(&s, r);
+                have += by_count ? o->listed : o->listed_mass;
+            }
+            __syncwarp();
+            if (have >= (by_count ? static_cast<uint64_t>(k) : goal)) break;
+            if (bound == heat.deep) {            // fewer have weight: all of them stay
+                if (by_count) break;
+                goal = have;
+                break;
+            }
+            // four times as deep, and six octaves; then to the end
+            bound = top - 4.f * (top - bound) - 65.f * width;
+            cluster.sync();                      // all have read what is told anew
+        }
+
+        // ---- borders
+        const float fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
+        auto coarse = [&](float y) { return min(static_cast<int>((top - y) * fine), kBins - 1); };
+        // of the listed logits above `over` (all, where that is 0): the value at which `want` is reached
+        auto border = [&](bool count, uint64_t want, uint32_t over, bool& found) {
+            auto add = [&](int bin, float y) {
+                atomicAdd(&s.count[turn][bin], 1u);
+                if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[turn][bin]), static_cast<unsigned long long>(weight(y, heat, s.powers)));
+            };
+            __syncthreads();                     // the bins are free
+            for (int i = lane; i < n; i += 32) {
+                const float y = logit<kDtype>(segment, entry(i));
+                if (key_of<kDtype>(y) > over) add(coarse(y), y);
+            }
+            find_bin(count, want);
+            Cut c = {0, 0, 0};
+            found = s.bin >= 0;
+            if (!found) return c;
+            const int first = s.bin;
+            uint64_t before_mass = s.before_mass;
+            unsigned before = s.before;
+            // the values of that bin, and what rounding may add to them
+            const float high = top - static_cast<float>(first) / fine, low = top - static_cast<float>(first + 1) / fine;
+            const float slack = 1e-5f * (fabsf(top) + fabsf(bound));
+            uint32_t hi = key_of<kDtype>(fminf(high + slack, top));
+            uint32_t lo = key_of<kDtype>(fmaxf((first == kBins - 1 ? bound : low) - slack, -kTop));
+            unsigned in = s.in;
+            uint64_t in_mass = s.in_mass;
+            while (hi > lo) {
+                const int bits = 32 - __clz(hi - lo), down = max(bits - kBinBits, 0);
+                __syncthreads();
+                for (int i = lane; i < n; i += 32) {
+                    const float y = logit<kDtype>(segment, entry(i));
+                    const uint32_t key = key_of<kDtype>(y);
+                    if (key > over && key >= lo && key <= hi && coarse(y) == first) add((hi - key) >> down, y);
+                }
+                find_bin(count, count ? want - before : want - before_mass);
+                if (s.bin < 0) break;            // (cannot be: what was summed is summed again)
+                before += s.before, before_mass += s.before_mass;
+                in = s.in, in_mass = s.in_mass;
+                hi -= static_cast<uint32_t>(s.bin) << down;
+                lo = max(lo, hi - ((1u << down) - 1u));
+            }
+            c.key = hi, c.above = before_mass;
+            if (count) {
+                c.ties = static_cast<unsigned>(want - before);
+            } else {
+                const uint64_t one = in > 0 ? in_mass / in : 1;
+                c.ties = one > 0 ? static_cast<unsigned>((want - before_mass + one - 1) / one) : in;
+            }
+            return c;
+        };
+        bool found;
+        if (by_count) cut = border(true, k, 0, found);
+        if (by_mass) {
+            uint64_t want = goal;
+            uint64_t tie = 0;
+            if (by_count) {
+                if (found) {
+                    // the weight of a value: its key's
+                    uint32_t u32 = kDtype == HC_DTYPE_BF16 ? cut.key << 16 : kDtype == HC_DTYPE_FP16 ? cut.key << 13 : cut.key;
+                    u32 = (u32 & 0x80000000u) ? (u32 & 0x7FFFFFFFu) : ~u32;
+                    if (kDtype == HC_DTYPE_BF16 && (u32 & 0x80000000u)) u32 &= 0xFFFF0000u;
+                    if (kDtype == HC_DTYPE_FP16 && (u32 & 0x80000000u)) u32 &= 0xFFFFE000u;
+                    tie = weight(__uint_as_float(u32), heat, s.powers);
+                    total = cut.above + cut.ties * tie;
+                } else {
+                    // all that have weight stay
+                    uint64_t mass = 0;
+                    for (int i = lane; i < n; i += 32) mass += weight(logit<kDtype>(segment, entry(i)), heat, s.powers);
+                    __syncthreads();
+                    tell(mass, 0, &s.total, nullptr);
+                    cluster.sync();
+                    total = 0;
+                    for (int r = 0; r < ctas; ++r) total += cluster.map_shared_rank(&s, r)->total;
+                }
+                const double part = ceil(static_cast<double>(fmaxf(p, 0.f)) * static_cast<double>(total));
+                want = part < 1.0 ? 1 : static_cast<uint64_t>(part);
+            }
+            if (by_count && found && want > cut.above) {
+                if (tie > 0) cut.ties = min(cut.ties, static_cast<unsigned>((want - cut.above + tie - 1) / tie));
+            } else {
+                const Cut more = border(false, want, by_count && found ? cut.key : 0, found);
+                if (found) cut = more;
+            }
+        }
     }
+
+    // ---- the sums of what stays, and the token
     uint64_t low = 1;
     if (least > 0.f) {
         low = static_cast<uint64_t>(ceil(static_cast<double>(fminf(least, 1.f)) * static_cast<double>(kOne)));
         low = low < 1 ? 1 : low;
     }
-    const uint64_t total = mass(cut, low, a.vocab - 1);
+    uint64_t mass = 0, tie = 0;
+    unsigned ties = 0;
+    for (int i = lane; i < n; i += 32) {
+        const float y = logit<kDtype>(segment, entry(i));
+        const uint32_t key = key_of<kDtype>(y);
+        if (key < cut.key) continue;
+        const uint64_t w = weight(y, heat, s.powers);
+        if (w < low) continue;
+        if (key > cut.key || cut.key == 0) mass += w;
+        else ++ties, tie = w;
+    }
+    // (the equal ones' weight, where this warp has one)
+    __syncthreads();
+    {
+        const unsigned with = __ballot_sync(~0u, ties > 0);
+        if (with) tie = __shfl_sync(~0u, tie, __ffs(with) - 1);
+    }
+    tell(mass, ties, &s.kept, &s.ties);
+    if (tid == 0) s.total = 0;
+    __syncthreads();
+    if (lane == 0 && tie > 0) s.total = tie;     // the same from any warp
+    const uint64_t warp_mass = s.warp_mass[warp];
+    const unsigned warp_ties = s.warp_count[warp];
+    cluster.sync();
+    uint64_t total = 0;
+    unsigned left = cut.ties;
+    tie = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const uint64_t o = cluster.map_shared_rank(&s, r)->total;
+        tie = o > tie ? o : tie;
+    }
+    uint64_t before = 0, here = 0;               // the CTA's place in the sum
+    unsigned here_ties = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const Shared* o = cluster.map_shared_rank(&s, r);
+        const unsigned take = min(left, o->ties);
+        left -= take;
+        const uint64_t sum = o->kept + take * tie;
+        if (r == rank) before = total, here = sum, here_ties = take;
+        total += sum;
+    }
     const double at = floor(static_cast<double>(fmaxf(u, 0.f)) * static_cast<double>(total));
-    uint64_t below = at < static_cast<double>(total) ? static_cast<uint64_t>(at) : total - 1;
-    below = below < total ? below : total - 1;
-    int lo = 0, hi = a.vocab - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (mass(cut, low, mid) > below) hi = mid;
-        else lo = mid + 1;
+    uint64_t goal = at < static_cast<double>(total) ? static_cast<uint64_t>(at) : total - 1;
+    goal = min(goal, total - 1);
+    if (goal >= before && goal - before < here) {
+        // the warp's place in the CTA
+        uint64_t from = before;
+        unsigned allow = here_ties;
+        for (int w = 0; w < warp; ++w) {
+            const unsigned take = min(allow, s.warp_count[w]);
+            allow -= take;
+            from += s.warp_mass[w] + take * tie;
+        }
+        allow = min(allow, warp_ties);
+        if (goal >= from && goal - from < warp_mass + allow * tie) {
+            uint64_t sum = from;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                uint64_t w = 0;
+                bool equal = false;
+                float y = 0.f;
+                int index = 0;
+                if (i0 + lane < n) {
+                    index = entry(i0 + lane);
+                    y = logit<kDtype>(segment, index);
+                    const uint32_t key = key_of<kDtype>(y);
+                    if (key >= cut.key) w = weight(y, heat, s.powers);
+                    if (w < low) w = 0;
+                    equal = w > 0 && key == cut.key && cut.key != 0;
+                }
+                const unsigned votes = __ballot_sync(~0u, equal);
+                if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w = 0;
+                allow -= min(allow, static_cast<unsigned>(__popc(votes)));
+                const uint64_t upto = sum + warp_scan(w, lane);
+                const unsigned past = __ballot_sync(~0u, upto > goal);
+                if (past) {
+                    if (lane == __ffs(past) - 1) {
+                        a.ids[row] = id0 + index;
+                        a.logprob[row] = ((y - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
+                    }
+                    break;
+                }
+                sum = __shfl_sync(~0u, upto, 31);
+            }
+        }
     }
-    if (tid == 0) {
-        a.ids[row] = lo;
-        const float y = logit<kDtype>(x, lo);
-        const float z = (y - top) * heat.hi * kLn2;
-        a.logprob[row] = z - logf(static_cast<float>(total) * (1.f / kOne));
+    cluster.sync();                              // no CTA leaves while another reads its memory
+}
+
+// CTAs of a row: as many as keep a part within 16384 logits, and twice, four times as many where there
+// are too few rows to fill the GPU and a part stays above 2048.
+int row_ctas(int sm_count, int rows, int vocab) {
+    int n = 1;
+    while (n < kMaxCtas && vocab > n * 16384) n *= 2;
+    while (n < kMaxCtas && static_cast<int64_t>(rows) * n * 2 <= sm_count && vocab > n * 2 * 2048) n *= 2;
+    return n;
+}
+
+template <int kDtype>
+cudaError_t call(const Ctx& ctx, const SampleArgs& a, cudaStream_t st) {
+    constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
+    const int ctas = row_ctas(ctx.sm_count, a.tokens, a.vocab);
+    // a row may begin anywhere in its first vector
+    const int vectors = ((a.vocab + 2 * kN - 2) / kN + ctas - 1) / ctas;
+    const size_t smem = static_cast<size_t>(vectors) * (16 + 2 * kN);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.tokens) * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sample_kernel<kDtype>, a, ctas, vectors * 16, ctx.s.status);
+}
+
+// A launch has at most 2^31 - 1 CTAs.
+template <int kDtype>
+cudaError_t call_in_parts(const Ctx& ctx, const SampleArgs& a, cudaStream_t st) {
+    constexpr int kRows = 1 << 27, kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2;
+    for (int64_t at = 0; at < a.tokens; at += kRows) {
+        SampleArgs b = a;
+        b.tokens = static_cast<int>(a.tokens - at < kRows ? a.tokens - at : kRows);
+        b.logits = static_cast<const unsigned char*>(a.logits) + at * a.row * kItem;
+        b.uniform += at, b.ids += at, b.logprob += at;
+        if (a.temperature) b.temperature += at;
+        if (a.top_k) b.top_k += at;
+        if (a.top_p) b.top_p += at;
+        if (a.min_p) b.min_p += at;
+        const cudaError_t e = call<kDtype>(ctx, b, st);
+        if (e != cudaSuccess) return e;
     }
+    return cudaSuccess;
+}
+
+template <int kDtype>
+cudaError_t allow_smem() {
+    constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
+    const int vectors = ((HC_SAMPLE_MAX_VOCAB + 2 * kN - 2) / kN + kMaxCtas - 1) / kMaxCtas;
+    return cudaFuncSetAttribute(sample_kernel<kDtype>, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors * (16 + 2 * kN));
 }
 
 }  // namespace
 
+cudaError_t sample_setup() {
+    cudaError_t e = allow_smem<HC_DTYPE_BF16>();
+    if (e == cudaSuccess) e = allow_smem<HC_DTYPE_FP16>();
+    if (e == cudaSuccess) e = allow_smem<HC_DTYPE_FP32>();
+    return e;
+}
+
 cudaError_t launch_sample_tokens(const Ctx& ctx, const SampleArgs& a, int dtype, cudaStream_t st) {
     switch (dtype) {
-        case HC_DTYPE_BF16: return launch_early(sample_kernel<HC_DTYPE_BF16>, dim3(a.tokens), kThreads, 0, st, a, ctx.s.status);
-        case HC_DTYPE_FP16: return launch_early(sample_kernel<HC_DTYPE_FP16>, dim3(a.tokens), kThreads, 0, st, a, ctx.s.status);
-        default: return launch_early(sample_kernel<HC_DTYPE_FP32>, dim3(a.tokens), kThreads, 0, st, a, ctx.s.status);
+        case HC_DTYPE_BF16: return call_in_parts<HC_DTYPE_BF16>(ctx, a, st);
+        case HC_DTYPE_FP16: return call_in_parts<HC_DTYPE_FP16>(ctx, a, st);
+        default: return call_in_parts<HC_DTYPE_FP32>(ctx, a, st);
     }
 }
 
