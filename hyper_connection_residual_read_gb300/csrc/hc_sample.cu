@@ -14,10 +14,11 @@
 //
 // * the largest logit; for a top-p without a top-k also the sum of all weights
 // * an estimate, from an eighth of the logits, of a bound above which what stays must lie, and a list
-//   of the logits above it (where it turns out too high, of all that have weight)
-// * counts or weights of the listed logits by value, in 512 bins; those of the bin in which the border
-//   lies again, in bins 512 times as narrow, until one value is left. Of equal logits the first ones in
-//   the order of their ids stay, so that a border is a value and how many of it stay.
+//   of the logits above it
+// * counts and weights of the listed logits by value, in 512 bins (where they are too few, a deeper
+//   bound is taken, at last that of all that have weight); those of the bin in which the border lies
+//   again, in bins 512 times as narrow, until one value is left. Of equal logits the first ones in the
+//   order of their ids stay, so that a border is a value and how many of it stay.
 // * the sum of what stays by CTA, warp and lane, in the order of the ids, down to the token.
 //
 // Each step ends in a barrier of the cluster, after which every CTA reads what the others found and
@@ -96,6 +97,14 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return kDtype == HC_DTYPE_BF16 ? k >> 16 : kDtype == HC_DTYPE_FP16 ? k >> 13 : k;
 }
 
+template <int kDtype>
+__device__ __forceinline__ float value_of(uint32_t key) {
+    // (a negative value's pattern is the complement of its key: its unused bits are zeros)
+    constexpr int kUnused = kDtype == HC_DTYPE_BF16 ? 16 : kDtype == HC_DTYPE_FP16 ? 13 : 0;
+    const uint32_t k = key << kUnused;
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k & ~((1u << kUnused) - 1u));
+}
+
 // A row's temperature and largest logit, as the weights need them.
 struct Heat {
     float c, c_low, a, rest;                 // c in two floats; 1.5 2^23 - rint(M c); what makes g(M) 0
@@ -103,46 +112,61 @@ struct Heat {
     float z, z_low;                          // c / 128 (for the slow way)
     bool far;                                // M c is beyond what a rounds well
 };
+// (In fp32 alone: 64-bit operations took 15 us of a row's 40.)
 __device__ __forceinline__ Heat heat_of(float t, float top) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;             // log2(e)
     Heat h;
-    const double one = 1.4426950408889634 / static_cast<double>(t);
-    const double c = one * kSteps;
-    h.c = static_cast<float>(c), h.c_low = static_cast<float>(c - static_cast<double>(h.c));
+    h.z = kHi / t;
+    h.z_low = (fmaf(-h.z, t, kHi) + kLo) / t;
+    h.c = h.z * kSteps, h.c_low = h.z_low * kSteps;
     // M's own weight is 2^45: its m is 0, and so is its g to 2^-25, whose p is held as 0
-    const double at = static_cast<double>(h.c) * static_cast<double>(top), whole = rint(at);
-    h.z = static_cast<float>(one), h.z_low = static_cast<float>(one - static_cast<double>(h.z));
-    h.a = kRound - static_cast<float>(whole);
-    h.rest = static_cast<float>(whole - at - static_cast<double>(h.c_low) * static_cast<double>(top));
+    const float at = h.c * top;
+    float whole = rintf(at);
+    whole += fmaf(top, h.c, kRound - whole) - kRound;
+    h.a = kRound - whole;
+    h.rest = fmaf(-h.c_low, top, -fmaf(top, h.c, -whole));
     h.top = top;
-    h.deep = fmaxf(static_cast<float>(static_cast<double>(top) + static_cast<double>(kDeep) / one), -kTop);    // never -inf
-    h.far = !(fabs(at) < 4000000.0 - 47.0 * kSteps);
+    h.deep = fmaxf(fmaf(t, kDeep * kLn2, top), -kTop);                   // never -inf
+    h.far = !(fabsf(at) < 4000000.f);
     return h;
 }
 
-// 2^(m / 128 + g / 128) in multiples of 2^-45, |g| <= 1.2, -47 128 <= m <= 1.
-__device__ __forceinline__ uint64_t power(int m, float g, const uint64_t* powers) {
+// Whole numbers times an fp32 factor in [0, 1), rounded down or up, exactly.
+__device__ __forceinline__ uint64_t part_of(uint64_t x, float by, bool up) {
+    const uint32_t bits = __float_as_uint(by), e = bits >> 23;
+    const uint64_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+    const int down = e ? 150 - static_cast<int>(e) : 149;                // by = m 2^-down, 24 <= down
+    const uint64_t lo = x * m, hi = __umul64hi(x, m);
+    uint64_t r = 0, rest = lo | hi;
+    if (down < 64) r = (hi << (64 - down)) | (lo >> down), rest = lo << (64 - down);
+    else if (down < 128) r = down == 64 ? hi : hi >> (down - 64), rest = lo | (down == 64 ? 0 : hi << (128 - down));
+    return r + (up && rest != 0);
+}
+
+// 2^((m + g) / 128) in multiples of 2^-45, |g| <= 1.2, -47 128 <= m <= 1; m is given as the low bits of
+// `bits` = m + the pattern of kRound.
+__device__ __forceinline__ uint64_t power(int bits, float g, const uint64_t* powers) {
     const float p = g * fmaf(g, fmaf(g, fmaf(g, 3.5830323054e-11f, 2.6466421444e-08f), 1.4662262388e-05f), 5.4152123481e-03f);
     const int part = __float_as_int(fmaf(p, 536870912.f, kRound)) - __float_as_int(kRound);      // 2^29 p
-    const uint64_t t = powers[m & (kSteps - 1)];
-    const int64_t more = static_cast<int64_t>(static_cast<int>(t >> 29)) * part;                 // 2^30 2^29
-    return (t + static_cast<uint64_t>(more)) >> (59 - kUnitBits - (m >> 7));
+    const uint64_t t = powers[bits & (kSteps - 1)];
+    const uint64_t w = t + static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(t >> 29)) * part);      // 2^30 2^29
+    return w >> (59 - kUnitBits + (__float_as_int(kRound) >> 7) - (bits >> 7));
 }
-// Where M c is so large that the first way loses bits: from the difference to M, in two floats.
+// The weight of a logit, 0 below h.deep.
+__device__ __forceinline__ uint64_t weight(float x, const Heat& h, const uint64_t* powers) {
+    x = fmaxf(x, h.deep);
+    const float v = fmaf(x, h.c, h.a);
+    return power(__float_as_int(v), fmaf(x, h.c, h.a - v) + fmaf(x, h.c_low, h.rest), powers);
+}
+// Where M c is so large that this way loses bits: from the difference to M, in two floats.
 __device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const uint64_t* powers) {
     const float d = __fsub_rn(x, top), z = __fmul_rn(d, c);
     if (!(z > kDeep)) return 0;
     const float b = __fsub_rn(d, x);
     const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));     // x - top = d + dl
     const float zl = fmaf(dl, c, fmaf(d, c_low, fmaf(d, c, -z)));
-    const int m = __float2int_rn(z * kSteps);
-    return power(m, fmaf(z, kSteps, -static_cast<float>(m)) + zl * kSteps, powers);
-}
-__device__ __forceinline__ uint64_t weight(float x, const Heat& h, const uint64_t* powers) {
-    if (h.far) return weight_far(x, h.top, h.z, h.z_low, powers);
-    if (!(x >= h.deep)) return 0;
-    const float v = fmaf(x, h.c, h.a);
-    const float g = fmaf(x, h.c, h.a - v) + fmaf(x, h.c_low, h.rest);
-    return power(__float_as_int(v) - __float_as_int(kRound), g, powers);
+    const float v = fmaf(z, kSteps, kRound);
+    return power(__float_as_int(v), fmaf(z, kSteps, kRound - v) + zl * kSteps, powers);
 }
 
 template <typename T>
@@ -170,8 +194,6 @@ struct Shared {
     float top;
     int bad, first;
     uint64_t total;
-    uint64_t listed_mass;
-    unsigned listed;
     uint64_t kept;                           // beside the equal ones at the border
     unsigned ties;
     // within the CTA
@@ -183,9 +205,15 @@ struct Shared {
     int warp_listed[kWarps];
 };
 
-// Of equal logits at the border `key` the first `ties` stay, of smaller ones none.
+// A value of each CTA, one a lane (0 for lanes past them), brought at once.
+template <typename T, typename Get>
+__device__ __forceinline__ T of_ctas(cg::cluster_group& cluster, int ctas, int lane, Shared& s, Get get) {
+    return lane < ctas ? get(*cluster.map_shared_rank(&s, lane)) : T(0);
+}
+
+// Logits above `at` stay, and of those equal to it the first `ties`.
 struct Cut {
-    uint32_t key;
+    float at;
     unsigned ties;
     uint64_t above;                          // weight of those above
 };
@@ -272,8 +300,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         s.top = most;
     }
     cluster.sync();
-    float top = -CUDART_INF_F;
-    for (int r = 0; r < ctas; ++r) top = max_nan(top, cluster.map_shared_rank(&s, r)->top);
+    float top = cluster.map_shared_rank(&s, lane < ctas ? lane : 0)->top;
+#pragma unroll
+    for (int d = kMaxCtas / 2; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+    top = __shfl_sync(~0u, top, 0);
     bad = bad || !(fabsf(top) <= kTop);
     // each warp's part of the segment
     const int all = (v1 - v0) * kN, per = ((v1 - v0 + kWarps - 1) / kWarps) * kN;
@@ -315,58 +345,68 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
     };
 
-    // ---- what stays is listed
+    // The logits that this warp goes through, four a lane at a time: all of its part, or those listed.
     bool listed = false;
-    int n = end - begin;                         // logits that this warp goes through
+    int n = end - begin;
     uint16_t* mine = list + begin;
-    auto entry = [&](int i) { return listed ? static_cast<int>(mine[i]) : begin + i; };
-    Cut cut = {0, 0, 0};
-    int turn = 0;                                // bins of the step
-    // Sums a step's bins over the cluster and finds the one in which the border lies: with the sums
-    // before it and in it.
-    auto find_bin = [&](bool count, uint64_t want) {
-        cluster.sync();
-        uint64_t mass = 0;
-        unsigned number = 0;
-        for (int r = 0; r < ctas; ++r) {
-            const Shared* o = cluster.map_shared_rank(&s, r);
-            mass += o->mass[turn][tid], number += o->count[turn][tid];
+    auto index_of = [&](int i) { return listed ? static_cast<int>(mine[i]) : begin + i; };
+    auto each = [&](auto use) {
+        for (int i = lane; i < n; i += 128) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = i + 32 * e < n ? logit<kDtype>(segment, index_of(i + 32 * e)) : -CUDART_INF_F;
+            use(y);
         }
-        // the other bins, read by all in the step before, are free for the next
-        turn ^= 1;
-        s.count[turn][tid] = 0, s.mass[turn][tid] = 0;
-        uint64_t upto = warp_scan(mass, lane);
-        unsigned numbers = warp_scan(number, lane);
-        if (lane == 31) s.warp_mass[warp] = upto, s.warp_count[warp] = numbers;
-        if (tid == 0) s.bin = -1;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += s.warp_mass[w], numbers += s.warp_count[w];
-        const bool here = count ? numbers >= want && numbers - number < want : upto >= want && upto - mass < want;
-        if (here) s.bin = tid, s.before_mass = upto - mass, s.in_mass = mass, s.before = numbers - number, s.in = number;
-        __syncthreads();
     };
+    // and their weights, 0 for those at -inf
+    auto weigh = [&](const float (&y)[4], uint64_t (&w)[4]) {
+        if (heat.far) {
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+                const float x = e < 2 ? e == 0 ? y[0] : y[1] : e == 2 ? y[2] : y[3];
+                const uint64_t one = weight_far(x, top, heat.z, heat.z_low, s.powers);
+                if (e == 0) w[0] = one;
+                else if (e == 1) w[1] = one;
+                else if (e == 2) w[2] = one;
+                else w[3] = one;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = weight(y[e], heat, s.powers);
+        }
+    };
+    Cut cut = {-CUDART_INF_F, 0, 0};             // all stay
     if (by_count || by_mass) {
-        // an eighth of the logits, by how far they lie below the largest: the bins are octaves / 10
-        const float width = -kDeep / kBins * 0.6931472f * t;            // of a bin, in logits
+        int turn = 0;                            // bins of the step
+        // ---- an eighth of the logits, by how far they lie below the largest, in bins of an octave / 11
+        const float width = -kDeep / kBins * kLn2 * t;                  // of a bin, in logits
         const float per_logit = 1.f / width;
-        auto depth = [&](float y) { return (top - y) * per_logit; };
         for (int i = tid; i < all / 8; i += kThreads) {
-            const float z = depth(logit<kDtype>(segment, i * 8 + (i & 7)));
-            if (z < static_cast<float>(kBins)) atomicAdd(&s.count[turn][min(static_cast<int>(z), kBins - 1)], 1u);
+            const float z = (top - logit<kDtype>(segment, i * 8 + (i & 7))) * per_logit;
+            if (z < static_cast<float>(kBins)) atomicAdd(&s.count[0][min(static_cast<int>(z), kBins - 1)], 1u);
         }
         uint64_t total = 0;
-        if (!by_count)
-            for (int i = begin + lane; i < end; i += 32) total += weight(logit<kDtype>(segment, i), heat, s.powers);
+        auto add_up = [&](const float (&y)[4]) {
+            uint64_t w[4];
+            weigh(y, w);
+            total += (w[0] + w[1]) + (w[2] + w[3]);
+        };
+        if (!by_count) each(add_up);
         tell(total, 0, &s.total, nullptr);
-        // turned into weights of whole bins once they are summed: see below
         cluster.sync();
-        total = 0;
-        for (int r = 0; r < ctas; ++r) total += cluster.map_shared_rank(&s, r)->total;
+        total = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; }));
         unsigned number = 0;
-        for (int r = 0; r < ctas; ++r) number += cluster.map_shared_rank(&s, r)->count[turn][tid];
-        turn ^= 1;
+        {
+            unsigned theirs[kMaxCtas];
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) theirs[r] = r < ctas ? cluster.map_shared_rank(&s, r < ctas ? r : 0)->count[0][tid] : 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) number += theirs[r];
+        }
+        turn = 1;
         const float share = 8.f * static_cast<float>(number) * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins));
-        uint64_t upto = warp_scan(by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f), lane);
+        uint64_t mass = by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f);
+        uint64_t upto = warp_scan(mass, lane);
         if (lane == 31) s.warp_mass[warp] = upto;
         if (tid == 0) s.bin = kBins - 1;
         __syncthreads();
@@ -375,165 +415,187 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             if (w == warp) upto += sum;
             sum += s.warp_mass[w];
         }
-        uint64_t want = static_cast<uint64_t>(k) + k / 4 + 64;
-        uint64_t goal = 0;                       // of a top-p alone
+        uint64_t want = k;
+        uint64_t most_of = static_cast<uint64_t>(k) + k / 4 + 64;
         if (!by_count) {
-            const double part = ceil(static_cast<double>(fmaxf(p, 0.f)) * static_cast<double>(total));
-            goal = part < 1.0 ? 1 : static_cast<uint64_t>(part);
+            want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
             // what may lie below the bound, a little less than the rest, from the estimate's end
-            const uint64_t rest = (total - goal) >> (kUnitBits - 30);
+            const uint64_t rest = (total - want) >> (kUnitBits - 30);
             const uint64_t below = rest - rest / 8;
-            want = sum > below ? sum - below : 0;
+            most_of = sum > below ? sum - below : 0;
         }
-        if (upto >= want) atomicMin(&s.bin, tid);
+        if (upto >= most_of) atomicMin(&s.bin, tid);
         __syncthreads();
         float bound = top - static_cast<float>(s.bin + 1) * width;
+
+        // ---- the step's bins summed over the cluster, a bin a thread: its own, those up to it
+        unsigned upto_count = 0;
+        auto sum_bins = [&]() {
+            cluster.sync();
+            uint64_t masses[kMaxCtas];
+            unsigned numbers[kMaxCtas];
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) {
+                const Shared* o = cluster.map_shared_rank(&s, r < ctas ? r : 0);
+                masses[r] = by_mass && r < ctas ? o->mass[turn][tid] : 0;
+                numbers[r] = r < ctas ? o->count[turn][tid] : 0;
+            }
+            mass = number = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) mass += masses[r], number += numbers[r];
+            // the other bins, read by all in the step before, are free for the next
+            turn ^= 1;
+            s.count[turn][tid] = 0, s.mass[turn][tid] = 0;
+            upto = warp_scan(mass, lane), upto_count = warp_scan(number, lane);
+            if (lane == 31) s.warp_mass[warp] = upto, s.warp_count[warp] = upto_count;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) upto += s.warp_mass[w], upto_count += s.warp_count[w];
+        };
+        // the bin in which `goal` is reached: it, what lies before it and in it (false: none)
+        int bin;
+        uint64_t before_mass, in_mass;
+        unsigned before, in;
+        auto find_bin = [&](bool count, uint64_t goal) {
+            __syncthreads();
+            if (tid == 0) s.bin = -1;
+            __syncthreads();
+            const bool here = count ? upto_count >= goal && upto_count - number < goal : upto >= goal && upto - mass < goal;
+            if (here) s.bin = tid, s.before_mass = upto - mass, s.in_mass = mass, s.before = upto_count - number, s.in = number;
+            __syncthreads();
+            bin = s.bin, before_mass = s.before_mass, in_mass = s.in_mass, before = s.before, in = s.in;
+            return bin >= 0;
+        };
+        auto add = [&](int to, uint64_t w) {
+            atomicAdd(&s.count[turn][to], 1u);
+            if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[turn][to]), static_cast<unsigned long long>(w));
+        };
+
+        // ---- the list, and its bins by value
+        float fine = 0.f;
+        auto coarse = [&](float y) { return min(static_cast<int>((top - y) * fine), kBins - 1); };
+        bool found = false;
         for (int attempt = 0;; ++attempt) {
             bound = attempt < 2 ? fmaxf(bound, heat.deep) : heat.deep;
+            fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
             int m = 0;
-            uint64_t mass = 0;
-            for (int i = begin; i < end; i += 32) {
-                const float y = i + lane < end ? logit<kDtype>(segment, i + lane) : -CUDART_INF_F;
-                const bool in = y >= bound;
-                const unsigned votes = __ballot_sync(~0u, in);
-                if (in) {
-                    mine[m + __popc(votes & ((1u << lane) - 1u))] = static_cast<uint16_t>(i + lane);
-                    if (!by_count) mass += weight(y, heat, s.powers);
+            for (int i = begin; i < end; i += 128) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < end ? logit<kDtype>(segment, i + lane + 32 * e) : -CUDART_INF_F;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool stays = y[e] >= bound;
+                    const unsigned votes = __ballot_sync(~0u, stays);
+                    if (stays) mine[m + __popc(votes & ((1u << lane) - 1u))] = static_cast<uint16_t>(i + lane + 32 * e);
+                    m += __popc(votes);
                 }
-                m += __popc(votes);
             }
-            listed = true;
-            n = m;
-            tell(mass, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
-            cluster.sync();
-            uint64_t have = 0;
-            for (int r = 0; r < ctas; ++r) {
-                const Shared* o = cluster.map_shared_rank(&s, r);
-                have += by_count ? o->listed : o->listed_mass;
-            }
+            listed = true, n = m;
             __syncwarp();
-            if (have >= (by_count ? static_cast<uint64_t>(k) : goal)) break;
-            if (bound == heat.deep) {            // fewer have weight: all of them stay
-                if (by_count) break;
-                goal = have;
-                break;
-            }
+            each([&](const float (&y)[4]) {
+                uint64_t w[4] = {};
+                if (by_mass) weigh(y, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (y[e] >= bound) add(coarse(y[e]), w[e]);
+            });
+            sum_bins();
+            found = find_bin(by_count, want);
+            if (found || bound == heat.deep) break;             // (fewer have weight: all of them stay)
             // four times as deep, and six octaves; then to the end
             bound = top - 4.f * (top - bound) - 65.f * width;
-            cluster.sync();                      // all have read what is told anew
         }
 
-        // ---- borders
-        const float fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
-        auto coarse = [&](float y) { return min(static_cast<int>((top - y) * fine), kBins - 1); };
-        // of the listed logits above `over` (all, where that is 0): the value at which `want` is reached
-        auto border = [&](bool count, uint64_t want, uint32_t over, bool& found) {
-            auto add = [&](int bin, float y) {
-                atomicAdd(&s.count[turn][bin], 1u);
-                if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[turn][bin]), static_cast<unsigned long long>(weight(y, heat, s.powers)));
-            };
-            __syncthreads();                     // the bins are free
-            for (int i = lane; i < n; i += 32) {
-                const float y = logit<kDtype>(segment, entry(i));
-                if (key_of<kDtype>(y) > over) add(coarse(y), y);
-            }
-            find_bin(count, want);
-            Cut c = {0, 0, 0};
-            found = s.bin >= 0;
-            if (!found) return c;
-            const int first = s.bin;
-            uint64_t before_mass = s.before_mass;
-            unsigned before = s.before;
+        // ---- borders: the value at which `goal` is reached, in the bin that has been found
+        auto border = [&](bool count, uint64_t goal) {
             // the values of that bin, and what rounding may add to them
-            const float high = top - static_cast<float>(first) / fine, low = top - static_cast<float>(first + 1) / fine;
+            const int first = bin;
+            const float high = top - static_cast<float>(first) / fine, least_of = top - static_cast<float>(first + 1) / fine;
             const float slack = 1e-5f * (fabsf(top) + fabsf(bound));
             uint32_t hi = key_of<kDtype>(fminf(high + slack, top));
-            uint32_t lo = key_of<kDtype>(fmaxf((first == kBins - 1 ? bound : low) - slack, -kTop));
-            unsigned in = s.in;
-            uint64_t in_mass = s.in_mass;
+            uint32_t lo = key_of<kDtype>(fmaxf((first == kBins - 1 ? bound : least_of) - slack, -kTop));
+            uint64_t mass_above = before_mass;
+            unsigned above = before;
             while (hi > lo) {
-                const int bits = 32 - __clz(hi - lo), down = max(bits - kBinBits, 0);
-                __syncthreads();
-                for (int i = lane; i < n; i += 32) {
-                    const float y = logit<kDtype>(segment, entry(i));
-                    const uint32_t key = key_of<kDtype>(y);
-                    if (key > over && key >= lo && key <= hi && coarse(y) == first) add((hi - key) >> down, y);
-                }
-                find_bin(count, count ? want - before : want - before_mass);
-                if (s.bin < 0) break;            // (cannot be: what was summed is summed again)
-                before += s.before, before_mass += s.before_mass;
-                in = s.in, in_mass = s.in_mass;
-                hi -= static_cast<uint32_t>(s.bin) << down;
+                const int down = max(32 - __clz(hi - lo) - kBinBits, 0);
+                __syncthreads();                                // the bins are free
+                each([&](const float (&y)[4]) {
+                    bool in_it[4];
+                    uint32_t key[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        key[e] = key_of<kDtype>(y[e]);
+                        in_it[e] = y[e] >= bound && key[e] >= lo && key[e] <= hi && coarse(y[e]) == first;
+                    }
+                    if (!__any_sync(__activemask(), in_it[0] | in_it[1] | in_it[2] | in_it[3])) return;
+                    uint64_t w[4] = {};
+                    if (by_mass) weigh(y, w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (in_it[e]) add((hi - key[e]) >> down, w[e]);
+                });
+                sum_bins();
+                if (!find_bin(count, goal - (count ? above : mass_above))) break;   // (cannot be: what was summed is summed again)
+                above += before, mass_above += before_mass;
+                hi -= static_cast<uint32_t>(bin) << down;
                 lo = max(lo, hi - ((1u << down) - 1u));
             }
-            c.key = hi, c.above = before_mass;
-            if (count) {
-                c.ties = static_cast<unsigned>(want - before);
-            } else {
-                const uint64_t one = in > 0 ? in_mass / in : 1;
-                c.ties = one > 0 ? static_cast<unsigned>((want - before_mass + one - 1) / one) : in;
-            }
+            Cut c;
+            c.at = value_of<kDtype>(hi);
+            c.above = mass_above;
+            const uint64_t one = in > 0 ? in_mass / in : 1;
+            c.ties = static_cast<unsigned>(count ? goal - above : (goal - mass_above + one - 1) / one);
             return c;
         };
-        bool found;
-        if (by_count) cut = border(true, k, 0, found);
-        if (by_mass) {
-            uint64_t want = goal;
+        // what a thread found of the first bins, for a second border
+        const uint64_t first_upto = upto, first_mass = mass;
+        const unsigned first_count = upto_count, first_number = number;
+        if (found) cut = border(by_count, want);
+        if (by_count && by_mass) {
             uint64_t tie = 0;
-            if (by_count) {
-                if (found) {
-                    // the weight of a value: its key's
-                    uint32_t u32 = kDtype == HC_DTYPE_BF16 ? cut.key << 16 : kDtype == HC_DTYPE_FP16 ? cut.key << 13 : cut.key;
-                    u32 = (u32 & 0x80000000u) ? (u32 & 0x7FFFFFFFu) : ~u32;
-                    if (kDtype == HC_DTYPE_BF16 && (u32 & 0x80000000u)) u32 &= 0xFFFF0000u;
-                    if (kDtype == HC_DTYPE_FP16 && (u32 & 0x80000000u)) u32 &= 0xFFFFE000u;
-                    tie = weight(__uint_as_float(u32), heat, s.powers);
-                    total = cut.above + cut.ties * tie;
-                } else {
-                    // all that have weight stay
-                    uint64_t mass = 0;
-                    for (int i = lane; i < n; i += 32) mass += weight(logit<kDtype>(segment, entry(i)), heat, s.powers);
-                    __syncthreads();
-                    tell(mass, 0, &s.total, nullptr);
-                    cluster.sync();
-                    total = 0;
-                    for (int r = 0; r < ctas; ++r) total += cluster.map_shared_rank(&s, r)->total;
-                }
-                const double part = ceil(static_cast<double>(fmaxf(p, 0.f)) * static_cast<double>(total));
-                want = part < 1.0 ? 1 : static_cast<uint64_t>(part);
+            if (found) {
+                const float y[4] = {cut.at, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                uint64_t w[4];
+                weigh(y, w);
+                tie = w[0];
+                total = cut.above + cut.ties * tie;
+            } else {
+                __syncthreads();
+                if (tid == kBins - 1) s.before_mass = first_upto;               // all that are listed
+                __syncthreads();
+                total = s.before_mass;
             }
-            if (by_count && found && want > cut.above) {
+            want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+            if (found && want > cut.above) {
                 if (tie > 0) cut.ties = min(cut.ties, static_cast<unsigned>((want - cut.above + tie - 1) / tie));
             } else {
-                const Cut more = border(false, want, by_count && found ? cut.key : 0, found);
-                if (found) cut = more;
+                upto = first_upto, mass = first_mass, upto_count = first_count, number = first_number;
+                if (find_bin(false, want)) cut = border(false, want);
             }
         }
     }
 
     // ---- the sums of what stays, and the token
-    uint64_t low = 1;
-    if (least > 0.f) {
-        low = static_cast<uint64_t>(ceil(static_cast<double>(fminf(least, 1.f)) * static_cast<double>(kOne)));
-        low = low < 1 ? 1 : low;
-    }
+    const uint64_t low = !(least > 0.f) ? 1 : least < 1.f ? max(part_of(kOne, least, true), static_cast<uint64_t>(1)) : kOne;
     uint64_t mass = 0, tie = 0;
     unsigned ties = 0;
-    for (int i = lane; i < n; i += 32) {
-        const float y = logit<kDtype>(segment, entry(i));
-        const uint32_t key = key_of<kDtype>(y);
-        if (key < cut.key) continue;
-        const uint64_t w = weight(y, heat, s.powers);
-        if (w < low) continue;
-        if (key > cut.key || cut.key == 0) mass += w;
-        else ++ties, tie = w;
-    }
+    auto keep = [&](const float (&y)[4]) {
+        uint64_t w[4];
+        weigh(y, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (w[e] < low) continue;
+            if (y[e] > cut.at) mass += w[e];
+            if (y[e] == cut.at) ++ties, tie = w[e];
+        }
+    };
+    each(keep);
     // (the equal ones' weight, where this warp has one)
-    __syncthreads();
     {
         const unsigned with = __ballot_sync(~0u, ties > 0);
         if (with) tie = __shfl_sync(~0u, tie, __ffs(with) - 1);
     }
+    __syncthreads();
     tell(mass, ties, &s.kept, &s.ties);
     if (tid == 0) s.total = 0;
     __syncthreads();
@@ -541,64 +603,70 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const uint64_t warp_mass = s.warp_mass[warp];
     const unsigned warp_ties = s.warp_count[warp];
     cluster.sync();
-    uint64_t total = 0;
-    unsigned left = cut.ties;
-    tie = 0;
-    for (int r = 0; r < ctas; ++r) {
-        const uint64_t o = cluster.map_shared_rank(&s, r)->total;
-        tie = o > tie ? o : tie;
-    }
-    uint64_t before = 0, here = 0;               // the CTA's place in the sum
-    unsigned here_ties = 0;
-    for (int r = 0; r < ctas; ++r) {
-        const Shared* o = cluster.map_shared_rank(&s, r);
-        const unsigned take = min(left, o->ties);
-        left -= take;
-        const uint64_t sum = o->kept + take * tie;
-        if (r == rank) before = total, here = sum, here_ties = take;
-        total += sum;
-    }
-    const double at = floor(static_cast<double>(fmaxf(u, 0.f)) * static_cast<double>(total));
-    uint64_t goal = at < static_cast<double>(total) ? static_cast<uint64_t>(at) : total - 1;
-    goal = min(goal, total - 1);
+    // (each lane a CTA's part)
+    tie = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; });
+    const uint64_t kept = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.kept; });
+    const unsigned their_ties = of_ctas<unsigned>(cluster, ctas, lane, s, [](const Shared& o) { return o.ties; });
+#pragma unroll
+    for (int d = kMaxCtas / 2; d > 0; d >>= 1) tie = max(tie, __shfl_xor_sync(~0u, tie, d));
+    tie = __shfl_sync(~0u, tie, 0);
+    const unsigned ties_before = warp_scan(their_ties, lane) - their_ties;
+    const unsigned take = min(cut.ties - min(cut.ties, ties_before), their_ties);
+    const uint64_t upto = warp_scan(kept + take * tie, lane);
+    const uint64_t total = __shfl_sync(~0u, upto, 31);
+    // the CTA's place in the sum
+    const uint64_t here = __shfl_sync(~0u, kept + take * tie, rank), before = __shfl_sync(~0u, upto, rank) - here;
+    const unsigned here_ties = __shfl_sync(~0u, take, rank);
+    const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
     if (goal >= before && goal - before < here) {
         // the warp's place in the CTA
         uint64_t from = before;
         unsigned allow = here_ties;
         for (int w = 0; w < warp; ++w) {
-            const unsigned take = min(allow, s.warp_count[w]);
-            allow -= take;
-            from += s.warp_mass[w] + take * tie;
+            const unsigned some = min(allow, s.warp_count[w]);
+            allow -= some;
+            from += s.warp_mass[w] + some * tie;
         }
         allow = min(allow, warp_ties);
         if (goal >= from && goal - from < warp_mass + allow * tie) {
+            // 128 logits at a time, then the 32 and the one among them
             uint64_t sum = from;
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                uint64_t w = 0;
-                bool equal = false;
-                float y = 0.f;
-                int index = 0;
-                if (i0 + lane < n) {
-                    index = entry(i0 + lane);
-                    y = logit<kDtype>(segment, index);
-                    const uint32_t key = key_of<kDtype>(y);
-                    if (key >= cut.key) w = weight(y, heat, s.powers);
-                    if (w < low) w = 0;
-                    equal = w > 0 && key == cut.key && cut.key != 0;
+            for (int i = 0; i < n; i += 128) {
+                float y[4];
+                uint64_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < n ? logit<kDtype>(segment, index_of(i + lane + 32 * e)) : -CUDART_INF_F;
+                weigh(y, w);
+                uint64_t sums = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (w[e] < low || y[e] < cut.at) w[e] = 0;
+                    const bool equal = w[e] > 0 && y[e] == cut.at;
+                    const unsigned votes = __ballot_sync(~0u, equal);
+                    if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w[e] = 0;
+                    allow -= min(allow, static_cast<unsigned>(__popc(votes)));
+                    sums += w[e];
                 }
-                const unsigned votes = __ballot_sync(~0u, equal);
-                if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w = 0;
-                allow -= min(allow, static_cast<unsigned>(__popc(votes)));
-                const uint64_t upto = sum + warp_scan(w, lane);
-                const unsigned past = __ballot_sync(~0u, upto > goal);
-                if (past) {
-                    if (lane == __ffs(past) - 1) {
-                        a.ids[row] = id0 + index;
-                        a.logprob[row] = ((y - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
+                sums = warp_sum(sums);
+                if (sum + sums <= goal) {
+                    sum += sums;
+                    continue;
+                }
+                bool done = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t at = sum + warp_scan(w[e], lane);
+                    const unsigned past = __ballot_sync(~0u, at > goal);
+                    if (past && !done) {
+                        done = true;
+                        if (lane == __ffs(past) - 1) {
+                            a.ids[row] = id0 + index_of(i + lane + 32 * e);
+                            a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
+                        }
                     }
-                    break;
+                    sum = __shfl_sync(~0u, at, 31);
                 }
-                sum = __shfl_sync(~0u, upto, 31);
+                break;
             }
         }
     }
