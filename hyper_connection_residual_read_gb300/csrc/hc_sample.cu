@@ -14,15 +14,16 @@
 //
 // * the largest logit; for a top-p without a top-k also the sum of all weights
 // * an estimate, from an eighth of the logits, of a bound above which what stays must lie, and a list
-//   of the logits above it
-// * counts and weights of the listed logits by value, in 512 bins (where they are too few, a deeper
-//   bound is taken, at last that of all that have weight); those of the bin in which the border lies
-//   again, in bins 512 times as narrow, until one value is left. Of equal logits the first ones in the
-//   order of their ids stay, so that a border is a value and how many of it stay.
+//   of the logits above it; where they turn out too few, a deeper bound is taken, at last that of all
+//   that have weight
+// * counts and weights of the listed logits by value, in 256 bins; those of the bin in which the border
+//   lies again, in bins 256 times as narrow, until one value is left. Of equal logits the first ones in
+//   the order of their ids stay, so that a border is a value and how many of it stay.
 // * the sum of what stays by CTA, warp and lane, in the order of the ids, down to the token.
 //
 // Each step ends in a barrier of the cluster, after which every CTA reads what the others found and
-// comes to the same end. Lists and rows are gone through in the order of the ids, by each warp its part.
+// comes to the same end. A short list is handed to the first CTA, which ends the row alone. Lists and
+// rows are gone through in the order of the ids, by each warp its part.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,10 +39,11 @@ namespace cg = cooperative_groups;
 namespace hc {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;              // a thread a bin when they are summed
-constexpr int kBinBits = 9;
+constexpr int kBinBits = 8;
+constexpr int kShort = 1408;                 // logits of a list that one CTA takes
 constexpr int kUnitBits = 45;
 constexpr uint64_t kOne = 1ull << kUnitBits;
 constexpr int kMaxCtas = 8;                  // of a cluster
@@ -143,20 +145,25 @@ __device__ __forceinline__ uint64_t part_of(uint64_t x, float by, bool up) {
     return r + (up && rest != 0);
 }
 
-// 2^((m + g) / 128) in multiples of 2^-45, |g| <= 1.2, -47 128 <= m <= 1; m is given as the low bits of
-// `bits` = m + the pattern of kRound.
-__device__ __forceinline__ uint64_t power(int bits, float g, const uint64_t* powers) {
-    const float p = g * fmaf(g, fmaf(g, fmaf(g, 3.5830323054e-11f, 2.6466421444e-08f), 1.4662262388e-05f), 5.4152123481e-03f);
-    const int part = __float_as_int(fmaf(p, 536870912.f, kRound)) - __float_as_int(kRound);      // 2^29 p
+// 2^((m + g) / 128) in multiples of 2^-45, -47 128 <= m <= 1, of `bits` = m + the pattern of kRound and
+// `part` = 2^29 p(g) + that pattern.
+__device__ __forceinline__ uint64_t power(int bits, int part, const uint64_t* powers) {
+    constexpr int kPattern = 0x4B400000;
     const uint64_t t = powers[bits & (kSteps - 1)];
-    const uint64_t w = t + static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(t >> 29)) * part);      // 2^30 2^29
-    return w >> (59 - kUnitBits + (__float_as_int(kRound) >> 7) - (bits >> 7));
+    const uint64_t w = t + static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(t >> 29)) * (part - kPattern));     // 2^30 2^29
+    return w >> (59 - kUnitBits + (kPattern >> 7) - (bits >> 7));
 }
-// The weight of a logit, 0 below h.deep.
-__device__ __forceinline__ uint64_t weight(float x, const Heat& h, const uint64_t* powers) {
-    x = fmaxf(x, h.deep);
-    const float v = fmaf(x, h.c, h.a);
-    return power(__float_as_int(v), fmaf(x, h.c, h.a - v) + fmaf(x, h.c_low, h.rest), powers);
+// p(g) = 2^(g / 128) - 1 in multiples of 2^-29, behind kRound: (g l) + (g l)^2 / 2 + ..., l = ln 2 / 128; |g| <= 1.2
+constexpr float kP1 = 5.4152123481e-03f, kP2 = 1.4662262388e-05f, kP3 = 2.6466421444e-08f, kP4 = 3.5830323054e-11f, kPart = 536870912.f;
+// The weights of two logits, 0 below h.deep. Two fp32 operations in one instruction.
+__device__ __forceinline__ void weights(float x0, float x1, const Heat& h, const uint64_t* powers, uint64_t& w0, uint64_t& w1) {
+    const uint64_t x = pair(fmaxf(x0, h.deep), fmaxf(x1, h.deep)), c = pair(h.c, h.c), a = pair(h.a, h.a);
+    const uint64_t v = fma2(x, c, a);
+    const uint64_t g = add2(fma2(x, c, fma2(v, pair(-1.f, -1.f), a)), fma2(x, pair(h.c_low, h.c_low), pair(h.rest, h.rest)));
+    const uint64_t p = mul2(g, fma2(g, fma2(g, fma2(g, pair(kP4, kP4), pair(kP3, kP3)), pair(kP2, kP2)), pair(kP1, kP1)));
+    const float2 bits = unpair(v), part = unpair(fma2(p, pair(kPart, kPart), pair(kRound, kRound)));
+    w0 = power(__float_as_int(bits.x), __float_as_int(part.x), powers);
+    w1 = power(__float_as_int(bits.y), __float_as_int(part.y), powers);
 }
 // Where M c is so large that this way loses bits: from the difference to M, in two floats.
 __device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const uint64_t* powers) {
@@ -166,7 +173,9 @@ __device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c
     const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));     // x - top = d + dl
     const float zl = fmaf(dl, c, fmaf(d, c_low, fmaf(d, c, -z)));
     const float v = fmaf(z, kSteps, kRound);
-    return power(__float_as_int(v), fmaf(z, kSteps, kRound - v) + zl * kSteps, powers);
+    const float g = fmaf(z, kSteps, kRound - v) + zl * kSteps;
+    const float p = g * fmaf(g, fmaf(g, fmaf(g, kP4, kP3), kP2), kP1);
+    return power(__float_as_int(v), __float_as_int(fmaf(p, kPart, kRound)), powers);
 }
 
 template <typename T>
@@ -188,12 +197,16 @@ __device__ __forceinline__ T warp_scan(T x, int lane) {
 
 struct Shared {
     uint64_t powers[kSteps];
-    uint64_t mass[2][kBins];                 // of a step's bins, two steps' in turn
-    unsigned count[2][kBins];
+    // of a step's bins, two steps' in turn: their logits, and their weights as sums of each 16 bits of them
+    // (shared memory adds 32 bits at a time by itself: three such sums take 8 cycles a warp, one of 64
+    // bits 50 to 570)
+    unsigned count[2][kBins], mass[2][3][kBins];
     // what a CTA tells the others
     float top;
-    int bad, first;
+    int first;
     uint64_t total;
+    uint64_t listed_mass;
+    unsigned listed;
     uint64_t kept;                           // beside the equal ones at the border
     unsigned ties;
     // within the CTA
@@ -202,7 +215,10 @@ struct Shared {
     uint64_t before_mass, in_mass;           // of the bin with the border
     unsigned before, in;
     int bin;
-    int warp_listed[kWarps];
+    int warp_first[kWarps];
+    // a short list: values and ids
+    float value[kShort];
+    int id[kShort];
 };
 
 // A value of each CTA, one a lane (0 for lanes past them), brought at once.
@@ -218,8 +234,52 @@ struct Cut {
     uint64_t above;                          // weight of those above
 };
 
+// Packed maxima, NaN where one is.
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int segment_bytes, int* status) {
+struct Most {
+    float m = -__builtin_huge_valf();
+    __device__ __forceinline__ void take(const uint4& v) {
+        m = max_nan(m, max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w))));
+    }
+    __device__ __forceinline__ float get() const { return m; }
+};
+template <typename Two>
+__device__ __forceinline__ Two two_of(uint32_t w) { return *reinterpret_cast<const Two*>(&w); }
+template <>
+struct Most<HC_DTYPE_BF16> {
+    __nv_bfloat162 m = __float2bfloat162_rn(-__builtin_huge_valf());
+    __device__ __forceinline__ void take(const uint4& v) {
+        using Two = __nv_bfloat162;
+        m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(two_of<Two>(v.x), two_of<Two>(v.y)), __hmax2_nan(two_of<Two>(v.z), two_of<Two>(v.w))));
+    }
+    __device__ __forceinline__ float get() const { return max_nan(__low2float(m), __high2float(m)); }
+};
+template <>
+struct Most<HC_DTYPE_FP16> {
+    __half2 m = __float2half2_rn(-__builtin_huge_valf());
+    __device__ __forceinline__ void take(const uint4& v) {
+        using Two = __half2;
+        m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(two_of<Two>(v.x), two_of<Two>(v.y)), __hmax2_nan(two_of<Two>(v.z), two_of<Two>(v.w))));
+    }
+    __device__ __forceinline__ float get() const { return max_nan(__low2float(m), __high2float(m)); }
+};
+// The logits of a vector.
+template <int kDtype>
+__device__ __forceinline__ void unpack(const uint4& v, float (&y)[kDtype == HC_DTYPE_FP32 ? 4 : 8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (kDtype == HC_DTYPE_FP32) {
+            y[e] = __uint_as_float(w[e]);
+        } else {
+            const float2 f = widen2<kDtype>(w[e]);
+            y[2 * e] = f.x, y[2 * e + 1] = f.y;
+        }
+    }
+}
+
+template <int kDtype>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a, int ctas, int segment_bytes, int list_room, int* status) {
     constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
     __shared__ Shared s;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -227,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + segment_bytes);
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+    const int row = blockIdx.x / ctas;
+    int rank = blockIdx.x % ctas;
     begin_early();
     // (the whole cluster has one row, so that all of it leaves together)
     if (!HC_IN_RANGE(row, 1, a.tokens, status)) return;
@@ -238,57 +299,53 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const int vectors = (shift + a.vocab + kN - 1) / kN;
     const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), v1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
     const int id0 = v0 * kN - shift;             // the id of local index 0
-    float most = -CUDART_INF_F;
+    uint4* const vec = reinterpret_cast<uint4*>(segment);
+    float most;
     {
         const uint4* from = reinterpret_cast<const uint4*>(x - shift * kItem) + v0;
-        uint4* to = reinterpret_cast<uint4*>(segment);
-        constexpr uint32_t kNothing = kDtype == HC_DTYPE_FP32 ? 0xFF800000u : kDtype == HC_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-        auto bring = [&](int i) {
-            const int id = id0 + i * kN;
-            if (id >= 0 && id + kN <= a.vocab) return ldg_stream_v4(from + i);
-            uint32_t w[4] = {kNothing, kNothing, kNothing, kNothing};
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                if (id + e < 0 || id + e >= a.vocab) continue;           // in every build
-                if (kItem == 4) {
-                    w[e % 4] = reinterpret_cast<const uint32_t*>(x)[id + e];
-                } else {
-                    const uint32_t y = reinterpret_cast<const uint16_t*>(x)[id + e];
-                    w[(e / 2) % 4] = (e & 1) ? (w[(e / 2) % 4] & 0xFFFFu) | (y << 16) : (w[(e / 2) % 4] & 0xFFFF0000u) | y;
-                }
-            }
-            return make_uint4(w[0], w[1], w[2], w[3]);
-        };
-        auto put = [&](int i, const uint4& v) {
-            to[i] = v;
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (kDtype == HC_DTYPE_FP32) {
-                    most = max_nan(most, __uint_as_float(w[e]));
-                } else {
-                    const float2 y = widen2<kDtype>(w[e]);
-                    most = max_nan(most, max_nan(y.x, y.y));
-                }
-            }
-        };
-        const int n = v1 - v0;
-        int i = tid;
-        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
+        Most<kDtype> largest;
+        // whole vectors, and the ends of the row by one thread each
+        const int n = v1 - v0, w0 = id0 < 0 ? 1 : 0, w1 = id0 + n * kN > a.vocab ? n - 1 : n;
+        int i = w0 + tid;
+        for (; i + 3 * kThreads < w1; i += 4 * kThreads) {
             uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = bring(i + e * kThreads);
+            for (int e = 0; e < 4; ++e) v[e] = ldg_stream_v4(from + i + e * kThreads);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) put(i + e * kThreads, v[e]);
+            for (int e = 0; e < 4; ++e) vec[i + e * kThreads] = v[e], largest.take(v[e]);
         }
-        for (; i < n; i += kThreads) put(i, bring(i));
+        for (; i < w1; i += kThreads) {
+            const uint4 v = ldg_stream_v4(from + i);
+            vec[i] = v;
+            largest.take(v);
+        }
+        if ((tid == 0 && w0 > 0) || (tid == 32 && w1 < n && n > w0)) {
+            const int at = tid == 0 ? 0 : n - 1;
+            uint4 v;
+            for (int e = 0; e < kN; ++e) {
+                const int id = id0 + at * kN + e;
+                const bool in = id >= 0 && id < a.vocab;
+                if (kItem == 4) {
+                    reinterpret_cast<uint32_t*>(&vec[at])[e] = in ? reinterpret_cast<const uint32_t*>(x)[id] : 0xFF800000u;
+                } else {
+                    reinterpret_cast<uint16_t*>(&vec[at])[e] = in ? reinterpret_cast<const uint16_t*>(x)[id] : static_cast<uint16_t>(kDtype == HC_DTYPE_BF16 ? 0xFF80u : 0xFC00u);
+                }
+            }
+            v = vec[at];
+            largest.take(v);
+        }
+        most = largest.get();
     }
     const float u = a.uniform[row], t = a.temperature ? a.temperature[row] : 1.f;
     const float p = a.top_p ? a.top_p[row] : 1.f, least = a.min_p ? a.min_p[row] : 0.f;
     const int k = a.top_k ? a.top_k[row] : 0;
     bool bad = !(u == u && p == p && least == least) || !(fabsf(t) <= kTop);
     for (int i = tid; i < kSteps; i += kThreads) s.powers[i] = kPowers[i];
-    for (int i = tid; i < kBins; i += kThreads) s.count[0][i] = s.count[1][i] = 0, s.mass[0][i] = s.mass[1][i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) {
+        s.count[0][i] = s.count[1][i] = 0;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) s.mass[0][e][i] = s.mass[1][e][i] = 0;
+    }
 
     // ---- the largest logit
 #pragma unroll
@@ -307,18 +364,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     bad = bad || !(fabsf(top) <= kTop);
     // each warp's part of the segment
     const int all = (v1 - v0) * kN, per = ((v1 - v0 + kWarps - 1) / kWarps) * kN;
-    const int begin = min(warp * per, all), end = min(begin + per, all);
+    const int part_begin = min(warp * per, all), part_end = min(part_begin + per, all);
     if (bad || t < 5.421010862427522e-20f) {
         // nothing, or the first of the largest
         int first = 0x7FFFFFFF;
         if (!bad)
-            for (int i = begin + lane; i < end; i += 32)
-                if (logit<kDtype>(segment, i) == top) first = min(first, id0 + i);
+            for (int i = part_begin / kN + lane; i < part_end / kN; i += 32) {
+                float y[kN];
+                unpack<kDtype>(vec[i], y);
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (y[e] == top) first = min(first, id0 + i * kN + e);
+            }
         first = __reduce_min_sync(~0u, first);
-        if (lane == 0) s.warp_listed[warp] = first;
+        if (lane == 0) s.warp_first[warp] = first;
         __syncthreads();
         if (tid == 0) {
-            for (int w = 1; w < kWarps; ++w) first = min(first, s.warp_listed[w]);
+            for (int w = 1; w < kWarps; ++w) first = min(first, s.warp_first[w]);
             s.first = first;
         }
         cluster.sync();
@@ -345,17 +407,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
     };
 
-    // The logits that this warp goes through, four a lane at a time: all of its part, or those listed.
-    bool listed = false;
-    int n = end - begin;
-    uint16_t* mine = list + begin;
-    auto index_of = [&](int i) { return listed ? static_cast<int>(mine[i]) : begin + i; };
+    // The logits that this warp goes through, four a lane at a time: all of its part, those listed of it, or
+    // its share of the short list.
+    enum { kAll, kListed, kAlone } mode = kAll;
+    int n = part_end - part_begin, begin = part_begin;
+    uint16_t* mine = list + warp * list_room;
+    auto value_at = [&](int i) {
+        if (mode == kAlone) return s.value[begin + i];
+        return logit<kDtype>(segment, mode == kListed ? static_cast<int>(mine[i]) : begin + i);
+    };
     auto each = [&](auto use) {
         for (int i = lane; i < n; i += 128) {
             float y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = i + 32 * e < n ? logit<kDtype>(segment, index_of(i + 32 * e)) : -CUDART_INF_F;
+            for (int e = 0; e < 4; ++e) y[e] = i + 32 * e < n ? value_at(i + 32 * e) : -CUDART_INF_F;
             use(y);
+        }
+    };
+    // (in no order)
+    auto each_of_all = [&](auto use) {
+        for (int i = part_begin / kN + lane; i < part_end / kN; i += 32) {
+            float y[kN];
+            unpack<kDtype>(vec[i], y);
+#pragma unroll
+            for (int e = 0; e < kN; e += 4) {
+                const float z[4] = {y[e], y[e + 1], y[e + 2], y[e + 3]};
+                use(z);
+            }
         }
     };
     // and their weights, 0 for those at -inf
@@ -371,81 +449,165 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 else w[3] = one;
             }
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = weight(y[e], heat, s.powers);
+            weights(y[0], y[1], heat, s.powers, w[0], w[1]);
+            weights(y[2], y[3], heat, s.powers, w[2], w[3]);
         }
+    };
+    // the end of a step
+    auto sync = [&]() {
+        if (mode == kAlone) __syncthreads();
+        else cluster.sync();
     };
     Cut cut = {-CUDART_INF_F, 0, 0};             // all stay
     if (by_count || by_mass) {
-        int turn = 0;                            // bins of the step
-        // ---- an eighth of the logits, by how far they lie below the largest, in bins of an octave / 11
-        const float width = -kDeep / kBins * kLn2 * t;                  // of a bin, in logits
-        const float per_logit = 1.f / width;
-        for (int i = tid; i < all / 8; i += kThreads) {
-            const float z = (top - logit<kDtype>(segment, i * 8 + (i & 7))) * per_logit;
-            if (z < static_cast<float>(kBins)) atomicAdd(&s.count[0][min(static_cast<int>(z), kBins - 1)], 1u);
-        }
-        uint64_t total = 0;
-        auto add_up = [&](const float (&y)[4]) {
-            uint64_t w[4];
-            weigh(y, w);
-            total += (w[0] + w[1]) + (w[2] + w[3]);
-        };
-        if (!by_count) each(add_up);
-        tell(total, 0, &s.total, nullptr);
-        cluster.sync();
-        total = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; }));
+        const bool few = a.vocab <= kShort;                             // they go to one CTA without an estimate
+        const float width = -kDeep / kBins * kLn2 * t;                  // of an estimate's bin, in logits
+        uint64_t total = 0, want = k, mass = 0, upto = 0;
         unsigned number = 0;
-        {
+        float bound = heat.deep;
+        if (!few) {
+            // ---- an eighth of the logits, by how far they lie below the largest, in bins of an octave / 5.5
+            const float per_logit = 1.f / width;
+            for (int i = tid; i < all / 8; i += kThreads) {
+                const float z = (top - logit<kDtype>(segment, i * 8 + (i & 7))) * per_logit;
+                if (z < static_cast<float>(kBins)) atomicAdd(&s.count[0][min(static_cast<int>(z), kBins - 1)], 1u);
+            }
+            auto add_up = [&](const float (&y)[4]) {
+                uint64_t w[4];
+                weigh(y, w);
+                total += (w[0] + w[1]) + (w[2] + w[3]);
+            };
+            if (!by_count) each_of_all(add_up);
+            tell(total, 0, &s.total, nullptr);
+            cluster.sync();
+            total = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; }));
             unsigned theirs[kMaxCtas];
 #pragma unroll
             for (int r = 0; r < kMaxCtas; ++r) theirs[r] = r < ctas ? cluster.map_shared_rank(&s, r < ctas ? r : 0)->count[0][tid] : 0;
 #pragma unroll
             for (int r = 0; r < kMaxCtas; ++r) number += theirs[r];
+            const float share = 8.f * static_cast<float>(number) * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins));
+            mass = by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f);
+            upto = warp_scan(mass, lane);
+            if (lane == 31) s.warp_mass[warp] = upto;
+            if (tid == 0) s.bin = kBins - 1;
+            __syncthreads();
+            uint64_t sum = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) upto += sum;
+                sum += s.warp_mass[w];
+            }
+            uint64_t most_of = static_cast<uint64_t>(k) + k / 4 + 64;
+            if (!by_count) {
+                want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+                // what may lie below the bound, a little less than the rest, from the estimate's end
+                const uint64_t rest = (total - want) >> (kUnitBits - 30);
+                const uint64_t below = rest - rest / 8;
+                most_of = sum > below ? sum - below : 0;
+            }
+            if (upto >= most_of) atomicMin(&s.bin, tid);
+            __syncthreads();
+            bound = top - static_cast<float>(s.bin + 1) * width;
         }
-        turn = 1;
-        const float share = 8.f * static_cast<float>(number) * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins));
-        uint64_t mass = by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f);
-        uint64_t upto = warp_scan(mass, lane);
-        if (lane == 31) s.warp_mass[warp] = upto;
-        if (tid == 0) s.bin = kBins - 1;
-        __syncthreads();
-        uint64_t sum = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) upto += sum;
-            sum += s.warp_mass[w];
-        }
-        uint64_t want = k;
-        uint64_t most_of = static_cast<uint64_t>(k) + k / 4 + 64;
-        if (!by_count) {
-            want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
-            // what may lie below the bound, a little less than the rest, from the estimate's end
-            const uint64_t rest = (total - want) >> (kUnitBits - 30);
-            const uint64_t below = rest - rest / 8;
-            most_of = sum > below ? sum - below : 0;
-        }
-        if (upto >= most_of) atomicMin(&s.bin, tid);
-        __syncthreads();
-        float bound = top - static_cast<float>(s.bin + 1) * width;
 
+        // ---- the list of the logits at the bound and above
+        for (int attempt = 0;; ++attempt) {
+            bound = attempt < 2 ? fmaxf(bound, heat.deep) : heat.deep;
+            int m = 0;
+            for (int i = part_begin / kN; i < part_end / kN; i += 32) {
+                unsigned set = 0;                               // a bit a logit of this lane's vector
+                if (i + lane < part_end / kN) {
+                    const uint4 v = vec[i + lane];
+                    Most<kDtype> largest;
+                    largest.take(v);
+                    if (largest.get() >= bound) {
+                        float y[kN];
+                        unpack<kDtype>(v, y);
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) set |= (y[e] >= bound ? 1u : 0u) << e;
+                    }
+                }
+                if (__any_sync(~0u, set != 0)) {
+                    const int count = __popc(set), before = warp_scan(count, lane) - count;
+                    int to = m + before;
+                    for (; set != 0; set &= set - 1, ++to)
+                        if (to < list_room) mine[to] = static_cast<uint16_t>((i + lane) * kN + __ffs(set) - 1);
+                    m += __shfl_sync(~0u, before + count, 31);
+                }
+            }
+            __syncwarp();
+            // all of the CTA's warps go through their lists, or all through everything
+            const bool fits = !__syncthreads_or(m > list_room);
+            mode = fits ? kListed : kAll;
+            n = fits ? m : part_end - part_begin;
+            uint64_t have = 0;
+            if (!by_count && !few) each([&](const float (&y)[4]) {
+                uint64_t w[4];
+                weigh(y, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (y[e] >= bound) have += w[e];
+            });
+            tell(have, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
+            cluster.sync();
+            const unsigned theirs = of_ctas<unsigned>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed; });
+            have = by_count ? theirs : of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed_mass; });
+            have = warp_sum(have);
+            const unsigned listed_upto = warp_scan(theirs, lane), listed = __shfl_sync(~0u, listed_upto, 31);
+            if (few || have >= want || bound == heat.deep) {
+                if (listed > kShort) break;
+                // to the first CTA, in the order of the ids
+                Shared* first = cluster.map_shared_rank(&s, 0);
+                int to = __shfl_sync(~0u, listed_upto - theirs, rank);
+                for (int w = 0; w < warp; ++w) to += s.warp_count[w];
+                for (int i = lane; i < m; i += 32) {
+                    // (a warp whose list has no room for so many finds them again below)
+                    const int at = fits ? static_cast<int>(mine[i]) : 0;
+                    if (fits) first->value[to + i] = logit<kDtype>(segment, at), first->id[to + i] = id0 + at;
+                }
+                if (!fits) {
+                    for (int i = part_begin; i < part_end; i += 32) {
+                        const float y = i + lane < part_end ? logit<kDtype>(segment, i + lane) : -CUDART_INF_F;
+                        const unsigned votes = __ballot_sync(~0u, y >= bound);
+                        const int at = to + __popc(votes & ((1u << lane) - 1u));
+                        if (y >= bound) first->value[at] = y, first->id[at] = id0 + i + lane;
+                        to += __popc(votes);
+                    }
+                }
+                cluster.sync();
+                if (rank != 0) return;
+                mode = kAlone, ctas = 1;
+                const int share = (static_cast<int>(listed) + kWarps - 1) / kWarps;
+                begin = min(warp * share, static_cast<int>(listed));
+                n = min(share, static_cast<int>(listed) - begin);
+                break;
+            }
+            // four times as deep, and six octaves; then to the end
+            bound = top - 4.f * (top - bound) - 33.f * width;
+            cluster.sync();                      // all have read what is told anew
+        }
+
+        int turn = 1;                            // bins of the step
         // ---- the step's bins summed over the cluster, a bin a thread: its own, those up to it
         unsigned upto_count = 0;
         auto sum_bins = [&]() {
-            cluster.sync();
-            uint64_t masses[kMaxCtas];
-            unsigned numbers[kMaxCtas];
-#pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) {
-                const Shared* o = cluster.map_shared_rank(&s, r < ctas ? r : 0);
-                masses[r] = by_mass && r < ctas ? o->mass[turn][tid] : 0;
-                numbers[r] = r < ctas ? o->count[turn][tid] : 0;
-            }
+            sync();
             mass = number = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) mass += masses[r], number += numbers[r];
+            auto take = [&](const Shared& o) {
+                number += o.count[turn][tid];
+                if (by_mass) mass += o.mass[turn][0][tid] + (static_cast<uint64_t>(o.mass[turn][1][tid]) << 16) + (static_cast<uint64_t>(o.mass[turn][2][tid]) << 32);
+            };
+            if (ctas == 1) {
+                take(s);
+            } else {
+#pragma unroll 4
+                for (int r = 0; r < ctas; ++r) take(*cluster.map_shared_rank(&s, r));
+            }
             // the other bins, read by all in the step before, are free for the next
             turn ^= 1;
-            s.count[turn][tid] = 0, s.mass[turn][tid] = 0;
+            s.count[turn][tid] = 0;
+#pragma unroll
+            for (int e = 0; e < 3; ++e) s.mass[turn][e][tid] = 0;
             upto = warp_scan(mass, lane), upto_count = warp_scan(number, lane);
             if (lane == 31) s.warp_mass[warp] = upto, s.warp_count[warp] = upto_count;
             __syncthreads();
@@ -467,44 +629,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         };
         auto add = [&](int to, uint64_t w) {
             atomicAdd(&s.count[turn][to], 1u);
-            if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[turn][to]), static_cast<unsigned long long>(w));
+            if (!by_mass) return;
+            atomicAdd(&s.mass[turn][0][to], static_cast<unsigned>(w) & 0xFFFFu);
+            atomicAdd(&s.mass[turn][1][to], static_cast<unsigned>(w) >> 16);
+            atomicAdd(&s.mass[turn][2][to], static_cast<unsigned>(w >> 32));
         };
 
-        // ---- the list, and its bins by value
-        float fine = 0.f;
+        // ---- the listed logits by value
+        const float fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
         auto coarse = [&](float y) { return min(static_cast<int>((top - y) * fine), kBins - 1); };
-        bool found = false;
-        for (int attempt = 0;; ++attempt) {
-            bound = attempt < 2 ? fmaxf(bound, heat.deep) : heat.deep;
-            fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
-            int m = 0;
-            for (int i = begin; i < end; i += 128) {
-                float y[4];
+        each([&](const float (&y)[4]) {
+            uint64_t w[4] = {};
+            if (by_mass) weigh(y, w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < end ? logit<kDtype>(segment, i + lane + 32 * e) : -CUDART_INF_F;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool stays = y[e] >= bound;
-                    const unsigned votes = __ballot_sync(~0u, stays);
-                    if (stays) mine[m + __popc(votes & ((1u << lane) - 1u))] = static_cast<uint16_t>(i + lane + 32 * e);
-                    m += __popc(votes);
-                }
-            }
-            listed = true, n = m;
-            __syncwarp();
-            each([&](const float (&y)[4]) {
-                uint64_t w[4] = {};
-                if (by_mass) weigh(y, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (y[e] >= bound) add(coarse(y[e]), w[e]);
-            });
-            sum_bins();
-            found = find_bin(by_count, want);
-            if (found || bound == heat.deep) break;             // (fewer have weight: all of them stay)
-            // four times as deep, and six octaves; then to the end
-            bound = top - 4.f * (top - bound) - 65.f * width;
+            for (int e = 0; e < 4; ++e)
+                if (y[e] >= bound) add(coarse(y[e]), w[e]);
+        });
+        sum_bins();
+        if (few && by_mass && !by_count) {
+            __syncthreads();
+            if (tid == kBins - 1) s.before_mass = upto;         // all that have weight
+            __syncthreads();
+            total = s.before_mass;
+            want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
         }
+        const bool found = find_bin(by_count, want);            // (else fewer have weight: all of them stay)
 
         // ---- borders: the value at which `goal` is reached, in the bin that has been found
         auto border = [&](bool count, uint64_t goal) {
@@ -589,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             if (y[e] == cut.at) ++ties, tie = w[e];
         }
     };
-    each(keep);
+    if (mode == kAll) each_of_all(keep);
+    else each(keep);
     // (the equal ones' weight, where this warp has one)
     {
         const unsigned with = __ballot_sync(~0u, ties > 0);
@@ -602,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     if (lane == 0 && tie > 0) s.total = tie;     // the same from any warp
     const uint64_t warp_mass = s.warp_mass[warp];
     const unsigned warp_ties = s.warp_count[warp];
-    cluster.sync();
+    sync();
     // (each lane a CTA's part)
     tie = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; });
     const uint64_t kept = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.kept; });
@@ -635,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 float y[4];
                 uint64_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < n ? logit<kDtype>(segment, index_of(i + lane + 32 * e)) : -CUDART_INF_F;
+                for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < n ? value_at(i + lane + 32 * e) : -CUDART_INF_F;
                 weigh(y, w);
                 uint64_t sums = 0;
 #pragma unroll
@@ -660,7 +810,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                     if (past && !done) {
                         done = true;
                         if (lane == __ffs(past) - 1) {
-                            a.ids[row] = id0 + index_of(i + lane + 32 * e);
+                            const int at = i + lane + 32 * e;
+                            a.ids[row] = mode == kAlone ? s.id[begin + at] : id0 + (mode == kListed ? static_cast<int>(mine[at]) : begin + at);
                             a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
                         }
                     }
@@ -670,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             }
         }
     }
-    cluster.sync();                              // no CTA leaves while another reads its memory
+    sync();                                      // no CTA leaves while another reads its memory
 }
 
 // CTAs of a row: as many as keep a part within 16384 logits, and twice, four times as many where there
@@ -688,7 +839,10 @@ cudaError_t call(const Ctx& ctx, const SampleArgs& a, cudaStream_t st) {
     const int ctas = row_ctas(ctx.sm_count, a.tokens, a.vocab);
     // a row may begin anywhere in its first vector
     const int vectors = ((a.vocab + 2 * kN - 2) / kN + ctas - 1) / ctas;
-    const size_t smem = static_cast<size_t>(vectors) * (16 + 2 * kN);
+    // a list of all that a warp goes through, 16 bits each; of a quarter where CTAs share the SMs
+    const bool alone = static_cast<int64_t>(a.tokens) * ctas <= 2 * ctx.sm_count;
+    const int room = (vectors + kWarps - 1) / kWarps * kN / (alone ? 1 : 4);
+    const size_t smem = static_cast<size_t>(vectors) * 16 + sizeof(uint16_t) * kWarps * room;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.tokens) * ctas);
     cfg.blockDim = dim3(kThreads);
@@ -701,7 +855,7 @@ cudaError_t call(const Ctx& ctx, const SampleArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.x = ctas, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<kDtype>, a, ctas, vectors * 16, ctx.s.status);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<kDtype>, a, ctas, vectors * 16, room, ctx.s.status);
 }
 
 // A launch has at most 2^31 - 1 CTAs.
@@ -727,7 +881,8 @@ template <int kDtype>
 cudaError_t allow_smem() {
     constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
     const int vectors = ((HC_SAMPLE_MAX_VOCAB + 2 * kN - 2) / kN + kMaxCtas - 1) / kMaxCtas;
-    return cudaFuncSetAttribute(sample_kernel<kDtype>, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors * (16 + 2 * kN));
+    const int room = (vectors + kWarps - 1) / kWarps * kN;
+    return cudaFuncSetAttribute(sample_kernel<kDtype>, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors * 16 + static_cast<int>(sizeof(uint16_t)) * kWarps * room);
 }
 
 }  // namespace
