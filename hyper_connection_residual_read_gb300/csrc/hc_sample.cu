@@ -462,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     if (by_count || by_mass) {
         const bool few = a.vocab <= kShort;                             // they go to one CTA without an estimate
         const float width = -kDeep / kBins * kLn2 * t;                  // of an estimate's bin, in logits
-        uint64_t total = 0, want = k, mass = 0, upto = 0;
+        uint64_t total = 0, want = k, mass = 0, upto = 0, estimated = 0;
         unsigned number = 0;
-        float bound = heat.deep;
+        float bound;
         if (!few) {
             // ---- an eighth of the logits, by how far they lie below the largest, in bins of an octave / 5.5
             const float per_logit = 1.f / width;
@@ -490,102 +490,30 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             mass = by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f);
             upto = warp_scan(mass, lane);
             if (lane == 31) s.warp_mass[warp] = upto;
+            __syncthreads();
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) upto += estimated;
+                estimated += s.warp_mass[w];
+            }
+            if (!by_count) want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+        }
+        const uint64_t estimated_upto = upto;
+        // The bound of an attempt. Counts, or the weight that may lie below (the whole less 'want', of which
+        // an eighth of the logits give an idea), with room for what chance does to the estimate.
+        auto bound_of = [&](int attempt) {
+            if (few || attempt == 2) return heat.deep;
+            uint64_t most_of = attempt == 0 ? want + want / 4 + 64 : 2 * want + 512;
+            if (!by_count) {
+                const uint64_t rest = (total - want) >> (kUnitBits - 30), below = attempt == 0 ? rest - rest / 4 : rest / 4;
+                most_of = estimated > below ? estimated - below : 0;
+            }
+            __syncthreads();
             if (tid == 0) s.bin = kBins - 1;
             __syncthreads();
-            uint64_t sum = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) upto += sum;
-                sum += s.warp_mass[w];
-            }
-            uint64_t most_of = static_cast<uint64_t>(k) + k / 4 + 64;
-            if (!by_count) {
-                want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
-                // what may lie below the bound, a little less than the rest, from the estimate's end
-                const uint64_t rest = (total - want) >> (kUnitBits - 30);
-                const uint64_t below = rest - rest / 8;
-                most_of = sum > below ? sum - below : 0;
-            }
-            if (upto >= most_of) atomicMin(&s.bin, tid);
+            if (estimated_upto >= most_of) atomicMin(&s.bin, tid);
             __syncthreads();
-            bound = top - static_cast<float>(s.bin + 1) * width;
-        }
-
-        // ---- the list of the logits at the bound and above
-        for (int attempt = 0;; ++attempt) {
-            bound = attempt < 2 ? fmaxf(bound, heat.deep) : heat.deep;
-            int m = 0;
-            for (int i = part_begin / kN; i < part_end / kN; i += 32) {
-                unsigned set = 0;                               // a bit a logit of this lane's vector
-                if (i + lane < part_end / kN) {
-                    const uint4 v = vec[i + lane];
-                    Most<kDtype> largest;
-                    largest.take(v);
-                    if (largest.get() >= bound) {
-                        float y[kN];
-                        unpack<kDtype>(v, y);
-#pragma unroll
-                        for (int e = 0; e < kN; ++e) set |= (y[e] >= bound ? 1u : 0u) << e;
-                    }
-                }
-                if (__any_sync(~0u, set != 0)) {
-                    const int count = __popc(set), before = warp_scan(count, lane) - count;
-                    int to = m + before;
-                    for (; set != 0; set &= set - 1, ++to)
-                        if (to < list_room) mine[to] = static_cast<uint16_t>((i + lane) * kN + __ffs(set) - 1);
-                    m += __shfl_sync(~0u, before + count, 31);
-                }
-            }
-            __syncwarp();
-            // all of the CTA's warps go through their lists, or all through everything
-            const bool fits = !__syncthreads_or(m > list_room);
-            mode = fits ? kListed : kAll;
-            n = fits ? m : part_end - part_begin;
-            uint64_t have = 0;
-            if (!by_count && !few) each([&](const float (&y)[4]) {
-                uint64_t w[4];
-                weigh(y, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (y[e] >= bound) have += w[e];
-            });
-            tell(have, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
-            cluster.sync();
-            const unsigned theirs = of_ctas<unsigned>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed; });
-            have = by_count ? theirs : of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed_mass; });
-            have = warp_sum(have);
-            const unsigned listed_upto = warp_scan(theirs, lane), listed = __shfl_sync(~0u, listed_upto, 31);
-            if (few || have >= want || bound == heat.deep) {
-                if (listed > kShort) break;
-                // to the first CTA, in the order of the ids
-                Shared* first = cluster.map_shared_rank(&s, 0);
-                int to = __shfl_sync(~0u, listed_upto - theirs, rank);
-                for (int w = 0; w < warp; ++w) to += s.warp_count[w];
-                for (int i = lane; i < m; i += 32) {
-                    // (a warp whose list has no room for so many finds them again below)
-                    const int at = fits ? static_cast<int>(mine[i]) : 0;
-                    if (fits) first->value[to + i] = logit<kDtype>(segment, at), first->id[to + i] = id0 + at;
-                }
-                if (!fits) {
-                    for (int i = part_begin; i < part_end; i += 32) {
-                        const float y = i + lane < part_end ? logit<kDtype>(segment, i + lane) : -CUDART_INF_F;
-                        const unsigned votes = __ballot_sync(~0u, y >= bound);
-                        const int at = to + __popc(votes & ((1u << lane) - 1u));
-                        if (y >= bound) first->value[at] = y, first->id[at] = id0 + i + lane;
-                        to += __popc(votes);
-                    }
-                }
-                cluster.sync();
-                if (rank != 0) return;
-                mode = kAlone, ctas = 1;
-                const int share = (static_cast<int>(listed) + kWarps - 1) / kWarps;
-                begin = min(warp * share, static_cast<int>(listed));
-                n = min(share, static_cast<int>(listed) - begin);
-                break;
-            }
-            // four times as deep, and six octaves; then to the end
-            bound = top - 4.f * (top - bound) - 33.f * width;
-            cluster.sync();                      // all have read what is told anew
-        }
+            return fmaxf(top - static_cast<float>(s.bin + 1) * width, heat.deep);
+        };
 
         int turn = 1;                            // bins of the step
         // ---- the step's bins summed over the cluster, a bin a thread: its own, those up to it
@@ -635,26 +563,122 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             atomicAdd(&s.mass[turn][2][to], static_cast<unsigned>(w >> 32));
         };
 
-        // ---- the listed logits by value
-        const float fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
+        // the listed logits by value
+        float fine = 0.f;
+        bool found = false;
         auto coarse = [&](float y) { return min(static_cast<int>((top - y) * fine), kBins - 1); };
-        each([&](const float (&y)[4]) {
-            uint64_t w[4] = {};
-            if (by_mass) weigh(y, w);
+        auto by_value = [&]() {
+            fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
+            each([&](const float (&y)[4]) {
+                uint64_t w[4] = {};
+                if (by_mass) weigh(y, w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (y[e] >= bound) add(coarse(y[e]), w[e]);
-        });
-        sum_bins();
-        if (few && by_mass && !by_count) {
-            __syncthreads();
-            if (tid == kBins - 1) s.before_mass = upto;         // all that have weight
-            __syncthreads();
-            total = s.before_mass;
-            want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
-        }
-        const bool found = find_bin(by_count, want);            // (else fewer have weight: all of them stay)
+                for (int e = 0; e < 4; ++e)
+                    if (y[e] >= bound) add(coarse(y[e]), w[e]);
+            });
+            sum_bins();
+        };
 
+        // ---- the list of the logits at the bound and above
+        for (int attempt = 0;; ++attempt) {
+            bound = bound_of(attempt);
+            int m = 0;
+            for (int i = part_begin / kN; i < part_end / kN; i += 32) {
+                unsigned set = 0;                               // a bit a logit of this lane's vector
+                if (i + lane < part_end / kN) {
+                    const uint4 v = vec[i + lane];
+                    Most<kDtype> largest;
+                    largest.take(v);
+                    if (largest.get() >= bound) {
+                        float y[kN];
+                        unpack<kDtype>(v, y);
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) set |= (y[e] >= bound ? 1u : 0u) << e;
+                    }
+                }
+                if (__any_sync(~0u, set != 0)) {
+                    const int count = __popc(set), before = warp_scan(count, lane) - count;
+                    int to = m + before;
+                    for (; set != 0; set &= set - 1, ++to)
+                        if (to < list_room) mine[to] = static_cast<uint16_t>((i + lane) * kN + __ffs(set) - 1);
+                    m += __shfl_sync(~0u, before + count, 31);
+                }
+            }
+            __syncwarp();
+            // all of the CTA's warps go through their lists, or all through everything
+            const bool fits = !__syncthreads_or(m > list_room);
+            mode = fits ? kListed : kAll;
+            n = fits ? m : part_end - part_begin;
+            tell(0, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
+            cluster.sync();
+            const unsigned theirs = of_ctas<unsigned>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed; });
+            const unsigned listed_upto = warp_scan(theirs, lane), listed = __shfl_sync(~0u, listed_upto, 31);
+            const bool last = bound == heat.deep;
+            if (listed > kShort) {
+                // by value; whether they are enough is seen from it
+                if (by_count && listed < want && !last) {
+                    cluster.sync();              // all have read what is told anew
+                    continue;
+                }
+                by_value();
+                found = find_bin(by_count, want);
+                if (found || last) break;        // (else fewer have weight: all of them stay)
+                continue;
+            }
+            bool enough = last || (by_count && listed >= want);
+            const unsigned my_listed = lane < kWarps ? s.warp_count[lane] : 0;      // of the warps, one a lane
+            if (!enough && !by_count) {
+                uint64_t have = 0;
+                each([&](const float (&y)[4]) {
+                    uint64_t w[4];
+                    weigh(y, w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (y[e] >= bound) have += w[e];
+                });
+                __syncthreads();
+                tell(have, 0, &s.listed_mass, nullptr);
+                cluster.sync();
+                enough = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed_mass; })) >= want;
+            }
+            if (enough) {
+                // to the first CTA, in the order of the ids
+                Shared* first = cluster.map_shared_rank(&s, 0);
+                int to = __shfl_sync(~0u, listed_upto - theirs, rank);
+                to += __reduce_add_sync(~0u, lane < warp ? my_listed : 0);
+                for (int i = lane; i < m; i += 32) {
+                    // (a warp whose list has no room for so many finds them again below)
+                    const int at = fits ? static_cast<int>(mine[i]) : 0;
+                    if (fits) first->value[to + i] = logit<kDtype>(segment, at), first->id[to + i] = id0 + at;
+                }
+                if (!fits) {
+                    for (int i = part_begin; i < part_end; i += 32) {
+                        const float y = i + lane < part_end ? logit<kDtype>(segment, i + lane) : -CUDART_INF_F;
+                        const unsigned votes = __ballot_sync(~0u, y >= bound);
+                        const int at = to + __popc(votes & ((1u << lane) - 1u));
+                        if (y >= bound) first->value[at] = y, first->id[at] = id0 + i + lane;
+                        to += __popc(votes);
+                    }
+                }
+                cluster.sync();
+                if (rank != 0) return;
+                mode = kAlone, ctas = 1;
+                const int share = (static_cast<int>(listed) + kWarps - 1) / kWarps;
+                begin = min(warp * share, static_cast<int>(listed));
+                n = min(share, static_cast<int>(listed) - begin);
+                by_value();
+                if (few && by_mass && !by_count) {
+                    __syncthreads();
+                    if (tid == kBins - 1) s.before_mass = upto;         // all that have weight
+                    __syncthreads();
+                    total = s.before_mass;
+                    want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+                }
+                found = find_bin(by_count, want);
+                break;
+            }
+            cluster.sync();                      // all have read what is told anew
+        }
         // ---- borders: the value at which `goal` is reached, in the bin that has been found
         auto border = [&](bool count, uint64_t goal) {
             // the values of that bin, and what rounding may add to them
@@ -738,7 +762,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             if (y[e] == cut.at) ++ties, tie = w[e];
         }
     };
-    if (mode == kAll) each_of_all(keep);
+    if (mode == kAll && cut.at == -CUDART_INF_F && low == 1) each_of_all([&](const float (&y)[4]) {
+        uint64_t w[4];
+        weigh(y, w);
+        mass += (w[0] + w[1]) + (w[2] + w[3]);
+    });
+    else if (mode == kAll) each_of_all(keep);
     else each(keep);
     // (the equal ones' weight, where this warp has one)
     {
@@ -768,6 +797,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const uint64_t here = __shfl_sync(~0u, kept + take * tie, rank), before = __shfl_sync(~0u, upto, rank) - here;
     const unsigned here_ties = __shfl_sync(~0u, take, rank);
     const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
+    sync();                                      // no CTA leaves while another reads its memory
     if (goal >= before && goal - before < here) {
         // the warp's place in the CTA
         uint64_t from = before;
@@ -821,7 +851,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             }
         }
     }
-    sync();                                      // no CTA leaves while another reads its memory
 }
 
 // CTAs of a row: as many as keep a part within 16384 logits, and twice, four times as many where there
@@ -839,9 +868,9 @@ cudaError_t call(const Ctx& ctx, const SampleArgs& a, cudaStream_t st) {
     const int ctas = row_ctas(ctx.sm_count, a.tokens, a.vocab);
     // a row may begin anywhere in its first vector
     const int vectors = ((a.vocab + 2 * kN - 2) / kN + ctas - 1) / ctas;
-    // a list of all that a warp goes through, 16 bits each; of a quarter where CTAs share the SMs
+    // a list of all that a warp goes through, 16 bits each; of a half where CTAs share the SMs
     const bool alone = static_cast<int64_t>(a.tokens) * ctas <= 2 * ctx.sm_count;
-    const int room = (vectors + kWarps - 1) / kWarps * kN / (alone ? 1 : 4);
+    const int room = (vectors + kWarps - 1) / kWarps * kN / (alone ? 1 : 2);
     const size_t smem = static_cast<size_t>(vectors) * 16 + sizeof(uint16_t) * kWarps * room;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.tokens) * ctas);
