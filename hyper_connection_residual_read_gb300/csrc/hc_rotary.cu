@@ -41,44 +41,87 @@ __device__ __forceinline__ void load_weights(const void* w, int sub, float (&x)[
     raw.get(x);
 }
 
-// The 8 values of this lane, normed and rotated. c and s: this lane's cosines and sines (of its 8
-// elements for halves, of its 4 pairs for neighbours); `partner`: the lane of the group with the
-// other halves, or its own for lanes past the rotated dimensions.
-template <int kLanes, bool kInterleaved>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, const float (&w)[8], float eps, bool rotated, bool second,
-                                            int partner, const float (&c)[kInterleaved ? 4 : 8], const float (&s)[kInterleaved ? 4 : 8]) {
-    if (norm) {
-        float y[8];
+// The sum of squares of a lane's 8 values, neighbours first. (Products two at a time; a sum directly behind them
+// would be joined to an fma.)
+__device__ __forceinline__ float squares(const float (&x)[8]) {
+    float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], x[i]);
-        float sum = __fadd_rn(__fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3])), __fadd_rn(__fadd_rn(y[4], y[5]), __fadd_rn(y[6], y[7])));
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, d));
-        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / (8 * kLanes)), eps)));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t v = pair(x[i], x[i + 1]);
+        const float2 z = unpair(mul2(v, v));
+        y[i] = z.x, y[i + 1] = z.y;
     }
+    return __fadd_rn(__fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3])), __fadd_rn(__fadd_rn(y[4], y[5]), __fadd_rn(y[6], y[7])));
+}
+template <int kLanes>
+__device__ __forceinline__ float scale_of(float sum, float eps) {
+    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / (8 * kLanes)), eps)));
+}
+// The norms' scales of kQ heads, of whose squares each lane has its sum. The lanes share the heads: after an
+// exchange with the neighbour a lane goes on with half of them, so that four heads take five exchanges, a root
+// and a quotient instead of sixteen and four of each (8191 tokens of 32/8 heads: 52 us against @@).
+template <int kLanes, int kQ>
+__device__ __forceinline__ void scales_of(float (&sum)[kQ], int sub, float eps) {
+    const bool odd = sub & 1, upper = sub & 2;
+    float x;
+    if constexpr (kQ == 4) {
+        float a0 = odd ? sum[2] : sum[0], a1 = odd ? sum[3] : sum[1];
+        a0 = __fadd_rn(a0, __shfl_xor_sync(~0u, odd ? sum[0] : sum[2], 1));
+        a1 = __fadd_rn(a1, __shfl_xor_sync(~0u, odd ? sum[1] : sum[3], 1));
+        x = __fadd_rn(upper ? a1 : a0, __shfl_xor_sync(~0u, upper ? a0 : a1, 2));
+    } else {
+        x = __fadd_rn(odd ? sum[1] : sum[0], __shfl_xor_sync(~0u, odd ? sum[0] : sum[1], 1));
+        x = __fadd_rn(x, __shfl_xor_sync(~0u, x, 2));
+    }
+#pragma unroll
+    for (int d = 4; d < kLanes; d <<= 1) x = __fadd_rn(x, __shfl_xor_sync(~0u, x, d));
+    x = scale_of<kLanes>(x, eps);
+#pragma unroll
+    for (int n = 0; n < kQ; ++n) sum[n] = __shfl_sync(~0u, x, kQ == 4 ? (n >> 1) | ((n & 1) << 1) : n, kLanes);
+}
+// x r w.
+__device__ __forceinline__ void scaled(float (&x)[8], float r, const float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 y = unpair(mul2(mul2(pair(x[i], x[i + 1]), pair(r, r)), pair(w[i], w[i + 1])));
+        x[i] = y.x, x[i + 1] = y.y;
+    }
+}
+// The 8 values of this lane rotated. c and s: this lane's cosines and sines (of its 8 elements for halves, of its 4
+// pairs for neighbours); `partner`: the lane of the group with the other halves, or its own for lanes past
+// the rotated dimensions.
+template <int kLanes, bool kInterleaved>
+__device__ __forceinline__ void rotate(float (&x)[8], bool rotated, int partner, const float (&c)[kInterleaved ? 4 : 8],
+                                       const float (&s)[kInterleaved ? 4 : 8]) {
     if constexpr (kInterleaved) {
         if (rotated) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+                const float2 u = unpair(mul2(pair(x[2 * i], x[2 * i + 1]), pair(c[i], c[i])));
+                const float2 v = unpair(mul2(pair(x[2 * i + 1], x[2 * i]), pair(s[i], s[i])));
+                x[2 * i] = __fsub_rn(u.x, v.x);
+                x[2 * i + 1] = __fadd_rn(u.y, v.y);
             }
         }
     } else {
         // a c - b s of the first half, b c + a s of the second: s has the sign (a - b is a + (-b), rounded alike)
+        float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(~0u, x[i], partner, kLanes);
-            if (rotated) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]));
+        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(~0u, x[i], partner, kLanes);
+        if (rotated) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 u = unpair(mul2(pair(x[i], x[i + 1]), pair(c[i], c[i + 1])));
+                const float2 v = unpair(mul2(pair(o[i], o[i + 1]), pair(s[i], s[i + 1])));
+                x[i] = __fadd_rn(u.x, v.x), x[i + 1] = __fadd_rn(u.y, v.y);
+            }
         }
     }
 }
 
-// A thread keeps its token's cosines and sines and goes through heads: query heads blockIdx.y, blockIdx.y +
-// gridDim.y, ..., kQ of them on their way at once, then kv heads.
+// A thread keeps its token's cosines and sines and goes through heads. They are numbered through, the kv heads
+// first, and a CTA has each gridDim.y-th: the query heads of these, kQ of them on their way at once, then the kv
+// heads.
 template <int kD, int kDtype, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a, int* status) {
     begin_early();
@@ -121,28 +164,41 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a,
     float w[8] = {};
     if (a.r.q_norm && a.q_heads > 0) load_weights<kDtype>(a.r.q_norm, sub, w);
     const int64_t q0 = t * a.q_token + sub * 8;
-    for (int h0 = blockIdx.y; h0 < a.q_heads; h0 += kQ * gridDim.y) {
+    const int step = gridDim.y;
+    const int first = static_cast<int>(blockIdx.y) - a.c.kv_heads % step;
+    for (int h0 = first < 0 ? first + step : first; h0 < a.q_heads; h0 += kQ * step) {
         Raw8<kDtype> raw[kQ] = {};
 #pragma unroll
         for (int n = 0; n < kQ; ++n) {
-            const int h = h0 + n * gridDim.y;
+            const int h = h0 + n * step;
             const int64_t at = q0 + h * a.q_head;
             if (here && h < a.q_heads && HC_IN_RANGE(at, 8, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), status)) raw[n].load(a.q, at);
         }
+        float r[kQ] = {};
+        if (a.r.q_norm) {
+#pragma unroll
+            for (int n = 0; n < kQ; ++n) {
+                float x[8];
+                raw[n].get(x);
+                r[n] = squares(x);
+            }
+            scales_of<kLanes, kQ>(r, sub, a.r.eps);
+        }
 #pragma unroll
         for (int n = 0; n < kQ; ++n) {
-            const int h = h0 + n * gridDim.y;
+            const int h = h0 + n * step;
             if (h >= a.q_heads) break;
             float x[8];
             raw[n].get(x);
-            norm_rotate<kLanes, kInterleaved>(x, a.r.q_norm != nullptr, w, a.r.eps, rotated, second, partner, c, s);
+            if (a.r.q_norm) scaled(x, r[n], w);
+            rotate<kLanes, kInterleaved>(x, rotated, partner, c, s);
             const int64_t to = (t * a.q_heads + h) * kD + sub * 8;
             raw[n].set(x);
             if (here && HC_IN_RANGE(to, 8, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) raw[n].store(a.q_out, to);
         }
     }
     if (a.r.k_norm) load_weights<kDtype>(a.r.k_norm, sub, w);
-    for (int h = blockIdx.y; h < a.c.kv_heads; h += gridDim.y) {
+    for (int h = blockIdx.y; h < a.c.kv_heads; h += step) {
         Raw8<kDtype> raw = {}, value = {};
         if (here) {
             const int64_t k = t * a.k_token + h * a.k_head + sub * 8, v = t * a.v_token + h * a.v_head + sub * 8;
@@ -151,7 +207,13 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a,
         }
         float x[8];
         raw.get(x);
-        norm_rotate<kLanes, kInterleaved>(x, a.r.k_norm != nullptr, w, a.r.eps, rotated, second, partner, c, s);
+        if (a.r.k_norm) {
+            float sum = squares(x);
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, d));
+            scaled(x, scale_of<kLanes>(sum, a.r.eps), w);
+        }
+        rotate<kLanes, kInterleaved>(x, rotated, partner, c, s);
         Raw8<HC_DTYPE_FP32> key;
         key.set(x);
         uint32_t sm[2], code[2];
@@ -173,9 +235,10 @@ cudaError_t call(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
     constexpr int kTile = kThreads / (kD / 8);
     const int tiles = (a.tokens - 1) / kTile + 1;
     // as many CTAs for the heads of a tile as fill the GPU, and no more than heads
-    const int most = a.q_heads > a.c.kv_heads ? a.q_heads : a.c.kv_heads;
+    const int heads = a.q_heads + a.c.kv_heads;
     int split = (4 * ctx.sm_count + tiles - 1) / tiles;
-    split = split < most ? split : most;
+    split = split < heads ? split : heads;
+    split = split < 65535 ? split : 65535;
     const dim3 grid(tiles, split);
     return a.r.interleaved ? launch_early(rotary_kernel<kD, kDtype, true>, grid, kThreads, 0, st, a, ctx.s.status)
                            : launch_early(rotary_kernel<kD, kDtype, false>, grid, kThreads, 0, st, a, ctx.s.status);
