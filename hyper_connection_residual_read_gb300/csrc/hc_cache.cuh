@@ -123,20 +123,10 @@ __device__ __forceinline__ void extremes(const Raw8<HC_DTYPE_FP16>& r, float& lo
     lo = min_nan(__low2float(l), __high2float(l)), hi = max_nan(__low2float(h), __high2float(h));
 }
 
-// Rounds one group spread over kLanes neighbouring lanes; returns the lane's 8 codes
-// and, in sm, the packed bf16 step and minimum. A code is at most 15 by itself: s >= width
-// / 15 up to 2^-23, so that (x - m) / s rounds to 15 at most. 2^23 + 2^22 + z holds z rounded
-// to the nearest integer, ties to even, in its low bits.
-template <int kLanes, int kDtype>
-__device__ __forceinline__ uint32_t round_group(const Raw8<kDtype>& raw, uint32_t& sm) {
-    float lo, hi;
-    extremes(raw, lo, hi);
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(~0u, lo, d));
-        hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
-    }
-    const float m = bf16_floor(lo);
+// A group's step and minimum from its extremes: packed as the cache holds them, the minimum, and 1 / step
+// (0 where the step is). False for a group that is held as NaN.
+__device__ __forceinline__ bool group_steps(float lo, float hi, uint32_t& sm, float& m, float& r) {
+    m = bf16_floor(lo);
     const float width = __fsub_rn(hi, m);
     float s = bf16_ceil(__fmul_rn(width, 1.0f / 15.0f));
     // 2^-126, so that 1 / s is finite
@@ -144,9 +134,16 @@ __device__ __forceinline__ uint32_t round_group(const Raw8<kDtype>& raw, uint32_
     const float top = __uint_as_float(0x7F7FFFFFu);
     if (!(fabsf(lo) <= top && fabsf(hi) <= top && s <= top)) {
         sm = 0x7FC07FC0u;
-        return 0;
+        return false;
     }
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    r = s > 0.f ? __frcp_rn(s) : 0.f;
+    sm = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
+    return true;
+}
+// A lane's 8 codes. One is at most 15 by itself: s >= width / 15 up to 2^-23, so that (x - m) / s rounds to 15 at
+// most. 2^23 + 2^22 + z holds z rounded to the nearest integer, ties to even, in its low bits.
+template <int kDtype>
+__device__ __forceinline__ uint32_t group_codes(const Raw8<kDtype>& raw, float m, float r) {
     float x[8];
     raw.get(x);
     constexpr float kRound = 12582912.f;
@@ -162,8 +159,35 @@ __device__ __forceinline__ uint32_t round_group(const Raw8<kDtype>& raw, uint32_
     uint32_t code = bits[7];
 #pragma unroll
     for (int i = 6; i >= 0; --i) code = code * 16 + bits[i];
-    sm = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
     return code - 0x4B400000u * 0x11111111u;
+}
+// Rounds one group spread over kLanes neighbouring lanes; returns the lane's 8 codes
+// and, in sm, the packed bf16 step and minimum.
+template <int kLanes, int kDtype>
+__device__ __forceinline__ uint32_t round_group(const Raw8<kDtype>& raw, uint32_t& sm) {
+    float lo, hi, m, r;
+    extremes(raw, lo, hi);
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(~0u, lo, d));
+        hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
+    }
+    return group_steps(lo, hi, sm, m, r) ? group_codes(raw, m, r) : 0;
+}
+// The same for lanes of 8 values of each half of a group.
+template <int kLanes, int kDtype>
+__device__ __forceinline__ uint2 round_group(const Raw8<kDtype> (&raw)[2], uint32_t& sm) {
+    float lo, hi, lo2, hi2, m, r;
+    extremes(raw[0], lo, hi);
+    extremes(raw[1], lo2, hi2);
+    lo = min_nan(lo, lo2), hi = max_nan(hi, hi2);
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(~0u, lo, d));
+        hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
+    }
+    if (!group_steps(lo, hi, sm, m, r)) return make_uint2(0, 0);
+    return make_uint2(group_codes(raw[0], m, r), group_codes(raw[1], m, r));
 }
 
 // Index of a slot's group among all groups of the cache, or -1 (with the status bit)

@@ -1,11 +1,13 @@
 // Queries and keys normed by head and rotated by their positions, keys and values rounded into
 // the 4-bit cache, in one pass over the projection's output.
 //
-// A head of a token is D values, held by D / 8 neighbouring lanes of 8 values each: its squares
-// are summed within a lane and then by shuffles, neighbours first, which is the order that the
-// operator states; the second element of a pair is in the same lane (neighbouring pairs) or D_rot
-// / 16 lanes on (halves). Every step is a single rounded operation (no fma): the codes of a key
-// are a step function of it, and would differ from place to place with the last bit of it.
+// A head of a token is D values, held by D / 16 neighbouring lanes: 8 of the first half and the 8 as far into the
+// second, 16 bytes each. So the pairs of halves lie in one lane (where all dimensions are rotated), and so do
+// neighbouring pairs. Squares are summed within a lane and then by shuffles, neighbours first, which is the
+// order that the operator states. Every step is a single rounded operation (no fma): the codes of a key are a
+// step function of it, and would differ from place to place with the last bit of it.
+//
+// MEASURED
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,15 +36,17 @@ __device__ __forceinline__ int table_row(const RotaryArgs& a, int64_t t, int axi
     return p;
 }
 
+enum Pairs { kHalves, kNeighbours, kPartHalves };     // (i, i + D / 2); (2i, 2i + 1); (i, i + dim / 2), dim < D
+
 template <int kDtype>
-__device__ __forceinline__ void load_weights(const void* w, int sub, float (&x)[8]) {
+__device__ __forceinline__ void load_weights(const void* w, int at, float (&x)[8]) {
     Raw8<kDtype> raw;
-    raw.load(w, sub * 8);
+    raw.load(w, at);
     raw.get(x);
 }
 
-// The sum of squares of a lane's 8 values, neighbours first. (Products two at a time; a sum directly behind them
-// would be joined to an fma.)
+// The sum of squares of 8 values, neighbours first. (Products two at a time; a sum directly behind them would be
+// joined to an fma.)
 __device__ __forceinline__ float squares(const float (&x)[8]) {
     float y[8];
 #pragma unroll
@@ -53,31 +57,30 @@ __device__ __forceinline__ float squares(const float (&x)[8]) {
     }
     return __fadd_rn(__fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3])), __fadd_rn(__fadd_rn(y[4], y[5]), __fadd_rn(y[6], y[7])));
 }
-template <int kLanes>
-__device__ __forceinline__ float scale_of(float sum, float eps) {
-    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / (8 * kLanes)), eps)));
-}
-// The norms' scales of kQ heads, of whose squares each lane has its sum. The lanes share the heads: after an
-// exchange with the neighbour a lane goes on with half of them, so that four heads take five exchanges, a root
-// and a quotient instead of sixteen and four of each (8191 tokens of 32/8 heads: 52 us against @@).
-template <int kLanes, int kQ>
-__device__ __forceinline__ void scales_of(float (&sum)[kQ], int sub, float eps) {
-    const bool odd = sub & 1, upper = sub & 2;
-    float x;
-    if constexpr (kQ == 4) {
-        float a0 = odd ? sum[2] : sum[0], a1 = odd ? sum[3] : sum[1];
-        a0 = __fadd_rn(a0, __shfl_xor_sync(~0u, odd ? sum[0] : sum[2], 1));
-        a1 = __fadd_rn(a1, __shfl_xor_sync(~0u, odd ? sum[1] : sum[3], 1));
-        x = __fadd_rn(upper ? a1 : a0, __shfl_xor_sync(~0u, upper ? a0 : a1, 2));
-    } else {
-        x = __fadd_rn(odd ? sum[1] : sum[0], __shfl_xor_sync(~0u, odd ? sum[0] : sum[1], 1));
-        x = __fadd_rn(x, __shfl_xor_sync(~0u, x, 2));
+__device__ __forceinline__ float add_xor(float x, float sent, int d) { return __fadd_rn(x, __shfl_xor_sync(~0u, sent, d)); }
+
+// The norms' scales of kN heads from each lane's sums of its two halves. The lanes share them: in an exchange with
+// a neighbour a lane gives half of what it has and goes on with the others, so that one root and one quotient
+// do for two heads.
+template <int kLanes, int kN>
+__device__ __forceinline__ void scales_of(const float (&sum)[kN][2], int sub, float eps, float (&r)[kN]) {
+    const bool odd = sub & 1, last = sub & 4;
+    float x[2];                              // of this lane's head
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        x[h] = kN == 2 ? add_xor(odd ? sum[kN - 1][h] : sum[0][h], odd ? sum[0][h] : sum[kN - 1][h], 1) : add_xor(sum[0][h], sum[0][h], 1);
+        x[h] = add_xor(x[h], x[h], 2);
     }
+    float total;
+    if constexpr (kLanes == 8) {             // a half a lane, then both
+        total = add_xor(last ? x[1] : x[0], last ? x[0] : x[1], 4);
+        total = add_xor(total, total, 4);
+    } else {
+        total = __fadd_rn(x[0], x[1]);
+    }
+    total = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(total, 1.f / (16 * kLanes)), eps)));
 #pragma unroll
-    for (int d = 4; d < kLanes; d <<= 1) x = __fadd_rn(x, __shfl_xor_sync(~0u, x, d));
-    x = scale_of<kLanes>(x, eps);
-#pragma unroll
-    for (int n = 0; n < kQ; ++n) sum[n] = __shfl_sync(~0u, x, kQ == 4 ? (n >> 1) | ((n & 1) << 1) : n, kLanes);
+    for (int n = 0; n < kN; ++n) r[n] = kN == 1 ? total : __shfl_sync(~0u, total, n, kLanes);
 }
 // x r w.
 __device__ __forceinline__ void scaled(float (&x)[8], float r, const float (&w)[8]) {
@@ -87,55 +90,75 @@ __device__ __forceinline__ void scaled(float (&x)[8], float r, const float (&w)[
         x[i] = y.x, x[i + 1] = y.y;
     }
 }
-// The 8 values of this lane rotated. c and s: this lane's cosines and sines (of its 8 elements for halves, of its 4
-// pairs for neighbours); `partner`: the lane of the group with the other halves, or its own for lanes past
-// the rotated dimensions.
-template <int kLanes, bool kInterleaved>
-__device__ __forceinline__ void rotate(float (&x)[8], bool rotated, int partner, const float (&c)[kInterleaved ? 4 : 8],
-                                       const float (&s)[kInterleaved ? 4 : 8]) {
-    if constexpr (kInterleaved) {
-        if (rotated) {
+
+// What a lane keeps of its token's angles: of its 8 pairs of halves; of the 4 pairs of each of its vectors; of
+// the 8 elements of each, with the sign of what the other half adds in the sine.
+template <Pairs kPairs>
+struct Angles {
+    static constexpr int kN = kPairs == kPartHalves ? 16 : 8;
+    float c[kN], s[kN];
+    bool turns[2];                           // whether the vectors are rotated
+};
+// Lane and vector of the other half of vector `chunk` of a head, of dim / 16 vectors a half.
+__device__ __forceinline__ int other_half(int chunk, int half) { return chunk < half ? chunk + half : chunk < 2 * half ? chunk - half : chunk; }
+
+template <int kLanes, Pairs kPairs>
+__device__ __forceinline__ void rotate(float (&x)[2][8], const Angles<kPairs>& t, int sub, int half) {
+    if constexpr (kPairs == kHalves) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t a = pair(x[0][i], x[0][i + 1]), b = pair(x[1][i], x[1][i + 1]);
+            const uint64_t c = pair(t.c[i], t.c[i + 1]), s = pair(t.s[i], t.s[i + 1]);
+            const float2 ac = unpair(mul2(a, c)), bs = unpair(mul2(b, s)), bc = unpair(mul2(b, c)), as = unpair(mul2(a, s));
+            x[0][i] = __fsub_rn(ac.x, bs.x), x[0][i + 1] = __fsub_rn(ac.y, bs.y);
+            x[1][i] = __fadd_rn(bc.x, as.x), x[1][i + 1] = __fadd_rn(bc.y, as.y);
+        }
+    } else if constexpr (kPairs == kNeighbours) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            if (!t.turns[v]) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 u = unpair(mul2(pair(x[2 * i], x[2 * i + 1]), pair(c[i], c[i])));
-                const float2 v = unpair(mul2(pair(x[2 * i + 1], x[2 * i]), pair(s[i], s[i])));
-                x[2 * i] = __fsub_rn(u.x, v.x);
-                x[2 * i + 1] = __fadd_rn(u.y, v.y);
+                const float a = x[v][2 * i], b = x[v][2 * i + 1];
+                const float2 c = unpair(mul2(pair(a, b), pair(t.c[4 * v + i], t.c[4 * v + i])));
+                const float2 s = unpair(mul2(pair(b, a), pair(t.s[4 * v + i], t.s[4 * v + i])));
+                x[v][2 * i] = __fsub_rn(c.x, s.x), x[v][2 * i + 1] = __fadd_rn(c.y, s.y);
             }
         }
     } else {
-        // a c - b s of the first half, b c + a s of the second: s has the sign (a - b is a + (-b), rounded alike)
-        float o[8];
+        float o[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(~0u, x[i], partner, kLanes);
-        if (rotated) {
+        for (int v = 0; v < 2; ++v) {
+            const int from = other_half(v * kLanes + sub, half);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float2 u = unpair(mul2(pair(x[i], x[i + 1]), pair(c[i], c[i + 1])));
-                const float2 v = unpair(mul2(pair(o[i], o[i + 1]), pair(s[i], s[i + 1])));
-                x[i] = __fadd_rn(u.x, v.x), x[i + 1] = __fadd_rn(u.y, v.y);
+            for (int i = 0; i < 8; ++i) {
+                const float low = __shfl_sync(~0u, x[0][i], from % kLanes, kLanes), high = __shfl_sync(~0u, x[1][i], from % kLanes, kLanes);
+                o[v][i] = from < kLanes ? low : high;
             }
+        }
+        // a c - b s of the first half, b c + a s of the second (a - b is a + (-b), rounded alike)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            if (!t.turns[v]) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[v][i] = __fadd_rn(__fmul_rn(x[v][i], t.c[8 * v + i]), __fmul_rn(o[v][i], t.s[8 * v + i]));
         }
     }
 }
 
-// A thread keeps its token's cosines and sines and goes through heads. They are numbered through, the kv heads
-// first, and a CTA has each gridDim.y-th: the query heads of these, kQ of them on their way at once, then the kv
-// heads.
-template <int kD, int kDtype, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a, int* status) {
+// A thread keeps its token's angles and goes through heads. They are numbered through, the kv heads first, and a
+// CTA has each gridDim.y-th: the query heads of these, kQ of them on their way at once, then the kv heads.
+template <int kD, int kDtype, Pairs kPairs>
+__global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : 3) rotary_kernel(const RotaryArgs a, int* status) {
     begin_early();
-    constexpr int kLanes = kD / 8, kTile = kThreads / kLanes, kAngles = kInterleaved ? 4 : 8;
-    constexpr int kQ = kDtype == HC_DTYPE_FP32 ? 2 : 4;
+    constexpr int kLanes = kD / 16, kTile = kThreads / kLanes, kQ = 2;
     const int sub = threadIdx.x % kLanes;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x / kLanes;
     const int sh = 31 - __clz(a.c.block_size);
     // a lane without a token still takes part in the shuffles
     bool here = t < a.tokens;
-    const int half = a.r.dim / 2, half_lanes = half / 8;
-    const bool rotated = sub < 2 * half_lanes, second = sub >= half_lanes;
-    const int partner = !rotated ? sub : second ? sub - half_lanes : sub + half_lanes;
-    float c[kAngles] = {}, s[kAngles] = {};
+    const int half = a.r.dim / 16;               // vectors of a half of the rotated dimensions
+    Angles<kPairs> angles = {};
     int64_t slot = -1;
     if (here) {
         if (HC_IN_RANGE(t, 1, a.tokens, status)) slot = a.slots[t];
@@ -144,79 +167,104 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a,
                 const int64_t at = static_cast<int64_t>(x) * a.tokens + t;
                 here = here && HC_IN_RANGE(at, 1, static_cast<size_t>(a.r.axes) * a.tokens, status) && a.positions[at] >= 0;
             }
-        if (here && rotated) {
-            const int i0 = kInterleaved ? sub * 4 : (second ? sub - half_lanes : sub) * 8;
-            int axis = 0, row = table_row(a, t, a.r.axis_of ? a.r.axis_of[i0] : 0, status);
-            if (a.r.axis_of) axis = a.r.axis_of[i0];
+    }
 #pragma unroll
-            for (int i = 0; i < kAngles; ++i) {
-                if (i > 0 && a.r.axis_of && a.r.axis_of[i0 + i] != axis) {
-                    axis = a.r.axis_of[i0 + i];
-                    row = table_row(a, t, axis, status);
-                }
-                const int64_t at = static_cast<int64_t>(row) * a.r.dim + i0 + i;
-                if (!HC_IN_RANGE(at + half, 1, static_cast<size_t>(a.r.length) * a.r.dim, status)) continue;
-                c[i] = a.r.cos_sin[at], s[i] = a.r.cos_sin[at + half];
-                if (!kInterleaved && !second) s[i] = -s[i];
+    for (int v = 0; v < 2; ++v) {
+        const int chunk = v * kLanes + sub;
+        angles.turns[v] = chunk < 2 * half;
+        if (!here || !angles.turns[v] || (kPairs == kHalves && v == 1)) continue;
+        constexpr int kEach = kPairs == kNeighbours ? 4 : 8;
+        const int i0 = kPairs == kNeighbours ? chunk * 4 : (chunk < half ? chunk : chunk - half) * 8;
+        const bool minus = kPairs == kPartHalves && chunk < half;
+        int axis = a.r.axis_of ? a.r.axis_of[i0] : 0, row = table_row(a, t, axis, status);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (i > 0 && a.r.axis_of && a.r.axis_of[i0 + i] != axis) {
+                axis = a.r.axis_of[i0 + i];
+                row = table_row(a, t, axis, status);
             }
+            const int64_t at = static_cast<int64_t>(row) * a.r.dim + i0 + i;
+            if (!HC_IN_RANGE(at + a.r.dim / 2, 1, static_cast<size_t>(a.r.length) * a.r.dim, status)) continue;
+            const float s = a.r.cos_sin[at + a.r.dim / 2];
+            angles.c[kEach * v + i] = a.r.cos_sin[at], angles.s[kEach * v + i] = minus ? -s : s;
         }
     }
-    float w[8] = {};
-    if (a.r.q_norm && a.q_heads > 0) load_weights<kDtype>(a.r.q_norm, sub, w);
-    const int64_t q0 = t * a.q_token + sub * 8;
+    // this lane's two vectors of a head that begins at `at`
+    auto bring = [&](const void* from, int64_t at, size_t extent, Raw8<kDtype> (&raw)[2]) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            if (HC_IN_RANGE(at + v * (kD / 2) + sub * 8, 8, extent, status)) raw[v].load(from, at + v * (kD / 2) + sub * 8);
+    };
+    float w[2][8] = {};
+    if (a.r.q_norm && a.q_heads > 0)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) load_weights<kDtype>(a.r.q_norm, v * (kD / 2) + sub * 8, w[v]);
     const int step = gridDim.y;
     const int first = static_cast<int>(blockIdx.y) - a.c.kv_heads % step;
     for (int h0 = first < 0 ? first + step : first; h0 < a.q_heads; h0 += kQ * step) {
-        Raw8<kDtype> raw[kQ] = {};
+        Raw8<kDtype> raw[kQ][2] = {};
 #pragma unroll
         for (int n = 0; n < kQ; ++n) {
             const int h = h0 + n * step;
-            const int64_t at = q0 + h * a.q_head;
-            if (here && h < a.q_heads && HC_IN_RANGE(at, 8, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), status)) raw[n].load(a.q, at);
+            if (here && h < a.q_heads) bring(a.q, t * a.q_token + h * a.q_head, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), raw[n]);
         }
         float r[kQ] = {};
         if (a.r.q_norm) {
+            float sum[kQ][2];
 #pragma unroll
-            for (int n = 0; n < kQ; ++n) {
-                float x[8];
-                raw[n].get(x);
-                r[n] = squares(x);
-            }
-            scales_of<kLanes, kQ>(r, sub, a.r.eps);
+            for (int n = 0; n < kQ; ++n)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    float x[8];
+                    raw[n][v].get(x);
+                    sum[n][v] = squares(x);
+                }
+            scales_of<kLanes, kQ>(sum, sub, a.r.eps, r);
         }
 #pragma unroll
         for (int n = 0; n < kQ; ++n) {
             const int h = h0 + n * step;
             if (h >= a.q_heads) break;
-            float x[8];
-            raw[n].get(x);
-            if (a.r.q_norm) scaled(x, r[n], w);
-            rotate<kLanes, kInterleaved>(x, rotated, partner, c, s);
+            float x[2][8];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                raw[n][v].get(x[v]);
+                if (a.r.q_norm) scaled(x[v], r[n], w[v]);
+            }
+            rotate<kLanes, kPairs>(x, angles, sub, half);
             const int64_t to = (t * a.q_heads + h) * kD + sub * 8;
-            raw[n].set(x);
-            if (here && HC_IN_RANGE(to, 8, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) raw[n].store(a.q_out, to);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                raw[n][v].set(x[v]);
+                if (here && HC_IN_RANGE(to + v * (kD / 2), 8, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) raw[n][v].store(a.q_out, to + v * (kD / 2));
+            }
         }
     }
-    if (a.r.k_norm) load_weights<kDtype>(a.r.k_norm, sub, w);
-    for (int h = blockIdx.y; h < a.c.kv_heads; h += step) {
-        Raw8<kDtype> raw = {}, value = {};
-        if (here) {
-            const int64_t k = t * a.k_token + h * a.k_head + sub * 8, v = t * a.v_token + h * a.v_head + sub * 8;
-            if (HC_IN_RANGE(k, 8, row_extent(a.tokens, a.c.kv_heads, kD, a.k_token, a.k_head), status)) raw.load(a.k, k);
-            if (HC_IN_RANGE(v, 8, row_extent(a.tokens, a.c.kv_heads, kD, a.v_token, a.v_head), status)) value.load(a.v, v);
-        }
-        float x[8];
-        raw.get(x);
-        if (a.r.k_norm) {
-            float sum = squares(x);
+    if (a.r.k_norm)
 #pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, d));
-            scaled(x, scale_of<kLanes>(sum, a.r.eps), w);
+        for (int v = 0; v < 2; ++v) load_weights<kDtype>(a.r.k_norm, v * (kD / 2) + sub * 8, w[v]);
+    for (int h = blockIdx.y; h < a.c.kv_heads; h += step) {
+        Raw8<kDtype> raw[2] = {}, value[2] = {};
+        if (here) {
+            bring(a.k, t * a.k_token + h * a.k_head, row_extent(a.tokens, a.c.kv_heads, kD, a.k_token, a.k_head), raw);
+            bring(a.v, t * a.v_token + h * a.v_head, row_extent(a.tokens, a.c.kv_heads, kD, a.v_token, a.v_head), value);
         }
-        rotate<kLanes, kInterleaved>(x, rotated, partner, c, s);
-        Raw8<HC_DTYPE_FP32> key;
-        key.set(x);
-        uint32_t sm[2], code[2];
+        float x[2][8];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) raw[v].get(x[v]);
+        if (a.r.k_norm) {
+            const float sum[1][2] = {{squares(x[0]), squares(x[1])}};
+            float r[1];
+            scales_of<kLanes, 1>(sum, sub, a.r.eps, r);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) scaled(x[v], r[0], w[v]);
+        }
+        rotate<kLanes, kPairs>(x, angles, sub, half);
+        Raw8<HC_DTYPE_FP32> key[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) key[v].set(x[v]);
+        uint32_t sm[2];
+        uint2 code[2];
         code[0] = round_group<kLanes>(key, sm[0]);
         code[1] = round_group<kLanes>(value, sm[1]);
         if (!here || slot < 0) continue;
@@ -224,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a,
         for (int kv = 0; kv < 2; ++kv) {
             const int64_t g = group_index(a.c, sh, slot, kv, h, status);
             if (g < 0 || !HC_IN_RANGE(g, 1, group_count(a.c), status)) continue;
-            reinterpret_cast<uint32_t*>(a.c.codes)[g * kLanes + sub] = code[kv];
+            uint32_t* to = reinterpret_cast<uint32_t*>(a.c.codes) + g * (2 * kLanes) + sub;
+            to[0] = code[kv].x, to[kLanes] = code[kv].y;
             if (sub == 0) reinterpret_cast<uint32_t*>(a.c.scales)[g] = sm[kv];
         }
     }
@@ -232,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a,
 
 template <int kD, int kDtype>
 cudaError_t call(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
-    constexpr int kTile = kThreads / (kD / 8);
+    constexpr int kTile = kThreads / (kD / 16);
     const int tiles = (a.tokens - 1) / kTile + 1;
     // as many CTAs for the heads of a tile as fill the GPU, and no more than heads
     const int heads = a.q_heads + a.c.kv_heads;
@@ -240,8 +289,9 @@ cudaError_t call(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
     split = split < heads ? split : heads;
     split = split < 65535 ? split : 65535;
     const dim3 grid(tiles, split);
-    return a.r.interleaved ? launch_early(rotary_kernel<kD, kDtype, true>, grid, kThreads, 0, st, a, ctx.s.status)
-                           : launch_early(rotary_kernel<kD, kDtype, false>, grid, kThreads, 0, st, a, ctx.s.status);
+    if (a.r.interleaved || a.r.dim == 0) return launch_early(rotary_kernel<kD, kDtype, kNeighbours>, grid, kThreads, 0, st, a, ctx.s.status);
+    if (a.r.dim == kD) return launch_early(rotary_kernel<kD, kDtype, kHalves>, grid, kThreads, 0, st, a, ctx.s.status);
+    return launch_early(rotary_kernel<kD, kDtype, kPartHalves>, grid, kThreads, 0, st, a, ctx.s.status);
 }
 
 template <int kDtype>
