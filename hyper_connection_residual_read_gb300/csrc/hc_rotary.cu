@@ -20,6 +20,7 @@ namespace hc {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 3;
 
 // A token's row of the table for frequency i.
 __device__ __forceinline__ int table_row(const RotaryArgs& a, int64_t t, int axis, int* status) {
@@ -43,6 +44,19 @@ __device__ __forceinline__ void load_weights(const void* w, int at, float (&x)[8
     Raw8<kDtype> raw;
     raw.load(w, at);
     raw.get(x);
+}
+
+// This thread's 8 values of a ring's slot.
+template <int kDtype, int kPieces>
+__device__ __forceinline__ Raw8<kDtype> from_ring(const uint4 (&slot)[kPieces][kThreads]) {
+    Raw8<kDtype> raw;
+    if constexpr (kPieces == 1) {
+        raw.v = slot[0][threadIdx.x];
+    } else {
+        raw.a = *reinterpret_cast<const float4*>(&slot[0][threadIdx.x]);
+        raw.b = *reinterpret_cast<const float4*>(&slot[1][threadIdx.x]);
+    }
+    return raw;
 }
 
 // The sum of squares of 8 values, neighbours first. (Products two at a time; a sum directly behind them would be
@@ -147,11 +161,12 @@ __device__ __forceinline__ void rotate(float (&x)[2][8], const Angles<kPairs>& t
 }
 
 // A thread keeps its token's angles and goes through heads. They are numbered through, the kv heads first, and a
-// CTA has each gridDim.y-th: the query heads of these, kQ of them on their way at once, then the kv heads.
+// CTA has each gridDim.y-th: the query heads of these, two at a time, then the kv heads, a key and a value. What a
+// thread needs comes to a ring of its own in shared memory, two such steps ahead.
 template <int kD, int kDtype, Pairs kPairs>
-__global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : 3) rotary_kernel(const RotaryArgs a, int* status) {
+__global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : kCtasPerSm) rotary_kernel(const RotaryArgs a, int* status) {
     begin_early();
-    constexpr int kLanes = kD / 16, kTile = kThreads / kLanes, kQ = 2;
+    constexpr int kLanes = kD / 16, kTile = kThreads / kLanes;
     const int sub = threadIdx.x % kLanes;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x / kLanes;
     const int sh = 31 - __clz(a.c.block_size);
@@ -189,69 +204,90 @@ __global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : 3) rotar
             angles.c[kEach * v + i] = a.r.cos_sin[at], angles.s[kEach * v + i] = minus ? -s : s;
         }
     }
-    // this lane's two vectors of a head that begins at `at`
-    auto bring = [&](const void* from, int64_t at, size_t extent, Raw8<kDtype> (&raw)[2]) {
+    // the CTA's heads: q0 + j step, j < nq, and k0 + j step, j < nk
+    const int step = gridDim.y, kv_heads = a.c.kv_heads, k0 = blockIdx.y, q0 = (k0 + step - kv_heads % step) % step;
+    const int nq = a.q_heads > q0 ? (a.q_heads - q0 - 1) / step + 1 : 0, nk = kv_heads > k0 ? (kv_heads - k0 - 1) / step + 1 : 0;
+    constexpr int kPieces = kDtype == HC_DTYPE_FP32 ? 2 : 1, kRing = kDtype == HC_DTYPE_FP32 ? 1 : 3;   // 16 bytes a piece
+    __shared__ uint4 ring[kRing][2][2][kPieces][kThreads];       // [step][head, or key and value][half]
+    const int q_steps = (nq + 1) / 2, steps = q_steps + nk;
+    auto bring = [&](uint4 (&to)[2][kPieces][kThreads], const void* from, int64_t at, size_t extent) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-            if (HC_IN_RANGE(at + v * (kD / 2) + sub * 8, 8, extent, status)) raw[v].load(from, at + v * (kD / 2) + sub * 8);
+        for (int v = 0; v < 2; ++v) {
+            if (!HC_IN_RANGE(at + v * (kD / 2), 8, extent, status)) continue;
+            const unsigned char* bytes = static_cast<const unsigned char*>(from) + (at + v * (kD / 2)) * (2 * kPieces);
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e) copy16(tc::smem_u32(&to[v][e][threadIdx.x]), bytes + 16 * e);
+        }
+    };
+    auto issue = [&](int b) {
+        if (here && b < steps) {
+            auto& to = ring[b % kRing];
+            if (b < q_steps) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    if (2 * b + n < nq)
+                        bring(to[n], a.q, t * a.q_token + static_cast<int64_t>(q0 + (2 * b + n) * step) * a.q_head + sub * 8,
+                              row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head));
+            } else {
+                const int h = k0 + (b - q_steps) * step;
+                bring(to[0], a.k, t * a.k_token + h * a.k_head + sub * 8, row_extent(a.tokens, kv_heads, kD, a.k_token, a.k_head));
+                bring(to[1], a.v, t * a.v_token + h * a.v_head + sub * 8, row_extent(a.tokens, kv_heads, kD, a.v_token, a.v_head));
+            }
+        }
+        copy_commit();
     };
     float w[2][8] = {};
-    if (a.r.q_norm && a.q_heads > 0)
+    auto take_weights = [&](const void* from) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) load_weights<kDtype>(a.r.q_norm, v * (kD / 2) + sub * 8, w[v]);
-    const int step = gridDim.y;
-    const int first = static_cast<int>(blockIdx.y) - a.c.kv_heads % step;
-    for (int h0 = first < 0 ? first + step : first; h0 < a.q_heads; h0 += kQ * step) {
-        Raw8<kDtype> raw[kQ][2] = {};
+        for (int v = 0; v < 2; ++v) load_weights<kDtype>(from, v * (kD / 2) + sub * 8, w[v]);
+    };
 #pragma unroll
-        for (int n = 0; n < kQ; ++n) {
-            const int h = h0 + n * step;
-            if (here && h < a.q_heads) bring(a.q, t * a.q_token + h * a.q_head, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), raw[n]);
-        }
-        float r[kQ] = {};
-        if (a.r.q_norm) {
-            float sum[kQ][2];
+    for (int b = 0; b < kRing - 1; ++b) issue(b);
+    if (a.r.q_norm && nq > 0) take_weights(a.r.q_norm);
+    for (int b = 0; b < steps; ++b) {
+        issue(b + kRing - 1);
+        copy_wait<kRing - 1>();
+        auto& in = ring[b % kRing];
+        if (b < q_steps) {
+            float r[2] = {};
+            if (a.r.q_norm) {
+                float sum[2][2];
 #pragma unroll
-            for (int n = 0; n < kQ; ++n)
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        float x[8];
+                        from_ring<kDtype>(in[n][v]).get(x);
+                        sum[n][v] = squares(x);
+                    }
+                scales_of<kLanes, 2>(sum, sub, a.r.eps, r);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int h = q0 + (2 * b + n) * step;
+                if (2 * b + n >= nq) break;
+                float x[2][8];
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    float x[8];
-                    raw[n][v].get(x);
-                    sum[n][v] = squares(x);
+                    from_ring<kDtype>(in[n][v]).get(x[v]);
+                    if (a.r.q_norm) scaled(x[v], r[n], w[v]);
                 }
-            scales_of<kLanes, kQ>(sum, sub, a.r.eps, r);
-        }
+                rotate<kLanes, kPairs>(x, angles, sub, half);
+                const int64_t to = (t * a.q_heads + h) * kD + sub * 8;
 #pragma unroll
-        for (int n = 0; n < kQ; ++n) {
-            const int h = h0 + n * step;
-            if (h >= a.q_heads) break;
-            float x[2][8];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                raw[n][v].get(x[v]);
-                if (a.r.q_norm) scaled(x[v], r[n], w[v]);
+                for (int v = 0; v < 2; ++v) {
+                    Raw8<kDtype> out;
+                    out.set(x[v]);
+                    if (here && HC_IN_RANGE(to + v * (kD / 2), 8, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) out.store(a.q_out, to + v * (kD / 2));
+                }
             }
-            rotate<kLanes, kPairs>(x, angles, sub, half);
-            const int64_t to = (t * a.q_heads + h) * kD + sub * 8;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                raw[n][v].set(x[v]);
-                if (here && HC_IN_RANGE(to + v * (kD / 2), 8, static_cast<size_t>(a.tokens) * a.q_heads * kD, status)) raw[n][v].store(a.q_out, to + v * (kD / 2));
-            }
+            continue;
         }
-    }
-    if (a.r.k_norm)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) load_weights<kDtype>(a.r.k_norm, v * (kD / 2) + sub * 8, w[v]);
-    for (int h = blockIdx.y; h < a.c.kv_heads; h += step) {
-        Raw8<kDtype> raw[2] = {}, value[2] = {};
-        if (here) {
-            bring(a.k, t * a.k_token + h * a.k_head, row_extent(a.tokens, a.c.kv_heads, kD, a.k_token, a.k_head), raw);
-            bring(a.v, t * a.v_token + h * a.v_head, row_extent(a.tokens, a.c.kv_heads, kD, a.v_token, a.v_head), value);
-        }
+        if (b == q_steps && a.r.k_norm) take_weights(a.r.k_norm);
+        const int h = k0 + (b - q_steps) * step;
         float x[2][8];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) raw[v].get(x[v]);
+        for (int v = 0; v < 2; ++v) from_ring<kDtype>(in[0][v]).get(x[v]);
         if (a.r.k_norm) {
             const float sum[1][2] = {{squares(x[0]), squares(x[1])}};
             float r[1];
@@ -263,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : 3) rotar
         Raw8<HC_DTYPE_FP32> key[2];
 #pragma unroll
         for (int v = 0; v < 2; ++v) key[v].set(x[v]);
+        const Raw8<kDtype> value[2] = {from_ring<kDtype>(in[1][0]), from_ring<kDtype>(in[1][1])};
         uint32_t sm[2];
         uint2 code[2];
         code[0] = round_group<kLanes>(key, sm[0]);
@@ -277,17 +314,26 @@ __global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : 3) rotar
             if (sub == 0) reinterpret_cast<uint32_t*>(a.c.scales)[g] = sm[kv];
         }
     }
+    copy_wait<0>();
+}
+
+// CTAs that share a tile's heads: those that take the fewest rounds of all resident CTAs, each as long as its
+// heads and two more for its start (8191 tokens of 40 heads: 5 CTAs take 34.9 us, 3 36.2, 10 38.9).
+int head_split(int tiles, int heads, int resident) {
+    int best = 1;
+    int64_t least = -1;
+    for (int n = 1; n <= heads && n <= 64; ++n) {
+        const int64_t rounds = (static_cast<int64_t>(tiles) * n + resident - 1) / resident, cost = rounds * ((heads + n - 1) / n + 2);
+        if (least < 0 || cost < least) least = cost, best = n;
+    }
+    return best;
 }
 
 template <int kD, int kDtype>
 cudaError_t call(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
     constexpr int kTile = kThreads / (kD / 16);
     const int tiles = (a.tokens - 1) / kTile + 1;
-    // as many CTAs for the heads of a tile as fill the GPU, and no more than heads
-    const int heads = a.q_heads + a.c.kv_heads;
-    int split = (4 * ctx.sm_count + tiles - 1) / tiles;
-    split = split < heads ? split : heads;
-    split = split < 65535 ? split : 65535;
+    const int split = head_split(tiles, a.q_heads + a.c.kv_heads, kCtasPerSm * ctx.sm_count);
     const dim3 grid(tiles, split);
     if (a.r.interleaved || a.r.dim == 0) return launch_early(rotary_kernel<kD, kDtype, kNeighbours>, grid, kThreads, 0, st, a, ctx.s.status);
     if (a.r.dim == kD) return launch_early(rotary_kernel<kD, kDtype, kHalves>, grid, kThreads, 0, st, a, ctx.s.status);
