@@ -693,7 +693,31 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         const bool whole = done.u0 == 0 && done.u1 == done.units;
         float* piece = scratch + (static_cast<int64_t>(blockIdx.x) * 2 + (done.u0 == 0 ? 1 : 0)) * kPieceFloats;
         constexpr int kParts = kVW * 4;                      // units of one nt
-        auto write_rows = [&](int nt, int m, const float4& x, const float (&peak)[2], const float (&total)[2]) {
+        // what the prefix left of rows 2 tq and 2 tq + 1 of each 8 in the parts that this warp ends: asked for
+        // before the merge, whose steps would wait for it one after the other
+        struct Prior {
+            float2 stats, value;
+        };
+        constexpr int kMine = kSide == kJoined ? (kNT * kParts + kWarps - 1) / kWarps : 1;
+        Prior prior[kMine][2] = {};
+        auto ask = [&](int nt, int m, Prior (&p)[2]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nt * 8 + 2 * tq + e;
+                const int64_t at = static_cast<int64_t>(done.w.begin + r / group) * a.q_heads + done.h * group + r % group;
+                if (r >= rows || !HC_IN_RANGE(at, 1, static_cast<size_t>(a.tokens) * a.q_heads, status)) continue;
+                p[e].stats = partial_stats(a, kD)[at];
+                p[e].value = *reinterpret_cast<const float2*>(a.partial + at * kD + g * (kD / 8) + 2 * m);
+            }
+        };
+        if (kSide == kJoined && whole) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int turn = i * kWarps + warp;
+                if (turn < kNT * kParts) ask(turn / kParts, turn % kParts, prior[i]);
+            }
+        }
+        auto write_rows = [&](int nt, int m, const float4& x, const float (&peak)[2], const float (&total)[2], const Prior (&p)[2]) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = nt * 8 + 2 * tq + e;
@@ -710,10 +734,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 float lse = total[e] == 0.f ? -CUDART_INF_F : (peak[e] + log2f(total[e])) * kLn2;
                 float2 y = make_float2(0.f, 0.f);
                 if constexpr (kSide == kJoined) {
-                    const Join j = join_parts_of_row(peak[e], total[e], partial_stats(a, kD)[at]);
-                    const float2 prefix = *reinterpret_cast<const float2*>(a.partial + at * kD + d);
+                    const Join j = join_parts_of_row(peak[e], total[e], p[e].stats);
                     inv = j.by_own, lse = j.lse;
-                    y = make_float2(j.by_prefix * prefix.x, j.by_prefix * prefix.y);
+                    y = make_float2(j.by_prefix * p[e].value.x, j.by_prefix * p[e].value.y);
                 }
                 // (with a prefix's part: one more fma; without, the product alone)
                 auto scaled = [&](float v, float more) { return kSide == kJoined ? fmaf(v, inv, more) : v * inv; };
@@ -730,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
             }
             if (whole) {
-                write_rows(nt, m, x, peak, total);
+                write_rows(nt, m, x, peak, total, prior[kMine > 1 ? (nt * kParts + m) / kWarps : 0]);
             } else {
                 __stcg(reinterpret_cast<float4*>(piece) + (nt * kParts + m) * 32 + lane, x);
                 if (m == 0 && g == 0) {
@@ -821,7 +844,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                         x.x = x.x * fx[0] + y.x * fy[0], x.z = x.z * fx[0] + y.z * fy[0];
                         x.y = x.y * fx[1] + y.y * fy[1], x.w = x.w * fx[1] + y.w * fy[1];
                     }
-                    write_rows(nt, m, x, peak, sums_all);
+                    Prior p[2] = {};
+                    if (kSide == kJoined) ask(nt, m, p);
+                    write_rows(nt, m, x, peak, sums_all, p);
                 }
             }
         }

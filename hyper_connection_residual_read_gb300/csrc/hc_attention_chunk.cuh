@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -794,6 +795,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll 1
                 for (int c = 0; c < kD / 32; ++c) {
+                    // (the prefix's part comes while the sums do)
+                    float4 prior[kSide == kJoined ? 8 : 1];
+                    if constexpr (kSide == kJoined) {
+                        if (here && whole)
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) prior[n] = reinterpret_cast<const float4*>(a.partial + at * kD + c * 32)[n];
+                    }
                     uint32_t v[32];
                     tmem_load32(o_mem + c * 32, v);
                     tmem_wait_load();
@@ -805,10 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (here && whole) {
                         if constexpr (kSide == kJoined) {
-                            const float4* prefix = reinterpret_cast<const float4*>(a.partial + at * kD + c * 32);
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
-                                const float4 y = prefix[n];
+                                const float4 y = prior[n];
                                 o[4 * n] = fmaf(o[4 * n], inv, y.x * by_prefix), o[4 * n + 1] = fmaf(o[4 * n + 1], inv, y.y * by_prefix);
                                 o[4 * n + 2] = fmaf(o[4 * n + 2], inv, y.z * by_prefix), o[4 * n + 3] = fmaf(o[4 * n + 3], inv, y.w * by_prefix);
                             }
@@ -838,7 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Both together to the next piece: the exchange is read; and a warpgroup without rows
             // must not run ahead, since a wait tells only whether a phase of its parity is over.
             if (alone) asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (!whole && writes) {
+            // (pieces of a prefix stay in scratch: a kernel of its own joins them, since they are many: 64
+            // requests behind 16384 tokens took 73 us where the last CTA of each head joined them)
+            if (kSide != kPrefix && !whole && writes) {
                 // each row tile is joined by the last CTA that has part of it
                 const int64_t n = run.ctas;
                 const int c0 = static_cast<int>(((k.base + kPieceCost + 1) * n - 1) / run.total);
@@ -864,13 +873,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         joined[wg][row] = make_float2(top, all == 0.f ? 0.f : 1.f / all);
                         float lse = all == 0.f ? -CUDART_INF_F : (top + log2f(all)) * kLn2;
-                        if constexpr (kSide == kPrefix) partial_stats(a, kD)[at] = make_float2(top, all);
                         if constexpr (kSide == kJoined) {
                             const Join j = join_parts_of_row(top, all, partial_stats(a, kD)[at]);
                             joined[wg][row].y = j.by_own, lse = j.lse;
                             by_prefix[wg][row] = j.by_prefix;
                         }
-                        if (kSide != kPrefix && a.lse) a.lse[at] = lse;
+                        if (a.lse) a.lse[at] = lse;
                     }
                     asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
                     // Four dimensions of each half or quarter of a row a thread, of kAhead parts at
@@ -918,10 +926,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < kOf; ++x) {
                             const int64_t put = to + (x * kQuads + q) * 4;
                             float4 y = make_float4(o[x].x * join.y, o[x].y * join.y, o[x].z * join.y, o[x].w * join.y);
-                            if constexpr (kSide == kPrefix) {
-                                *reinterpret_cast<float4*>(a.partial + put) = y;
-                                continue;
-                            }
                             if constexpr (kSide == kJoined) {
                                 const float4 prefix = *reinterpret_cast<const float4*>(a.partial + put);
                                 const float by = by_prefix[wg][r];
@@ -1163,6 +1167,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Joins the pieces of a prefix's row tiles that several CTAs share: a CTA takes 8 rows, a thread four dimensions
+// of one of them, of all pieces. The rows of a request and head are numbered through, 8 to a number. `ctas` and
+// `step` are the chunk kernel's.
+constexpr int kJoinRows = 8;
+template <int kD>
+__global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const AttentionArgs a, const float* scratch, int ctas, int step, int* status) {
+    begin_early();
+    extern __shared__ float2 stats[];                          // [pieces][kJoinRows]
+    __shared__ Window window;
+    __shared__ int64_t base, total;                            // slots before the row tile, and all
+    __shared__ int head, row0;
+    __shared__ float2 joined[kJoinRows];                       // maximum, 1 / sum
+    const int tid = threadIdx.x, lane = tid & 31, group = a.q_heads / a.c.kv_heads;
+    if (tid < 32) {
+        // the request and head of this CTA's number, a request a lane
+        if (lane == 0) row0 = -1;
+        __syncwarp();
+        int64_t numbers = 0, slots = 0;
+        for (int b0 = 0; b0 < a.requests; b0 += 32) {
+            int64_t mine = 0, mine_slots = 0;
+            Window w = {};
+            if (b0 + lane < a.requests) {
+                w = load_window<kPrefix>(a, b0 + lane, nullptr);
+                mine = static_cast<int64_t>((w.rows * group + kJoinRows - 1) / kJoinRows) * a.c.kv_heads;
+                mine_slots = head_slots<kPrefix>(a, w, group, step) * a.c.kv_heads;
+            }
+            int64_t upto = mine, slots_upto = mine_slots;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t x = __shfl_up_sync(~0u, upto, d), y = __shfl_up_sync(~0u, slots_upto, d);
+                if (lane >= d) upto += x, slots_upto += y;
+            }
+            const int64_t at = static_cast<int64_t>(blockIdx.x) - (numbers + upto - mine);
+            if (at >= 0 && at < mine) {
+                const int64_t per = mine / a.c.kv_heads;
+                head = static_cast<int>(at / per), row0 = static_cast<int>(at % per) * kJoinRows;
+                window = w;
+                // the row tiles of a prefix have its key tiles each
+                base = slots + slots_upto - mine_slots + head * (mine_slots / a.c.kv_heads) +
+                       static_cast<int64_t>(row0 / step) * (key_tiles<kPrefix>(a, w, group, step, 0) + kPieceCost);
+            }
+            numbers += __shfl_sync(~0u, upto, 31);
+            slots += __shfl_sync(~0u, slots_upto, 31);
+        }
+        if (lane == 0) total = slots;
+    }
+    __syncthreads();
+    if (row0 < 0) return;
+    const int tiles = key_tiles<kPrefix>(a, window, group, step, 0);
+    const int64_t n = min(static_cast<int64_t>(ctas), total);
+    const int c0 = static_cast<int>(((base + kPieceCost + 1) * n - 1) / total), c1 = static_cast<int>(((base + kPieceCost + tiles) * n - 1) / total);
+    if (c0 == c1 || !HC_IN_RANGE(c0, c1 - c0 + 1, ctas, status)) return;      // one piece: its CTA wrote it
+    auto piece = [&](int c) { return scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats; };
+    const int in_tile = row0 % step, rows = min(window.rows * group - row0, kJoinRows);
+    const int r = tid % kJoinRows, quad = tid / kJoinRows;
+    for (int i = quad; i <= c1 - c0; i += kD / 4)
+        stats[i * kJoinRows + r] = r < rows ? __ldcg(reinterpret_cast<const float2*>(piece(c0 + i) + 256 * kD) + in_tile + r) : make_float2(-CUDART_INF_F, 0.f);
+    __syncthreads();
+    const int of = row0 + r;
+    const int64_t at = static_cast<int64_t>(window.begin + of / group) * a.q_heads + head * group + of % group;
+    const bool here = r < rows && HC_IN_RANGE(at, 1, static_cast<size_t>(a.tokens) * a.q_heads, status);
+    if (tid < kJoinRows) {
+        float top = -CUDART_INF_F, all = 0.f;
+        for (int i = 0; i <= c1 - c0; ++i) top = fmaxf(top, stats[i * kJoinRows + r].x);
+        for (int i = 0; i <= c1 - c0; ++i) {
+            const float2 st = stats[i * kJoinRows + r];
+            if (st.x != -CUDART_INF_F) all += st.y * exp2_fast(st.x - top);
+        }
+        joined[r] = make_float2(top, all == 0.f ? 0.f : 1.f / all);
+        if (here) partial_stats(a, kD)[at] = make_float2(top, all);
+    }
+    __syncthreads();
+    if (!here) return;
+    const float2 join = joined[r];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i <= c1 - c0; ++i) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(piece(c0 + i)) + quad * 256 + in_tile + r);
+        const float peak = stats[i * kJoinRows + r].x;
+        if (peak == -CUDART_INF_F) continue;
+        const float by = exp2_fast(peak - join.x);
+        o.x = fmaf(y.x, by, o.x), o.y = fmaf(y.y, by, o.y), o.z = fmaf(y.z, by, o.z), o.w = fmaf(y.w, by, o.w);
+    }
+    *reinterpret_cast<float4*>(a.partial + at * kD + quad * 4) = make_float4(o.x * join.y, o.y * join.y, o.z * join.y, o.w * join.y);
+}
+
+template <int kD>
+cudaError_t launch_join(const Ctx& ctx, const AttentionArgs& a, int step, cudaStream_t st) {
+    // as many numbers as there can be
+    const int64_t rows = static_cast<int64_t>(a.tokens) * (a.q_heads / a.c.kv_heads);
+    const int64_t most = (rows / kJoinRows + a.requests) * a.c.kv_heads;
+    if (most > INT_MAX) return cudaErrorInvalidConfiguration;
+    return launch_early(join_kernel<kD>, dim3(static_cast<unsigned>(most)), kJoinRows * kD / 4, sizeof(float2) * kJoinRows * ctx.sm_count, st,
+                        a, ctx.attn_pieces, ctx.sm_count, step, ctx.s.status);
+}
+
 template <int kD, int kDtype, bool kSame, Side kSide>
 cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
     return launch_early(chunk_kernel<kD, kDtype, kSame, kSide>, dim3(ctx.sm_count), kThreads, Smem<kD>::kBytes, st, a, ctx.attn_pieces,
@@ -1171,8 +1271,10 @@ cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st
 
 template <int kD, int kDtype, Side kSide>
 cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
-    return static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= kTile ? launch_chunk<kD, kDtype, true, kSide>(ctx, a, st)
-                                                                                  : launch_chunk<kD, kDtype, false, kSide>(ctx, a, st);
+    const bool same = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= kTile;
+    const cudaError_t e = same ? launch_chunk<kD, kDtype, true, kSide>(ctx, a, st) : launch_chunk<kD, kDtype, false, kSide>(ctx, a, st);
+    if constexpr (kSide == kPrefix) return e != cudaSuccess ? e : launch_join<kD>(ctx, a, same ? kTile : 2 * kTile, st);
+    return e;
 }
 
 // A kernel's shared memory; and that it was compiled with the registers which its warps share out
