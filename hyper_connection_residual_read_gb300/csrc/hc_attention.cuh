@@ -96,7 +96,7 @@ constexpr int kPieceFloats = kPieceRows * (128 + 2);
 // units, and before them kPieceCost slots that stand for the work of starting and merging.
 struct Walk {
     int b, h, u0, u1, units;     // the units [u0, u1) of (b, h), of `units`
-    int64_t left, base;          // slots left, and the number of (b, h)'s first slot
+    int64_t left, base;          // slots left, and the number of (b, h)'s first slot; or kWhole and (b, h)'s number
     int cost;                    // slots before its units
     Window w;
 };
@@ -118,9 +118,31 @@ __device__ __forceinline__ bool walk_piece(Walk& k, int from) {
     return k.u1 > k.u0;
 }
 
+// Where the requests behind a prefix are many and short, a CTA takes each gridDim.x-th of all (request, head)s
+// as a whole instead of a run: the joins of cut ones cost more than they even out (64 requests of up to 1K tokens
+// of their own, 8 heads: @@).
+constexpr int64_t kWhole = -1;
+constexpr int kWholeUnits = 8;                   // of the longest request
+constexpr int kWholeHeads = 128;                 // fewer leave most SMs without one
+
+__device__ __forceinline__ bool walk_whole(const AttentionArgs& a, Walk& k, int64_t number) {
+    const int64_t all = static_cast<int64_t>(a.requests) * a.c.kv_heads;
+    for (; number < all; number += gridDim.x) {
+        k.b = static_cast<int>(number / a.c.kv_heads), k.h = static_cast<int>(number % a.c.kv_heads);
+        k.w = load_window<kJoined>(a, k.b, nullptr);
+        k.units = window_units(k.w);
+        if (k.units == 0) continue;
+        k.u0 = 0, k.u1 = k.units;
+        k.left = kWhole, k.base = number;
+        return true;
+    }
+    return false;
+}
+
 // To the next piece; false at the end of the run.
 template <Side kSide>
 __device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
+    if (kSide == kJoined && k.left == kWhole) return walk_whole(a, k, k.base + gridDim.x);
     if (k.left == 0) return false;
     k.base += k.units + k.cost;
     if (++k.h == a.c.kv_heads) {
@@ -139,6 +161,7 @@ struct Run {
     int b;
     int64_t offset, begin, end, total, ctas;
     int cost;
+    bool whole;
     Window w;                    // of request b
 };
 
@@ -157,6 +180,8 @@ __device__ __forceinline__ void cut_run(Run& run, int64_t total) {
 template <Side kSide>
 __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int* status) {
     const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t heads = static_cast<int64_t>(a.requests) * a.c.kv_heads;
+    const bool many = kSide == kJoined && heads >= kWholeHeads && 2 * heads >= gridDim.x;
     if (a.requests <= 32) {
         Window w = {};
         if (lane < a.requests) w = load_window<kSide>(a, lane, blockIdx.x == 0 ? status : nullptr);
@@ -173,6 +198,7 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
         }
         Run run;
         run.cost = cost;
+        run.whole = many && !__any_sync(~0u, lane < a.requests && window_units(w) > kWholeUnits);
         cut_run(run, __shfl_sync(~0u, upto, 31));
         run.b = min(__popc(__ballot_sync(~0u, upto <= run.begin)), 31);
         run.offset = run.begin - __shfl_sync(~0u, upto - mine, run.b);
@@ -186,8 +212,13 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
     const int per = (a.requests + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += window_slots(a, load_window<kSide>(a, b, blockIdx.x == 0 ? status : nullptr), kPieceCost);
+    bool long_one = false;
+    for (int b = b0; b < b1; ++b) {
+        const Window w = load_window<kSide>(a, b, blockIdx.x == 0 ? status : nullptr);
+        mine += window_slots(a, w, kPieceCost);
+        if (kSide == kJoined) long_one = long_one || window_units(w) > kWholeUnits;
+    }
+    const bool whole = kSide == kJoined && !__syncthreads_or(long_one) && many;
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -203,6 +234,7 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
     }
     Run run;
     run.cost = kPieceCost;
+    run.whole = whole;
     cut_run(run, total);
     if (run.begin < run.end && run.begin < upto && run.begin >= upto - mine) {
         int64_t at = upto - mine;
@@ -226,6 +258,7 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
 // The first piece of the run; false if it has none.
 template <Side kSide>
 __device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, Walk& k) {
+    if (kSide == kJoined && run.whole) return walk_whole(a, k, blockIdx.x);
     if (run.begin >= run.end) return false;
     k.b = run.b;
     k.w = run.w;

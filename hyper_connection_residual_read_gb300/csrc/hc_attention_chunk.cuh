@@ -795,13 +795,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll 1
                 for (int c = 0; c < kD / 32; ++c) {
-                    // (the prefix's part comes while the sums do)
-                    float4 prior[kSide == kJoined ? 8 : 1];
-                    if constexpr (kSide == kJoined) {
-                        if (here && whole)
-#pragma unroll
-                            for (int n = 0; n < 8; ++n) prior[n] = reinterpret_cast<const float4*>(a.partial + at * kD + c * 32)[n];
-                    }
                     uint32_t v[32];
                     tmem_load32(o_mem + c * 32, v);
                     tmem_wait_load();
@@ -813,9 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (here && whole) {
                         if constexpr (kSide == kJoined) {
+                            const float4* prefix = reinterpret_cast<const float4*>(a.partial + at * kD + c * 32);
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
-                                const float4 y = prior[n];
+                                const float4 y = prefix[n];
                                 o[4 * n] = fmaf(o[4 * n], inv, y.x * by_prefix), o[4 * n + 1] = fmaf(o[4 * n + 1], inv, y.y * by_prefix);
                                 o[4 * n + 2] = fmaf(o[4 * n + 2], inv, y.z * by_prefix), o[4 * n + 3] = fmaf(o[4 * n + 3], inv, y.w * by_prefix);
                             }
