@@ -56,7 +56,12 @@
 namespace hc {
 namespace {
 
-constexpr int kWarps = 8;
+#ifndef HC_WINDOW_WARPS
+#define HC_WINDOW_WARPS 8
+#endif
+constexpr int kWarps = HC_WINDOW_WARPS;          // of a CTA; fewer where the requests behind a prefix are short (hc_attention_short.cu)
+constexpr bool kShort = kWarps < 8;              // and then each (request, head) is one CTA's
+constexpr int kCtasPerSm = kAttnCtasPerSm * 8 / kWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                        // tokens of a warp's step
 constexpr int kUnit = kWarps * kStep;            // tokens of a unit
@@ -125,11 +130,11 @@ constexpr int64_t kWhole = -1;
 constexpr int kWholeUnits = 8;                   // of the longest request
 constexpr int kWholeHeads = 128;                 // fewer leave most SMs without one
 
-__device__ __forceinline__ bool walk_whole(const AttentionArgs& a, Walk& k, int64_t number) {
+__device__ __forceinline__ bool walk_whole(const AttentionArgs& a, Walk& k, int64_t number, int* status) {
     const int64_t all = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     for (; number < all; number += gridDim.x) {
         k.b = static_cast<int>(number / a.c.kv_heads), k.h = static_cast<int>(number % a.c.kv_heads);
-        k.w = load_window<kJoined>(a, k.b, nullptr);
+        k.w = load_window<kJoined>(a, k.b, status);
         k.units = window_units(k.w);
         if (k.units == 0) continue;
         k.u0 = 0, k.u1 = k.units;
@@ -141,8 +146,8 @@ __device__ __forceinline__ bool walk_whole(const AttentionArgs& a, Walk& k, int6
 
 // To the next piece; false at the end of the run.
 template <Side kSide>
-__device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k) {
-    if (kSide == kJoined && k.left == kWhole) return walk_whole(a, k, k.base + gridDim.x);
+__device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k, int* status) {
+    if (kSide == kJoined && k.left == kWhole) return walk_whole(a, k, k.base + gridDim.x, status);
     if (k.left == 0) return false;
     k.base += k.units + k.cost;
     if (++k.h == a.c.kv_heads) {
@@ -180,6 +185,11 @@ __device__ __forceinline__ void cut_run(Run& run, int64_t total) {
 template <Side kSide>
 __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int* status) {
     const int tid = threadIdx.x, lane = tid & 31;
+    if (kShort) {                                // (what does not fit is reported as it is loaded)
+        Run run = {};
+        run.whole = true;
+        return run;
+    }
     const int64_t heads = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     const bool many = kSide == kJoined && heads >= kWholeHeads && 2 * heads >= gridDim.x;
     if (a.requests <= 32) {
@@ -257,8 +267,8 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
 
 // The first piece of the run; false if it has none.
 template <Side kSide>
-__device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, Walk& k) {
-    if (kSide == kJoined && run.whole) return walk_whole(a, k, blockIdx.x);
+__device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, Walk& k, int* status) {
+    if (kSide == kJoined && run.whole) return walk_whole(a, k, blockIdx.x, status);
     if (run.begin >= run.end) return false;
     k.b = run.b;
     k.w = run.w;
@@ -269,7 +279,7 @@ __device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& ru
     const int from = static_cast<int>(run.offset - static_cast<int64_t>(k.h) * slots);
     k.left = run.end - run.begin;
     k.base = run.begin - from;
-    return walk_piece(k, from) || walk_next<kSide>(a, k);
+    return walk_piece(k, from) || walk_next<kSide>(a, k, status);
 }
 
 // D += A (16 x 16, row-major fragments) B (16 x 8), fp16 with fp32 sums.
@@ -297,7 +307,7 @@ __device__ __forceinline__ uint32_t permute(uint32_t x, uint32_t y, uint32_t how
 __device__ __forceinline__ int tile_token(int m) { return m ^ ((m >> 1) & 1); }
 
 template <int kD, int kDtype, int kNT, Side kSide>
-__global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm / 2)
     window_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
     constexpr int kW = kD / 32;              // words of a key row that a lane loads
     constexpr int kVW = kD / 64;             // words of a value row that a lane loads
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     };
     {
         Walk first;
-        if (!walk_start<kSide>(a, run, first)) return;
+        if (!walk_start<kSide>(a, run, first, kShort ? status : nullptr)) return;
         keep(first);
     }
 
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
     // a piece's first steps, on their way before the piece before it is merged
     auto begin = [&]() {
         u1 = k.u1, kv = k.w.kv;
-        pages = a.table + static_cast<int64_t>(k.b) * a.width;
+        pages = a.table + static_cast<int64_t>(kSide == kPrefix ? k.b / a.subs : k.b) * a.width;
         head_codes = a.c.codes + l16 * 16 + static_cast<int64_t>(k.h) * a.c.block_size * (kD / 2);
         head_scales = reinterpret_cast<const unsigned char*>(a.c.scales) + static_cast<int64_t>((l16 >> 2) * to_values + k.h * a.c.block_size) * 4 + (l16 & 3) * 16;
         const int u0 = k.u0;
@@ -690,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
         const Walk done = k;
         {
             Walk next = done;
-            more = walk_next<kSide>(a, next);
+            more = walk_next<kSide>(a, next, kShort ? status : nullptr);
             if (more) {
                 keep(next);
                 begin();
@@ -778,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 if (a.lse && d == 0) a.lse[at] = lse;
             }
         };
-        auto finish = [&](int nt, int m, const float4* buffer, const float (&peak)[2], const float (&total)[2]) {
+        auto finish = [&](int nt, int m, const float4* buffer, const float (&peak)[2], const float (&total)[2], const Prior (&p)[2]) {
             float4 x = buffer[lane];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) {
@@ -786,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
             }
             if (whole) {
-                write_rows(nt, m, x, peak, total, prior[kMine > 1 ? (nt * kParts + m) / kWarps : 0]);
+                write_rows(nt, m, x, peak, total, p);
             } else {
                 __stcg(reinterpret_cast<float4*>(piece) + (nt * kParts + m) * 32 + lane, x);
                 if (m == 0 && g == 0) {
@@ -831,14 +841,22 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 2 : 1)
                 buffer[warp * 32 + lane] = x;
                 if (more) {
                     asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-                    if (warp == turn_m % kWarps) finish(nt, m, buffer, peak, total);
+                    if (warp == turn_m % kWarps) finish(nt, m, buffer, peak, total, prior[kSide == kJoined ? turn_m / kWarps : 0]);
                 }
             }
             if (!more) {
                 asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+                if constexpr (kSide == kJoined) {            // (unrolled: what was asked for lies in registers)
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        const int turn = i * kWarps + warp;
+                        if (turn / kParts == nt) finish(nt, turn % kParts, merge + turn * kWarps * 32, peak, total, prior[i]);
+                    }
+                } else {
 #pragma unroll 1
-                for (int m = 0; m < kParts; ++m)
-                    if (warp == (nt * kParts + m) % kWarps) finish(nt, m, merge + (nt * kParts + m) * kWarps * 32, peak, total);
+                    for (int m = 0; m < kParts; ++m)
+                        if (warp == (nt * kParts + m) % kWarps) finish(nt, m, merge + (nt * kParts + m) * kWarps * 32, peak, total, prior[0]);
+                }
             }
         }
         if (!whole) {
@@ -890,8 +908,8 @@ template <int kD, int kDtype, int kNT, Side kSide>
 cudaError_t launch_window(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
     // as many CTAs as are resident at once, and no more than there can be units
     const int64_t most = static_cast<int64_t>(a.requests) * a.c.kv_heads *
-                         ((static_cast<int64_t>(a.width) * a.c.block_size + kUnit - 1) / kUnit);
-    const int64_t resident = static_cast<int64_t>(ctx.sm_count) * (kNT == 1 ? kAttnCtasPerSm : 1);
+                         (kShort ? 1 : (static_cast<int64_t>(a.width) * a.c.block_size + kUnit - 1) / kUnit);
+    const int64_t resident = static_cast<int64_t>(ctx.sm_count) * (kNT == 1 ? kCtasPerSm : kCtasPerSm / 2);
     const int grid = static_cast<int>(most < resident ? most : resident);
     return launch_early(window_kernel<kD, kDtype, kNT, kSide>, dim3(grid), kThreads, Smem<kD, kNT>::kBytes, st, a, ctx.attn_pieces,
                         ctx.attn_arrivals, ctx.s.status);

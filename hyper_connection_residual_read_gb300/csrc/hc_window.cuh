@@ -29,7 +29,7 @@ __device__ __forceinline__ size_t group_count(const hc_kv4_cache& c) {
 __device__ __forceinline__ size_t row_extent(int tokens, int heads, int dim, int64_t token, int64_t head) {
     return static_cast<size_t>(tokens - 1) * token + static_cast<size_t>(heads - 1) * head + dim;
 }
-__device__ __forceinline__ size_t table_extent(const AttentionArgs& a) { return static_cast<size_t>(a.requests) * a.width; }
+__device__ __forceinline__ size_t table_extent(const AttentionArgs& a) { return static_cast<size_t>(a.requests / a.subs) * a.width; }
 
 // The window of one request, with what does not fit its arrays cut off and reported. (That kv
 // fits the request's row of the table is what the kernels' lookups there rely on.)
@@ -49,22 +49,29 @@ template <Side kSide>
 __device__ __forceinline__ Window load_window(const AttentionArgs& a, int b, int* status) {
     Window w = {};
     if (!HC_IN_RANGE(b, 1, a.requests, status)) return w;
-    int at = b, to = b + 1;
+    int at = b, to = b + 1, of = b;
     bool none = false;
     if (kSide == kPrefix) {
-        at = a.groups[b], to = a.groups[b + 1];
+        of = b / a.subs;
+        at = a.groups[of], to = a.groups[of + 1];
         none = at < 0 || to < at || to > a.members;
         if (none) at = to = 0;
     }
-    const int lo = a.cu[at], hi = a.cu[to], kv = a.kv[b];
+    const int lo = a.cu[at], hi = a.cu[to], kv = a.kv[of];
     const int64_t room = static_cast<int64_t>(a.width) * a.c.block_size;
     const bool bad = none || lo < 0 || hi < lo || hi > a.tokens;
     w.begin = bad ? 0 : lo;
     w.n = bad ? 0 : hi - lo;
+    const bool more = w.n > (kSide == kPrefix ? a.shared : a.max_new);
+    if (kSide == kPrefix) {                    // this share of the group's tokens
+        const int skip = static_cast<int>(min(static_cast<int64_t>(b % a.subs) * a.max_new, static_cast<int64_t>(w.n)));
+        w.begin += skip, w.n -= skip;
+        if (a.subs > 1) w.n = min(w.n, a.max_new);
+    }
     w.rows = min(w.n, a.max_new);
     w.kv = kv < 0 ? 0 : static_cast<int>(kv > room ? room : kv);
     w.first = kSide == kPrefix ? w.kv : w.kv - w.n;    // every row sees all of a prefix
-    if ((bad || w.n > a.max_new || kv > room) && status) atomicOr(status, kStatusBounds);
+    if ((bad || more || kv > room) && status) atomicOr(status, kStatusBounds);
     return w;
 }
 
@@ -224,5 +231,8 @@ cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int d
 template <Side kSide>
 cudaError_t attention_chunk_setup();
 size_t attention_chunk_scratch_floats(int sm_count);
+// Own parts behind a prefix, of short requests with few rows (hc_attention_short.cu).
+cudaError_t launch_attention_short(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+cudaError_t attention_short_setup();
 
 }  // namespace hc

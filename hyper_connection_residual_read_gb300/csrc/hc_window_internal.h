@@ -51,10 +51,11 @@ struct AttentionArgs {
     const uint64_t* mask;
     void* out;
     float* lse;
-    // behind a shared prefix (hc_serve.h): the prefixes' part, whose `requests` are the groups, goes
-    // to `partial`, from where the own part takes it
+    // behind a shared prefix (hc_serve.h): the prefixes' part, whose `requests` are the groups (or `subs`
+    // shares of max_new tokens of each), goes to `partial`, from where the own part takes it
     const int32_t* groups;                      // first request of each group
     int members;                                // requests of all groups
+    int subs, shared;                           // tokens that a group may have
     float* partial;                             // [tokens][q_heads][head_dim], then (maximum, sum) of each row
 };
 cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);

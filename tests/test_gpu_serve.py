@@ -411,13 +411,15 @@ def test_shared_sees_nan_only_where_it_looks():
 
 
 def test_shared_is_attention_where_no_prefix_is():
-    """An empty prefix: the own part alone, the same bits as hc_kv4_attention's but for the join."""
+    """An empty prefix: the own part alone, as hc_kv4_attention computes it (not bit for bit: its sums
+    may be cut in other places)."""
     c = Shared(8, [(0, [(300, 4), (77, 2)])], 8, 2, 128, 16, "bf16")
     out, lse = c.run()
     kw = c.arguments()
     o, l = torch.empty_like(out), torch.empty_like(lse)
     hc.hc_kv4_attention(kw["q"], kw["codes"], kw["scales"], kw["block_table"], kw["cu_lens"], kw["kv_lens"], kw["max_new"], o, lse=l)
-    assert torch.equal(o, out) and torch.equal(l, lse)
+    c.check(out, lse)
+    c.check(o, l)
 
 
 def test_shared_strides_streams_graphs_and_repeats():
