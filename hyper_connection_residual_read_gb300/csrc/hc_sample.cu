@@ -31,6 +31,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hc_serve_internal.h"
 #include "hc_window.cuh"
 
@@ -85,9 +87,9 @@ __constant__ uint64_t kPowers[kSteps] = {
 
 // Logits in shared memory.
 template <int kDtype>
-__device__ __forceinline__ float logit(const unsigned char* p, int i) {
-    if (kDtype == HC_DTYPE_FP32) return reinterpret_cast<const float*>(p)[i];
-    const uint16_t u = reinterpret_cast<const uint16_t*>(p)[i];
+__device__ __forceinline__ float logit(const void* p, int i) {
+    if (kDtype == HC_DTYPE_FP32) return static_cast<const float*>(p)[i];
+    const uint16_t u = static_cast<const uint16_t*>(p)[i];
     return kDtype == HC_DTYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
 }
 
@@ -195,15 +197,14 @@ __device__ __forceinline__ T warp_scan(T x, int lane) {
     return x;
 }
 
+template <int kDtype>
 struct Shared {
     uint64_t powers[kSteps];
-    // of a step's bins, two steps' in turn: their logits, and their weights as sums of each 16 bits of them
-    // (shared memory adds 32 bits at a time by itself: three such sums take 8 cycles a warp, one of 64
-    // bits 50 to 570)
-    unsigned count[2][kBins], mass[2][3][kBins];
+    // of a step's bins: their logits, and their weights as sums of each 16 bits of them (shared memory adds
+    // 32 bits at a time by itself: three such sums take 8 cycles a warp, one of 64 bits 50 to 570)
+    unsigned count[kBins], mass[3][kBins];
     // what a CTA tells the others
     float top;
-    int first;
     uint64_t total;
     uint64_t listed_mass;
     unsigned listed;
@@ -214,16 +215,15 @@ struct Shared {
     unsigned warp_count[kWarps];
     uint64_t before_mass, in_mass;           // of the bin with the border
     unsigned before, in;
-    int bin;
     int warp_first[kWarps];
-    // a short list: values and ids
-    float value[kShort];
+    // a short list: ids and values; before it, the bins of the estimate lie in the first
     int id[kShort];
+    typename std::conditional<kDtype == HC_DTYPE_FP32, float, uint16_t>::type value[kShort];
 };
 
 // A value of each CTA, one a lane (0 for lanes past them), brought at once.
-template <typename T, typename Get>
-__device__ __forceinline__ T of_ctas(cg::cluster_group& cluster, int ctas, int lane, Shared& s, Get get) {
+template <typename T, int kDtype, typename Get>
+__device__ __forceinline__ T of_ctas(cg::cluster_group& cluster, int ctas, int lane, Shared<kDtype>& s, Get get) {
     return lane < ctas ? get(*cluster.map_shared_rank(&s, lane)) : T(0);
 }
 
@@ -281,7 +281,8 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&y)[kDtype == HC_D
 template <int kDtype>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a, int ctas, int segment_bytes, int list_room, int* status) {
     constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
-    __shared__ Shared s;
+    using S = Shared<kDtype>;
+    __shared__ S s;
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char* segment = smem;
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + segment_bytes);
@@ -300,52 +301,35 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), v1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
     const int id0 = v0 * kN - shift;             // the id of local index 0
     uint4* const vec = reinterpret_cast<uint4*>(segment);
-    float most;
+    // whole vectors by asynchronous copies, all on their way at once; the ends of the row by one thread each
+    const int n_vec = v1 - v0, w0 = id0 < 0 ? 1 : 0, w1 = id0 + n_vec * kN > a.vocab ? n_vec - 1 : n_vec;
     {
         const uint4* from = reinterpret_cast<const uint4*>(x - shift * kItem) + v0;
-        Most<kDtype> largest;
-        // whole vectors, and the ends of the row by one thread each
-        const int n = v1 - v0, w0 = id0 < 0 ? 1 : 0, w1 = id0 + n * kN > a.vocab ? n - 1 : n;
-        int i = w0 + tid;
-        for (; i + 3 * kThreads < w1; i += 4 * kThreads) {
-            uint4 v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = ldg_stream_v4(from + i + e * kThreads);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vec[i + e * kThreads] = v[e], largest.take(v[e]);
-        }
-        for (; i < w1; i += kThreads) {
-            const uint4 v = ldg_stream_v4(from + i);
-            vec[i] = v;
-            largest.take(v);
-        }
-        if ((tid == 0 && w0 > 0) || (tid == 32 && w1 < n && n > w0)) {
-            const int at = tid == 0 ? 0 : n - 1;
-            uint4 v;
-            for (int e = 0; e < kN; ++e) {
-                const int id = id0 + at * kN + e;
-                const bool in = id >= 0 && id < a.vocab;
-                if (kItem == 4) {
-                    reinterpret_cast<uint32_t*>(&vec[at])[e] = in ? reinterpret_cast<const uint32_t*>(x)[id] : 0xFF800000u;
-                } else {
-                    reinterpret_cast<uint16_t*>(&vec[at])[e] = in ? reinterpret_cast<const uint16_t*>(x)[id] : static_cast<uint16_t>(kDtype == HC_DTYPE_BF16 ? 0xFF80u : 0xFC00u);
-                }
-            }
-            v = vec[at];
-            largest.take(v);
-        }
-        most = largest.get();
+        for (int i = w0 + tid; i < w1; i += kThreads)
+            if (HC_IN_RANGE(id0 + i * kN, kN, a.vocab, status)) copy16(tc::smem_u32(vec + i), from + i);
+        copy_commit();
     }
     const float u = a.uniform[row], t = a.temperature ? a.temperature[row] : 1.f;
     const float p = a.top_p ? a.top_p[row] : 1.f, least = a.min_p ? a.min_p[row] : 0.f;
     const int k = a.top_k ? a.top_k[row] : 0;
     bool bad = !(u == u && p == p && least == least) || !(fabsf(t) <= kTop);
     for (int i = tid; i < kSteps; i += kThreads) s.powers[i] = kPowers[i];
-    for (int i = tid; i < kBins; i += kThreads) {
-        s.count[0][i] = s.count[1][i] = 0;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) s.mass[0][e][i] = s.mass[1][e][i] = 0;
+    s.count[tid] = s.mass[0][tid] = s.mass[1][tid] = s.mass[2][tid] = 0, s.id[tid] = 0;
+    Most<kDtype> largest;
+    const int end = tid == 0 && w0 > 0 ? 0 : tid == 32 && w1 < n_vec && n_vec > w0 ? n_vec - 1 : -1;
+    if (end >= 0) {
+        for (int e = 0; e < kN; ++e) {
+            const int id = id0 + end * kN + e;
+            const bool in = id >= 0 && id < a.vocab;
+            if (kItem == 4) reinterpret_cast<uint32_t*>(vec + end)[e] = in ? reinterpret_cast<const uint32_t*>(x)[id] : 0xFF800000u;
+            else reinterpret_cast<uint16_t*>(vec + end)[e] = in ? reinterpret_cast<const uint16_t*>(x)[id] : static_cast<uint16_t>(kDtype == HC_DTYPE_BF16 ? 0xFF80u : 0xFC00u);
+        }
+        largest.take(vec[end]);
     }
+    copy_wait<0>();
+    for (int i = w0 + tid; i < w1; i += kThreads) largest.take(vec[i]);
+    const float my_most = largest.get();         // of this thread's logits
+    float most = my_most;
 
     // ---- the largest logit
 #pragma unroll
@@ -357,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         s.top = most;
     }
     cluster.sync();
-    float top = cluster.map_shared_rank(&s, lane < ctas ? lane : 0)->top;
+    const float tops = cluster.map_shared_rank(&s, lane < ctas ? lane : 0)->top;
+    float top = tops;
 #pragma unroll
     for (int d = kMaxCtas / 2; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
     top = __shfl_sync(~0u, top, 0);
@@ -366,7 +351,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const int all = (v1 - v0) * kN, per = ((v1 - v0 + kWarps - 1) / kWarps) * kN;
     const int part_begin = min(warp * per, all), part_end = min(part_begin + per, all);
     if (bad || t < 5.421010862427522e-20f) {
-        // nothing, or the first of the largest
+        // nothing, or the first of the largest: the first CTA that has it finds it
+        const unsigned with = __ballot_sync(~0u, lane < ctas && tops == top);
+        cluster.sync();                          // all have read what the others told
+        if (bad ? rank != 0 : rank != __ffs(with) - 1) return;
         int first = 0x7FFFFFFF;
         if (!bad)
             for (int i = part_begin / kN + lane; i < part_end / kN; i += 32) {
@@ -381,15 +369,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         __syncthreads();
         if (tid == 0) {
             for (int w = 1; w < kWarps; ++w) first = min(first, s.warp_first[w]);
-            s.first = first;
-        }
-        cluster.sync();
-        if (rank == 0 && tid == 0) {
-            for (int r = 1; r < ctas; ++r) first = min(first, cluster.map_shared_rank(&s, r)->first);
             a.ids[row] = bad ? -1 : first;
             a.logprob[row] = bad ? CUDART_NAN_F : 0.f;
         }
-        cluster.sync();
         return;
     }
     const Heat heat = heat_of(t, top);
@@ -413,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     int n = part_end - part_begin, begin = part_begin;
     uint16_t* mine = list + warp * list_room;
     auto value_at = [&](int i) {
-        if (mode == kAlone) return s.value[begin + i];
+        if (mode == kAlone) return logit<kDtype>(s.value, begin + i);
         return logit<kDtype>(segment, mode == kListed ? static_cast<int>(mine[i]) : begin + i);
     };
     auto each = [&](auto use) {
@@ -465,13 +447,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         uint64_t total = 0, want = k, mass = 0, upto = 0, estimated = 0;
         unsigned number = 0;
         float bound;
+        const bool by_largest = by_count && k <= kThreads / 2 * ctas;
         if (!few) {
-            // ---- an eighth of the logits, by how far they lie below the largest, in bins of an octave / 5.5
+            // ---- the threads' largest logits (at least as many logits lie above a bound), or an eighth of all, by how
+            // far they lie below the largest, in bins of an octave / 5.5
             const float per_logit = 1.f / width;
-            for (int i = tid; i < all / 8; i += kThreads) {
-                const float z = (top - logit<kDtype>(segment, i * 8 + (i & 7))) * per_logit;
-                if (z < static_cast<float>(kBins)) atomicAdd(&s.count[0][min(static_cast<int>(z), kBins - 1)], 1u);
-            }
+            auto add_depth = [&](float y) {
+                const float z = (top - y) * per_logit;
+                if (z < static_cast<float>(kBins)) atomicAdd(&s.id[min(static_cast<int>(z), kBins - 1)], 1);
+            };
+            if (by_largest) add_depth(my_most);
+            else
+                for (int i = tid; i < all / 8; i += kThreads) add_depth(logit<kDtype>(segment, i * 8 + (i & 7)));
             auto add_up = [&](const float (&y)[4]) {
                 uint64_t w[4];
                 weigh(y, w);
@@ -480,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             if (!by_count) each_of_all(add_up);
             tell(total, 0, &s.total, nullptr);
             cluster.sync();
-            total = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; }));
+            total = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.total; }));
             unsigned theirs[kMaxCtas];
 #pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) theirs[r] = r < ctas ? cluster.map_shared_rank(&s, r < ctas ? r : 0)->count[0][tid] : 0;
+            for (int r = 0; r < kMaxCtas; ++r) theirs[r] = r < ctas ? cluster.map_shared_rank(&s, r < ctas ? r : 0)->id[tid] : 0;
 #pragma unroll
             for (int r = 0; r < kMaxCtas; ++r) number += theirs[r];
             const float share = 8.f * static_cast<float>(number) * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins));
-            mass = by_count ? static_cast<uint64_t>(number) * 8 : static_cast<uint64_t>(share * 1073741824.f);
+            mass = by_count ? static_cast<uint64_t>(number) * (by_largest ? 1 : 8) : static_cast<uint64_t>(share * 1073741824.f);
             upto = warp_scan(mass, lane);
             if (lane == 31) s.warp_mass[warp] = upto;
             __syncthreads();
@@ -502,40 +489,34 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         // an eighth of the logits give an idea), with room for what chance does to the estimate.
         auto bound_of = [&](int attempt) {
             if (few || attempt == 2) return heat.deep;
-            uint64_t most_of = attempt == 0 ? want + want / 4 + 64 : 2 * want + 512;
+            uint64_t most_of = attempt > 0 ? 2 * want + 512 : by_largest ? want : want + want / 4 + 64;
             if (!by_count) {
                 const uint64_t rest = (total - want) >> (kUnitBits - 30), below = attempt == 0 ? rest - rest / 4 : rest / 4;
                 most_of = estimated > below ? estimated - below : 0;
             }
-            __syncthreads();
-            if (tid == 0) s.bin = kBins - 1;
-            __syncthreads();
-            if (estimated_upto >= most_of) atomicMin(&s.bin, tid);
-            __syncthreads();
-            return fmaxf(top - static_cast<float>(s.bin + 1) * width, heat.deep);
+            const int bin = min(__syncthreads_count(estimated_upto < most_of), kBins - 1);
+            return fmaxf(top - static_cast<float>(bin + 1) * width, heat.deep);
         };
 
-        int turn = 1;                            // bins of the step
         // ---- the step's bins summed over the cluster, a bin a thread: its own, those up to it
         unsigned upto_count = 0;
         auto sum_bins = [&]() {
             sync();
             mass = number = 0;
-            auto take = [&](const Shared& o) {
-                number += o.count[turn][tid];
-                if (by_mass) mass += o.mass[turn][0][tid] + (static_cast<uint64_t>(o.mass[turn][1][tid]) << 16) + (static_cast<uint64_t>(o.mass[turn][2][tid]) << 32);
+            auto take = [&](const S& o) {
+                number += o.count[tid];
+                if (by_mass) mass += o.mass[0][tid] + (static_cast<uint64_t>(o.mass[1][tid]) << 16) + (static_cast<uint64_t>(o.mass[2][tid]) << 32);
             };
-            if (ctas == 1) {
+            if (mode == kAlone) {
                 take(s);
             } else {
 #pragma unroll 4
                 for (int r = 0; r < ctas; ++r) take(*cluster.map_shared_rank(&s, r));
+                cluster.sync();                                 // all have read them
             }
-            // the other bins, read by all in the step before, are free for the next
-            turn ^= 1;
-            s.count[turn][tid] = 0;
+            s.count[tid] = 0;
 #pragma unroll
-            for (int e = 0; e < 3; ++e) s.mass[turn][e][tid] = 0;
+            for (int e = 0; e < 3; ++e) s.mass[e][tid] = 0;
             upto = warp_scan(mass, lane), upto_count = warp_scan(number, lane);
             if (lane == 31) s.warp_mass[warp] = upto, s.warp_count[warp] = upto_count;
             __syncthreads();
@@ -546,21 +527,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         uint64_t before_mass, in_mass;
         unsigned before, in;
         auto find_bin = [&](bool count, uint64_t goal) {
+            bin = __syncthreads_count(count ? upto_count < goal : upto < goal);
+            if (bin == tid) s.before_mass = upto - mass, s.in_mass = mass, s.before = upto_count - number, s.in = number;
             __syncthreads();
-            if (tid == 0) s.bin = -1;
-            __syncthreads();
-            const bool here = count ? upto_count >= goal && upto_count - number < goal : upto >= goal && upto - mass < goal;
-            if (here) s.bin = tid, s.before_mass = upto - mass, s.in_mass = mass, s.before = upto_count - number, s.in = number;
-            __syncthreads();
-            bin = s.bin, before_mass = s.before_mass, in_mass = s.in_mass, before = s.before, in = s.in;
-            return bin >= 0;
+            before_mass = s.before_mass, in_mass = s.in_mass, before = s.before, in = s.in;
+            return bin < kBins;
         };
         auto add = [&](int to, uint64_t w) {
-            atomicAdd(&s.count[turn][to], 1u);
+            atomicAdd(&s.count[to], 1u);
             if (!by_mass) return;
-            atomicAdd(&s.mass[turn][0][to], static_cast<unsigned>(w) & 0xFFFFu);
-            atomicAdd(&s.mass[turn][1][to], static_cast<unsigned>(w) >> 16);
-            atomicAdd(&s.mass[turn][2][to], static_cast<unsigned>(w >> 32));
+            atomicAdd(&s.mass[0][to], static_cast<unsigned>(w) & 0xFFFFu);
+            atomicAdd(&s.mass[1][to], static_cast<unsigned>(w) >> 16);
+            atomicAdd(&s.mass[2][to], static_cast<unsigned>(w >> 32));
         };
 
         // the listed logits by value
@@ -611,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             n = fits ? m : part_end - part_begin;
             tell(0, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
             cluster.sync();
-            const unsigned theirs = of_ctas<unsigned>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed; });
+            const unsigned theirs = of_ctas<unsigned>(cluster, ctas, lane, s, [](const S& o) { return o.listed; });
             const unsigned listed_upto = warp_scan(theirs, lane), listed = __shfl_sync(~0u, listed_upto, 31);
             const bool last = bound == heat.deep;
             if (listed > kShort) {
@@ -639,24 +617,25 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 __syncthreads();
                 tell(have, 0, &s.listed_mass, nullptr);
                 cluster.sync();
-                enough = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.listed_mass; })) >= want;
+                enough = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.listed_mass; })) >= want;
             }
             if (enough) {
                 // to the first CTA, in the order of the ids
-                Shared* first = cluster.map_shared_rank(&s, 0);
+                S* first = cluster.map_shared_rank(&s, 0);
+                auto put = [&](int to, int at) {
+                    if constexpr (kDtype == HC_DTYPE_FP32) first->value[to] = reinterpret_cast<const float*>(segment)[at];
+                    else first->value[to] = reinterpret_cast<const uint16_t*>(segment)[at];
+                    first->id[to] = id0 + at;
+                };
                 int to = __shfl_sync(~0u, listed_upto - theirs, rank);
                 to += __reduce_add_sync(~0u, lane < warp ? my_listed : 0);
-                for (int i = lane; i < m; i += 32) {
-                    // (a warp whose list has no room for so many finds them again below)
-                    const int at = fits ? static_cast<int>(mine[i]) : 0;
-                    if (fits) first->value[to + i] = logit<kDtype>(segment, at), first->id[to + i] = id0 + at;
-                }
-                if (!fits) {
+                if (fits) {
+                    for (int i = lane; i < m; i += 32) put(to + i, mine[i]);
+                } else {                                        // (found again)
                     for (int i = part_begin; i < part_end; i += 32) {
                         const float y = i + lane < part_end ? logit<kDtype>(segment, i + lane) : -CUDART_INF_F;
                         const unsigned votes = __ballot_sync(~0u, y >= bound);
-                        const int at = to + __popc(votes & ((1u << lane) - 1u));
-                        if (y >= bound) first->value[at] = y, first->id[at] = id0 + i + lane;
+                        if (y >= bound) put(to + __popc(votes & ((1u << lane) - 1u)), i + lane);
                         to += __popc(votes);
                     }
                 }
@@ -783,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const unsigned warp_ties = s.warp_count[warp];
     sync();
     // (each lane a CTA's part)
-    tie = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.total; });
-    const uint64_t kept = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const Shared& o) { return o.kept; });
-    const unsigned their_ties = of_ctas<unsigned>(cluster, ctas, lane, s, [](const Shared& o) { return o.ties; });
+    tie = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.total; });
+    const uint64_t kept = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.kept; });
+    const unsigned their_ties = of_ctas<unsigned>(cluster, ctas, lane, s, [](const S& o) { return o.ties; });
 #pragma unroll
     for (int d = kMaxCtas / 2; d > 0; d >>= 1) tie = max(tie, __shfl_xor_sync(~0u, tie, d));
     tie = __shfl_sync(~0u, tie, 0);
@@ -868,9 +847,10 @@ cudaError_t call(const Ctx& ctx, const SampleArgs& a, cudaStream_t st) {
     const int ctas = row_ctas(ctx.sm_count, a.tokens, a.vocab);
     // a row may begin anywhere in its first vector
     const int vectors = ((a.vocab + 2 * kN - 2) / kN + ctas - 1) / ctas;
-    // a list of all that a warp goes through, 16 bits each; of a half where CTAs share the SMs
+    // a list of all that a warp goes through, 16 bits each; of three tenths where CTAs share the SMs, so that four
+    // CTAs do
     const bool alone = static_cast<int64_t>(a.tokens) * ctas <= 2 * ctx.sm_count;
-    const int room = (vectors + kWarps - 1) / kWarps * kN / (alone ? 1 : 2);
+    const int most = (vectors + kWarps - 1) / kWarps * kN, room = alone ? most : most * 3 / 10;
     const size_t smem = static_cast<size_t>(vectors) * 16 + sizeof(uint16_t) * kWarps * room;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.tokens) * ctas);
