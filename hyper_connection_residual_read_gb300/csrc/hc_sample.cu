@@ -203,13 +203,10 @@ struct Shared {
     // of a step's bins: their logits, and their weights as sums of each 16 bits of them (shared memory adds
     // 32 bits at a time by itself: three such sums take 8 cycles a warp, one of 64 bits 50 to 570)
     unsigned count[kBins], mass[3][kBins];
-    // what a CTA tells the others
-    float top;
-    uint64_t total;
-    uint64_t listed_mass;
-    unsigned listed;
-    uint64_t kept;                           // beside the equal ones at the border
-    unsigned ties;
+    // what the warps tell the cluster
+    alignas(16) uint64_t told_mass[kWarps];
+    alignas(16) unsigned told_count[kWarps];
+    alignas(16) float told_top[kWarps];
     // within the CTA
     uint64_t warp_mass[kWarps];
     unsigned warp_count[kWarps];
@@ -221,10 +218,19 @@ struct Shared {
     typename std::conditional<kDtype == HC_DTYPE_FP32, float, uint16_t>::type value[kShort];
 };
 
-// A value of each CTA, one a lane (0 for lanes past them), brought at once.
-template <typename T, int kDtype, typename Get>
-__device__ __forceinline__ T of_ctas(cg::cluster_group& cluster, int ctas, int lane, Shared<kDtype>& s, Get get) {
-    return lane < ctas ? get(*cluster.map_shared_rank(&s, lane)) : T(0);
+// What the warps of a cluster have told, two warps a lane, in their order: CTA lane / 4, warps 2 (lane % 4) and the
+// next. Lanes past the CTAs get `none`.
+template <typename T>
+struct Two {
+    T x, y;
+};
+template <typename T, int kDtype>
+__device__ __forceinline__ Two<T> of_warps(cg::cluster_group& cluster, int ctas, int lane, Shared<kDtype>& s, T (Shared<kDtype>::*told)[kWarps], T none) {
+    static_assert(kWarps == 8, "four lanes a CTA");
+    const bool there = lane < 4 * ctas;
+    const Shared<kDtype>* o = ctas == 1 ? &s : cluster.map_shared_rank(&s, there ? lane >> 2 : 0);
+    const T* p = (o->*told) + 2 * (lane & 3);
+    return there ? Two<T>{p[0], p[1]} : Two<T>{none, none};
 }
 
 // Logits above `at` stay, and of those equal to it the first `ties`.
@@ -275,6 +281,64 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&y)[kDtype == HC_D
             const float2 f = widen2<kDtype>(w[e]);
             y[2 * e] = f.x, y[2 * e + 1] = f.y;
         }
+    }
+}
+
+// The end of a row of which at most kThreads logits are left, in one CTA, a logit a thread: each counts and weighs
+// those before it. `want`: the weight of a top-p alone (`whole`: it follows from the list's). (A row of a top-50 among
+// 131072 13.4 us in bins, @@ so.)
+template <int kDtype, typename Weigh>
+__device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs& a, int row, int n, int k, bool by_count, bool by_mass, bool whole,
+                                             uint64_t want, float p, uint64_t low, float u, float t, float top, Weigh& weigh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // the bins' room is free: values and weights of the list
+    float* value = reinterpret_cast<float*>(s.count);
+    uint64_t* mass = reinterpret_cast<uint64_t*>(s.mass);
+    static_assert(sizeof(s.count) >= kThreads * sizeof(float) && sizeof(s.mass) >= kThreads * sizeof(uint64_t));
+    const float y[4] = {tid < n ? logit<kDtype>(s.value, tid) : -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+    uint64_t w[4];
+    weigh(y, w);
+    value[tid] = y[0], mass[tid] = w[0];
+    __syncthreads();
+    // sums over the CTA: in every thread; up to and with this one
+    auto sum_of = [&](uint64_t x) {
+        x = warp_sum(x);
+        if (lane == 0) s.warp_mass[warp] = x;
+        __syncthreads();
+        x = 0;
+        for (int i = 0; i < kWarps; ++i) x += s.warp_mass[i];
+        __syncthreads();
+        return x;
+    };
+    unsigned rank = 0;
+    uint64_t before = 0;
+    if (warp * 32 < n) {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const bool first = j < tid ? value[j] >= y[0] : value[j] > y[0];
+            rank += first;
+            if (by_mass) before += first ? mass[j] : 0;
+        }
+    }
+    bool stays = tid < n && w[0] >= low && (!by_count || rank < static_cast<unsigned>(k));
+    if (by_mass) {
+        if (by_count) want = max(part_of(sum_of(tid < n && rank < static_cast<unsigned>(k) ? w[0] : 0), fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+        else if (whole) want = max(part_of(sum_of(w[0]), fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+        stays = stays && before < want;
+    }
+    const uint64_t kept = stays ? w[0] : 0;
+    uint64_t upto = warp_scan(kept, lane);
+    if (lane == 31) s.warp_mass[warp] = upto;
+    __syncthreads();
+    uint64_t total = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) upto += total;
+        total += s.warp_mass[i];
+    }
+    const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
+    if (upto > goal && upto - kept <= goal) {
+        a.ids[row] = s.id[tid];
+        a.logprob[row] = ((y[0] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
     }
 }
 
@@ -334,27 +398,21 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     // ---- the largest logit
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) most = max_nan(most, __shfl_xor_sync(~0u, most, d));
-    if (lane == 0) s.warp_count[warp] = __float_as_uint(most);
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) most = max_nan(most, __uint_as_float(s.warp_count[w]));
-        s.top = most;
-    }
+    if (lane == 0) s.told_top[warp] = most;
     cluster.sync();
-    const float tops = cluster.map_shared_rank(&s, lane < ctas ? lane : 0)->top;
-    float top = tops;
+    const Two<float> tops = of_warps<float>(cluster, ctas, lane, s, &S::told_top, -CUDART_INF_F);
+    float top = max_nan(tops.x, tops.y);
 #pragma unroll
-    for (int d = kMaxCtas / 2; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
-    top = __shfl_sync(~0u, top, 0);
+    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
     bad = bad || !(fabsf(top) <= kTop);
     // each warp's part of the segment
     const int all = (v1 - v0) * kN, per = ((v1 - v0 + kWarps - 1) / kWarps) * kN;
     const int part_begin = min(warp * per, all), part_end = min(part_begin + per, all);
     if (bad || t < 5.421010862427522e-20f) {
         // nothing, or the first of the largest: the first CTA that has it finds it
-        const unsigned with = __ballot_sync(~0u, lane < ctas && tops == top);
+        const unsigned with = __ballot_sync(~0u, tops.x == top || tops.y == top);
         cluster.sync();                          // all have read what the others told
-        if (bad ? rank != 0 : rank != __ffs(with) - 1) return;
+        if (bad ? rank != 0 : rank != (__ffs(with) - 1) / 4) return;
         int first = 0x7FFFFFFF;
         if (!bad)
             for (int i = part_begin / kN + lane; i < part_end / kN; i += 32) {
@@ -376,17 +434,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     }
     const Heat heat = heat_of(t, top);
     const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1.f;
-    // sums of a value over the CTA, told to the others
-    auto tell = [&](uint64_t mass, unsigned count, uint64_t* to_mass, unsigned* to_count) {
+    // a warp's sum, told to the cluster
+    auto tell_mass = [&](uint64_t mass) {
         mass = warp_sum(mass);
-        count = __reduce_add_sync(~0u, count);
-        if (lane == 0) s.warp_mass[warp] = mass, s.warp_count[warp] = count;
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < kWarps; ++w) mass += s.warp_mass[w], count += s.warp_count[w];
-            *to_mass = mass;
-            if (to_count) *to_count = count;
-        }
+        if (lane == 0) s.told_mass[warp] = mass;
+    };
+    auto all_mass = [&]() {
+        const Two<uint64_t> told = of_warps<uint64_t>(cluster, ctas, lane, s, &S::told_mass, 0);
+        return warp_sum(told.x + told.y);
     };
 
     // The logits that this warp goes through, four a lane at a time: all of its part, those listed of it, or
@@ -440,6 +495,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         if (mode == kAlone) __syncthreads();
         else cluster.sync();
     };
+    // the least weight that stays
+    const uint64_t low = !(least > 0.f) ? 1 : least < 1.f ? max(part_of(kOne, least, true), static_cast<uint64_t>(1)) : kOne;
     Cut cut = {-CUDART_INF_F, 0, 0};             // all stay
     if (by_count || by_mass) {
         const bool few = a.vocab <= kShort;                             // they go to one CTA without an estimate
@@ -464,10 +521,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 weigh(y, w);
                 total += (w[0] + w[1]) + (w[2] + w[3]);
             };
-            if (!by_count) each_of_all(add_up);
-            tell(total, 0, &s.total, nullptr);
+            if (!by_count) {
+                each_of_all(add_up);
+                tell_mass(total);
+            }
             cluster.sync();
-            total = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.total; }));
+            if (!by_count) total = all_mass();
             unsigned theirs[kMaxCtas];
 #pragma unroll
             for (int r = 0; r < kMaxCtas; ++r) theirs[r] = r < ctas ? cluster.map_shared_rank(&s, r < ctas ? r : 0)->id[tid] : 0;
@@ -561,36 +620,43 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         for (int attempt = 0;; ++attempt) {
             bound = bound_of(attempt);
             int m = 0;
-            for (int i = part_begin / kN; i < part_end / kN; i += 32) {
-                unsigned set = 0;                               // a bit a logit of this lane's vector
-                if (i + lane < part_end / kN) {
-                    const uint4 v = vec[i + lane];
-                    Most<kDtype> largest;
-                    largest.take(v);
-                    if (largest.get() >= bound) {
-                        float y[kN];
-                        unpack<kDtype>(v, y);
+            for (int i0 = part_begin / kN; i0 < part_end / kN; i0 += 128) {
+                // 128 vectors, four a lane: a bit a logit
+                unsigned set[4] = {};
 #pragma unroll
-                        for (int e = 0; e < kN; ++e) set |= (y[e] >= bound ? 1u : 0u) << e;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + 32 * e + lane;
+                    if (i >= part_end / kN) continue;
+                    const uint4 v = vec[i];
+                    Most<kDtype> most_of;
+                    most_of.take(v);
+                    if (!(most_of.get() >= bound)) continue;
+                    float y[kN];
+                    unpack<kDtype>(v, y);
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) set[e] |= (y[n] >= bound ? 1u : 0u) << n;
                 }
-                if (__any_sync(~0u, set != 0)) {
-                    const int count = __popc(set), before = warp_scan(count, lane) - count;
-                    int to = m + before;
-                    for (; set != 0; set &= set - 1, ++to)
-                        if (to < list_room) mine[to] = static_cast<uint16_t>((i + lane) * kN + __ffs(set) - 1);
-                    m += __shfl_sync(~0u, before + count, 31);
+                if (!__any_sync(~0u, (set[0] | set[1] | set[2] | set[3]) != 0)) continue;
+                // the counts of all four in one scan (at most 256 each)
+                const uint64_t count = static_cast<uint64_t>(__popc(set[0])) | static_cast<uint64_t>(__popc(set[1])) << 16 |
+                                       static_cast<uint64_t>(__popc(set[2])) << 32 | static_cast<uint64_t>(__popc(set[3])) << 48;
+                const uint64_t upto = warp_scan(count, lane), sums = __shfl_sync(~0u, upto, 31), before = upto - count;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    int to = m + static_cast<int>((before >> (16 * e)) & 0xFFFF);
+                    for (; set[e] != 0; set[e] &= set[e] - 1, ++to)
+                        if (to < list_room) mine[to] = static_cast<uint16_t>((i0 + 32 * e + lane) * kN + __ffs(set[e]) - 1);
+                    m += static_cast<int>((sums >> (16 * e)) & 0xFFFF);
                 }
             }
-            __syncwarp();
+            if (lane == 0) s.told_count[warp] = m;
+            cluster.sync();
+            const Two<unsigned> lists = of_warps<unsigned>(cluster, ctas, lane, s, &S::told_count, 0);
+            const unsigned lists_upto = warp_scan(lists.x + lists.y, lane), listed = __shfl_sync(~0u, lists_upto, 31);
             // all of the CTA's warps go through their lists, or all through everything
-            const bool fits = !__syncthreads_or(m > list_room);
+            const bool fits = !__any_sync(~0u, lane / 4 == rank && (lists.x > list_room || lists.y > list_room));
             mode = fits ? kListed : kAll;
             n = fits ? m : part_end - part_begin;
-            tell(0, lane == 0 ? m : 0, &s.listed_mass, &s.listed);
-            cluster.sync();
-            const unsigned theirs = of_ctas<unsigned>(cluster, ctas, lane, s, [](const S& o) { return o.listed; });
-            const unsigned listed_upto = warp_scan(theirs, lane), listed = __shfl_sync(~0u, listed_upto, 31);
             const bool last = bound == heat.deep;
             if (listed > kShort) {
                 // by value; whether they are enough is seen from it
@@ -604,7 +670,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 continue;
             }
             bool enough = last || (by_count && listed >= want);
-            const unsigned my_listed = lane < kWarps ? s.warp_count[lane] : 0;      // of the warps, one a lane
             if (!enough && !by_count) {
                 uint64_t have = 0;
                 each([&](const float (&y)[4]) {
@@ -614,10 +679,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                     for (int e = 0; e < 4; ++e)
                         if (y[e] >= bound) have += w[e];
                 });
-                __syncthreads();
-                tell(have, 0, &s.listed_mass, nullptr);
+                tell_mass(have);
                 cluster.sync();
-                enough = warp_sum(of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.listed_mass; })) >= want;
+                enough = all_mass() >= want;
             }
             if (enough) {
                 // to the first CTA, in the order of the ids
@@ -627,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                     else first->value[to] = reinterpret_cast<const uint16_t*>(segment)[at];
                     first->id[to] = id0 + at;
                 };
-                int to = __shfl_sync(~0u, listed_upto - theirs, rank);
-                to += __reduce_add_sync(~0u, lane < warp ? my_listed : 0);
+                const unsigned first_of_two = lists_upto - lists.x - lists.y;
+                int to = __shfl_sync(~0u, (warp & 1) ? first_of_two + lists.x : first_of_two, 4 * rank + warp / 2);
                 if (fits) {
                     for (int i = lane; i < m; i += 32) put(to + i, mine[i]);
                 } else {                                        // (found again)
@@ -641,6 +705,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 }
                 cluster.sync();
                 if (rank != 0) return;
+                if (listed <= kThreads) {
+                    finish_alone(s, a, row, static_cast<int>(listed), k, by_count, by_mass, few && !by_count, want, p, low, u, t, top, weigh);
+                    return;
+                }
                 mode = kAlone, ctas = 1;
                 const int share = (static_cast<int>(listed) + kWarps - 1) / kWarps;
                 begin = min(warp * share, static_cast<int>(listed));
@@ -728,8 +796,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     }
 
     // ---- the sums of what stays, and the token
-    const uint64_t low = !(least > 0.f) ? 1 : least < 1.f ? max(part_of(kOne, least, true), static_cast<uint64_t>(1)) : kOne;
-    uint64_t mass = 0, tie = 0;
+    uint64_t mass = 0;
     unsigned ties = 0;
     auto keep = [&](const float (&y)[4]) {
         uint64_t w[4];
@@ -738,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         for (int e = 0; e < 4; ++e) {
             if (w[e] < low) continue;
             if (y[e] > cut.at) mass += w[e];
-            if (y[e] == cut.at) ++ties, tie = w[e];
+            if (y[e] == cut.at) ++ties;
         }
     };
     if (mode == kAll && cut.at == -CUDART_INF_F && low == 1) each_of_all([&](const float (&y)[4]) {
@@ -748,86 +815,73 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     });
     else if (mode == kAll) each_of_all(keep);
     else each(keep);
-    // (the equal ones' weight, where this warp has one)
-    {
-        const unsigned with = __ballot_sync(~0u, ties > 0);
-        if (with) tie = __shfl_sync(~0u, tie, __ffs(with) - 1);
-    }
-    __syncthreads();
-    tell(mass, ties, &s.kept, &s.ties);
-    if (tid == 0) s.total = 0;
-    __syncthreads();
-    if (lane == 0 && tie > 0) s.total = tie;     // the same from any warp
-    const uint64_t warp_mass = s.warp_mass[warp];
-    const unsigned warp_ties = s.warp_count[warp];
+    tell_mass(mass);
+    ties = __reduce_add_sync(~0u, ties);
+    if (lane == 0) s.told_count[warp] = ties;
     sync();
-    // (each lane a CTA's part)
-    tie = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.total; });
-    const uint64_t kept = of_ctas<uint64_t>(cluster, ctas, lane, s, [](const S& o) { return o.kept; });
-    const unsigned their_ties = of_ctas<unsigned>(cluster, ctas, lane, s, [](const S& o) { return o.ties; });
-#pragma unroll
-    for (int d = kMaxCtas / 2; d > 0; d >>= 1) tie = max(tie, __shfl_xor_sync(~0u, tie, d));
-    tie = __shfl_sync(~0u, tie, 0);
-    const unsigned ties_before = warp_scan(their_ties, lane) - their_ties;
-    const unsigned take = min(cut.ties - min(cut.ties, ties_before), their_ties);
-    const uint64_t upto = warp_scan(kept + take * tie, lane);
+    // two warps a lane: how many of their equal ones stay, and the sums up to them
+    const Two<uint64_t> masses = of_warps<uint64_t>(cluster, ctas, lane, s, &S::told_mass, 0);
+    const Two<unsigned> all_ties = of_warps<unsigned>(cluster, ctas, lane, s, &S::told_count, 0);
+    uint64_t tie = 0;
+    if (cut.ties > 0) {
+        const float y[4] = {cut.at, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        uint64_t w[4];
+        weigh(y, w);
+        tie = w[0];
+    }
+    const unsigned ties_before = warp_scan(all_ties.x + all_ties.y, lane) - all_ties.x - all_ties.y;
+    const unsigned take_x = min(cut.ties - min(cut.ties, ties_before), all_ties.x);
+    const unsigned take_y = min(cut.ties - min(cut.ties, ties_before + all_ties.x), all_ties.y);
+    const uint64_t sum_x = masses.x + take_x * tie, sum_y = masses.y + take_y * tie, upto = warp_scan(sum_x + sum_y, lane);
     const uint64_t total = __shfl_sync(~0u, upto, 31);
-    // the CTA's place in the sum
-    const uint64_t here = __shfl_sync(~0u, kept + take * tie, rank), before = __shfl_sync(~0u, upto, rank) - here;
-    const unsigned here_ties = __shfl_sync(~0u, take, rank);
     const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
+    // this warp's
+    const bool is_y = warp & 1;
+    const int at_lane = 4 * rank + warp / 2;
+    const uint64_t from = __shfl_sync(~0u, is_y ? upto - sum_y : upto - sum_y - sum_x, at_lane);
+    const uint64_t here = __shfl_sync(~0u, is_y ? sum_y : sum_x, at_lane);
+    unsigned allow = __shfl_sync(~0u, is_y ? take_y : take_x, at_lane);
     sync();                                      // no CTA leaves while another reads its memory
-    if (goal >= before && goal - before < here) {
-        // the warp's place in the CTA
-        uint64_t from = before;
-        unsigned allow = here_ties;
-        for (int w = 0; w < warp; ++w) {
-            const unsigned some = min(allow, s.warp_count[w]);
-            allow -= some;
-            from += s.warp_mass[w] + some * tie;
-        }
-        allow = min(allow, warp_ties);
-        if (goal >= from && goal - from < warp_mass + allow * tie) {
-            // 128 logits at a time, then the 32 and the one among them
-            uint64_t sum = from;
-            for (int i = 0; i < n; i += 128) {
-                float y[4];
-                uint64_t w[4];
+    if (goal >= from && goal - from < here) {
+        // 128 logits at a time, then the 32 and the one among them
+        uint64_t sum = from;
+        for (int i = 0; i < n; i += 128) {
+            float y[4];
+            uint64_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < n ? value_at(i + lane + 32 * e) : -CUDART_INF_F;
-                weigh(y, w);
-                uint64_t sums = 0;
+            for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < n ? value_at(i + lane + 32 * e) : -CUDART_INF_F;
+            weigh(y, w);
+            uint64_t sums = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (w[e] < low || y[e] < cut.at) w[e] = 0;
-                    const bool equal = w[e] > 0 && y[e] == cut.at;
-                    const unsigned votes = __ballot_sync(~0u, equal);
-                    if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w[e] = 0;
-                    allow -= min(allow, static_cast<unsigned>(__popc(votes)));
-                    sums += w[e];
-                }
-                sums = warp_sum(sums);
-                if (sum + sums <= goal) {
-                    sum += sums;
-                    continue;
-                }
-                bool done = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint64_t at = sum + warp_scan(w[e], lane);
-                    const unsigned past = __ballot_sync(~0u, at > goal);
-                    if (past && !done) {
-                        done = true;
-                        if (lane == __ffs(past) - 1) {
-                            const int at = i + lane + 32 * e;
-                            a.ids[row] = mode == kAlone ? s.id[begin + at] : id0 + (mode == kListed ? static_cast<int>(mine[at]) : begin + at);
-                            a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
-                        }
-                    }
-                    sum = __shfl_sync(~0u, at, 31);
-                }
-                break;
+            for (int e = 0; e < 4; ++e) {
+                if (w[e] < low || y[e] < cut.at) w[e] = 0;
+                const bool equal = w[e] > 0 && y[e] == cut.at;
+                const unsigned votes = __ballot_sync(~0u, equal);
+                if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w[e] = 0;
+                allow -= min(allow, static_cast<unsigned>(__popc(votes)));
+                sums += w[e];
             }
+            sums = warp_sum(sums);
+            if (sum + sums <= goal) {
+                sum += sums;
+                continue;
+            }
+            bool done = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t at = sum + warp_scan(w[e], lane);
+                const unsigned past = __ballot_sync(~0u, at > goal);
+                if (past && !done) {
+                    done = true;
+                    if (lane == __ffs(past) - 1) {
+                        const int at = i + lane + 32 * e;
+                        a.ids[row] = mode == kAlone ? s.id[begin + at] : id0 + (mode == kListed ? static_cast<int>(mine[at]) : begin + at);
+                        a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
+                    }
+                }
+                sum = __shfl_sync(~0u, at, 31);
+            }
+            break;
         }
     }
 }
