@@ -212,7 +212,7 @@ struct Shared {
     unsigned warp_count[kWarps];
     uint64_t before_mass, in_mass;           // of the bin with the border
     unsigned before, in;
-    int warp_first[kWarps];
+    int warp_first[kWarps], warp_begin[kWarps], warp_n[kWarps];
     // a short list: ids and values; before it, the bins of the estimate lie in the first
     int id[kShort];
     typename std::conditional<kDtype == HC_DTYPE_FP32, float, uint16_t>::type value[kShort];
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     else each(keep);
     tell_mass(mass);
     ties = __reduce_add_sync(~0u, ties);
-    if (lane == 0) s.told_count[warp] = ties;
+    if (lane == 0) s.told_count[warp] = ties, s.warp_begin[warp] = begin, s.warp_n[warp] = n;
     sync();
     // two warps a lane: how many of their equal ones stay, and the sums up to them
     const Two<uint64_t> masses = of_warps<uint64_t>(cluster, ctas, lane, s, &S::told_mass, 0);
@@ -835,53 +835,68 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const uint64_t sum_x = masses.x + take_x * tie, sum_y = masses.y + take_y * tie, upto = warp_scan(sum_x + sum_y, lane);
     const uint64_t total = __shfl_sync(~0u, upto, 31);
     const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
-    // this warp's
-    const bool is_y = warp & 1;
-    const int at_lane = 4 * rank + warp / 2;
-    const uint64_t from = __shfl_sync(~0u, is_y ? upto - sum_y : upto - sum_y - sum_x, at_lane);
-    const uint64_t here = __shfl_sync(~0u, is_y ? sum_y : sum_x, at_lane);
-    unsigned allow = __shfl_sync(~0u, is_y ? take_y : take_x, at_lane);
+    // the warp whose sum passes the goal, what lies before it, and how many equal ones of it stay
+    const unsigned past = __ballot_sync(~0u, upto > goal);
+    const int at_lane = __ffs(past) - 1;
+    const bool in_y = __shfl_sync(~0u, goal >= upto - sum_y, at_lane);
+    uint64_t from = __shfl_sync(~0u, in_y ? upto - sum_y : upto - sum_y - sum_x, at_lane);
+    unsigned allow = __shfl_sync(~0u, in_y ? take_y : take_x, at_lane);
     sync();                                      // no CTA leaves while another reads its memory
-    if (goal >= from && goal - from < here) {
-        // 128 logits at a time, then the 32 and the one among them
-        uint64_t sum = from;
-        for (int i = 0; i < n; i += 128) {
-            float y[4];
-            uint64_t w[4];
+    if (at_lane / 4 != rank) return;
+    // its logits, shared out over the CTA's warps: 128 at a time
+    const int owner = 2 * (at_lane % 4) + in_y, its_n = s.warp_n[owner];
+    begin = s.warp_begin[owner], mine = list + owner * list_room;
+    const int share = (its_n + 128 * kWarps - 1) / (128 * kWarps) * 128, i0 = min(warp * share, its_n), i1 = min(i0 + share, its_n);
+    auto bring = [&](int i, float (&y)[4], uint64_t (&w)[4]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < n ? value_at(i + lane + 32 * e) : -CUDART_INF_F;
-            weigh(y, w);
-            uint64_t sums = 0;
+        for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < i1 ? value_at(i + lane + 32 * e) : -CUDART_INF_F;
+        weigh(y, w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (w[e] < low || y[e] < cut.at) w[e] = 0;
-                const bool equal = w[e] > 0 && y[e] == cut.at;
-                const unsigned votes = __ballot_sync(~0u, equal);
-                if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w[e] = 0;
-                allow -= min(allow, static_cast<unsigned>(__popc(votes)));
-                sums += w[e];
-            }
-            sums = warp_sum(sums);
-            if (sum + sums <= goal) {
-                sum += sums;
-                continue;
-            }
-            bool done = false;
+        for (int e = 0; e < 4; ++e)
+            if (w[e] < low || y[e] < cut.at) w[e] = 0;
+    };
+    mass = ties = 0;
+    for (int i = i0; i < i1; i += 128) {
+        float y[4];
+        uint64_t w[4];
+        bring(i, y, w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint64_t at = sum + warp_scan(w[e], lane);
-                const unsigned past = __ballot_sync(~0u, at > goal);
-                if (past && !done) {
-                    done = true;
-                    if (lane == __ffs(past) - 1) {
-                        const int at = i + lane + 32 * e;
-                        a.ids[row] = mode == kAlone ? s.id[begin + at] : id0 + (mode == kListed ? static_cast<int>(mine[at]) : begin + at);
-                        a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
-                    }
+        for (int e = 0; e < 4; ++e) {
+            if (y[e] != cut.at) mass += w[e];
+            else ties += w[e] > 0;
+        }
+    }
+    mass = warp_sum(mass), ties = __reduce_add_sync(~0u, ties);
+    if (lane == 0) s.warp_mass[warp] = mass, s.warp_count[warp] = ties;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        const unsigned some = min(allow, s.warp_count[w]);
+        allow -= some;
+        from += s.warp_mass[w] + some * tie;
+    }
+    if (goal < from || goal - from >= mass + min(allow, ties) * tie) return;
+    // the 128, the 32 and the one among them
+    for (int i = i0; i < i1; i += 128) {
+        float y[4];
+        uint64_t w[4];
+        bring(i, y, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool equal = w[e] > 0 && y[e] == cut.at;
+            const unsigned votes = __ballot_sync(~0u, equal);
+            if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w[e] = 0;
+            allow -= min(allow, static_cast<unsigned>(__popc(votes)));
+            const uint64_t at = from + warp_scan(w[e], lane);
+            const unsigned found = __ballot_sync(~0u, at > goal);
+            if (found) {
+                if (lane == __ffs(found) - 1) {
+                    const int j = i + lane + 32 * e;
+                    a.ids[row] = mode == kAlone ? s.id[begin + j] : id0 + (mode == kListed ? static_cast<int>(mine[j]) : begin + j);
+                    a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
                 }
-                sum = __shfl_sync(~0u, at, 31);
+                return;
             }
-            break;
+            from = __shfl_sync(~0u, at, 31);
         }
     }
 }
