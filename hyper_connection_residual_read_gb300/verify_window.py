@@ -13,6 +13,13 @@ the drafted ones) through
 
 A drafted token is accepted while it is the most likely one (greedy verification). Drafts
 come from the request's own text: what followed the last token when it occurred before.
+
+With ``positions`` queries and keys are normed by head and rotated (hc_kv4_append_rotary in place
+of hc_kv4_append); with ``sampling`` a token is drawn for each of the window's
+(hc_sample_tokens), and a drafted one is accepted while it is the one drawn, which leaves the
+text as likely as without drafts; and a prompt that all requests begin with is cached once
+(``share``) and read once a step for all of them (hc_kv4_attention_shared).
+
 The matrix products between the operators (projections, logits) are torch's. Everything a
 step launches reads its lengths from device memory; the host reads back one small table a
 step, the verified tokens.
@@ -35,7 +42,8 @@ class Decoder:
     """Random weights, and one paged 4-bit cache a layer with a table shared by them."""
 
     def __init__(self, requests: int, layers: int = 2, vocab: int = 4096, blocks: int = 512,
-                 block_size: int = 32, max_tokens: int = 4096, drafts: int = 7, seed: int = 0):
+                 block_size: int = 32, max_tokens: int = 4096, drafts: int = 7, seed: int = 0,
+                 positions: bool = False, sampling: dict | None = None, longest: int = 8192):
         g = torch.Generator().manual_seed(seed)
         normal = lambda *shape, scale: (torch.randn(shape, generator=g) * scale).bfloat16().cuda()  # noqa: E731
         self.requests, self.block_size, self.drafts, self.vocab = requests, block_size, drafts, vocab
@@ -58,6 +66,16 @@ class Decoder:
         self.free = torch.arange(blocks, dtype=torch.int32, device="cuda")
         self.free_count = torch.full((1,), blocks, dtype=torch.int32, device="cuda")
         self.free_left = ints(1)
+        self.sampling, self.uniform = sampling, torch.Generator(device="cuda").manual_seed(seed)
+        self.cos_sin = None
+        if positions:
+            angle = torch.arange(longest)[:, None] * 10000.0 ** (-torch.arange(0, HEAD_DIM, 2).double() / HEAD_DIM)
+            self.cos_sin = torch.stack([angle.cos(), angle.sin()], 1).float().cuda()
+            for w in self.layers:
+                w["q_norm"], w["k_norm"] = ((1 + 0.1 * torch.randn(HEAD_DIM, generator=g)).bfloat16().cuda() for _ in range(2))
+        # the blocks that all requests share, if any
+        self.prefix_table, self.prefix_len = None, torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.one_group = torch.tensor([0, requests], dtype=torch.int32, device="cuda")
         hc.hc_read_init(torch.cuda.current_device(), max_tokens, 1e-6)
 
     def step(self, windows, top: int = 4) -> dict:
@@ -73,6 +91,9 @@ class Decoder:
         request_of, positions = torch.empty(total, **ints), torch.empty(total, **ints)
         hc.hc_window_plan(self.cached, self.new, self.free, self.free_count, self.block_size, self.table,
                           slots, request_of, positions, self.cu, self.kv, self.free_left)
+        at = positions + self.prefix_len
+        if self.prefix_table is not None:
+            workspace = torch.empty(total * Q_HEADS * (HEAD_DIM + 2), device="cuda")
         R = self.embed[tokens.long()].float()[:, None].repeat(1, STREAMS, 1).contiguous()
         P = None
         Rmix = self.mix.expand(total, STREAMS, STREAMS).contiguous()
@@ -82,9 +103,18 @@ class Decoder:
             hc.hc_read(total, R, P, w["w_norm"], w["W_down"], w["W_up"], Rmix, mixed, image, image16)
             qkv = image.view(torch.bfloat16)[:, 0] @ w["qkv"].T
             q, k, v = qkv.view(total, -1, HEAD_DIM).split([Q_HEADS, KV_HEADS, KV_HEADS], 1)
-            hc.hc_kv4_append(k, v, slots, w["codes"], w["scales"])
+            if self.cos_sin is None:
+                hc.hc_kv4_append(k, v, slots, w["codes"], w["scales"])
+            else:
+                turned = torch.empty((total, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device="cuda")
+                hc.hc_kv4_append_rotary(q, k, v, self.cos_sin, at, slots, w["codes"], w["scales"], turned, w["q_norm"], w["k_norm"])
+                q = turned
             o = torch.empty((total, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device="cuda")
-            hc.hc_kv4_attention(q, w["codes"], w["scales"], self.table, self.cu, self.kv, max(lens), o)
+            if self.prefix_table is None:
+                hc.hc_kv4_attention(q, w["codes"], w["scales"], self.table, self.cu, self.kv, max(lens), o)
+            else:
+                hc.hc_kv4_attention_shared(q, w["codes"], w["scales"], self.prefix_table, self.prefix_len, self.one_group, total,
+                                           self.table, self.cu, self.kv, max(lens), workspace, o)
             # the layer's result is the pending write of the next read
             R, P = mixed, (o.view(total, -1) @ w["out"].T).float()[:, None].repeat(1, STREAMS, 1).contiguous()
         logits = (R + P).mean(1).bfloat16() @ self.unembed.T
@@ -93,12 +123,29 @@ class Decoder:
              "rank": flat(torch.int32), "top_ids": torch.empty((total, top), **ints),
              "top_logprobs": torch.empty((total, top), device="cuda")}
         hc.hc_token_logprobs(logits, follow, *r.values())
+        r["next"] = r["top_ids"]
+        if self.sampling is not None:
+            r["next"], r["drawn"] = torch.empty((total, 1), **ints), flat(torch.float32)
+            r["uniform"] = torch.rand(total, generator=self.uniform, device="cuda")
+            settings = {k: torch.full((total,), v, dtype=torch.int32 if k == "top_k" else torch.float32, device="cuda")
+                        for k, v in self.sampling.items()}
+            hc.hc_sample_tokens(logits, r["uniform"], r["next"].view(-1), r["drawn"], **settings)
         return {**r, "logits": logits, "follow": follow, "slots": slots, "request_of": request_of,
                 "positions": positions, "last_keys_values": (k, v)}
 
+    def share(self, prompt) -> None:
+        """Caches what every request begins with, once; before any of them has a cache."""
+        self.step([prompt, *[[]] * (self.requests - 1)])
+        if int(self.kv[0]) != len(prompt):
+            raise RuntimeError("no blocks left for the shared prompt")
+        held = -(-len(prompt) // self.block_size)
+        self.prefix_table = self.table[:1, :held].clone()
+        self.prefix_len += len(prompt)
+        self.free_count.copy_(self.free_left)
+
     def accept(self, windows, top_ids, prompt=False) -> list:
-        """The tokens that each window gained: its drafted ones as far as each is the most
-        likely, and one more. The cache keeps what was verified (a prompt as a whole: ``prompt``
+        """The tokens that each window gained: its drafted ones as far as each is the first of
+        ``top_ids`` (the most likely, or drawn), and one more. The cache keeps what was verified (a prompt as a whole: ``prompt``
         says of all windows, or of each, that they are), and blocks past it are free again. A
         request whose blocks were not granted gains nothing."""
         prompt = [prompt] * len(windows) if isinstance(prompt, bool) else prompt
@@ -160,7 +207,7 @@ def generate(decoder: Decoder, prompts: list, tokens: int, propose=draft) -> tup
         windows = [[] if len(t) >= n else list(t) if w else [t[-1], *propose(t, decoder.drafts)]
                    for t, n, w in zip(texts, goal, waits)]
         r = decoder.step(windows)
-        gained = decoder.accept(windows, r["top_ids"], prompt=waits)
+        gained = decoder.accept(windows, r["next"], prompt=waits)
         logprob, at = r["logprob"].tolist(), 0
         for b, (text, window, more) in enumerate(zip(texts, windows, gained)):
             text += more
@@ -184,13 +231,27 @@ def main() -> None:
     parser.add_argument("--requests", type=int, default=8)
     parser.add_argument("--tokens", type=int, default=64)
     parser.add_argument("--layers", type=int, default=2)
+    parser.add_argument("--positions", action="store_true", help="norm and rotate queries and keys")
+    parser.add_argument("--shared", type=int, default=0, help="tokens of a prompt that all requests begin with")
+    parser.add_argument("--temperature", type=float, help="draw tokens instead of taking the most likely")
+    parser.add_argument("--top-k", type=int, default=0)
+    parser.add_argument("--top-p", type=float, default=1.0)
+    parser.add_argument("--min-p", type=float, default=0.0)
     args = parser.parse_args()
     g = np.random.default_rng(0)
-    decoder = Decoder(args.requests, args.layers)
+    sampling = None if args.temperature is None else dict(temperature=args.temperature, top_k=args.top_k, top_p=args.top_p, min_p=args.min_p)
+    shared = np.random.default_rng(1).integers(0, 4096, args.shared).tolist()
+
+    def make():
+        decoder = Decoder(args.requests, args.layers, positions=args.positions, sampling=sampling)
+        if shared:
+            decoder.share(shared)
+        return decoder
+    decoder = make()
     prompts = [g.integers(0, decoder.vocab, 20 + 30 * b).tolist() for b in range(args.requests)]
     texts, steps, accepted = generate(decoder, prompts, args.tokens)
     # the same text again, drafted from what was generated
-    again = Decoder(args.requests, args.layers)
+    again = make()
     known = {tuple(p): t for p, t in zip(prompts, texts)}
 
     def recall(text, count):
