@@ -8,8 +8,8 @@ namespace hc {
 // Requests whose tables hold at most so many tokens of their own are short.
 constexpr int kShortRoom = 2048;
 
-extern template cudaError_t launch_attention<kPrefix>(const Ctx&, const AttentionArgs&, int, cudaStream_t);
-extern template cudaError_t launch_attention<kJoined>(const Ctx&, const AttentionArgs&, int, cudaStream_t);
+extern template cudaError_t launch_attention<kPrefix>(const Ctx&, const SharedArgs&, int, cudaStream_t);
+extern template cudaError_t launch_attention<kJoined>(const Ctx&, const SharedArgs&, int, cudaStream_t);
 extern template cudaError_t attention_window_setup<kPrefix>();
 extern template cudaError_t attention_window_setup<kJoined>();
 
@@ -36,14 +36,14 @@ cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dty
 // A group's rows are many, but where prefixes are short the chunk kernel's start is longer than its work: then each
 // group is cut into shares of up to 8 or 16 rows, and each share reads the prefix for itself. The costs are what
 // the kernels take, in us: a start, and rounds of units over the resident CTAs.
-cudaError_t launch_kv4_attention_prefix(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_kv4_attention_prefix(const Ctx& ctx, const SharedArgs& a, int dtype, cudaStream_t st) {
     const int group = a.q_heads / a.c.kv_heads;
     const int64_t rows = static_cast<int64_t>(a.shared) * group, room = static_cast<int64_t>(a.width) * a.c.block_size;
     const int64_t heads = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     if (rows <= kMaxRows) return launch_attention<kPrefix>(ctx, a, dtype, st);
     auto rounds = [&](int64_t units, int ctas) { return static_cast<double>((units + ctas - 1) / ctas); };
     double least = 20 + 2.4 * rounds(heads * ((rows + 255) / 256) * ((room + 127) / 128), ctx.sm_count);
-    AttentionArgs b = a;
+    SharedArgs b = a;
     for (int most = 8; most <= kMaxRows; most += 8) {
         const int each = most / group;                       // tokens of a share
         if (each == 0) continue;
@@ -55,7 +55,7 @@ cudaError_t launch_kv4_attention_prefix(const Ctx& ctx, const AttentionArgs& a, 
     }
     return launch_attention<kPrefix>(ctx, b, dtype, st);
 }
-cudaError_t launch_kv4_attention_joined(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_kv4_attention_joined(const Ctx& ctx, const SharedArgs& a, int dtype, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads), room = static_cast<int64_t>(a.width) * a.c.block_size;
     const int64_t heads = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     if (rows <= kMaxRows && room <= kShortRoom && heads >= kWholeHeads) return launch_attention_short(ctx, a, dtype, st);

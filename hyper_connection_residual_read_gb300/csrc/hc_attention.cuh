@@ -130,7 +130,7 @@ constexpr int64_t kWhole = -1;
 constexpr int kWholeUnits = 8;                   // of the longest request
 constexpr int kWholeHeads = 128;                 // fewer leave most SMs without one
 
-__device__ __forceinline__ bool walk_whole(const AttentionArgs& a, Walk& k, int64_t number, int* status) {
+__device__ __forceinline__ bool walk_whole(const SharedArgs& a, Walk& k, int64_t number, int* status) {
     const int64_t all = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     for (; number < all; number += gridDim.x) {
         k.b = static_cast<int>(number / a.c.kv_heads), k.h = static_cast<int>(number % a.c.kv_heads);
@@ -146,8 +146,9 @@ __device__ __forceinline__ bool walk_whole(const AttentionArgs& a, Walk& k, int6
 
 // To the next piece; false at the end of the run.
 template <Side kSide>
-__device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k, int* status) {
-    if (kSide == kJoined && k.left == kWhole) return walk_whole(a, k, k.base + gridDim.x, status);
+__device__ __forceinline__ bool walk_next(const Args<kSide>& a, Walk& k, int* status) {
+    if constexpr (kSide == kJoined)
+        if (k.left == kWhole) return walk_whole(a, k, k.base + gridDim.x, status);
     if (k.left == 0) return false;
     k.base += k.units + k.cost;
     if (++k.h == a.c.kv_heads) {
@@ -183,7 +184,7 @@ __device__ __forceinline__ void cut_run(Run& run, int64_t total) {
 // the requests holds the run's first slot says where it lies. Up to 32 requests each warp
 // does so for itself, a request a lane, without a barrier.
 template <Side kSide>
-__device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int* status) {
+__device__ Run find_run(const Args<kSide>& a, Run* shared, int64_t* sums, int* status) {
     const int tid = threadIdx.x, lane = tid & 31;
     if (kShort) {                                // (what does not fit is reported as it is loaded)
         Run run = {};
@@ -267,8 +268,9 @@ __device__ Run find_run(const AttentionArgs& a, Run* shared, int64_t* sums, int*
 
 // The first piece of the run; false if it has none.
 template <Side kSide>
-__device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, Walk& k, int* status) {
-    if (kSide == kJoined && run.whole) return walk_whole(a, k, blockIdx.x, status);
+__device__ __forceinline__ bool walk_start(const Args<kSide>& a, const Run& run, Walk& k, int* status) {
+    if constexpr (kSide == kJoined)
+        if (run.whole) return walk_whole(a, k, blockIdx.x, status);
     if (run.begin >= run.end) return false;
     k.b = run.b;
     k.w = run.w;
@@ -308,7 +310,7 @@ __device__ __forceinline__ int tile_token(int m) { return m ^ ((m >> 1) & 1); }
 
 template <int kD, int kDtype, int kNT, Side kSide>
 __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm / 2)
-    window_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
+    window_kernel(const Args<kSide> a, float* scratch, unsigned* arrivals, int* status) {
     constexpr int kW = kD / 32;              // words of a key row that a lane loads
     constexpr int kVW = kD / 64;             // words of a value row that a lane loads
     constexpr int kRows = 8 * kNT;
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
     // a piece's first steps, on their way before the piece before it is merged
     auto begin = [&]() {
         u1 = k.u1, kv = k.w.kv;
-        pages = a.table + static_cast<int64_t>(kSide == kPrefix ? k.b / a.subs : k.b) * a.width;
+        pages = a.table + static_cast<int64_t>(table_row(a, k.b)) * a.width;
         head_codes = a.c.codes + l16 * 16 + static_cast<int64_t>(k.h) * a.c.block_size * (kD / 2);
         head_scales = reinterpret_cast<const unsigned char*>(a.c.scales) + static_cast<int64_t>((l16 >> 2) * to_values + k.h * a.c.block_size) * 4 + (l16 & 3) * 16;
         const int u0 = k.u0;
@@ -749,8 +751,10 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
                 const int r = nt * 8 + 2 * tq + e;
                 const int64_t at = static_cast<int64_t>(done.w.begin + r / group) * a.q_heads + done.h * group + r % group;
                 if (r >= rows || !HC_IN_RANGE(at, 1, static_cast<size_t>(a.tokens) * a.q_heads, status)) continue;
-                p[e].stats = partial_stats(a, kD)[at];
-                p[e].value = *reinterpret_cast<const float2*>(a.partial + at * kD + g * (kD / 8) + 2 * m);
+                if constexpr (kSide == kJoined) {
+                    p[e].stats = partial_stats(a, kD)[at];
+                    p[e].value = *reinterpret_cast<const float2*>(a.partial + at * kD + g * (kD / 8) + 2 * m);
+                }
             }
         };
         if (kSide == kJoined && whole) {
@@ -905,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
 }
 
 template <int kD, int kDtype, int kNT, Side kSide>
-cudaError_t launch_window(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+cudaError_t launch_window(const Ctx& ctx, const Args<kSide>& a, cudaStream_t st) {
     // as many CTAs as are resident at once, and no more than there can be units
     const int64_t most = static_cast<int64_t>(a.requests) * a.c.kv_heads *
                          (kShort ? 1 : (static_cast<int64_t>(a.width) * a.c.block_size + kUnit - 1) / kUnit);
@@ -916,7 +920,7 @@ cudaError_t launch_window(const Ctx& ctx, const AttentionArgs& a, cudaStream_t s
 }
 
 template <int kD, int kDtype, Side kSide>
-cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+cudaError_t launch_rows(const Ctx& ctx, const Args<kSide>& a, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads);
     if (rows <= 8) return launch_window<kD, kDtype, 1, kSide>(ctx, a, st);
     return launch_window<kD, kDtype, 2, kSide>(ctx, a, st);
@@ -944,7 +948,7 @@ cudaError_t attention_window_setup() {
 }
 
 template <Side kSide>
-cudaError_t launch_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_attention(const Ctx& ctx, const Args<kSide>& a, int dtype, cudaStream_t st) {
     if (static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) > kMaxRows)
         return launch_attention_chunk<kSide>(ctx, a, dtype, st);
     if (a.c.head_dim == 64)

@@ -114,13 +114,13 @@ __device__ __forceinline__ int row_tiles(const Window& w, int group, int step) {
     return (w.rows * group + step - 1) / step;
 }
 template <Side kSide>
-__device__ __forceinline__ int key_tiles(const AttentionArgs& a, const Window& w, int group, int step, int i) {
+__device__ __forceinline__ int key_tiles(const Args<kSide>& a, const Window& w, int group, int step, int i) {
     const int last = min(((i + 1) * step - 1) / group, w.rows - 1);
     const int seen = kSide == kPrefix || a.mask ? w.kv : min(w.kv, w.first + last + 1);
     return max((seen - 1) / kTile + 1, 1);     // (seen may be 2^31 - 1)
 }
 template <Side kSide>
-__device__ __forceinline__ int64_t head_slots(const AttentionArgs& a, const Window& w, int group, int step) {
+__device__ __forceinline__ int64_t head_slots(const Args<kSide>& a, const Window& w, int group, int step) {
     int64_t n = 0;
     for (int i = row_tiles(w, group, step) - 1; i >= 0; --i) n += key_tiles<kSide>(a, w, group, step, i) + kPieceCost;
     return n;
@@ -135,14 +135,14 @@ __device__ __forceinline__ bool walk_piece(Walk& k, int from) {
 }
 
 template <Side kSide>
-__device__ __forceinline__ void walk_row_tile(const AttentionArgs& a, Walk& k, int group, int step, int i) {
+__device__ __forceinline__ void walk_row_tile(const Args<kSide>& a, Walk& k, int group, int step, int i) {
     k.row0 = i * step;
     k.rows = min(k.w.rows * group - k.row0, step);
     k.tiles = key_tiles<kSide>(a, k.w, group, step, i);
 }
 
 template <Side kSide>
-__device__ __forceinline__ bool walk_next(const AttentionArgs& a, Walk& k, int group, int step) {
+__device__ __forceinline__ bool walk_next(const Args<kSide>& a, Walk& k, int group, int step) {
     if (k.left == 0) return false;
     k.base += k.tiles + kPieceCost;
     int i = k.row0 / step + 1;
@@ -167,7 +167,7 @@ struct Run {
 };
 
 template <Side kSide>
-__device__ void find_run(const AttentionArgs& a, int group, int step, Run* run, int64_t* sums, int* status) {
+__device__ void find_run(const Args<kSide>& a, int group, int step, Run* run, int64_t* sums, int* status) {
     const int tid = threadIdx.x;
     const int per = (a.requests + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
@@ -212,7 +212,7 @@ __device__ void find_run(const AttentionArgs& a, int group, int step, Run* run, 
 }
 
 template <Side kSide>
-__device__ __forceinline__ bool walk_start(const AttentionArgs& a, const Run& run, int group, int step, Walk& k) {
+__device__ __forceinline__ bool walk_start(const Args<kSide>& a, const Run& run, int group, int step, Walk& k) {
     if (run.begin >= run.end) return false;
     k.b = run.b;
     k.w = load_window<kSide>(a, k.b, nullptr);
@@ -313,7 +313,7 @@ __device__ __forceinline__ void scale_word(uint32_t (&h)[4], __half2 s, __half2 
 // kSame: both warpgroups have the same rows.
 template <int kD, int kDtype, bool kSame, Side kSide>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const AttentionArgs a, float* scratch, unsigned* arrivals, int* status) {
+    chunk_kernel(const Args<kSide> a, float* scratch, unsigned* arrivals, int* status) {
     pdl_wait();                                // also before tensor memory is taken, which the kernel before may hold
     using S = Smem<kD>;
     constexpr bool same = kSame;
@@ -789,9 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (writes) {
                 float inv = total == 0.f ? 0.f : 1.f / total, by_prefix = 0.f, lse = 0.f;
-                if (kSide == kJoined && whole && here) {
-                    const Join j = join_parts_of_row(peak, total, partial_stats(a, kD)[at]);
-                    inv = j.by_own, by_prefix = j.by_prefix, lse = j.lse;
+                if constexpr (kSide == kJoined) {
+                    if (whole && here) {
+                        const Join j = join_parts_of_row(peak, total, partial_stats(a, kD)[at]);
+                        inv = j.by_own, by_prefix = j.by_prefix, lse = j.lse;
+                    }
                 }
 #pragma unroll 1
                 for (int c = 0; c < kD / 32; ++c) {
@@ -826,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 if (whole) {
-                    if (kSide == kPrefix) {
+                    if constexpr (kSide == kPrefix) {
                         if (here) partial_stats(a, kD)[at] = make_float2(peak, total);
                     } else if (here && a.lse) {
                         a.lse[at] = kSide == kJoined ? lse : total == 0.f ? -CUDART_INF_F : (peak + log2f(total)) * kLn2;
@@ -1166,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // `step` are the chunk kernel's.
 constexpr int kJoinRows = 8;
 template <int kD>
-__global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const AttentionArgs a, const float* scratch, int ctas, int step, int* status) {
+__global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const SharedArgs a, const float* scratch, int ctas, int step, int* status) {
     begin_early();
     extern __shared__ float2 stats[];                          // [pieces][kJoinRows]
     __shared__ Window window;
@@ -1248,7 +1250,7 @@ __global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const Attentio
 }
 
 template <int kD>
-cudaError_t launch_join(const Ctx& ctx, const AttentionArgs& a, int step, cudaStream_t st) {
+cudaError_t launch_join(const Ctx& ctx, const SharedArgs& a, int step, cudaStream_t st) {
     // as many numbers as there can be
     const int64_t rows = static_cast<int64_t>(a.tokens) * (a.q_heads / a.c.kv_heads);
     const int64_t most = (rows / kJoinRows + a.requests) * a.c.kv_heads;
@@ -1258,13 +1260,13 @@ cudaError_t launch_join(const Ctx& ctx, const AttentionArgs& a, int step, cudaSt
 }
 
 template <int kD, int kDtype, bool kSame, Side kSide>
-cudaError_t launch_chunk(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+cudaError_t launch_chunk(const Ctx& ctx, const Args<kSide>& a, cudaStream_t st) {
     return launch_early(chunk_kernel<kD, kDtype, kSame, kSide>, dim3(ctx.sm_count), kThreads, Smem<kD>::kBytes, st, a, ctx.attn_pieces,
                         ctx.attn_arrivals, ctx.s.status);
 }
 
 template <int kD, int kDtype, Side kSide>
-cudaError_t launch_rows(const Ctx& ctx, const AttentionArgs& a, cudaStream_t st) {
+cudaError_t launch_rows(const Ctx& ctx, const Args<kSide>& a, cudaStream_t st) {
     const bool same = static_cast<int64_t>(a.max_new) * (a.q_heads / a.c.kv_heads) <= kTile;
     const cudaError_t e = same ? launch_chunk<kD, kDtype, true, kSide>(ctx, a, st) : launch_chunk<kD, kDtype, false, kSide>(ctx, a, st);
     if constexpr (kSide == kPrefix) return e != cudaSuccess ? e : launch_join<kD>(ctx, a, same ? kTile : 2 * kTile, st);
@@ -1300,7 +1302,7 @@ cudaError_t attention_chunk_setup() {
 }
 
 template <Side kSide>
-cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_attention_chunk(const Ctx& ctx, const Args<kSide>& a, int dtype, cudaStream_t st) {
     if (a.c.head_dim == 64)
         return dtype == HC_DTYPE_BF16 ? launch_rows<64, HC_DTYPE_BF16, kSide>(ctx, a, st) : launch_rows<64, HC_DTYPE_FP16, kSide>(ctx, a, st);
     return dtype == HC_DTYPE_BF16 ? launch_rows<128, HC_DTYPE_BF16, kSide>(ctx, a, st) : launch_rows<128, HC_DTYPE_FP16, kSide>(ctx, a, st);

@@ -3,7 +3,7 @@
 
 namespace hc {
 
-template cudaError_t launch_attention_chunk<kPrefix>(const Ctx&, const AttentionArgs&, int, cudaStream_t);
+template cudaError_t launch_attention_chunk<kPrefix>(const Ctx&, const SharedArgs&, int, cudaStream_t);
 template cudaError_t attention_chunk_setup<kPrefix>();
 
 }  // namespace hc

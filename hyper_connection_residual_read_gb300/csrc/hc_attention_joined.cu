@@ -3,7 +3,7 @@
 
 namespace hc {
 
-template cudaError_t launch_attention<kJoined>(const Ctx&, const AttentionArgs&, int, cudaStream_t);
+template cudaError_t launch_attention<kJoined>(const Ctx&, const SharedArgs&, int, cudaStream_t);
 template cudaError_t attention_window_setup<kJoined>();
 
 }  // namespace hc

@@ -13,7 +13,7 @@ cudaError_t attention_short_setup() {
     return e;
 }
 
-cudaError_t launch_attention_short(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_attention_short(const Ctx& ctx, const SharedArgs& a, int dtype, cudaStream_t st) {
     if (a.c.head_dim == 64)
         return dtype == HC_DTYPE_BF16 ? launch_rows<64, HC_DTYPE_BF16, kJoined>(ctx, a, st) : launch_rows<64, HC_DTYPE_FP16, kJoined>(ctx, a, st);
     return dtype == HC_DTYPE_BF16 ? launch_rows<128, HC_DTYPE_BF16, kJoined>(ctx, a, st) : launch_rows<128, HC_DTYPE_FP16, kJoined>(ctx, a, st);

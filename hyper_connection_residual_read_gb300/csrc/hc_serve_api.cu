@@ -104,13 +104,13 @@ extern "C" int hc_kv4_attention_shared(const hc_kv4_cache* cache, int requests, 
                       {mask, mask ? 8ull * tokens : 0}};
     if (any_meet(s, 3, 13)) return HC_ERR_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const AttentionArgs prefix{*cache, groups, tokens, q_heads, max_shared, prefix_width, scale, q,
-                               q_token_stride, q_head_stride, cu_lens, prefix_lens, prefix_table, nullptr,
-                               nullptr, nullptr, cu_groups, requests, 1, max_shared, workspace};
+    const SharedArgs prefix{{*cache, groups, tokens, q_heads, max_shared, prefix_width, scale, q, q_token_stride,
+                             q_head_stride, cu_lens, prefix_lens, prefix_table, nullptr, nullptr, nullptr},
+                            cu_groups, requests, 1, max_shared, workspace};
     if (launch_kv4_attention_prefix(*c, prefix, dtype, st) != cudaSuccess) return HC_ERR_CUDA;
-    const AttentionArgs own{*cache, requests, tokens, q_heads, max_new, table_width, scale, q,
-                            q_token_stride, q_head_stride, cu_lens, kv_lens, block_table, mask, out, lse,
-                            nullptr, 0, 1, 0, workspace};
+    const SharedArgs own{{*cache, requests, tokens, q_heads, max_new, table_width, scale, q, q_token_stride,
+                          q_head_stride, cu_lens, kv_lens, block_table, mask, out, lse},
+                         nullptr, 0, 1, 0, workspace};
     return launch_kv4_attention_joined(*c, own, dtype, st) == cudaSuccess ? HC_OK : HC_ERR_CUDA;
 }
 

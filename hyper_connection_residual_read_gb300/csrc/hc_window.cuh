@@ -5,6 +5,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hc_common.cuh"
 #include "hc_tc.cuh"
 #include "hc_window_internal.h"
@@ -29,7 +31,11 @@ __device__ __forceinline__ size_t group_count(const hc_kv4_cache& c) {
 __device__ __forceinline__ size_t row_extent(int tokens, int heads, int dim, int64_t token, int64_t head) {
     return static_cast<size_t>(tokens - 1) * token + static_cast<size_t>(heads - 1) * head + dim;
 }
-__device__ __forceinline__ size_t table_extent(const AttentionArgs& a) { return static_cast<size_t>(a.requests / a.subs) * a.width; }
+__device__ __forceinline__ size_t table_extent(const AttentionArgs& a) { return static_cast<size_t>(a.requests) * a.width; }
+__device__ __forceinline__ size_t table_extent(const SharedArgs& a) { return static_cast<size_t>(a.requests / a.subs) * a.width; }
+// The table's row of a request, or of a share of a group.
+__device__ __forceinline__ int table_row(const AttentionArgs&, int b) { return b; }
+__device__ __forceinline__ int table_row(const SharedArgs& a, int b) { return b / a.subs; }
 
 // The window of one request, with what does not fit its arrays cut off and reported. (That kv
 // fits the request's row of the table is what the kernels' lookups there rely on.)
@@ -46,12 +52,15 @@ struct Window {
 enum Side { kOwn, kPrefix, kJoined };
 
 template <Side kSide>
-__device__ __forceinline__ Window load_window(const AttentionArgs& a, int b, int* status) {
+using Args = typename std::conditional<kSide == kOwn, AttentionArgs, SharedArgs>::type;
+
+template <Side kSide>
+__device__ __forceinline__ Window load_window(const Args<kSide>& a, int b, int* status) {
     Window w = {};
     if (!HC_IN_RANGE(b, 1, a.requests, status)) return w;
     int at = b, to = b + 1, of = b;
     bool none = false;
-    if (kSide == kPrefix) {
+    if constexpr (kSide == kPrefix) {
         of = b / a.subs;
         at = a.groups[of], to = a.groups[of + 1];
         none = at < 0 || to < at || to > a.members;
@@ -62,8 +71,9 @@ __device__ __forceinline__ Window load_window(const AttentionArgs& a, int b, int
     const bool bad = none || lo < 0 || hi < lo || hi > a.tokens;
     w.begin = bad ? 0 : lo;
     w.n = bad ? 0 : hi - lo;
-    const bool more = w.n > (kSide == kPrefix ? a.shared : a.max_new);
-    if (kSide == kPrefix) {                    // this share of the group's tokens
+    bool more = w.n > a.max_new;
+    if constexpr (kSide == kPrefix) {          // this share of the group's tokens
+        more = w.n > a.shared;
         const int skip = static_cast<int>(min(static_cast<int64_t>(b % a.subs) * a.max_new, static_cast<int64_t>(w.n)));
         w.begin += skip, w.n -= skip;
         if (a.subs > 1) w.n = min(w.n, a.max_new);
@@ -193,7 +203,7 @@ __device__ __forceinline__ int query_exponent(float top) {
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // A prefix's part of a row in the workspace: where its (maximum, sum) lie, behind all rows' values.
-__device__ __forceinline__ float2* partial_stats(const AttentionArgs& a, int dim) {
+__device__ __forceinline__ float2* partial_stats(const SharedArgs& a, int dim) {
     return reinterpret_cast<float2*>(a.partial + static_cast<int64_t>(a.tokens) * a.q_heads * dim);
 }
 // A row's own part, sums x about 2^peak with the weights' sum `total`, joined with the prefix's,
@@ -223,16 +233,16 @@ __device__ __forceinline__ void copy_wait() {
 
 // Launches by part (hc_attention.cuh; hc_attention_chunk.cuh: more than 16 rows).
 template <Side kSide>
-cudaError_t launch_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_attention(const Ctx& ctx, const Args<kSide>& a, int dtype, cudaStream_t st);
 template <Side kSide>
 cudaError_t attention_window_setup();
 template <Side kSide>
-cudaError_t launch_attention_chunk(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_attention_chunk(const Ctx& ctx, const Args<kSide>& a, int dtype, cudaStream_t st);
 template <Side kSide>
 cudaError_t attention_chunk_setup();
 size_t attention_chunk_scratch_floats(int sm_count);
 // Own parts behind a prefix, of short requests with few rows (hc_attention_short.cu).
-cudaError_t launch_attention_short(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_attention_short(const Ctx& ctx, const SharedArgs& a, int dtype, cudaStream_t st);
 cudaError_t attention_short_setup();
 
 }  // namespace hc

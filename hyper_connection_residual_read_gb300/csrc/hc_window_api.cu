@@ -127,8 +127,7 @@ extern "C" int hc_kv4_attention(const hc_kv4_cache* cache, int requests, int tok
                       {mask, mask ? 8ull * tokens : 0}};
     if (any_meet(s, 2, 9)) return HC_ERR_ARG;
     const AttentionArgs a{*cache, requests, tokens, q_heads, max_new, table_width, scale, q,
-                          q_token_stride, q_head_stride, cu_lens, kv_lens, block_table, mask, out, lse,
-                          nullptr, 0, 1, 0, nullptr};
+                          q_token_stride, q_head_stride, cu_lens, kv_lens, block_table, mask, out, lse};
     return launch_kv4_attention(*c, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HC_OK : HC_ERR_CUDA;
 }
 
