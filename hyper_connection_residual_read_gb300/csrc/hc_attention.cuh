@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int group = a.q_heads / a.c.kv_heads;
 
-    begin_early();
+    // The own part behind a prefix runs beside the kernel that ends the prefix, which began after all that
+    // this one reads was written; it waits for it where it first touches what the two have in common.
+    if (kSide != kJoined) begin_early();
     const Run run = find_run<kSide>(a, &shared_run, sums, status);
     // The walk, a copy a warp, kept here and not in registers, which the loop over the steps has
     // none to spare of.
@@ -336,7 +338,10 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
     };
     {
         Walk first;
-        if (!walk_start<kSide>(a, run, first, kShort ? status : nullptr)) return;
+        if (!walk_start<kSide>(a, run, first, kShort ? status : nullptr)) {
+            if (kSide == kJoined) begin_early();             // (who waits for this kernel waits for the one before)
+            return;
+        }
         keep(first);
     }
 
@@ -709,6 +714,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
             }
         }
 
+        if (kSide == kJoined) begin_early();     // the workspace, scratch and counters are free, the prefix's part is there
+
         // ---- merge the warps: their fragments lie alike, so that unit m of 4 values a lane
         // is exchanged through [warp][lane] and summed by warp m % 8: one after the other through
         // two buffers, or, after the last piece, all at once through the ring (2 us
@@ -752,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : kCtasPerSm /
                 const int64_t at = static_cast<int64_t>(done.w.begin + r / group) * a.q_heads + done.h * group + r % group;
                 if (r >= rows || !HC_IN_RANGE(at, 1, static_cast<size_t>(a.tokens) * a.q_heads, status)) continue;
                 if constexpr (kSide == kJoined) {
-                    p[e].stats = partial_stats(a, kD)[at];
-                    p[e].value = *reinterpret_cast<const float2*>(a.partial + at * kD + g * (kD / 8) + 2 * m);
+                    p[e].stats = __ldcg(partial_stats(a, kD) + at);
+                    p[e].value = __ldcg(reinterpret_cast<const float2*>(a.partial + at * kD + g * (kD / 8) + 2 * m));
                 }
             }
         };

@@ -314,7 +314,11 @@ __device__ __forceinline__ void scale_word(uint32_t (&h)[4], __half2 s, __half2 
 template <int kD, int kDtype, bool kSame, Side kSide>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const Args<kSide> a, float* scratch, unsigned* arrivals, int* status) {
-    pdl_wait();                                // also before tensor memory is taken, which the kernel before may hold
+    // also before tensor memory is taken, which the kernel before may hold. (Not so the own part behind a prefix:
+    // the kernel before it, which ends the prefix and has none, began after all that this one reads was written
+    // and after tensor memory was given back. It waits where it first touches what the two have in common.)
+    if (kSide != kJoined) pdl_wait();
+    if (kSide == kPrefix) pdl_launch_dependents();
     using S = Smem<kD>;
     constexpr bool same = kSame;
     // registers of a softmax thread and of a decoding one, 512 in all for two of each
@@ -736,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             o_phase += done_tiles;
             if (fresh && sum == sum) base = -CUDART_INF_F;     // (a sum of NaN alone has to be told, about 0)
+            if (kSide == kJoined) pdl_wait();                  // scratch and counters are free, the prefix's part is there
             const bool whole = k.t0 == 0 && k.t1 == k.tiles;
             float other_base = -CUDART_INF_F, other_sum = 0.f;
             float* exchange = reinterpret_cast<float*>(smem + S::kQ);          // [kD][128], both row tiles' room
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float inv = total == 0.f ? 0.f : 1.f / total, by_prefix = 0.f, lse = 0.f;
                 if constexpr (kSide == kJoined) {
                     if (whole && here) {
-                        const Join j = join_parts_of_row(peak, total, partial_stats(a, kD)[at]);
+                        const Join j = join_parts_of_row(peak, total, __ldcg(partial_stats(a, kD) + at));
                         inv = j.by_own, by_prefix = j.by_prefix, lse = j.lse;
                     }
                 }
@@ -811,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float4* prefix = reinterpret_cast<const float4*>(a.partial + at * kD + c * 32);
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
-                                const float4 y = prefix[n];
+                                const float4 y = __ldcg(prefix + n);
                                 o[4 * n] = fmaf(o[4 * n], inv, y.x * by_prefix), o[4 * n + 1] = fmaf(o[4 * n + 1], inv, y.y * by_prefix);
                                 o[4 * n + 2] = fmaf(o[4 * n + 2], inv, y.z * by_prefix), o[4 * n + 3] = fmaf(o[4 * n + 3], inv, y.w * by_prefix);
                             }
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         joined[wg][row] = make_float2(top, all == 0.f ? 0.f : 1.f / all);
                         float lse = all == 0.f ? -CUDART_INF_F : (top + log2f(all)) * kLn2;
                         if constexpr (kSide == kJoined) {
-                            const Join j = join_parts_of_row(top, all, partial_stats(a, kD)[at]);
+                            const Join j = join_parts_of_row(top, all, __ldcg(partial_stats(a, kD) + at));
                             joined[wg][row].y = j.by_own, lse = j.lse;
                             by_prefix[wg][row] = j.by_prefix;
                         }
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int64_t put = to + (x * kQuads + q) * 4;
                             float4 y = make_float4(o[x].x * join.y, o[x].y * join.y, o[x].z * join.y, o[x].w * join.y);
                             if constexpr (kSide == kJoined) {
-                                const float4 prefix = *reinterpret_cast<const float4*>(a.partial + put);
+                                const float4 prefix = __ldcg(reinterpret_cast<const float4*>(a.partial + put));
                                 const float by = by_prefix[wg][r];
                                 y.x = fmaf(prefix.x, by, y.x), y.y = fmaf(prefix.y, by, y.y);
                                 y.z = fmaf(prefix.z, by, y.z), y.w = fmaf(prefix.w, by, y.w);
@@ -1156,6 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             advance(4 + is_v);
         }
     }
+    if (kSide == kJoined) pdl_wait();          // (who waits for this kernel waits for the one before)
     __syncthreads();
     if (warp == 0) {
         tc::tc_fence_after();
@@ -1169,7 +1175,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinRows = 8;
 template <int kD>
 __global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const SharedArgs a, const float* scratch, int ctas, int step, int* status) {
-    begin_early();
     extern __shared__ float2 stats[];                          // [pieces][kJoinRows]
     __shared__ Window window;
     __shared__ int64_t base, total;                            // slots before the row tile, and all
@@ -1209,6 +1214,8 @@ __global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const SharedAr
         }
         if (lane == 0) total = slots;
     }
+    // (the chunk kernel before began after all lengths were written; the kernel behind may begin once it has ended)
+    begin_early();
     __syncthreads();
     if (row0 < 0) return;
     const int tiles = key_tiles<kPrefix>(a, window, group, step, 0);
