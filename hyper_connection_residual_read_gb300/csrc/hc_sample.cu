@@ -4,10 +4,11 @@
 // same in any order: which token a uniform number falls on, and where a filter cuts, are decided
 // by comparing whole numbers.
 //
-// exp((x - M) / T) = 2^z. 128 z = x c - M c, c = 128 log2(e) / T, is cut into a whole number m and a
+// exp((x - M) / T) = 2^z. 32 z = x c - M c, c = 32 log2(e) / T, is cut into a whole number m and a
 // rest g by one fma that rounds x c to a whole number and a second that leaves what that lacks: 2^z =
-// 2^(m / 128) (1 + p(g)), the first from a table of 59 bits, p by its series to the fourth power
-// (2^-38), held to 2^-30. c and M c are two floats each. In all 2^-28 of a weight.
+// 2^(m / 32) (1 + p(g)), the first from a table of 32 bits (32 words: no two lanes that look up different ones
+// meet on a bank), p by its series to the fourth power (2^-34), held to 2^-28. c and M c are two floats each. In
+// all 2^-27 of a weight.
 //
 // A row belongs to a cluster of CTAs, which hold it in their shared memory: it is read once. What
 // the filters leave is found in steps that look at less and less of it:
@@ -49,40 +50,18 @@ constexpr int kShort = 1408;                 // logits of a list that one CTA ta
 constexpr int kUnitBits = 45;
 constexpr uint64_t kOne = 1ull << kUnitBits;
 constexpr int kMaxCtas = 8;                  // of a cluster
-constexpr int kSteps = 128;                  // of the table, an octave
+constexpr int kSteps = 32;                   // of the table, an octave
 constexpr float kRound = 12582912.f;         // 1.5 2^23
 constexpr float kDeep = -46.5f;              // log2 of weights that are 0
 constexpr float kTop = 3.402823466e38f;
 static_assert(HC_SAMPLE_MAX_VOCAB <= kMaxCtas * 32768);
 
-// 2^(j / 128) 2^59
-__constant__ uint64_t kPowers[kSteps] = {
-    0x800000000000000ull, 0x80B1ED4FD999AB7ull, 0x8164D1F3BC03077ull, 0x8218AF4373FC25Full, 0x82CD8698AC2BA1Dull,
-    0x8383594EEFB6EE3ull, 0x843A28C3ACDE404ull, 0x84F1F656379C1A3ull, 0x85AAC367CC487B1ull, 0x8664915B923FBA0ull,
-    0x871F61969E8D101ull, 0x87DB357FF698D79ull, 0x88980E8092DA852ull, 0x8955EE03618E5FEull, 0x8A14D575496EFDAull,
-    0x8AD4C6452C72892ull, 0x8B95C1E3EA8BD6Eull, 0x8C57C9C4646F4DEull, 0x8D1ADF5B7E5BA9Eull, 0x8DDF042022E69CDull,
-    0x8EA4398B45CD53Cull, 0x8F6A8117E6C8E5Cull, 0x9031DC431466B1Eull, 0x90FA4C8BEEE4B13ull, 0x91C3D373AB11C33ull,
-    0x928E727D9531F9Bull, 0x935A2B2F13E6E93ull, 0x9426FF0FAB1C04Bull, 0x94F4EFA8FEF7096ull, 0x95C3FE86D6CC7FFull,
-    0x96942D3720185A0ull, 0x97657D49F17AB09ull, 0x9837F0518DB8A97ull, 0x990B87E266C189Bull, 0x99E0459320B7FA6ull,
-    0x9AB62AFC94FF865ull, 0x9B8D39B9D54E554ull, 0x9C6573682EC32C3ull, 0x9D3ED9A72CFFB75ull, 0x9E196E189D47242ull,
-    0x9EF5326091A111Bull, 0x9FD228256400DD0ull, 0xA0B0510FB9714FCull, 0xA18FAECA8544B6Eull, 0xA27043030C49682ull,
-    0xA3520F68E802BB9ull, 0xA43515AE09E680Aull, 0xA5195786BE9EF34ull, 0xA5FED6A9B15138Full, 0xA6E594CFEEE86B2ull,
-    0xA7CD93B4E965357ull, 0xA8B6D5167B320E1ull, 0xA9A15AB4EA7C0F0ull, 0xAA8D2652EC90763ull, 0xAB7A39B5A93ED33ull,
-    0xAC6896A4BE3FE93ull, 0xAD583EEA42A14ACull, 0xAE493452CA35B81ull, 0xAF3B78AD690A437ull, 0xB02F0DCBB6E0458ull,
-    0xB123F581D2AC259ull, 0xB21A31A66618FE4ull, 0xB311C412A911249ull, 0xB40AAEA2654B984ull, 0xB504F333F9DE648ull,
-    0xB60093A85ED5F77ull, 0xB6FD91E328D1779ull, 0xB7FBEFCA8CA41E8ull, 0xB8FBAF4762FB9EFull, 0xB9FCD2452C0B9DFull,
-    0xBAFF5AB2133E460ull, 0xBC034A7EF2E9FB1ull, 0xBD08A39F580C36Cull, 0xBE0F6809860993Eull, 0xBF1799B67A73108ull,
-    0xC0213AA1F0D08DBull, 0xC12C4CCA6670945ull, 0xC238D2311E3D667ull, 0xC346CCDA2497640ull, 0xC4563ECC5334CB3ull,
-    0xC5672A115506DAEull, 0xC67990B5AA245F8ull, 0xC78D74C8ABB9B16ull, 0xC8A2D85C8FFE2C4ull, 0xC9B9BD866E2F27Aull,
-    0xCAD2265E4290775ull, 0xCBEC14FEF2727C6ull, 0xCD078B86503DCDDull, 0xCE248C151F8480Eull, 0xCF4318CF191918Cull,
-    0xD06333DAEF2B259ull, 0xD184DF6251699ACull, 0xD2A81D91F12AE46ull, 0xD3CCF099859AC38ull, 0xD4F35AABCFEDFA2ull,
-    0xD61B5DFE9F9BCE0ull, 0xD744FCCAD69D6AFull, 0xD870394C6DB32C8ull, 0xD99D15C278AFD7Bull, 0xDACB946F2AC9CC7ull,
-    0xDBFBB797DAF2375ull, 0xDD2D818508324C2ull, 0xDE60F4825E0E912ull, 0xDF9612DEB8F0442ull, 0xE0CCDEEC2A94E11ull,
-    0xE2055AFFFE83D37ull, 0xE33F8972BE8A5A5ull, 0xE47B6CA0373DA89ull, 0xE5B906E77C8348Bull, 0xE6F85AAAEE1FCE2ull,
-    0xE8396A503C4BDC7ull, 0xE97C38406C4F8C5ull, 0xEAC0C6E7DD24393ull, 0xEC0718B64C1CBDEull, 0xED4F301ED9942B8ull,
-    0xEE990F980DA3026ull, 0xEFE4B99BDCDAF5Dull, 0xF13230A7AD09451ull, 0xF281773C59FFB14ull, 0xF3D28FDE3A641A6ull,
-    0xF5257D152486CC3ull, 0xF67A416C733F847ull, 0xF7D0DF730AD13BCull, 0xF92959BB5DD4BA7ull, 0xFA83B2DB722A034ull,
-    0xFBDFED6CE5F09C5ull, 0xFD3E0C0CF486C17ull, 0xFE9E115C7B8F885ull,
+// 2^(j / 32) 2^31
+__constant__ uint32_t kPowers[kSteps] = {
+    0x80000000u, 0x82CD8699u, 0x85AAC368u, 0x88980E81u, 0x8B95C1E4u, 0x8EA4398Bu, 0x91C3D374u, 0x94F4EFA9u,
+    0x9837F052u, 0x9B8D39BAu, 0x9EF53261u, 0xA2704303u, 0xA5FED6AAu, 0xA9A15AB5u, 0xAD583EEAu, 0xB123F582u,
+    0xB504F334u, 0xB8FBAF47u, 0xBD08A39Fu, 0xC12C4CCAu, 0xC5672A11u, 0xC9B9BD86u, 0xCE248C15u, 0xD2A81D92u,
+    0xD744FCCBu, 0xDBFBB798u, 0xE0CCDEECu, 0xE5B906E7u, 0xEAC0C6E8u, 0xEFE4B99Cu, 0xF5257D15u, 0xFA83B2DBu,
 };
 
 // Logits in shared memory.
@@ -113,7 +92,7 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 struct Heat {
     float c, c_low, a, rest;                 // c in two floats; 1.5 2^23 - rint(M c); what makes g(M) 0
     float top, deep;                         // M; the logit below which weights are 0
-    float z, z_low;                          // c / 128 (for the slow way)
+    float z, z_low;                          // c / 32 (for the slow way)
     bool far;                                // M c is beyond what a rounds well
 };
 // (In fp32 alone: 64-bit operations took 15 us of a row's 40.)
@@ -131,7 +110,7 @@ __device__ __forceinline__ Heat heat_of(float t, float top) {
     h.rest = fmaf(-h.c_low, top, -fmaf(top, h.c, -whole));
     h.top = top;
     h.deep = fmaxf(fmaf(t, kDeep * kLn2, top), -kTop);                   // never -inf
-    h.far = !(fabsf(at) < 4000000.f);
+    h.far = !(fabsf(at) < 1000000.f);
     return h;
 }
 
@@ -147,18 +126,18 @@ __device__ __forceinline__ uint64_t part_of(uint64_t x, float by, bool up) {
     return r + (up && rest != 0);
 }
 
-// 2^((m + g) / 128) in multiples of 2^-45, -47 128 <= m <= 1, of `bits` = m + the pattern of kRound and
-// `part` = 2^29 p(g) + that pattern.
-__device__ __forceinline__ uint64_t power(int bits, int part, const uint64_t* powers) {
-    constexpr int kPattern = 0x4B400000;
-    const uint64_t t = powers[bits & (kSteps - 1)];
-    const uint64_t w = t + static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(t >> 29)) * (part - kPattern));     // 2^30 2^29
-    return w >> (59 - kUnitBits + (kPattern >> 7) - (bits >> 7));
+// 2^((m + g) / 32) in multiples of 2^-45, -47 32 <= m <= 1, of `bits` = m + the pattern of kRound and
+// `part` = 2^27 p(g) + that pattern.
+__device__ __forceinline__ uint64_t power(int bits, int part, const uint32_t* powers) {
+    constexpr int kPattern = 0x4B400000, kStepBits = 5;
+    static_assert(kSteps == 1 << kStepBits);
+    const uint64_t w = static_cast<uint64_t>(powers[bits & (kSteps - 1)]) * static_cast<uint32_t>(part - kPattern + (1 << 27));     // 2^31 2^27
+    return w >> (58 - kUnitBits + (kPattern >> kStepBits) - (bits >> kStepBits));
 }
-// p(g) = 2^(g / 128) - 1 in multiples of 2^-29, behind kRound: (g l) + (g l)^2 / 2 + ..., l = ln 2 / 128; |g| <= 1.2
-constexpr float kP1 = 5.4152123481e-03f, kP2 = 1.4662262388e-05f, kP3 = 2.6466421444e-08f, kP4 = 3.5830323054e-11f, kPart = 536870912.f;
+// p(g) = 2^(g / 32) - 1 in multiples of 2^-27, behind kRound: (g l) + (g l)^2 / 2 + ..., l = ln 2 / 32; |g| <= 1.2, |p| < 2^-5
+constexpr float kP1 = 2.1660849392e-2f, kP2 = 2.3459619820e-4f, kP3 = 1.6938509724e-6f, kP4 = 9.1725627018e-9f, kPart = 134217728.f;
 // The weights of two logits, 0 below h.deep. Two fp32 operations in one instruction.
-__device__ __forceinline__ void weights(float x0, float x1, const Heat& h, const uint64_t* powers, uint64_t& w0, uint64_t& w1) {
+__device__ __forceinline__ void weights(float x0, float x1, const Heat& h, const uint32_t* powers, uint64_t& w0, uint64_t& w1) {
     const uint64_t x = pair(fmaxf(x0, h.deep), fmaxf(x1, h.deep)), c = pair(h.c, h.c), a = pair(h.a, h.a);
     const uint64_t v = fma2(x, c, a);
     const uint64_t g = add2(fma2(x, c, fma2(v, pair(-1.f, -1.f), a)), fma2(x, pair(h.c_low, h.c_low), pair(h.rest, h.rest)));
@@ -168,7 +147,7 @@ __device__ __forceinline__ void weights(float x0, float x1, const Heat& h, const
     w1 = power(__float_as_int(bits.y), __float_as_int(part.y), powers);
 }
 // Where M c is so large that this way loses bits: from the difference to M, in two floats.
-__device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const uint64_t* powers) {
+__device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const uint32_t* powers) {
     const float d = __fsub_rn(x, top), z = __fmul_rn(d, c);
     if (!(z > kDeep)) return 0;
     const float b = __fsub_rn(d, x);
@@ -199,7 +178,7 @@ __device__ __forceinline__ T warp_scan(T x, int lane) {
 
 template <int kDtype>
 struct Shared {
-    uint64_t powers[kSteps];
+    uint32_t powers[kSteps];
     // of a step's bins: their logits, and their weights as sums of each 16 bits of them (shared memory adds
     // 32 bits at a time by itself: three such sums take 8 cycles a warp, one of 64 bits 50 to 570)
     unsigned count[kBins], mass[3][kBins];

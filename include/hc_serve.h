@@ -117,7 +117,7 @@ int hc_kv4_attention_shared(const hc_kv4_cache* cache, int requests, int groups,
  * of -inf has no weight. A row with a NaN or +inf, or of -inf alone, or with a NaN (or an
  * infinity as temperature) among its settings, has token -1 and logprob NaN.
  *
- * Weights are whole multiples of 2^-45, within 2^-29 of w_i (up to e^-24) or the multiple, and their sums
+ * Weights are whole multiples of 2^-45, within 2^-27 of w_i (up to e^-24) or the multiple, and their sums
  * are exact, so that the token does not depend on the order of anything; it is the formula's
  * but where uniform lies as near to a border between two tokens as that, or another weight to
  * the border of a filter. logprob within 2^-20 of 1 + its size.
