@@ -92,16 +92,14 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 struct Heat {
     float c, c_low, a, rest;                 // c in two floats; 1.5 2^23 - rint(M c); what makes g(M) 0
     float top, deep;                         // M; the logit below which weights are 0
-    float z, z_low;                          // c / 32 (for the slow way)
     bool far;                                // M c is beyond what a rounds well
 };
 // (In fp32 alone: 64-bit operations took 15 us of a row's 40.)
 __device__ __forceinline__ Heat heat_of(float t, float top) {
     constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;             // log2(e)
     Heat h;
-    h.z = kHi / t;
-    h.z_low = (fmaf(-h.z, t, kHi) + kLo) / t;
-    h.c = h.z * kSteps, h.c_low = h.z_low * kSteps;
+    const float z = kHi / t, z_low = (fmaf(-z, t, kHi) + kLo) / t;
+    h.c = z * kSteps, h.c_low = z_low * kSteps;
     // M's own weight is 2^45: its m is 0, and so is its g to 2^-25, whose p is held as 0
     const float at = h.c * top;
     float whole = rintf(at);
@@ -124,6 +122,11 @@ __device__ __forceinline__ uint64_t part_of(uint64_t x, float by, bool up) {
     if (down < 64) r = (hi << (64 - down)) | (lo >> down), rest = lo << (64 - down);
     else if (down < 128) r = down == 64 ? hi : hi >> (down - 64), rest = lo | (down == 64 ? 0 : hi << (128 - down));
     return r + (up && rest != 0);
+}
+
+// The least weight that a min-p leaves.
+__device__ __forceinline__ uint64_t least_weight(float least) {
+    return !(least > 0.f) ? 1 : least < 1.f ? max(part_of(kOne, least, true), static_cast<uint64_t>(1)) : kOne;
 }
 
 // 2^((m + g) / 32) in multiples of 2^-45, -47 32 <= m <= 1, of `bits` = m + the pattern of kRound and
@@ -186,6 +189,7 @@ struct Shared {
     alignas(16) uint64_t told_mass[kWarps];
     alignas(16) unsigned told_count[kWarps];
     alignas(16) float told_top[kWarps];
+    float u, p, t, least;                    // the row's settings, for where they are needed again (registers are short)
     // within the CTA
     uint64_t warp_mass[kWarps];
     unsigned warp_count[kWarps];
@@ -268,7 +272,7 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&y)[kDtype == HC_D
 // 131072 13.4 us in bins, @@ so.)
 template <int kDtype, typename Weigh>
 __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs& a, int row, int n, int k, bool by_count, bool by_mass, bool whole,
-                                             uint64_t want, float p, uint64_t low, float u, float t, float top, Weigh& weigh) {
+                                             uint64_t want, float top, Weigh& weigh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // the bins' room is free: values and weights of the list
     float* value = reinterpret_cast<float*>(s.count);
@@ -289,6 +293,7 @@ __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs
         __syncthreads();
         return x;
     };
+    const uint64_t low = least_weight(s.least);
     unsigned rank = 0;
     uint64_t before = 0;
     if (warp * 32 < n) {
@@ -301,8 +306,8 @@ __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs
     }
     bool stays = tid < n && w[0] >= low && (!by_count || rank < static_cast<unsigned>(k));
     if (by_mass) {
-        if (by_count) want = max(part_of(sum_of(tid < n && rank < static_cast<unsigned>(k) ? w[0] : 0), fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
-        else if (whole) want = max(part_of(sum_of(w[0]), fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+        if (by_count) want = max(part_of(sum_of(tid < n && rank < static_cast<unsigned>(k) ? w[0] : 0), fmaxf(s.p, 0.f), true), static_cast<uint64_t>(1));
+        else if (whole) want = max(part_of(sum_of(w[0]), fmaxf(s.p, 0.f), true), static_cast<uint64_t>(1));
         stays = stays && before < want;
     }
     const uint64_t kept = stays ? w[0] : 0;
@@ -314,15 +319,15 @@ __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs
         if (i == warp) upto += total;
         total += s.warp_mass[i];
     }
-    const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
+    const uint64_t goal = s.u < 1.f ? part_of(total, fmaxf(s.u, 0.f), false) : total - 1;
     if (upto > goal && upto - kept <= goal) {
         a.ids[row] = s.id[tid];
-        a.logprob[row] = ((y[0] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
+        a.logprob[row] = ((y[0] - top) / s.t) - logf(static_cast<float>(total) * (1.f / kOne));
     }
 }
 
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a, int ctas, int segment_bytes, int list_room, int* status) {
+__global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sample_kernel(const SampleArgs a, int ctas, int segment_bytes, int list_room, int* status) {
     constexpr int kItem = kDtype == HC_DTYPE_FP32 ? 4 : 2, kN = 16 / kItem;
     using S = Shared<kDtype>;
     __shared__ S s;
@@ -357,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const int k = a.top_k ? a.top_k[row] : 0;
     bool bad = !(u == u && p == p && least == least) || !(fabsf(t) <= kTop);
     for (int i = tid; i < kSteps; i += kThreads) s.powers[i] = kPowers[i];
+    if (tid == 0) s.u = u, s.p = p, s.t = t, s.least = least;
     s.count[tid] = s.mass[0][tid] = s.mass[1][tid] = s.mass[2][tid] = 0, s.id[tid] = 0;
     Most<kDtype> largest;
     const int end = tid == 0 && w0 > 0 ? 0 : tid == 32 && w1 < n_vec && n_vec > w0 ? n_vec - 1 : -1;
@@ -453,34 +459,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         }
     };
     // and their weights, 0 for those at -inf
-    auto weigh = [&](const float (&y)[4], uint64_t (&w)[4]) {
+    auto weigh2 = [&](float y0, float y1, uint64_t& w0, uint64_t& w1) {
         if (heat.far) {
-#pragma unroll 1
-            for (int e = 0; e < 4; ++e) {
-                const float x = e < 2 ? e == 0 ? y[0] : y[1] : e == 2 ? y[2] : y[3];
-                const uint64_t one = weight_far(x, top, heat.z, heat.z_low, s.powers);
-                if (e == 0) w[0] = one;
-                else if (e == 1) w[1] = one;
-                else if (e == 2) w[2] = one;
-                else w[3] = one;
-            }
+            w0 = weight_far(y0, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), s.powers);
+            w1 = weight_far(y1, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), s.powers);
         } else {
-            weights(y[0], y[1], heat, s.powers, w[0], w[1]);
-            weights(y[2], y[3], heat, s.powers, w[2], w[3]);
+            weights(y0, y1, heat, s.powers, w0, w1);
         }
     };
+    auto weigh = [&](const float (&y)[4], uint64_t (&w)[4]) { weigh2(y[0], y[1], w[0], w[1]), weigh2(y[2], y[3], w[2], w[3]); };
     // the end of a step
     auto sync = [&]() {
         if (mode == kAlone) __syncthreads();
         else cluster.sync();
     };
-    // the least weight that stays
-    const uint64_t low = !(least > 0.f) ? 1 : least < 1.f ? max(part_of(kOne, least, true), static_cast<uint64_t>(1)) : kOne;
     Cut cut = {-CUDART_INF_F, 0, 0};             // all stay
     if (by_count || by_mass) {
         const bool few = a.vocab <= kShort;                             // they go to one CTA without an estimate
         const float width = -kDeep / kBins * kLn2 * t;                  // of an estimate's bin, in logits
-        uint64_t total = 0, want = k, mass = 0, upto = 0, estimated = 0;
+        uint64_t total = 0, want = k, mass = 0, upto = 0;
+        float estimated = 0.f, estimated_upto = 0.f;
         unsigned number = 0;
         float bound;
         const bool by_largest = by_count && k <= kThreads / 2 * ctas;
@@ -511,28 +509,29 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             for (int r = 0; r < kMaxCtas; ++r) theirs[r] = r < ctas ? cluster.map_shared_rank(&s, r < ctas ? r : 0)->id[tid] : 0;
 #pragma unroll
             for (int r = 0; r < kMaxCtas; ++r) number += theirs[r];
-            const float share = 8.f * static_cast<float>(number) * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins));
-            mass = by_count ? static_cast<uint64_t>(number) * (by_largest ? 1 : 8) : static_cast<uint64_t>(share * 1073741824.f);
-            upto = warp_scan(mass, lane);
-            if (lane == 31) s.warp_mass[warp] = upto;
+            // (every CTA adds up the same in the same order)
+            const float share = static_cast<float>(number) * (by_largest ? 1.f : by_count ? 8.f : 8.f * exp2_fast((static_cast<float>(tid) + 0.5f) * (kDeep / kBins)));
+            estimated_upto = warp_scan(share, lane);
+            if (lane == 31) s.told_top[warp] = estimated_upto;
             __syncthreads();
             for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) upto += estimated;
-                estimated += s.warp_mass[w];
+                if (w == warp) estimated_upto += estimated;
+                estimated += s.told_top[w];
             }
-            if (!by_count) want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+            if (!by_count) want = max(part_of(total, fmaxf(s.p, 0.f), true), static_cast<uint64_t>(1));
         }
-        const uint64_t estimated_upto = upto;
+        float lid = top;                         // above which the border does not lie, by the same estimate
         // The bound of an attempt. Counts, or the weight that may lie below (the whole less 'want', of which
         // an eighth of the logits give an idea), with room for what chance does to the estimate.
         auto bound_of = [&](int attempt) {
+            lid = top;
             if (few || attempt == 2) return heat.deep;
-            uint64_t most_of = attempt > 0 ? 2 * want + 512 : by_largest ? want : want + want / 4 + 64;
-            if (!by_count) {
-                const uint64_t rest = (total - want) >> (kUnitBits - 30), below = attempt == 0 ? rest - rest / 4 : rest / 4;
-                most_of = estimated > below ? estimated - below : 0;
-            }
-            const int bin = min(__syncthreads_count(estimated_upto < most_of), kBins - 1);
+            const float goal = static_cast<float>(want), rest = static_cast<float>(total - want) * (1.f / kOne);
+            const float least_of = by_largest ? 0.f : by_count ? goal - goal * 0.25f - 64.f : estimated - 1.25f * rest;
+            const float most_of = !by_count ? estimated - (attempt == 0 ? 0.75f : 0.25f) * rest : attempt > 0 ? 2.f * goal + 512.f : by_largest ? goal : goal * 1.25f + 64.f;
+            const int bin = min(__syncthreads_count(estimated_upto < most_of), kBins - 1), lid_bin = min(__syncthreads_count(estimated_upto < least_of), bin);
+            // (a top-p of a top-k may cut anywhere)
+            if (attempt == 0 && !(by_count && by_mass)) lid = top - static_cast<float>(lid_bin) * width;
             return fmaxf(top - static_cast<float>(bin + 1) * width, heat.deep);
         };
 
@@ -571,30 +570,38 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             before_mass = s.before_mass, in_mass = s.in_mass, before = s.before, in = s.in;
             return bin < kBins;
         };
-        auto add = [&](int to, uint64_t w) {
-            atomicAdd(&s.count[to], 1u);
+        auto add = [&](int to, uint64_t w, unsigned n = 1) {
+            atomicAdd(&s.count[to], n);
             if (!by_mass) return;
             atomicAdd(&s.mass[0][to], static_cast<unsigned>(w) & 0xFFFFu);
             atomicAdd(&s.mass[1][to], static_cast<unsigned>(w) >> 16);
             atomicAdd(&s.mass[2][to], static_cast<unsigned>(w >> 32));
         };
 
-        // the listed logits by value
+        // the listed logits by value: those above the lid in the first bin, which a warp adds up by itself
         float fine = 0.f;
         bool found = false;
-        auto coarse = [&](float y) { return min(static_cast<int>((top - y) * fine), kBins - 1); };
+        auto coarse = [&](float y) { return y > lid ? 0 : min(1 + static_cast<int>((lid - y) * fine), kBins - 1); };
         auto by_value = [&]() {
-            fine = (kBins - 0.5f) / fmaxf(top - bound, 1e-30f);
+            fine = (kBins - 1.5f) / fmaxf(lid - bound, 1e-30f);
+            unsigned over = 0;
+            uint64_t over_mass = 0;
             each([&](const float (&y)[4]) {
-                uint64_t w[4] = {};
-                if (by_mass) weigh(y, w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (y[e] >= bound) add(coarse(y[e]), w[e]);
+                for (int e = 0; e < 4; e += 2) {
+                    uint64_t w[2] = {};
+                    if (by_mass) weigh2(y[e], y[e + 1], w[0], w[1]);
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        if (y[e + f] > lid) ++over, over_mass += w[f];
+                        else if (y[e + f] >= bound) add(coarse(y[e + f]), w[f]);
+                    }
+                }
             });
+            over = __reduce_add_sync(~0u, over), over_mass = warp_sum(over_mass);
+            if (lane == 0 && over > 0) add(0, over_mass, over);
             sum_bins();
         };
-
         // ---- the list of the logits at the bound and above
         for (int attempt = 0;; ++attempt) {
             bound = bound_of(attempt);
@@ -637,18 +644,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             mode = fits ? kListed : kAll;
             n = fits ? m : part_end - part_begin;
             const bool last = bound == heat.deep;
-            if (listed > kShort) {
-                // by value; whether they are enough is seen from it
-                if (by_count && listed < want && !last) {
-                    cluster.sync();              // all have read what is told anew
-                    continue;
-                }
-                by_value();
-                found = find_bin(by_count, want);
-                if (found || last) break;        // (else fewer have weight: all of them stay)
-                continue;
-            }
-            bool enough = last || (by_count && listed >= want);
+            // (of a long list of a top-p alone it is seen by value)
+            bool enough = last || (by_count ? listed >= want : listed > kShort);
             if (!enough && !by_count) {
                 uint64_t have = 0;
                 each([&](const float (&y)[4]) {
@@ -662,7 +659,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 cluster.sync();
                 enough = all_mass() >= want;
             }
-            if (enough) {
+            if (!enough) {
+                cluster.sync();                  // all have read what is told anew
+                continue;
+            }
+            if (listed <= kShort) {
                 // to the first CTA, in the order of the ids
                 S* first = cluster.map_shared_rank(&s, 0);
                 auto put = [&](int to, int at) {
@@ -685,34 +686,43 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 cluster.sync();
                 if (rank != 0) return;
                 if (listed <= kThreads) {
-                    finish_alone(s, a, row, static_cast<int>(listed), k, by_count, by_mass, few && !by_count, want, p, low, u, t, top, weigh);
+                    finish_alone(s, a, row, static_cast<int>(listed), k, by_count, by_mass, few && !by_count, want, top, weigh);
                     return;
                 }
                 mode = kAlone, ctas = 1;
                 const int share = (static_cast<int>(listed) + kWarps - 1) / kWarps;
                 begin = min(warp * share, static_cast<int>(listed));
                 n = min(share, static_cast<int>(listed) - begin);
+            }
+            // by value, and the bin with the border that `want` makes
+            while (true) {
                 by_value();
-                if (few && by_mass && !by_count) {
+                if (few && by_mass && !by_count) {              // (the whole is known from the bins)
                     __syncthreads();
-                    if (tid == kBins - 1) s.before_mass = upto;         // all that have weight
+                    if (tid == kBins - 1) s.before_mass = upto;
                     __syncthreads();
                     total = s.before_mass;
-                    want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
+                    want = max(part_of(total, fmaxf(s.p, 0.f), true), static_cast<uint64_t>(1));
                 }
                 found = find_bin(by_count, want);
-                break;
+                if (bin > 0 || lid >= top) break;
+                lid = top;                       // the estimate was wrong
             }
-            cluster.sync();                      // all have read what is told anew
+            if (found || last || mode == kAlone) break;         // (else fewer have weight: all of them stay)
         }
         // ---- borders: the value at which `goal` is reached, in the bin that has been found
         auto border = [&](bool count, uint64_t goal) {
             // the values of that bin, and what rounding may add to them
             const int first = bin;
-            const float high = top - static_cast<float>(first) / fine, least_of = top - static_cast<float>(first + 1) / fine;
+            const float high = lid - static_cast<float>(first - 1) / fine, least_of = lid - static_cast<float>(first) / fine;
             const float slack = 1e-5f * (fabsf(top) + fabsf(bound));
             uint32_t hi = key_of<kDtype>(fminf(high + slack, top));
             uint32_t lo = key_of<kDtype>(fmaxf((first == kBins - 1 ? bound : least_of) - slack, -kTop));
+            if (hi - lo < 32) {
+                // where one value falls into that bin, it is the border
+                const unsigned fall = __ballot_sync(~0u, lo + lane <= hi && value_of<kDtype>(lo + lane) >= bound && coarse(value_of<kDtype>(lo + lane)) == first);
+                if (__popc(fall) == 1) lo += __ffs(fall) - 1, hi = lo;
+            }
             uint64_t mass_above = before_mass;
             unsigned above = before;
             while (hi > lo) {
@@ -726,12 +736,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                         key[e] = key_of<kDtype>(y[e]);
                         in_it[e] = y[e] >= bound && key[e] >= lo && key[e] <= hi && coarse(y[e]) == first;
                     }
-                    if (!__any_sync(__activemask(), in_it[0] | in_it[1] | in_it[2] | in_it[3])) return;
-                    uint64_t w[4] = {};
-                    if (by_mass) weigh(y, w);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (in_it[e]) add((hi - key[e]) >> down, w[e]);
+                    for (int e = 0; e < 4; e += 2) {
+                        if (!__any_sync(__activemask(), in_it[e] | in_it[e + 1])) continue;
+                        uint64_t w[2] = {};
+                        if (by_mass) weigh2(y[e], y[e + 1], w[0], w[1]);
+#pragma unroll
+                        for (int f = 0; f < 2; ++f)
+                            if (in_it[e + f]) add((hi - key[e + f]) >> down, w[f]);
+                    }
                 });
                 sum_bins();
                 if (!find_bin(count, goal - (count ? above : mass_above))) break;   // (cannot be: what was summed is summed again)
@@ -749,32 +762,32 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         // what a thread found of the first bins, for a second border
         const uint64_t first_upto = upto, first_mass = mass;
         const unsigned first_count = upto_count, first_number = number;
-        if (found) cut = border(by_count, want);
-        if (by_count && by_mass) {
-            uint64_t tie = 0;
-            if (found) {
-                const float y[4] = {cut.at, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                uint64_t w[4];
-                weigh(y, w);
-                tie = w[0];
-                total = cut.above + cut.ties * tie;
-            } else {
-                __syncthreads();
-                if (tid == kBins - 1) s.before_mass = first_upto;               // all that are listed
-                __syncthreads();
-                total = s.before_mass;
-            }
-            want = max(part_of(total, fmaxf(p, 0.f), true), static_cast<uint64_t>(1));
-            if (found && want > cut.above) {
+        bool count = by_count;
+        if (by_count && by_mass && !found) {
+            __syncthreads();
+            if (tid == kBins - 1) s.before_mass = upto;                         // all that are listed
+            __syncthreads();
+            want = max(part_of(s.before_mass, fmaxf(s.p, 0.f), true), static_cast<uint64_t>(1));
+            count = false, found = find_bin(false, want);
+        }
+        while (found) {
+            cut = border(count, want);
+            if (!(count && by_mass)) break;
+            // the top-p of what the top-k leaves
+            uint64_t tie, none;
+            weigh2(cut.at, -CUDART_INF_F, tie, none);
+            want = max(part_of(cut.above + cut.ties * tie, fmaxf(s.p, 0.f), true), static_cast<uint64_t>(1));
+            if (want > cut.above) {
                 if (tie > 0) cut.ties = min(cut.ties, static_cast<unsigned>((want - cut.above + tie - 1) / tie));
-            } else {
-                upto = first_upto, mass = first_mass, upto_count = first_count, number = first_number;
-                if (find_bin(false, want)) cut = border(false, want);
+                break;
             }
+            upto = first_upto, mass = first_mass, upto_count = first_count, number = first_number;
+            count = false, found = find_bin(false, want);
         }
     }
 
     // ---- the sums of what stays, and the token
+    const uint64_t low = least_weight(s.least);
     uint64_t mass = 0;
     unsigned ties = 0;
     auto keep = [&](const float (&y)[4]) {
@@ -803,17 +816,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     const Two<unsigned> all_ties = of_warps<unsigned>(cluster, ctas, lane, s, &S::told_count, 0);
     uint64_t tie = 0;
     if (cut.ties > 0) {
-        const float y[4] = {cut.at, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-        uint64_t w[4];
-        weigh(y, w);
-        tie = w[0];
+        uint64_t none;
+        weigh2(cut.at, -CUDART_INF_F, tie, none);
     }
     const unsigned ties_before = warp_scan(all_ties.x + all_ties.y, lane) - all_ties.x - all_ties.y;
     const unsigned take_x = min(cut.ties - min(cut.ties, ties_before), all_ties.x);
     const unsigned take_y = min(cut.ties - min(cut.ties, ties_before + all_ties.x), all_ties.y);
     const uint64_t sum_x = masses.x + take_x * tie, sum_y = masses.y + take_y * tie, upto = warp_scan(sum_x + sum_y, lane);
     const uint64_t total = __shfl_sync(~0u, upto, 31);
-    const uint64_t goal = u < 1.f ? part_of(total, fmaxf(u, 0.f), false) : total - 1;
+    const uint64_t goal = s.u < 1.f ? part_of(total, fmaxf(s.u, 0.f), false) : total - 1;
     // the warp whose sum passes the goal, what lies before it, and how many equal ones of it stay
     const unsigned past = __ballot_sync(~0u, upto > goal);
     const int at_lane = __ffs(past) - 1;
@@ -871,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 if (lane == __ffs(found) - 1) {
                     const int j = i + lane + 32 * e;
                     a.ids[row] = mode == kAlone ? s.id[begin + j] : id0 + (mode == kListed ? static_cast<int>(mine[j]) : begin + j);
-                    a.logprob[row] = ((y[e] - top) / t) - logf(static_cast<float>(total) * (1.f / kOne));
+                    a.logprob[row] = ((y[e] - top) / s.t) - logf(static_cast<float>(total) * (1.f / kOne));
                 }
                 return;
             }
