@@ -125,7 +125,7 @@ __device__ __forceinline__ bool walk_piece(Walk& k, int from) {
 
 // Where the requests behind a prefix are many and short, a CTA takes each gridDim.x-th of all (request, head)s
 // as a whole instead of a run: the joins of cut ones cost more than they even out (64 requests of up to 1K tokens
-// of their own, 8 heads: @@).
+// of their own, 8 heads: 31 us in runs, 28.5 whole, 20 with CTAs of four warps).
 constexpr int64_t kWhole = -1;
 constexpr int kWholeUnits = 8;                   // of the longest request
 constexpr int kWholeHeads = 128;                 // fewer leave most SMs without one

@@ -108,7 +108,7 @@ Ctx* current_ctx(int* err);
 int check_ptr(const void* p, int device);
 
 // Kernel attributes of the operators beside the read, once a context (hc_window.cu, hc_attention.cu,
-// hc_sample.cu).
+// hc_attention_*.cu, hc_sample.cu).
 cudaError_t window_setup();
 cudaError_t attention_setup();
 cudaError_t sample_setup();

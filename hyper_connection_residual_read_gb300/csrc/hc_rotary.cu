@@ -7,7 +7,13 @@
 // order that the operator states. Every step is a single rounded operation (no fma): the codes of a key are a
 // step function of it, and would differ from place to place with the last bit of it.
 //
-// MEASURED
+// A CTA takes some heads of a share of the tokens, so that a token's cosines and sines are fetched once for them,
+// and brings heads through a ring of three steps of asynchronous copies.
+//
+// Measured: 8191 tokens, 32 query and 8 kv heads of 128, bf16, with norms, 34.9 us, 176 MB at 5.0 TB/s (74% of the
+// copy rate): issue bounds it (65% of the slots; ALU 46%, FMA 32%), since without fma and with each rounding of its
+// own a value costs some ten instructions. 4099 tokens of 16 + 16 heads of 64, fp16, three axes, no norm, 12.1 us:
+// a CTA's few steps hardly outlast its start. 32 tokens 3.3 us, a launch and a chain of loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
