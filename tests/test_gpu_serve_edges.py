@@ -241,3 +241,29 @@ def test_sample_of_one_large_row_batch_is_that_of_its_rows():
     for t in range(0, 400, 40):
         one = run_sample(x[t:t + 1], u[t:t + 1], **{k: v[t:t + 1] for k, v in settings.items()})
         assert one[0][0] == got[t] and one[1][0] == lp[t]
+
+
+@pytest.mark.parametrize("kind", ["deep", "blind", "top"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_sample_where_every_eighth_logit_misleads(kind, dtype):
+    """Rows whose logits at the places 8 j + j % 8 are unlike the others: of little weight but much of it in
+    eighths, none, or all of the largest. An estimate from them is wrong to either side."""
+    vocab, rows = 65536, 12
+    g = np.random.default_rng(5)
+    at = np.arange(vocab)
+    eighth = at % 8 == at // 8 % 8
+    x = np.zeros((rows, vocab))
+    if kind == "deep":                           # 1, 2.03 and 0.155 of weight
+        x[:] = np.where(eighth, -10.875, -10.25)
+        x[:, 8] = 0.0
+    elif kind == "blind":
+        x[:] = np.where(eighth, -np.inf, g.integers(-64, 64, (rows, vocab)) / 16)
+    else:
+        x[:] = np.where(eighth, 4.0, -4.0) + g.integers(-16, 16, (rows, vocab)) / 16
+    x = torch.from_numpy(x).to(dtype).cuda()
+    p = np.array([0.1, 0.3, 0.5, 0.7, 0.8, 0.8425, 0.85, 0.9, 0.95, 0.97, 0.99, 0.999])
+    k = np.array([1, 100, 1000, 1025, 1500, 3000, 8191, 8192, 8193, 20000, 40000, 65535])
+    check_sample(x, g.random(rows), top_p=p)
+    check_sample(x, g.random(rows), top_k=k)
+    check_sample(x, g.random(rows), top_k=k[::-1].copy(), top_p=p)
+    check_sample(x, g.random(rows), top_p=p, temperature=np.full(rows, 0.5), min_p=np.full(rows, 1e-5))
