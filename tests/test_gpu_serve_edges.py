@@ -123,6 +123,53 @@ def test_two_graphs_of_shared_attention_in_turns():
         assert torch.equal(kw["out"], want[0]) and torch.equal(kw["lse"], want[1])
 
 
+@pytest.mark.parametrize("heads,groups", [
+    ((32, 8, 128), [(2001, [(30 + i, 1) for i in range(8)])]),
+    ((32, 8, 128), [(2001, [(50 + 3 * i, 1) for i in range(40)])]),
+    ((20, 4, 128), [(3000, [(100, 8)] * 4), (500, [(700, 8), (1, 3), (90, 8)])]),
+    ((8, 2, 64), [(300, [(1000, 1), (5, 1)])]),
+    ((4, 1, 64), [(9000, [(3000 + i, 1) for i in range(24)])]),
+    ((4, 4, 64), [(700, [(60, 60), (0, 0), (200, 200)]), (0, [(90, 70)])]),
+], ids=str)
+def test_shared_directly_behind_the_write_of_what_it_reads(heads, groups):
+    """Writes of all keys and values and calls that read them, one after the other without a pause, with one
+    workspace: what each call returns is what it returns alone."""
+    c = Shared(11, groups, *heads, 16, "bf16")
+    kw = c.arguments()
+    t, _, d = c.q.shape
+    at = [(b, n) for b, n in enumerate(np.concatenate([c.kv, c.prefix]))]
+    tables = np.concatenate([c.table, c.prefix_table])
+    slots = torch.from_numpy(np.concatenate([tables[b, np.arange(n) // 16] * 16 + np.arange(n) % 16 for b, n in at])).cuda()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows = [[torch.randn(len(slots), heads[1], d, generator=g, device="cuda").bfloat16() for _ in range(2)] for _ in range(2)]
+    qs = [torch.randn(kw["q"].shape, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    outs = [torch.empty_like(kw["out"]) for _ in range(12)]
+    lses = [torch.empty_like(kw["lse"]) for _ in range(12)]
+
+    def step(i):
+        hc.hc_kv4_append(*rows[i % 2], slots, kw["codes"], kw["scales"])
+        hc.hc_kv4_attention_shared(**dict(kw, q=qs[i // 2 % 2], out=outs[i], lse=lses[i]))
+
+    want = []
+    for i in range(12):
+        torch.cuda.synchronize()
+        step(i)
+        torch.cuda.synchronize()
+        want.append((outs[i].clone(), lses[i].clone()))
+    assert not torch.equal(want[0][0], want[1][0]) and torch.equal(want[0][0], want[4][0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(12):
+            step(i)
+    for run in (lambda: [step(i) for i in range(12)], graph.replay, graph.replay):
+        for x in outs + lses:
+            x.zero_()
+        run()
+        torch.cuda.synchronize()
+        for i in range(12):
+            assert torch.equal(outs[i], want[i][0]) and torch.equal(lses[i], want[i][1])
+
+
 # ---------------------------------------------------------------------------
 # rotary
 # ---------------------------------------------------------------------------
