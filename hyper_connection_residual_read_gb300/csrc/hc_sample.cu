@@ -26,9 +26,9 @@
 // comes to the same end. A short list is handed to the first CTA, which ends the row alone. Lists and
 // rows are gone through in the order of the ids, by each warp its part.
 //
-// Measured: rows of 131072 bf16 logits, 8 and 512 of them: the largest 4.1 and 42 us, no filter 11 and 110, a top-50
-// 8.8 and 86, a top-1000 16 and 143, a top-p of 0.5 19 and 185, of 0.95 26 and 280; 512 of mixed settings 141 us,
-// 0.95 TB/s. The logits are read once (20 us of it at the copy rate). Few rows wait at barriers (a cluster's takes
+// Measured: rows of 131072 bf16 logits, 8 and 512 of them: the largest 3.6 and 38 us, no filter 9.8 and 103, a top-50
+// 8.2 and 81, a top-1000 16 and 139, a top-p of 0.5 18 and 178, of 0.95 25 and 274; 512 of mixed settings 136 us,
+// 1.0 TB/s. The logits are read once (20 us of it at the copy rate). Few rows wait at barriers (a cluster's takes
 // some 0.5 us, a filter has 6 to 10); many are bound by issue (38% of the slots, four CTAs an SM wait for one
 // another) and by the weights, 64-bit arithmetic.
 #include <cooperative_groups.h>
@@ -63,7 +63,7 @@ constexpr float kTop = 3.402823466e38f;
 static_assert(HC_SAMPLE_MAX_VOCAB <= kMaxCtas * 32768);
 
 // 2^(j / 32) 2^31
-__constant__ uint32_t kPowers[kSteps] = {
+__device__ const uint32_t kPowers[kSteps] = {
     0x80000000u, 0x82CD8699u, 0x85AAC368u, 0x88980E81u, 0x8B95C1E4u, 0x8EA4398Bu, 0x91C3D374u, 0x94F4EFA9u,
     0x9837F052u, 0x9B8D39BAu, 0x9EF53261u, 0xA2704303u, 0xA5FED6AAu, 0xA9A15AB5u, 0xAD583EEAu, 0xB123F582u,
     0xB504F334u, 0xB8FBAF47u, 0xBD08A39Fu, 0xC12C4CCAu, 0xC5672A11u, 0xC9B9BD86u, 0xCE248C15u, 0xD2A81D92u,
@@ -222,6 +222,10 @@ __device__ __forceinline__ Two<T> of_warps(cg::cluster_group& cluster, int ctas,
     return there ? Two<T>{p[0], p[1]} : Two<T>{none, none};
 }
 
+// The two halves of a cluster's barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // Logits above `at` stay, and of those equal to it the first `ties`.
 struct Cut {
     float at;
@@ -275,7 +279,7 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&y)[kDtype == HC_D
 
 // The end of a row of which at most kThreads logits are left, in one CTA, a logit a thread: each counts and weighs
 // those before it. `want`: the weight of a top-p alone (`whole`: it follows from the list's). (A row of a top-50 among
-// 131072 13.4 us in bins, 9.0 so.)
+// 131072 13.4 us in bins, 9.1 so.)
 template <int kDtype, typename Weigh>
 __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs& a, int row, int n, int k, bool by_count, bool by_mass, bool whole,
                                              uint64_t want, float top, Weigh& weigh) {
@@ -342,33 +346,36 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + segment_bytes);
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / ctas;
-    int rank = blockIdx.x % ctas;
+    const int log_ctas = 31 - __clz(ctas);       // (a power of two)
+    const int row = blockIdx.x >> log_ctas, rank = blockIdx.x & (ctas - 1);
     begin_early();
     // (the whole cluster has one row, so that all of it leaves together)
     if (!HC_IN_RANGE(row, 1, a.tokens, status)) return;
+
+    // on their way together with the row
+    const float u = a.uniform[row], t = a.temperature ? a.temperature[row] : 1.f;
+    const float p = a.top_p ? a.top_p[row] : 1.f, least = a.min_p ? a.min_p[row] : 0.f;
+    const int k = a.top_k ? a.top_k[row] : 0;
+    const uint32_t power_of = kPowers[lane];
+    static_assert(kSteps == 32);
 
     // ---- the CTA's part of the row: whole vectors of 16 bytes, with -inf for what lies around the row
     const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.row * kItem;
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15) / kItem;
     const int vectors = (shift + a.vocab + kN - 1) / kN;
-    const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), v1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
+    const int v0 = (vectors * rank) >> log_ctas, v1 = (vectors * (rank + 1)) >> log_ctas;
     const int id0 = v0 * kN - shift;             // the id of local index 0
     uint4* const vec = reinterpret_cast<uint4*>(segment);
     // whole vectors by asynchronous copies, all on their way at once; the ends of the row by one thread each
     const int n_vec = v1 - v0, w0 = id0 < 0 ? 1 : 0, w1 = id0 + n_vec * kN > a.vocab ? n_vec - 1 : n_vec;
     {
         const uint4* from = reinterpret_cast<const uint4*>(x - shift * kItem) + v0;
+#pragma unroll 4
         for (int i = w0 + tid; i < w1; i += kThreads)
             if (HC_IN_RANGE(id0 + i * kN, kN, a.vocab, status)) copy16(tc::smem_u32(vec + i), from + i);
         copy_commit();
     }
-    const float u = a.uniform[row], t = a.temperature ? a.temperature[row] : 1.f;
-    const float p = a.top_p ? a.top_p[row] : 1.f, least = a.min_p ? a.min_p[row] : 0.f;
-    const int k = a.top_k ? a.top_k[row] : 0;
     bool bad = !(u == u && p == p && least == least) || !(fabsf(t) <= kTop);
-    for (int i = tid; i < kSteps; i += kThreads) s.powers[i] = kPowers[i];
-    if (tid == 0) s.u = u, s.p = p, s.t = t, s.least = least;
     s.count[tid] = s.mass[0][tid] = s.mass[1][tid] = s.mass[2][tid] = 0, s.id[tid] = 0;
     Most<kDtype> largest;
     const int end = tid == 0 && w0 > 0 ? 0 : tid == 32 && w1 < n_vec && n_vec > w0 ? n_vec - 1 : -1;
@@ -382,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
         largest.take(vec[end]);
     }
     copy_wait<0>();
+#pragma unroll 4
     for (int i = w0 + tid; i < w1; i += kThreads) largest.take(vec[i]);
     const float my_most = largest.get();         // of this thread's logits
     float most = my_most;
@@ -390,6 +398,8 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) most = max_nan(most, __shfl_xor_sync(~0u, most, d));
     if (lane == 0) s.told_top[warp] = most;
+    if (tid < kSteps) s.powers[tid] = power_of;
+    if (tid == 0) s.u = u, s.p = p, s.t = t, s.least = least;
     cluster.sync();
     const Two<float> tops = of_warps<float>(cluster, ctas, lane, s, &S::told_top, -CUDART_INF_F);
     float top = max_nan(tops.x, tops.y);
@@ -402,25 +412,27 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
     if (bad || t < 5.421010862427522e-20f) {
         // nothing, or the first of the largest: the first CTA that has it finds it
         const unsigned with = __ballot_sync(~0u, tops.x == top || tops.y == top);
-        cluster.sync();                          // all have read what the others told
-        if (bad ? rank != 0 : rank != (__ffs(with) - 1) / 4) return;
-        int first = 0x7FFFFFFF;
-        if (!bad)
-            for (int i = part_begin / kN + lane; i < part_end / kN; i += 32) {
-                float y[kN];
-                unpack<kDtype>(vec[i], y);
+        cluster_arrive();                        // all have read what the others told: they wait for it in the end
+        if (bad ? rank == 0 : rank == (__ffs(with) - 1) / 4) {
+            int first = 0x7FFFFFFF;
+            if (!bad)
+                for (int i = part_begin / kN + lane; i < part_end / kN; i += 32) {
+                    float y[kN];
+                    unpack<kDtype>(vec[i], y);
 #pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    if (y[e] == top) first = min(first, id0 + i * kN + e);
+                    for (int e = 0; e < kN; ++e)
+                        if (y[e] == top) first = min(first, id0 + i * kN + e);
+                }
+            first = __reduce_min_sync(~0u, first);
+            if (lane == 0) s.warp_first[warp] = first;
+            __syncthreads();
+            if (tid == 0) {
+                for (int w = 1; w < kWarps; ++w) first = min(first, s.warp_first[w]);
+                a.ids[row] = bad ? -1 : first;
+                a.logprob[row] = bad ? CUDART_NAN_F : 0.f;
             }
-        first = __reduce_min_sync(~0u, first);
-        if (lane == 0) s.warp_first[warp] = first;
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < kWarps; ++w) first = min(first, s.warp_first[w]);
-            a.ids[row] = bad ? -1 : first;
-            a.logprob[row] = bad ? CUDART_NAN_F : 0.f;
         }
+        cluster_wait();
         return;
     }
     const Heat heat = heat_of(t, top);
@@ -837,64 +849,68 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
     const bool in_y = __shfl_sync(~0u, goal >= upto - sum_y, at_lane);
     uint64_t from = __shfl_sync(~0u, in_y ? upto - sum_y : upto - sum_y - sum_x, at_lane);
     unsigned allow = __shfl_sync(~0u, in_y ? take_y : take_x, at_lane);
-    sync();                                      // no CTA leaves while another reads its memory
-    if (at_lane / 4 != rank) return;
-    // its logits, shared out over the CTA's warps: 128 at a time
-    const int owner = 2 * (at_lane % 4) + in_y, its_n = s.warp_n[owner];
-    begin = s.warp_begin[owner], mine = list + owner * list_room;
-    const int share = (its_n + 128 * kWarps - 1) / (128 * kWarps) * 128, i0 = min(warp * share, its_n), i1 = min(i0 + share, its_n);
-    auto bring = [&](int i, float (&y)[4], uint64_t (&w)[4]) {
+    // no CTA leaves while another reads its memory: the one with the token waits behind the rest of its work
+    const bool joined = mode != kAlone;
+    if (joined) cluster_arrive();
+    if (at_lane / 4 == rank) {
+        // the warp's logits, a run of them a thread: how many equal ones stay, and the sum, of those before
+        const int owner = 2 * (at_lane % 4) + in_y, its_n = s.warp_n[owner];
+        begin = s.warp_begin[owner], mine = list + owner * list_room;
+        const int share = (its_n + kThreads - 1) / kThreads, i0 = min(tid * share, its_n), i1 = min(i0 + share, its_n);
+        auto bring = [&](int i, float (&y)[4], uint64_t (&w)[4]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = i + lane + 32 * e < i1 ? value_at(i + lane + 32 * e) : -CUDART_INF_F;
-        weigh(y, w);
+            for (int e = 0; e < 4; ++e) y[e] = i + e < i1 ? value_at(i + e) : -CUDART_INF_F;
+            weigh(y, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (w[e] < low || y[e] < cut.at) w[e] = 0;
-    };
-    mass = ties = 0;
-    for (int i = i0; i < i1; i += 128) {
-        float y[4];
-        uint64_t w[4];
-        bring(i, y, w);
+            for (int e = 0; e < 4; ++e)
+                if (w[e] < low || y[e] < cut.at) w[e] = 0;
+        };
+        mass = ties = 0;
+        for (int i = i0; i < i1; i += 4) {
+            float y[4];
+            uint64_t w[4];
+            bring(i, y, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (y[e] != cut.at) mass += w[e];
-            else ties += w[e] > 0;
-        }
-    }
-    mass = warp_sum(mass), ties = __reduce_add_sync(~0u, ties);
-    if (lane == 0) s.warp_mass[warp] = mass, s.warp_count[warp] = ties;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        const unsigned some = min(allow, s.warp_count[w]);
-        allow -= some;
-        from += s.warp_mass[w] + some * tie;
-    }
-    if (goal < from || goal - from >= mass + min(allow, ties) * tie) return;
-    // the 128, the 32 and the one among them
-    for (int i = i0; i < i1; i += 128) {
-        float y[4];
-        uint64_t w[4];
-        bring(i, y, w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool equal = w[e] > 0 && y[e] == cut.at;
-            const unsigned votes = __ballot_sync(~0u, equal);
-            if (equal && static_cast<unsigned>(__popc(votes & ((1u << lane) - 1u))) >= allow) w[e] = 0;
-            allow -= min(allow, static_cast<unsigned>(__popc(votes)));
-            const uint64_t at = from + warp_scan(w[e], lane);
-            const unsigned found = __ballot_sync(~0u, at > goal);
-            if (found) {
-                if (lane == __ffs(found) - 1) {
-                    const int j = i + lane + 32 * e;
-                    a.ids[row] = mode == kAlone ? s.id[begin + j] : id0 + (mode == kListed ? static_cast<int>(mine[j]) : begin + j);
-                    a.logprob[row] = ((y[e] - top) / s.t) - logf(static_cast<float>(total) * (1.f / kOne));
-                }
-                return;
+            for (int e = 0; e < 4; ++e) {
+                if (y[e] != cut.at) mass += w[e];
+                else ties += w[e] > 0;
             }
-            from = __shfl_sync(~0u, at, 31);
+        }
+        unsigned ties_upto = warp_scan(ties, lane);
+        if (lane == 31) s.warp_count[warp] = ties_upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) ties_upto += s.warp_count[w];
+        unsigned take = min(allow - min(allow, ties_upto - ties), ties);
+        const uint64_t sum = mass + take * tie;
+        uint64_t at = warp_scan(sum, lane);
+        if (lane == 31) s.warp_mass[warp] = at;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) at += s.warp_mass[w];
+        at += from - sum;
+        // the thread whose sum passes the goal goes through its own
+        if (goal >= at && goal - at < sum) {
+            for (int i = i0; i < i1 && at <= goal; i += 4) {
+                float y[4];
+                uint64_t w[4];
+                bring(i, y, w);
+                int j = -1;
+                float drawn = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (w[e] > 0 && y[e] == cut.at) {
+                        if (take == 0) w[e] = 0;
+                        else --take;
+                    }
+                    at += w[e];
+                    if (j < 0 && at > goal) j = i + e, drawn = y[e];
+                }
+                if (j < 0) continue;
+                a.ids[row] = mode == kAlone ? s.id[begin + j] : id0 + (mode == kListed ? static_cast<int>(mine[j]) : begin + j);
+                a.logprob[row] = ((drawn - top) / s.t) - logf(static_cast<float>(total) * (1.f / kOne));
+            }
         }
     }
+    if (joined) cluster_wait();
 }
 
 // CTAs of a row: as many as keep a part within 16384 logits, and twice, four times as many where there
