@@ -1219,13 +1219,16 @@ __global__ void __launch_bounds__(kJoinRows * kD / 4) join_kernel(const SharedAr
         }
         if (lane == 0) total = slots;
     }
+    __syncthreads();
+    int c0 = 0, c1 = 0;
+    if (row0 >= 0) {
+        const int tiles = key_tiles<kPrefix>(a, window, group, step, 0);
+        const int64_t n = min(static_cast<int64_t>(ctas), total);
+        c0 = static_cast<int>(((base + kPieceCost + 1) * n - 1) / total), c1 = static_cast<int>(((base + kPieceCost + tiles) * n - 1) / total);
+    }
     // (the chunk kernel before began after all lengths were written; the kernel behind may begin once it has ended)
     begin_early();
-    __syncthreads();
     if (row0 < 0) return;
-    const int tiles = key_tiles<kPrefix>(a, window, group, step, 0);
-    const int64_t n = min(static_cast<int64_t>(ctas), total);
-    const int c0 = static_cast<int>(((base + kPieceCost + 1) * n - 1) / total), c1 = static_cast<int>(((base + kPieceCost + tiles) * n - 1) / total);
     if (c0 == c1 || !HC_IN_RANGE(c0, c1 - c0 + 1, ctas, status)) return;      // one piece: its CTA wrote it
     auto piece = [&](int c) { return scratch + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPieceFloats; };
     const int in_tile = row0 % step, rows = min(window.rows * group - row0, kJoinRows);
