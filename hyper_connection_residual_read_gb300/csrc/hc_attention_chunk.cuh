@@ -169,6 +169,7 @@ __device__ __forceinline__ bool walk_next(const Args<kSide>& a, Walk& k, int gro
 struct Run {
     int b;
     int64_t offset, head, begin, end, total, ctas;
+    Window w;                    // of request b
 };
 
 template <Side kSide>
@@ -177,8 +178,11 @@ __device__ void find_run(const Args<kSide>& a, int group, int step, Run* run, in
     const int per = (a.requests + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += head_slots<kSide>(a, load_window<kSide>(a, b, blockIdx.x == 0 ? status : nullptr), group, step) * a.c.kv_heads;
+    Window w = {};                               // the last of them, which is the only one up to kThreads requests
+    for (int b = b0; b < b1; ++b) {
+        w = load_window<kSide>(a, b, blockIdx.x == 0 ? status : nullptr);
+        mine += head_slots<kSide>(a, w, group, step) * a.c.kv_heads;
+    }
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -193,7 +197,7 @@ __device__ void find_run(const Args<kSide>& a, int group, int step, Run* run, in
         total += sums[w];
     }
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), i = blockIdx.x;
-    const int64_t begin = i < ctas ? total * i / ctas : total, end = i < ctas ? total * (i + 1) / ctas : total;
+    const int64_t begin = i < ctas ? quotient(total * i, ctas) : total, end = i < ctas ? quotient(total * (i + 1), ctas) : total;
     if (tid == 0) {
         run->begin = begin;
         run->end = end;
@@ -203,9 +207,11 @@ __device__ void find_run(const Args<kSide>& a, int group, int step, Run* run, in
     if (begin < end && begin < upto && begin >= upto - mine) {
         int64_t at = upto - mine;
         for (int b = b0; b < b1; ++b) {
-            const int64_t head = head_slots<kSide>(a, load_window<kSide>(a, b, nullptr), group, step), n = head * a.c.kv_heads;
+            if (b1 - b0 > 1) w = load_window<kSide>(a, b, nullptr);
+            const int64_t head = head_slots<kSide>(a, w, group, step), n = head * a.c.kv_heads;
             if (begin < at + n) {
                 run->b = b;
+                run->w = w;
                 run->offset = begin - at;
                 run->head = head;
                 break;
@@ -220,8 +226,8 @@ template <Side kSide>
 __device__ __forceinline__ bool walk_start(const Args<kSide>& a, const Run& run, int group, int step, Walk& k) {
     if (run.begin >= run.end) return false;
     k.b = run.b;
-    k.w = load_window<kSide>(a, k.b, nullptr);
-    k.h = static_cast<int>(run.offset / run.head);
+    k.w = run.w;
+    k.h = static_cast<int>(quotient(run.offset, run.head));
     int64_t from = run.offset - k.h * run.head;
     int i = 0;
     while (true) {
@@ -450,45 +456,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float factor = 0.f, qsum = 0.f;
             if (active) {
-                // ---- this row of Q: scaled to fp16, in the order of the decoded keys
+                // ---- this warp's rows of Q: scaled to fp16, in the order of the decoded keys. A row is brought by
+                // neighbouring lanes, 16 bytes each. (A row a thread touches 32 lines with each load: the start of
+                // 256 rows took 12000 cycles of an L1 that looks up a line a cycle, where this takes 7000.)
                 const Row m = my_row();
-                const int i = m.i, hq = m.hq;
-                const int64_t from = static_cast<int64_t>(k.w.begin + i) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
-                const bool here = m.here && HC_IN_RANGE(from, kD, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), status);
-                const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + from);
-                float top = 0.f;
-#pragma unroll 8
-                for (int c = 0; c < kD / 8; ++c) {
-                    const uint4 raw = here ? in[c] : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+                const int64_t own = static_cast<int64_t>(k.w.begin + m.i) * a.q_token + static_cast<int64_t>(m.hq) * a.q_head;
+                const int64_t from = m.here && HC_IN_RANGE(own, kD, row_extent(a.tokens, a.q_heads, kD, a.q_token, a.q_head), status) ? own : -1;
+                constexpr int kOfRow = kD / 8, kRowsAt = 32 / kOfRow;  // lanes of a row, rows at a time
+                const int c = lane % kOfRow;
+                uint4 ahead[4];
+                auto fetch = [&](int turn) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = widen2<kDtype>(x[e]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int n = 0; n < 4; ++n) {
+                        const int64_t at = __shfl_sync(~0u, from, (turn + n) * kRowsAt + lane / kOfRow);
+                        ahead[n] = at >= 0 ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + 8 * c) : make_uint4(0, 0, 0, 0);
+                    }
+                };
+                fetch(0);
+                float my_top = 0.f;
+#pragma unroll 1
+                for (int turn0 = 0; turn0 < 32 / kRowsAt; turn0 += 4) {
+                    const uint4 four[4] = {ahead[0], ahead[1], ahead[2], ahead[3]};
+                    if (turn0 + 4 < 32 / kRowsAt) fetch(turn0 + 4);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint32_t x[4] = {four[n].x, four[n].y, four[n].z, four[n].w};
+                        float top = 0.f;
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float2 y = widen2<kDtype>(x[p]);
+                            top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                        }
+#pragma unroll
+                        for (int d = 1; d < kOfRow; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                        const float down = power_of_two(-query_exponent(top));
+                        float f[8];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float2 y = widen2<kDtype>(x[p]);
+                            f[2 * p] = y.x * down, f[2 * p + 1] = y.y * down;
+                        }
+                        const int to = (warp & 3) * 32 + (turn0 + n) * kRowsAt + lane / kOfRow;
+                        *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kTile * 128) + tc::sw128_offset(to, (c & 7) * 8)) =
+                            make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
+                        const float theirs = __shfl_sync(~0u, top, (lane % kRowsAt) * kOfRow);
+                        if (lane / kRowsAt == turn0 + n) my_top = theirs;
                     }
                 }
-                const int e = query_exponent(top);
-                const float down = power_of_two(-e);
-                factor = a.scale * kLog2e * power_of_two(e);
+                factor = a.scale * kLog2e * power_of_two(query_exponent(my_top));
+                __syncwarp();
 #pragma unroll 4
-                for (int c = 0; c < kD / 8; ++c) {
-                    const uint4 raw = here ? in[c] : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-                    float f[8];
+                for (int x = 0; x < kD / 8; ++x) {
+                    const uint4 o4 = *reinterpret_cast<const uint4*>(q_tile + (x >> 3) * (kTile * 128) + tc::sw128_offset(row, (x & 7) * 8));
+                    const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const float2 y = widen2<kDtype>(x[p]);
-                        f[2 * p] = y.x * down, f[2 * p + 1] = y.y * down;
-                    }
-                    uint32_t o[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        o[p] = pack_half2(f[p], f[p + 4]);
                         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&o[p]));
                         qsum += y.x + y.y;
                     }
-                    *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kTile * 128) + tc::sw128_offset(row, (c & 7) * 8)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 // sum(q), met by the keys' m + 8 s
                 __half hi, lo;
@@ -1030,6 +1055,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t most = __reduce_max_sync(~0u, mine), least = __reduce_min_sync(~0u, mine - 1u);   // not of 0
                 if (lane == 0) step_ends[is_v][parity][w] = make_uint2(most, least);
             };
+            look_up(k.t0 + 1);
+            const int second = ids;                             // (asked for together with the first)
             look_up(k.t0);
             parts = check(k.t0);
             scale = load_scale(parts);
@@ -1040,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) load_keys(u, place(parts, key_token(u)));
             }
-            look_up(k.t0 + 1);
+            ids = second;
             parts = check(k.t0 + 1);
             scale_next = load_scale(parts);
             look_up(k.t0 + 2);

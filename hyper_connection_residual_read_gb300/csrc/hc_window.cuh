@@ -172,6 +172,12 @@ __device__ __forceinline__ void begin_early() {
     pdl_launch_dependents();
 }
 
+// x / y; most sums are short enough for 32 bits, in a fraction of the time.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+
 // Counts a block of the launch that has written its part; the count before it. One thread calls
 // it, behind a barrier that the writers have passed: release and acquire cover what the barrier
 // ordered, on both sides (a fence by every writer, and one by every reader, cost 0.3 us more).
