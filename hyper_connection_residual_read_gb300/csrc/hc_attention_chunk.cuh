@@ -34,17 +34,17 @@
 //   both warpgroups on the same rows, each on every other key tile.
 // * Work is cut as in the window kernel: runs of equal cost over the CTAs, in key tiles.
 //
-// Measured: 8192 tokens behind 8192, 32/8 heads of 128, 1.65 ms, 999 TFLOP/s of the causal
+// Measured: 8192 tokens behind 8192, 32/8 heads of 128, 1.65 ms, 1000 TFLOP/s of the causal
 // products (52% of the library's rate): softmax, key and value warps each need 4500 to 5000
 // cycles for a step of 256 rows x 128 keys, the products 2300. 16 windows of 8 tokens over up
-// to 32K tokens, 20/4 heads of 128, 110 us, 1.2 TB/s of cache: the key warps are busy all of
+// to 32K tokens, 20/4 heads of 128, 107 us, 1.2 TB/s of cache: the key warps are busy all of
 // the time (some 4000 cycles a tile), the others wait for them. 6 ragged chunks of up to 1001
-// tokens, 16 heads of 64, 96 us.
+// tokens, 16 heads of 64, 92 us.
 // Behind shared prefixes (kPrefix without a causal order, its pieces joined by a kernel of its own; kJoined the own
-// parts, beside and behind that): 64 requests of a token behind 16384 tokens, 32/8 heads of 128, prefix 35 us, join 8,
-// with the window kernel's own parts 58 in all. 16 windows of up to 8 tokens behind 83K tokens in three prefixes, 20/4
-// heads, prefix 61 us, 99 in all. 6 chunks of up to 501 tokens behind two prefixes of 5K, 16 heads of 64, fp16, prefix 98
-// us, 152 in all.
+// parts, beside and behind that): 64 requests of a token behind 16384 tokens, 32/8 heads of 128, prefix some 30 us, join 8,
+// with the window kernel's own parts 54 in all. 16 windows of up to 8 tokens behind 83K tokens in three prefixes, 20/4
+// heads, prefix 57 us, 92 in all. 6 chunks of up to 501 tokens behind two prefixes of 5K, 16 heads of 64, fp16, prefix 97
+// us, 149 in all.
 #pragma once
 
 #include <cuda_bf16.h>
