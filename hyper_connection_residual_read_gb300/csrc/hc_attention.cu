@@ -1,6 +1,8 @@
 // Attention over the 4-bit cache: windows of few rows, and the choice between the kernels.
 #include <limits.h>
 
+#include <cmath>
+
 #include "hc_attention.cuh"
 
 namespace hc {
@@ -35,24 +37,25 @@ cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dty
 }
 // A group's rows are many, but where prefixes are short the chunk kernel's start is longer than its work: then each
 // group is cut into shares of up to 8 or 16 rows, and each share reads the prefix for itself. The costs are what
-// the kernels take, in us: a start, and rounds of units over the resident CTAs.
+// calls take, in us: a start, rounds of units over the resident CTAs, and of the chunk kernel the join of the CTAs that
+// share a head. (64 rows of 8 heads: behind 8000 tokens 27.4 by shares, 30.1 by chunks; behind 16000 37.8 and 34.4. 256
+// rows of 8 heads behind 2000 31.1 and 29.5, of 2 heads behind 8000 27.8 and 38.5.)
 cudaError_t launch_kv4_attention_prefix(const Ctx& ctx, const SharedArgs& a, int dtype, cudaStream_t st) {
     const int group = a.q_heads / a.c.kv_heads;
     const int64_t rows = static_cast<int64_t>(a.shared) * group, room = static_cast<int64_t>(a.width) * a.c.block_size;
     const int64_t heads = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     if (rows <= kMaxRows) return launch_attention<kPrefix>(ctx, a, dtype, st);
-    auto rounds = [&](int64_t units, int ctas) { return static_cast<double>((units + ctas - 1) / ctas); };
-    double least = 20 + 2.4 * rounds(heads * ((rows + 255) / 256) * ((room + 127) / 128), ctx.sm_count);
+    auto rounds = [](double units, int ctas) { return std::ceil(units / ctas); };      // (products may pass 64 bits)
+    const int64_t tiles = heads * ((rows + 255) / 256), keys = (room + 127) / 128, sharing = (ctx.sm_count + tiles - 1) / tiles;
+    const double chunks = 15 + 0.27 * static_cast<double>(keys < sharing ? keys : sharing) + 2.4 * rounds(static_cast<double>(tiles) * keys, ctx.sm_count);
+    // (shares of 16 rows where a token has more than 8)
+    const int each = group <= 8 ? 8 / group : 1;              // tokens of a share
+    const int64_t subs = (static_cast<int64_t>(a.shared) + each - 1) / each;
+    const double units = static_cast<double>(heads) * subs * ((room + kUnit - 1) / kUnit);
+    const double shares = group <= 8 ? 13 + 1.9 * rounds(units, 2 * ctx.sm_count) : 15 + 1.8 * rounds(units, ctx.sm_count);
     SharedArgs b = a;
-    for (int most = 8; most <= kMaxRows; most += 8) {
-        const int each = most / group;                       // tokens of a share
-        if (each == 0) continue;
-        const int64_t subs = (a.shared + each - 1) / each, units = heads * subs * ((room + kUnit - 1) / kUnit);
-        const double cost = most == 8 ? 7 + 2.2 * rounds(units, 2 * ctx.sm_count) : 14 + 3.5 * rounds(units, ctx.sm_count);
-        if (cost >= least || a.requests * subs > INT_MAX) continue;
-        least = cost;
+    if (group <= kMaxRows && shares < chunks && a.requests * subs <= INT_MAX)
         b.subs = static_cast<int>(subs), b.requests = static_cast<int>(a.requests * subs), b.max_new = each;
-    }
     return launch_attention<kPrefix>(ctx, b, dtype, st);
 }
 cudaError_t launch_kv4_attention_joined(const Ctx& ctx, const SharedArgs& a, int dtype, cudaStream_t st) {
