@@ -233,13 +233,16 @@ def main() -> None:
     parser.add_argument("--layers", type=int, default=2)
     parser.add_argument("--positions", action="store_true", help="norm and rotate queries and keys")
     parser.add_argument("--shared", type=int, default=0, help="tokens of a prompt that all requests begin with")
-    parser.add_argument("--temperature", type=float, help="draw tokens instead of taking the most likely")
+    parser.add_argument("--temperature", type=float, help="draw tokens instead of taking the most likely (1 where a filter is given)")
     parser.add_argument("--top-k", type=int, default=0)
     parser.add_argument("--top-p", type=float, default=1.0)
     parser.add_argument("--min-p", type=float, default=0.0)
     args = parser.parse_args()
     g = np.random.default_rng(0)
-    sampling = None if args.temperature is None else dict(temperature=args.temperature, top_k=args.top_k, top_p=args.top_p, min_p=args.min_p)
+    sampling = None
+    if args.temperature is not None or args.top_k > 0 or args.top_p < 1 or args.min_p > 0:
+        sampling = dict(temperature=1.0 if args.temperature is None else args.temperature, top_k=args.top_k,
+                        top_p=args.top_p, min_p=args.min_p)
     shared = np.random.default_rng(1).integers(0, 4096, args.shared).tolist()
 
     def make():
