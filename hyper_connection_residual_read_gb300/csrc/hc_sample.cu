@@ -60,6 +60,9 @@ constexpr int kSteps = 32;                   // of the table, an octave
 constexpr float kRound = 12582912.f;         // 1.5 2^23
 constexpr float kDeep = -46.5f;              // log2 of weights that are 0
 constexpr float kTop = 3.402823466e38f;
+// A temperature above kHot, and the logits with it, are weighed as 2^-64 of themselves: M - x and 46.5 T ln 2 pass fp32's
+// range there, and c falls below its normal numbers. (The logits that 2^-64 makes subnormal are all 0 beside such a T.)
+constexpr float kHot = 18446744073709551616.f, kCooled = 1.f / kHot;
 static_assert(HC_SAMPLE_MAX_VOCAB <= kMaxCtas * 32768);
 
 // 2^(j / 32) 2^31
@@ -97,14 +100,15 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // A row's temperature and largest logit, as the weights need them.
 struct Heat {
     float c, c_low, a, rest;                 // c in two floats; 1.5 2^23 - rint(M c); what makes g(M) 0
-    float top, deep;                         // M; the logit below which weights are 0
-    bool far;                                // M c is beyond what a rounds well
+    float top, deep;                         // M; the logit below which weights are 0 (-kTop: of finite ones perhaps none)
+    bool far;                                // T is above kHot (and c that of 2^-64 T), or M c is beyond what a rounds well
 };
 // (In fp32 alone: 64-bit operations took 15 us of a row's 40.)
 __device__ __forceinline__ Heat heat_of(float t, float top) {
     constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;             // log2(e)
     Heat h;
-    const float z = kHi / t, z_low = (fmaf(-z, t, kHi) + kLo) / t;
+    const bool hot = t > kHot;
+    const float by = hot ? t * kCooled : t, z = kHi / by, z_low = (fmaf(-z, by, kHi) + kLo) / by;
     h.c = z * kSteps, h.c_low = z_low * kSteps;
     // M's own weight is 2^45: its m is 0, and so is its g to 2^-25, whose p is held as 0
     const float at = h.c * top;
@@ -114,7 +118,7 @@ __device__ __forceinline__ Heat heat_of(float t, float top) {
     h.rest = fmaf(-h.c_low, top, -fmaf(top, h.c, -whole));
     h.top = top;
     h.deep = fmaxf(fmaf(t, kDeep * kLn2, top), -kTop);                   // never -inf
-    h.far = !(fabsf(at) < 1000000.f);
+    h.far = hot || !(fabsf(at) < 1000000.f);
     return h;
 }
 
@@ -155,8 +159,10 @@ __device__ __forceinline__ void weights(float x0, float x1, const Heat& h, const
     w0 = power(__float_as_int(bits.x), __float_as_int(part.x), powers);
     w1 = power(__float_as_int(bits.y), __float_as_int(part.y), powers);
 }
-// Where M c is so large that this way loses bits: from the difference to M, in two floats.
-__device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const uint32_t* powers) {
+// Where M c or T is so large that this way loses bits: from the difference to M, in two floats. 0 of -inf. (T is looked up:
+// registers are short.)
+__device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const float* t, const uint32_t* powers) {
+    if (*t > kHot) x *= kCooled, top *= kCooled;
     const float d = __fsub_rn(x, top), z = __fmul_rn(d, c);
     if (!(z > kDeep)) return 0;
     const float b = __fsub_rn(d, x);
@@ -167,6 +173,9 @@ __device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c
     const float p = g * fmaf(g, fmaf(g, fmaf(g, kP4, kP3), kP2), kP1);
     return power(__float_as_int(v), __float_as_int(fmaf(p, kPart, kRound)), powers);
 }
+
+// ln of a weight, by halves: a difference of logits may pass fp32's range where that over T does not.
+__device__ __forceinline__ float log_weight(float x, float top, float t) { return (0.5f * x - 0.5f * top) / t * 2.f; }
 
 template <typename T>
 __device__ __forceinline__ T warp_sum(T x) {
@@ -332,7 +341,7 @@ __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs
     const uint64_t goal = s.u < 1.f ? part_of(total, fmaxf(s.u, 0.f), false) : total - 1;
     if (upto > goal && upto - kept <= goal) {
         a.ids[row] = s.id[tid];
-        a.logprob[row] = ((y[0] - top) / s.t) - logf(static_cast<float>(total) * (1.f / kOne));
+        a.logprob[row] = log_weight(y[0], top, s.t) - logf(static_cast<float>(total) * (1.f / kOne));
     }
 }
 
@@ -479,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
     // and their weights, 0 for those at -inf
     auto weigh2 = [&](float y0, float y1, uint64_t& w0, uint64_t& w1) {
         if (heat.far) {
-            w0 = weight_far(y0, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), s.powers);
-            w1 = weight_far(y1, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), s.powers);
+            w0 = weight_far(y0, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), &s.t, s.powers);
+            w1 = weight_far(y1, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), &s.t, s.powers);
         } else {
             weights(y0, y1, heat, s.powers, w0, w1);
         }
@@ -906,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
                 }
                 if (j < 0) continue;
                 a.ids[row] = mode == kAlone ? s.id[begin + j] : id0 + (mode == kListed ? static_cast<int>(mine[j]) : begin + j);
-                a.logprob[row] = ((drawn - top) / s.t) - logf(static_cast<float>(total) * (1.f / kOne));
+                a.logprob[row] = log_weight(drawn, top, s.t) - logf(static_cast<float>(total) * (1.f / kOne));
             }
         }
     }
