@@ -220,8 +220,8 @@ __device__ Run find_run(const Args<kSide>& a, Run* shared, int64_t* sums, int* s
         run.w.first = __shfl_sync(~0u, w.first, run.b);
         return run;
     }
-    const int per = (a.requests + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
+    const int per = (a.requests - 1) / kThreads + 1;             // (of up to 2^31 - 1)
+    const int b0 = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(a.requests))), b1 = b0 + min(per, a.requests - b0);
     int64_t mine = 0;
     bool long_one = false;
     for (int b = b0; b < b1; ++b) {

@@ -174,8 +174,8 @@ struct Run {
 template <Side kSide>
 __device__ void find_run(const Args<kSide>& a, int group, int step, Run* run, int64_t* sums, int* status) {
     const int tid = threadIdx.x;
-    const int per = (a.requests + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
+    const int per = (a.requests - 1) / kThreads + 1;             // (of up to 2^31 - 1)
+    const int b0 = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(a.requests))), b1 = b0 + min(per, a.requests - b0);
     int64_t mine = 0;
     Window w = {};                               // the last of them, which is the only one up to kThreads requests
     for (int b = b0; b < b1; ++b) {

@@ -98,8 +98,8 @@ extern "C" int hc_kv4_attention_shared(const hc_kv4_cache* cache, int requests, 
     const Span s[] = {{out, rows * d * item(dtype)}, {lse, lse ? 4 * rows : 0}, {workspace, 4 * rows * (d + 2)},
                       {cache->codes, n * (d / 2)}, {cache->scales, 4 * n},
                       {q, extent(tokens, q_heads, d, q_token_stride, q_head_stride, dtype)},
-                      {cu_lens, 4ull * (requests + 1)}, {kv_lens, 4ull * requests},
-                      {block_table, 4ull * requests * table_width}, {cu_groups, 4ull * (groups + 1)},
+                      {cu_lens, 4ull * requests + 4}, {kv_lens, 4ull * requests},
+                      {block_table, 4ull * requests * table_width}, {cu_groups, 4ull * groups + 4},
                       {prefix_lens, 4ull * groups}, {prefix_table, 4ull * groups * prefix_width},
                       {mask, mask ? 8ull * tokens : 0}};
     if (any_meet(s, 3, 13)) return HC_ERR_ARG;

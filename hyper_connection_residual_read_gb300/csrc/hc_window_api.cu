@@ -122,7 +122,7 @@ extern "C" int hc_kv4_attention(const hc_kv4_cache* cache, int requests, int tok
     const Span s[] = {{out, rows * d * item(dtype)}, {lse, lse ? 4 * rows : 0},
                       {cache->codes, n * (d / 2)}, {cache->scales, 4 * n},
                       {q, extent(tokens, q_heads, d, q_token_stride, q_head_stride, dtype)},
-                      {cu_lens, 4ull * (requests + 1)}, {kv_lens, 4ull * requests},
+                      {cu_lens, 4ull * requests + 4}, {kv_lens, 4ull * requests},
                       {block_table, 4ull * requests * table_width},
                       {mask, mask ? 8ull * tokens : 0}};
     if (any_meet(s, 2, 9)) return HC_ERR_ARG;
