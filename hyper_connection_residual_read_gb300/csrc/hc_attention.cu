@@ -45,9 +45,10 @@ cudaError_t launch_kv4_attention_prefix(const Ctx& ctx, const SharedArgs& a, int
     const int64_t rows = static_cast<int64_t>(a.shared) * group, room = static_cast<int64_t>(a.width) * a.c.block_size;
     const int64_t heads = static_cast<int64_t>(a.requests) * a.c.kv_heads;
     if (rows <= kMaxRows) return launch_attention<kPrefix>(ctx, a, dtype, st);
-    auto rounds = [](double units, int ctas) { return std::ceil(units / ctas); };      // (products may pass 64 bits)
-    const int64_t tiles = heads * ((rows + 255) / 256), keys = (room + 127) / 128, sharing = (ctx.sm_count + tiles - 1) / tiles;
-    const double chunks = 15 + 0.27 * static_cast<double>(keys < sharing ? keys : sharing) + 2.4 * rounds(static_cast<double>(tiles) * keys, ctx.sm_count);
+    // (in fp64: max_shared bounds tokens and need not be near them, and its products may pass 64 bits)
+    auto rounds = [](double units, int ctas) { return std::ceil(units / ctas); };
+    const double tiles = static_cast<double>(heads) * static_cast<double>((rows + 255) / 256), keys = static_cast<double>((room + 127) / 128);
+    const double sharing = std::ceil(ctx.sm_count / tiles), chunks = 15 + 0.27 * (keys < sharing ? keys : sharing) + 2.4 * rounds(tiles * keys, ctx.sm_count);
     // (shares of 16 rows where a token has more than 8)
     const int each = group <= 8 ? 8 / group : 1;              // tokens of a share
     const int64_t subs = (static_cast<int64_t>(a.shared) + each - 1) / each;

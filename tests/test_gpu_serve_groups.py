@@ -72,3 +72,17 @@ def test_shared_of_more_shares_than_a_launch_has():
     # the others are within two roundings of these
     first = kw["out"][:, :1].float()
     assert ((kw["out"].float() - first).abs() <= 2.0 ** -6 * first.abs() + 2.0 ** -8).all()
+
+
+def test_shared_of_the_largest_bound_of_many_groups():
+    """2^34 (group, head)s of up to 2^38 rows each, as far as the host knows: 2^64 row tiles."""
+    kv_heads, groups = 1 << 12, 1 << 22
+    c = Shared(2, [(40, [(1, 1)])], 128, 1, 64, 16, "bf16")
+    kw = among(c, groups, groups - 3)
+    wide = lambda t, axis: t.repeat_interleave(kv_heads, axis)  # noqa: E731
+    q = kw["q"].repeat(1, kv_heads, 1)
+    kw.update(q=q, codes=wide(kw["codes"], 2), scales=wide(kw["scales"], 2), workspace=torch.empty(q.shape[1] * 66, device="cuda"),
+              out=torch.full_like(q, 55.0), lse=torch.empty(1, q.shape[1], device="cuda"), max_shared=(1 << 31) - 1)
+    hc.hc_kv4_attention_shared(**kw)
+    for h in (0, 1, 2049, kv_heads - 1):
+        c.check(kw["out"][:, 128 * h:128 * (h + 1)], kw["lse"][:, 128 * h:128 * (h + 1)])
