@@ -26,7 +26,6 @@ namespace hc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 3;
 
 // A token's row of the table for frequency i.
 __device__ __forceinline__ int table_row(const RotaryArgs& a, int64_t t, int axis, int* status) {
@@ -44,6 +43,8 @@ __device__ __forceinline__ int table_row(const RotaryArgs& a, int64_t t, int axi
 }
 
 enum Pairs { kHalves, kNeighbours, kPartHalves };     // (i, i + D / 2); (2i, 2i + 1); (i, i + dim / 2), dim < D
+template <Pairs kPairs>
+constexpr int kCtasPerSm = kPairs == kPartHalves ? 2 : 3;      // (of 120 to 124 registers a thread, and of 80)
 
 template <int kDtype>
 __device__ __forceinline__ void load_weights(const void* w, int at, float (&x)[8]) {
@@ -170,7 +171,7 @@ __device__ __forceinline__ void rotate(float (&x)[2][8], const Angles<kPairs>& t
 // CTA has each gridDim.y-th: the query heads of these, two at a time, then the kv heads, a key and a value. What a
 // thread needs comes to a ring of its own in shared memory, two such steps ahead.
 template <int kD, int kDtype, Pairs kPairs>
-__global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : kCtasPerSm) rotary_kernel(const RotaryArgs a, int* status) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<kPairs>) rotary_kernel(const RotaryArgs a, int* status) {
     begin_early();
     constexpr int kLanes = kD / 16, kTile = kThreads / kLanes;
     const int sub = threadIdx.x % kLanes;
@@ -324,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, kPairs == kPartHalves ? 2 : kCtasPer
 }
 
 // CTAs that share a tile's heads: those that take the fewest rounds of all resident CTAs, each as long as its
-// heads and two more for its start (8191 tokens of 40 heads: 5 CTAs take 34.9 us, 3 36.2, 10 38.9).
+// heads and two more for its start (8191 tokens of 40 heads: 5 CTAs take 34.9 us, 3 36.2, 10 38.9). `resident` are those
+// of the kernel that is launched (4099 tokens of 32 + 8 heads half of which are rotated, by halves: 21.7 us, and 27.8 with
+// the other kernels' three an SM).
 int head_split(int tiles, int heads, int resident) {
     int best = 1;
     int64_t least = -1;
@@ -335,15 +338,18 @@ int head_split(int tiles, int heads, int resident) {
     return best;
 }
 
-template <int kD, int kDtype>
-cudaError_t call(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
+template <int kD, int kDtype, Pairs kPairs>
+cudaError_t call_pairs(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
     constexpr int kTile = kThreads / (kD / 16);
     const int tiles = (a.tokens - 1) / kTile + 1;
-    const int split = head_split(tiles, a.q_heads + a.c.kv_heads, kCtasPerSm * ctx.sm_count);
-    const dim3 grid(tiles, split);
-    if (a.r.interleaved || a.r.dim == 0) return launch_early(rotary_kernel<kD, kDtype, kNeighbours>, grid, kThreads, 0, st, a, ctx.s.status);
-    if (a.r.dim == kD) return launch_early(rotary_kernel<kD, kDtype, kHalves>, grid, kThreads, 0, st, a, ctx.s.status);
-    return launch_early(rotary_kernel<kD, kDtype, kPartHalves>, grid, kThreads, 0, st, a, ctx.s.status);
+    const dim3 grid(tiles, head_split(tiles, a.q_heads + a.c.kv_heads, kCtasPerSm<kPairs> * ctx.sm_count));
+    return launch_early(rotary_kernel<kD, kDtype, kPairs>, grid, kThreads, 0, st, a, ctx.s.status);
+}
+
+template <int kD, int kDtype>
+cudaError_t call(const Ctx& ctx, const RotaryArgs& a, cudaStream_t st) {
+    if (a.r.interleaved || a.r.dim == 0) return call_pairs<kD, kDtype, kNeighbours>(ctx, a, st);
+    return a.r.dim == kD ? call_pairs<kD, kDtype, kHalves>(ctx, a, st) : call_pairs<kD, kDtype, kPartHalves>(ctx, a, st);
 }
 
 template <int kDtype>
