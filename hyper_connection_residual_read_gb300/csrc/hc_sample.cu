@@ -36,6 +36,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -199,7 +200,8 @@ struct Shared {
     uint32_t powers[kSteps];
     // of a step's bins: their logits, and their weights as sums of each 16 bits of them (shared memory adds
     // 32 bits at a time by itself: three such sums take 8 cycles a warp, one of 64 bits 50 to 570)
-    unsigned count[kBins], mass[3][kBins];
+    unsigned count[kBins];
+    alignas(uint64_t) unsigned mass[3][kBins];           // (taken as 64-bit words by finish_alone)
     // what the warps tell the cluster
     alignas(16) uint64_t told_mass[kWarps];
     alignas(16) unsigned told_count[kWarps];
@@ -297,6 +299,7 @@ __device__ __forceinline__ void finish_alone(Shared<kDtype>& s, const SampleArgs
     float* value = reinterpret_cast<float*>(s.count);
     uint64_t* mass = reinterpret_cast<uint64_t*>(s.mass);
     static_assert(sizeof(s.count) >= kThreads * sizeof(float) && sizeof(s.mass) >= kThreads * sizeof(uint64_t));
+    static_assert(offsetof(Shared<kDtype>, mass) % alignof(uint64_t) == 0 && alignof(Shared<kDtype>) % alignof(uint64_t) == 0);
     const float y[4] = {tid < n ? logit<kDtype>(s.value, tid) : -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
     uint64_t w[4];
     weigh(y, w);
