@@ -102,14 +102,13 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 struct Heat {
     float c, c_low, a, rest;                 // c in two floats; 1.5 2^23 - rint(M c); what makes g(M) 0
     float top, deep;                         // M; the logit below which weights are 0 (-kTop: of finite ones perhaps none)
-    bool far;                                // T is above kHot (and c that of 2^-64 T), or M c is beyond what a rounds well
+    bool far;                                // M c is beyond what a rounds well, or T above kHot (c is not used then)
 };
+constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;     // log2(e)
 // (In fp32 alone: 64-bit operations took 15 us of a row's 40.)
 __device__ __forceinline__ Heat heat_of(float t, float top) {
-    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;             // log2(e)
     Heat h;
-    const bool hot = t > kHot;
-    const float by = hot ? t * kCooled : t, z = kHi / by, z_low = (fmaf(-z, by, kHi) + kLo) / by;
+    const float z = kHi / t, z_low = (fmaf(-z, t, kHi) + kLo) / t;
     h.c = z * kSteps, h.c_low = z_low * kSteps;
     // M's own weight is 2^45: its m is 0, and so is its g to 2^-25, whose p is held as 0
     const float at = h.c * top;
@@ -119,7 +118,11 @@ __device__ __forceinline__ Heat heat_of(float t, float top) {
     h.rest = fmaf(-h.c_low, top, -fmaf(top, h.c, -whole));
     h.top = top;
     h.deep = fmaxf(fmaf(t, kDeep * kLn2, top), -kTop);                   // never -inf
-    h.far = hot || !(fabsf(at) < 1000000.f);
+    // (a word of which the compiler knows nothing: what it made of the comparisons in all that follows took 5 us of the
+    // 142 of 512 rows)
+    unsigned far = !(fabsf(at) < 1000000.f && t <= kHot);
+    asm volatile("" : "+r"(far));
+    h.far = far != 0;
     return h;
 }
 
@@ -160,10 +163,18 @@ __device__ __forceinline__ void weights(float x0, float x1, const Heat& h, const
     w0 = power(__float_as_int(bits.x), __float_as_int(part.x), powers);
     w1 = power(__float_as_int(bits.y), __float_as_int(part.y), powers);
 }
-// Where M c or T is so large that this way loses bits: from the difference to M, in two floats. 0 of -inf. (T is looked up:
-// registers are short.)
-__device__ __noinline__ uint64_t weight_far(float x, float top, float c, float c_low, const float* t, const uint32_t* powers) {
-    if (*t > kHot) x *= kCooled, top *= kCooled;
+// Where M c or T is so large that this way loses bits: from the difference to M, in two floats. 0 of -inf. What it needs of
+// the row lies in shared memory, since registers are short.
+struct Far {
+    float by, c, c_low;                      // 1, or 2^-64 of a hot row; log2(e) / (by T) in two floats
+};
+__device__ __noinline__ void far_of(float t, Far* to) {
+    const float by = t > kHot ? kCooled : 1.f, cool = t * by, c = kHi / cool;
+    to->by = by, to->c = c, to->c_low = (fmaf(-c, cool, kHi) + kLo) / cool;
+}
+__device__ __noinline__ uint64_t weight_far(float x, float top, const Far* far, const uint32_t* powers) {
+    const float by = far->by, c = far->c, c_low = far->c_low;
+    x *= by, top *= by;
     const float d = __fsub_rn(x, top), z = __fmul_rn(d, c);
     if (!(z > kDeep)) return 0;
     const float b = __fsub_rn(d, x);
@@ -206,6 +217,7 @@ struct Shared {
     alignas(16) uint64_t told_mass[kWarps];
     alignas(16) unsigned told_count[kWarps];
     alignas(16) float told_top[kWarps];
+    Far far;                                 // of a row whose weights are found that way
     float u, p, t, least;                    // the row's settings, for where they are needed again (registers are short)
     // within the CTA
     uint64_t warp_mass[kWarps];
@@ -448,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
         return;
     }
     const Heat heat = heat_of(t, top);
+    if (heat.far) far_of(t, &s.far);             // (all threads the same)
     const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1.f;
     // a warp's sum, told to the cluster
     auto tell_mass = [&](uint64_t mass) {
@@ -491,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, kDtype == HC_DTYPE_FP32 ? 3 : 4) sam
     // and their weights, 0 for those at -inf
     auto weigh2 = [&](float y0, float y1, uint64_t& w0, uint64_t& w1) {
         if (heat.far) {
-            w0 = weight_far(y0, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), &s.t, s.powers);
-            w1 = weight_far(y1, top, heat.c * (1.f / kSteps), heat.c_low * (1.f / kSteps), &s.t, s.powers);
+            w0 = weight_far(y0, top, &s.far, s.powers);
+            w1 = weight_far(y1, top, &s.far, s.powers);
         } else {
             weights(y0, y1, heat, s.powers, w0, w1);
         }
