@@ -35,6 +35,9 @@ cudaError_t attention_setup() {
 cudaError_t launch_kv4_attention(const Ctx& ctx, const AttentionArgs& a, int dtype, cudaStream_t st) {
     return launch_attention<kOwn>(ctx, a, dtype, st);
 }
+// Both rules below go by max_new, max_shared and the room of the tables: lengths lie on the device. (With tables of 32K tokens
+// 16 requests behind 2000 take 26 us where tight ones take 19, 64 behind 16384 57 and 48.5.)
+//
 // A group's rows are many, but where prefixes are short the chunk kernel's start is longer than its work: then each
 // group is cut into shares of up to 8 or 16 rows, and each share reads the prefix for itself. The costs are what
 // calls take, in us: a start, rounds of units over the resident CTAs, and of the chunk kernel the join of the CTAs that

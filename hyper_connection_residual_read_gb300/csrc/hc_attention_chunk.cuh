@@ -42,9 +42,9 @@
 // tokens, 16 heads of 64, 92 us.
 // Behind shared prefixes (kPrefix without a causal order, its pieces joined by a kernel of its own; kJoined the own
 // parts, beside and behind that): 64 requests of a token behind 16384 tokens, 32/8 heads of 128, prefix some 30 us, join 8,
-// with the window kernel's own parts 54 in all. 16 windows of up to 8 tokens behind 83K tokens in three prefixes, 20/4
+// with the window kernel's own parts 53 in all. 16 windows of up to 8 tokens behind 83K tokens in three prefixes, 20/4
 // heads, prefix 57 us, 92 in all. 6 chunks of up to 501 tokens behind two prefixes of 5K, 16 heads of 64, fp16, prefix 97
-// us, 149 in all.
+// us, 148 in all.
 #pragma once
 
 #include <cuda_bf16.h>

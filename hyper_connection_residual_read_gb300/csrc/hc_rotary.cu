@@ -8,12 +8,14 @@
 // step function of it, and would differ from place to place with the last bit of it.
 //
 // A CTA takes some heads of a share of the tokens, so that a token's cosines and sines are fetched once for them,
-// and brings heads through a ring of three steps of asynchronous copies.
+// and brings heads through a ring of three steps of asynchronous copies. (Of one step in fp32, whose heads are twice as
+// large: nothing is brought ahead there, and each step waits for its loads.)
 //
 // Measured: 8191 tokens, 32 query and 8 kv heads of 128, bf16, with norms, 34.9 us, 176 MB at 5.0 TB/s (74% of the
 // copy rate): issue bounds it (65% of the slots; ALU 46%, FMA 32%), since without fma and with each rounding of its
 // own a value costs some ten instructions. 4099 tokens of 16 + 16 heads of 64, fp16, three axes, no norm, 12.1 us:
-// a CTA's few steps hardly outlast its start. 32 tokens 3.3 us, a launch and a chain of loads.
+// a CTA's few steps hardly outlast its start. 32 tokens 3.3 us, a launch and a chain of loads. In fp32 8191 tokens of
+// 32 + 8 heads take 81 us, 349 MB at 4.3 TB/s. Halves of a part of the head (8191 tokens, 64 of 128 dimensions) 40 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -169,7 +171,7 @@ __device__ __forceinline__ void rotate(float (&x)[2][8], const Angles<kPairs>& t
 
 // A thread keeps its token's angles and goes through heads. They are numbered through, the kv heads first, and a
 // CTA has each gridDim.y-th: the query heads of these, two at a time, then the kv heads, a key and a value. What a
-// thread needs comes to a ring of its own in shared memory, two such steps ahead.
+// thread needs comes to a ring of its own in shared memory, two such steps ahead (fp32: as it is needed).
 template <int kD, int kDtype, Pairs kPairs>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<kPairs>) rotary_kernel(const RotaryArgs a, int* status) {
     begin_early();

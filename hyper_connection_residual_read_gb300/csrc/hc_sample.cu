@@ -26,9 +26,9 @@
 // comes to the same end. A short list is handed to the first CTA, which ends the row alone. Lists and
 // rows are gone through in the order of the ids, by each warp its part.
 //
-// Measured: rows of 131072 bf16 logits, 8 and 512 of them: the largest 3.5 and 38 us, no filter 9.4 and 103, a top-50
-// 8.0 and 81, a top-1000 16 and 139, a top-p of 0.5 18 and 178, of 0.95 25 and 274; 512 of mixed settings 135 us,
-// 1.0 TB/s. The logits are read once (20 us of it at the copy rate). Few rows wait at barriers (a cluster's takes
+// Measured: rows of 131072 bf16 logits, 8 and 512 of them: the largest 3.5 and 35 us, no filter 9.5 and 101, a top-50
+// 8.1 and 79, a top-1000 16 and 136, a top-p of 0.5 18 and 177, of 0.95 24 and 271; 512 of mixed settings 126 to 146 us
+// by the draw of these, 1.0 TB/s; 96 of 50257 in fp32 33 to 52, by the slowest row. The logits are read once (20 us of it at the copy rate). Few rows wait at barriers (a cluster's takes
 // some 0.5 us, a filter has 6 to 10); many are bound by issue (38% of the slots, four CTAs an SM wait for one
 // another) and by the weights, 64-bit arithmetic.
 #include <cooperative_groups.h>

@@ -88,6 +88,14 @@ int hc_kv4_append_rotary(const hc_kv4_cache* cache, const hc_rotary* rotary, int
  *   workspace    floats [tokens][q_heads][head_dim + 2]: sums over the prefixes. Written by the
  *                call; nothing is kept there for another.
  *
+ * The host reads no lengths: kernels are chosen by max_new, max_shared and what the tables have
+ * room for (width * block_size tokens). Results do not depend on it, the time does: a table no
+ * wider than its longest row needs, and of own tokens one of at most 2048 where there are many
+ * requests of few tokens, is the faster one. A prefix of whole blocks can also stand at the
+ * beginning of each request's row in hc_kv4_attention, which needs no workspace: faster where the
+ * prefix is short or the tokens are chunks of prompts, whose products are the same either way;
+ * this call where tokens are few and the prefix is long, which that one reads once a request.
+ *
  * Everything else is as in hc_kv4_attention, its roundings among them: the prefix's part and the
  * own one are each as exact as a call of it, and are joined in fp32 before the one rounding to
  * `dtype`. */
@@ -119,8 +127,8 @@ int hc_kv4_attention_shared(const hc_kv4_cache* cache, int requests, int groups,
  *
  * Weights are whole multiples of 2^-45, within 2^-27 of w_i (up to e^-24) or the multiple, and their sums
  * are exact, so that the token does not depend on the order of anything; it is the formula's
- * but where uniform lies as near to a border between two tokens as that, or another weight to
- * the border of a filter. logprob within 2^-20 of 1 + its size.
+ * but where uniform lies within 2^-26 of a border between two tokens (two sums, each off by up
+ * to 2^-27), or a filter's border as near to another weight. logprob within 2^-20 of 1 + its size.
  */
 int hc_sample_tokens(int tokens, int vocab, int dtype, const void* logits, int64_t row_stride,
                      const float* uniform, const float* temperature, const int32_t* top_k,
